@@ -17,6 +17,14 @@ Entry points (same names as the C-ABI):
     segment_transfer(k, v, log_alpha, beta, G)         -> (S_zero_end, M)
     segment_merge(S_zero_end, M, S_in=None)            -> (S_start, S_T)
     prefill_backward(q, k, v, log_alpha, beta, S0, dO, dS_T) -> dict of gradients
+    conv_prefill(x, weight, bias=None, state=None, ...) -> (o, state_out)
+    conv_step(x, state, weight, bias=None, ...)        -> o          (state moved on in place)
+    conv_backward(x, weight, bias, state, dO, dstate_out=None, ...) -> dict of gradients
+    ssm_prefill(q, k, v, log_alpha, beta, D=None, S0=None, ...) -> (o, S_T)
+    ssm_step(q, k, v, log_alpha, beta, S, D=None)      -> o          (S updated in place)
+    ssm_backward(q, k, v, log_alpha, beta, D, S0, dO, dS_T) -> dict of gradients
+    state_cache(nslots, H, dk, dv, fmt, device)        -> (cache, scales)
+    state_store(S, slots, cache, scales), state_load(cache, scales, slots) -> S
     set_option(name, value), get_option(name), options(**values) (context manager)
 """
 from __future__ import annotations
@@ -37,7 +45,26 @@ _DT = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 (KDA_OK, KDA_ERR_NULL, KDA_ERR_SHAPE, KDA_ERR_UNSUPPORTED, KDA_ERR_ALIGN, KDA_ERR_WORKSPACE,
  KDA_ERR_PRECONDITION, KDA_ERR_HIP) = range(8)
 
+# kda_activation, kda_cache_format
+_ACT = {None: 0, "silu": 1}
+_CACHE = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
 _lib = None
+
+
+class _Strides(ctypes.Structure):
+    """kda_strides: elements between consecutive b, h, t."""
+    _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("t", ctypes.c_longlong)]
+
+
+class _SsmStrides(ctypes.Structure):
+    """kda_ssm_strides."""
+    _fields_ = [(n, _Strides) for n in ("q", "k", "v", "log_alpha", "beta", "o")]
+
+
+class _SsmGradStrides(ctypes.Structure):
+    """kda_ssm_grad_strides."""
+    _fields_ = [(n, _Strides) for n in ("dO", "dq", "dk", "dv", "dlog_alpha", "dbeta")]
 
 
 class KdaError(RuntimeError):
@@ -77,6 +104,25 @@ def load() -> ctypes.CDLL:
     lib.kda_backward_workspace_bytes.argtypes = [i] * 6
     lib.kda_backward_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_prefill_backward.argtypes = [vp] * 14 + [i] * 6 + [vp, ctypes.c_size_t, vp]
+    sz, st = ctypes.c_size_t, ctypes.POINTER(_Strides)
+    lib.kda_conv_prefill.argtypes = [vp, st, vp, vp, vp, vp, vp, st, vp] + [i] * 7 + [vp]
+    lib.kda_conv_step.argtypes = [vp, st, vp, vp, vp, vp, st] + [i] * 6 + [vp]
+    lib.kda_conv_backward_workspace_bytes.argtypes = [i] * 6
+    lib.kda_conv_backward_workspace_bytes.restype = sz
+    lib.kda_conv_backward.argtypes = [vp, st, vp, vp, vp, vp, st, vp, vp, st, vp, vp, vp] + [i] * 7 + [vp, sz, vp]
+    lib.kda_ssm_prefill_workspace_bytes.argtypes = [i] * 7
+    lib.kda_ssm_prefill_workspace_bytes.restype = sz
+    lib.kda_ssm_prefill.argtypes = [vp] * 10 + [ctypes.POINTER(_SsmStrides)] + [i] * 7 + [vp, sz, vp]
+    lib.kda_ssm_step.argtypes = [vp] * 8 + [i] * 6 + [vp]
+    lib.kda_ssm_backward_workspace_bytes.argtypes = [i] * 7
+    lib.kda_ssm_backward_workspace_bytes.restype = sz
+    lib.kda_ssm_backward.argtypes = ([vp] * 16 + [ctypes.POINTER(_SsmStrides), ctypes.POINTER(_SsmGradStrides)] +
+                                     [i] * 7 + [vp, sz, vp])
+    lib.kda_state_store.argtypes = [vp] * 4 + [i] * 6 + [vp]
+    lib.kda_state_load.argtypes = [vp] * 4 + [i] * 6 + [vp]
+    for f in (lib.kda_conv_prefill, lib.kda_conv_step, lib.kda_conv_backward, lib.kda_ssm_prefill, lib.kda_ssm_step,
+              lib.kda_ssm_backward, lib.kda_state_store, lib.kda_state_load):
+        f.restype = i
     for f in (lib.kda_chunk_prefill, lib.kda_chunk_prefill_snap, lib.kda_chunk_prefill_noalloc, lib.kda_prefill_plan, lib.kda_chunk_prefill_segments,
               lib.kda_decode_step, lib.kda_decode_tokens, lib.kda_segment_transfer,
               lib.kda_segment_merge, lib.kda_prefill_backward):
@@ -451,3 +497,299 @@ def prefill_backward(q, k, v, log_alpha, beta, S0=None, dO=None, dS_T=None, work
                                      _stream())
     _check(rc, "kda_prefill_backward")
     return out
+
+
+# ------------------------------------------------------- companion operators
+def _here(t: torch.Tensor, name: str) -> None:
+    """The call runs on the current device's current stream."""
+    if not t.is_cuda:
+        raise KdaError(f"{name} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise KdaError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
+    _here(t, name)
+    _io(t, name, dtype, shape)
+
+
+def _view(t: torch.Tensor, name: str, dtype: torch.dtype, shape, rows: bool = True) -> _Strides:
+    """A [B, H, T] or (rows) [B, H, T, d] tensor with any strides but a contiguous last
+    dimension of rows; the library checks their alignment."""
+    _here(t, name)
+    if t.dtype != dtype:
+        raise KdaError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise KdaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if rows and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise KdaError(f"{name} must have contiguous rows")
+    return _Strides(*t.stride()[:3])
+
+
+def _new_like(t: torch.Tensor, dtype=None) -> torch.Tensor:
+    """A new tensor in the memory order of t where t is dense, contiguous otherwise."""
+    return torch.empty_like(t, dtype=dtype or t.dtype)
+
+
+def _scratch(workspace, need: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    _here(workspace, "workspace")
+    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+        raise KdaError(f"workspace must be a contiguous device tensor of at least {need} bytes")
+    return workspace
+
+
+def _dtype(t: torch.Tensor) -> int:
+    if t.dtype not in _DT:
+        raise KdaError(f"unsupported dtype {t.dtype}")
+    return _DT[t.dtype]
+
+
+def _rank(t: torch.Tensor, name: str, n: int) -> None:
+    if t.dim() != n:
+        raise KdaError(f"{name} has {t.dim()} dimensions, expected {n}")
+
+
+def _act(activation) -> int:
+    if activation not in _ACT:
+        raise KdaError(f"unknown activation {activation!r} (None or 'silu')")
+    return _ACT[activation]
+
+
+def _conv_args(x, weight, bias, state, B, H, d):
+    _rank(weight, "weight", 3)
+    K = weight.shape[2]
+    _dense(weight, "weight", x.dtype, (H, d, K))
+    if bias is not None:
+        _dense(bias, "bias", x.dtype, (H, d))
+    if state is not None:
+        _dense(state, "state", x.dtype, (B, H, K - 1, d))
+    return K
+
+
+def conv_prefill(x, weight, bias=None, state=None, activation="silu", lens=None, o=None, state_out=None):
+    """Short causal convolution with K taps per channel (kda_conv_prefill).  x [B,H,T,d] (strides
+    free, rows contiguous: a projection's [B,T,H*d] output as .view(B,T,H,d).transpose(1,2)),
+    weight [H,d,K], bias [H,d], state [B,H,K-1,d] (the tokens before, or None), lens [B] int32 or
+    None.  Returns o (contiguous unless given, rows behind lens not written) and the state after
+    the sequence."""
+    _rank(x, "x", 4)
+    B, H, T, d = x.shape
+    dt = _dtype(x)
+    xs = _view(x, "x", x.dtype, (B, H, T, d))
+    K = _conv_args(x, weight, bias, state, B, H, d)
+    if lens is not None:
+        _dense(lens, "lens", torch.int32, (B,))
+    if o is None:
+        o = torch.empty(B, H, T, d, dtype=x.dtype, device=x.device)
+    os_ = _view(o, "o", x.dtype, (B, H, T, d))
+    if state_out is None:
+        state_out = torch.empty(B, H, K - 1, d, dtype=x.dtype, device=x.device)
+    _dense(state_out, "state_out", x.dtype, (B, H, K - 1, d))
+    rc = load().kda_conv_prefill(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state), _ptr(lens), _ptr(o), os_,
+                                 _ptr(state_out), B, H, T, d, K, _act(activation), dt, _stream())
+    _check(rc, "kda_conv_prefill")
+    return o, state_out
+
+
+def conv_step(x, state, weight, bias=None, activation="silu", o=None) -> torch.Tensor:
+    """One token of the convolution: x [N,H,d] (strides free), state [N,H,K-1,d] moved on in
+    place.  Returns o [N,H,d]."""
+    _rank(x, "x", 3)
+    N, H, d = x.shape
+    dt = _dtype(x)
+    xs = _view(x, "x", x.dtype, (N, H, d))
+    K = _conv_args(x, weight, bias, state, N, H, d)
+    if state is None:
+        raise KdaError("state is required")
+    if o is None:
+        o = torch.empty(N, H, d, dtype=x.dtype, device=x.device)
+    os_ = _view(o, "o", x.dtype, (N, H, d))
+    rc = load().kda_conv_step(_ptr(x), xs, _ptr(state), _ptr(weight), _ptr(bias), _ptr(o), os_, N, H, d, K,
+                              _act(activation), dt, _stream())
+    _check(rc, "kda_conv_step")
+    return o
+
+
+def conv_backward(x, weight, bias, state, dO, dstate_out=None, activation="silu", workspace=None):
+    """Gradients of conv_prefill (without lens).  Returns a dict: dx, dweight, and dbias and dstate
+    where bias and state were given, in x's dtype."""
+    _rank(x, "x", 4)
+    B, H, T, d = x.shape
+    dt = _dtype(x)
+    xs = _view(x, "x", x.dtype, (B, H, T, d))
+    K = _conv_args(x, weight, bias, state, B, H, d)
+    dos = _view(dO, "dO", x.dtype, (B, H, T, d))
+    if dstate_out is not None:
+        _dense(dstate_out, "dstate_out", x.dtype, (B, H, K - 1, d))
+    out = dict(dx=_new_like(x), dweight=_new_like(weight))
+    if bias is not None:
+        out["dbias"] = _new_like(bias)
+    if state is not None:
+        out["dstate"] = _new_like(state)
+    lib = load()
+    need = int(lib.kda_conv_backward_workspace_bytes(B, H, T, d, K, dt))
+    workspace = _scratch(workspace, need, x.device)
+    rc = lib.kda_conv_backward(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state), _ptr(dO), dos, _ptr(dstate_out),
+                               _ptr(out["dx"]), _view(out["dx"], "dx", x.dtype, (B, H, T, d)), _ptr(out["dweight"]),
+                               _ptr(out.get("dbias")), _ptr(out.get("dstate")), B, H, T, d, K, _act(activation), dt,
+                               _ptr(workspace), workspace.numel() * workspace.element_size(), _stream())
+    _check(rc, "kda_conv_backward")
+    return out
+
+
+def _ssm_args(q, k, v, log_alpha, beta, D, S0):
+    _rank(k, "k", 4)
+    _rank(v, "v", 4)
+    (B, G, T, dk), (H, dv) = k.shape, (v.shape[1], v.shape[3])
+    dt = v.dtype
+    _dtype(v)
+    st = _SsmStrides(q=_view(q, "q", dt, (B, G, T, dk)), k=_view(k, "k", dt, (B, G, T, dk)),
+                     v=_view(v, "v", dt, (B, H, T, dv)),
+                     log_alpha=_view(log_alpha, "log_alpha", dt, (B, H, T), rows=False),
+                     beta=_view(beta, "beta", dt, (B, H, T), rows=False))
+    if D is not None:
+        _dense(D, "D", dt, (H,))
+    if S0 is not None:
+        _dense(S0, "S0", torch.float32, (B, H, dk, dv))
+    return (B, H, G, T, dk, dv), st
+
+
+def ssm_prefill_workspace_bytes(B: int, H: int, G: int, T: int, dk: int, dv: int, dtype: torch.dtype) -> int:
+    """Workspace with which kda_ssm_prefill may cut the sequences into segments (0: it would not)."""
+    if dtype not in _DT:
+        raise KdaError(f"unsupported dtype {dtype}")
+    return int(load().kda_ssm_prefill_workspace_bytes(B, H, G, T, dk, dv, _DT[dtype]))
+
+
+def ssm_prefill(q, k, v, log_alpha, beta, D=None, S0=None, lens=None, o=None, S_T=None, workspace="auto"):
+    """Selective state space scan over a prompt (kda_ssm_prefill): per head
+    S_t = exp(log_alpha_t) S_{t-1} + beta_t k_t v_t^T, o_t = S_t^T q_t + D v_t.  q, k [B,G,T,dk]
+    shared by the H / G heads of a group, v [B,H,T,dv], log_alpha, beta [B,H,T] (strides free, rows
+    contiguous), D [H] or None, S0 [B,H,dk,dv] fp32 or None, lens [B] int32 or None.  Returns o (in
+    v's memory order unless given, rows behind lens not written) and S_T fp32.  workspace: "auto",
+    None (each sequence in one piece) or a device uint8 tensor."""
+    (B, H, G, T, dk, dv), st = _ssm_args(q, k, v, log_alpha, beta, D, S0)
+    dt = _dtype(v)
+    if lens is not None:
+        _dense(lens, "lens", torch.int32, (B,))
+    if o is None:
+        o = _new_like(v)
+    st.o = _view(o, "o", v.dtype, (B, H, T, dv))
+    if S_T is None:
+        S_T = torch.empty(B, H, dk, dv, dtype=torch.float32, device=v.device)
+    _dense(S_T, "S_T", torch.float32, (B, H, dk, dv))
+    lib = load()
+    if isinstance(workspace, str):
+        need = int(lib.kda_ssm_prefill_workspace_bytes(B, H, G, T, dk, dv, dt))
+        workspace = torch.empty(need, dtype=torch.uint8, device=v.device) if need else None
+    elif workspace is not None:
+        _scratch(workspace, 0, v.device)
+    rc = lib.kda_ssm_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(D), _ptr(S0), _ptr(lens),
+                             _ptr(o), _ptr(S_T), st, B, H, G, T, dk, dv, dt, _ptr(workspace),
+                             0 if workspace is None else workspace.numel() * workspace.element_size(), _stream())
+    _check(rc, "kda_ssm_prefill")
+    return o, S_T
+
+
+def ssm_step(q, k, v, log_alpha, beta, S, D=None, o=None) -> torch.Tensor:
+    """One token of the scan: q, k [N,G,dk], v [N,H,dv], log_alpha, beta [N,H], S [N,H,dk,dv] fp32
+    updated in place.  Returns o [N,H,dv]."""
+    _rank(k, "k", 3)
+    _rank(v, "v", 3)
+    (N, G, dk), (H, dv) = k.shape, v.shape[1:]
+    dt = _dtype(v)
+    for name, t, shp in (("q", q, (N, G, dk)), ("k", k, (N, G, dk)), ("v", v, (N, H, dv)),
+                         ("log_alpha", log_alpha, (N, H)), ("beta", beta, (N, H))):
+        _dense(t, name, v.dtype, shp)
+    if D is not None:
+        _dense(D, "D", v.dtype, (H,))
+    _dense(S, "S", torch.float32, (N, H, dk, dv))
+    if o is None:
+        o = torch.empty(N, H, dv, dtype=v.dtype, device=v.device)
+    _dense(o, "o", v.dtype, (N, H, dv))
+    rc = load().kda_ssm_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(D), _ptr(S), _ptr(o),
+                             N, H, G, dk, dv, dt, _stream())
+    _check(rc, "kda_ssm_step")
+    return o
+
+
+def ssm_backward(q, k, v, log_alpha, beta, D=None, S0=None, dO=None, dS_T=None, workspace=None):
+    """Gradients of L = sum(dO * o) + sum(dS_T * S_T) of ssm_prefill (without lens).  Returns a dict:
+    dq, dk (summed over a group's heads), dv, dlog_alpha, dbeta, and dD and dS0 (fp32) where D and S0
+    were given."""
+    (B, H, G, T, dk, dv), st = _ssm_args(q, k, v, log_alpha, beta, D, S0)
+    dt = _dtype(v)
+    if dO is None:
+        raise KdaError("dO is required")
+    if dS_T is not None:
+        _dense(dS_T, "dS_T", torch.float32, (B, H, dk, dv))
+    out = dict(dq=_new_like(q), dk=_new_like(k), dv=_new_like(v), dlog_alpha=_new_like(log_alpha), dbeta=_new_like(beta))
+    gst = _SsmGradStrides(dO=_view(dO, "dO", v.dtype, (B, H, T, dv)),
+                          **{n: _Strides(*t.stride()[:3]) for n, t in out.items()})
+    if D is not None:
+        out["dD"] = _new_like(D)
+    if S0 is not None:
+        out["dS0"] = _new_like(S0)
+    lib = load()
+    need = int(lib.kda_ssm_backward_workspace_bytes(B, H, G, T, dk, dv, dt))
+    workspace = _scratch(workspace, need, v.device)
+    rc = lib.kda_ssm_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(D), _ptr(S0), _ptr(dO),
+                              _ptr(dS_T), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dlog_alpha"]),
+                              _ptr(out["dbeta"]), _ptr(out.get("dD")), _ptr(out.get("dS0")), st, gst, B, H, G, T, dk, dv,
+                              dt, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream())
+    _check(rc, "kda_ssm_backward")
+    return out
+
+
+def state_cache(nslots: int, H: int, dk: int, dv: int, fmt: str = "int8", device="cuda"):
+    """An empty quantised state cache: values [nslots,H,dk,dv] ("int8", or "e4m3" as
+    torch.float8_e4m3fn) and scale exponents [nslots,H,dk,dv/32] uint8."""
+    if fmt not in ("int8", "e4m3"):
+        raise KdaError(f"unknown cache format {fmt!r} ('int8' or 'e4m3')")
+    if dv % 32:
+        raise KdaError(f"rows of {dv} values are not whole blocks of 32")
+    cache = torch.zeros(nslots, H, dk, dv, dtype=torch.uint8, device=device)
+    return (cache.view(torch.int8 if fmt == "int8" else torch.float8_e4m3fn),
+            torch.ones(nslots, H, dk, dv // 32, dtype=torch.uint8, device=device))
+
+
+def _cache_args(cache, scales, slots):
+    _rank(cache, "cache", 4)
+    if cache.dtype not in _CACHE:
+        raise KdaError(f"cache has dtype {cache.dtype}, expected torch.int8 or torch.float8_e4m3fn")
+    nslots, H, dk, dv = cache.shape
+    _dense(cache, "cache", cache.dtype, cache.shape)
+    _dense(scales, "scales", torch.uint8, (nslots, H, dk, dv // 32))
+    _rank(slots, "slots", 1)
+    _dense(slots, "slots", torch.int32, slots.shape)
+    return nslots, H, dk, dv
+
+
+def state_store(S, slots, cache, scales) -> None:
+    """Quantise states S [..., H,dk,dv] fp32 into the entries slots [n] int32 of a state_cache
+    (kda_state_store; S may be prefill_snap's S_snap with slots.numel() states).  Slots outside the
+    cache are skipped; of entries that name the same slot the last one is stored."""
+    nslots, H, dk, dv = _cache_args(cache, scales, slots)
+    n = slots.numel()
+    if S.dim() < 3 or tuple(S.shape[-3:]) != (H, dk, dv) or S.numel() != n * H * dk * dv:
+        raise KdaError(f"S has shape {tuple(S.shape)}, expected {n} states of {(H, dk, dv)}")
+    _dense(S, "S", torch.float32, S.shape)
+    rc = load().kda_state_store(_ptr(S), _ptr(slots), _ptr(cache), _ptr(scales), n, nslots, H, dk, dv,
+                                _CACHE[cache.dtype], _stream())
+    _check(rc, "kda_state_store")
+
+
+def state_load(cache, scales, slots, S=None) -> torch.Tensor:
+    """States [n,H,dk,dv] fp32 of the entries slots [n] int32 of a state_cache (zeros for slots
+    outside it)."""
+    nslots, H, dk, dv = _cache_args(cache, scales, slots)
+    n = slots.numel()
+    if S is None:
+        S = torch.empty(n, H, dk, dv, dtype=torch.float32, device=cache.device)
+    _dense(S, "S", torch.float32, (n, H, dk, dv))
+    rc = load().kda_state_load(_ptr(cache), _ptr(scales), _ptr(slots), _ptr(S), n, nslots, H, dk, dv,
+                               _CACHE[cache.dtype], _stream())
+    _check(rc, "kda_state_load")
+    return S

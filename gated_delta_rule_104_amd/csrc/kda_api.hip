@@ -13,6 +13,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "kda_host.hpp"
 #include "kda_launch.hpp"
 
 namespace {
@@ -474,6 +475,22 @@ kda_status check_prefill_args(const void* q, const void* k, const void* v, const
 }
 
 }  // namespace
+
+namespace kda {
+
+kda_status api_fail(kda_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return st;
+}
+kda_status api_ok() { return ok(); }
+int api_cu_count() { return cu_count(); }
+bool api_check_on() { return opt(OPT_CHECK) == 1; }
+bool api_log_on() { return log_on(); }
+
+}  // namespace kda
 
 extern "C" {
 

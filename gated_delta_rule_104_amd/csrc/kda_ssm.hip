@@ -1,0 +1,1333 @@
+// Selective state space scan with one decay per head and token, prefill and
+// gradients, in 64-token chunks on the matrix cores.
+//
+// One form serves every pass.  For row vectors Q_i, K_i (the contracted ones) and
+// V_i of a chunk, decays x_i <= 0 and weights rho_i, kappa_j, with l_i the sum of
+// x up to and including i,
+//     Y_i  = rho_i ( e^{l_i} S^T Q_i + sum_{j <= i} e^{l_i - l_j} kappa_j (Q_i.K_j) V_j )
+//     S   <- e^{l_end} S + sum_j e^{l_end - l_j} kappa_j K_j V_j^T.
+//   pass                Q   K   V   kappa  rho   result
+//   outputs             q   k   v   beta   1     o (+ D v)
+//   reversed outputs    k   q   dO  1      1     z = dS^T k: dv = beta z + D dO, dbeta = v.z
+//   dq (heads summed)   dO  v   k   beta   1     dq
+//   dk (heads summed)   v   dO  q   1      beta  dk
+// The reversed passes walk the tokens backwards; a position's decay is then the
+// one of the token after it (1 at the last token).
+//
+// Decays.  e^{l_i - l_j} is never formed from sums over the chunk, whose
+// difference would lose digits: sums run inside blocks of 16 tokens only, from
+// the block's start (u_i), to its end (w_j) and over whole blocks (E_J), so that
+// e^{l_i - l_j} = w_j E.. u_i across blocks is a product of factors <= 1, and
+// inside a block the exponential of a difference of 16-token sums.  Nothing
+// overflows for any log_alpha <= 0; -inf is held at 2^-180, which is zero in fp32.
+//
+// Tiles.  v_mfma 16x16: the accumulator's rows 4g + e (g = lane / 16) are also the
+// contraction order of the next product's operand, so the scores (formed
+// transposed) and the state feed it from registers.  Rows of the state and columns
+// of V are taken in the order 32c + 8(r / 4) + 4(odd) + r % 4 for row r of an (even,
+// odd) pair of tiles, which makes a lane's share of a pair eight consecutive
+// channels: q is then read in its natural order and results stored 16 bytes a lane.
+//
+// Precision.  bf16 inputs are exact operands.  The scores and the state are
+// rounded once to bf16 where they multiply V and Q (both times one rounding in
+// front of an fp32 sum, like the output's own); the weighted V that updates the
+// fp32 state is carried in three bf16 terms (24 bits), as the state is an fp32
+// result.  The gradient of log_alpha is a difference of two sums that nearly
+// cancel, so the score sums it needs are taken from fp32 scores and the state
+// terms from a two-term (16-bit) state.  fp32 inputs run the same kernels on the
+// fp32 matrix instructions.
+#include <mutex>
+
+#include "kda_ops.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int CH = kSsmChunk;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// --------------------------------------------------------------- operands
+template <typename T> struct Op;
+template <> struct Op<bf16> {
+  typedef bf16x8 F;
+  static __device__ __forceinline__ f32x4 mma(f32x4 acc, F a, F b) { return mfma_bf16_k32(acc, a, b); }
+  static __device__ __forceinline__ F round(f32x4 lo, f32x4 hi) {
+    return __builtin_bit_cast(F, u32x4{cvt2(lo[0], lo[1]), cvt2(lo[2], lo[3]), cvt2(hi[0], hi[1]), cvt2(hi[2], hi[3])});
+  }
+  static __device__ __forceinline__ float at(F f, int i) { return (float)f[i]; }
+};
+template <> struct Op<float> {
+  struct F { float v[8]; };
+  static __device__ __forceinline__ f32x4 mma(f32x4 acc, const F& a, const F& b) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc = mfma_f32_k4(acc, a.v[i], b.v[i]);
+    return acc;
+  }
+  static __device__ __forceinline__ F round(f32x4 lo, f32x4 hi) {
+    return F{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  }
+  static __device__ __forceinline__ float at(const F& f, int i) { return f.v[i]; }
+};
+
+// The terms of an fp32 operand: NT bf16 values whose sum is x to 8 NT bits
+// (fp32: x itself).
+template <typename T, int NT>
+struct Split {
+  typename Op<T>::F t[sizeof(T) == 2 ? NT : 1];
+  __device__ __forceinline__ Split(f32x4 lo, f32x4 hi) {
+    t[0] = Op<T>::round(lo, hi);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int n = 1; n < NT; ++n) {
+        // the remainder of each rounding is exact in fp32
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          lo[e] -= (float)t[n - 1][e];
+          hi[e] -= (float)t[n - 1][4 + e];
+        }
+        t[n] = Op<T>::round(lo, hi);
+      }
+    }
+  }
+  static constexpr int N = sizeof(T) == 2 ? NT : 1;
+};
+
+// ------------------------------------------------------------- LDS tiles
+// [64 tokens][COLS] of T, 16-byte granules XOR-swizzled by row (swz).
+template <typename T, int COLS>
+struct Tile {
+  static constexpr int R = COLS * (int)sizeof(T);
+  static constexpr int BYTES = CH * R;
+  static constexpr int GPR = R / 16;  // granules per row
+
+  // channels 32m + 8g .. + 7 of row `row`
+  static __device__ __forceinline__ typename Op<T>::F row(const char* s, int row, int m, int g) {
+    if constexpr (sizeof(T) == 2) {
+      return lds_ld<bf16x8>(s, swz<R>(row, (32 * m + 8 * g) * 2));
+    } else {
+      const f32x4 lo = lds_ld<f32x4>(s, swz<R>(row, (32 * m + 8 * g) * 4));
+      const f32x4 hi = lds_ld<f32x4>(s, swz<R>(row, (32 * m + 8 * g) * 4 + 16));
+      return Op<T>::round(lo, hi);
+    }
+  }
+  // Contraction over tokens: lane (g, i) gets tokens 32m + 4g + e and 32m + 16 +
+  // 4g + e of channel 32c + 8(i / 4) + 4 odd + i % 4.  bf16: the transposing read
+  // takes lane i's 8 bytes as row i of a 16 x 4 matrix and returns element
+  // [4e + i / 4][i % 4] as lane i's e-th.
+  static __device__ __forceinline__ typename Op<T>::F col(const char* s, int m, int c, int odd, int g, int i) {
+    if constexpr (sizeof(T) == 2) {
+      const int byte = (32 * c + 8 * (i & 3) + 4 * odd) * 2, r = 32 * m + 4 * g + (i >> 2);
+      const bf16x4 lo = lds_tr16(s, swz<R>(r, byte)), hi = lds_tr16(s, swz<R>(r + 16, byte));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      typename Op<T>::F f;
+      const int byte = (32 * c + 8 * (i >> 2) + 4 * odd + (i & 3)) * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f.v[e] = lds_ld<float>(s, swz<R>(32 * m + 4 * g + e, byte));
+        f.v[4 + e] = lds_ld<float>(s, swz<R>(32 * m + 16 + 4 * g + e, byte));
+      }
+      return f;
+    }
+  }
+};
+
+// A tile on its way from HBM: NT threads hold 16-byte granules of it.
+template <typename T, int COLS, int NT>
+struct Fetch {
+  static constexpr int N = CH * Tile<T, COLS>::GPR / NT;
+  u32x4 r[N];
+  // position p of the chunk is token tok0 + p, or tok0 + n - 1 - p reversed; rows past n are zero
+  template <bool REV>
+  __device__ __forceinline__ void get(const T* p, long long st, int tok0, int n, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int gi = tid + i * NT, row = gi / Tile<T, COLS>::GPR, c = gi % Tile<T, COLS>::GPR;
+      r[i] = u32x4{0u, 0u, 0u, 0u};
+      if (row < n)
+        r[i] = *reinterpret_cast<const u32x4*>(p + (long long)(REV ? tok0 + n - 1 - row : tok0 + row) * st +
+                                               c * (16 / (int)sizeof(T)));
+    }
+  }
+  __device__ __forceinline__ void put(char* s, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int gi = tid + i * NT, row = gi / Tile<T, COLS>::GPR, c = gi % Tile<T, COLS>::GPR;
+      lds_st<u32x4>(s, swz<Tile<T, COLS>::R>(row, 16 * c), r[i]);
+    }
+  }
+};
+
+// ---------------------------------------------------------------- decays
+// Per head of the chunk, floats.  PB: sums from the block's start; U: u rho; W: w
+// kappa; KP: kappa; RH: rho (or, in the reversed outputs, beta); IN: rho e^{l_i};
+// WS: kappa e^{l_end - l_j}; ET: E of the four blocks; GM: e^{l_end}.  The first
+// four are read only while the scores are formed.
+enum { V_PB = 0, V_U = 64, V_W = 128, V_KP = 192, V_RH = 256, V_IN = 320, V_WS = 384, V_ET = 448, V_GM = 452, V_SIZE = 456 };
+
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// One wave fills a head's vectors; lane r is position r with decay x (log2 units).
+__device__ __forceinline__ void fill_vec(float* v, int r, float x, float kappa, float rho, float rh) {
+  x = x < -180.f ? -180.f : x;  // (a NaN passes)
+  float pre = x;
+  pre += dpp<DPP_ROW_SHR + 1>(pre);
+  pre += dpp<DPP_ROW_SHR + 2>(pre);
+  pre += dpp<DPP_ROW_SHR + 4>(pre);
+  pre += dpp<DPP_ROW_SHR + 8>(pre);
+  constexpr int DPP_ROW_SHL = 0x100;
+  float suf = dpp<DPP_ROW_SHL + 1>(x);
+  suf += dpp<DPP_ROW_SHL + 1>(suf);
+  suf += dpp<DPP_ROW_SHL + 2>(suf);
+  suf += dpp<DPP_ROW_SHL + 4>(suf);
+  suf += dpp<DPP_ROW_SHL + 8>(suf);
+  const float et = ex2(__shfl(pre, r | 15));
+  const float e0 = __shfl(et, 0), e1 = __shfl(et, 16), e2 = __shfl(et, 32), e3 = __shfl(et, 48);
+  const int blk = r >> 4;
+  const float before = (blk > 0 ? e0 : 1.f) * (blk > 1 ? e1 : 1.f) * (blk > 2 ? e2 : 1.f);
+  const float after = (blk < 1 ? e1 : 1.f) * (blk < 2 ? e2 : 1.f) * (blk < 3 ? e3 : 1.f);
+  const float u = ex2(pre), w = ex2(suf);
+  v[V_PB + r] = pre;
+  v[V_U + r] = u * rho;
+  v[V_W + r] = w * kappa;
+  v[V_KP + r] = kappa;
+  v[V_RH + r] = rh;
+  v[V_IN + r] = u * before * rho;
+  v[V_WS + r] = w * after * kappa;
+  if ((r & 15) == 0) v[V_ET + blk] = et;
+  if (r == 0) v[V_GM] = e0 * e1 * e2 * e3;
+}
+
+// The decay of position p in log2 units: the token's own, or reversed the next
+// token's (0 behind the last).
+template <typename T, bool REV>
+__device__ __forceinline__ float decay_at(const T* la, long long st, int tok0, int n, int Ttot, int p) {
+  if (p >= n) return 0.f;
+  const int t = REV ? tok0 + n - p : tok0 + p;
+  if (REV && t >= Ttot) return 0.f;
+  const float x = to_f32(la[(long long)t * st]) * kLog2e;
+  return x;
+}
+
+// ---------------------------------------------------------------- scores
+// Transposed score tiles, bf16 or fp32, as the operand of the product with V:
+// slot (I, J / 2) holds, lane by lane, tiles (I, 2m) and (I, 2m + 1).
+template <typename T>
+struct Scores {
+  static constexpr int LANE = 8 * (int)sizeof(T);  // bytes of a lane in a slot
+  static constexpr int SLOT = 64 * LANE;
+  static constexpr int BYTES = 6 * SLOT;
+  static __device__ __forceinline__ int slot(int I, int m) { return I + (I == 3) + m; }
+  static __device__ __forceinline__ void put(char* s, int I, int J, int l, f32x4 v) {
+    char* p = s + slot(I, J >> 1) * SLOT + l * LANE + (J & 1) * 4 * (int)sizeof(T);
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4*>(p) = pack4(v);
+    else *reinterpret_cast<f32x4*>(p) = v;
+  }
+  static __device__ __forceinline__ typename Op<T>::F get(const char* s, int I, int m, int l) {
+    const char* p = s + slot(I, m) * SLOT + l * LANE;
+    if constexpr (sizeof(T) == 2) return *reinterpret_cast<const bf16x8*>(p);
+    else return Op<T>::round(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16));
+  }
+  // the upper halves of the diagonal slots are never written again
+  static __device__ __forceinline__ void clear(char* s, int tid, int nt) {
+    for (int i = tid * 16; i < BYTES; i += nt * 16) *reinterpret_cast<u32x4*>(s + i) = u32x4{0u, 0u, 0u, 0u};
+  }
+};
+
+// tile t of the ten (I, J <= I), diagonal first
+__device__ __forceinline__ int tile_i(int t) { return (int)((0x0fe9e4u >> (2 * t)) & 3u); }  // 0 1 2 3 1 2 2 3 3 3
+__device__ __forceinline__ int tile_j(int t) { return (int)((0x0910e4u >> (2 * t)) & 3u); }  // 0 1 2 3 0 0 1 0 1 2
+
+// decayed, weighted scores of a transposed tile: rows j = 16J + 4g + e, column i = 16I + r16
+__device__ __forceinline__ f32x4 weigh(f32x4 acc, const float* v, int I, int J, int g, int r16) {
+  f32x4 m;
+  if (I == J) {
+    const float pi = v[V_PB + 16 * I + r16];
+    const f32x4 pj = *reinterpret_cast<const f32x4*>(v + V_PB + 16 * J + 4 * g);
+    const f32x4 kp = *reinterpret_cast<const f32x4*>(v + V_KP + 16 * J + 4 * g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = 4 * g + e <= r16 ? acc[e] * (ex2(pi - pj[e]) * kp[e]) : 0.f;
+  } else {
+    float c = v[V_U + 16 * I + r16];
+    for (int b = J + 1; b < I; ++b) c *= v[V_ET + b];
+    const f32x4 wj = *reinterpret_cast<const f32x4*>(v + V_W + 16 * J + 4 * g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = acc[e] * (c * wj[e]);
+  }
+  return m;
+}
+
+// -------------------------------------------------------- state and results
+// A wave's state: NK = rows / 16 by two column tiles.
+template <int NK>
+struct State {
+  f32x4 t[NK][2];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int a = 0; a < NK; ++a) t[a][0] = t[a][1] = zero4();
+  }
+  __device__ __forceinline__ void scale(float s) {
+#pragma unroll
+    for (int a = 0; a < NK; ++a)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[a][p][e] *= s;
+  }
+};
+__device__ __forceinline__ int pair_chan(int tile, int r) { return 32 * (tile >> 1) + 8 * (r >> 2) + 4 * (tile & 1) + (r & 3); }
+
+// S += K^T (w V): w the per-token weights, V the wave's two column tiles (two
+// 32-token halves each)
+template <typename T, int NK, typename KT>
+__device__ __forceinline__ void update(State<NK>& S, const char* ktile, const typename Op<T>::F (&vf)[2][2], const float* ws,
+                                       int g, int i) {
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const f32x4 w0 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 4 * g);
+    const f32x4 w1 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 16 + 4 * g);
+    f32x4 lo[2], hi[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        lo[p][e] = Op<T>::at(vf[p][m], e) * w0[e];
+        hi[p][e] = Op<T>::at(vf[p][m], 4 + e) * w1[e];
+      }
+    const Split<T, 3> x0(lo[0], hi[0]), x1(lo[1], hi[1]);
+#pragma unroll
+    for (int a = 0; a < NK; ++a) {
+      const typename Op<T>::F kf = KT::col(ktile, m, a >> 1, a & 1, g, i);
+#pragma unroll
+      for (int n = Split<T, 3>::N - 1; n >= 0; --n) {
+        S.t[a][0] = Op<T>::mma(S.t[a][0], kf, x0.t[n]);
+        S.t[a][1] = Op<T>::mma(S.t[a][1], kf, x1.t[n]);
+      }
+    }
+  }
+}
+
+// Y^T[p][I] = S^T Q^T (rows: the wave's columns, columns: tokens), NT terms of S
+template <typename T, int NK, int NT, typename QT>
+__device__ __forceinline__ void inter(f32x4 (&y)[2][4], const State<NK>& S, const char* qtile, int g, int i) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int I = 0; I < 4; ++I) y[p][I] = zero4();
+#pragma unroll
+  for (int m = 0; m < NK / 2; ++m) {
+    const Split<T, NT> s0(S.t[2 * m][0], S.t[2 * m + 1][0]), s1(S.t[2 * m][1], S.t[2 * m + 1][1]);
+#pragma unroll
+    for (int I = 0; I < 4; ++I) {
+      const typename Op<T>::F qf = QT::row(qtile, 16 * I + i, m, g);
+#pragma unroll
+      for (int n = Split<T, NT>::N - 1; n >= 0; --n) {
+        y[0][I] = Op<T>::mma(y[0][I], s0.t[n], qf);
+        y[1][I] = Op<T>::mma(y[1][I], s1.t[n], qf);
+      }
+    }
+  }
+}
+
+// Y^T += V^T M^T
+template <typename T>
+__device__ __forceinline__ void intra(f32x4 (&y)[2][4], const typename Op<T>::F (&vf)[2][2], const char* scores, int l) {
+#pragma unroll
+  for (int I = 0; I < 4; ++I)
+#pragma unroll
+    for (int m = 0; m <= I / 2; ++m) {
+      const typename Op<T>::F mf = Scores<T>::get(scores, I, m, l);
+      y[0][I] = Op<T>::mma(y[0][I], vf[0][m], mf);
+      y[1][I] = Op<T>::mma(y[1][I], vf[1][m], mf);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* x) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<u32x4*>(p) = u32x4{cvt2(x[0], x[1]), cvt2(x[2], x[3]), cvt2(x[4], x[5]), cvt2(x[6], x[7])};
+  } else {
+    *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+  }
+}
+
+__device__ __forceinline__ int clamp_len(const int* lens, int b, int T) {
+  if (!lens) return T;
+  const int n = lens[b];
+  return n < 0 ? 0 : (n > T ? T : n);
+}
+
+// Work items: `sub` of np workgroups that share one (b, group, segment), which are
+// placed on one XCD (workgroups go to the eight in turn) so that the tiles they
+// share come from its L2.
+struct Item {
+  int b, g, seg, sub;
+  bool valid;
+};
+__device__ __forceinline__ Item item_of(int B, int G, int nseg, int np) {
+  const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
+  const int grp = (y / np) * 8 + x;
+  Item it;
+  it.sub = y % np;
+  it.valid = grp < B * G * nseg;
+  it.seg = grp % nseg;
+  const int bg = grp / nseg;
+  it.g = bg % G;
+  it.b = bg / G;
+  return it;
+}
+unsigned item_grid(long long B, long long G, long long nseg, long long np) { return (unsigned)((B * G * nseg + 7) / 8 * 8 * np); }
+
+// What a pass over [B, G] groups of 64-column units reads.
+struct PassArgs {
+  const void* Q;     // contracted rows, [B, G, T, DK]
+  const void* K;
+  const void* V;     // [B, H, T, dv]
+  const void* V2;    // reversed outputs: v
+  const void* la;
+  const void* beta;
+  const void* D;
+  const int* lens;
+  Str3 qs, ks, vs, v2s, ls, bs, os;
+  void* o;
+  const float* start;  // start state of order o at start + o * B * H * dk * dv, or null (zero)
+  float* end;          // end state of the last order [B, H, dk, dv], or null
+  float* dec;          // state pass: e^{sum of decays} of order o at dec + o * B * H
+  float* c;            // reversed outputs: [B, H * dv / 64, T] each
+  float* r;
+  float* d;
+  int B, H, G, T, dk, dv, nseg, seg_chunks;
+  int norders;  // state pass: orders walked (the last ones' end states may not be needed)
+};
+
+// The state's rows and columns of a lane in global memory, [dk][dv] row-major.
+template <int NK>
+__device__ __forceinline__ void load_state(State<NK>& S, const float* p, int ld, int col0, int g, int i) {
+#pragma unroll
+  for (int a = 0; a < NK; ++a)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S.t[a][c][e] = p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + pair_chan(c, i)];
+}
+template <int NK>
+__device__ __forceinline__ void store_state(const State<NK>& S, float* p, int ld, int col0, int g, int i, float s) {
+#pragma unroll
+  for (int a = 0; a < NK; ++a)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + pair_chan(c, i)] = s * S.t[a][c][e];
+}
+
+// ------------------------------------------------------------- state pass
+// End state of every segment from zero.  Workgroup = two 64-column units of one
+// group, wave = 32 columns of one.
+template <typename T, int DK, bool REV>
+__global__ __launch_bounds__(256, 2) void kda_ssm_state_kernel(PassArgs a) {
+  typedef Tile<T, DK> KT;
+  typedef Tile<T, 64> VT;
+  __shared__ __attribute__((aligned(16))) char smem[KT::BYTES + 2 * VT::BYTES + 2 * V_SIZE * 4];
+  char* const sk = smem;
+  char* const sv = smem + KT::BYTES;
+  float* const vec = reinterpret_cast<float*>(sv + 2 * VT::BYTES);
+  const int cpu = a.dv / 64, nu = a.H / a.G * cpu;  // column units per head, units per group
+  const Item it = item_of(a.B, a.G, a.norders, (nu + 1) / 2);
+  if (!it.valid) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g = l >> 4, i = l & 15;
+  const int len = clamp_len(a.lens, it.b, a.T);
+  const int nch = (len + CH - 1) / CH;
+  const int seg = REV ? a.nseg - 1 - it.seg : it.seg;
+  const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
+  const int uw = wave >> 1, half = wave & 1;
+  const T* K = static_cast<const T*>(a.K) + it.b * a.ks.b + it.g * a.ks.h;
+  int head[2];
+  const T* V[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int un = min(2 * it.sub + u, nu - 1);
+    head[u] = it.g * (a.H / a.G) + un / cpu;
+    V[u] = static_cast<const T*>(a.V) + it.b * a.vs.b + head[u] * a.vs.h + (un % cpu) * 64;
+  }
+  const int hv = head[wave & 1];
+  const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
+  const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
+  State<DK / 16> S;
+  S.zero();
+  float dec = 1.f;
+  Fetch<T, DK, 256> fk;
+  Fetch<T, 64, 256> fv[2];
+  float fx = 0.f, fb = 0.f;
+  auto fetch = [&](int step) {
+    const int c = REV ? c1 - 1 - step : c0 + step;
+    const int tok0 = c * CH, n = min(CH, len - tok0);
+    fk.template get<REV>(K, a.ks.t, tok0, n, tid);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) fv[u].template get<REV>(V[u], a.vs.t, tok0, n, tid);
+    if (wave < 2) {
+      fx = decay_at<T, REV>(la, a.ls.t, tok0, n, a.T, l);
+      fb = !REV && l < n ? to_f32(beta[(long long)(tok0 + l) * a.bs.t]) : 1.f;
+    }
+  };
+  if (c0 < c1) fetch(0);
+  for (int step = 0; step < c1 - c0; ++step) {
+    fk.put(sk, tid);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) fv[u].put(sv + u * VT::BYTES, tid);
+    if (wave < 2) fill_vec(vec + wave * V_SIZE, l, fx, fb, 1.f, 1.f);
+    if (step + 1 < c1 - c0) fetch(step + 1);
+    sync_lds();
+    const float* v = vec + uw * V_SIZE;
+    typename Op<T>::F vf[2][2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv + uw * VT::BYTES, m, half, p, g, i);
+    const float gm = v[V_GM];
+    dec *= gm;
+    S.scale(gm);
+    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, g, i);
+    sync_lds();
+  }
+  const int un = 2 * it.sub + uw;
+  if (un >= nu) return;
+  const size_t bh = (size_t)it.b * a.H + head[uw];
+  // order o's end state lies in slot o + 1
+  float* out = a.end + ((size_t)(it.seg + 1) * a.B * a.H + bh) * a.dk * a.dv;
+  store_state(S, out, a.dv, (un % cpu) * 64 + half * 32, g, i, 1.f);
+  if (half == 0 && un % cpu == 0 && l == 0) a.dec[(size_t)it.seg * a.B * a.H + bh] = dec;
+}
+
+// slots[0] = start; slots[o + 1] = dec[o] slots[o] + slots[o + 1], o = 0 .. n - 1
+__global__ __launch_bounds__(256) void kda_ssm_merge_kernel(const float* start, float* slots, const float* dec, long long BH,
+                                                            int elems, int n) {
+  const long long f = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (f >= BH * elems) return;
+  const long long bh = f / elems;
+  f32x4 s = start ? *reinterpret_cast<const f32x4*>(start + f) : zero4();
+  *reinterpret_cast<f32x4*>(slots + f) = s;
+  for (int o = 0; o < n; ++o) {
+    float* p = slots + (o + 1) * BH * elems + f;
+    const f32x4 z = *reinterpret_cast<const f32x4*>(p);
+    const float d = dec[o * BH + bh];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = d * s[e] + z[e];
+    *reinterpret_cast<f32x4*>(p) = s;
+  }
+}
+
+__global__ __launch_bounds__(256) void kda_ssm_copy_kernel(const float* src, float* dst, long long n4) {
+  const long long f = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (f < n4) reinterpret_cast<f32x4*>(dst)[f] = src ? reinterpret_cast<const f32x4*>(src)[f] : zero4();
+}
+
+// ----------------------------------------------------------------- outputs
+// Workgroup = two 64-column units of one group over a segment's chunks, wave = 32
+// columns of one unit.  Per chunk: the scores are formed once (Q.K once for both
+// units) and left in LDS; every wave then forms its columns of Y and moves its
+// state on.  The next chunk's tiles are loaded to registers meanwhile.
+// BWD: the reversed pass, which also leaves, per unit and token, what the
+// gradients of beta and log_alpha need:
+//   c[j] = sum_i P_ij (and the state's part), r[i] = sum_j beta_j P_ij (inside the
+//   chunk), d[i] = dO_i.v_i, with P_ij = (dO_i.v_j) (q_i.k_j) e^{l_i - l_j}.
+template <typename T, int DK, bool BWD>
+__global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1) void kda_ssm_out_kernel(PassArgs a) {
+  typedef Tile<T, DK> KT;
+  typedef Tile<T, 64> VT;
+  typedef Scores<T> SC;
+  constexpr int OV = 2 * KT::BYTES, OV2 = OV + 2 * VT::BYTES, OM = OV2 + (BWD ? 2 * VT::BYTES : 0);
+  constexpr int OVEC = OM + 2 * SC::BYTES, ORED = OVEC + 2 * V_SIZE * 4;
+  constexpr int RED = 4 * 64 + 4 * 64;  // column sums by J, row sums by I
+  __shared__ __attribute__((aligned(16))) char smem[ORED + (BWD ? 2 * RED * 4 : 0)];
+  char* const sq = smem;
+  char* const sk = smem + KT::BYTES;
+  char* const sv = smem + OV;
+  char* const sv2 = smem + OV2;
+  char* const sm = smem + OM;
+  float* const vec = reinterpret_cast<float*>(smem + OVEC);
+  float* const red = reinterpret_cast<float*>(smem + ORED);
+  const int cpu = a.dv / 64, nu = a.H / a.G * cpu;
+  const Item it = item_of(a.B, a.G, a.nseg, (nu + 1) / 2);
+  if (!it.valid) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g = l >> 4, i = l & 15;
+  const int len = clamp_len(a.lens, it.b, a.T);
+  const int nch = (len + CH - 1) / CH;
+  const int seg = BWD ? a.nseg - 1 - it.seg : it.seg;
+  const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
+  const int uw = wave >> 1, half = wave & 1;
+  const T* Q = static_cast<const T*>(a.Q) + it.b * a.qs.b + it.g * a.qs.h;
+  const T* K = static_cast<const T*>(a.K) + it.b * a.ks.b + it.g * a.ks.h;
+  int head[2], colu[2];
+  const T *V[2], *V2[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int un = min(2 * it.sub + u, nu - 1);
+    head[u] = it.g * (a.H / a.G) + un / cpu;
+    colu[u] = (un % cpu) * 64;
+    V[u] = static_cast<const T*>(a.V) + it.b * a.vs.b + head[u] * a.vs.h + colu[u];
+    V2[u] = BWD ? static_cast<const T*>(a.V2) + it.b * a.v2s.b + head[u] * a.v2s.h + colu[u] : nullptr;
+  }
+  const int un = 2 * it.sub + uw;
+  const bool mine = un < nu;
+  const int hv = head[wave & 1];
+  const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
+  const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
+  float skip[2] = {0.f, 0.f};
+  if (a.D) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) skip[u] = to_f32(static_cast<const T*>(a.D)[head[u]]);
+  }
+  T* o = static_cast<T*>(a.o) + it.b * a.os.b + head[uw] * a.os.h + colu[uw] + half * 32 + 8 * g;
+  const size_t bh = (size_t)it.b * a.H + head[uw];
+  State<DK / 16> S;
+  if (a.start) load_state(S, a.start + ((size_t)it.seg * a.B * a.H + bh) * a.dk * a.dv, a.dv, colu[uw] + half * 32, g, i);
+  else S.zero();
+  SC::clear(sm, tid, 256);
+  SC::clear(sm + SC::BYTES, tid, 256);
+
+  Fetch<T, DK, 256> fq, fk;
+  Fetch<T, 64, 256> fv[2], fw[2];
+  float fx = 0.f, fb = 0.f;
+  auto fetch = [&](int step) {
+    const int c = BWD ? c1 - 1 - step : c0 + step;
+    const int tok0 = c * CH, n = min(CH, len - tok0);
+    fq.template get<BWD>(Q, a.qs.t, tok0, n, tid);
+    fk.template get<BWD>(K, a.ks.t, tok0, n, tid);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      fv[u].template get<BWD>(V[u], a.vs.t, tok0, n, tid);
+      if constexpr (BWD) fw[u].template get<BWD>(V2[u], a.v2s.t, tok0, n, tid);
+    }
+    if (wave < 2) {
+      fx = decay_at<T, BWD>(la, a.ls.t, tok0, n, a.T, l);
+      fb = l < n ? to_f32(beta[(long long)(BWD ? tok0 + n - 1 - l : tok0 + l) * a.bs.t]) : 0.f;
+    }
+  };
+  if (c0 < c1) fetch(0);
+  for (int step = 0; step < c1 - c0; ++step) {
+    const int c = BWD ? c1 - 1 - step : c0 + step;
+    const int tok0 = c * CH, n = min(CH, len - tok0);
+    fq.put(sq, tid);
+    fk.put(sk, tid);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      fv[u].put(sv + u * VT::BYTES, tid);
+      if constexpr (BWD) fw[u].put(sv2 + u * VT::BYTES, tid);
+    }
+    if (wave < 2) fill_vec(vec + wave * V_SIZE, l, fx, BWD ? 1.f : fb, 1.f, fb);
+    if (step + 1 < c1 - c0) fetch(step + 1);
+    sync_lds();
+
+    // scores, tiles dealt to the waves
+    for (int t = wave; t < 10; t += 4) {
+      const int I = tile_i(t), J = tile_j(t);
+      f32x4 acc = zero4();
+#pragma unroll
+      for (int m = 0; m < DK / 32; ++m)
+        acc = Op<T>::mma(acc, KT::row(sk, 16 * J + i, m, g), KT::row(sq, 16 * I + i, m, g));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float* v = vec + u * V_SIZE;
+        f32x4 mm = weigh(acc, v, I, J, g, i);
+        if constexpr (BWD) {
+          float* rd = red + u * RED;
+          f32x4 dd = zero4();
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            dd = Op<T>::mma(dd, VT::row(sv + u * VT::BYTES, 16 * J + i, m, g), VT::row(sv2 + u * VT::BYTES, 16 * I + i, m, g));
+          const float bi = v[V_RH + 16 * I + i];
+          float cs = 0.f, rs[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float pp = mm[e] * dd[e];
+            cs += pp;
+            rs[e] = bi * pp;
+          }
+          cs += __shfl_xor(cs, 16);
+          cs += __shfl_xor(cs, 32);
+          if (g == 0) rd[64 * J + 16 * I + i] = cs;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) rs[e] += __shfl_xor(rs[e], off);
+          }
+          if (i == 0) *reinterpret_cast<f32x4*>(rd + 256 + 64 * I + 16 * J + 4 * g) = f32x4{rs[0], rs[1], rs[2], rs[3]};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mm[e] += I == J && 4 * g + e == i ? skip[u] : 0.f;
+        }
+        SC::put(sm + u * SC::BYTES, I, J, l, mm);
+      }
+    }
+    const float* v = vec + uw * V_SIZE;
+    f32x4 y[2][4];
+    inter<T, DK / 16, BWD ? 2 : 1, KT>(y, S, sq, g, i);
+#pragma unroll
+    for (int I = 0; I < 4; ++I) {
+      const float s = v[V_IN + 16 * I + i];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[p][I][e] *= s;
+    }
+    typename Op<T>::F vf[2][2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv + uw * VT::BYTES, m, half, p, g, i);
+    S.scale(v[V_GM]);
+    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, g, i);
+    sync_lds();
+    if constexpr (BWD) {
+      // the state's part of c, z.v before the chunk's own part joins z, and dO.v;
+      // left where the score vectors were
+      float* w = vec + uw * V_SIZE;
+#pragma unroll
+      for (int I = 0; I < 4; ++I) {
+        const typename Op<T>::F x = VT::row(sv2 + uw * VT::BYTES, 16 * I + i, half, g);
+        const typename Op<T>::F gy = VT::row(sv + uw * VT::BYTES, 16 * I + i, half, g);
+        float s = 0.f, d = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += y[0][I][e] * Op<T>::at(x, e) + y[1][I][e] * Op<T>::at(x, 4 + e);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d += Op<T>::at(gy, e) * Op<T>::at(x, e);
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        d += __shfl_xor(d, 16);
+        d += __shfl_xor(d, 32);
+        if (g == 0) {
+          w[64 * half + 16 * I + i] = s;
+          w[128 + 64 * half + 16 * I + i] = d;
+        }
+      }
+    }
+    intra<T>(y, vf, sm + uw * SC::BYTES, l);
+#pragma unroll
+    for (int I = 0; I < 4; ++I) {
+      const int p = 16 * I + i;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = y[0][I][e];
+        x[4 + e] = y[1][I][e];
+      }
+      if constexpr (BWD) {
+        const float bi = v[V_RH + p];
+        const typename Op<T>::F gy = VT::row(sv + uw * VT::BYTES, p, half, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = bi * x[e] + skip[uw] * Op<T>::at(gy, e);
+      }
+      if (p < n && mine) store8<T>(o + (long long)(BWD ? tok0 + n - 1 - p : tok0 + p) * a.os.t, x);
+    }
+    sync_lds();
+    if constexpr (BWD) {
+      // wave u writes unit u's sums (and refills that unit's vectors next)
+      if (wave < 2 && 2 * it.sub + wave < nu && l < n) {
+        const float* rd = red + wave * RED;
+        const float* w = vec + wave * V_SIZE;
+        float cs = w[l] + w[64 + l], rs = 0.f;
+        for (int J = 0; J <= (l >> 4); ++J) cs += rd[64 * J + l];
+        for (int I = l >> 4; I < 4; ++I) rs += rd[256 + 64 * I + l];
+        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)head[wave & 1] * cpu + (2 * it.sub + wave) % cpu) * a.T + tok0 + n - 1 - l;
+        a.c[at] = cs;
+        a.r[at] = rs;
+        a.d[at] = w[128 + l] + w[192 + l];
+      }
+    }
+  }
+  if (it.seg == a.nseg - 1 && a.end && mine) {
+    // reversed: the state before the first token owes its own decay too
+    float s = 1.f;
+    if (BWD) s = ex2(fmaxf(to_f32((static_cast<const T*>(a.la) + it.b * a.ls.b + head[uw] * a.ls.h)[0]) * kLog2e, -180.f));
+    store_state(S, a.end + bh * a.dk * a.dv, a.dv, colu[uw] + half * 32, g, i, s);
+  }
+}
+
+// ---------------------------------------------------------- summed over heads
+// dq (REV = false) and dk (REV): V is the group's shared row (k or q, DK
+// columns), Q and K are the heads' rows (dO and v, DV).  Workgroup = HG heads of
+// one group, wave = 32 of the DK columns for all of them, so that the sum over
+// the heads stays in its accumulators; groups with more heads leave one partial
+// result per workgroup.  The forward pass also leaves, per head and token,
+// rs[i] = q_i . (the state's part of dq_i).
+template <typename T, int DV, int DK, bool REV>
+__global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) void kda_ssm_group_kernel(
+    PassArgs a, const void* qrow, Str3 qrs, float* rs, float* parts) {
+  constexpr int HG = 128 / DV, NW = DK / 32, NT = 64 * NW;
+  typedef Tile<T, DV> QT;
+  typedef Tile<T, DK> VT;
+  typedef Scores<T> SC;
+  constexpr int OQ = VT::BYTES, OK = OQ + HG * QT::BYTES, OW = OK + HG * QT::BYTES, OM = OW + (REV ? 0 : VT::BYTES);
+  constexpr int OVEC = OM + HG * SC::BYTES;
+  __shared__ __attribute__((aligned(16))) char smem[OVEC + HG * V_SIZE * 4];
+  char* const sv = smem;
+  char* const sq = smem + OQ;
+  char* const sk = smem + OK;
+  char* const sw = smem + OW;  // forward: the q rows
+  char* const sm = smem + OM;
+  float* const vec = reinterpret_cast<float*>(smem + OVEC);
+  const int R = a.H / a.G, np = (R + HG - 1) / HG;
+  const Item it = item_of(a.B, a.G, a.nseg, np);
+  if (!it.valid) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g = l >> 4, i = l & 15;
+  const int nch = (a.T + CH - 1) / CH;
+  const int seg = REV ? a.nseg - 1 - it.seg : it.seg;
+  const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
+  const T* V = static_cast<const T*>(a.V) + it.b * a.vs.b + it.g * a.vs.h;
+  const T* W = REV ? nullptr : static_cast<const T*>(qrow) + it.b * qrs.b + it.g * qrs.h;
+  const int nh = min(HG, R - it.sub * HG);  // heads of this workgroup
+  int head[HG];
+  const T *Q[HG], *K[HG];
+  State<DV / 16> S[HG];
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+    head[h] = it.g * R + it.sub * HG + min(h, nh - 1);
+    Q[h] = static_cast<const T*>(a.Q) + it.b * a.qs.b + head[h] * a.qs.h;
+    K[h] = static_cast<const T*>(a.K) + it.b * a.ks.b + head[h] * a.ks.h;
+    S[h].zero();
+    if (a.start && h < nh) {
+      // the transposed state: rows are dv channels
+      const float* p = a.start + ((size_t)it.seg * a.B * a.H + (size_t)it.b * a.H + head[h]) * DK * DV;
+#pragma unroll
+      for (int t = 0; t < DV / 16; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          S[h].t[t][c] = *reinterpret_cast<const f32x4*>(p + (size_t)(32 * wave + pair_chan(c, i)) * DV + pair_chan(t, 4 * g));
+    }
+  }
+  const int hv = head[HG == 2 ? (wave & 1) : 0];
+  const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
+  const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
+#pragma unroll
+  for (int h = 0; h < HG; ++h) SC::clear(sm + h * SC::BYTES, tid, NT);
+
+  Fetch<T, DK, NT> fv, fw;
+  Fetch<T, DV, NT> fq[HG], fk[HG];
+  float fx = 0.f, fb = 0.f;
+  auto fetch = [&](int step) {
+    const int c = REV ? c1 - 1 - step : c0 + step;
+    const int tok0 = c * CH, n = min(CH, a.T - tok0);
+    fv.template get<REV>(V, a.vs.t, tok0, n, tid);
+    if constexpr (!REV) fw.template get<REV>(W, qrs.t, tok0, n, tid);
+#pragma unroll
+    for (int h = 0; h < HG; ++h) {
+      const int nn = h < nh ? n : 0;
+      fq[h].template get<REV>(Q[h], a.qs.t, tok0, n, tid);
+      fk[h].template get<REV>(K[h], a.ks.t, tok0, n, tid);
+      (void)nn;
+    }
+    if (wave < HG) {
+      fx = decay_at<T, REV>(la, a.ls.t, tok0, n, a.T, l);
+      // a head past the group's last one gets no weight
+      fb = l < n && wave < nh ? to_f32(beta[(long long)(REV ? tok0 + n - 1 - l : tok0 + l) * a.bs.t]) : 0.f;
+    }
+  };
+  if (c0 < c1) fetch(0);
+  for (int step = 0; step < c1 - c0; ++step) {
+    const int c = REV ? c1 - 1 - step : c0 + step;
+    const int tok0 = c * CH, n = min(CH, a.T - tok0);
+    fv.put(sv, tid);
+    if constexpr (!REV) fw.put(sw, tid);
+#pragma unroll
+    for (int h = 0; h < HG; ++h) {
+      fq[h].put(sq + h * QT::BYTES, tid);
+      fk[h].put(sk + h * QT::BYTES, tid);
+    }
+    if (wave < HG) fill_vec(vec + wave * V_SIZE, l, fx, REV ? 1.f : fb, REV ? fb : 1.f, fb);
+    if (step + 1 < c1 - c0) fetch(step + 1);
+    sync_lds();
+
+    for (int t = wave; t < 10; t += NW) {
+      const int I = tile_i(t), J = tile_j(t);
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+        f32x4 acc = zero4();
+#pragma unroll
+        for (int m = 0; m < DV / 32; ++m)
+          acc = Op<T>::mma(acc, QT::row(sk + h * QT::BYTES, 16 * J + i, m, g), QT::row(sq + h * QT::BYTES, 16 * I + i, m, g));
+        const float* v = vec + h * V_SIZE;
+        f32x4 mm = weigh(acc, v, I, J, g, i);
+        if (REV && I == J) {
+          const float rho = v[V_RH + 16 * I + i];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mm[e] *= rho;
+        }
+        SC::put(sm + h * SC::BYTES, I, J, l, mm);
+      }
+    }
+    sync_lds();
+
+    typename Op<T>::F vf[2][2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv, m, wave, p, g, i);
+    f32x4 y[2][4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int I = 0; I < 4; ++I) y[p][I] = zero4();
+#pragma unroll
+    for (int h = 0; h < HG; ++h) {
+      float* v = vec + h * V_SIZE;
+      f32x4 z[2][4];
+      inter<T, DV / 16, REV ? 1 : 2, QT>(z, S[h], sq + h * QT::BYTES, g, i);
+#pragma unroll
+      for (int I = 0; I < 4; ++I) {
+        const float s = h < nh ? v[V_IN + 16 * I + i] : 0.f;
+        float dot = 0.f;
+        if constexpr (!REV) {
+          const typename Op<T>::F x = VT::row(sw, 16 * I + i, wave, g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot += z[0][I][e] * Op<T>::at(x, e) + z[1][I][e] * Op<T>::at(x, 4 + e);
+          dot *= s;
+          dot += __shfl_xor(dot, 16);
+          dot += __shfl_xor(dot, 32);
+          // (the score vectors are no longer needed)
+          if (g == 0) v[64 * wave + 16 * I + i] = dot;
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[p][I][e] += s * z[p][I][e];
+      }
+      intra<T>(y, vf, sm + h * SC::BYTES, l);
+      S[h].scale(v[V_GM]);
+      update<T, DV / 16, QT>(S[h], sk + h * QT::BYTES, vf, v + V_WS, g, i);
+    }
+#pragma unroll
+    for (int I = 0; I < 4; ++I) {
+      const int p = 16 * I + i;
+      const int tok = REV ? tok0 + n - 1 - p : tok0 + p;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = y[0][I][e];
+        x[4 + e] = y[1][I][e];
+      }
+      if (p < n) {
+        if (np == 1)
+          store8<T>(static_cast<T*>(a.o) + it.b * a.os.b + it.g * a.os.h + (long long)tok * a.os.t + 32 * wave + 8 * g, x);
+        else
+          store8<float>(parts + (((size_t)it.sub * a.B * a.G + (size_t)it.b * a.G + it.g) * a.T + tok) * DK + 32 * wave + 8 * g, x);
+      }
+    }
+    sync_lds();
+    if constexpr (!REV) {
+      if (wave < nh && l < n) {
+        const float* v = vec + wave * V_SIZE;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) s += v[64 * w + l];
+        const int hh = it.g * R + it.sub * HG + wave;
+        rs[((size_t)it.b * a.H + hh) * a.T + tok0 + l] = s;
+      }
+      // (read before this wave refills the same vectors for the next chunk)
+    }
+  }
+}
+
+// out[row] = sum of np partials, rows of dk values
+template <typename T>
+__global__ __launch_bounds__(256) void kda_ssm_parts_kernel(const float* parts, int np, T* out, Str3 os, int B, int G, int T_, int dk) {
+  const long long rows = (long long)B * G * T_;
+  const long long f = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int vpr = dk / 8;
+  const long long row = f / vpr;
+  if (row >= rows) return;
+  const int c = (int)(f % vpr) * 8;
+  float x[8] = {};
+  for (int p = 0; p < np; ++p) {
+    const float* s = parts + ((size_t)p * rows + row) * dk + c;
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(s), hi = *reinterpret_cast<const f32x4*>(s + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] += lo[e];
+      x[4 + e] += hi[e];
+    }
+  }
+  const int t = (int)(row % T_);
+  const long long bg = row / T_;
+  store8<T>(out + (bg / G) * os.b + (bg % G) * os.h + (long long)t * os.t + c, x);
+}
+
+// dlog_alpha and dbeta of one (b, h, segment), and the segment's share of dD.
+//     dlog_alpha[t] = sum_{i >= t in the segment} (rows_i - beta_i dbeta_i) + <S, dS> at its end
+// slots_f, slots_r: start states of the segments in both directions.
+template <typename T>
+__global__ __launch_bounds__(256) void kda_ssm_finish_kernel(PassArgs a, const float* slots_f, const float* slots_r,
+                                                             const float* rs, T* dla, Str3 dls, T* dbeta, Str3 dbs, float* dDp) {
+  __shared__ float sh[8];
+  const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63;
+  const int seg = blockIdx.x % a.nseg;
+  const long long bh = blockIdx.x / a.nseg;
+  const int b = (int)(bh / a.H), h = (int)(bh % a.H), cpu = a.dv / 64;
+  const int t0 = seg * a.seg_chunks * CH, t1 = min(t0 + a.seg_chunks * CH, a.T);
+  const size_t elems = (size_t)a.dk * a.dv, all = (size_t)a.B * a.H * elems;
+  const T* la = static_cast<const T*>(a.la) + b * a.ls.b + h * a.ls.h;
+  const T* beta = static_cast<const T*>(a.beta) + b * a.bs.b + h * a.bs.h;
+  auto block_sum = [&](float s) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+    __syncthreads();
+    if (l == 0) sh[wave] = s;
+    __syncthreads();
+    return (sh[0] + sh[1]) + (sh[2] + sh[3]);
+  };
+  float dot = 0.f;
+  {
+    const float* p = slots_f + (seg + 1) * all + bh * elems;
+    const float* q = slots_r + (a.nseg - 1 - seg) * all + bh * elems;
+    for (size_t e = tid * 4; e < elems; e += 1024) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(p + e), y = *reinterpret_cast<const f32x4*>(q + e);
+      dot += (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
+    }
+  }
+  float tail = block_sum(dot);
+  if (t1 < a.T) tail *= ex2(fmaxf(to_f32(la[(long long)t1 * a.ls.t]) * kLog2e, -180.f));
+  float dsum = 0.f;
+  // 256 tokens at a time, last ones first; lane order is token order reversed
+  for (int e = t1; e > t0; e -= 256) {
+    const int t = e - 1 - tid;
+    float x = 0.f;
+    if (t >= t0) {
+      float c = 0.f, r = rs[bh * a.T + t];
+      for (int u = 0; u < cpu; ++u) {
+        const size_t at = ((size_t)bh * cpu + u) * a.T + t;
+        c += a.c[at];
+        r += a.r[at];
+        dsum += a.d[at];
+      }
+      x = r - to_f32(beta[(long long)t * a.bs.t]) * c;
+      dbeta[b * dbs.b + h * dbs.h + (long long)t * dbs.t] = from_f32<T>(c);
+    }
+    float s = x;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const float y = __shfl_up(s, off);
+      s += l >= off ? y : 0.f;
+    }
+    __syncthreads();
+    if (l == 63) sh[4 + wave] = s;
+    __syncthreads();
+    float base = tail;
+    for (int w = 0; w < wave; ++w) base += sh[4 + w];
+    tail += (sh[4] + sh[5]) + (sh[6] + sh[7]);
+    if (t >= t0) dla[b * dls.b + h * dls.h + (long long)t * dls.t] = from_f32<T>(base + s);
+  }
+  dsum = block_sum(dsum);
+  if (tid == 0 && dDp) dDp[((size_t)b * a.nseg + seg) * a.H + h] = dsum;
+}
+
+template <typename T>
+__global__ __launch_bounds__(64) void kda_ssm_skip_kernel(const float* dDp, T* dD, int H, int n) {
+  const int h = blockIdx.x * 64 + threadIdx.x;
+  if (h >= H) return;
+  float s = 0.f;
+  for (int p = 0; p < n; ++p) s += dDp[(size_t)p * H + h];
+  dD[h] = from_f32<T>(s);
+}
+
+// ----------------------------------------------------------------- one token
+// S = a S + k (beta v)^T, o = S^T q + D v.  Workgroup = one (sequence, head), four
+// waves of dv / 4 columns each; lane = 4 columns of consecutive rows.  Bound by
+// the state, which is read and written once, past the caches.
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(256) void kda_ssm_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                                                           const T* __restrict__ la, const T* __restrict__ beta,
+                                                           const T* __restrict__ D, float* S, T* __restrict__ o, int H, int G) {
+  constexpr int CPW = DV / 4, LPR = CPW / 4, RG = 64 / LPR, RPL = DK / RG;
+  const int nh = blockIdx.x, n = nh / H, h = nh - n * H;
+  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int c0 = wave * CPW + 4 * (l % LPR), r0 = (l / LPR) * RPL;
+  float* s = S + (size_t)nh * DK * DV + (size_t)r0 * DV + c0;
+  f32x4 st[RPL];
+#pragma unroll
+  for (int r = 0; r < RPL; ++r) st[r] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(s + r * DV));
+  const size_t row = ((size_t)n * G + h / (H / G)) * DK + r0;
+  float kk[RPL], qq[RPL];
+#pragma unroll
+  for (int r = 0; r < RPL; ++r) {
+    kk[r] = to_f32(k[row + r]);
+    qq[r] = to_f32(q[row + r]);
+  }
+  const float al = expf(to_f32(la[nh])), b = to_f32(beta[nh]);
+  float vv[4], y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) vv[c] = to_f32(v[(size_t)nh * DV + c0 + c]);
+#pragma unroll
+  for (int r = 0; r < RPL; ++r) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      st[r][c] = al * st[r][c] + kk[r] * (b * vv[c]);
+      y[c] += qq[r] * st[r][c];
+    }
+    __builtin_nontemporal_store(st[r], reinterpret_cast<f32x4*>(s + r * DV));
+  }
+#pragma unroll
+  for (int off = LPR; off < 64; off <<= 1)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] += __shfl_xor(y[c], off);
+  if (l < LPR) {
+    const float d = D ? to_f32(D[h]) : 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[(size_t)nh * DV + c0 + c] = from_f32<T>(y[c] + d * vv[c]);
+  }
+}
+
+// ------------------------------------------------------------------- check
+__device__ unsigned int g_ssm_check_bits;
+
+__global__ void kda_ssm_check_clear_kernel(unsigned int* bits) { *bits = 0u; }
+
+template <typename T>
+__global__ __launch_bounds__(256) void kda_ssm_check_kernel(const T* la, Str3 ls, const T* beta, Str3 bs, int H, int T_,
+                                                            long long n, unsigned int* bits) {
+  unsigned int b = 0u;
+  for (long long f = (long long)blockIdx.x * 256 + threadIdx.x; f < n; f += (long long)gridDim.x * 256) {
+    const int t = (int)(f % T_);
+    const long long bh = f / T_, bb = bh / H, h = bh % H;
+    if (!(to_f32(la[bb * ls.b + h * ls.h + t * ls.t]) <= 0.f)) b |= 1u;
+    if (!(fabsf(to_f32(beta[bb * bs.b + h * bs.h + t * bs.t])) < __builtin_inff())) b |= 2u;
+  }
+  if (b) atomicOr(bits, b);
+}
+
+// ------------------------------------------------------------------ launch
+template <typename T, bool REV>
+hipError_t run_state(const PassArgs& a, hipStream_t s) {
+  const int nu = a.H / a.G * (a.dv / 64);
+  const dim3 grid(item_grid(a.B, a.G, a.norders, (nu + 1) / 2));
+  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_state_kernel<T, 128, REV>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((kda_ssm_state_kernel<T, 64, REV>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool BWD>
+hipError_t run_out(const PassArgs& a, hipStream_t s) {
+  const int nu = a.H / a.G * (a.dv / 64);
+  const dim3 grid(item_grid(a.B, a.G, a.nseg, (nu + 1) / 2));
+  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_out_kernel<T, 128, BWD>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((kda_ssm_out_kernel<T, 64, BWD>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool REV>
+hipError_t run_group(const PassArgs& a, const void* qrow, Str3 qrs, float* rs, float* parts, hipStream_t s) {
+  const int hg = 128 / a.dv, np = (a.H / a.G + hg - 1) / hg;
+  const dim3 grid(item_grid(a.B, a.G, a.nseg, np));
+#define KDA_GROUP(DV, DK)                                                                                            \
+  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK, REV>), grid, dim3(2 * DK), 0, s, a, qrow, qrs, rs, parts)
+  if (a.dv == 64 && a.dk == 64) KDA_GROUP(64, 64);
+  else if (a.dv == 64) KDA_GROUP(64, 128);
+  else if (a.dk == 64) KDA_GROUP(128, 64);
+  else KDA_GROUP(128, 128);
+#undef KDA_GROUP
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || np == 1) return e;
+  const long long n = (long long)a.B * a.G * a.T * (a.dk / 8);
+  hipLaunchKernelGGL((kda_ssm_parts_kernel<T>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, parts, np,
+                     static_cast<T*>(a.o), a.os, a.B, a.G, a.T, a.dk);
+  return hipGetLastError();
+}
+
+hipError_t run_merge(const float* start, float* slots, const float* dec, const PassArgs& a, int n, hipStream_t s) {
+  const long long BH = (long long)a.B * a.H;
+  const int elems = a.dk * a.dv;
+  hipLaunchKernelGGL(kda_ssm_merge_kernel, dim3((unsigned)((BH * elems / 4 + 255) / 256)), dim3(256), 0, s, start, slots, dec,
+                     BH, elems, n);
+  return hipGetLastError();
+}
+
+#define SSM_TRY(expr)                       \
+  do {                                      \
+    const hipError_t e_ = (expr);           \
+    if (e_ != hipSuccess) return e_;        \
+  } while (0)
+
+template <typename T>
+hipError_t prefill(const SsmArgs& x, hipStream_t s) {
+  PassArgs a{};
+  a.Q = x.q; a.K = x.k; a.V = x.v; a.la = x.la; a.beta = x.beta; a.D = x.D; a.lens = x.lens; a.o = x.o;
+  a.qs = x.qs; a.ks = x.ks; a.vs = x.vs; a.ls = x.ls; a.bs = x.bs; a.os = x.os;
+  a.B = x.B; a.H = x.H; a.G = x.G; a.T = x.T; a.dk = x.dk; a.dv = x.dv;
+  a.nseg = x.nseg; a.seg_chunks = x.seg_chunks;
+  a.start = x.S0;
+  if (x.nseg > 1) {
+    float* slots = x.ws;
+    a.dec = slots + (size_t)x.nseg * x.B * x.H * x.dk * x.dv;
+    a.end = slots;
+    a.norders = x.nseg - 1;  // the last segment's end state is not needed
+    SSM_TRY((run_state<T, false>(a, s)));
+    SSM_TRY(run_merge(x.S0, slots, a.dec, a, x.nseg - 1, s));
+    a.start = slots;
+  }
+  a.end = x.S_T;
+  return run_out<T, false>(a, s);
+}
+
+struct BwdWs {
+  size_t slots_f, slots_r, dec, c, r, d, rs, dDp, parts, total;
+};
+BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg) {
+  BwdWs w;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t p = at;
+    at += (n + 3) / 4 * 4;  // 16-byte aligned
+    return p;
+  };
+  const size_t st = (size_t)B * H * dk * dv, bht = (size_t)B * H * T, cpu = dv / 64;
+  w.slots_f = take((nseg + 1) * st);
+  w.slots_r = take((size_t)nseg * st);
+  w.dec = take((size_t)nseg * B * H);
+  w.c = take(bht * cpu);
+  w.r = take(bht * cpu);
+  w.d = take(bht * cpu);
+  w.rs = take(bht);
+  w.dDp = take((size_t)nseg * B * H);
+  const int hg = 128 / dv, np = (H / G + hg - 1) / hg;
+  w.parts = take(np > 1 ? (size_t)np * B * G * T * dk : 0);
+  w.total = at;
+  return w;
+}
+
+template <typename T>
+hipError_t backward(const SsmArgs& x, hipStream_t s) {
+  const BwdWs w = backward_ws(x.B, x.H, x.G, x.T, x.dk, x.dv, x.nseg);
+  float* const ws = x.ws;
+  PassArgs a{};
+  a.la = x.la; a.beta = x.beta; a.D = x.D;
+  a.ls = x.ls; a.bs = x.bs;
+  a.B = x.B; a.H = x.H; a.G = x.G; a.T = x.T; a.dk = x.dk; a.dv = x.dv;
+  a.nseg = x.nseg; a.seg_chunks = x.seg_chunks;
+  a.c = ws + w.c; a.r = ws + w.r; a.d = ws + w.d;
+  a.dec = ws + w.dec;
+  // start states of the segments, forwards (with the end state) and reversed
+  a.K = x.k; a.ks = x.ks; a.V = x.v; a.vs = x.vs;
+  a.end = ws + w.slots_f;
+  a.norders = x.nseg;
+  SSM_TRY((run_state<T, false>(a, s)));
+  SSM_TRY(run_merge(x.S0, ws + w.slots_f, a.dec, a, x.nseg, s));
+  a.K = x.q; a.ks = x.qs; a.V = x.dO; a.vs = x.dos;
+  a.end = ws + w.slots_r;
+  a.norders = x.nseg - 1;  // (dS0 comes from the outputs' pass)
+  if (a.norders > 0) SSM_TRY((run_state<T, true>(a, s)));
+  SSM_TRY(run_merge(x.dS_T, ws + w.slots_r, a.dec, a, x.nseg - 1, s));
+  // dv, dbeta's and dlog_alpha's sums, dS0
+  a.Q = x.k; a.qs = x.ks;
+  a.V2 = x.v; a.v2s = x.vs;
+  a.o = x.dvv; a.os = x.dvs;
+  a.start = ws + w.slots_r;
+  a.end = x.dS0;
+  SSM_TRY((run_out<T, true>(a, s)));
+  // dq
+  a.Q = x.dO; a.qs = x.dos; a.K = x.v; a.ks = x.vs; a.V = x.k; a.vs = x.ks;
+  a.o = x.dq; a.os = x.dqs;
+  a.start = ws + w.slots_f;
+  SSM_TRY((run_group<T, false>(a, x.q, x.qs, ws + w.rs, ws + w.parts, s)));
+  // dk
+  a.Q = x.v; a.qs = x.vs; a.K = x.dO; a.ks = x.dos; a.V = x.q; a.vs = x.qs;
+  a.o = x.dkk; a.os = x.dks;
+  a.start = ws + w.slots_r;
+  SSM_TRY((run_group<T, true>(a, nullptr, Str3(), nullptr, ws + w.parts, s)));
+  hipLaunchKernelGGL((kda_ssm_finish_kernel<T>), dim3((unsigned)((long long)x.B * x.H * x.nseg)), dim3(256), 0, s, a,
+                     ws + w.slots_f, ws + w.slots_r, ws + w.rs, static_cast<T*>(x.dla), x.dls, static_cast<T*>(x.dbeta), x.dbs,
+                     x.dD ? ws + w.dDp : nullptr);
+  SSM_TRY(hipGetLastError());
+  if (x.dD) {
+    hipLaunchKernelGGL((kda_ssm_skip_kernel<T>), dim3((x.H + 63) / 64), dim3(64), 0, s, ws + w.dDp, static_cast<T*>(x.dD), x.H,
+                       x.B * x.nseg);
+    SSM_TRY(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+// Two workgroups a compute unit (one with fp32 tiles) fill the device; where the
+// sequences and heads alone give fewer, the sequence is cut, into runs of at least
+// four chunks.
+int ssm_plan(int B, int H, int G, int T, int dk, int dv, bool bf16_io, bool backward, int cus, int* seg_chunks) {
+  const int nch = (T + CH - 1) / CH;
+  const long long np = ((long long)H / G * (dv / 64) + 1) / 2, base = (long long)B * G * np;
+  long long nseg = base > 0 ? (bf16_io ? 2 : 1) * (long long)cus / base : 1;
+  if (nseg > nch / 4) nseg = nch / 4;
+  if (nseg < 1) nseg = 1;
+  const int sc = (int)((nch + nseg - 1) / nseg);
+  *seg_chunks = sc > 0 ? sc : 1;
+  return nch > 0 ? (nch + *seg_chunks - 1) / *seg_chunks : 1;
+}
+
+size_t ssm_ws_floats(int B, int H, int dk, int dv, int nseg) {
+  if (nseg <= 1) return 0;
+  return (size_t)nseg * B * H * dk * dv + ((size_t)nseg * B * H + 3) / 4 * 4;
+}
+
+size_t ssm_backward_ws_floats(int B, int H, int G, int T, int dk, int dv, int nseg) {
+  return backward_ws(B, H, G, T, dk, dv, nseg).total;
+}
+
+hipError_t launch_ssm_prefill(const SsmArgs& a, bool bf16_io, hipStream_t stream) {
+  if (a.T == 0) {
+    if (a.S_T == a.S0) return hipSuccess;
+    const long long n4 = (long long)a.B * a.H * a.dk * a.dv / 4;
+    hipLaunchKernelGGL(kda_ssm_copy_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, stream, a.S0, a.S_T, n4);
+    return hipGetLastError();
+  }
+  return bf16_io ? prefill<bf16>(a, stream) : prefill<float>(a, stream);
+}
+
+hipError_t launch_ssm_backward(const SsmArgs& a, bool bf16_io, hipStream_t stream) {
+  return bf16_io ? backward<bf16>(a, stream) : backward<float>(a, stream);
+}
+
+hipError_t launch_ssm_step(const void* q, const void* k, const void* v, const void* la, const void* beta, const void* D,
+                           float* S, void* o, int N, int H, int G, int dk, int dv, bool bf16_io, hipStream_t stream) {
+#define KDA_STEP(TY, DK, DV)                                                                                              \
+  hipLaunchKernelGGL((kda_ssm_step_kernel<TY, DK, DV>), dim3((unsigned)((long long)N * H)), dim3(256), 0, stream,         \
+                     (const TY*)q, (const TY*)k, (const TY*)v, (const TY*)la, (const TY*)beta, (const TY*)D, S, (TY*)o, H, G)
+#define KDA_STEP_T(TY)                                    \
+  do {                                                    \
+    if (dk == 128 && dv == 128) KDA_STEP(TY, 128, 128);   \
+    else if (dk == 128) KDA_STEP(TY, 128, 64);            \
+    else if (dv == 128) KDA_STEP(TY, 64, 128);            \
+    else KDA_STEP(TY, 64, 64);                            \
+  } while (0)
+  if (bf16_io) KDA_STEP_T(bf16);
+  else KDA_STEP_T(float);
+#undef KDA_STEP_T
+#undef KDA_STEP
+  return hipGetLastError();
+}
+
+hipError_t check_ssm_gates(const void* la, Str3 ls, const void* beta, Str3 bs, int B, int H, int T, bool bf16_io,
+                           hipStream_t stream, unsigned int* bits_out) {
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);  // one check at a time: the flag is the device's only one
+  void* p = nullptr;
+  hipError_t e;
+  if ((e = hipGetSymbolAddress(&p, HIP_SYMBOL(g_ssm_check_bits))) != hipSuccess) return e;
+  unsigned int* f = static_cast<unsigned int*>(p);
+  hipLaunchKernelGGL(kda_ssm_check_clear_kernel, dim3(1), dim3(1), 0, stream, f);
+  SSM_TRY(hipGetLastError());
+  const long long n = (long long)B * H * T;
+  const long long nb = (n + 255) / 256;
+  const dim3 grid((unsigned)(nb < 2048 ? nb : 2048));
+  if (bf16_io)
+    hipLaunchKernelGGL(kda_ssm_check_kernel<bf16>, grid, dim3(256), 0, stream, static_cast<const bf16*>(la), ls,
+                       static_cast<const bf16*>(beta), bs, H, T, n, f);
+  else
+    hipLaunchKernelGGL(kda_ssm_check_kernel<float>, grid, dim3(256), 0, stream, static_cast<const float*>(la), ls,
+                       static_cast<const float*>(beta), bs, H, T, n, f);
+  SSM_TRY(hipGetLastError());
+  unsigned int h = 0u;
+  if ((e = hipMemcpyAsync(&h, f, sizeof(h), hipMemcpyDeviceToHost, stream)) != hipSuccess) return e;
+  if ((e = hipStreamSynchronize(stream)) != hipSuccess) return e;
+  *bits_out = h;
+  return hipSuccess;
+}
+
+}  // namespace kda

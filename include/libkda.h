@@ -299,6 +299,150 @@ kda_status kda_prefill_backward(const void* q, const void* k, const void* v, con
                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Companion operators.  A layer runs its q, k and v through a short causal
+ * convolution before the recurrence; hybrid models interleave KDA layers with
+ * scalar-decay (selective state space) layers; and a serving engine keeps the
+ * fixed-size states of many prefixes.  The calls below share the conventions at
+ * the top of this file except where they say otherwise:
+ *  - sequences may be strided: a kda_strides gives the distance in elements
+ *    between consecutive batch entries, heads and tokens of a [B, H, T, d]
+ *    array whose rows of d elements are contiguous, so that a projection's
+ *    token-major output [B, T, H * d] is read in place.  NULL means contiguous
+ *    [B, H, T, d].  Rows must start on 16-byte boundaries: strides (of
+ *    dimensions larger than 1) are multiples of 16 bytes and not negative;
+ *    those of an output are not 0 and its rows do not overlap.
+ *  - `lens` (NULL: every sequence has T tokens) is a device array of B ints:
+ *    sequence b has its first lens[b] tokens (clamped to [0, T]).  The padding
+ *    behind them is neither read into the results nor written.
+ * Outputs must not overlap inputs except where stated.
+ */
+typedef struct { long long b, h, t; } kda_strides;
+
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_activation;
+
+/*
+ * Short causal convolution, one filter of K taps (2, 3 or 4) per channel:
+ *     e = [state_in; x],  pre[t] = bias + sum_k weight[k] e[t + k],  o[t] = act(pre[t])
+ * with act(x) = x or x * sigmoid(x) (SiLU).
+ *   x, o       : [B, H, T, d] dtype, strides xs and os; d * sizeof(dtype) a
+ *                multiple of 16
+ *   weight     : [H, d, K] dtype (any element alignment);  bias : [H, d] or NULL
+ *   state_in   : [B, H, K - 1, d] dtype, contiguous: the tokens before the first
+ *                one, oldest first; NULL for zeros
+ *   state_out  : the same shape, or NULL: the last K - 1 rows of e before token
+ *                T (lens[b]), to go on from; must not be state_in
+ * T == 0 copies state_in (or zeros) to state_out.
+ */
+kda_status kda_conv_prefill(const void* x, const kda_strides* xs, const void* weight, const void* bias,
+                            const void* state_in, const int* lens, void* o, const kda_strides* os,
+                            void* state_out, int B, int H, int T, int d, int K, kda_activation act,
+                            kda_dtype dtype, hipStream_t stream);
+
+/*
+ * One token of the same convolution for N sequences: x, o [N, H, d] (strides b
+ * and h; t is ignored), state [N, H, K - 1, d] read and moved on in place.
+ */
+kda_status kda_conv_step(const void* x, const kda_strides* xs, void* state, const void* weight,
+                         const void* bias, void* o, const kda_strides* os, int N, int H, int d, int K,
+                         kda_activation act, kda_dtype dtype, hipStream_t stream);
+
+/*
+ * Gradients of kda_conv_prefill (without lens) for dL/do = dO and dL/dstate_out =
+ * dstate_out (NULL: zero): dx as x, dweight as weight, dbias as bias (NULL: not
+ * written), dstate_in as state_in (NULL: not written), each in dtype; sums over
+ * tokens and sequences are held in fp32 and added in a fixed order.  T >= 1.
+ * The workspace (kda_conv_backward_workspace_bytes) holds partial sums.
+ */
+size_t kda_conv_backward_workspace_bytes(int B, int H, int T, int d, int K, kda_dtype dtype);
+kda_status kda_conv_backward(const void* x, const kda_strides* xs, const void* weight, const void* bias,
+                             const void* state_in, const void* dO, const kda_strides* dos,
+                             const void* dstate_out, void* dx, const kda_strides* dxs, void* dweight,
+                             void* dbias, void* dstate_in, int B, int H, int T, int d, int K,
+                             kda_activation act, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/*
+ * Selective state space scan with one decay per head and token.  Per head, with
+ * state S (dk x dv):
+ *     S_t = exp(log_alpha_t) S_{t-1} + beta_t k_t v_t^T,   o_t = S_t^T q_t + D v_t
+ * In state space terms k and q are B and C, v the input, beta the step size dt,
+ * log_alpha = dt * A, and D the skip.
+ *   q, k            : [B, G, T, dk] dtype, G dividing H: heads h with the same
+ *                     h / (H / G) share them
+ *   v, o            : [B, H, T, dv] dtype
+ *   log_alpha, beta : [B, H, T] dtype (strides b, h, t in elements, any element
+ *                     alignment), log_alpha <= 0 (-inf clears the state), beta
+ *                     finite.  Option "check" validates that before launching.
+ *   D               : [H] dtype (any element alignment) or NULL (no skip)
+ *   S0, S_T         : [B, H, dk, dv] fp32; S0 NULL for zero; S_T may be S0
+ * dk and dv are 64 or 128, independently.  T == 0 copies S0 (or zeros) to S_T.
+ * bf16 inputs use bf16 matrix products with fp32 accumulation; states are
+ * carried in fp32.  Sequences too few to fill the device are cut into segments
+ * (each one's zero-start end state, a merge, then every segment from its true
+ * start); that needs kda_ssm_prefill_workspace_bytes() of workspace, and with
+ * less, or NULL, the call walks each sequence in one piece.
+ */
+typedef struct { kda_strides q, k, v, log_alpha, beta, o; } kda_ssm_strides;
+
+size_t kda_ssm_prefill_workspace_bytes(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype);
+kda_status kda_ssm_prefill(const void* q, const void* k, const void* v, const void* log_alpha,
+                           const void* beta, const void* D, const float* S0, const int* lens, void* o,
+                           float* S_T, const kda_ssm_strides* strides, int B, int H, int G, int T, int dk,
+                           int dv, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/*
+ * One token of the scan for N sequences: q, k [N, G, dk], v, o [N, H, dv],
+ * log_alpha, beta [N, H] (any element alignment), all contiguous; S [N, H, dk,
+ * dv] fp32 in place.
+ */
+kda_status kda_ssm_step(const void* q, const void* k, const void* v, const void* log_alpha,
+                        const void* beta, const void* D, float* S, void* o, int N, int H, int G, int dk,
+                        int dv, kda_dtype dtype, hipStream_t stream);
+
+/*
+ * Gradients of kda_ssm_prefill (without lens; padding tokens with beta = 0 and
+ * log_alpha = 0 pass the state on) for dL/do = dO and dL/dS_T = dS_T (NULL:
+ * zero).  dq, dk_ (summed over a group's heads), dv_, dlog_alpha, dbeta and dD
+ * (NULL without D) take their input's shape, in dtype, dS0 fp32 (NULL: not
+ * written).  Sums are fp32 in a fixed order.  The strides of dlog_alpha and
+ * dbeta are free; T >= 1.
+ */
+typedef struct { kda_strides dO, dq, dk, dv, dlog_alpha, dbeta; } kda_ssm_grad_strides;
+
+size_t kda_ssm_backward_workspace_bytes(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype);
+kda_status kda_ssm_backward(const void* q, const void* k, const void* v, const void* log_alpha,
+                            const void* beta, const void* D, const float* S0, const void* dO,
+                            const float* dS_T, void* dq, void* dk_, void* dv_, void* dlog_alpha,
+                            void* dbeta, void* dD, float* dS0, const kda_ssm_strides* strides,
+                            const kda_ssm_grad_strides* grad_strides, int B, int H, int G, int T, int dk,
+                            int dv, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/*
+ * The quantised state cache: KDA or scan states (prefix snapshots, parked
+ * requests) in 8 bits.  A row of dv values is cut into blocks of 32 that share a
+ * power-of-two scale, so that only the rounding of each value loses anything:
+ * at most half a step of the block's largest value / 127 .. 2/127 (int8), or
+ * 2^-4 of the value itself (e4m3).
+ *   S      : [n, H, dk, dv] fp32 (S_snap of kda_chunk_prefill_snap as it stands)
+ *   slots  : [n] ints on the device, the cache entry of each state.  Store skips
+ *            entries outside [0, nslots); of entries that name the same slot
+ *            the last one is stored.  Load writes zeros for entries outside.
+ *   cache  : [nslots, H, dk, dv] bytes (int8 or OCP e4m3 values)
+ *   scales : [nslots, H, dk, dv / 32] bytes: exponent + 127; 255 marks a block
+ *            that held an infinity or NaN and reads back as NaN
+ * dv is a multiple of 32.  slots, and scales, may have any alignment.
+ */
+typedef enum { KDA_CACHE_INT8 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_format;
+
+kda_status kda_state_store(const float* S, const int* slots, void* cache, void* scales, int n, int nslots,
+                           int H, int dk, int dv, kda_cache_format format, hipStream_t stream);
+kda_status kda_state_load(const void* cache, const void* scales, const int* slots, float* S, int n,
+                          int nslots, int H, int dk, int dv, kda_cache_format format, hipStream_t stream);
+
+/*
  * Process-wide options.  Each starts from the environment variable of the same
  * name in capitals with a KDA_ prefix (KDA_SPLIT, ...), read once, at the first
  * call that needs the options; kda_set_option changes one for every later call
@@ -331,7 +475,8 @@ kda_status kda_prefill_backward(const void* q, const void* k, const void* v, con
  *                      stream; 0 (default) runs the chain whole, then every
  *                      chunk's gradients.  Same results bit for bit
  *   "check"            1: validate log_alpha and beta on the device before every
- *                      call that reads them (see the conventions above); default 0
+ *                      call that reads them (see the conventions above; for the
+ *                      scan log_alpha <= 0 and beta finite); default 0
  *   "log"              1: print every launch's shape to stderr; default 0
  * kda_set_option returns KDA_ERR_SHAPE for an unknown name or a value the option
  * does not take; kda_get_option writes the value in effect (-1: default).
