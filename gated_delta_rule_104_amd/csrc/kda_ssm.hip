@@ -37,6 +37,7 @@
 // terms from a two-term (16-bit) state.  fp32 inputs run the same kernels on the
 // fp32 matrix instructions.
 #include <mutex>
+#include <type_traits>
 
 #include "kda_ops.hpp"
 
@@ -94,39 +95,51 @@ struct Split {
 };
 
 // ------------------------------------------------------------- LDS tiles
-// [64 tokens][COLS] of T, 16-byte granules XOR-swizzled by row (swz).
+// [64 tokens][COLS] of T, 16-byte granules XOR-swizzled by row (swz).  Reads take
+// a lane's base offset, row_off or col_off, computed afresh for every chunk
+// (fresh_lane): a granule's number enters an address by XOR and a row tile by
+// addition, so that one register serves every read of a kind, where addresses
+// hoisted out of the chunk loop would not leave enough for the tiles in flight.
 template <typename T, int COLS>
 struct Tile {
   static constexpr int R = COLS * (int)sizeof(T);
   static constexpr int BYTES = CH * R;
   static constexpr int GPR = R / 16;  // granules per row
+  static constexpr uint32_t MASK = GPR < 16 ? GPR - 1 : 15;
+  static constexpr int GB = 32 * (int)sizeof(T);  // bytes of 32 channels
 
-  // channels 32m + 8g .. + 7 of row `row`
-  static __device__ __forceinline__ typename Op<T>::F row(const char* s, int row, int m, int g) {
-    if constexpr (sizeof(T) == 2) {
-      return lds_ld<bf16x8>(s, swz<R>(row, (32 * m + 8 * g) * 2));
-    } else {
-      const f32x4 lo = lds_ld<f32x4>(s, swz<R>(row, (32 * m + 8 * g) * 4));
-      const f32x4 hi = lds_ld<f32x4>(s, swz<R>(row, (32 * m + 8 * g) * 4 + 16));
-      return Op<T>::round(lo, hi);
-    }
+  static __device__ __forceinline__ uint32_t row_off(int g, int i) { return i * R + ((((GB / 64) * g) ^ (i & MASK)) << 4); }
+  // channels 32m + 8g .. + 7 of row 16 I + i
+  static __device__ __forceinline__ typename Op<T>::F row(const char* s, uint32_t off, int I, int m) {
+    const char* p = s + I * 16 * R;
+    if constexpr (sizeof(T) == 2) return lds_ld<bf16x8>(p, off ^ (m * GB));
+    else return Op<T>::round(lds_ld<f32x4>(p, off ^ (m * GB)), lds_ld<f32x4>(p, off ^ (m * GB) ^ 16));
   }
   // Contraction over tokens: lane (g, i) gets tokens 32m + 4g + e and 32m + 16 +
   // 4g + e of channel 32c + 8(i / 4) + 4 odd + i % 4.  bf16: the transposing read
   // takes lane i's 8 bytes as row i of a 16 x 4 matrix and returns element
   // [4e + i / 4][i % 4] as lane i's e-th.
-  static __device__ __forceinline__ typename Op<T>::F col(const char* s, int m, int c, int odd, int g, int i) {
+  static __device__ __forceinline__ uint32_t col_off(int g, int i) {
     if constexpr (sizeof(T) == 2) {
-      const int byte = (32 * c + 8 * (i & 3) + 4 * odd) * 2, r = 32 * m + 4 * g + (i >> 2);
-      const bf16x4 lo = lds_tr16(s, swz<R>(r, byte)), hi = lds_tr16(s, swz<R>(r + 16, byte));
+      const int r = 4 * g + (i >> 2);
+      return r * R + (((i & 3) ^ (r & MASK)) << 4);
+    } else {
+      return 4 * g * R + (((2 * (i >> 2)) ^ ((4 * g) & MASK)) << 4) + 4 * (i & 3);
+    }
+  }
+  static __device__ __forceinline__ typename Op<T>::F col(const char* s, uint32_t off, int m, int c, int odd) {
+    const char* p = s + 32 * m * R;
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t o = (off ^ (c * GB)) + 8 * odd;
+      const bf16x4 lo = lds_tr16(p, o), hi = lds_tr16(p + 16 * R, o);
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
       typename Op<T>::F f;
-      const int byte = (32 * c + 8 * (i >> 2) + 4 * odd + (i & 3)) * 4;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        f.v[e] = lds_ld<float>(s, swz<R>(32 * m + 4 * g + e, byte));
-        f.v[4 + e] = lds_ld<float>(s, swz<R>(32 * m + 16 + 4 * g + e, byte));
+        const uint32_t o = off ^ (c * GB) ^ (odd * 16) ^ (e * 16);
+        f.v[e] = lds_ld<float>(p + e * R, o);
+        f.v[4 + e] = lds_ld<float>(p + (16 + e) * R, o);
       }
       return f;
     }
@@ -136,26 +149,28 @@ struct Tile {
 // A tile on its way from HBM: NT threads hold 16-byte granules of it.
 template <typename T, int COLS, int NT>
 struct Fetch {
-  static constexpr int N = CH * Tile<T, COLS>::GPR / NT;
+  typedef Tile<T, COLS> L;
+  static constexpr int STEP = NT / L::GPR;  // rows between a thread's granules
+  static constexpr int N = CH / STEP;
+  static_assert(STEP >= 1 && (STEP & (STEP - 1)) == 0 && STEP * L::GPR == NT, "whole rows");
   u32x4 r[N];
   // position p of the chunk is token tok0 + p, or tok0 + n - 1 - p reversed; rows past n are zero
   template <bool REV>
   __device__ __forceinline__ void get(const T* p, long long st, int tok0, int n, int tid) {
+    const int row = tid / L::GPR, c = tid % L::GPR;
+    const T* q = p + (long long)(REV ? tok0 + n - 1 - row : tok0 + row) * st + c * (16 / (int)sizeof(T));
+    const long long d = REV ? -STEP * st : STEP * st;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int gi = tid + i * NT, row = gi / Tile<T, COLS>::GPR, c = gi % Tile<T, COLS>::GPR;
       r[i] = u32x4{0u, 0u, 0u, 0u};
-      if (row < n)
-        r[i] = *reinterpret_cast<const u32x4*>(p + (long long)(REV ? tok0 + n - 1 - row : tok0 + row) * st +
-                                               c * (16 / (int)sizeof(T)));
+      if (row + i * STEP < n) r[i] = *reinterpret_cast<const u32x4*>(q + i * d);
     }
   }
   __device__ __forceinline__ void put(char* s, int tid) const {
+    const int row = tid / L::GPR, c = tid % L::GPR;
+    const uint32_t off = swz<L::R>(row, 16 * c);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int gi = tid + i * NT, row = gi / Tile<T, COLS>::GPR, c = gi % Tile<T, COLS>::GPR;
-      lds_st<u32x4>(s, swz<Tile<T, COLS>::R>(row, 16 * c), r[i]);
-    }
+    for (int i = 0; i < N; ++i) lds_st<u32x4>(s + i * STEP * L::R, off ^ (((i * STEP) & L::MASK) << 4), r[i]);
   }
 };
 
@@ -267,6 +282,12 @@ struct State {
 #pragma unroll
     for (int a = 0; a < NK; ++a) t[a][0] = t[a][1] = zero4();
   }
+  // Makes the compiler take the values as new, so that operands formed from them
+  // before are formed again rather than kept in registers.
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int a = 0; a < NK; ++a) asm volatile("" : "+v"(t[a][0]), "+v"(t[a][1]));
+  }
   __device__ __forceinline__ void scale(float s) {
 #pragma unroll
     for (int a = 0; a < NK; ++a)
@@ -282,7 +303,7 @@ __device__ __forceinline__ int pair_chan(int tile, int r) { return 32 * (tile >>
 // 32-token halves each)
 template <typename T, int NK, typename KT>
 __device__ __forceinline__ void update(State<NK>& S, const char* ktile, const typename Op<T>::F (&vf)[2][2], const float* ws,
-                                       int g, int i) {
+                                       uint32_t kcol, int g) {
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const f32x4 w0 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 4 * g);
@@ -298,7 +319,7 @@ __device__ __forceinline__ void update(State<NK>& S, const char* ktile, const ty
     const Split<T, 3> x0(lo[0], hi[0]), x1(lo[1], hi[1]);
 #pragma unroll
     for (int a = 0; a < NK; ++a) {
-      const typename Op<T>::F kf = KT::col(ktile, m, a >> 1, a & 1, g, i);
+      const typename Op<T>::F kf = KT::col(ktile, kcol, m, a >> 1, a & 1);
 #pragma unroll
       for (int n = Split<T, 3>::N - 1; n >= 0; --n) {
         S.t[a][0] = Op<T>::mma(S.t[a][0], kf, x0.t[n]);
@@ -308,19 +329,20 @@ __device__ __forceinline__ void update(State<NK>& S, const char* ktile, const ty
   }
 }
 
-// Y^T[p][I] = S^T Q^T (rows: the wave's columns, columns: tokens), NT terms of S
-template <typename T, int NK, int NT, typename QT>
-__device__ __forceinline__ void inter(f32x4 (&y)[2][4], const State<NK>& S, const char* qtile, int g, int i) {
+// Y^T[p][I] = S^T Q^T (rows: the wave's columns, columns: tokens) for the NI row
+// tiles from I0 on, NT terms of S
+template <typename T, int NK, int NT, typename QT, int NI>
+__device__ __forceinline__ void inter(f32x4 (&y)[2][NI], const State<NK>& S, const char* qtile, uint32_t qrow, int I0) {
 #pragma unroll
   for (int p = 0; p < 2; ++p)
 #pragma unroll
-    for (int I = 0; I < 4; ++I) y[p][I] = zero4();
+    for (int I = 0; I < NI; ++I) y[p][I] = zero4();
 #pragma unroll
   for (int m = 0; m < NK / 2; ++m) {
     const Split<T, NT> s0(S.t[2 * m][0], S.t[2 * m + 1][0]), s1(S.t[2 * m][1], S.t[2 * m + 1][1]);
 #pragma unroll
-    for (int I = 0; I < 4; ++I) {
-      const typename Op<T>::F qf = QT::row(qtile, 16 * I + i, m, g);
+    for (int I = 0; I < NI; ++I) {
+      const typename Op<T>::F qf = QT::row(qtile, qrow, I0 + I, m);
 #pragma unroll
       for (int n = Split<T, NT>::N - 1; n >= 0; --n) {
         y[0][I] = Op<T>::mma(y[0][I], s0.t[n], qf);
@@ -331,13 +353,13 @@ __device__ __forceinline__ void inter(f32x4 (&y)[2][4], const State<NK>& S, cons
 }
 
 // Y^T += V^T M^T
-template <typename T>
-__device__ __forceinline__ void intra(f32x4 (&y)[2][4], const typename Op<T>::F (&vf)[2][2], const char* scores, int l) {
+template <typename T, int I0, int NI>
+__device__ __forceinline__ void intra(f32x4 (&y)[2][NI], const typename Op<T>::F (&vf)[2][2], const char* scores, int l) {
 #pragma unroll
-  for (int I = 0; I < 4; ++I)
+  for (int I = 0; I < NI; ++I)
 #pragma unroll
-    for (int m = 0; m <= I / 2; ++m) {
-      const typename Op<T>::F mf = Scores<T>::get(scores, I, m, l);
+    for (int m = 0; m <= (I0 + I) / 2; ++m) {
+      const typename Op<T>::F mf = Scores<T>::get(scores, I0 + I, m, l);
       y[0][I] = Op<T>::mma(y[0][I], vf[0][m], mf);
       y[1][I] = Op<T>::mma(y[1][I], vf[1][m], mf);
     }
@@ -436,7 +458,7 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_state_kernel(PassArgs a) {
   const int cpu = a.dv / 64, nu = a.H / a.G * cpu;  // column units per head, units per group
   const Item it = item_of(a.B, a.G, a.norders, (nu + 1) / 2);
   if (!it.valid) return;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g = l >> 4, i = l & 15;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int len = clamp_len(a.lens, it.b, a.T);
   const int nch = (len + CH - 1) / CH;
   const int seg = REV ? a.nseg - 1 - it.seg : it.seg;
@@ -480,19 +502,22 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_state_kernel(PassArgs a) {
     if (step + 1 < c1 - c0) fetch(step + 1);
     sync_lds();
     const float* v = vec + uw * V_SIZE;
+    const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
+    const uint32_t vcol = VT::col_off(g, i) ^ (half * VT::GB);
     typename Op<T>::F vf[2][2];
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv + uw * VT::BYTES, m, half, p, g, i);
+      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv + uw * VT::BYTES, vcol, m, 0, p);
     const float gm = v[V_GM];
     dec *= gm;
     S.scale(gm);
-    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, g, i);
+    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, KT::col_off(g, i), g);
     sync_lds();
   }
   const int un = 2 * it.sub + uw;
   if (un >= nu) return;
+  const int g = l >> 4, i = l & 15;
   const size_t bh = (size_t)it.b * a.H + head[uw];
   // order o's end state lies in slot o + 1
   float* out = a.end + ((size_t)(it.seg + 1) * a.B * a.H + bh) * a.dk * a.dv;
@@ -551,7 +576,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
   const int cpu = a.dv / 64, nu = a.H / a.G * cpu;
   const Item it = item_of(a.B, a.G, a.nseg, (nu + 1) / 2);
   if (!it.valid) return;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g = l >> 4, i = l & 15;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int len = clamp_len(a.lens, it.b, a.T);
   const int nch = (len + CH - 1) / CH;
   const int seg = BWD ? a.nseg - 1 - it.seg : it.seg;
@@ -579,10 +604,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
 #pragma unroll
     for (int u = 0; u < 2; ++u) skip[u] = to_f32(static_cast<const T*>(a.D)[head[u]]);
   }
-  T* o = static_cast<T*>(a.o) + it.b * a.os.b + head[uw] * a.os.h + colu[uw] + half * 32 + 8 * g;
+  T* o = static_cast<T*>(a.o) + it.b * a.os.b + head[uw] * a.os.h + colu[uw] + half * 32;
   const size_t bh = (size_t)it.b * a.H + head[uw];
   State<DK / 16> S;
-  if (a.start) load_state(S, a.start + ((size_t)it.seg * a.B * a.H + bh) * a.dk * a.dv, a.dv, colu[uw] + half * 32, g, i);
+  if (a.start) load_state(S, a.start + ((size_t)it.seg * a.B * a.H + bh) * a.dk * a.dv, a.dv, colu[uw] + half * 32, l >> 4, l & 15);
   else S.zero();
   SC::clear(sm, tid, 256);
   SC::clear(sm + SC::BYTES, tid, 256);
@@ -620,13 +645,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
     if (step + 1 < c1 - c0) fetch(step + 1);
     sync_lds();
 
+    const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
+    const uint32_t krow = KT::row_off(g, i), vrow = VT::row_off(g, i);
     // scores, tiles dealt to the waves
     for (int t = wave; t < 10; t += 4) {
       const int I = tile_i(t), J = tile_j(t);
       f32x4 acc = zero4();
 #pragma unroll
       for (int m = 0; m < DK / 32; ++m)
-        acc = Op<T>::mma(acc, KT::row(sk, 16 * J + i, m, g), KT::row(sq, 16 * I + i, m, g));
+        acc = Op<T>::mma(acc, KT::row(sk, krow, J, m), KT::row(sq, krow, I, m));
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const float* v = vec + u * V_SIZE;
@@ -636,7 +663,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
           f32x4 dd = zero4();
 #pragma unroll
           for (int m = 0; m < 2; ++m)
-            dd = Op<T>::mma(dd, VT::row(sv + u * VT::BYTES, 16 * J + i, m, g), VT::row(sv2 + u * VT::BYTES, 16 * I + i, m, g));
+            dd = Op<T>::mma(dd, VT::row(sv + u * VT::BYTES, vrow, J, m), VT::row(sv2 + u * VT::BYTES, vrow, I, m));
           const float bi = v[V_RH + 16 * I + i];
           float cs = 0.f, rs[4];
 #pragma unroll
@@ -663,7 +690,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
     }
     const float* v = vec + uw * V_SIZE;
     f32x4 y[2][4];
-    inter<T, DK / 16, BWD ? 2 : 1, KT>(y, S, sq, g, i);
+    inter<T, DK / 16, BWD ? 2 : 1, KT, 4>(y, S, sq, krow, 0);
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
       const float s = v[V_IN + 16 * I + i];
@@ -672,13 +699,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[p][I][e] *= s;
     }
-    typename Op<T>::F vf[2][2];
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv + uw * VT::BYTES, m, half, p, g, i);
-    S.scale(v[V_GM]);
-    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, g, i);
     sync_lds();
     if constexpr (BWD) {
       // the state's part of c, z.v before the chunk's own part joins z, and dO.v;
@@ -686,8 +706,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
       float* w = vec + uw * V_SIZE;
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
-        const typename Op<T>::F x = VT::row(sv2 + uw * VT::BYTES, 16 * I + i, half, g);
-        const typename Op<T>::F gy = VT::row(sv + uw * VT::BYTES, 16 * I + i, half, g);
+        const typename Op<T>::F x = VT::row(sv2 + uw * VT::BYTES, vrow, I, half);
+        const typename Op<T>::F gy = VT::row(sv + uw * VT::BYTES, vrow, I, half);
         float s = 0.f, d = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) s += y[0][I][e] * Op<T>::at(x, e) + y[1][I][e] * Op<T>::at(x, 4 + e);
@@ -703,7 +723,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
         }
       }
     }
-    intra<T>(y, vf, sm + uw * SC::BYTES, l);
+    typename Op<T>::F vf[2][2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv + uw * VT::BYTES, VT::col_off(g, i) ^ (half * VT::GB), m, 0, p);
+    intra<T, 0, 4>(y, vf, sm + uw * SC::BYTES, l);
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
       const int p = 16 * I + i;
@@ -715,12 +740,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
       }
       if constexpr (BWD) {
         const float bi = v[V_RH + p];
-        const typename Op<T>::F gy = VT::row(sv + uw * VT::BYTES, p, half, g);
+        const typename Op<T>::F gy = VT::row(sv + uw * VT::BYTES, vrow, I, half);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = bi * x[e] + skip[uw] * Op<T>::at(gy, e);
       }
-      if (p < n && mine) store8<T>(o + (long long)(BWD ? tok0 + n - 1 - p : tok0 + p) * a.os.t, x);
+      if (p < n && mine) store8<T>(o + (long long)(BWD ? tok0 + n - 1 - p : tok0 + p) * a.os.t + 8 * g, x);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    S.scale(v[V_GM]);
+    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, KT::col_off(g, i), g);
     sync_lds();
     if constexpr (BWD) {
       // wave u writes unit u's sums (and refills that unit's vectors next)
@@ -741,7 +769,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
     // reversed: the state before the first token owes its own decay too
     float s = 1.f;
     if (BWD) s = ex2(fmaxf(to_f32((static_cast<const T*>(a.la) + it.b * a.ls.b + head[uw] * a.ls.h)[0]) * kLog2e, -180.f));
-    store_state(S, a.end + bh * a.dk * a.dv, a.dv, colu[uw] + half * 32, g, i, s);
+    store_state(S, a.end + bh * a.dk * a.dv, a.dv, colu[uw] + half * 32, l >> 4, l & 15, s);
   }
 }
 
@@ -754,33 +782,33 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
 // rs[i] = q_i . (the state's part of dq_i).
 template <typename T, int DV, int DK, bool REV>
 __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) void kda_ssm_group_kernel(
-    PassArgs a, const void* qrow, Str3 qrs, float* rs, float* parts) {
+    PassArgs a, const void* qin, Str3 qrs, float* rs, float* parts) {
   constexpr int HG = 128 / DV, NW = DK / 32, NT = 64 * NW;
   typedef Tile<T, DV> QT;
   typedef Tile<T, DK> VT;
   typedef Scores<T> SC;
-  constexpr int OQ = VT::BYTES, OK = OQ + HG * QT::BYTES, OW = OK + HG * QT::BYTES, OM = OW + (REV ? 0 : VT::BYTES);
+  constexpr int OQ = VT::BYTES, OK = OQ + HG * QT::BYTES, OM = OK + HG * QT::BYTES;
   constexpr int OVEC = OM + HG * SC::BYTES;
   __shared__ __attribute__((aligned(16))) char smem[OVEC + HG * V_SIZE * 4];
   char* const sv = smem;
   char* const sq = smem + OQ;
   char* const sk = smem + OK;
-  char* const sw = smem + OW;  // forward: the q rows
   char* const sm = smem + OM;
   float* const vec = reinterpret_cast<float*>(smem + OVEC);
   const int R = a.H / a.G, np = (R + HG - 1) / HG;
   const Item it = item_of(a.B, a.G, a.nseg, np);
   if (!it.valid) return;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, g = l >> 4, i = l & 15;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int nch = (a.T + CH - 1) / CH;
   const int seg = REV ? a.nseg - 1 - it.seg : it.seg;
   const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
   const T* V = static_cast<const T*>(a.V) + it.b * a.vs.b + it.g * a.vs.h;
-  const T* W = REV ? nullptr : static_cast<const T*>(qrow) + it.b * qrs.b + it.g * qrs.h;
+  const T* W = REV ? nullptr : static_cast<const T*>(qin) + it.b * qrs.b + it.g * qrs.h;
   const int nh = min(HG, R - it.sub * HG);  // heads of this workgroup
   int head[HG];
   const T *Q[HG], *K[HG];
   State<DV / 16> S[HG];
+  const int i0 = l & 15, g0 = l >> 4;
 #pragma unroll
   for (int h = 0; h < HG; ++h) {
     head[h] = it.g * R + it.sub * HG + min(h, nh - 1);
@@ -794,7 +822,7 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
       for (int t = 0; t < DV / 16; ++t)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          S[h].t[t][c] = *reinterpret_cast<const f32x4*>(p + (size_t)(32 * wave + pair_chan(c, i)) * DV + pair_chan(t, 4 * g));
+          S[h].t[t][c] = *reinterpret_cast<const f32x4*>(p + (size_t)(32 * wave + pair_chan(c, i0)) * DV + pair_chan(t, 4 * g0));
     }
   }
   const int hv = head[HG == 2 ? (wave & 1) : 0];
@@ -803,14 +831,13 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
 #pragma unroll
   for (int h = 0; h < HG; ++h) SC::clear(sm + h * SC::BYTES, tid, NT);
 
-  Fetch<T, DK, NT> fv, fw;
+  Fetch<T, DK, NT> fv;
   Fetch<T, DV, NT> fq[HG], fk[HG];
   float fx = 0.f, fb = 0.f;
   auto fetch = [&](int step) {
     const int c = REV ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, a.T - tok0);
     fv.template get<REV>(V, a.vs.t, tok0, n, tid);
-    if constexpr (!REV) fw.template get<REV>(W, qrs.t, tok0, n, tid);
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
       const int nn = h < nh ? n : 0;
@@ -829,16 +856,32 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
     const int c = REV ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, a.T - tok0);
     fv.put(sv, tid);
-    if constexpr (!REV) fw.put(sw, tid);
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
       fq[h].put(sq + h * QT::BYTES, tid);
       fk[h].put(sk + h * QT::BYTES, tid);
     }
     if (wave < HG) fill_vec(vec + wave * V_SIZE, l, fx, REV ? 1.f : fb, REV ? fb : 1.f, fb);
+    // the wave's columns of the q rows, for rs: straight from memory, in the layout of its results
+    typename Op<T>::F xq[4];
+    if constexpr (!REV) {
+#pragma unroll
+      for (int I = 0; I < 4; ++I) {
+        const int p = 16 * I + (l & 15);
+        u32x4 w[sizeof(T) / 2] = {};
+        if (p < n) {
+          const u32x4* src = reinterpret_cast<const u32x4*>(W + (long long)(tok0 + p) * qrs.t + 32 * wave + 8 * (l >> 4));
+#pragma unroll
+          for (int b = 0; b < (int)sizeof(T) / 2; ++b) w[b] = src[b];
+        }
+        __builtin_memcpy(&xq[I], w, sizeof(w));
+      }
+    }
     if (step + 1 < c1 - c0) fetch(step + 1);
     sync_lds();
 
+    const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
+    const uint32_t qrow = QT::row_off(g, i);
     for (int t = wave; t < 10; t += NW) {
       const int I = tile_i(t), J = tile_j(t);
 #pragma unroll
@@ -846,7 +889,7 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
         f32x4 acc = zero4();
 #pragma unroll
         for (int m = 0; m < DV / 32; ++m)
-          acc = Op<T>::mma(acc, QT::row(sk + h * QT::BYTES, 16 * J + i, m, g), QT::row(sq + h * QT::BYTES, 16 * I + i, m, g));
+          acc = Op<T>::mma(acc, QT::row(sk + h * QT::BYTES, qrow, J, m), QT::row(sq + h * QT::BYTES, qrow, I, m));
         const float* v = vec + h * V_SIZE;
         f32x4 mm = weigh(acc, v, I, J, g, i);
         if (REV && I == J) {
@@ -863,56 +906,72 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv, m, wave, p, g, i);
-    f32x4 y[2][4];
+      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv, VT::col_off(g, i) ^ (wave * VT::GB), m, 0, p);
+    // two halves of the tokens in turn, so that a half's sum over the heads and one
+    // head's part of it fit beside the states
+    auto half = [&](auto H2) {
+      constexpr int I0 = 2 * decltype(H2)::value;
+      f32x4 y[2][2];
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int I = 0; I < 4; ++I) y[p][I] = zero4();
+        for (int I = 0; I < 2; ++I) y[p][I] = zero4();
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+        float* v = vec + h * V_SIZE;
+        f32x4 z[2][2];
+        inter<T, DV / 16, REV ? 1 : 2, QT, 2>(z, S[h], sq + h * QT::BYTES, qrow, I0);
+#pragma unroll
+        for (int I = 0; I < 2; ++I) {
+          const float s = h < nh ? v[V_IN + 16 * (I0 + I) + i] : 0.f;
+          if constexpr (!REV) {
+            const typename Op<T>::F x = xq[I0 + I];
+            float dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dot += z[0][I][e] * Op<T>::at(x, e) + z[1][I][e] * Op<T>::at(x, 4 + e);
+            dot *= s;
+            dot += __shfl_xor(dot, 16);
+            dot += __shfl_xor(dot, 32);
+            // (the score vectors are no longer needed)
+            if (g == 0) v[64 * wave + 16 * (I0 + I) + i] = dot;
+          }
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[p][I][e] += s * z[p][I][e];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        intra<T, I0, 2>(y, vf, sm + h * SC::BYTES, l);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int I = 0; I < 2; ++I) {
+        const int p = 16 * (I0 + I) + i;
+        const int tok = REV ? tok0 + n - 1 - p : tok0 + p;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = y[0][I][e];
+          x[4 + e] = y[1][I][e];
+        }
+        if (p < n) {
+          if (np == 1)
+            store8<T>(static_cast<T*>(a.o) + it.b * a.os.b + it.g * a.os.h + (long long)tok * a.os.t + 32 * wave + 8 * g, x);
+          else
+            store8<float>(parts + (((size_t)it.sub * a.B * a.G + (size_t)it.b * a.G + it.g) * a.T + tok) * DK + 32 * wave + 8 * g, x);
+        }
+      }
+    };
+    half(std::integral_constant<int, 0>());
+#pragma unroll
+    for (int h = 0; h < HG; ++h) S[h].renew();
+    half(std::integral_constant<int, 1>());
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
-      float* v = vec + h * V_SIZE;
-      f32x4 z[2][4];
-      inter<T, DV / 16, REV ? 1 : 2, QT>(z, S[h], sq + h * QT::BYTES, g, i);
-#pragma unroll
-      for (int I = 0; I < 4; ++I) {
-        const float s = h < nh ? v[V_IN + 16 * I + i] : 0.f;
-        float dot = 0.f;
-        if constexpr (!REV) {
-          const typename Op<T>::F x = VT::row(sw, 16 * I + i, wave, g);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dot += z[0][I][e] * Op<T>::at(x, e) + z[1][I][e] * Op<T>::at(x, 4 + e);
-          dot *= s;
-          dot += __shfl_xor(dot, 16);
-          dot += __shfl_xor(dot, 32);
-          // (the score vectors are no longer needed)
-          if (g == 0) v[64 * wave + 16 * I + i] = dot;
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[p][I][e] += s * z[p][I][e];
-      }
-      intra<T>(y, vf, sm + h * SC::BYTES, l);
+      const float* v = vec + h * V_SIZE;
       S[h].scale(v[V_GM]);
-      update<T, DV / 16, QT>(S[h], sk + h * QT::BYTES, vf, v + V_WS, g, i);
-    }
-#pragma unroll
-    for (int I = 0; I < 4; ++I) {
-      const int p = 16 * I + i;
-      const int tok = REV ? tok0 + n - 1 - p : tok0 + p;
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = y[0][I][e];
-        x[4 + e] = y[1][I][e];
-      }
-      if (p < n) {
-        if (np == 1)
-          store8<T>(static_cast<T*>(a.o) + it.b * a.os.b + it.g * a.os.h + (long long)tok * a.os.t + 32 * wave + 8 * g, x);
-        else
-          store8<float>(parts + (((size_t)it.sub * a.B * a.G + (size_t)it.b * a.G + it.g) * a.T + tok) * DK + 32 * wave + 8 * g, x);
-      }
+      update<T, DV / 16, QT>(S[h], sk + h * QT::BYTES, vf, v + V_WS, QT::col_off(g, i), g);
+      __builtin_amdgcn_sched_barrier(0);
     }
     sync_lds();
     if constexpr (!REV) {
@@ -1115,11 +1174,11 @@ hipError_t run_out(const PassArgs& a, hipStream_t s) {
 }
 
 template <typename T, bool REV>
-hipError_t run_group(const PassArgs& a, const void* qrow, Str3 qrs, float* rs, float* parts, hipStream_t s) {
+hipError_t run_group(const PassArgs& a, const void* qin, Str3 qrs, float* rs, float* parts, hipStream_t s) {
   const int hg = 128 / a.dv, np = (a.H / a.G + hg - 1) / hg;
   const dim3 grid(item_grid(a.B, a.G, a.nseg, np));
 #define KDA_GROUP(DV, DK)                                                                                            \
-  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK, REV>), grid, dim3(2 * DK), 0, s, a, qrow, qrs, rs, parts)
+  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK, REV>), grid, dim3(2 * DK), 0, s, a, qin, qrs, rs, parts)
   if (a.dv == 64 && a.dk == 64) KDA_GROUP(64, 64);
   else if (a.dv == 64) KDA_GROUP(64, 128);
   else if (a.dk == 64) KDA_GROUP(128, 64);
