@@ -160,10 +160,15 @@ struct Fetch {
     const int row = tid / L::GPR, c = tid % L::GPR;
     const T* q = p + (long long)(REV ? tok0 + n - 1 - row : tok0 + row) * st + c * (16 / (int)sizeof(T));
     const long long d = REV ? -STEP * st : STEP * st;
+    if (n == CH) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      r[i] = u32x4{0u, 0u, 0u, 0u};
-      if (row + i * STEP < n) r[i] = *reinterpret_cast<const u32x4*>(q + i * d);
+      for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const u32x4*>(q + i * d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        r[i] = u32x4{0u, 0u, 0u, 0u};
+        if (row + i * STEP < n) r[i] = *reinterpret_cast<const u32x4*>(q + i * d);
+      }
     }
   }
   __device__ __forceinline__ void put(char* s, int tid) const {
@@ -299,31 +304,92 @@ struct State {
 };
 __device__ __forceinline__ int pair_chan(int tile, int r) { return 32 * (tile >> 1) + 8 * (r >> 2) + 4 * (tile & 1) + (r & 3); }
 
-// S += K^T (w V): w the per-token weights, V the wave's two column tiles (two
-// 32-token halves each)
+// One word (two elements) of the three bf16 terms of w V.
+__device__ __forceinline__ void split_word(uint32_t x, float wa, float wb, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
+  float a = __uint_as_float(x << 16) * wa, b = __uint_as_float(x & 0xffff0000u) * wb;
+  t0 = cvt2(a, b);
+  a -= __uint_as_float(t0 << 16);  // exact, as is the next
+  b -= __uint_as_float(t0 & 0xffff0000u);
+  t1 = cvt2(a, b);
+  a -= __uint_as_float(t1 << 16);
+  b -= __uint_as_float(t1 & 0xffff0000u);
+  t2 = cvt2(a, b);
+}
+
+// S <- gm S + K^T (w V): w the per-token weights, V the wave's two column tiles
+// (two 32-token halves each).  bf16: six products a row tile and token half; the
+// state's scaling and the second half's terms are dealt over the first half's
+// products, whose time on the matrix cores they fit into.
 template <typename T, int NK, typename KT>
 __device__ __forceinline__ void update(State<NK>& S, const char* ktile, const typename Op<T>::F (&vf)[2][2], const float* ws,
-                                       uint32_t kcol, int g) {
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const f32x4 w0 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 4 * g);
-    const f32x4 w1 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 16 + 4 * g);
-    f32x4 lo[2], hi[2];
+                                       float gm, uint32_t kcol, int g) {
+  if constexpr (sizeof(T) == 2) {
+    u32x4 x[2][2];  // [p][m]
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lo[p][e] = Op<T>::at(vf[p][m], e) * w0[e];
-        hi[p][e] = Op<T>::at(vf[p][m], 4 + e) * w1[e];
+      for (int m = 0; m < 2; ++m) x[p][m] = __builtin_bit_cast(u32x4, vf[p][m]);
+    f32x4 w[4];  // tokens 16j + 4g ..
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const f32x4*>(ws + 16 * j + 4 * g);
+    u32x4 t[2][2][3];  // [m][p][term]
+    auto word = [&](int m, int p, int q) {
+      const f32x4& ww = w[2 * m + (q >> 1)];
+      uint32_t a, b, c;
+      split_word(x[p][m][q], ww[2 * (q & 1)], ww[2 * (q & 1) + 1], a, b, c);
+      t[m][p][0][q] = a;
+      t[m][p][1][q] = b;
+      t[m][p][2][q] = c;
+    };
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      word(0, 0, q);
+      word(0, 1, q);
+    }
+    bf16x8 kf = KT::col(ktile, kcol, 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    constexpr int WPS = 8 / NK;  // words of the second half a step (NK = 4: two)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int a = 0; a < NK; ++a) {
+        const bf16x8 k = kf;
+        const int an = a + 1 < NK ? a + 1 : 0, mn = a + 1 < NK ? m : 1;
+        if (m == 0 || a + 1 < NK) kf = KT::col(ktile, kcol, mn, an >> 1, an & 1);
+        if (m == 0) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S.t[a][p][e] *= gm;
+#pragma unroll
+          for (int z = 0; z < WPS; ++z) word(1, (a * WPS + z) & 1, (a * WPS + z) >> 1);
+        }
+#pragma unroll
+        for (int n = 2; n >= 0; --n) {
+          S.t[a][0] = mfma_bf16_k32(S.t[a][0], k, __builtin_bit_cast(bf16x8, t[m][0][n]));
+          S.t[a][1] = mfma_bf16_k32(S.t[a][1], k, __builtin_bit_cast(bf16x8, t[m][1][n]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-    const Split<T, 3> x0(lo[0], hi[0]), x1(lo[1], hi[1]);
+  } else {
+    S.scale(gm);
 #pragma unroll
-    for (int a = 0; a < NK; ++a) {
-      const typename Op<T>::F kf = KT::col(ktile, kcol, m, a >> 1, a & 1);
+    for (int m = 0; m < 2; ++m) {
+      const f32x4 w0 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 4 * g);
+      const f32x4 w1 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 16 + 4 * g);
+      typename Op<T>::F y[2];
 #pragma unroll
-      for (int n = Split<T, 3>::N - 1; n >= 0; --n) {
-        S.t[a][0] = Op<T>::mma(S.t[a][0], kf, x0.t[n]);
-        S.t[a][1] = Op<T>::mma(S.t[a][1], kf, x1.t[n]);
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[p].v[e] = vf[p][m].v[e] * w0[e];
+          y[p].v[4 + e] = vf[p][m].v[4 + e] * w1[e];
+        }
+#pragma unroll
+      for (int a = 0; a < NK; ++a) {
+        const typename Op<T>::F kf = KT::col(ktile, kcol, m, a >> 1, a & 1);
+        S.t[a][0] = Op<T>::mma(S.t[a][0], kf, y[0]);
+        S.t[a][1] = Op<T>::mma(S.t[a][1], kf, y[1]);
       }
     }
   }
@@ -373,6 +439,24 @@ __device__ __forceinline__ void store8(T* p, const float* x) {
     *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
     *reinterpret_cast<f32x4*>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
   }
+}
+
+// sum over channels of A row tile J by B row tile I (both [64][COLS]): all operands
+// are read before the first product, so that one LDS latency is exposed and not one each
+template <typename T, int COLS>
+__device__ __forceinline__ f32x4 score_tile(const char* at, const char* bt, uint32_t off, int I, int J) {
+  typedef Tile<T, COLS> L;
+  typename Op<T>::F x[COLS / 32], y[COLS / 32];
+#pragma unroll
+  for (int m = 0; m < COLS / 32; ++m) {
+    x[m] = L::row(at, off, J, m);
+    y[m] = L::row(bt, off, I, m);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  f32x4 acc = zero4();
+#pragma unroll
+  for (int m = 0; m < COLS / 32; ++m) acc = Op<T>::mma(acc, x[m], y[m]);
+  return acc;
 }
 
 __device__ __forceinline__ int clamp_len(const int* lens, int b, int T) {
@@ -511,8 +595,7 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_state_kernel(PassArgs a) {
       for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv + uw * VT::BYTES, vcol, m, 0, p);
     const float gm = v[V_GM];
     dec *= gm;
-    S.scale(gm);
-    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, KT::col_off(g, i), g);
+    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, gm, KT::col_off(g, i), g);
     sync_lds();
   }
   const int un = 2 * it.sub + uw;
@@ -563,7 +646,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
   typedef Tile<T, 64> VT;
   typedef Scores<T> SC;
   constexpr int OV = 2 * KT::BYTES, OV2 = OV + 2 * VT::BYTES, OM = OV2 + (BWD ? 2 * VT::BYTES : 0);
-  constexpr int OVEC = OM + 2 * SC::BYTES, ORED = OVEC + 2 * V_SIZE * 4;
+  // two buffers of decay vectors, the next chunk's filled beside this one's products
+  // (one where the tiles leave no room)
+  constexpr int NB = sizeof(T) == 4 && BWD && DK == 128 ? 1 : 2;
+  constexpr int OVEC = OM + 2 * SC::BYTES, ORED = OVEC + NB * 2 * V_SIZE * 4;
   constexpr int RED = 4 * 64 + 4 * 64;  // column sums by J, row sums by I
   __shared__ __attribute__((aligned(16))) char smem[ORED + (BWD ? 2 * RED * 4 : 0)];
   char* const sq = smem;
@@ -571,7 +657,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
   char* const sv = smem + OV;
   char* const sv2 = smem + OV2;
   char* const sm = smem + OM;
-  float* const vec = reinterpret_cast<float*>(smem + OVEC);
+  float* const vecs = reinterpret_cast<float*>(smem + OVEC);
   float* const red = reinterpret_cast<float*>(smem + ORED);
   const int cpu = a.dv / 64, nu = a.H / a.G * cpu;
   const Item it = item_of(a.B, a.G, a.nseg, (nu + 1) / 2);
@@ -625,15 +711,29 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
       fv[u].template get<BWD>(V[u], a.vs.t, tok0, n, tid);
       if constexpr (BWD) fw[u].template get<BWD>(V2[u], a.v2s.t, tok0, n, tid);
     }
-    if (wave < 2) {
-      fx = decay_at<T, BWD>(la, a.ls.t, tok0, n, a.T, l);
-      fb = l < n ? to_f32(beta[(long long)(BWD ? tok0 + n - 1 - l : tok0 + l) * a.bs.t]) : 0.f;
-    }
   };
+  // decays and weights of a chunk, lane = position; waves 2 and 3, for units 0 and 1
+  const bool filler = wave >= 2;
+  auto fetch_gates = [&](int step) {
+    if (!filler || step >= c1 - c0) return;
+    const int c = BWD ? c1 - 1 - step : c0 + step;
+    const int tok0 = c * CH, n = min(CH, len - tok0);
+    fx = decay_at<T, BWD>(la, a.ls.t, tok0, n, a.T, l);
+    fb = l < n ? to_f32(beta[(long long)(BWD ? tok0 + n - 1 - l : tok0 + l) * a.bs.t]) : 0.f;
+  };
+  auto fill = [&](int step) {
+    if (filler && step < c1 - c0) fill_vec(vecs + ((step % NB) * 2 + wave - 2) * V_SIZE, l, fx, BWD ? 1.f : fb, 1.f, fb);
+  };
+  fetch_gates(0);
   if (c0 < c1) fetch(0);
+  if (NB == 2) {
+    fill(0);
+    fetch_gates(1);
+  }
   for (int step = 0; step < c1 - c0; ++step) {
     const int c = BWD ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, len - tok0);
+    float* const vec = vecs + (step % NB) * 2 * V_SIZE;
     fq.put(sq, tid);
     fk.put(sk, tid);
 #pragma unroll
@@ -641,7 +741,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
       fv[u].put(sv + u * VT::BYTES, tid);
       if constexpr (BWD) fw[u].put(sv2 + u * VT::BYTES, tid);
     }
-    if (wave < 2) fill_vec(vec + wave * V_SIZE, l, fx, BWD ? 1.f : fb, 1.f, fb);
+    if (NB == 1) {
+      fill(step);
+      fetch_gates(step + 1);
+    }
     if (step + 1 < c1 - c0) fetch(step + 1);
     sync_lds();
 
@@ -650,20 +753,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
     // scores, tiles dealt to the waves
     for (int t = wave; t < 10; t += 4) {
       const int I = tile_i(t), J = tile_j(t);
-      f32x4 acc = zero4();
-#pragma unroll
-      for (int m = 0; m < DK / 32; ++m)
-        acc = Op<T>::mma(acc, KT::row(sk, krow, J, m), KT::row(sq, krow, I, m));
+      const f32x4 acc = score_tile<T, DK>(sk, sq, krow, I, J);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const float* v = vec + u * V_SIZE;
         f32x4 mm = weigh(acc, v, I, J, g, i);
         if constexpr (BWD) {
           float* rd = red + u * RED;
-          f32x4 dd = zero4();
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-            dd = Op<T>::mma(dd, VT::row(sv + u * VT::BYTES, vrow, J, m), VT::row(sv2 + u * VT::BYTES, vrow, I, m));
+          const f32x4 dd = score_tile<T, 64>(sv + u * VT::BYTES, sv2 + u * VT::BYTES, vrow, I, J);
           const float bi = v[V_RH + 16 * I + i];
           float cs = 0.f, rs[4];
 #pragma unroll
@@ -687,6 +784,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
         }
         SC::put(sm + u * SC::BYTES, I, J, l, mm);
       }
+    }
+    if (NB == 2) {
+      fill(step + 1);
+      fetch_gates(step + 2);
     }
     const float* v = vec + uw * V_SIZE;
     f32x4 y[2][4];
@@ -747,18 +848,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
       if (p < n && mine) store8<T>(o + (long long)(BWD ? tok0 + n - 1 - p : tok0 + p) * a.os.t + 8 * g, x);
     }
     __builtin_amdgcn_sched_barrier(0);
-    S.scale(v[V_GM]);
-    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, KT::col_off(g, i), g);
+    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, v[V_GM], KT::col_off(g, i), g);
     sync_lds();
     if constexpr (BWD) {
-      // wave u writes unit u's sums (and refills that unit's vectors next)
-      if (wave < 2 && 2 * it.sub + wave < nu && l < n) {
-        const float* rd = red + wave * RED;
-        const float* w = vec + wave * V_SIZE;
+      // one wave writes a unit's sums, the one that fills that unit's vectors
+      if (filler && 2 * it.sub + wave - 2 < nu && l < n) {
+        const float* rd = red + (wave - 2) * RED;
+        const float* w = vec + (wave - 2) * V_SIZE;
         float cs = w[l] + w[64 + l], rs = 0.f;
         for (int J = 0; J <= (l >> 4); ++J) cs += rd[64 * J + l];
         for (int I = l >> 4; I < 4; ++I) rs += rd[256 + 64 * I + l];
-        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)head[wave & 1] * cpu + (2 * it.sub + wave) % cpu) * a.T + tok0 + n - 1 - l;
+        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)hv * cpu + (2 * it.sub + wave - 2) % cpu) * a.T + tok0 + n - 1 - l;
         a.c[at] = cs;
         a.r[at] = rs;
         a.d[at] = w[128 + l] + w[192 + l];
@@ -789,12 +889,12 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
   typedef Scores<T> SC;
   constexpr int OQ = VT::BYTES, OK = OQ + HG * QT::BYTES, OM = OK + HG * QT::BYTES;
   constexpr int OVEC = OM + HG * SC::BYTES;
-  __shared__ __attribute__((aligned(16))) char smem[OVEC + HG * V_SIZE * 4];
+  __shared__ __attribute__((aligned(16))) char smem[OVEC + 2 * HG * V_SIZE * 4];  // two buffers of decay vectors
   char* const sv = smem;
   char* const sq = smem + OQ;
   char* const sk = smem + OK;
   char* const sm = smem + OM;
-  float* const vec = reinterpret_cast<float*>(smem + OVEC);
+  float* const vecs = reinterpret_cast<float*>(smem + OVEC);
   const int R = a.H / a.G, np = (R + HG - 1) / HG;
   const Item it = item_of(a.B, a.G, a.nseg, np);
   if (!it.valid) return;
@@ -825,7 +925,7 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
           S[h].t[t][c] = *reinterpret_cast<const f32x4*>(p + (size_t)(32 * wave + pair_chan(c, i0)) * DV + pair_chan(t, 4 * g0));
     }
   }
-  const int hv = head[HG == 2 ? (wave & 1) : 0];
+  const int hv = head[HG == 2 ? (wave & 1) : 0];  // of the waves that fill the decay vectors, the last HG
   const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
 #pragma unroll
@@ -840,28 +940,38 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
     fv.template get<REV>(V, a.vs.t, tok0, n, tid);
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
-      const int nn = h < nh ? n : 0;
       fq[h].template get<REV>(Q[h], a.qs.t, tok0, n, tid);
       fk[h].template get<REV>(K[h], a.ks.t, tok0, n, tid);
-      (void)nn;
-    }
-    if (wave < HG) {
-      fx = decay_at<T, REV>(la, a.ls.t, tok0, n, a.T, l);
-      // a head past the group's last one gets no weight
-      fb = l < n && wave < nh ? to_f32(beta[(long long)(REV ? tok0 + n - 1 - l : tok0 + l) * a.bs.t]) : 0.f;
     }
   };
+  const bool filler = wave >= NW - HG;
+  const int fh = wave - (NW - HG);
+  auto fetch_gates = [&](int step) {
+    if (!filler || step >= c1 - c0) return;
+    const int c = REV ? c1 - 1 - step : c0 + step;
+    const int tok0 = c * CH, n = min(CH, a.T - tok0);
+    fx = decay_at<T, REV>(la, a.ls.t, tok0, n, a.T, l);
+    // a head past the group's last one gets no weight
+    fb = l < n && fh < nh ? to_f32(beta[(long long)(REV ? tok0 + n - 1 - l : tok0 + l) * a.bs.t]) : 0.f;
+  };
+  auto fill = [&](int step) {
+    if (filler && step < c1 - c0)
+      fill_vec(vecs + ((step & 1) * HG + fh) * V_SIZE, l, fx, REV ? 1.f : fb, REV ? fb : 1.f, fb);
+  };
+  fetch_gates(0);
   if (c0 < c1) fetch(0);
+  fill(0);
+  fetch_gates(1);
   for (int step = 0; step < c1 - c0; ++step) {
     const int c = REV ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, a.T - tok0);
+    float* const vec = vecs + (step & 1) * HG * V_SIZE;
     fv.put(sv, tid);
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
       fq[h].put(sq + h * QT::BYTES, tid);
       fk[h].put(sk + h * QT::BYTES, tid);
     }
-    if (wave < HG) fill_vec(vec + wave * V_SIZE, l, fx, REV ? 1.f : fb, REV ? fb : 1.f, fb);
     // the wave's columns of the q rows, for rs: straight from memory, in the layout of its results
     typename Op<T>::F xq[4];
     if constexpr (!REV) {
@@ -886,10 +996,7 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
       const int I = tile_i(t), J = tile_j(t);
 #pragma unroll
       for (int h = 0; h < HG; ++h) {
-        f32x4 acc = zero4();
-#pragma unroll
-        for (int m = 0; m < DV / 32; ++m)
-          acc = Op<T>::mma(acc, QT::row(sk + h * QT::BYTES, qrow, J, m), QT::row(sq + h * QT::BYTES, qrow, I, m));
+        const f32x4 acc = score_tile<T, DV>(sk + h * QT::BYTES, sq + h * QT::BYTES, qrow, I, J);
         const float* v = vec + h * V_SIZE;
         f32x4 mm = weigh(acc, v, I, J, g, i);
         if (REV && I == J) {
@@ -900,6 +1007,8 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
         SC::put(sm + h * SC::BYTES, I, J, l, mm);
       }
     }
+    fill(step + 1);
+    fetch_gates(step + 2);
     sync_lds();
 
     typename Op<T>::F vf[2][2];
@@ -969,8 +1078,7 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
       const float* v = vec + h * V_SIZE;
-      S[h].scale(v[V_GM]);
-      update<T, DV / 16, QT>(S[h], sk + h * QT::BYTES, vf, v + V_WS, QT::col_off(g, i), g);
+      update<T, DV / 16, QT>(S[h], sk + h * QT::BYTES, vf, v + V_WS, v[V_GM], QT::col_off(g, i), g);
       __builtin_amdgcn_sched_barrier(0);
     }
     sync_lds();
@@ -983,7 +1091,6 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
         const int hh = it.g * R + it.sub * HG + wave;
         rs[((size_t)it.b * a.H + hh) * a.T + tok0 + l] = s;
       }
-      // (read before this wave refills the same vectors for the next chunk)
     }
   }
 }
