@@ -46,13 +46,15 @@ kda_status check_dtype(kda_dtype dt) {
 // 16-byte boundaries.  Strides of dimensions of size 1 are not looked at.
 kda_status take_strides(const kda_strides* s, int B, int H, int T, int d, int es, bool row16, bool output,
                         const char* name, Str3* out) {
+  // (a chunk's rows are addressed with 32-bit offsets from its first one)
+  const long long most[3] = {kMaxElems, kMaxElems, 1 << 23};
   Str3 r{(long long)H * T * d, (long long)T * d, d};
   if (s) r = Str3{s->b, s->h, s->t};
   const long long v[3] = {r.b, r.h, r.t};
   const int n[3] = {B, H, T};
   for (int i = 0; i < 3; ++i) {
     if (n[i] <= 1) continue;
-    if (v[i] < 0 || v[i] > kMaxElems || (output && v[i] == 0))
+    if (v[i] < 0 || v[i] > most[i] || (output && v[i] == 0))
       return api_fail(KDA_ERR_SHAPE, "%s: stride %lld of dimension %d is not usable", name, v[i], i);
     if (row16 && v[i] * es % 16)
       return api_fail(KDA_ERR_ALIGN, "%s: stride %lld of dimension %d is not a multiple of 16 bytes", name, v[i], i);

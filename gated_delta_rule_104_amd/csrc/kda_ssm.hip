@@ -23,10 +23,12 @@
 //
 // Tiles.  v_mfma 16x16: the accumulator's rows 4g + e (g = lane / 16) are also the
 // contraction order of the next product's operand, so the scores (formed
-// transposed) and the state feed it from registers.  Rows of the state and columns
-// of V are taken in the order 32c + 8(r / 4) + 4(odd) + r % 4 for row r of an (even,
-// odd) pair of tiles, which makes a lane's share of a pair eight consecutive
-// channels: q is then read in its natural order and results stored 16 bytes a lane.
+// transposed) and the state feed it from registers.  Rows of the state are taken in
+// the order 32c + 8(r / 4) + 4(odd) + r % 4 for row r of an (even, odd) pair of
+// tiles, which makes a lane's share of a pair eight consecutive channels, so that
+// the rows it is multiplied with are read in their natural order.  A wave owns 16
+// columns of a state (32 registers a lane for 128 rows): with half as many waves of
+// 32 columns the products of one rarely ran beside the vector work of another.
 //
 // Precision.  bf16 inputs are exact operands.  The scores and the state are
 // rounded once to bf16 where they multiply V and Q (both times one rounding in
@@ -95,7 +97,12 @@ struct Split {
 };
 
 // ------------------------------------------------------------- LDS tiles
-// [64 tokens][COLS] of T, 16-byte granules XOR-swizzled by row (swz).  Reads take
+// [64 tokens][COLS] of T, 16-byte granules XORed with a function of the row, f: the
+// row's low bits, or, in rows of 256 bytes, its low four bits with the two pairs
+// exchanged.  The transposing reads take four neighbouring rows of four lanes each,
+// which that sends to four different parts of the banks (1.8 ns a wave's read and
+// compute unit, 3.4 with the plain bits; rows of 128 bytes: 1.8 plain, 3.4
+// exchanged).  Reads take
 // a lane's base offset, row_off or col_off, computed afresh for every chunk
 // (fresh_lane): a granule's number enters an address by XOR and a row tile by
 // addition, so that one register serves every read of a kind, where addresses
@@ -107,8 +114,14 @@ struct Tile {
   static constexpr int GPR = R / 16;  // granules per row
   static constexpr uint32_t MASK = GPR < 16 ? GPR - 1 : 15;
   static constexpr int GB = 32 * (int)sizeof(T);  // bytes of 32 channels
+  static __host__ __device__ __forceinline__ constexpr uint32_t f(uint32_t row) {
+    return GPR == 16 ? ((row & 3) << 2) | ((row >> 2) & 3) : row & MASK;
+  }
+  static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t byte) {
+    return row * R + ((((byte >> 4) ^ f(row)) << 4) | (byte & 15u));
+  }
 
-  static __device__ __forceinline__ uint32_t row_off(int g, int i) { return i * R + ((((GB / 64) * g) ^ (i & MASK)) << 4); }
+  static __device__ __forceinline__ uint32_t row_off(int g, int i) { return i * R + ((((GB / 64) * g) ^ f(i)) << 4); }
   // channels 32m + 8g .. + 7 of row 16 I + i
   static __device__ __forceinline__ typename Op<T>::F row(const char* s, uint32_t off, int I, int m) {
     const char* p = s + I * 16 * R;
@@ -116,15 +129,16 @@ struct Tile {
     else return Op<T>::round(lds_ld<f32x4>(p, off ^ (m * GB)), lds_ld<f32x4>(p, off ^ (m * GB) ^ 16));
   }
   // Contraction over tokens: lane (g, i) gets tokens 32m + 4g + e and 32m + 16 +
-  // 4g + e of channel 32c + 8(i / 4) + 4 odd + i % 4.  bf16: the transposing read
+  // 4g + e of channel 32c + 8(i / 4) + 4 odd + i % 4 (col, row tiles of a state) or
+  // 16 c + i (vcol, column tiles).  bf16: the transposing read
   // takes lane i's 8 bytes as row i of a 16 x 4 matrix and returns element
   // [4e + i / 4][i % 4] as lane i's e-th.
   static __device__ __forceinline__ uint32_t col_off(int g, int i) {
     if constexpr (sizeof(T) == 2) {
       const int r = 4 * g + (i >> 2);
-      return r * R + (((i & 3) ^ (r & MASK)) << 4);
+      return r * R + (((i & 3) ^ f(r)) << 4);
     } else {
-      return 4 * g * R + (((2 * (i >> 2)) ^ ((4 * g) & MASK)) << 4) + 4 * (i & 3);
+      return 4 * g * R + (((2 * (i >> 2)) ^ f(4 * g)) << 4) + 4 * (i & 3);
     }
   }
   static __device__ __forceinline__ typename Op<T>::F col(const char* s, uint32_t off, int m, int c, int odd) {
@@ -134,14 +148,49 @@ struct Tile {
       const bf16x4 lo = lds_tr16(p, o), hi = lds_tr16(p + 16 * R, o);
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
-      typename Op<T>::F f;
+      typename Op<T>::F x;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t o = off ^ (c * GB) ^ (odd * 16) ^ (e * 16);
-        f.v[e] = lds_ld<float>(p + e * R, o);
-        f.v[4 + e] = lds_ld<float>(p + (16 + e) * R, o);
+        const uint32_t o = off ^ (c * GB) ^ (odd * 16) ^ (f(e) << 4);
+        x.v[e] = lds_ld<float>(p + e * R, o);
+        x.v[4 + e] = lds_ld<float>(p + (16 + e) * R, o);
       }
-      return f;
+      return x;
+    }
+  }
+  static __device__ __forceinline__ uint32_t vcol_off(int g, int i) {
+    if constexpr (sizeof(T) == 2) {
+      const int r = 4 * g + (i >> 2);
+      return r * R + ((((i & 3) >> 1) ^ f(r)) << 4) + 8 * (i & 1);
+    } else {
+      return 4 * g * R + (((i >> 2) ^ f(4 * g)) << 4) + 4 * (i & 3);
+    }
+  }
+  static __device__ __forceinline__ typename Op<T>::F vcol(const char* s, uint32_t off, int m, int c) {
+    const char* p = s + 32 * m * R;
+    off ^= c * (GB / 2);
+    if constexpr (sizeof(T) == 2) {
+      const bf16x4 lo = lds_tr16(p, off), hi = lds_tr16(p + 16 * R, off);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      typename Op<T>::F x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t o = off ^ (f(e) << 4);
+        x.v[e] = lds_ld<float>(p + e * R, o);
+        x.v[4 + e] = lds_ld<float>(p + (16 + e) * R, o);
+      }
+      return x;
+    }
+  }
+  // channels 16c + 4g .. + 3 of row 16 I + i, as floats (a lane's place in a result)
+  static __device__ __forceinline__ f32x4 quad(const char* s, int I, int i, int c, int g) {
+    const uint32_t o = at(16 * I + i, (16 * c + 4 * g) * (int)sizeof(T));
+    if constexpr (sizeof(T) == 2) {
+      const bf16x4 x = lds_ld<bf16x4>(s, o);
+      return f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+    } else {
+      return lds_ld<f32x4>(s, o);
     }
   }
 };
@@ -154,28 +203,37 @@ struct Fetch {
   static constexpr int N = CH / STEP;
   static_assert(STEP >= 1 && (STEP & (STEP - 1)) == 0 && STEP * L::GPR == NT, "whole rows");
   u32x4 r[N];
+  // Byte offset of the thread's first granule from the chunk's base: a uniform base
+  // and a 32-bit offset are all that a load needs, so that a full chunk's addresses
+  // cost no vector instructions.  Position p is token p, or CH - 1 - p reversed.
+  template <bool REV>
+  static __device__ __forceinline__ uint32_t lane_off(long long st, int tid) {
+    const int row = tid / L::GPR, c = tid % L::GPR;
+    return ((uint32_t)(REV ? CH - 1 - row : row) * (uint32_t)st) * (uint32_t)sizeof(T) + 16u * c;
+  }
   // position p of the chunk is token tok0 + p, or tok0 + n - 1 - p reversed; rows past n are zero
   template <bool REV>
-  __device__ __forceinline__ void get(const T* p, long long st, int tok0, int n, int tid) {
-    const int row = tid / L::GPR, c = tid % L::GPR;
-    const T* q = p + (long long)(REV ? tok0 + n - 1 - row : tok0 + row) * st + c * (16 / (int)sizeof(T));
-    const long long d = REV ? -STEP * st : STEP * st;
+  __device__ __forceinline__ void get(const T* p, long long st, int tok0, int n, uint32_t off, int tid) {
+    off = fresh_lane(off);  // (or its sum with the tensor's address would be kept, in two registers)
+    const char* b = reinterpret_cast<const char*>(p + (long long)(REV ? tok0 + n - CH : tok0) * st);
+    const long long d = (REV ? -STEP : STEP) * st * (long long)sizeof(T);
     if (n == CH) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const u32x4*>(q + i * d);
+      for (int i = 0; i < N; ++i) r[i] = *reinterpret_cast<const u32x4*>(b + i * d + off);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         r[i] = u32x4{0u, 0u, 0u, 0u};
-        if (row + i * STEP < n) r[i] = *reinterpret_cast<const u32x4*>(q + i * d);
+        if (tid / L::GPR + i * STEP < n) r[i] = *reinterpret_cast<const u32x4*>(b + i * d + off);
       }
     }
   }
   __device__ __forceinline__ void put(char* s, int tid) const {
+    tid = fresh_lane(tid);  // (formed again for every chunk rather than kept in a register)
     const int row = tid / L::GPR, c = tid % L::GPR;
-    const uint32_t off = swz<L::R>(row, 16 * c);
+    const uint32_t off = L::at(row, 16 * c);
 #pragma unroll
-    for (int i = 0; i < N; ++i) lds_st<u32x4>(s + i * STEP * L::R, off ^ (((i * STEP) & L::MASK) << 4), r[i]);
+    for (int i = 0; i < N; ++i) lds_st<u32x4>(s + i * STEP * L::R, off ^ (L::f(i * STEP) << 4), r[i]);
   }
 };
 
@@ -188,8 +246,9 @@ enum { V_PB = 0, V_U = 64, V_W = 128, V_KP = 192, V_RH = 256, V_IN = 320, V_WS =
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// One wave fills a head's vectors; lane r is position r with decay x (log2 units).
+// One wave fills a head's vectors; lane r is position r with decay x.
 __device__ __forceinline__ void fill_vec(float* v, int r, float x, float kappa, float rho, float rh) {
+  x *= kLog2e;
   x = x < -180.f ? -180.f : x;  // (a NaN passes)
   float pre = x;
   pre += dpp<DPP_ROW_SHR + 1>(pre);
@@ -219,14 +278,24 @@ __device__ __forceinline__ void fill_vec(float* v, int r, float x, float kappa, 
   if (r == 0) v[V_GM] = e0 * e1 * e2 * e3;
 }
 
-// The decay of position p in log2 units: the token's own, or reversed the next
-// token's (0 behind the last).
+// The gate of position p as it is stored: the token's own, or reversed the next
+// token's (0 behind the last).  It is converted where it is used: a conversion here
+// would wait for the tiles on their way too.
 template <typename T, bool REV>
-__device__ __forceinline__ float decay_at(const T* la, long long st, int tok0, int n, int Ttot, int p) {
-  if (p >= n) return 0.f;
+__device__ __forceinline__ T decay_at(const T* la, long long st, int tok0, int n, int Ttot, int p) {
+  p = fresh_lane(p);
   const int t = REV ? tok0 + n - p : tok0 + p;
-  if (REV && t >= Ttot) return 0.f;
-  const float x = to_f32(la[(long long)t * st]) * kLog2e;
+  T x = T(0.f);
+  const T* b = la + (long long)(REV ? tok0 + n - CH + 1 : tok0) * st;
+  if (p < n && !(REV && t >= Ttot)) x = b[(uint32_t)(REV ? CH - 1 - p : p) * (uint32_t)st];
+  return x;
+}
+template <typename T, bool REV>
+__device__ __forceinline__ T weight_at(const T* beta, long long st, int tok0, int n, int p, bool on) {
+  p = fresh_lane(p);
+  T x = T(0.f);
+  const T* b = beta + (long long)(REV ? tok0 + n - CH : tok0) * st;
+  if (p < n && on) x = b[(uint32_t)(REV ? CH - 1 - p : p) * (uint32_t)st];
   return x;
 }
 
@@ -279,27 +348,13 @@ __device__ __forceinline__ f32x4 weigh(f32x4 acc, const float* v, int I, int J, 
 }
 
 // -------------------------------------------------------- state and results
-// A wave's state: NK = rows / 16 by two column tiles.
+// A wave's state: NK = rows / 16 tiles of 16 columns.
 template <int NK>
 struct State {
-  f32x4 t[NK][2];
+  f32x4 t[NK];
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int a = 0; a < NK; ++a) t[a][0] = t[a][1] = zero4();
-  }
-  // Makes the compiler take the values as new, so that operands formed from them
-  // before are formed again rather than kept in registers.
-  __device__ __forceinline__ void renew() {
-#pragma unroll
-    for (int a = 0; a < NK; ++a) asm volatile("" : "+v"(t[a][0]), "+v"(t[a][1]));
-  }
-  __device__ __forceinline__ void scale(float s) {
-#pragma unroll
-    for (int a = 0; a < NK; ++a)
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[a][p][e] *= s;
+    for (int a = 0; a < NK; ++a) t[a] = zero4();
   }
 };
 __device__ __forceinline__ int pair_chan(int tile, int r) { return 32 * (tile >> 1) + 8 * (r >> 2) + 4 * (tile & 1) + (r & 3); }
@@ -316,121 +371,111 @@ __device__ __forceinline__ void split_word(uint32_t x, float wa, float wb, uint3
   t2 = cvt2(a, b);
 }
 
-// S <- gm S + K^T (w V): w the per-token weights, V the wave's two column tiles
-// (two 32-token halves each).  bf16: six products a row tile and token half; the
-// state's scaling and the second half's terms are dealt over the first half's
-// products, whose time on the matrix cores they fit into.
+// S <- gm S + K^T (w V): w the per-token weights, V the wave's column tile (two
+// 32-token halves).  bf16: row tiles in pairs, so that the three products into one
+// accumulator have others between them; the state's scaling and the second half's
+// terms are dealt over the first half's products, whose time on the matrix cores
+// they fit into.
 template <typename T, int NK, typename KT>
-__device__ __forceinline__ void update(State<NK>& S, const char* ktile, const typename Op<T>::F (&vf)[2][2], const float* ws,
+__device__ __forceinline__ void update(State<NK>& S, const char* ktile, const typename Op<T>::F (&vf)[2], const float* ws,
                                        float gm, uint32_t kcol, int g) {
   if constexpr (sizeof(T) == 2) {
-    u32x4 x[2][2];  // [p][m]
+    u32x4 x[2], t[2][3];  // [m], [m][term]
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) x[p][m] = __builtin_bit_cast(u32x4, vf[p][m]);
-    f32x4 w[4];  // tokens 16j + 4g ..
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const f32x4*>(ws + 16 * j + 4 * g);
-    u32x4 t[2][2][3];  // [m][p][term]
-    auto word = [&](int m, int p, int q) {
-      const f32x4& ww = w[2 * m + (q >> 1)];
+    for (int m = 0; m < 2; ++m) x[m] = __builtin_bit_cast(u32x4, vf[m]);
+    auto word = [&](int m, int q) {
+      const f32x2 w = *reinterpret_cast<const f32x2*>(ws + 32 * m + 16 * (q >> 1) + 4 * g + 2 * (q & 1));
       uint32_t a, b, c;
-      split_word(x[p][m][q], ww[2 * (q & 1)], ww[2 * (q & 1) + 1], a, b, c);
-      t[m][p][0][q] = a;
-      t[m][p][1][q] = b;
-      t[m][p][2][q] = c;
+      split_word(x[m][q], w[0], w[1], a, b, c);
+      t[m][0][q] = a;
+      t[m][1][q] = b;
+      t[m][2][q] = c;
     };
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      word(0, 0, q);
-      word(0, 1, q);
-    }
-    bf16x8 kf = KT::col(ktile, kcol, 0, 0, 0);
+    for (int q = 0; q < 4; ++q) word(0, q);
+    bf16x8 k0 = KT::col(ktile, kcol, 0, 0, 0), k1 = KT::col(ktile, kcol, 0, 0, 1);
     __builtin_amdgcn_sched_barrier(0);
-    constexpr int WPS = 8 / NK;  // words of the second half a step (NK = 4: two)
+    constexpr int NP = NK / 2;      // pairs of row tiles
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int a = 0; a < NK; ++a) {
-        const bf16x8 k = kf;
-        const int an = a + 1 < NK ? a + 1 : 0, mn = a + 1 < NK ? m : 1;
-        if (m == 0 || a + 1 < NK) kf = KT::col(ktile, kcol, mn, an >> 1, an & 1);
+      for (int a = 0; a < NP; ++a) {
+        const bf16x8 c0 = k0, c1 = k1;
+        const int an = a + 1 < NP ? a + 1 : 0, mn = a + 1 < NP ? m : 1;
+        if (m == 0 || a + 1 < NP) {
+          k0 = KT::col(ktile, kcol, mn, an, 0);
+          k1 = KT::col(ktile, kcol, mn, an, 1);
+        }
         if (m == 0) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
+          for (int e = 0; e < 4; ++e) {
+            S.t[2 * a][e] *= gm;
+            S.t[2 * a + 1][e] *= gm;
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S.t[a][p][e] *= gm;
-#pragma unroll
-          for (int z = 0; z < WPS; ++z) word(1, (a * WPS + z) & 1, (a * WPS + z) >> 1);
+          for (int q = a * 4 / NP; q < (a + 1) * 4 / NP; ++q) word(1, q);
         }
 #pragma unroll
         for (int n = 2; n >= 0; --n) {
-          S.t[a][0] = mfma_bf16_k32(S.t[a][0], k, __builtin_bit_cast(bf16x8, t[m][0][n]));
-          S.t[a][1] = mfma_bf16_k32(S.t[a][1], k, __builtin_bit_cast(bf16x8, t[m][1][n]));
+          S.t[2 * a] = mfma_bf16_k32(S.t[2 * a], c0, __builtin_bit_cast(bf16x8, t[m][n]));
+          S.t[2 * a + 1] = mfma_bf16_k32(S.t[2 * a + 1], c1, __builtin_bit_cast(bf16x8, t[m][n]));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
   } else {
-    S.scale(gm);
+#pragma unroll
+    for (int a = 0; a < NK; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S.t[a][e] *= gm;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const f32x4 w0 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 4 * g);
       const f32x4 w1 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 16 + 4 * g);
-      typename Op<T>::F y[2];
+      typename Op<T>::F y;
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[p].v[e] = vf[p][m].v[e] * w0[e];
-          y[p].v[4 + e] = vf[p][m].v[4 + e] * w1[e];
-        }
-#pragma unroll
-      for (int a = 0; a < NK; ++a) {
-        const typename Op<T>::F kf = KT::col(ktile, kcol, m, a >> 1, a & 1);
-        S.t[a][0] = Op<T>::mma(S.t[a][0], kf, y[0]);
-        S.t[a][1] = Op<T>::mma(S.t[a][1], kf, y[1]);
+      for (int e = 0; e < 4; ++e) {
+        y.v[e] = vf[m].v[e] * w0[e];
+        y.v[4 + e] = vf[m].v[4 + e] * w1[e];
       }
+#pragma unroll
+      for (int a = 0; a < NK; ++a) S.t[a] = Op<T>::mma(S.t[a], KT::col(ktile, kcol, m, a >> 1, a & 1), y);
     }
   }
 }
 
-// Y^T[p][I] = S^T Q^T (rows: the wave's columns, columns: tokens) for the NI row
-// tiles from I0 on, NT terms of S
-template <typename T, int NK, int NT, typename QT, int NI>
-__device__ __forceinline__ void inter(f32x4 (&y)[2][NI], const State<NK>& S, const char* qtile, uint32_t qrow, int I0) {
+// Y^T[I] = S^T Q^T (rows: the wave's columns, columns: tokens), NT terms of S
+template <typename T, int NK, int NT, typename QT>
+__device__ __forceinline__ void inter(f32x4 (&y)[4], const State<NK>& S, const char* qtile, uint32_t qrow) {
 #pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int I = 0; I < NI; ++I) y[p][I] = zero4();
+  for (int I = 0; I < 4; ++I) y[I] = zero4();
 #pragma unroll
   for (int m = 0; m < NK / 2; ++m) {
-    const Split<T, NT> s0(S.t[2 * m][0], S.t[2 * m + 1][0]), s1(S.t[2 * m][1], S.t[2 * m + 1][1]);
+    const Split<T, NT> s(S.t[2 * m], S.t[2 * m + 1]);
+    typename Op<T>::F qf[4];
 #pragma unroll
-    for (int I = 0; I < NI; ++I) {
-      const typename Op<T>::F qf = QT::row(qtile, qrow, I0 + I, m);
+    for (int I = 0; I < 4; ++I) qf[I] = QT::row(qtile, qrow, I, m);
 #pragma unroll
-      for (int n = Split<T, NT>::N - 1; n >= 0; --n) {
-        y[0][I] = Op<T>::mma(y[0][I], s0.t[n], qf);
-        y[1][I] = Op<T>::mma(y[1][I], s1.t[n], qf);
-      }
-    }
+    for (int n = Split<T, NT>::N - 1; n >= 0; --n)
+#pragma unroll
+      for (int I = 0; I < 4; ++I) y[I] = Op<T>::mma(y[I], s.t[n], qf[I]);
+    __builtin_amdgcn_sched_barrier(0);  // (one step's operands in registers)
   }
 }
 
 // Y^T += V^T M^T
-template <typename T, int I0, int NI>
-__device__ __forceinline__ void intra(f32x4 (&y)[2][NI], const typename Op<T>::F (&vf)[2][2], const char* scores, int l) {
+template <typename T>
+__device__ __forceinline__ void intra(f32x4 (&y)[4], const typename Op<T>::F (&vf)[2], const char* scores, int l) {
 #pragma unroll
-  for (int I = 0; I < NI; ++I)
+  for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int m = 0; m <= (I0 + I) / 2; ++m) {
-      const typename Op<T>::F mf = Scores<T>::get(scores, I0 + I, m, l);
-      y[0][I] = Op<T>::mma(y[0][I], vf[0][m], mf);
-      y[1][I] = Op<T>::mma(y[1][I], vf[1][m], mf);
-    }
+    for (int I = 2 * m; I < 4; ++I) y[I] = Op<T>::mma(y[I], vf[m], Scores<T>::get(scores, I, m, l));
 }
 
+template <typename T>
+__device__ __forceinline__ void store4(T* p, f32x4 x) {
+  if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2*>(p) = u32x2{cvt2(x[0], x[1]), cvt2(x[2], x[3])};
+  else *reinterpret_cast<f32x4*>(p) = x;
+}
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float* x) {
   if constexpr (sizeof(T) == 2) {
@@ -457,6 +502,22 @@ __device__ __forceinline__ f32x4 score_tile(const char* at, const char* bt, uint
 #pragma unroll
   for (int m = 0; m < COLS / 32; ++m) acc = Op<T>::mma(acc, x[m], y[m]);
   return acc;
+}
+
+// The wave's four row tiles of results, row 16 I + i at p + I * d + off, rows below n.
+// A full chunk's four stores stand in no branch of their own: the wait for the next
+// chunk's tiles, which were loaded earlier, can then leave them on their way.
+template <typename T>
+__device__ __forceinline__ void store_rows(const f32x4 (&y)[4], char* p, long long d, uint32_t off, int n, int i) {
+  if (n == CH) {
+#pragma unroll
+    for (int I = 0; I < 4; ++I) store4<T>(reinterpret_cast<T*>(p + I * d + off), y[I]);
+  } else {
+#pragma unroll
+    for (int I = 0; I < 4; ++I)
+      if (16 * I + i < n) store4<T>(reinterpret_cast<T*>(p + I * d + off), y[I]);
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no unknown number of them is left
+  }
 }
 
 __device__ __forceinline__ int clamp_len(const int* lens, int b, int T) {
@@ -514,31 +575,28 @@ __device__ __forceinline__ void load_state(State<NK>& S, const float* p, int ld,
 #pragma unroll
   for (int a = 0; a < NK; ++a)
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S.t[a][c][e] = p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + pair_chan(c, i)];
+    for (int e = 0; e < 4; ++e) S.t[a][e] = p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + i];
 }
 template <int NK>
 __device__ __forceinline__ void store_state(const State<NK>& S, float* p, int ld, int col0, int g, int i, float s) {
 #pragma unroll
   for (int a = 0; a < NK; ++a)
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + pair_chan(c, i)] = s * S.t[a][c][e];
+    for (int e = 0; e < 4; ++e) p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + i] = s * S.t[a][e];
 }
 
 // ------------------------------------------------------------- state pass
 // End state of every segment from zero.  Workgroup = two 64-column units of one
-// group, wave = 32 columns of one.
+// group, wave = 16 columns of one.
 template <typename T, int DK, bool REV>
-__global__ __launch_bounds__(256, 2) void kda_ssm_state_kernel(PassArgs a) {
+__global__ __launch_bounds__(512, 4) void kda_ssm_state_kernel(PassArgs a) {
   typedef Tile<T, DK> KT;
   typedef Tile<T, 64> VT;
-  __shared__ __attribute__((aligned(16))) char smem[KT::BYTES + 2 * VT::BYTES + 2 * V_SIZE * 4];
+  constexpr int NT = 512;
+  __shared__ __attribute__((aligned(16))) char smem[KT::BYTES + 2 * VT::BYTES + 4 * V_SIZE * 4];
   char* const sk = smem;
   char* const sv = smem + KT::BYTES;
-  float* const vec = reinterpret_cast<float*>(sv + 2 * VT::BYTES);
+  float* const vecs = reinterpret_cast<float*>(sv + 2 * VT::BYTES);
   const int cpu = a.dv / 64, nu = a.H / a.G * cpu;  // column units per head, units per group
   const Item it = item_of(a.B, a.G, a.norders, (nu + 1) / 2);
   if (!it.valid) return;
@@ -547,7 +605,7 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_state_kernel(PassArgs a) {
   const int nch = (len + CH - 1) / CH;
   const int seg = REV ? a.nseg - 1 - it.seg : it.seg;
   const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
-  const int uw = wave >> 1, half = wave & 1;
+  const int uw = wave >> 2, quarter = wave & 3;
   const T* K = static_cast<const T*>(a.K) + it.b * a.ks.b + it.g * a.ks.h;
   int head[2];
   const T* V[2];
@@ -557,42 +615,52 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_state_kernel(PassArgs a) {
     head[u] = it.g * (a.H / a.G) + un / cpu;
     V[u] = static_cast<const T*>(a.V) + it.b * a.vs.b + head[u] * a.vs.h + (un % cpu) * 64;
   }
-  const int hv = head[wave & 1];
+  const bool filler = wave >= 6;  // waves 6 and 7, for units 0 and 1
+  const int hv = wave & 1 ? head[1] : head[0];
   const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
   State<DK / 16> S;
   S.zero();
   float dec = 1.f;
-  Fetch<T, DK, 256> fk;
-  Fetch<T, 64, 256> fv[2];
-  float fx = 0.f, fb = 0.f;
+  Fetch<T, DK, NT> fk;
+  Fetch<T, 64, NT> fv[2];
+  const uint32_t ofk = fk.template lane_off<REV>(a.ks.t, tid), ofv = fv[0].template lane_off<REV>(a.vs.t, tid);
+  T fx = T(0.f), fb = T(0.f);
   auto fetch = [&](int step) {
     const int c = REV ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, len - tok0);
-    fk.template get<REV>(K, a.ks.t, tok0, n, tid);
+    fk.template get<REV>(K, a.ks.t, tok0, n, ofk, tid);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) fv[u].template get<REV>(V[u], a.vs.t, tok0, n, tid);
-    if (wave < 2) {
-      fx = decay_at<T, REV>(la, a.ls.t, tok0, n, a.T, l);
-      fb = !REV && l < n ? to_f32(beta[(long long)(tok0 + l) * a.bs.t]) : 1.f;
-    }
+    for (int u = 0; u < 2; ++u) fv[u].template get<REV>(V[u], a.vs.t, tok0, n, ofv, tid);
   };
+  auto fetch_gates = [&](int step) {
+    if (!filler || step >= c1 - c0) return;
+    const int c = REV ? c1 - 1 - step : c0 + step;
+    const int tok0 = c * CH, n = min(CH, len - tok0);
+    fx = decay_at<T, REV>(la, a.ls.t, tok0, n, a.T, l);
+    fb = weight_at<T, false>(beta, a.bs.t, tok0, n, l, !REV);
+  };
+  auto fill = [&](int step) {
+    if (filler && step < c1 - c0) fill_vec(vecs + ((step & 1) * 2 + wave - 6) * V_SIZE, l, to_f32(fx), REV ? 1.f : to_f32(fb), 1.f, 1.f);
+  };
+  fetch_gates(0);
   if (c0 < c1) fetch(0);
+  fill(0);
+  fetch_gates(1);
   for (int step = 0; step < c1 - c0; ++step) {
+    const float* const v = vecs + ((step & 1) * 2 + uw) * V_SIZE;
     fk.put(sk, tid);
 #pragma unroll
     for (int u = 0; u < 2; ++u) fv[u].put(sv + u * VT::BYTES, tid);
-    if (wave < 2) fill_vec(vec + wave * V_SIZE, l, fx, fb, 1.f, 1.f);
     if (step + 1 < c1 - c0) fetch(step + 1);
     sync_lds();
-    const float* v = vec + uw * V_SIZE;
+    fill(step + 1);
+    fetch_gates(step + 2);
     const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
-    const uint32_t vcol = VT::col_off(g, i) ^ (half * VT::GB);
-    typename Op<T>::F vf[2][2];
+    const uint32_t vcol = VT::vcol_off(g, i);
+    typename Op<T>::F vf[2];
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv + uw * VT::BYTES, vcol, m, 0, p);
+    for (int m = 0; m < 2; ++m) vf[m] = VT::vcol(sv + uw * VT::BYTES, vcol, m, quarter);
     const float gm = v[V_GM];
     dec *= gm;
     update<T, DK / 16, KT>(S, sk, vf, v + V_WS, gm, KT::col_off(g, i), g);
@@ -600,12 +668,11 @@ __global__ __launch_bounds__(256, 2) void kda_ssm_state_kernel(PassArgs a) {
   }
   const int un = 2 * it.sub + uw;
   if (un >= nu) return;
-  const int g = l >> 4, i = l & 15;
-  const size_t bh = (size_t)it.b * a.H + head[uw];
+  const size_t bh = (size_t)it.b * a.H + (uw ? head[1] : head[0]);
   // order o's end state lies in slot o + 1
   float* out = a.end + ((size_t)(it.seg + 1) * a.B * a.H + bh) * a.dk * a.dv;
-  store_state(S, out, a.dv, (un % cpu) * 64 + half * 32, g, i, 1.f);
-  if (half == 0 && un % cpu == 0 && l == 0) a.dec[(size_t)it.seg * a.B * a.H + bh] = dec;
+  store_state(S, out, a.dv, (un % cpu) * 64 + quarter * 16, l >> 4, l & 15, 1.f);
+  if (quarter == 0 && un % cpu == 0 && l == 0) a.dec[(size_t)it.seg * a.B * a.H + bh] = dec;
 }
 
 // slots[0] = start; slots[o + 1] = dec[o] slots[o] + slots[o + 1], o = 0 .. n - 1
@@ -632,7 +699,7 @@ __global__ __launch_bounds__(256) void kda_ssm_copy_kernel(const float* src, flo
 }
 
 // ----------------------------------------------------------------- outputs
-// Workgroup = two 64-column units of one group over a segment's chunks, wave = 32
+// Workgroup = two 64-column units of one group over a segment's chunks, wave = 16
 // columns of one unit.  Per chunk: the scores are formed once (Q.K once for both
 // units) and left in LDS; every wave then forms its columns of Y and moves its
 // state on.  The next chunk's tiles are loaded to registers meanwhile.
@@ -641,10 +708,11 @@ __global__ __launch_bounds__(256) void kda_ssm_copy_kernel(const float* src, flo
 //   c[j] = sum_i P_ij (and the state's part), r[i] = sum_j beta_j P_ij (inside the
 //   chunk), d[i] = dO_i.v_i, with P_ij = (dO_i.v_j) (q_i.k_j) e^{l_i - l_j}.
 template <typename T, int DK, bool BWD>
-__global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1) void kda_ssm_out_kernel(PassArgs a) {
+__global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2) void kda_ssm_out_kernel(PassArgs a) {
   typedef Tile<T, DK> KT;
   typedef Tile<T, 64> VT;
   typedef Scores<T> SC;
+  constexpr int NT = 512;
   constexpr int OV = 2 * KT::BYTES, OV2 = OV + 2 * VT::BYTES, OM = OV2 + (BWD ? 2 * VT::BYTES : 0);
   // two buffers of decay vectors, the next chunk's filled beside this one's products
   // (one where the tiles leave no room)
@@ -667,7 +735,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
   const int nch = (len + CH - 1) / CH;
   const int seg = BWD ? a.nseg - 1 - it.seg : it.seg;
   const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
-  const int uw = wave >> 1, half = wave & 1;
+  const int uw = wave >> 2, quarter = wave & 3;
   const T* Q = static_cast<const T*>(a.Q) + it.b * a.qs.b + it.g * a.qs.h;
   const T* K = static_cast<const T*>(a.K) + it.b * a.ks.b + it.g * a.ks.h;
   int head[2], colu[2];
@@ -680,9 +748,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
     V[u] = static_cast<const T*>(a.V) + it.b * a.vs.b + head[u] * a.vs.h + colu[u];
     V2[u] = BWD ? static_cast<const T*>(a.V2) + it.b * a.v2s.b + head[u] * a.v2s.h + colu[u] : nullptr;
   }
-  const int un = 2 * it.sub + uw;
-  const bool mine = un < nu;
-  const int hv = head[wave & 1];
+  const bool mine = 2 * it.sub + uw < nu;
+  const int hw = uw ? head[1] : head[0], cw = (uw ? colu[1] : colu[0]) + quarter * 16;  // the wave's head and column
+  const bool filler = wave >= 6;  // waves 6 and 7 fill the decay vectors, of units 0 and 1
+  const int hv = wave & 1 ? head[1] : head[0];
   const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
   float skip[2] = {0.f, 0.f};
@@ -690,39 +759,41 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
 #pragma unroll
     for (int u = 0; u < 2; ++u) skip[u] = to_f32(static_cast<const T*>(a.D)[head[u]]);
   }
-  T* o = static_cast<T*>(a.o) + it.b * a.os.b + head[uw] * a.os.h + colu[uw] + half * 32;
-  const size_t bh = (size_t)it.b * a.H + head[uw];
+  const float skip_w = uw ? skip[1] : skip[0];
+  T* o = static_cast<T*>(a.o) + it.b * a.os.b + hw * a.os.h + cw;
+  const size_t bh = (size_t)it.b * a.H + hw;
   State<DK / 16> S;
-  if (a.start) load_state(S, a.start + ((size_t)it.seg * a.B * a.H + bh) * a.dk * a.dv, a.dv, colu[uw] + half * 32, l >> 4, l & 15);
+  if (a.start) load_state(S, a.start + ((size_t)it.seg * a.B * a.H + bh) * a.dk * a.dv, a.dv, cw, l >> 4, l & 15);
   else S.zero();
-  SC::clear(sm, tid, 256);
-  SC::clear(sm + SC::BYTES, tid, 256);
+  SC::clear(sm, tid, NT);
+  SC::clear(sm + SC::BYTES, tid, NT);
 
-  Fetch<T, DK, 256> fq, fk;
-  Fetch<T, 64, 256> fv[2], fw[2];
-  float fx = 0.f, fb = 0.f;
+  Fetch<T, DK, NT> fq, fk;
+  Fetch<T, 64, NT> fv[2], fw[2];
+  const uint32_t ofq = fq.template lane_off<BWD>(a.qs.t, tid), ofk = fk.template lane_off<BWD>(a.ks.t, tid);
+  const uint32_t ofv = fv[0].template lane_off<BWD>(a.vs.t, tid), ofw = BWD ? fw[0].template lane_off<BWD>(a.v2s.t, tid) : 0u;
+  T fx = T(0.f), fb = T(0.f);
   auto fetch = [&](int step) {
     const int c = BWD ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, len - tok0);
-    fq.template get<BWD>(Q, a.qs.t, tok0, n, tid);
-    fk.template get<BWD>(K, a.ks.t, tok0, n, tid);
+    fq.template get<BWD>(Q, a.qs.t, tok0, n, ofq, tid);
+    fk.template get<BWD>(K, a.ks.t, tok0, n, ofk, tid);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      fv[u].template get<BWD>(V[u], a.vs.t, tok0, n, tid);
-      if constexpr (BWD) fw[u].template get<BWD>(V2[u], a.v2s.t, tok0, n, tid);
+      fv[u].template get<BWD>(V[u], a.vs.t, tok0, n, ofv, tid);
+      if constexpr (BWD) fw[u].template get<BWD>(V2[u], a.v2s.t, tok0, n, ofw, tid);
     }
   };
-  // decays and weights of a chunk, lane = position; waves 2 and 3, for units 0 and 1
-  const bool filler = wave >= 2;
+  // decays and weights of a chunk, lane = position
   auto fetch_gates = [&](int step) {
     if (!filler || step >= c1 - c0) return;
     const int c = BWD ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, len - tok0);
     fx = decay_at<T, BWD>(la, a.ls.t, tok0, n, a.T, l);
-    fb = l < n ? to_f32(beta[(long long)(BWD ? tok0 + n - 1 - l : tok0 + l) * a.bs.t]) : 0.f;
+    fb = weight_at<T, BWD>(beta, a.bs.t, tok0, n, l, true);
   };
   auto fill = [&](int step) {
-    if (filler && step < c1 - c0) fill_vec(vecs + ((step % NB) * 2 + wave - 2) * V_SIZE, l, fx, BWD ? 1.f : fb, 1.f, fb);
+    if (filler && step < c1 - c0) fill_vec(vecs + ((step % NB) * 2 + wave - 6) * V_SIZE, l, to_f32(fx), BWD ? 1.f : to_f32(fb), 1.f, to_f32(fb));
   };
   fetch_gates(0);
   if (c0 < c1) fetch(0);
@@ -749,9 +820,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
     sync_lds();
 
     const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
-    const uint32_t krow = KT::row_off(g, i), vrow = VT::row_off(g, i);
-    // scores, tiles dealt to the waves
-    for (int t = wave; t < 10; t += 4) {
+    const uint32_t krow = KT::row_off(g, i);
+    // scores: the ten tiles dealt to the waves, the two left over to waves 4 and 5
+    for (int t = wave; t < 10; t += wave < 4 ? 16 : 4) {
       const int I = tile_i(t), J = tile_j(t);
       const f32x4 acc = score_tile<T, DK>(sk, sq, krow, I, J);
 #pragma unroll
@@ -760,7 +831,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
         f32x4 mm = weigh(acc, v, I, J, g, i);
         if constexpr (BWD) {
           float* rd = red + u * RED;
-          const f32x4 dd = score_tile<T, 64>(sv + u * VT::BYTES, sv2 + u * VT::BYTES, vrow, I, J);
+          const f32x4 dd = score_tile<T, 64>(sv + u * VT::BYTES, sv2 + u * VT::BYTES, VT::row_off(g, i), I, J);
           const float bi = v[V_RH + 16 * I + i];
           float cs = 0.f, rs[4];
 #pragma unroll
@@ -790,111 +861,109 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !(BWD && DK == 128) ? 2 : 1)
       fetch_gates(step + 2);
     }
     const float* v = vec + uw * V_SIZE;
-    f32x4 y[2][4];
-    inter<T, DK / 16, BWD ? 2 : 1, KT, 4>(y, S, sq, krow, 0);
+    f32x4 y[4];
+    inter<T, DK / 16, BWD ? 2 : 1, KT>(y, S, sq, krow);
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
       const float s = v[V_IN + 16 * I + i];
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[p][I][e] *= s;
+      for (int e = 0; e < 4; ++e) y[I][e] *= s;
     }
     sync_lds();
     if constexpr (BWD) {
-      // the state's part of c, z.v before the chunk's own part joins z, and dO.v;
-      // left where the score vectors were
+      // the state's part of c, z.v before the chunk's own part joins z, and dO.v, one
+      // sum per wave; left where the score vectors were
       float* w = vec + uw * V_SIZE;
+      static_assert(V_PB == 0 && V_KP == 192, "four score vectors");
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
-        const typename Op<T>::F x = VT::row(sv2 + uw * VT::BYTES, vrow, I, half);
-        const typename Op<T>::F gy = VT::row(sv + uw * VT::BYTES, vrow, I, half);
-        float s = 0.f, d = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s += y[0][I][e] * Op<T>::at(x, e) + y[1][I][e] * Op<T>::at(x, 4 + e);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d += Op<T>::at(gy, e) * Op<T>::at(x, e);
+        const f32x4 x = VT::quad(sv2 + uw * VT::BYTES, I, i, quarter, g);
+        float s = (y[I][0] * x[0] + y[I][1] * x[1]) + (y[I][2] * x[2] + y[I][3] * x[3]);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
-        d += __shfl_xor(d, 16);
-        d += __shfl_xor(d, 32);
-        if (g == 0) {
-          w[64 * half + 16 * I + i] = s;
-          w[128 + 64 * half + 16 * I + i] = d;
-        }
+        if (g == 0) w[64 * quarter + 16 * I + i] = s;
       }
     }
-    typename Op<T>::F vf[2][2];
+    typename Op<T>::F vf[2];
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int m = 0; m < 2; ++m) vf[m] = VT::vcol(sv + uw * VT::BYTES, VT::vcol_off(g, i), m, quarter);
+    intra<T>(y, vf, sm + uw * SC::BYTES, l);
+    char* const ob = reinterpret_cast<char*>(o + (long long)(BWD ? tok0 + n - CH : tok0) * a.os.t);
+    const long long od = (BWD ? -16 : 16) * a.os.t * (long long)sizeof(T);
+    const uint32_t oo = ((uint32_t)(BWD ? CH - 1 - i : i) * (uint32_t)a.os.t + 4u * g) * (uint32_t)sizeof(T);
+    if constexpr (BWD) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv + uw * VT::BYTES, VT::col_off(g, i) ^ (half * VT::GB), m, 0, p);
-    intra<T, 0, 4>(y, vf, sm + uw * SC::BYTES, l);
+      for (int I = 0; I < 4; ++I) {
+        const float bi = v[V_RH + 16 * I + i];
+        const f32x4 gy = VT::quad(sv + uw * VT::BYTES, I, i, quarter, g);
 #pragma unroll
-    for (int I = 0; I < 4; ++I) {
-      const int p = 16 * I + i;
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = y[0][I][e];
-        x[4 + e] = y[1][I][e];
+        for (int e = 0; e < 4; ++e) y[I][e] = bi * y[I][e] + skip_w * gy[e];
       }
-      if constexpr (BWD) {
-        const float bi = v[V_RH + p];
-        const typename Op<T>::F gy = VT::row(sv + uw * VT::BYTES, vrow, I, half);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = bi * x[e] + skip[uw] * Op<T>::at(gy, e);
-      }
-      if (p < n && mine) store8<T>(o + (long long)(BWD ? tok0 + n - 1 - p : tok0 + p) * a.os.t + 8 * g, x);
     }
+    store_rows<T>(y, ob, od, oo, mine ? n : 0, i);
     __builtin_amdgcn_sched_barrier(0);
     update<T, DK / 16, KT>(S, sk, vf, v + V_WS, v[V_GM], KT::col_off(g, i), g);
+    if constexpr (BWD) {
+      // dO.v of the unit's rows, 16 rows a wave
+      const int p = 16 * quarter + i;
+      float d = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 x = VT::quad(sv2 + uw * VT::BYTES, quarter, i, q, g), gy = VT::quad(sv + uw * VT::BYTES, quarter, i, q, g);
+        d += (x[0] * gy[0] + x[1] * gy[1]) + (x[2] * gy[2] + x[3] * gy[3]);
+      }
+      d += __shfl_xor(d, 16);
+      d += __shfl_xor(d, 32);
+      if (g == 0 && p < n && mine)
+        a.d[((size_t)it.b * a.H * cpu + (size_t)hw * cpu + (cw >> 6)) * a.T + tok0 + n - 1 - p] = d;
+    }
     sync_lds();
     if constexpr (BWD) {
       // one wave writes a unit's sums, the one that fills that unit's vectors
-      if (filler && 2 * it.sub + wave - 2 < nu && l < n) {
-        const float* rd = red + (wave - 2) * RED;
-        const float* w = vec + (wave - 2) * V_SIZE;
-        float cs = w[l] + w[64 + l], rs = 0.f;
+      if (filler && 2 * it.sub + wave - 6 < nu && l < n) {
+        const float* rd = red + (wave - 6) * RED;
+        const float* w = vec + (wave - 6) * V_SIZE;
+        float cs = (w[l] + w[64 + l]) + (w[128 + l] + w[192 + l]), rs = 0.f;
         for (int J = 0; J <= (l >> 4); ++J) cs += rd[64 * J + l];
         for (int I = l >> 4; I < 4; ++I) rs += rd[256 + 64 * I + l];
-        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)hv * cpu + (2 * it.sub + wave - 2) % cpu) * a.T + tok0 + n - 1 - l;
+        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)hv * cpu + (2 * it.sub + wave - 6) % cpu) * a.T + tok0 + n - 1 - l;
         a.c[at] = cs;
         a.r[at] = rs;
-        a.d[at] = w[128 + l] + w[192 + l];
       }
     }
   }
   if (it.seg == a.nseg - 1 && a.end && mine) {
     // reversed: the state before the first token owes its own decay too
     float s = 1.f;
-    if (BWD) s = ex2(fmaxf(to_f32((static_cast<const T*>(a.la) + it.b * a.ls.b + head[uw] * a.ls.h)[0]) * kLog2e, -180.f));
-    store_state(S, a.end + bh * a.dk * a.dv, a.dv, colu[uw] + half * 32, l >> 4, l & 15, s);
+    if (BWD) s = ex2(fmaxf(to_f32((static_cast<const T*>(a.la) + it.b * a.ls.b + hw * a.ls.h)[0]) * kLog2e, -180.f));
+    store_state(S, a.end + bh * a.dk * a.dv, a.dv, cw, l >> 4, l & 15, s);
   }
 }
 
 // ---------------------------------------------------------- summed over heads
 // dq (REV = false) and dk (REV): V is the group's shared row (k or q, DK
 // columns), Q and K are the heads' rows (dO and v, DV).  Workgroup = HG heads of
-// one group, wave = 32 of the DK columns for all of them, so that the sum over
+// one group, wave = 16 of the DK columns for all of them, so that the sum over
 // the heads stays in its accumulators; groups with more heads leave one partial
 // result per workgroup.  The forward pass also leaves, per head and token,
 // rs[i] = q_i . (the state's part of dq_i).
 template <typename T, int DV, int DK, bool REV>
-__global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) void kda_ssm_group_kernel(
+__global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? (DK == 128 && REV && DV == 128 ? 4 : 2) : DK / 64) void kda_ssm_group_kernel(
     PassArgs a, const void* qin, Str3 qrs, float* rs, float* parts) {
-  constexpr int HG = 128 / DV, NW = DK / 32, NT = 64 * NW;
+  constexpr int HG = 128 / DV, NW = DK / 16, NT = 64 * NW;
   typedef Tile<T, DV> QT;
   typedef Tile<T, DK> VT;
   typedef Scores<T> SC;
   constexpr int OQ = VT::BYTES, OK = OQ + HG * QT::BYTES, OM = OK + HG * QT::BYTES;
-  constexpr int OVEC = OM + HG * SC::BYTES;
-  __shared__ __attribute__((aligned(16))) char smem[OVEC + 2 * HG * V_SIZE * 4];  // two buffers of decay vectors
+  constexpr int OVEC = OM + HG * SC::BYTES, ORS = OVEC + 2 * HG * V_SIZE * 4;
+  // rs: one sum per wave, head and token; four waves' where the score vectors were, four more
+  __shared__ __attribute__((aligned(16))) char smem[ORS + (!REV && NW > 4 ? HG * 256 * 4 : 0)];
   char* const sv = smem;
   char* const sq = smem + OQ;
   char* const sk = smem + OK;
   char* const sm = smem + OM;
   float* const vecs = reinterpret_cast<float*>(smem + OVEC);
+  float* const rsx = reinterpret_cast<float*>(smem + ORS);
   const int R = a.H / a.G, np = (R + HG - 1) / HG;
   const Item it = item_of(a.B, a.G, a.nseg, np);
   if (!it.valid) return;
@@ -908,7 +977,6 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
   int head[HG];
   const T *Q[HG], *K[HG];
   State<DV / 16> S[HG];
-  const int i0 = l & 15, g0 = l >> 4;
 #pragma unroll
   for (int h = 0; h < HG; ++h) {
     head[h] = it.g * R + it.sub * HG + min(h, nh - 1);
@@ -920,12 +988,12 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
       const float* p = a.start + ((size_t)it.seg * a.B * a.H + (size_t)it.b * a.H + head[h]) * DK * DV;
 #pragma unroll
       for (int t = 0; t < DV / 16; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          S[h].t[t][c] = *reinterpret_cast<const f32x4*>(p + (size_t)(32 * wave + pair_chan(c, i0)) * DV + pair_chan(t, 4 * g0));
+        S[h].t[t] = *reinterpret_cast<const f32x4*>(p + (size_t)(16 * wave + (l & 15)) * DV + pair_chan(t, 4 * (l >> 4)));
     }
   }
-  const int hv = head[HG == 2 ? (wave & 1) : 0];  // of the waves that fill the decay vectors, the last HG
+  const bool filler = wave >= NW - HG;  // the last HG waves fill the heads' decay vectors
+  const int fh = wave - (NW - HG);
+  const int hv = HG == 2 && (wave & 1) ? head[HG - 1] : head[0];
   const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
 #pragma unroll
@@ -933,30 +1001,31 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
 
   Fetch<T, DK, NT> fv;
   Fetch<T, DV, NT> fq[HG], fk[HG];
-  float fx = 0.f, fb = 0.f;
+  const uint32_t ofv = fv.template lane_off<REV>(a.vs.t, tid), ofq = fq[0].template lane_off<REV>(a.qs.t, tid),
+                 ofk = fk[0].template lane_off<REV>(a.ks.t, tid);
+  T fx = T(0.f), fb = T(0.f);
   auto fetch = [&](int step) {
     const int c = REV ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, a.T - tok0);
-    fv.template get<REV>(V, a.vs.t, tok0, n, tid);
+    fv.template get<REV>(V, a.vs.t, tok0, n, ofv, tid);
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
-      fq[h].template get<REV>(Q[h], a.qs.t, tok0, n, tid);
-      fk[h].template get<REV>(K[h], a.ks.t, tok0, n, tid);
+      fq[h].template get<REV>(Q[h], a.qs.t, tok0, n, ofq, tid);
+      fk[h].template get<REV>(K[h], a.ks.t, tok0, n, ofk, tid);
     }
   };
-  const bool filler = wave >= NW - HG;
-  const int fh = wave - (NW - HG);
   auto fetch_gates = [&](int step) {
     if (!filler || step >= c1 - c0) return;
     const int c = REV ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, a.T - tok0);
     fx = decay_at<T, REV>(la, a.ls.t, tok0, n, a.T, l);
     // a head past the group's last one gets no weight
-    fb = l < n && fh < nh ? to_f32(beta[(long long)(REV ? tok0 + n - 1 - l : tok0 + l) * a.bs.t]) : 0.f;
+    fb = weight_at<T, REV>(beta, a.bs.t, tok0, n, l, fh < nh);
   };
   auto fill = [&](int step) {
     if (filler && step < c1 - c0)
-      fill_vec(vecs + ((step & 1) * HG + fh) * V_SIZE, l, fx, REV ? 1.f : fb, REV ? fb : 1.f, fb);
+      fill_vec(vecs + ((step & 1) * HG + fh) * V_SIZE, l, to_f32(fx), REV ? 1.f : to_f32(fb), REV ? to_f32(fb) : 1.f,
+               to_f32(fb));
   };
   fetch_gates(0);
   if (c0 < c1) fetch(0);
@@ -973,18 +1042,15 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
       fk[h].put(sk + h * QT::BYTES, tid);
     }
     // the wave's columns of the q rows, for rs: straight from memory, in the layout of its results
-    typename Op<T>::F xq[4];
+    typedef typename std::conditional<sizeof(T) == 2, bf16x4, f32x4>::type X4;
+    X4 xq[4];
+    const uint32_t oxq = ((uint32_t)(l & 15) * (uint32_t)qrs.t + 4u * (l >> 4)) * (uint32_t)sizeof(T);
     if constexpr (!REV) {
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
         const int p = 16 * I + (l & 15);
-        u32x4 w[sizeof(T) / 2] = {};
-        if (p < n) {
-          const u32x4* src = reinterpret_cast<const u32x4*>(W + (long long)(tok0 + p) * qrs.t + 32 * wave + 8 * (l >> 4));
-#pragma unroll
-          for (int b = 0; b < (int)sizeof(T) / 2; ++b) w[b] = src[b];
-        }
-        __builtin_memcpy(&xq[I], w, sizeof(w));
+        xq[I] = X4{};
+        if (p < n) xq[I] = *reinterpret_cast<const X4*>(reinterpret_cast<const char*>(W + (tok0 + 16 * I) * qrs.t + 16 * wave) + oxq);
       }
     }
     if (step + 1 < c1 - c0) fetch(step + 1);
@@ -992,7 +1058,7 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
 
     const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
     const uint32_t qrow = QT::row_off(g, i);
-    for (int t = wave; t < 10; t += NW) {
+    for (int t = wave; t < 10; t += NW == 8 && wave < 4 ? 16 : 4) {
       const int I = tile_i(t), J = tile_j(t);
 #pragma unroll
       for (int h = 0; h < HG; ++h) {
@@ -1011,85 +1077,66 @@ __global__ __launch_bounds__(2 * DK, sizeof(T) == 2 ? (DK == 128 ? 2 : 1) : 1) v
     fetch_gates(step + 2);
     sync_lds();
 
-    typename Op<T>::F vf[2][2];
+    typename Op<T>::F vf[2];
+    f32x4 y[4];
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) vf[p][m] = VT::col(sv, VT::col_off(g, i) ^ (wave * VT::GB), m, 0, p);
-    // two halves of the tokens in turn, so that a half's sum over the heads and one
-    // head's part of it fit beside the states
-    auto half = [&](auto H2) {
-      constexpr int I0 = 2 * decltype(H2)::value;
-      f32x4 y[2][2];
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int I = 0; I < 2; ++I) y[p][I] = zero4();
-#pragma unroll
-      for (int h = 0; h < HG; ++h) {
-        float* v = vec + h * V_SIZE;
-        f32x4 z[2][2];
-        inter<T, DV / 16, REV ? 1 : 2, QT, 2>(z, S[h], sq + h * QT::BYTES, qrow, I0);
-#pragma unroll
-        for (int I = 0; I < 2; ++I) {
-          const float s = h < nh ? v[V_IN + 16 * (I0 + I) + i] : 0.f;
-          if constexpr (!REV) {
-            const typename Op<T>::F x = xq[I0 + I];
-            float dot = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dot += z[0][I][e] * Op<T>::at(x, e) + z[1][I][e] * Op<T>::at(x, 4 + e);
-            dot *= s;
-            dot += __shfl_xor(dot, 16);
-            dot += __shfl_xor(dot, 32);
-            // (the score vectors are no longer needed)
-            if (g == 0) v[64 * wave + 16 * (I0 + I) + i] = dot;
-          }
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[p][I][e] += s * z[p][I][e];
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        intra<T, I0, 2>(y, vf, sm + h * SC::BYTES, l);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int I = 0; I < 2; ++I) {
-        const int p = 16 * (I0 + I) + i;
-        const int tok = REV ? tok0 + n - 1 - p : tok0 + p;
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = y[0][I][e];
-          x[4 + e] = y[1][I][e];
-        }
-        if (p < n) {
-          if (np == 1)
-            store8<T>(static_cast<T*>(a.o) + it.b * a.os.b + it.g * a.os.h + (long long)tok * a.os.t + 32 * wave + 8 * g, x);
-          else
-            store8<float>(parts + (((size_t)it.sub * a.B * a.G + (size_t)it.b * a.G + it.g) * a.T + tok) * DK + 32 * wave + 8 * g, x);
-        }
-      }
-    };
-    half(std::integral_constant<int, 0>());
-#pragma unroll
-    for (int h = 0; h < HG; ++h) S[h].renew();
-    half(std::integral_constant<int, 1>());
+    for (int I = 0; I < 4; ++I) y[I] = zero4();
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
+      float* v = vec + h * V_SIZE;
+      f32x4 z[4];
+      inter<T, DV / 16, REV ? 1 : 2, QT>(z, S[h], sq + h * QT::BYTES, qrow);
+#pragma unroll
+      for (int I = 0; I < 4; ++I) {
+        const float s = h < nh ? v[V_IN + 16 * I + i] : 0.f;
+        if constexpr (!REV) {
+          float dot = (z[I][0] * (float)xq[I][0] + z[I][1] * (float)xq[I][1]) + (z[I][2] * (float)xq[I][2] + z[I][3] * (float)xq[I][3]);
+          dot *= s;
+          dot += __shfl_xor(dot, 16);
+          dot += __shfl_xor(dot, 32);
+          // (the score vectors are no longer needed)
+          if (g == 0) (wave < 4 ? v + 64 * wave : rsx + 256 * h + 64 * (wave - 4))[16 * I + i] = dot;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[I][e] += s * z[I][e];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (h == 0) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) vf[m] = VT::vcol(sv, VT::vcol_off(g, i), m, wave);
+      }
+      intra<T>(y, vf, sm + h * SC::BYTES, l);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const long long rows = REV ? tok0 + n - CH : tok0;  // as in Fetch
+    const int ri = REV ? CH - 1 - i : i;
+    if (np == 1) {
+      char* const ob = reinterpret_cast<char*>(static_cast<T*>(a.o) + it.b * a.os.b + it.g * a.os.h + rows * a.os.t + 16 * wave);
+      const long long od = (REV ? -16 : 16) * a.os.t * (long long)sizeof(T);
+      const uint32_t oo = ((uint32_t)ri * (uint32_t)a.os.t + 4u * g) * (uint32_t)sizeof(T);
+      store_rows<T>(y, ob, od, oo, n, i);
+    } else {
+      char* const ob = reinterpret_cast<char*>(parts + (((long long)it.sub * a.B * a.G + (long long)it.b * a.G + it.g) * a.T + rows) * DK + 16 * wave);
+      const uint32_t oo = (uint32_t)(ri * DK + 4 * g) * 4u;
+      store_rows<float>(y, ob, (REV ? -16 : 16) * DK * 4, oo, n, i);
+    }
+    // after the stores, when the results' registers are free
+#pragma unroll
+    for (int h = 0; h < HG; ++h) {
+      __builtin_amdgcn_sched_barrier(0);
       const float* v = vec + h * V_SIZE;
       update<T, DV / 16, QT>(S[h], sk + h * QT::BYTES, vf, v + V_WS, v[V_GM], QT::col_off(g, i), g);
-      __builtin_amdgcn_sched_barrier(0);
     }
     sync_lds();
     if constexpr (!REV) {
       if (wave < nh && l < n) {
         const float* v = vec + wave * V_SIZE;
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) s += v[64 * w + l];
-        const int hh = it.g * R + it.sub * HG + wave;
-        rs[((size_t)it.b * a.H + hh) * a.T + tok0 + l] = s;
+        float s = (v[l] + v[64 + l]) + (v[128 + l] + v[192 + l]);
+        if (NW > 4) {
+          const float* x = rsx + 256 * wave;
+          s += (x[l] + x[64 + l]) + (x[128 + l] + x[192 + l]);
+        }
+        rs[((size_t)it.b * a.H + it.g * R + it.sub * HG + wave) * a.T + tok0 + l] = s;
       }
     }
   }
@@ -1266,8 +1313,8 @@ template <typename T, bool REV>
 hipError_t run_state(const PassArgs& a, hipStream_t s) {
   const int nu = a.H / a.G * (a.dv / 64);
   const dim3 grid(item_grid(a.B, a.G, a.norders, (nu + 1) / 2));
-  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_state_kernel<T, 128, REV>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((kda_ssm_state_kernel<T, 64, REV>), grid, dim3(256), 0, s, a);
+  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_state_kernel<T, 128, REV>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((kda_ssm_state_kernel<T, 64, REV>), grid, dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
@@ -1275,8 +1322,8 @@ template <typename T, bool BWD>
 hipError_t run_out(const PassArgs& a, hipStream_t s) {
   const int nu = a.H / a.G * (a.dv / 64);
   const dim3 grid(item_grid(a.B, a.G, a.nseg, (nu + 1) / 2));
-  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_out_kernel<T, 128, BWD>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((kda_ssm_out_kernel<T, 64, BWD>), grid, dim3(256), 0, s, a);
+  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_out_kernel<T, 128, BWD>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((kda_ssm_out_kernel<T, 64, BWD>), grid, dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
@@ -1285,7 +1332,7 @@ hipError_t run_group(const PassArgs& a, const void* qin, Str3 qrs, float* rs, fl
   const int hg = 128 / a.dv, np = (a.H / a.G + hg - 1) / hg;
   const dim3 grid(item_grid(a.B, a.G, a.nseg, np));
 #define KDA_GROUP(DV, DK)                                                                                            \
-  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK, REV>), grid, dim3(2 * DK), 0, s, a, qin, qrs, rs, parts)
+  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK, REV>), grid, dim3(4 * DK), 0, s, a, qin, qrs, rs, parts)
   if (a.dv == 64 && a.dk == 64) KDA_GROUP(64, 64);
   else if (a.dv == 64) KDA_GROUP(64, 128);
   else if (a.dk == 64) KDA_GROUP(128, 64);

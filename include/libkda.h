@@ -310,8 +310,9 @@ kda_status kda_prefill_backward(const void* q, const void* k, const void* v, con
  *    array whose rows of d elements are contiguous, so that a projection's
  *    token-major output [B, T, H * d] is read in place.  NULL means contiguous
  *    [B, H, T, d].  Rows must start on 16-byte boundaries: strides (of
- *    dimensions larger than 1) are multiples of 16 bytes and not negative;
- *    those of an output are not 0 and its rows do not overlap.
+ *    dimensions larger than 1) are multiples of 16 bytes and not negative, a
+ *    token's at most 2^23 elements; those of an output are not 0 and its rows
+ *    do not overlap.
  *  - `lens` (NULL: every sequence has T tokens) is a device array of B ints:
  *    sequence b has its first lens[b] tokens (clamped to [0, T]).  The padding
  *    behind them is neither read into the results nor written.
