@@ -26,15 +26,18 @@
 // transposed) and the state feed it from registers.  Rows of the state are taken in
 // the order 32c + 8(r / 4) + 4(odd) + r % 4 for row r of an (even, odd) pair of
 // tiles, which makes a lane's share of a pair eight consecutive channels, so that
-// the rows it is multiplied with are read in their natural order.  A wave owns 16
-// columns of a state (32 registers a lane for 128 rows): with half as many waves of
-// 32 columns the products of one rarely ran beside the vector work of another.
+// the rows it is multiplied with are read in their natural order.  A wave owns NC
+// column tiles of a state: two with bf16 (64 registers a lane for 128 rows, two waves
+// a SIMD; the columns taken in the same paired order, so that results are stored 16
+// bytes a lane), one with fp32, whose tiles fill the LDS and whose products are long.
+// bf16 with one column tile and twice the waves took as long (580 us against 561 for
+// the outputs of 64K tokens, 64 heads of 128 x 64) for more vector work in all.
 //
 // Precision.  bf16 inputs are exact operands.  The scores and the state are
 // rounded once to bf16 where they multiply V and Q (both times one rounding in
 // front of an fp32 sum, like the output's own); the weighted V that updates the
-// fp32 state is carried in three bf16 terms (24 bits), as the state is an fp32
-// result.  The gradient of log_alpha is a difference of two sums that nearly
+// fp32 state is carried in three bf16 terms (24 bits) where the state is a result,
+// in two (16 bits) where it only multiplies Q afterwards, rounded to fewer.  The gradient of log_alpha is a difference of two sums that nearly
 // cancel, so the score sums it needs are taken from fp32 scores and the state
 // terms from a two-term (16-bit) state.  fp32 inputs run the same kernels on the
 // fp32 matrix instructions.
@@ -51,6 +54,9 @@ constexpr int CH = kSsmChunk;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // --------------------------------------------------------------- operands
+// column tiles of 16 a wave owns
+template <typename T> constexpr int kNC = sizeof(T) == 2 ? 2 : 1;
+
 template <typename T> struct Op;
 template <> struct Op<bf16> {
   typedef bf16x8 F;
@@ -129,8 +135,7 @@ struct Tile {
     else return Op<T>::round(lds_ld<f32x4>(p, off ^ (m * GB)), lds_ld<f32x4>(p, off ^ (m * GB) ^ 16));
   }
   // Contraction over tokens: lane (g, i) gets tokens 32m + 4g + e and 32m + 16 +
-  // 4g + e of channel 32c + 8(i / 4) + 4 odd + i % 4 (col, row tiles of a state) or
-  // 16 c + i (vcol, column tiles).  bf16: the transposing read
+  // 4g + e of channel 32c + 8(i / 4) + 4 odd + i % 4 (col) or i (vcol).  bf16: the transposing read
   // takes lane i's 8 bytes as row i of a 16 x 4 matrix and returns element
   // [4e + i / 4][i % 4] as lane i's e-th.
   static __device__ __forceinline__ uint32_t col_off(int g, int i) {
@@ -166,9 +171,8 @@ struct Tile {
       return 4 * g * R + (((i >> 2) ^ f(4 * g)) << 4) + 4 * (i & 3);
     }
   }
-  static __device__ __forceinline__ typename Op<T>::F vcol(const char* s, uint32_t off, int m, int c) {
+  static __device__ __forceinline__ typename Op<T>::F vcol(const char* s, uint32_t off, int m) {
     const char* p = s + 32 * m * R;
-    off ^= c * (GB / 2);
     if constexpr (sizeof(T) == 2) {
       const bf16x4 lo = lds_tr16(p, off), hi = lds_tr16(p + 16 * R, off);
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -183,15 +187,32 @@ struct Tile {
       return x;
     }
   }
-  // channels 16c + 4g .. + 3 of row 16 I + i, as floats (a lane's place in a result)
-  static __device__ __forceinline__ f32x4 quad(const char* s, int I, int i, int c, int g) {
-    const uint32_t o = at(16 * I + i, (16 * c + 4 * g) * (int)sizeof(T));
-    if constexpr (sizeof(T) == 2) {
-      const bf16x4 x = lds_ld<bf16x4>(s, o);
-      return f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
-    } else {
-      return lds_ld<f32x4>(s, o);
+  // a lane's place in a result, row 16 I + i: 4 NC channels from 16 NC w + 4 NC g on
+  template <int NC>
+  static __device__ __forceinline__ void place(const char* s, int I, int i, int w, int g, float (&x)[4 * NC]) {
+#pragma unroll
+    for (int b = 0; b < NC * (int)sizeof(T) / 4; ++b) {  // 16 bytes (or one 8-byte read)
+      if constexpr (sizeof(T) == 2) {
+        if constexpr (NC == 2) {
+          const bf16x8 v = lds_ld<bf16x8>(s, at(16 * I + i, (32 * w + 8 * g) * 2));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = (float)v[e];
+        }
+      } else {
+        const f32x4 v = lds_ld<f32x4>(s, at(16 * I + i, (16 * NC * w + 4 * NC * g + 4 * b) * 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * b + e] = v[e];
+      }
     }
+  }
+  // V's column tile of a wave as an operand, half m of the tokens, tile p of NC
+  template <int NC>
+  static __device__ __forceinline__ uint32_t vtile_off(int g, int i, int w) {
+    return NC == 2 ? col_off(g, i) ^ (w * GB) : vcol_off(g, i) ^ (w * (GB / 2));
+  }
+  template <int NC>
+  static __device__ __forceinline__ typename Op<T>::F vtile(const char* s, uint32_t off, int m, int p) {
+    return NC == 2 ? col(s, off, m, 0, p) : vcol(s, off, m);
   }
 };
 
@@ -239,15 +260,18 @@ struct Fetch {
 
 // ---------------------------------------------------------------- decays
 // Per head of the chunk, floats.  PB: sums from the block's start; U: u rho; W: w
-// kappa; KP: kappa; RH: rho (or, in the reversed outputs, beta); IN: rho e^{l_i};
-// WS: kappa e^{l_end - l_j}; ET: E of the four blocks; GM: e^{l_end}.  The first
-// four are read only while the scores are formed.
-enum { V_PB = 0, V_U = 64, V_W = 128, V_KP = 192, V_RH = 256, V_IN = 320, V_WS = 384, V_ET = 448, V_GM = 452, V_SIZE = 456 };
+// kappa; RH: rho (or, in the reversed outputs, beta); IN: rho e^{l_i}; WS: kappa
+// e^{l_end - l_j}; ET: E of the four blocks; GM: e^{l_end}; KP: kappa, where it is not
+// one.  PB, U, W and KP are read only while the scores are formed.
+enum { V_PB = 0, V_U = 64, V_W = 128, V_RH = 192, V_IN = 256, V_WS = 320, V_ET = 384, V_GM = 388, V_KP = 392, V_SIZE = 456 };
+constexpr int kVecNoKappa = V_KP;  // floats of a head's vectors without KP
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// One wave fills a head's vectors; lane r is position r with decay x.
-__device__ __forceinline__ void fill_vec(float* v, int r, float x, float kappa, float rho, float rh) {
+// One wave fills a head's vectors; lane r is position r with decay x.  WS is also
+// multiplied by run.  Returns e^{l_end}.
+template <bool KAPPA>
+__device__ __forceinline__ float fill_vec(float* v, int r, float x, float kappa, float rho, float rh, float run = 1.f) {
   x *= kLog2e;
   x = x < -180.f ? -180.f : x;  // (a NaN passes)
   float pre = x;
@@ -270,12 +294,14 @@ __device__ __forceinline__ void fill_vec(float* v, int r, float x, float kappa, 
   v[V_PB + r] = pre;
   v[V_U + r] = u * rho;
   v[V_W + r] = w * kappa;
-  v[V_KP + r] = kappa;
+  if (KAPPA) v[V_KP + r] = kappa;
   v[V_RH + r] = rh;
   v[V_IN + r] = u * before * rho;
-  v[V_WS + r] = w * after * kappa;
+  v[V_WS + r] = w * after * kappa * run;
   if ((r & 15) == 0) v[V_ET + blk] = et;
-  if (r == 0) v[V_GM] = e0 * e1 * e2 * e3;
+  const float gm = e0 * e1 * e2 * e3;
+  if (r == 0) v[V_GM] = gm;
+  return gm;
 }
 
 // The gate of position p as it is stored: the token's own, or reversed the next
@@ -300,43 +326,56 @@ __device__ __forceinline__ T weight_at(const T* beta, long long st, int tok0, in
 }
 
 // ---------------------------------------------------------------- scores
-// Transposed score tiles, bf16 or fp32, as the operand of the product with V:
-// slot (I, J / 2) holds, lane by lane, tiles (I, 2m) and (I, 2m + 1).
+// Transposed score tiles (I, J <= I), bf16 or fp32, lane by lane, as half of an
+// operand of the product with V.
 template <typename T>
 struct Scores {
-  static constexpr int LANE = 8 * (int)sizeof(T);  // bytes of a lane in a slot
-  static constexpr int SLOT = 64 * LANE;
-  static constexpr int BYTES = 6 * SLOT;
-  static __device__ __forceinline__ int slot(int I, int m) { return I + (I == 3) + m; }
+  static constexpr int LANE = 4 * (int)sizeof(T);  // bytes of a lane in a tile
+  static constexpr int TILE = 64 * LANE;
+  static constexpr int BYTES = 10 * TILE;
+  typedef typename std::conditional<sizeof(T) == 2, bf16x4, f32x4>::type H;
+  static __device__ __forceinline__ int tile(int I, int J) { return I * (I + 1) / 2 + J; }
   static __device__ __forceinline__ void put(char* s, int I, int J, int l, f32x4 v) {
-    char* p = s + slot(I, J >> 1) * SLOT + l * LANE + (J & 1) * 4 * (int)sizeof(T);
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4*>(p) = pack4(v);
-    else *reinterpret_cast<f32x4*>(p) = v;
+    H h;
+    if constexpr (sizeof(T) == 2) h = pack4(v);
+    else h = v;
+    *reinterpret_cast<H*>(s + tile(I, J) * TILE + l * LANE) = h;
   }
+  // tiles (I, 2m) and (I, 2m + 1), the latter zero above the diagonal
   static __device__ __forceinline__ typename Op<T>::F get(const char* s, int I, int m, int l) {
-    const char* p = s + slot(I, m) * SLOT + l * LANE;
-    if constexpr (sizeof(T) == 2) return *reinterpret_cast<const bf16x8*>(p);
-    else return Op<T>::round(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16));
-  }
-  // the upper halves of the diagonal slots are never written again
-  static __device__ __forceinline__ void clear(char* s, int tid, int nt) {
-    for (int i = tid * 16; i < BYTES; i += nt * 16) *reinterpret_cast<u32x4*>(s + i) = u32x4{0u, 0u, 0u, 0u};
+    const char* p = s + tile(I, 2 * m) * TILE + l * LANE;
+    const H a = *reinterpret_cast<const H*>(p);
+    H b = {};
+    if (2 * m < I) b = *reinterpret_cast<const H*>(p + TILE);
+    if constexpr (sizeof(T) == 2) return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    else return Op<T>::round(a, b);
   }
 };
+
+// sum over a row of 16 lanes, in every lane of it
+__device__ __forceinline__ float row16_sum(float x) {
+  x += dpp<DPP_QUAD_SWAP1>(x);
+  x += dpp<DPP_QUAD_SWAP2>(x);
+  x += dpp<0x124>(x);  // rotations by 4 and 8 within the row
+  x += dpp<DPP_ROW_ROR8>(x);
+  return x;
+}
 
 // tile t of the ten (I, J <= I), diagonal first
 __device__ __forceinline__ int tile_i(int t) { return (int)((0x0fe9e4u >> (2 * t)) & 3u); }  // 0 1 2 3 1 2 2 3 3 3
 __device__ __forceinline__ int tile_j(int t) { return (int)((0x0910e4u >> (2 * t)) & 3u); }  // 0 1 2 3 0 0 1 0 1 2
 
 // decayed, weighted scores of a transposed tile: rows j = 16J + 4g + e, column i = 16I + r16
+template <bool KAPPA>
 __device__ __forceinline__ f32x4 weigh(f32x4 acc, const float* v, int I, int J, int g, int r16) {
   f32x4 m;
   if (I == J) {
     const float pi = v[V_PB + 16 * I + r16];
     const f32x4 pj = *reinterpret_cast<const f32x4*>(v + V_PB + 16 * J + 4 * g);
-    const f32x4 kp = *reinterpret_cast<const f32x4*>(v + V_KP + 16 * J + 4 * g);
+    f32x4 kp = {1.f, 1.f, 1.f, 1.f};
+    if (KAPPA) kp = *reinterpret_cast<const f32x4*>(v + V_KP + 16 * J + 4 * g);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = 4 * g + e <= r16 ? acc[e] * (ex2(pi - pj[e]) * kp[e]) : 0.f;
+    for (int e = 0; e < 4; ++e) m[e] = 4 * g + e <= r16 ? acc[e] * (KAPPA ? ex2(pi - pj[e]) * kp[e] : ex2(pi - pj[e])) : 0.f;
   } else {
     float c = v[V_U + 16 * I + r16];
     for (int b = J + 1; b < I; ++b) c *= v[V_ET + b];
@@ -348,142 +387,190 @@ __device__ __forceinline__ f32x4 weigh(f32x4 acc, const float* v, int I, int J, 
 }
 
 // -------------------------------------------------------- state and results
-// A wave's state: NK = rows / 16 tiles of 16 columns.
-template <int NK>
+// A wave's state: NK = rows / 16 by NC column tiles.
+template <int NK, int NC>
 struct State {
-  f32x4 t[NK];
+  f32x4 t[NK][NC];
   __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int a = 0; a < NK; ++a) t[a] = zero4();
-  }
-};
-__device__ __forceinline__ int pair_chan(int tile, int r) { return 32 * (tile >> 1) + 8 * (r >> 2) + 4 * (tile & 1) + (r & 3); }
-
-// One word (two elements) of the three bf16 terms of w V.
-__device__ __forceinline__ void split_word(uint32_t x, float wa, float wb, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
-  float a = __uint_as_float(x << 16) * wa, b = __uint_as_float(x & 0xffff0000u) * wb;
-  t0 = cvt2(a, b);
-  a -= __uint_as_float(t0 << 16);  // exact, as is the next
-  b -= __uint_as_float(t0 & 0xffff0000u);
-  t1 = cvt2(a, b);
-  a -= __uint_as_float(t1 << 16);
-  b -= __uint_as_float(t1 & 0xffff0000u);
-  t2 = cvt2(a, b);
-}
-
-// S <- gm S + K^T (w V): w the per-token weights, V the wave's column tile (two
-// 32-token halves).  bf16: row tiles in pairs, so that the three products into one
-// accumulator have others between them; the state's scaling and the second half's
-// terms are dealt over the first half's products, whose time on the matrix cores
-// they fit into.
-template <typename T, int NK, typename KT>
-__device__ __forceinline__ void update(State<NK>& S, const char* ktile, const typename Op<T>::F (&vf)[2], const float* ws,
-                                       float gm, uint32_t kcol, int g) {
-  if constexpr (sizeof(T) == 2) {
-    u32x4 x[2], t[2][3];  // [m], [m][term]
-#pragma unroll
-    for (int m = 0; m < 2; ++m) x[m] = __builtin_bit_cast(u32x4, vf[m]);
-    auto word = [&](int m, int q) {
-      const f32x2 w = *reinterpret_cast<const f32x2*>(ws + 32 * m + 16 * (q >> 1) + 4 * g + 2 * (q & 1));
-      uint32_t a, b, c;
-      split_word(x[m][q], w[0], w[1], a, b, c);
-      t[m][0][q] = a;
-      t[m][1][q] = b;
-      t[m][2][q] = c;
-    };
-#pragma unroll
-    for (int q = 0; q < 4; ++q) word(0, q);
-    bf16x8 k0 = KT::col(ktile, kcol, 0, 0, 0), k1 = KT::col(ktile, kcol, 0, 0, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    constexpr int NP = NK / 2;      // pairs of row tiles
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int a = 0; a < NP; ++a) {
-        const bf16x8 c0 = k0, c1 = k1;
-        const int an = a + 1 < NP ? a + 1 : 0, mn = a + 1 < NP ? m : 1;
-        if (m == 0 || a + 1 < NP) {
-          k0 = KT::col(ktile, kcol, mn, an, 0);
-          k1 = KT::col(ktile, kcol, mn, an, 1);
-        }
-        if (m == 0) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            S.t[2 * a][e] *= gm;
-            S.t[2 * a + 1][e] *= gm;
-          }
-#pragma unroll
-          for (int q = a * 4 / NP; q < (a + 1) * 4 / NP; ++q) word(1, q);
-        }
-#pragma unroll
-        for (int n = 2; n >= 0; --n) {
-          S.t[2 * a] = mfma_bf16_k32(S.t[2 * a], c0, __builtin_bit_cast(bf16x8, t[m][n]));
-          S.t[2 * a + 1] = mfma_bf16_k32(S.t[2 * a + 1], c1, __builtin_bit_cast(bf16x8, t[m][n]));
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-  } else {
 #pragma unroll
     for (int a = 0; a < NK; ++a)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S.t[a][e] *= gm;
+      for (int p = 0; p < NC; ++p) t[a][p] = zero4();
+  }
+  // Makes the compiler take the values as new, so that operands formed from them
+  // before are formed again rather than kept in registers.
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int a = 0; a < NK; ++a)
+#pragma unroll
+      for (int p = 0; p < NC; ++p) asm volatile("" : "+v"(t[a][p]));
+  }
+};
+__device__ __forceinline__ int pair_chan(int tile, int r) { return 32 * (tile >> 1) + 8 * (r >> 2) + 4 * (tile & 1) + (r & 3); }
+// column of lane i's column tile p, from the wave's first
+template <int NC>
+__device__ __forceinline__ int col_chan(int p, int i) { return NC == 2 ? pair_chan(p, i) : i; }
+
+// One word (two elements) of the TERMS bf16 terms of w V.
+template <int TERMS>
+__device__ __forceinline__ void split_word(uint32_t x, float wa, float wb, uint32_t (&t)[TERMS]) {
+  float a = __uint_as_float(x << 16) * wa, b = __uint_as_float(x & 0xffff0000u) * wb;
+#pragma unroll
+  for (int n = 0; n < TERMS; ++n) {
+    if (n > 0) {  // (exact)
+      a -= __uint_as_float(t[n - 1] << 16);
+      b -= __uint_as_float(t[n - 1] & 0xffff0000u);
+    }
+    t[n] = cvt2(a, b);
+  }
+}
+
+// S <- gm S + K^T (w V) (without SCALE: S + ..): w the per-token weights, V the wave's
+// column tiles (two 32-token halves each).  bf16: 2 TERMS products a step; the
+// state's scaling and the second half's terms are dealt over the first half's
+// products, whose time on the matrix cores they fit into.
+template <typename T, int NK, int NC, int TERMS, bool SCALE, typename KT>
+__device__ __forceinline__ void update(State<NK, NC>& S, const char* ktile, const typename Op<T>::F (&vf)[NC][2], const float* ws,
+                                       float gm, uint32_t kcol, int g) {
+  if constexpr (sizeof(T) == 2) {
+    constexpr int AP = 2 / NC, NS = NK / AP, NW = 4 * NC;  // row tiles a step, steps, words a half
+    u32x4 t[2][NC][TERMS];                                 // [half][column tile][term]
+    auto word = [&](int m, int n) {
+      const int p = n % NC, q = n / NC;
+      const f32x2 w = *reinterpret_cast<const f32x2*>(ws + 32 * m + 16 * (q >> 1) + 4 * g + 2 * (q & 1));
+      uint32_t r[TERMS];
+      split_word<TERMS>(__builtin_bit_cast(u32x4, vf[p][m])[q], w[0], w[1], r);
+#pragma unroll
+      for (int x = 0; x < TERMS; ++x) t[m][p][x][q] = r[x];
+    };
+#pragma unroll
+    for (int n = 0; n < NW; ++n) word(0, n);
+    bf16x8 kn[AP];
+#pragma unroll
+    for (int b = 0; b < AP; ++b) kn[b] = KT::col(ktile, kcol, 0, b >> 1, b & 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int st = 0; st < NS; ++st) {
+        bf16x8 kc[AP];
+        const int sn = st + 1 < NS ? st + 1 : 0, mn = st + 1 < NS ? m : 1;
+#pragma unroll
+        for (int b = 0; b < AP; ++b) {
+          kc[b] = kn[b];
+          const int a = sn * AP + b;
+          if (m == 0 || st + 1 < NS) kn[b] = KT::col(ktile, kcol, mn, a >> 1, a & 1);
+        }
+        if (m == 0) {
+          if (SCALE) {
+#pragma unroll
+            for (int b = 0; b < AP; ++b)
+#pragma unroll
+              for (int p = 0; p < NC; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S.t[st * AP + b][p][e] *= gm;
+          }
+#pragma unroll
+          for (int n = st * NW / NS; n < (st + 1) * NW / NS; ++n) word(1, n);
+        }
+#pragma unroll
+        for (int x = TERMS - 1; x >= 0; --x)
+#pragma unroll
+          for (int b = 0; b < AP; ++b)
+#pragma unroll
+            for (int p = 0; p < NC; ++p)
+              S.t[st * AP + b][p] = mfma_bf16_k32(S.t[st * AP + b][p], kc[b], __builtin_bit_cast(bf16x8, t[m][p][x]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  } else {
+    if (SCALE) {
+#pragma unroll
+      for (int a = 0; a < NK; ++a)
+#pragma unroll
+        for (int p = 0; p < NC; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S.t[a][p][e] *= gm;
+    }
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const f32x4 w0 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 4 * g);
       const f32x4 w1 = *reinterpret_cast<const f32x4*>(ws + 32 * m + 16 + 4 * g);
-      typename Op<T>::F y;
+      typename Op<T>::F y[NC];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y.v[e] = vf[m].v[e] * w0[e];
-        y.v[4 + e] = vf[m].v[4 + e] * w1[e];
+      for (int p = 0; p < NC; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[p].v[e] = vf[p][m].v[e] * w0[e];
+          y[p].v[4 + e] = vf[p][m].v[4 + e] * w1[e];
+        }
+#pragma unroll
+      for (int a = 0; a < NK; ++a) {
+        const typename Op<T>::F k = KT::col(ktile, kcol, m, a >> 1, a & 1);
+#pragma unroll
+        for (int p = 0; p < NC; ++p) S.t[a][p] = Op<T>::mma(S.t[a][p], k, y[p]);
       }
-#pragma unroll
-      for (int a = 0; a < NK; ++a) S.t[a] = Op<T>::mma(S.t[a], KT::col(ktile, kcol, m, a >> 1, a & 1), y);
     }
   }
 }
 
-// Y^T[I] = S^T Q^T (rows: the wave's columns, columns: tokens), NT terms of S
-template <typename T, int NK, int NT, typename QT>
-__device__ __forceinline__ void inter(f32x4 (&y)[4], const State<NK>& S, const char* qtile, uint32_t qrow) {
+// Y^T[p][I] = S^T Q^T (rows: the wave's columns, columns: tokens) for the NI row
+// tiles from I0 on, NT terms of S
+template <typename T, int NK, int NC, int NT, int NI, typename QT>
+__device__ __forceinline__ void inter(f32x4 (&y)[NC][NI], const State<NK, NC>& S, const char* qtile, uint32_t qrow, int I0) {
 #pragma unroll
-  for (int I = 0; I < 4; ++I) y[I] = zero4();
+  for (int p = 0; p < NC; ++p)
+#pragma unroll
+    for (int I = 0; I < NI; ++I) y[p][I] = zero4();
 #pragma unroll
   for (int m = 0; m < NK / 2; ++m) {
-    const Split<T, NT> s(S.t[2 * m], S.t[2 * m + 1]);
-    typename Op<T>::F qf[4];
+    typename Op<T>::F qf[NI];
 #pragma unroll
-    for (int I = 0; I < 4; ++I) qf[I] = QT::row(qtile, qrow, I, m);
+    for (int I = 0; I < NI; ++I) qf[I] = QT::row(qtile, qrow, I0 + I, m);
 #pragma unroll
-    for (int n = Split<T, NT>::N - 1; n >= 0; --n)
+    for (int p = 0; p < NC; ++p) {
+      const Split<T, NT> s(S.t[2 * m][p], S.t[2 * m + 1][p]);
 #pragma unroll
-      for (int I = 0; I < 4; ++I) y[I] = Op<T>::mma(y[I], s.t[n], qf[I]);
-    __builtin_amdgcn_sched_barrier(0);  // (one step's operands in registers)
+      for (int n = Split<T, NT>::N - 1; n >= 0; --n)
+#pragma unroll
+        for (int I = 0; I < NI; ++I) y[p][I] = Op<T>::mma(y[p][I], s.t[n], qf[I]);
+    }
+    if ((m & 1) || NT > 1 || NC == 1) __builtin_amdgcn_sched_barrier(0);  // (operands of a step or two in registers)
   }
 }
 
 // Y^T += V^T M^T
-template <typename T>
-__device__ __forceinline__ void intra(f32x4 (&y)[4], const typename Op<T>::F (&vf)[2], const char* scores, int l) {
+template <typename T, int NC, int I0, int NI>
+__device__ __forceinline__ void intra(f32x4 (&y)[NC][NI], const typename Op<T>::F (&vf)[NC][2], const char* scores, int l) {
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int I = 2 * m; I < 4; ++I) y[I] = Op<T>::mma(y[I], vf[m], Scores<T>::get(scores, I, m, l));
+    for (int I = 0; I < NI; ++I)
+      if (2 * m <= I0 + I) {
+        const typename Op<T>::F mf = Scores<T>::get(scores, I0 + I, m, l);
+#pragma unroll
+        for (int p = 0; p < NC; ++p) y[p][I] = Op<T>::mma(y[p][I], vf[p][m], mf);
+      }
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T* p, f32x4 x) {
-  if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x2*>(p) = u32x2{cvt2(x[0], x[1]), cvt2(x[2], x[3])};
-  else *reinterpret_cast<f32x4*>(p) = x;
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float* x) {
-  if constexpr (sizeof(T) == 2) {
+// N consecutive values
+template <typename T, int N>
+__device__ __forceinline__ void store_n(T* p, const float (&x)[N]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int b = 0; b < N; b += 4) *reinterpret_cast<f32x4*>(p + b) = f32x4{x[b], x[b + 1], x[b + 2], x[b + 3]};
+  } else if constexpr (N == 8) {
     *reinterpret_cast<u32x4*>(p) = u32x4{cvt2(x[0], x[1]), cvt2(x[2], x[3]), cvt2(x[4], x[5]), cvt2(x[6], x[7])};
   } else {
-    *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+    *reinterpret_cast<u32x2*>(p) = u32x2{cvt2(x[0], x[1]), cvt2(x[2], x[3])};
   }
+}
+// The values of a lane in row tile I of a result, in channel order.
+template <int NC, int NI>
+__device__ __forceinline__ void gather(const f32x4 (&y)[NC][NI], int I, float (&x)[4 * NC]) {
+#pragma unroll
+  for (int p = 0; p < NC; ++p)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[4 * p + e] = y[p][I][e];
 }
 
 // sum over channels of A row tile J by B row tile I (both [64][COLS]): all operands
@@ -504,19 +591,14 @@ __device__ __forceinline__ f32x4 score_tile(const char* at, const char* bt, uint
   return acc;
 }
 
-// The wave's four row tiles of results, row 16 I + i at p + I * d + off, rows below n.
-// A full chunk's four stores stand in no branch of their own: the wait for the next
-// chunk's tiles, which were loaded earlier, can then leave them on their way.
-template <typename T>
-__device__ __forceinline__ void store_rows(const f32x4 (&y)[4], char* p, long long d, uint32_t off, int n, int i) {
-  if (n == CH) {
+// A wave's row tiles I0 .. of results, row 16 I + i at p + I * d + off, rows below n.
+template <typename T, int NC, int NI>
+__device__ __forceinline__ void store_rows(const f32x4 (&y)[NC][NI], char* p, long long d, uint32_t off, int n, int i, int I0) {
 #pragma unroll
-    for (int I = 0; I < 4; ++I) store4<T>(reinterpret_cast<T*>(p + I * d + off), y[I]);
-  } else {
-#pragma unroll
-    for (int I = 0; I < 4; ++I)
-      if (16 * I + i < n) store4<T>(reinterpret_cast<T*>(p + I * d + off), y[I]);
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): no unknown number of them is left
+  for (int I = 0; I < NI; ++I) {
+    float x[4 * NC];
+    gather(y, I, x);
+    if (16 * (I0 + I) + i < n) store_n<T>(reinterpret_cast<T*>(p + (I0 + I) * d + off), x);
   }
 }
 
@@ -570,33 +652,40 @@ struct PassArgs {
 };
 
 // The state's rows and columns of a lane in global memory, [dk][dv] row-major.
-template <int NK>
-__device__ __forceinline__ void load_state(State<NK>& S, const float* p, int ld, int col0, int g, int i) {
+template <int NK, int NC>
+__device__ __forceinline__ void load_state(State<NK, NC>& S, const float* p, int ld, int col0, int g, int i) {
 #pragma unroll
   for (int a = 0; a < NK; ++a)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) S.t[a][e] = p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + i];
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S.t[a][c][e] = p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + col_chan<NC>(c, i)];
 }
-template <int NK>
-__device__ __forceinline__ void store_state(const State<NK>& S, float* p, int ld, int col0, int g, int i, float s) {
+template <int NK, int NC>
+__device__ __forceinline__ void store_state(const State<NK, NC>& S, float* p, int ld, int col0, int g, int i, float s) {
 #pragma unroll
   for (int a = 0; a < NK; ++a)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + i] = s * S.t[a][e];
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[(size_t)pair_chan(a, 4 * g + e) * ld + col0 + col_chan<NC>(c, i)] = s * S.t[a][c][e];
 }
 
 // ------------------------------------------------------------- state pass
 // End state of every segment from zero.  Workgroup = two 64-column units of one
-// group, wave = 16 columns of one.
+// group, wave = 16 NC columns of one.  The weight of a token is the decay from it to
+// the segment's end, so the chunks are walked from that end on and the state needs no
+// scaling; once the decay to the end is exactly zero for both units, every token
+// before adds exactly zero (for finite inputs), and the walk stops.
 template <typename T, int DK, bool REV>
-__global__ __launch_bounds__(512, 4) void kda_ssm_state_kernel(PassArgs a) {
+__global__ __launch_bounds__(512 / kNC<T>, 4 / kNC<T>) void kda_ssm_state_kernel(PassArgs a) {
   typedef Tile<T, DK> KT;
   typedef Tile<T, 64> VT;
-  constexpr int NT = 512;
-  __shared__ __attribute__((aligned(16))) char smem[KT::BYTES + 2 * VT::BYTES + 4 * V_SIZE * 4];
+  constexpr int NC = kNC<T>, NWV = 8 / NC, NT = 64 * NWV, VS = kVecNoKappa;
+  __shared__ __attribute__((aligned(16))) char smem[KT::BYTES + 2 * VT::BYTES + 4 * VS * 4];
   char* const sk = smem;
   char* const sv = smem + KT::BYTES;
-  float* const vecs = reinterpret_cast<float*>(sv + 2 * VT::BYTES);
+  float* const vecs = reinterpret_cast<float*>(sv + 2 * VT::BYTES);  // two buffers, two units
   const int cpu = a.dv / 64, nu = a.H / a.G * cpu;  // column units per head, units per group
   const Item it = item_of(a.B, a.G, a.norders, (nu + 1) / 2);
   if (!it.valid) return;
@@ -605,7 +694,7 @@ __global__ __launch_bounds__(512, 4) void kda_ssm_state_kernel(PassArgs a) {
   const int nch = (len + CH - 1) / CH;
   const int seg = REV ? a.nseg - 1 - it.seg : it.seg;
   const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
-  const int uw = wave >> 2, quarter = wave & 3;
+  const int uw = wave / (NWV / 2), part = wave % (NWV / 2);
   const T* K = static_cast<const T*>(a.K) + it.b * a.ks.b + it.g * a.ks.h;
   int head[2];
   const T* V[2];
@@ -615,40 +704,44 @@ __global__ __launch_bounds__(512, 4) void kda_ssm_state_kernel(PassArgs a) {
     head[u] = it.g * (a.H / a.G) + un / cpu;
     V[u] = static_cast<const T*>(a.V) + it.b * a.vs.b + head[u] * a.vs.h + (un % cpu) * 64;
   }
-  const bool filler = wave >= 6;  // waves 6 and 7, for units 0 and 1
-  const int hv = wave & 1 ? head[1] : head[0];
+  const int fu = wave - (NWV - 2);  // the last two waves fill the units' decay vectors
+  const bool filler = fu >= 0;
+  const int hv = fu == 1 ? head[1] : head[0];
   const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
-  State<DK / 16> S;
+  State<DK / 16, NC> S;
   S.zero();
-  float dec = 1.f;
+  float dec = 1.f;  // decay of the chunks walked
   Fetch<T, DK, NT> fk;
   Fetch<T, 64, NT> fv[2];
   const uint32_t ofk = fk.template lane_off<REV>(a.ks.t, tid), ofv = fv[0].template lane_off<REV>(a.vs.t, tid);
   T fx = T(0.f), fb = T(0.f);
+  float run = 1.f;  // filler: decay from the chunk's end to the segment's
+  auto chunk = [&](int step) { return REV ? c0 + step : c1 - 1 - step; };  // the order's last chunk first
   auto fetch = [&](int step) {
-    const int c = REV ? c1 - 1 - step : c0 + step;
-    const int tok0 = c * CH, n = min(CH, len - tok0);
+    const int tok0 = chunk(step) * CH, n = min(CH, len - tok0);
     fk.template get<REV>(K, a.ks.t, tok0, n, ofk, tid);
 #pragma unroll
     for (int u = 0; u < 2; ++u) fv[u].template get<REV>(V[u], a.vs.t, tok0, n, ofv, tid);
   };
   auto fetch_gates = [&](int step) {
     if (!filler || step >= c1 - c0) return;
-    const int c = REV ? c1 - 1 - step : c0 + step;
-    const int tok0 = c * CH, n = min(CH, len - tok0);
+    const int tok0 = chunk(step) * CH, n = min(CH, len - tok0);
     fx = decay_at<T, REV>(la, a.ls.t, tok0, n, a.T, l);
     fb = weight_at<T, false>(beta, a.bs.t, tok0, n, l, !REV);
   };
   auto fill = [&](int step) {
-    if (filler && step < c1 - c0) fill_vec(vecs + ((step & 1) * 2 + wave - 6) * V_SIZE, l, to_f32(fx), REV ? 1.f : to_f32(fb), 1.f, 1.f);
+    if (!filler || step >= c1 - c0) return;
+    float* v = vecs + ((step & 1) * 2 + fu) * VS;
+    run *= fill_vec<false>(v, l, to_f32(fx), REV ? 1.f : to_f32(fb), 1.f, 1.f, run);
+    if (l == 0) v[V_GM] = run;
   };
   fetch_gates(0);
   if (c0 < c1) fetch(0);
   fill(0);
   fetch_gates(1);
   for (int step = 0; step < c1 - c0; ++step) {
-    const float* const v = vecs + ((step & 1) * 2 + uw) * V_SIZE;
+    const float* const vec = vecs + (step & 1) * 2 * VS;
     fk.put(sk, tid);
 #pragma unroll
     for (int u = 0; u < 2; ++u) fv[u].put(sv + u * VT::BYTES, tid);
@@ -657,13 +750,16 @@ __global__ __launch_bounds__(512, 4) void kda_ssm_state_kernel(PassArgs a) {
     fill(step + 1);
     fetch_gates(step + 2);
     const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
-    const uint32_t vcol = VT::vcol_off(g, i);
-    typename Op<T>::F vf[2];
+    const uint32_t vcol = VT::template vtile_off<NC>(g, i, part);
+    typename Op<T>::F vf[NC][2];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) vf[m] = VT::vcol(sv + uw * VT::BYTES, vcol, m, quarter);
-    const float gm = v[V_GM];
-    dec *= gm;
-    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, gm, KT::col_off(g, i), g);
+    for (int p = 0; p < NC; ++p)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) vf[p][m] = VT::template vtile<NC>(sv + uw * VT::BYTES, vcol, m, p);
+    update<T, DK / 16, NC, 3, false, KT>(S, sk, vf, vec + uw * VS + V_WS, 1.f, KT::col_off(g, i), g);
+    const float r0 = vec[V_GM], r1 = vec[VS + V_GM];
+    dec = uw ? r1 : r0;
+    if (__builtin_amdgcn_readfirstlane(r0 == 0.f && r1 == 0.f)) break;
     sync_lds();
   }
   const int un = 2 * it.sub + uw;
@@ -671,13 +767,15 @@ __global__ __launch_bounds__(512, 4) void kda_ssm_state_kernel(PassArgs a) {
   const size_t bh = (size_t)it.b * a.H + (uw ? head[1] : head[0]);
   // order o's end state lies in slot o + 1
   float* out = a.end + ((size_t)(it.seg + 1) * a.B * a.H + bh) * a.dk * a.dv;
-  store_state(S, out, a.dv, (un % cpu) * 64 + quarter * 16, l >> 4, l & 15, 1.f);
-  if (quarter == 0 && un % cpu == 0 && l == 0) a.dec[(size_t)it.seg * a.B * a.H + bh] = dec;
+  store_state(S, out, a.dv, (un % cpu) * 64 + part * 16 * NC, l >> 4, l & 15, 1.f);
+  if (part == 0 && un % cpu == 0 && l == 0) a.dec[(size_t)it.seg * a.B * a.H + bh] = dec;
 }
 
-// slots[0] = start; slots[o + 1] = dec[o] slots[o] + slots[o + 1], o = 0 .. n - 1
+// slots[0] = start; slots[o + 1] = dec[o] slots[o] + slots[o + 1], o = 0 .. n - 1.  The
+// last one also goes to out (which may be start), with la times the decay of token 0.
+template <typename T>
 __global__ __launch_bounds__(256) void kda_ssm_merge_kernel(const float* start, float* slots, const float* dec, long long BH,
-                                                            int elems, int n) {
+                                                            int elems, int n, float* out, const T* la, Str3 ls, int H) {
   const long long f = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
   if (f >= BH * elems) return;
   const long long bh = f / elems;
@@ -691,6 +789,13 @@ __global__ __launch_bounds__(256) void kda_ssm_merge_kernel(const float* start, 
     for (int e = 0; e < 4; ++e) s[e] = d * s[e] + z[e];
     *reinterpret_cast<f32x4*>(p) = s;
   }
+  if (!out) return;
+  if (la) {
+    const float d = ex2(fmaxf(to_f32(la[(bh / H) * ls.b + (bh % H) * ls.h]) * kLog2e, -180.f));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] *= d;
+  }
+  *reinterpret_cast<f32x4*>(out + f) = s;
 }
 
 __global__ __launch_bounds__(256) void kda_ssm_copy_kernel(const float* src, float* dst, long long n4) {
@@ -699,26 +804,29 @@ __global__ __launch_bounds__(256) void kda_ssm_copy_kernel(const float* src, flo
 }
 
 // ----------------------------------------------------------------- outputs
-// Workgroup = two 64-column units of one group over a segment's chunks, wave = 16
+// Workgroup = two 64-column units of one group over a segment's chunks, wave = 16 NC
 // columns of one unit.  Per chunk: the scores are formed once (Q.K once for both
 // units) and left in LDS; every wave then forms its columns of Y and moves its
 // state on.  The next chunk's tiles are loaded to registers meanwhile.
+// TERMS: of the state's updates; three where the state is written at the end.
 // BWD: the reversed pass, which also leaves, per unit and token, what the
 // gradients of beta and log_alpha need:
 //   c[j] = sum_i P_ij (and the state's part), r[i] = sum_j beta_j P_ij (inside the
 //   chunk), d[i] = dO_i.v_i, with P_ij = (dO_i.v_j) (q_i.k_j) e^{l_i - l_j}.
-template <typename T, int DK, bool BWD>
-__global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2) void kda_ssm_out_kernel(PassArgs a) {
+template <typename T, int DK, bool BWD, int TERMS>
+__global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a) {
   typedef Tile<T, DK> KT;
   typedef Tile<T, 64> VT;
   typedef Scores<T> SC;
-  constexpr int NT = 512;
+  constexpr int NC = kNC<T>, NWV = 8 / NC, NT = 64 * NWV, NPU = NWV / 2;  // waves, threads, waves per unit
+  constexpr bool KAPPA = !BWD;
+  constexpr int VS = KAPPA ? V_SIZE : kVecNoKappa;
   constexpr int OV = 2 * KT::BYTES, OV2 = OV + 2 * VT::BYTES, OM = OV2 + (BWD ? 2 * VT::BYTES : 0);
   // two buffers of decay vectors, the next chunk's filled beside this one's products
-  // (one where the tiles leave no room)
-  constexpr int NB = sizeof(T) == 4 && BWD && DK == 128 ? 1 : 2;
-  constexpr int OVEC = OM + 2 * SC::BYTES, ORED = OVEC + NB * 2 * V_SIZE * 4;
-  constexpr int RED = 4 * 64 + 4 * 64;  // column sums by J, row sums by I
+  // (one where two would leave a compute unit with one workgroup)
+  constexpr int NB = sizeof(T) == 2 && BWD && DK == 128 ? 1 : 2;
+  constexpr int OVEC = OM + 2 * SC::BYTES, ORED = OVEC + NB * 2 * VS * 4;
+  constexpr int RED = 160 + 160 + (NPU > 3 ? 64 : 0);  // column and row sums of the ten tiles, a fourth wave's sums
   __shared__ __attribute__((aligned(16))) char smem[ORED + (BWD ? 2 * RED * 4 : 0)];
   char* const sq = smem;
   char* const sk = smem + KT::BYTES;
@@ -735,7 +843,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2)
   const int nch = (len + CH - 1) / CH;
   const int seg = BWD ? a.nseg - 1 - it.seg : it.seg;
   const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
-  const int uw = wave >> 2, quarter = wave & 3;
+  const int uw = wave / NPU, part = wave % NPU;
   const T* Q = static_cast<const T*>(a.Q) + it.b * a.qs.b + it.g * a.qs.h;
   const T* K = static_cast<const T*>(a.K) + it.b * a.ks.b + it.g * a.ks.h;
   int head[2], colu[2];
@@ -749,9 +857,10 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2)
     V2[u] = BWD ? static_cast<const T*>(a.V2) + it.b * a.v2s.b + head[u] * a.v2s.h + colu[u] : nullptr;
   }
   const bool mine = 2 * it.sub + uw < nu;
-  const int hw = uw ? head[1] : head[0], cw = (uw ? colu[1] : colu[0]) + quarter * 16;  // the wave's head and column
-  const bool filler = wave >= 6;  // waves 6 and 7 fill the decay vectors, of units 0 and 1
-  const int hv = wave & 1 ? head[1] : head[0];
+  const int hw = uw ? head[1] : head[0], cw = (uw ? colu[1] : colu[0]) + part * 16 * NC;  // the wave's head and column
+  const int fu = wave - (NWV - 2);  // the last two waves fill the units' decay vectors
+  const bool filler = fu >= 0;
+  const int hv = fu == 1 ? head[1] : head[0];
   const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
   float skip[2] = {0.f, 0.f};
@@ -762,11 +871,9 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2)
   const float skip_w = uw ? skip[1] : skip[0];
   T* o = static_cast<T*>(a.o) + it.b * a.os.b + hw * a.os.h + cw;
   const size_t bh = (size_t)it.b * a.H + hw;
-  State<DK / 16> S;
+  State<DK / 16, NC> S;
   if (a.start) load_state(S, a.start + ((size_t)it.seg * a.B * a.H + bh) * a.dk * a.dv, a.dv, cw, l >> 4, l & 15);
   else S.zero();
-  SC::clear(sm, tid, NT);
-  SC::clear(sm + SC::BYTES, tid, NT);
 
   Fetch<T, DK, NT> fq, fk;
   Fetch<T, 64, NT> fv[2], fw[2];
@@ -793,7 +900,8 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2)
     fb = weight_at<T, BWD>(beta, a.bs.t, tok0, n, l, true);
   };
   auto fill = [&](int step) {
-    if (filler && step < c1 - c0) fill_vec(vecs + ((step % NB) * 2 + wave - 6) * V_SIZE, l, to_f32(fx), BWD ? 1.f : to_f32(fb), 1.f, to_f32(fb));
+    if (filler && step < c1 - c0)
+      fill_vec<KAPPA>(vecs + ((step % NB) * 2 + fu) * VS, l, to_f32(fx), BWD ? 1.f : to_f32(fb), 1.f, to_f32(fb));
   };
   fetch_gates(0);
   if (c0 < c1) fetch(0);
@@ -804,7 +912,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2)
   for (int step = 0; step < c1 - c0; ++step) {
     const int c = BWD ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, len - tok0);
-    float* const vec = vecs + (step % NB) * 2 * V_SIZE;
+    float* const vec = vecs + (step % NB) * 2 * VS;
     fq.put(sq, tid);
     fk.put(sk, tid);
 #pragma unroll
@@ -821,16 +929,16 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2)
 
     const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
     const uint32_t krow = KT::row_off(g, i);
-    // scores: the ten tiles dealt to the waves, the two left over to waves 4 and 5
-    for (int t = wave; t < 10; t += wave < 4 ? 16 : 4) {
+    // scores: the ten tiles dealt to the waves (of eight waves, two to waves 4 and 5)
+    for (int t = wave; t < 10; t += NWV == 8 && wave < 4 ? 16 : 4) {
       const int I = tile_i(t), J = tile_j(t);
       const f32x4 acc = score_tile<T, DK>(sk, sq, krow, I, J);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float* v = vec + u * V_SIZE;
-        f32x4 mm = weigh(acc, v, I, J, g, i);
+        const float* v = vec + u * VS;
+        f32x4 mm = weigh<KAPPA>(acc, v, I, J, g, i);
         if constexpr (BWD) {
-          float* rd = red + u * RED;
+          float* rd = red + u * RED + 16 * SC::tile(I, J);
           const f32x4 dd = score_tile<T, 64>(sv + u * VT::BYTES, sv2 + u * VT::BYTES, VT::row_off(g, i), I, J);
           const float bi = v[V_RH + 16 * I + i];
           float cs = 0.f, rs[4];
@@ -842,13 +950,10 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2)
           }
           cs += __shfl_xor(cs, 16);
           cs += __shfl_xor(cs, 32);
-          if (g == 0) rd[64 * J + 16 * I + i] = cs;
+          if (g == 0) rd[i] = cs;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-#pragma unroll
-            for (int off = 1; off < 16; off <<= 1) rs[e] += __shfl_xor(rs[e], off);
-          }
-          if (i == 0) *reinterpret_cast<f32x4*>(rd + 256 + 64 * I + 16 * J + 4 * g) = f32x4{rs[0], rs[1], rs[2], rs[3]};
+          for (int e = 0; e < 4; ++e) rs[e] = row16_sum(rs[e]);
+          if (i == 0) *reinterpret_cast<f32x4*>(rd + 160 + 4 * g) = f32x4{rs[0], rs[1], rs[2], rs[3]};
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) mm[e] += I == J && 4 * g + e == i ? skip[u] : 0.f;
@@ -860,73 +965,93 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2)
       fill(step + 1);
       fetch_gates(step + 2);
     }
-    const float* v = vec + uw * V_SIZE;
-    f32x4 y[4];
-    inter<T, DK / 16, BWD ? 2 : 1, KT>(y, S, sq, krow);
+    float* const v = vec + uw * VS;
+    f32x4 y[NC][4];
+    inter<T, DK / 16, NC, BWD ? 2 : 1, 4, KT>(y, S, sq, krow, 0);
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
       const float s = v[V_IN + 16 * I + i];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[I][e] *= s;
+      for (int p = 0; p < NC; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[p][I][e] *= s;
     }
     sync_lds();
     if constexpr (BWD) {
-      // the state's part of c, z.v before the chunk's own part joins z, and dO.v, one
-      // sum per wave; left where the score vectors were
-      float* w = vec + uw * V_SIZE;
-      static_assert(V_PB == 0 && V_KP == 192, "four score vectors");
+      // the state's part of c, z.v before the chunk's own part joins z, one sum per
+      // wave, left where the score vectors were
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
-        const f32x4 x = VT::quad(sv2 + uw * VT::BYTES, I, i, quarter, g);
-        float s = (y[I][0] * x[0] + y[I][1] * x[1]) + (y[I][2] * x[2] + y[I][3] * x[3]);
+        float x[4 * NC], z[4 * NC], s = 0.f;
+        VT::template place<NC>(sv2 + uw * VT::BYTES, I, i, part, g, x);
+        gather(y, I, z);
+#pragma unroll
+        for (int e = 0; e < 4 * NC; ++e) s += z[e] * x[e];
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
-        if (g == 0) w[64 * quarter + 16 * I + i] = s;
+        if (g == 0) (part < 3 ? v + 64 * part : red + uw * RED + 320)[16 * I + i] = s;
       }
     }
-    typename Op<T>::F vf[2];
+    typename Op<T>::F vf[NC][2];
+    const uint32_t vcol = VT::template vtile_off<NC>(g, i, part);
 #pragma unroll
-    for (int m = 0; m < 2; ++m) vf[m] = VT::vcol(sv + uw * VT::BYTES, VT::vcol_off(g, i), m, quarter);
-    intra<T>(y, vf, sm + uw * SC::BYTES, l);
-    char* const ob = reinterpret_cast<char*>(o + (long long)(BWD ? tok0 + n - CH : tok0) * a.os.t);
-    const long long od = (BWD ? -16 : 16) * a.os.t * (long long)sizeof(T);
-    const uint32_t oo = ((uint32_t)(BWD ? CH - 1 - i : i) * (uint32_t)a.os.t + 4u * g) * (uint32_t)sizeof(T);
+    for (int p = 0; p < NC; ++p)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) vf[p][m] = VT::template vtile<NC>(sv + uw * VT::BYTES, vcol, m, p);
+    intra<T, NC, 0, 4>(y, vf, sm + uw * SC::BYTES, l);
     if constexpr (BWD) {
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
         const float bi = v[V_RH + 16 * I + i];
-        const f32x4 gy = VT::quad(sv + uw * VT::BYTES, I, i, quarter, g);
+        float gy[4 * NC];
+        VT::template place<NC>(sv + uw * VT::BYTES, I, i, part, g, gy);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[I][e] = bi * y[I][e] + skip_w * gy[e];
+        for (int p = 0; p < NC; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[p][I][e] = bi * y[p][I][e] + skip_w * gy[4 * p + e];
       }
     }
-    store_rows<T>(y, ob, od, oo, mine ? n : 0, i);
+    char* const ob = reinterpret_cast<char*>(o + (long long)(BWD ? tok0 + n - CH : tok0) * a.os.t);
+    const long long od = (BWD ? -16 : 16) * a.os.t * (long long)sizeof(T);
+    const uint32_t oo = ((uint32_t)(BWD ? CH - 1 - i : i) * (uint32_t)a.os.t + 4u * NC * g) * (uint32_t)sizeof(T);
+    store_rows<T>(y, ob, od, oo, mine ? n : 0, i, 0);
     __builtin_amdgcn_sched_barrier(0);
-    update<T, DK / 16, KT>(S, sk, vf, v + V_WS, v[V_GM], KT::col_off(g, i), g);
+    update<T, DK / 16, NC, TERMS, true, KT>(S, sk, vf, v + V_WS, v[V_GM], KT::col_off(g, i), g);
     if constexpr (BWD) {
-      // dO.v of the unit's rows, 16 rows a wave
-      const int p = 16 * quarter + i;
-      float d = 0.f;
+      // dO.v of the unit's rows, 64 / NPU rows a wave
+      if (a.D) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4 x = VT::quad(sv2 + uw * VT::BYTES, quarter, i, q, g), gy = VT::quad(sv + uw * VT::BYTES, quarter, i, q, g);
-        d += (x[0] * gy[0] + x[1] * gy[1]) + (x[2] * gy[2] + x[3] * gy[3]);
+        for (int r = 0; r < 4 / NPU; ++r) {
+          const int I = part * (4 / NPU) + r, p = 16 * I + i;
+          float d = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4 / NC; ++w) {
+            float x[4 * NC], gy[4 * NC];
+            VT::template place<NC>(sv2 + uw * VT::BYTES, I, i, w, g, x);
+            VT::template place<NC>(sv + uw * VT::BYTES, I, i, w, g, gy);
+#pragma unroll
+            for (int e = 0; e < 4 * NC; ++e) d += x[e] * gy[e];
+          }
+          d += __shfl_xor(d, 16);
+          d += __shfl_xor(d, 32);
+          if (g == 0 && p < n && mine)
+            a.d[((size_t)it.b * a.H * cpu + (size_t)hw * cpu + (cw >> 6)) * a.T + tok0 + n - 1 - p] = d;
+        }
       }
-      d += __shfl_xor(d, 16);
-      d += __shfl_xor(d, 32);
-      if (g == 0 && p < n && mine)
-        a.d[((size_t)it.b * a.H * cpu + (size_t)hw * cpu + (cw >> 6)) * a.T + tok0 + n - 1 - p] = d;
     }
     sync_lds();
     if constexpr (BWD) {
       // one wave writes a unit's sums, the one that fills that unit's vectors
-      if (filler && 2 * it.sub + wave - 6 < nu && l < n) {
-        const float* rd = red + (wave - 6) * RED;
-        const float* w = vec + (wave - 6) * V_SIZE;
-        float cs = (w[l] + w[64 + l]) + (w[128 + l] + w[192 + l]), rs = 0.f;
-        for (int J = 0; J <= (l >> 4); ++J) cs += rd[64 * J + l];
-        for (int I = l >> 4; I < 4; ++I) rs += rd[256 + 64 * I + l];
-        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)hv * cpu + (2 * it.sub + wave - 6) % cpu) * a.T + tok0 + n - 1 - l;
+      if (filler && 2 * it.sub + fu < nu && l < n) {
+        const float* rd = red + fu * RED;
+        const float* w = vec + fu * VS;
+        float cs = 0.f, rs = 0.f;
+#pragma unroll
+        for (int q = 0; q < NPU; ++q) cs += q < 3 ? w[64 * q + l] : rd[320 + l];
+        const int blk = l >> 4;
+        for (int J = 0; J <= blk; ++J) cs += rd[16 * SC::tile(blk, J) + (l & 15)];
+        for (int I = blk; I < 4; ++I) rs += rd[160 + 16 * SC::tile(I, blk) + (l & 15)];
+        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)hv * cpu + (2 * it.sub + fu) % cpu) * a.T + tok0 + n - 1 - l;
         a.c[at] = cs;
         a.r[at] = rs;
       }
@@ -943,19 +1068,22 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 && !(BWD && DK == 128) ? 4 : 2)
 // ---------------------------------------------------------- summed over heads
 // dq (REV = false) and dk (REV): V is the group's shared row (k or q, DK
 // columns), Q and K are the heads' rows (dO and v, DV).  Workgroup = HG heads of
-// one group, wave = 16 of the DK columns for all of them, so that the sum over
+// one group, wave = 16 NC of the DK columns for all of them, so that the sum over
 // the heads stays in its accumulators; groups with more heads leave one partial
 // result per workgroup.  The forward pass also leaves, per head and token,
 // rs[i] = q_i . (the state's part of dq_i).
 template <typename T, int DV, int DK, bool REV>
-__global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? (DK == 128 && REV && DV == 128 ? 4 : 2) : DK / 64) void kda_ssm_group_kernel(
-    PassArgs a, const void* qin, Str3 qrs, float* rs, float* parts) {
-  constexpr int HG = 128 / DV, NW = DK / 16, NT = 64 * NW;
+__global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_group_kernel(PassArgs a, const void* qin, Str3 qrs,
+                                                                                          float* rs, float* parts) {
+  constexpr int NC = kNC<T>, HG = 128 / DV, NW = DK / 16 / NC, NT = 64 * NW;
+  constexpr int NI = NC == 2 ? 2 : 4;  // row tiles at a time: with two column tiles a half of the tokens
+  constexpr bool KAPPA = !REV;
+  constexpr int VS = KAPPA ? V_SIZE : kVecNoKappa;
   typedef Tile<T, DV> QT;
   typedef Tile<T, DK> VT;
   typedef Scores<T> SC;
   constexpr int OQ = VT::BYTES, OK = OQ + HG * QT::BYTES, OM = OK + HG * QT::BYTES;
-  constexpr int OVEC = OM + HG * SC::BYTES, ORS = OVEC + 2 * HG * V_SIZE * 4;
+  constexpr int OVEC = OM + HG * SC::BYTES, ORS = OVEC + 2 * HG * VS * 4;
   // rs: one sum per wave, head and token; four waves' where the score vectors were, four more
   __shared__ __attribute__((aligned(16))) char smem[ORS + (!REV && NW > 4 ? HG * 256 * 4 : 0)];
   char* const sv = smem;
@@ -976,7 +1104,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? (DK == 128 && REV && DV ==
   const int nh = min(HG, R - it.sub * HG);  // heads of this workgroup
   int head[HG];
   const T *Q[HG], *K[HG];
-  State<DV / 16> S[HG];
+  State<DV / 16, NC> S[HG];
 #pragma unroll
   for (int h = 0; h < HG; ++h) {
     head[h] = it.g * R + it.sub * HG + min(h, nh - 1);
@@ -988,16 +1116,17 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? (DK == 128 && REV && DV ==
       const float* p = a.start + ((size_t)it.seg * a.B * a.H + (size_t)it.b * a.H + head[h]) * DK * DV;
 #pragma unroll
       for (int t = 0; t < DV / 16; ++t)
-        S[h].t[t] = *reinterpret_cast<const f32x4*>(p + (size_t)(16 * wave + (l & 15)) * DV + pair_chan(t, 4 * (l >> 4)));
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          S[h].t[t][c] = *reinterpret_cast<const f32x4*>(p + (size_t)(16 * NC * wave + col_chan<NC>(c, l & 15)) * DV +
+                                                         pair_chan(t, 4 * (l >> 4)));
     }
   }
-  const bool filler = wave >= NW - HG;  // the last HG waves fill the heads' decay vectors
-  const int fh = wave - (NW - HG);
-  const int hv = HG == 2 && (wave & 1) ? head[HG - 1] : head[0];
+  const int fh = wave - (NW - HG);  // the last HG waves fill the heads' decay vectors
+  const bool filler = fh >= 0;
+  const int hv = fh == 1 ? head[HG - 1] : head[0];
   const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
-#pragma unroll
-  for (int h = 0; h < HG; ++h) SC::clear(sm + h * SC::BYTES, tid, NT);
 
   Fetch<T, DK, NT> fv;
   Fetch<T, DV, NT> fq[HG], fk[HG];
@@ -1024,8 +1153,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? (DK == 128 && REV && DV ==
   };
   auto fill = [&](int step) {
     if (filler && step < c1 - c0)
-      fill_vec(vecs + ((step & 1) * HG + fh) * V_SIZE, l, to_f32(fx), REV ? 1.f : to_f32(fb), REV ? to_f32(fb) : 1.f,
-               to_f32(fb));
+      fill_vec<KAPPA>(vecs + ((step & 1) * HG + fh) * VS, l, to_f32(fx), REV ? 1.f : to_f32(fb), REV ? to_f32(fb) : 1.f, to_f32(fb));
   };
   fetch_gates(0);
   if (c0 < c1) fetch(0);
@@ -1034,7 +1162,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? (DK == 128 && REV && DV ==
   for (int step = 0; step < c1 - c0; ++step) {
     const int c = REV ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, a.T - tok0);
-    float* const vec = vecs + (step & 1) * HG * V_SIZE;
+    float* const vec = vecs + (step & 1) * HG * VS;
     fv.put(sv, tid);
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
@@ -1042,15 +1170,15 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? (DK == 128 && REV && DV ==
       fk[h].put(sk + h * QT::BYTES, tid);
     }
     // the wave's columns of the q rows, for rs: straight from memory, in the layout of its results
-    typedef typename std::conditional<sizeof(T) == 2, bf16x4, f32x4>::type X4;
-    X4 xq[4];
-    const uint32_t oxq = ((uint32_t)(l & 15) * (uint32_t)qrs.t + 4u * (l >> 4)) * (uint32_t)sizeof(T);
+    u32x4 xq[4];
+    const uint32_t oxq = ((uint32_t)(l & 15) * (uint32_t)qrs.t + 4u * NC * (l >> 4)) * (uint32_t)sizeof(T);
     if constexpr (!REV) {
+      static_assert(4 * NC * sizeof(T) == 16, "16 bytes a lane");
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
         const int p = 16 * I + (l & 15);
-        xq[I] = X4{};
-        if (p < n) xq[I] = *reinterpret_cast<const X4*>(reinterpret_cast<const char*>(W + (tok0 + 16 * I) * qrs.t + 16 * wave) + oxq);
+        xq[I] = u32x4{0u, 0u, 0u, 0u};
+        if (p < n) xq[I] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(W + (tok0 + 16 * I) * qrs.t + 16 * NC * wave) + oxq);
       }
     }
     if (step + 1 < c1 - c0) fetch(step + 1);
@@ -1058,13 +1186,13 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? (DK == 128 && REV && DV ==
 
     const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
     const uint32_t qrow = QT::row_off(g, i);
-    for (int t = wave; t < 10; t += NW == 8 && wave < 4 ? 16 : 4) {
+    for (int t = wave; t < 10; t += NW == 8 ? (wave < 4 ? 16 : 4) : NW) {
       const int I = tile_i(t), J = tile_j(t);
 #pragma unroll
       for (int h = 0; h < HG; ++h) {
         const f32x4 acc = score_tile<T, DV>(sk + h * QT::BYTES, sq + h * QT::BYTES, qrow, I, J);
-        const float* v = vec + h * V_SIZE;
-        f32x4 mm = weigh(acc, v, I, J, g, i);
+        const float* v = vec + h * VS;
+        f32x4 mm = weigh<KAPPA>(acc, v, I, J, g, i);
         if (REV && I == J) {
           const float rho = v[V_RH + 16 * I + i];
 #pragma unroll
@@ -1077,65 +1205,84 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? (DK == 128 && REV && DV ==
     fetch_gates(step + 2);
     sync_lds();
 
-    typename Op<T>::F vf[2];
-    f32x4 y[4];
-#pragma unroll
-    for (int I = 0; I < 4; ++I) y[I] = zero4();
-#pragma unroll
-    for (int h = 0; h < HG; ++h) {
-      float* v = vec + h * V_SIZE;
-      f32x4 z[4];
-      inter<T, DV / 16, REV ? 1 : 2, QT>(z, S[h], sq + h * QT::BYTES, qrow);
-#pragma unroll
-      for (int I = 0; I < 4; ++I) {
-        const float s = h < nh ? v[V_IN + 16 * I + i] : 0.f;
-        if constexpr (!REV) {
-          float dot = (z[I][0] * (float)xq[I][0] + z[I][1] * (float)xq[I][1]) + (z[I][2] * (float)xq[I][2] + z[I][3] * (float)xq[I][3]);
-          dot *= s;
-          dot += __shfl_xor(dot, 16);
-          dot += __shfl_xor(dot, 32);
-          // (the score vectors are no longer needed)
-          if (g == 0) (wave < 4 ? v + 64 * wave : rsx + 256 * h + 64 * (wave - 4))[16 * I + i] = dot;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[I][e] += s * z[I][e];
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if (h == 0) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) vf[m] = VT::vcol(sv, VT::vcol_off(g, i), m, wave);
-      }
-      intra<T>(y, vf, sm + h * SC::BYTES, l);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    const long long rows = REV ? tok0 + n - CH : tok0;  // as in Fetch
+    typename Op<T>::F vf[NC][2];
+    const uint32_t vcol = VT::template vtile_off<NC>(g, i, wave);
+    const long long row0 = REV ? tok0 + n - CH : tok0;  // as in Fetch
     const int ri = REV ? CH - 1 - i : i;
-    if (np == 1) {
-      char* const ob = reinterpret_cast<char*>(static_cast<T*>(a.o) + it.b * a.os.b + it.g * a.os.h + rows * a.os.t + 16 * wave);
-      const long long od = (REV ? -16 : 16) * a.os.t * (long long)sizeof(T);
-      const uint32_t oo = ((uint32_t)ri * (uint32_t)a.os.t + 4u * g) * (uint32_t)sizeof(T);
-      store_rows<T>(y, ob, od, oo, n, i);
-    } else {
-      char* const ob = reinterpret_cast<char*>(parts + (((long long)it.sub * a.B * a.G + (long long)it.b * a.G + it.g) * a.T + rows) * DK + 16 * wave);
-      const uint32_t oo = (uint32_t)(ri * DK + 4 * g) * 4u;
-      store_rows<float>(y, ob, (REV ? -16 : 16) * DK * 4, oo, n, i);
+    auto some = [&](auto B) {
+      constexpr int I0 = decltype(B)::value;
+      f32x4 y[NC][NI];
+#pragma unroll
+      for (int p = 0; p < NC; ++p)
+#pragma unroll
+        for (int I = 0; I < NI; ++I) y[p][I] = zero4();
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+        float* v = vec + h * VS;
+        f32x4 z[NC][NI];
+        inter<T, DV / 16, NC, REV ? 1 : 2, NI, QT>(z, S[h], sq + h * QT::BYTES, qrow, I0);
+#pragma unroll
+        for (int I = 0; I < NI; ++I) {
+          const float s = h < nh ? v[V_IN + 16 * (I0 + I) + i] : 0.f;
+          if constexpr (!REV) {
+            float zz[4 * NC], dot = 0.f;
+            gather(z, I, zz);
+#pragma unroll
+            for (int e = 0; e < 4 * NC; ++e) {
+              const uint32_t w = xq[I0 + I][e * (int)sizeof(T) / 4];
+              dot += zz[e] * __uint_as_float(sizeof(T) == 4 ? w : (e & 1 ? w & 0xffff0000u : w << 16));
+            }
+            dot *= s;
+            dot += __shfl_xor(dot, 16);
+            dot += __shfl_xor(dot, 32);
+            // (the score vectors are no longer needed)
+            if (g == 0) (wave < 4 ? v + 64 * wave : rsx + 256 * h + 64 * (wave - 4))[16 * (I0 + I) + i] = dot;
+          }
+#pragma unroll
+          for (int p = 0; p < NC; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[p][I][e] += s * z[p][I][e];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (h == 0 && I0 == 0) {
+#pragma unroll
+          for (int p = 0; p < NC; ++p)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) vf[p][m] = VT::template vtile<NC>(sv, vcol, m, p);
+        }
+        intra<T, NC, I0, NI>(y, vf, sm + h * SC::BYTES, l);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (np == 1) {
+        char* const ob = reinterpret_cast<char*>(static_cast<T*>(a.o) + it.b * a.os.b + it.g * a.os.h + row0 * a.os.t + 16 * NC * wave);
+        store_rows<T>(y, ob, (REV ? -16 : 16) * a.os.t * (long long)sizeof(T),
+                      ((uint32_t)ri * (uint32_t)a.os.t + 4u * NC * g) * (uint32_t)sizeof(T), n, i, I0);
+      } else {
+        char* const ob = reinterpret_cast<char*>(parts + (((long long)it.sub * a.B * a.G + (long long)it.b * a.G + it.g) * a.T + row0) * DK +
+                                                 16 * NC * wave);
+        store_rows<float>(y, ob, (REV ? -16 : 16) * DK * 4, (uint32_t)(ri * DK + 4 * NC * g) * 4u, n, i, I0);
+      }
+    };
+    some(std::integral_constant<int, 0>());
+    if constexpr (NI == 2) {
+#pragma unroll
+      for (int h = 0; h < HG; ++h) S[h].renew();
+      some(std::integral_constant<int, 2>());
     }
     // after the stores, when the results' registers are free
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
       __builtin_amdgcn_sched_barrier(0);
-      const float* v = vec + h * V_SIZE;
-      update<T, DV / 16, QT>(S[h], sk + h * QT::BYTES, vf, v + V_WS, v[V_GM], QT::col_off(g, i), g);
+      const float* v = vec + h * VS;
+      update<T, DV / 16, NC, 2, true, QT>(S[h], sk + h * QT::BYTES, vf, v + V_WS, v[V_GM], QT::col_off(g, i), g);
     }
     sync_lds();
     if constexpr (!REV) {
       if (wave < nh && l < n) {
-        const float* v = vec + wave * V_SIZE;
-        float s = (v[l] + v[64 + l]) + (v[128 + l] + v[192 + l]);
-        if (NW > 4) {
-          const float* x = rsx + 256 * wave;
-          s += (x[l] + x[64 + l]) + (x[128 + l] + x[192 + l]);
-        }
+        const float* v = vec + wave * VS;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) s += w < 4 ? v[64 * w + l] : rsx[256 * wave + 64 * (w - 4) + l];
         rs[((size_t)it.b * a.H + it.g * R + it.sub * HG + wave) * a.T + tok0 + l] = s;
       }
     }
@@ -1163,7 +1310,7 @@ __global__ __launch_bounds__(256) void kda_ssm_parts_kernel(const float* parts, 
   }
   const int t = (int)(row % T_);
   const long long bg = row / T_;
-  store8<T>(out + (bg / G) * os.b + (bg % G) * os.h + (long long)t * os.t + c, x);
+  store_n<T>(out + (bg / G) * os.b + (bg % G) * os.h + (long long)t * os.t + c, x);
 }
 
 // dlog_alpha and dbeta of one (b, h, segment), and the segment's share of dD.
@@ -1211,7 +1358,7 @@ __global__ __launch_bounds__(256) void kda_ssm_finish_kernel(PassArgs a, const f
         const size_t at = ((size_t)bh * cpu + u) * a.T + t;
         c += a.c[at];
         r += a.r[at];
-        dsum += a.d[at];
+        if (dDp) dsum += a.d[at];
       }
       x = r - to_f32(beta[(long long)t * a.bs.t]) * c;
       dbeta[b * dbs.b + h * dbs.h + (long long)t * dbs.t] = from_f32<T>(c);
@@ -1312,19 +1459,27 @@ __global__ __launch_bounds__(256) void kda_ssm_check_kernel(const T* la, Str3 ls
 template <typename T, bool REV>
 hipError_t run_state(const PassArgs& a, hipStream_t s) {
   const int nu = a.H / a.G * (a.dv / 64);
-  const dim3 grid(item_grid(a.B, a.G, a.norders, (nu + 1) / 2));
-  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_state_kernel<T, 128, REV>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((kda_ssm_state_kernel<T, 64, REV>), grid, dim3(512), 0, s, a);
+  const dim3 grid(item_grid(a.B, a.G, a.norders, (nu + 1) / 2)), block(512 / kNC<T>);
+  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_state_kernel<T, 128, REV>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((kda_ssm_state_kernel<T, 64, REV>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
+// (fp32 operands are whole: one variant)
+template <typename T, bool BWD, int TERMS>
+hipError_t run_out_terms(const PassArgs& a, hipStream_t s) {
+  const int nu = a.H / a.G * (a.dv / 64);
+  const dim3 grid(item_grid(a.B, a.G, a.nseg, (nu + 1) / 2)), block(512 / kNC<T>);
+  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_out_kernel<T, 128, BWD, TERMS>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((kda_ssm_out_kernel<T, 64, BWD, TERMS>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
 template <typename T, bool BWD>
 hipError_t run_out(const PassArgs& a, hipStream_t s) {
-  const int nu = a.H / a.G * (a.dv / 64);
-  const dim3 grid(item_grid(a.B, a.G, a.nseg, (nu + 1) / 2));
-  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_out_kernel<T, 128, BWD>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((kda_ssm_out_kernel<T, 64, BWD>), grid, dim3(512), 0, s, a);
-  return hipGetLastError();
+  if constexpr (sizeof(T) == 2) {
+    if (!a.end) return run_out_terms<T, BWD, 2>(a, s);
+  }
+  return run_out_terms<T, BWD, 3>(a, s);
 }
 
 template <typename T, bool REV>
@@ -1332,7 +1487,7 @@ hipError_t run_group(const PassArgs& a, const void* qin, Str3 qrs, float* rs, fl
   const int hg = 128 / a.dv, np = (a.H / a.G + hg - 1) / hg;
   const dim3 grid(item_grid(a.B, a.G, a.nseg, np));
 #define KDA_GROUP(DV, DK)                                                                                            \
-  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK, REV>), grid, dim3(4 * DK), 0, s, a, qin, qrs, rs, parts)
+  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK, REV>), grid, dim3(4 * DK / kNC<T>), 0, s, a, qin, qrs, rs, parts)
   if (a.dv == 64 && a.dk == 64) KDA_GROUP(64, 64);
   else if (a.dv == 64) KDA_GROUP(64, 128);
   else if (a.dk == 64) KDA_GROUP(128, 64);
@@ -1346,11 +1501,13 @@ hipError_t run_group(const PassArgs& a, const void* qin, Str3 qrs, float* rs, fl
   return hipGetLastError();
 }
 
-hipError_t run_merge(const float* start, float* slots, const float* dec, const PassArgs& a, int n, hipStream_t s) {
+// decayed: the last state owes the decay of token 0 too
+template <typename T>
+hipError_t run_merge(const float* start, float* slots, const PassArgs& a, int n, float* out, bool decayed, hipStream_t s) {
   const long long BH = (long long)a.B * a.H;
   const int elems = a.dk * a.dv;
-  hipLaunchKernelGGL(kda_ssm_merge_kernel, dim3((unsigned)((BH * elems / 4 + 255) / 256)), dim3(256), 0, s, start, slots, dec,
-                     BH, elems, n);
+  hipLaunchKernelGGL((kda_ssm_merge_kernel<T>), dim3((unsigned)((BH * elems / 4 + 255) / 256)), dim3(256), 0, s, start, slots,
+                     a.dec, BH, elems, n, out, decayed ? static_cast<const T*>(a.la) : nullptr, a.ls, a.H);
   return hipGetLastError();
 }
 
@@ -1367,17 +1524,20 @@ hipError_t prefill(const SsmArgs& x, hipStream_t s) {
   a.qs = x.qs; a.ks = x.ks; a.vs = x.vs; a.ls = x.ls; a.bs = x.bs; a.os = x.os;
   a.B = x.B; a.H = x.H; a.G = x.G; a.T = x.T; a.dk = x.dk; a.dv = x.dv;
   a.nseg = x.nseg; a.seg_chunks = x.seg_chunks;
-  a.start = x.S0;
-  if (x.nseg > 1) {
-    float* slots = x.ws;
-    a.dec = slots + (size_t)x.nseg * x.B * x.H * x.dk * x.dv;
-    a.end = slots;
-    a.norders = x.nseg - 1;  // the last segment's end state is not needed
-    SSM_TRY((run_state<T, false>(a, s)));
-    SSM_TRY(run_merge(x.S0, slots, a.dec, a, x.nseg - 1, s));
-    a.start = slots;
+  if (x.nseg == 1) {
+    a.start = x.S0;
+    a.end = x.S_T;
+    return run_out<T, false>(a, s);
   }
-  a.end = x.S_T;
+  // every segment's end state from zero, the states at the cuts and S_T from those,
+  // then the outputs, whose own states need not be results
+  a.dec = x.ws + (size_t)(x.nseg + 1) * x.B * x.H * x.dk * x.dv;
+  a.end = x.ws;
+  a.norders = x.nseg;
+  SSM_TRY((run_state<T, false>(a, s)));
+  SSM_TRY(run_merge<T>(x.S0, x.ws, a, x.nseg, x.S_T, false, s));
+  a.start = x.ws;
+  a.end = nullptr;
   return run_out<T, false>(a, s);
 }
 
@@ -1394,7 +1554,7 @@ BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg) {
   };
   const size_t st = (size_t)B * H * dk * dv, bht = (size_t)B * H * T, cpu = dv / 64;
   w.slots_f = take((nseg + 1) * st);
-  w.slots_r = take((size_t)nseg * st);
+  w.slots_r = take((nseg + 1) * st);
   w.dec = take((size_t)nseg * B * H);
   w.c = take(bht * cpu);
   w.r = take(bht * cpu);
@@ -1423,18 +1583,19 @@ hipError_t backward(const SsmArgs& x, hipStream_t s) {
   a.end = ws + w.slots_f;
   a.norders = x.nseg;
   SSM_TRY((run_state<T, false>(a, s)));
-  SSM_TRY(run_merge(x.S0, ws + w.slots_f, a.dec, a, x.nseg, s));
+  SSM_TRY(run_merge<T>(x.S0, ws + w.slots_f, a, x.nseg, nullptr, false, s));
   a.K = x.q; a.ks = x.qs; a.V = x.dO; a.vs = x.dos;
   a.end = ws + w.slots_r;
-  a.norders = x.nseg - 1;  // (dS0 comes from the outputs' pass)
+  // (of one segment dS0 comes from the outputs' pass)
+  a.norders = x.nseg == 1 ? 0 : x.dS0 ? x.nseg : x.nseg - 1;
   if (a.norders > 0) SSM_TRY((run_state<T, true>(a, s)));
-  SSM_TRY(run_merge(x.dS_T, ws + w.slots_r, a.dec, a, x.nseg - 1, s));
+  SSM_TRY(run_merge<T>(x.dS_T, ws + w.slots_r, a, a.norders, x.nseg > 1 ? x.dS0 : nullptr, true, s));
   // dv, dbeta's and dlog_alpha's sums, dS0
   a.Q = x.k; a.qs = x.ks;
   a.V2 = x.v; a.v2s = x.vs;
   a.o = x.dvv; a.os = x.dvs;
   a.start = ws + w.slots_r;
-  a.end = x.dS0;
+  a.end = x.nseg == 1 ? x.dS0 : nullptr;
   SSM_TRY((run_out<T, true>(a, s)));
   // dq
   a.Q = x.dO; a.qs = x.dos; a.K = x.v; a.ks = x.vs; a.V = x.k; a.vs = x.ks;
@@ -1476,7 +1637,7 @@ int ssm_plan(int B, int H, int G, int T, int dk, int dv, bool bf16_io, bool back
 
 size_t ssm_ws_floats(int B, int H, int dk, int dv, int nseg) {
   if (nseg <= 1) return 0;
-  return (size_t)nseg * B * H * dk * dv + ((size_t)nseg * B * H + 3) / 4 * 4;
+  return (size_t)(nseg + 1) * B * H * dk * dv + ((size_t)nseg * B * H + 3) / 4 * 4;
 }
 
 size_t ssm_backward_ws_floats(int B, int H, int G, int T, int dk, int dv, int nseg) {
