@@ -365,25 +365,37 @@ __device__ __forceinline__ float row16_sum(float x) {
 __device__ __forceinline__ int tile_i(int t) { return (int)((0x0fe9e4u >> (2 * t)) & 3u); }  // 0 1 2 3 1 2 2 3 3 3
 __device__ __forceinline__ int tile_j(int t) { return (int)((0x0910e4u >> (2 * t)) & 3u); }  // 0 1 2 3 0 0 1 0 1 2
 
-// decayed, weighted scores of a transposed tile: rows j = 16J + 4g + e, column i = 16I + r16
+// Decayed, weighted scores of a transposed tile: rows j = 16J + 4g + e, column
+// i = 16I + r16; on the diagonal and below it.
 template <bool KAPPA>
-__device__ __forceinline__ f32x4 weigh(f32x4 acc, const float* v, int I, int J, int g, int r16) {
+__device__ __forceinline__ f32x4 weigh_diag(f32x4 acc, const float* v, int I, int g, int r16) {
   f32x4 m;
-  if (I == J) {
-    const float pi = v[V_PB + 16 * I + r16];
-    const f32x4 pj = *reinterpret_cast<const f32x4*>(v + V_PB + 16 * J + 4 * g);
-    f32x4 kp = {1.f, 1.f, 1.f, 1.f};
-    if (KAPPA) kp = *reinterpret_cast<const f32x4*>(v + V_KP + 16 * J + 4 * g);
+  const float pi = v[V_PB + 16 * I + r16];
+  const f32x4 pj = *reinterpret_cast<const f32x4*>(v + V_PB + 16 * I + 4 * g);
+  f32x4 kp = {1.f, 1.f, 1.f, 1.f};
+  if (KAPPA) kp = *reinterpret_cast<const f32x4*>(v + V_KP + 16 * I + 4 * g);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = 4 * g + e <= r16 ? acc[e] * (KAPPA ? ex2(pi - pj[e]) * kp[e] : ex2(pi - pj[e])) : 0.f;
-  } else {
-    float c = v[V_U + 16 * I + r16];
-    for (int b = J + 1; b < I; ++b) c *= v[V_ET + b];
-    const f32x4 wj = *reinterpret_cast<const f32x4*>(v + V_W + 16 * J + 4 * g);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = acc[e] * (c * wj[e]);
-  }
+  for (int e = 0; e < 4; ++e) m[e] = 4 * g + e <= r16 ? acc[e] * (KAPPA ? ex2(pi - pj[e]) * kp[e] : ex2(pi - pj[e])) : 0.f;
   return m;
+}
+__device__ __forceinline__ f32x4 weigh_below(f32x4 acc, const float* v, int I, int J, int g, int r16) {
+  const f32x4 et = *reinterpret_cast<const f32x4*>(v + V_ET);
+  const f32x4 wj = *reinterpret_cast<const f32x4*>(v + V_W + 16 * J + 4 * g);
+  // the whole blocks between: 1 and 2 of (3, 0), 1 of (2, 0), 2 of (3, 1)
+  const float c = v[V_U + 16 * I + r16] * (I - J > 1 && J == 0 ? et[1] : 1.f) * (I - J > 1 && I == 3 ? et[2] : 1.f);
+  f32x4 m;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m[e] = acc[e] * (c * wj[e]);
+  return m;
+}
+
+// The ten score tiles dealt to NW waves, tile n of a wave; eight waves: the two left
+// over go to waves 4 and 5.  At most four waves take the diagonal's first.
+template <int NW> constexpr int kTiles = NW == 8 ? 2 : (10 + NW - 1) / NW;
+template <int NW>
+__device__ __forceinline__ int wave_tile(int wave, int n) {
+  if (NW == 8) return n == 0 ? wave : (wave < 4 ? 10 : wave + 4);
+  return wave + n * NW;
 }
 
 // -------------------------------------------------------- state and results
@@ -573,8 +585,8 @@ __device__ __forceinline__ void gather(const f32x4 (&y)[NC][NI], int I, float (&
     for (int e = 0; e < 4; ++e) x[4 * p + e] = y[p][I][e];
 }
 
-// sum over channels of A row tile J by B row tile I (both [64][COLS]): all operands
-// are read before the first product, so that one LDS latency is exposed and not one each
+// sum over channels of A row tile J by B row tile I (both [64][COLS]), the operands
+// read before the first product
 template <typename T, int COLS>
 __device__ __forceinline__ f32x4 score_tile(const char* at, const char* bt, uint32_t off, int I, int J) {
   typedef Tile<T, COLS> L;
@@ -589,6 +601,70 @@ __device__ __forceinline__ f32x4 score_tile(const char* at, const char* bt, uint
 #pragma unroll
   for (int m = 0; m < COLS / 32; ++m) acc = Op<T>::mma(acc, x[m], y[m]);
   return acc;
+}
+// acc[n] = the same for a
+// wave's tiles; the operands of PRE tiles are read before the first product, so that
+// one LDS latency is exposed and not one each (fp32: its products are long, none).
+template <typename T, int COLS, int NW, int PRE>
+__device__ __forceinline__ void score_tiles(f32x4 (&acc)[kTiles<NW>], const char* at, const char* bt, uint32_t off, int wave) {
+  typedef Tile<T, COLS> L;
+  constexpr int N = kTiles<NW>, ST = PRE > 0 ? PRE : 1;
+#pragma unroll
+  for (int n0 = 0; n0 < N; n0 += ST) {
+    if constexpr (PRE == 0) {
+      const int t = wave_tile<NW>(wave, n0);
+      if (t >= 10) continue;
+      acc[n0] = zero4();
+#pragma unroll
+      for (int m = 0; m < COLS / 32; ++m) acc[n0] = Op<T>::mma(acc[n0], L::row(at, off, tile_j(t), m), L::row(bt, off, tile_i(t), m));
+      continue;
+    }
+    typename Op<T>::F x[ST][COLS / 32], y[ST][COLS / 32];
+#pragma unroll
+    for (int k = 0; k < ST; ++k) {
+      const int t = wave_tile<NW>(wave, n0 + k);
+      if (n0 + k >= N || t >= 10) continue;
+#pragma unroll
+      for (int m = 0; m < COLS / 32; ++m) {
+        x[k][m] = L::row(at, off, tile_j(t), m);
+        y[k][m] = L::row(bt, off, tile_i(t), m);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < ST; ++k) {
+      const int t = wave_tile<NW>(wave, n0 + k);
+      if (n0 + k >= N || t >= 10) continue;
+      f32x4 s = zero4();
+#pragma unroll
+      for (int m = 0; m < COLS / 32; ++m) s = Op<T>::mma(s, x[k][m], y[k][m]);
+      acc[n0 + k] = s;
+    }
+  }
+}
+// f(n, I, J, diagonal) for each of a wave's tiles, the last argument an
+// integral_constant where it is known
+template <int NW, typename F>
+__device__ __forceinline__ void each_tile(int wave, F f) {
+  auto one = [&](auto n) {
+    const int t = wave_tile<NW>(wave, n.value);
+    if (t >= 10) return;
+    if constexpr (NW == 8) {
+      if (n.value == 0 && wave < 4) f(n.value, t, t, std::true_type());
+      else f(n.value, tile_i(t), tile_j(t), std::false_type());
+    } else if constexpr (n.value * NW < 4) {
+      f(n.value, t, t, std::true_type());
+    } else {
+      f(n.value, tile_i(t), tile_j(t), std::false_type());
+    }
+  };
+  one(std::integral_constant<int, 0>());
+  one(std::integral_constant<int, 1>());
+  if constexpr (kTiles<NW> > 2) one(std::integral_constant<int, 2>());
+  if constexpr (kTiles<NW> > 3) {
+    one(std::integral_constant<int, 3>());
+    one(std::integral_constant<int, 4>());
+  }
 }
 
 // A wave's row tiles I0 .. of results, row 16 I + i at p + I * d + off, rows below n.
@@ -880,11 +956,22 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
   const uint32_t ofq = fq.template lane_off<BWD>(a.qs.t, tid), ofk = fk.template lane_off<BWD>(a.ks.t, tid);
   const uint32_t ofv = fv[0].template lane_off<BWD>(a.vs.t, tid), ofw = BWD ? fw[0].template lane_off<BWD>(a.v2s.t, tid) : 0u;
   T fx = T(0.f), fb = T(0.f);
-  auto fetch = [&](int step) {
+  // the next chunk's loads, in three parts between this one's products: together they
+  // held the issuing wave up for 2300 of a chunk's 13500 cycles
+  auto fetch_q = [&](int step) {
+    if (step >= c1 - c0) return;
+    const int c = BWD ? c1 - 1 - step : c0 + step;
+    fq.template get<BWD>(Q, a.qs.t, c * CH, min(CH, len - c * CH), ofq, tid);
+  };
+  auto fetch_k = [&](int step) {
+    if (step >= c1 - c0) return;
+    const int c = BWD ? c1 - 1 - step : c0 + step;
+    fk.template get<BWD>(K, a.ks.t, c * CH, min(CH, len - c * CH), ofk, tid);
+  };
+  auto fetch_v = [&](int step) {
+    if (step >= c1 - c0) return;
     const int c = BWD ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, len - tok0);
-    fq.template get<BWD>(Q, a.qs.t, tok0, n, ofq, tid);
-    fk.template get<BWD>(K, a.ks.t, tok0, n, ofk, tid);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       fv[u].template get<BWD>(V[u], a.vs.t, tok0, n, ofv, tid);
@@ -904,7 +991,9 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
       fill_vec<KAPPA>(vecs + ((step % NB) * 2 + fu) * VS, l, to_f32(fx), BWD ? 1.f : to_f32(fb), 1.f, to_f32(fb));
   };
   fetch_gates(0);
-  if (c0 < c1) fetch(0);
+  fetch_q(0);
+  fetch_k(0);
+  fetch_v(0);
   if (NB == 2) {
     fill(0);
     fetch_gates(1);
@@ -924,22 +1013,45 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
       fill(step);
       fetch_gates(step + 1);
     }
-    if (step + 1 < c1 - c0) fetch(step + 1);
+    fetch_q(step + 1);
     sync_lds();
 
     const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
     const uint32_t krow = KT::row_off(g, i);
-    // scores: the ten tiles dealt to the waves (of eight waves, two to waves 4 and 5)
-    for (int t = wave; t < 10; t += NWV == 8 && wave < 4 ? 16 : 4) {
-      const int I = tile_i(t), J = tile_j(t);
-      const f32x4 acc = score_tile<T, DK>(sk, sq, krow, I, J);
+    if constexpr (!BWD) {
+      f32x4 acc[kTiles<NWV>];
+      score_tiles<T, DK, NWV, sizeof(T) == 2 ? 2 : 0>(acc, sk, sq, krow, wave);
+      fetch_k(step + 1);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const float* v = vec + u * VS;
-        f32x4 mm = weigh<KAPPA>(acc, v, I, J, g, i);
-        if constexpr (BWD) {
-          float* rd = red + u * RED + 16 * SC::tile(I, J);
+        each_tile<NWV>(wave, [&](int nt, int I, int J, auto diag) {
+          f32x4 mm;
+          if constexpr (decltype(diag)::value) {
+            mm = weigh_diag<KAPPA>(acc[nt], v, I, g, i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mm[e] += 4 * g + e == i ? skip[u] : 0.f;
+          } else {
+            mm = weigh_below(acc[nt], v, I, J, g, i);
+          }
+          SC::put(sm + u * SC::BYTES, I, J, l, mm);
+        });
+      }
+    } else {
+      fetch_k(step + 1);
+      // (tile by tile: two products' worth of operands and sums fill the registers)
+#pragma unroll 1
+      for (int n = 0; n < kTiles<NWV>; ++n) {
+        const int t = wave_tile<NWV>(wave, n);
+        if (t >= 10) break;
+        const int I = tile_i(t), J = tile_j(t);
+        const f32x4 acc = score_tile<T, DK>(sk, sq, krow, I, J);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float* v = vec + u * VS;
+          const f32x4 mm = I == J ? weigh_diag<KAPPA>(acc, v, I, g, i) : weigh_below(acc, v, I, J, g, i);
           const f32x4 dd = score_tile<T, 64>(sv + u * VT::BYTES, sv2 + u * VT::BYTES, VT::row_off(g, i), I, J);
+          float* rd = red + u * RED + 16 * SC::tile(I, J);
           const float bi = v[V_RH + 16 * I + i];
           float cs = 0.f, rs[4];
 #pragma unroll
@@ -954,11 +1066,8 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
 #pragma unroll
           for (int e = 0; e < 4; ++e) rs[e] = row16_sum(rs[e]);
           if (i == 0) *reinterpret_cast<f32x4*>(rd + 160 + 4 * g) = f32x4{rs[0], rs[1], rs[2], rs[3]};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mm[e] += I == J && 4 * g + e == i ? skip[u] : 0.f;
+          SC::put(sm + u * SC::BYTES, I, J, l, mm);
         }
-        SC::put(sm + u * SC::BYTES, I, J, l, mm);
       }
     }
     if (NB == 2) {
@@ -976,6 +1085,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[p][I][e] *= s;
     }
+    fetch_v(step + 1);
     sync_lds();
     if constexpr (BWD) {
       // the state's part of c, z.v before the chunk's own part joins z, one sum per
@@ -1133,15 +1243,23 @@ __global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_gr
   const uint32_t ofv = fv.template lane_off<REV>(a.vs.t, tid), ofq = fq[0].template lane_off<REV>(a.qs.t, tid),
                  ofk = fk[0].template lane_off<REV>(a.ks.t, tid);
   T fx = T(0.f), fb = T(0.f);
-  auto fetch = [&](int step) {
+  // (in three parts, as above)
+  auto fetch_q = [&](int step) {
+    if (step >= c1 - c0) return;
     const int c = REV ? c1 - 1 - step : c0 + step;
-    const int tok0 = c * CH, n = min(CH, a.T - tok0);
-    fv.template get<REV>(V, a.vs.t, tok0, n, ofv, tid);
 #pragma unroll
-    for (int h = 0; h < HG; ++h) {
-      fq[h].template get<REV>(Q[h], a.qs.t, tok0, n, ofq, tid);
-      fk[h].template get<REV>(K[h], a.ks.t, tok0, n, ofk, tid);
-    }
+    for (int h = 0; h < HG; ++h) fq[h].template get<REV>(Q[h], a.qs.t, c * CH, min(CH, a.T - c * CH), ofq, tid);
+  };
+  auto fetch_k = [&](int step) {
+    if (step >= c1 - c0) return;
+    const int c = REV ? c1 - 1 - step : c0 + step;
+#pragma unroll
+    for (int h = 0; h < HG; ++h) fk[h].template get<REV>(K[h], a.ks.t, c * CH, min(CH, a.T - c * CH), ofk, tid);
+  };
+  auto fetch_v = [&](int step) {
+    if (step >= c1 - c0) return;
+    const int c = REV ? c1 - 1 - step : c0 + step;
+    fv.template get<REV>(V, a.vs.t, c * CH, min(CH, a.T - c * CH), ofv, tid);
   };
   auto fetch_gates = [&](int step) {
     if (!filler || step >= c1 - c0) return;
@@ -1156,7 +1274,9 @@ __global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_gr
       fill_vec<KAPPA>(vecs + ((step & 1) * HG + fh) * VS, l, to_f32(fx), REV ? 1.f : to_f32(fb), REV ? to_f32(fb) : 1.f, to_f32(fb));
   };
   fetch_gates(0);
-  if (c0 < c1) fetch(0);
+  fetch_q(0);
+  fetch_k(0);
+  fetch_v(0);
   fill(0);
   fetch_gates(1);
   for (int step = 0; step < c1 - c0; ++step) {
@@ -1181,25 +1301,31 @@ __global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_gr
         if (p < n) xq[I] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(W + (tok0 + 16 * I) * qrs.t + 16 * NC * wave) + oxq);
       }
     }
-    if (step + 1 < c1 - c0) fetch(step + 1);
+    fetch_q(step + 1);
     sync_lds();
 
     const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
     const uint32_t qrow = QT::row_off(g, i);
-    for (int t = wave; t < 10; t += NW == 8 ? (wave < 4 ? 16 : 4) : NW) {
-      const int I = tile_i(t), J = tile_j(t);
 #pragma unroll
-      for (int h = 0; h < HG; ++h) {
-        const f32x4 acc = score_tile<T, DV>(sk + h * QT::BYTES, sq + h * QT::BYTES, qrow, I, J);
-        const float* v = vec + h * VS;
-        f32x4 mm = weigh<KAPPA>(acc, v, I, J, g, i);
-        if (REV && I == J) {
-          const float rho = v[V_RH + 16 * I + i];
+    for (int h = 0; h < HG; ++h) {
+      f32x4 acc[kTiles<NW>];
+      score_tiles<T, DV, NW, sizeof(T) == 2 ? 2 : 0>(acc, sk + h * QT::BYTES, sq + h * QT::BYTES, qrow, wave);
+      const float* v = vec + h * VS;
+      if (h == 0) fetch_k(step + 1);
+      each_tile<NW>(wave, [&](int nt, int I, int J, auto diag) {
+        f32x4 mm;
+        if constexpr (decltype(diag)::value) {
+          mm = weigh_diag<KAPPA>(acc[nt], v, I, g, i);
+          if constexpr (REV) {
+            const float rho = v[V_RH + 16 * I + i];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mm[e] *= rho;
+            for (int e = 0; e < 4; ++e) mm[e] *= rho;
+          }
+        } else {
+          mm = weigh_below(acc[nt], v, I, J, g, i);
         }
         SC::put(sm + h * SC::BYTES, I, J, l, mm);
-      }
+      });
     }
     fill(step + 1);
     fetch_gates(step + 2);
@@ -1264,6 +1390,7 @@ __global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_gr
       }
     };
     some(std::integral_constant<int, 0>());
+    fetch_v(step + 1);
     if constexpr (NI == 2) {
 #pragma unroll
       for (int h = 0; h < HG; ++h) S[h].renew();
