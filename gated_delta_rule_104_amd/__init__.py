@@ -500,30 +500,40 @@ def prefill_backward(q, k, v, log_alpha, beta, S0=None, dO=None, dS_T=None, work
 
 
 # ------------------------------------------------------- companion operators
-def _here(t: torch.Tensor, name: str) -> None:
-    """The call runs on the current device's current stream."""
+# (These calls take microseconds: what is right is checked in one expression, and
+# only what is wrong is looked at again to say why.)
+def _device(t: torch.Tensor, name: str) -> torch.device:
+    """The current device, on whose current stream the call runs; t has to be there."""
     if not t.is_cuda:
         raise KdaError(f"{name} must be a device tensor")
     if t.device.index != torch.cuda.current_device():
         raise KdaError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
 
 
-def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
-    _here(t, name)
+def _wrong(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: torch.device) -> None:
+    if not t.is_cuda:
+        raise KdaError(f"{name} must be a device tensor")
+    if t.device != dev:
+        raise KdaError(f"{name} is on {t.device}, expected {dev}")
     _io(t, name, dtype, shape)
 
 
-def _view(t: torch.Tensor, name: str, dtype: torch.dtype, shape, rows: bool = True) -> _Strides:
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: torch.device) -> None:
+    if t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _wrong(t, name, dtype, shape, dev)
+
+
+def _view(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: torch.device, rows: bool = True) -> _Strides:
     """A [B, H, T] or (rows) [B, H, T, d] tensor with any strides but a contiguous last
     dimension of rows; the library checks their alignment."""
-    _here(t, name)
-    if t.dtype != dtype:
-        raise KdaError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise KdaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if rows and t.shape[-1] > 1 and t.stride(-1) != 1:
+    st = t.stride()
+    if t.device != dev or t.dtype != dtype or t.shape != shape:
+        _wrong(t, name, dtype, shape, dev)
+        raise KdaError(f"{name} does not fit")
+    if rows and st[-1] != 1 and shape[-1] > 1:
         raise KdaError(f"{name} must have contiguous rows")
-    return _Strides(*t.stride()[:3])
+    return _Strides(*st[:3])
 
 
 def _new_like(t: torch.Tensor, dtype=None) -> torch.Tensor:
@@ -534,7 +544,8 @@ def _new_like(t: torch.Tensor, dtype=None) -> torch.Tensor:
 def _scratch(workspace, need: int, device) -> torch.Tensor:
     if workspace is None:
         return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    _here(workspace, "workspace")
+    if workspace.device != device:
+        raise KdaError(f"workspace is on {workspace.device}, expected {device}")
     if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
         raise KdaError(f"workspace must be a contiguous device tensor of at least {need} bytes")
     return workspace
@@ -557,14 +568,14 @@ def _act(activation) -> int:
     return _ACT[activation]
 
 
-def _conv_args(x, weight, bias, state, B, H, d):
+def _conv_args(x, weight, bias, state, B, H, d, dev):
     _rank(weight, "weight", 3)
     K = weight.shape[2]
-    _dense(weight, "weight", x.dtype, (H, d, K))
+    _dense(weight, "weight", x.dtype, (H, d, K), dev)
     if bias is not None:
-        _dense(bias, "bias", x.dtype, (H, d))
+        _dense(bias, "bias", x.dtype, (H, d), dev)
     if state is not None:
-        _dense(state, "state", x.dtype, (B, H, K - 1, d))
+        _dense(state, "state", x.dtype, (B, H, K - 1, d), dev)
     return K
 
 
@@ -576,17 +587,17 @@ def conv_prefill(x, weight, bias=None, state=None, activation="silu", lens=None,
     the sequence."""
     _rank(x, "x", 4)
     B, H, T, d = x.shape
-    dt = _dtype(x)
-    xs = _view(x, "x", x.dtype, (B, H, T, d))
-    K = _conv_args(x, weight, bias, state, B, H, d)
+    dt, dev = _dtype(x), _device(x, "x")
+    xs = _view(x, "x", x.dtype, (B, H, T, d), dev)
+    K = _conv_args(x, weight, bias, state, B, H, d, dev)
     if lens is not None:
-        _dense(lens, "lens", torch.int32, (B,))
+        _dense(lens, "lens", torch.int32, (B,), dev)
     if o is None:
         o = torch.empty(B, H, T, d, dtype=x.dtype, device=x.device)
-    os_ = _view(o, "o", x.dtype, (B, H, T, d))
+    os_ = _view(o, "o", x.dtype, (B, H, T, d), dev)
     if state_out is None:
         state_out = torch.empty(B, H, K - 1, d, dtype=x.dtype, device=x.device)
-    _dense(state_out, "state_out", x.dtype, (B, H, K - 1, d))
+    _dense(state_out, "state_out", x.dtype, (B, H, K - 1, d), dev)
     rc = load().kda_conv_prefill(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state), _ptr(lens), _ptr(o), os_,
                                  _ptr(state_out), B, H, T, d, K, _act(activation), dt, _stream())
     _check(rc, "kda_conv_prefill")
@@ -598,14 +609,14 @@ def conv_step(x, state, weight, bias=None, activation="silu", o=None) -> torch.T
     place.  Returns o [N,H,d]."""
     _rank(x, "x", 3)
     N, H, d = x.shape
-    dt = _dtype(x)
-    xs = _view(x, "x", x.dtype, (N, H, d))
-    K = _conv_args(x, weight, bias, state, N, H, d)
+    dt, dev = _dtype(x), _device(x, "x")
+    xs = _view(x, "x", x.dtype, (N, H, d), dev)
+    K = _conv_args(x, weight, bias, state, N, H, d, dev)
     if state is None:
         raise KdaError("state is required")
     if o is None:
         o = torch.empty(N, H, d, dtype=x.dtype, device=x.device)
-    os_ = _view(o, "o", x.dtype, (N, H, d))
+    os_ = _view(o, "o", x.dtype, (N, H, d), dev)
     rc = load().kda_conv_step(_ptr(x), xs, _ptr(state), _ptr(weight), _ptr(bias), _ptr(o), os_, N, H, d, K,
                               _act(activation), dt, _stream())
     _check(rc, "kda_conv_step")
@@ -617,12 +628,12 @@ def conv_backward(x, weight, bias, state, dO, dstate_out=None, activation="silu"
     where bias and state were given, in x's dtype."""
     _rank(x, "x", 4)
     B, H, T, d = x.shape
-    dt = _dtype(x)
-    xs = _view(x, "x", x.dtype, (B, H, T, d))
-    K = _conv_args(x, weight, bias, state, B, H, d)
-    dos = _view(dO, "dO", x.dtype, (B, H, T, d))
+    dt, dev = _dtype(x), _device(x, "x")
+    xs = _view(x, "x", x.dtype, (B, H, T, d), dev)
+    K = _conv_args(x, weight, bias, state, B, H, d, dev)
+    dos = _view(dO, "dO", x.dtype, (B, H, T, d), dev)
     if dstate_out is not None:
-        _dense(dstate_out, "dstate_out", x.dtype, (B, H, K - 1, d))
+        _dense(dstate_out, "dstate_out", x.dtype, (B, H, K - 1, d), dev)
     out = dict(dx=_new_like(x), dweight=_new_like(weight))
     if bias is not None:
         out["dbias"] = _new_like(bias)
@@ -632,7 +643,7 @@ def conv_backward(x, weight, bias, state, dO, dstate_out=None, activation="silu"
     need = int(lib.kda_conv_backward_workspace_bytes(B, H, T, d, K, dt))
     workspace = _scratch(workspace, need, x.device)
     rc = lib.kda_conv_backward(_ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(state), _ptr(dO), dos, _ptr(dstate_out),
-                               _ptr(out["dx"]), _view(out["dx"], "dx", x.dtype, (B, H, T, d)), _ptr(out["dweight"]),
+                               _ptr(out["dx"]), _Strides(*out["dx"].stride()[:3]), _ptr(out["dweight"]),
                                _ptr(out.get("dbias")), _ptr(out.get("dstate")), B, H, T, d, K, _act(activation), dt,
                                _ptr(workspace), workspace.numel() * workspace.element_size(), _stream())
     _check(rc, "kda_conv_backward")
@@ -643,17 +654,16 @@ def _ssm_args(q, k, v, log_alpha, beta, D, S0):
     _rank(k, "k", 4)
     _rank(v, "v", 4)
     (B, G, T, dk), (H, dv) = k.shape, (v.shape[1], v.shape[3])
-    dt = v.dtype
-    _dtype(v)
-    st = _SsmStrides(q=_view(q, "q", dt, (B, G, T, dk)), k=_view(k, "k", dt, (B, G, T, dk)),
-                     v=_view(v, "v", dt, (B, H, T, dv)),
-                     log_alpha=_view(log_alpha, "log_alpha", dt, (B, H, T), rows=False),
-                     beta=_view(beta, "beta", dt, (B, H, T), rows=False))
+    dt, dev = v.dtype, _device(v, "v")
+    st = _SsmStrides(_view(q, "q", dt, (B, G, T, dk), dev), _view(k, "k", dt, (B, G, T, dk), dev),
+                     _view(v, "v", dt, (B, H, T, dv), dev),
+                     _view(log_alpha, "log_alpha", dt, (B, H, T), dev, rows=False),
+                     _view(beta, "beta", dt, (B, H, T), dev, rows=False))
     if D is not None:
-        _dense(D, "D", dt, (H,))
+        _dense(D, "D", dt, (H,), dev)
     if S0 is not None:
-        _dense(S0, "S0", torch.float32, (B, H, dk, dv))
-    return (B, H, G, T, dk, dv), st
+        _dense(S0, "S0", torch.float32, (B, H, dk, dv), dev)
+    return (B, H, G, T, dk, dv), st, dev
 
 
 def ssm_prefill_workspace_bytes(B: int, H: int, G: int, T: int, dk: int, dv: int, dtype: torch.dtype) -> int:
@@ -670,16 +680,16 @@ def ssm_prefill(q, k, v, log_alpha, beta, D=None, S0=None, lens=None, o=None, S_
     contiguous), D [H] or None, S0 [B,H,dk,dv] fp32 or None, lens [B] int32 or None.  Returns o (in
     v's memory order unless given, rows behind lens not written) and S_T fp32.  workspace: "auto",
     None (each sequence in one piece) or a device uint8 tensor."""
-    (B, H, G, T, dk, dv), st = _ssm_args(q, k, v, log_alpha, beta, D, S0)
     dt = _dtype(v)
+    (B, H, G, T, dk, dv), st, dev = _ssm_args(q, k, v, log_alpha, beta, D, S0)
     if lens is not None:
-        _dense(lens, "lens", torch.int32, (B,))
+        _dense(lens, "lens", torch.int32, (B,), dev)
     if o is None:
         o = _new_like(v)
-    st.o = _view(o, "o", v.dtype, (B, H, T, dv))
+    st.o = _view(o, "o", v.dtype, (B, H, T, dv), dev)
     if S_T is None:
         S_T = torch.empty(B, H, dk, dv, dtype=torch.float32, device=v.device)
-    _dense(S_T, "S_T", torch.float32, (B, H, dk, dv))
+    _dense(S_T, "S_T", torch.float32, (B, H, dk, dv), dev)
     lib = load()
     if isinstance(workspace, str):
         need = int(lib.kda_ssm_prefill_workspace_bytes(B, H, G, T, dk, dv, dt))
@@ -699,16 +709,17 @@ def ssm_step(q, k, v, log_alpha, beta, S, D=None, o=None) -> torch.Tensor:
     _rank(k, "k", 3)
     _rank(v, "v", 3)
     (N, G, dk), (H, dv) = k.shape, v.shape[1:]
-    dt = _dtype(v)
+    dt, dev = _dtype(v), _device(v, "v")
     for name, t, shp in (("q", q, (N, G, dk)), ("k", k, (N, G, dk)), ("v", v, (N, H, dv)),
                          ("log_alpha", log_alpha, (N, H)), ("beta", beta, (N, H))):
-        _dense(t, name, v.dtype, shp)
+        _dense(t, name, v.dtype, shp, dev)
     if D is not None:
-        _dense(D, "D", v.dtype, (H,))
-    _dense(S, "S", torch.float32, (N, H, dk, dv))
+        _dense(D, "D", v.dtype, (H,), dev)
+    _dense(S, "S", torch.float32, (N, H, dk, dv), dev)
     if o is None:
-        o = torch.empty(N, H, dv, dtype=v.dtype, device=v.device)
-    _dense(o, "o", v.dtype, (N, H, dv))
+        o = torch.empty(N, H, dv, dtype=v.dtype, device=dev)
+    else:
+        _dense(o, "o", v.dtype, (N, H, dv), dev)
     rc = load().kda_ssm_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(D), _ptr(S), _ptr(o),
                              N, H, G, dk, dv, dt, _stream())
     _check(rc, "kda_ssm_step")
@@ -719,14 +730,14 @@ def ssm_backward(q, k, v, log_alpha, beta, D=None, S0=None, dO=None, dS_T=None, 
     """Gradients of L = sum(dO * o) + sum(dS_T * S_T) of ssm_prefill (without lens).  Returns a dict:
     dq, dk (summed over a group's heads), dv, dlog_alpha, dbeta, and dD and dS0 (fp32) where D and S0
     were given."""
-    (B, H, G, T, dk, dv), st = _ssm_args(q, k, v, log_alpha, beta, D, S0)
     dt = _dtype(v)
+    (B, H, G, T, dk, dv), st, dev = _ssm_args(q, k, v, log_alpha, beta, D, S0)
     if dO is None:
         raise KdaError("dO is required")
     if dS_T is not None:
-        _dense(dS_T, "dS_T", torch.float32, (B, H, dk, dv))
+        _dense(dS_T, "dS_T", torch.float32, (B, H, dk, dv), dev)
     out = dict(dq=_new_like(q), dk=_new_like(k), dv=_new_like(v), dlog_alpha=_new_like(log_alpha), dbeta=_new_like(beta))
-    gst = _SsmGradStrides(dO=_view(dO, "dO", v.dtype, (B, H, T, dv)),
+    gst = _SsmGradStrides(dO=_view(dO, "dO", v.dtype, (B, H, T, dv), dev),
                           **{n: _Strides(*t.stride()[:3]) for n, t in out.items()})
     if D is not None:
         out["dD"] = _new_like(D)
@@ -760,22 +771,23 @@ def _cache_args(cache, scales, slots):
     if cache.dtype not in _CACHE:
         raise KdaError(f"cache has dtype {cache.dtype}, expected torch.int8 or torch.float8_e4m3fn")
     nslots, H, dk, dv = cache.shape
-    _dense(cache, "cache", cache.dtype, cache.shape)
-    _dense(scales, "scales", torch.uint8, (nslots, H, dk, dv // 32))
+    dev = _device(cache, "cache")
+    _dense(cache, "cache", cache.dtype, cache.shape, dev)
+    _dense(scales, "scales", torch.uint8, (nslots, H, dk, dv // 32), dev)
     _rank(slots, "slots", 1)
-    _dense(slots, "slots", torch.int32, slots.shape)
-    return nslots, H, dk, dv
+    _dense(slots, "slots", torch.int32, slots.shape, dev)
+    return nslots, H, dk, dv, dev
 
 
 def state_store(S, slots, cache, scales) -> None:
     """Quantise states S [..., H,dk,dv] fp32 into the entries slots [n] int32 of a state_cache
     (kda_state_store; S may be prefill_snap's S_snap with slots.numel() states).  Slots outside the
     cache are skipped; of entries that name the same slot the last one is stored."""
-    nslots, H, dk, dv = _cache_args(cache, scales, slots)
+    nslots, H, dk, dv, dev = _cache_args(cache, scales, slots)
     n = slots.numel()
     if S.dim() < 3 or tuple(S.shape[-3:]) != (H, dk, dv) or S.numel() != n * H * dk * dv:
         raise KdaError(f"S has shape {tuple(S.shape)}, expected {n} states of {(H, dk, dv)}")
-    _dense(S, "S", torch.float32, S.shape)
+    _dense(S, "S", torch.float32, S.shape, dev)
     rc = load().kda_state_store(_ptr(S), _ptr(slots), _ptr(cache), _ptr(scales), n, nslots, H, dk, dv,
                                 _CACHE[cache.dtype], _stream())
     _check(rc, "kda_state_store")
@@ -784,11 +796,11 @@ def state_store(S, slots, cache, scales) -> None:
 def state_load(cache, scales, slots, S=None) -> torch.Tensor:
     """States [n,H,dk,dv] fp32 of the entries slots [n] int32 of a state_cache (zeros for slots
     outside it)."""
-    nslots, H, dk, dv = _cache_args(cache, scales, slots)
+    nslots, H, dk, dv, dev = _cache_args(cache, scales, slots)
     n = slots.numel()
     if S is None:
         S = torch.empty(n, H, dk, dv, dtype=torch.float32, device=cache.device)
-    _dense(S, "S", torch.float32, (n, H, dk, dv))
+    _dense(S, "S", torch.float32, (n, H, dk, dv), dev)
     rc = load().kda_state_load(_ptr(cache), _ptr(scales), _ptr(slots), _ptr(S), n, nslots, H, dk, dv,
                                _CACHE[cache.dtype], _stream())
     _check(rc, "kda_state_load")

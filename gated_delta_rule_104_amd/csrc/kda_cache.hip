@@ -6,9 +6,9 @@
 // exact and only the rounding of each value to nearest even loses anything.  A
 // block with an infinity or NaN gets the byte 255 and reads back as NaN.
 //
-// Both directions are bound by HBM (5 bytes a value and 1/32 byte of scale).
-// Four neighbouring lanes own a block, 8 values each: the block's largest value
-// takes two quad moves, and a lane's 8 bytes are one store.
+// Both directions are bound by HBM (5 bytes a value and 1/32 byte of scale).  On the
+// way in four neighbouring lanes own a block, 8 values each: the block's largest
+// value takes two quad moves, and a lane's 8 bytes are one store.
 #include "kda_ops.hpp"
 
 namespace kda {
@@ -84,6 +84,8 @@ __global__ __launch_bounds__(256) void kda_state_store_kernel(const float* __res
   }
 }
 
+// A lane reads four values at a time and writes 16 bytes, so that a wave's store is 1
+// KiB of one run; four of them are in flight.
 template <bool E4M3>
 __global__ __launch_bounds__(256) void kda_state_load_kernel(const unsigned char* __restrict__ cache,
                                                              const unsigned char* __restrict__ scales,
@@ -96,35 +98,41 @@ __global__ __launch_bounds__(256) void kda_state_load_kernel(const unsigned char
   const bool have = slot >= 0 && slot < nslots;
   const size_t src = ((size_t)(have ? slot : 0) * H + h) * elems;
   float* dst = S + (size_t)ih * elems;
-  for (int e = (part * 256 + (int)threadIdx.x) * 8; e < elems; e += share * 2048) {
-    f32x4 lo = zero4(), hi = zero4();
-    if (have) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(cache + src + e);
-      const uint32_t sb = scales[(src + e) >> 5];
-      const float s = sb == 255u ? __builtin_nanf("") : __uint_as_float(sb << 23);
-      if constexpr (E4M3) {
-        typedef float v2 __attribute__((ext_vector_type(2)));
-        const v2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[0], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[0], true);
-        const v2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[1], false), d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[1], true);
-        lo = f32x4{a[0] * s, a[1] * s, b[0] * s, b[1] * s};
-        hi = f32x4{c[0] * s, c[1] * s, d[0] * s, d[1] * s};
-      } else {
+  constexpr int U = 4;
+  for (int e0 = part * (1024 * U) + (int)threadIdx.x * 4; e0 < elems; e0 += share * (1024 * U)) {
+    uint32_t w[U], sb[U];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          lo[c] = (float)(int)(signed char)(w[0] >> (8 * c)) * s;
-          hi[c] = (float)(int)(signed char)(w[1] >> (8 * c)) * s;
-        }
+    for (int u = 0; u < U; ++u) {
+      const int e = e0 + u * 1024;
+      w[u] = sb[u] = 0u;
+      if (have && e < elems) {
+        w[u] = *reinterpret_cast<const uint32_t*>(cache + src + e);
+        sb[u] = scales[(src + e) >> 5];
       }
     }
-    __builtin_nontemporal_store(lo, reinterpret_cast<f32x4*>(dst + e));
-    __builtin_nontemporal_store(hi, reinterpret_cast<f32x4*>(dst + e + 4));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = e0 + u * 1024;
+      if (e >= elems) break;
+      const float s = sb[u] == 255u ? __builtin_nanf("") : __uint_as_float(sb[u] << 23);
+      f32x4 x;
+      if constexpr (E4M3) {
+        typedef float v2 __attribute__((ext_vector_type(2)));
+        const v2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u], true);
+        x = f32x4{a[0] * s, a[1] * s, b[0] * s, b[1] * s};
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = (float)(int)(signed char)(w[u] >> (8 * c)) * s;
+      }
+      *reinterpret_cast<f32x4*>(dst + e) = x;
+    }
   }
 }
 
-// Blocks per (entry, head): one for every 2048 values while there are few states,
-// one in all where the states alone give the chip 2048 blocks.
-int state_share(long long nh, int elems) {
-  int share = (elems + 2047) / 2048;
+// Blocks per (entry, head): one for every per_block values while there are few
+// states, fewer where that would give more than 8192 blocks.
+int state_share(long long nh, int elems, int per_block) {
+  int share = (elems + per_block - 1) / per_block;
   while (share > 1 && nh * share > 8192) share = (share + 1) / 2;
   return share;
 }
@@ -134,7 +142,7 @@ int state_share(long long nh, int elems) {
 hipError_t launch_state_store(const float* S, const int* slots, void* cache, unsigned char* scales, int n, int nslots,
                               int H, int dk, int dv, bool e4m3, hipStream_t stream) {
   const long long nh = (long long)n * H;
-  const int elems = dk * dv, share = state_share(nh, elems);
+  const int elems = dk * dv, share = state_share(nh, elems, 2048);
   const dim3 grid((unsigned)(nh * share));
   unsigned char* c = static_cast<unsigned char*>(cache);
   if (e4m3)
@@ -147,7 +155,7 @@ hipError_t launch_state_store(const float* S, const int* slots, void* cache, uns
 hipError_t launch_state_load(const void* cache, const unsigned char* scales, const int* slots, float* S, int n,
                              int nslots, int H, int dk, int dv, bool e4m3, hipStream_t stream) {
   const long long nh = (long long)n * H;
-  const int elems = dk * dv, share = state_share(nh, elems);
+  const int elems = dk * dv, share = state_share(nh, elems, 4096);
   const dim3 grid((unsigned)(nh * share));
   const unsigned char* c = static_cast<const unsigned char*>(cache);
   if (e4m3)

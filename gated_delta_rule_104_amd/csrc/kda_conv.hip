@@ -70,7 +70,12 @@ struct Taps {
   }
 };
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// The hardware's exponential and reciprocal, each within a unit in the last place of
+// fp32 (the exponent's product adds |x| 2^-24): with the correctly rounded division
+// and expf the four 8K prompts took 145 us, bound by vector instructions.
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * x));
+}
 
 // Row r of e, r = token + K - 1: the state's rows come first.
 template <typename T, int K>
