@@ -97,9 +97,9 @@ kda_status ssm_dims(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype)
 struct Plan {
   int nseg, chunks;
 };
-Plan ssm_plan(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype, bool backward) {
+Plan ssm_plan(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype) {
   Plan p;
-  p.nseg = kda::ssm_plan(B, H, G, T, dk, dv, dtype == KDA_BF16, backward, kda::api_cu_count(), &p.chunks);
+  p.nseg = kda::ssm_plan(B, H, G, T, dk, dv, dtype == KDA_BF16, kda::api_cu_count(), &p.chunks);
   return p;
 }
 
@@ -201,7 +201,7 @@ kda_status kda_conv_backward(const void* x, const kda_strides* xs, const void* w
 
 size_t kda_ssm_prefill_workspace_bytes(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype) {
   if (B <= 0 || H <= 0 || T <= 0 || ssm_dims(B, H, G, T, dk, dv, dtype) != KDA_OK) return 0;
-  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype, false);
+  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
   return kda::ssm_ws_floats(B, H, dk, dv, p.nseg) * sizeof(float);
 }
 
@@ -234,7 +234,7 @@ kda_status kda_ssm_prefill(const void* q, const void* k, const void* v, const vo
   a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.beta = beta; a.D = D; a.S0 = S0; a.lens = lens; a.o = o; a.S_T = S_T;
   a.B = B; a.H = H; a.G = G; a.T = T; a.dk = dk; a.dv = dv;
   if (T > 0) {
-    Plan p = ssm_plan(B, H, G, T, dk, dv, dtype, false);
+    Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
     if (p.nseg > 1 && (!workspace || workspace_bytes < kda::ssm_ws_floats(B, H, dk, dv, p.nseg) * sizeof(float)))
       p = Plan{1, (T + kda::kSsmChunk - 1) / kda::kSsmChunk};
     a.nseg = p.nseg;
@@ -268,7 +268,7 @@ kda_status kda_ssm_step(const void* q, const void* k, const void* v, const void*
 
 size_t kda_ssm_backward_workspace_bytes(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype) {
   if (B <= 0 || H <= 0 || T <= 0 || ssm_dims(B, H, G, T, dk, dv, dtype) != KDA_OK) return 0;
-  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype, true);
+  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
   return kda::ssm_backward_ws_floats(B, H, G, T, dk, dv, p.nseg) * sizeof(float);
 }
 
@@ -308,7 +308,7 @@ kda_status kda_ssm_backward(const void* q, const void* k, const void* v, const v
   OPS_TRY(need_any(dbeta, "dbeta"));
   if (D) OPS_TRY(need_any(dD, "dD"));
   OPS_TRY(maybe(dS0, "dS0"));
-  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype, true);
+  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
   const size_t bytes = kda::ssm_backward_ws_floats(B, H, G, T, dk, dv, p.nseg) * sizeof(float);
   if (!workspace) return api_fail(KDA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", bytes);
   if (!aligned(workspace)) return api_fail(KDA_ERR_ALIGN, "workspace is not 16-byte aligned");

@@ -1029,8 +1029,10 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
           f32x4 mm;
           if constexpr (decltype(diag)::value) {
             mm = weigh_diag<KAPPA>(acc[nt], v, I, g, i);
+            if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mm[e] += 4 * g + e == i ? skip[u] : 0.f;
+              for (int e = 0; e < 4; ++e) mm[e] += 4 * g + e == i ? skip[u] : 0.f;
+            }
           } else {
             mm = weigh_below(acc[nt], v, I, J, g, i);
           }
@@ -1109,6 +1111,23 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
 #pragma unroll
       for (int m = 0; m < 2; ++m) vf[p][m] = VT::template vtile<NC>(sv + uw * VT::BYTES, vcol, m, p);
     intra<T, NC, 0, 4>(y, vf, sm + uw * SC::BYTES, l);
+    if constexpr (!BWD && sizeof(T) == 2) {
+      // D v as products with a diagonal operand of its own: D is exact in bf16, its sum
+      // with a score would not be (and D is often just above one, where rounding is
+      // coarsest).  fp32 adds it to the scores.
+      if (a.D) {
+        bf16x4 dg;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dg[e] = (bf16)(4 * g + e == i ? skip_w : 0.f);
+#pragma unroll
+        for (int I = 0; I < 4; ++I)
+#pragma unroll
+          for (int p = 0; p < NC; ++p) {
+            const bf16x8 x = vf[p][I >> 1];
+            y[p][I] = mfma_bf16_k16(y[p][I], (I & 1) ? __builtin_shufflevector(x, x, 4, 5, 6, 7) : __builtin_shufflevector(x, x, 0, 1, 2, 3), dg);
+          }
+      }
+    }
     if constexpr (BWD) {
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
@@ -1749,14 +1768,19 @@ hipError_t backward(const SsmArgs& x, hipStream_t s) {
 }  // namespace
 
 // Two workgroups a compute unit (one with fp32 tiles) fill the device; where the
-// sequences and heads alone give fewer, the sequence is cut, into runs of at least
-// four chunks.
-int ssm_plan(int B, int H, int G, int T, int dk, int dv, bool bf16_io, bool backward, int cus, int* seg_chunks) {
+// sequences and heads alone give fewer, the sequence is cut.  A chunk walked alone
+// takes 3 to 8 us, the two launches that a cut adds about 8, so runs may be one chunk
+// long from four chunks on (fp32 three).  Measured against runs of at least four
+// chunks: 16 heads, 512 tokens, bf16 37 -> 23 us; 8 heads, 333 tokens, fp32 55 -> 26;
+// gradients of 8 heads, 256 tokens, bf16 128 -> 68.  Past 16 bf16 chunks runs of two
+// are as good or better (8 heads, 2048 tokens: 30 us, 32 with runs of one).
+int ssm_plan(int B, int H, int G, int T, int dk, int dv, bool bf16_io, int cus, int* seg_chunks) {
   const int nch = (T + CH - 1) / CH;
   const long long np = ((long long)H / G * (dv / 64) + 1) / 2, base = (long long)B * G * np;
+  const int least = bf16_io && nch > 16 ? 2 : 1;
   long long nseg = base > 0 ? (bf16_io ? 2 : 1) * (long long)cus / base : 1;
-  if (nseg > nch / 4) nseg = nch / 4;
-  if (nseg < 1) nseg = 1;
+  if (nseg > nch / least) nseg = nch / least;
+  if (nseg < 1 || nch < (bf16_io ? 4 : 3)) nseg = 1;
   const int sc = (int)((nch + nseg - 1) / nseg);
   *seg_chunks = sc > 0 ? sc : 1;
   return nch > 0 ? (nch + *seg_chunks - 1) / *seg_chunks : 1;
