@@ -43,7 +43,8 @@ kda_status check_dtype(kda_dtype dt) {
 }
 
 // Strides of [B, H, T, d] (contiguous without s) into *out.  row16: rows start on
-// 16-byte boundaries.  Strides of dimensions of size 1 are not looked at.
+// 16-byte boundaries.  Strides of dimensions of size 1, and of
+// tensors without elements, are not looked at.
 kda_status take_strides(const kda_strides* s, int B, int H, int T, int d, int es, bool row16, bool output,
                         const char* name, Str3* out) {
   // (a chunk's rows are addressed with 32-bit offsets from its first one)
@@ -52,8 +53,9 @@ kda_status take_strides(const kda_strides* s, int B, int H, int T, int d, int es
   if (s) r = Str3{s->b, s->h, s->t};
   const long long v[3] = {r.b, r.h, r.t};
   const int n[3] = {B, H, T};
+  const bool empty = B == 0 || H == 0 || T == 0;
   for (int i = 0; i < 3; ++i) {
-    if (n[i] <= 1) continue;
+    if (n[i] <= 1 || empty) continue;
     if (v[i] < 0 || v[i] > most[i] || (output && v[i] == 0))
       return api_fail(KDA_ERR_SHAPE, "%s: stride %lld of dimension %d is not usable", name, v[i], i);
     if (row16 && v[i] * es % 16)
@@ -75,8 +77,8 @@ kda_status conv_dims(int B, int H, int T, int d, int K, kda_activation act, kda_
   const int es = dtype == KDA_BF16 ? 2 : 4;
   if ((long long)d * es % 16) return api_fail(KDA_ERR_UNSUPPORTED, "rows of %d elements are not a multiple of 16 bytes", d);
   const long long C = (long long)H * d;
-  // (T + 8: a kernel's token index goes past the end by less than that)
-  if (C > (1 << 28) || T > INT32_MAX - 4096 || (long long)B * C > kMaxElems || (long long)B * C * T > kMaxElems ||
+  // (a kernel's token index may pass the end by a block's runs)
+  if (C > (1 << 28) || T > (1 << 30) || (long long)B * C > kMaxElems || (long long)B * C * T > kMaxElems ||
       (long long)B * C * (T / 8 + 1) / 8 / 64 > INT32_MAX)
     return api_fail(KDA_ERR_SHAPE, "problem too large");
   return KDA_OK;
@@ -90,7 +92,7 @@ kda_status ssm_dims(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype)
     return api_fail(KDA_ERR_UNSUPPORTED, "head sizes dk=%d dv=%d not supported (64 or 128)", dk, dv);
   if (H > 0 && (G == 0 || H % G)) return api_fail(KDA_ERR_SHAPE, "G=%d does not divide H=%d", G, H);
   const long long BH = (long long)B * H;
-  if (BH > (1 << 24) || T > INT32_MAX - 4096 || BH * T > kMaxElems / 128) return api_fail(KDA_ERR_SHAPE, "problem too large");
+  if (BH > (1 << 24) || T > (1 << 30) || BH * T > kMaxElems / 128) return api_fail(KDA_ERR_SHAPE, "problem too large");
   return KDA_OK;
 }
 
@@ -136,6 +138,7 @@ kda_status kda_conv_prefill(const void* x, const kda_strides* xs, const void* we
   OPS_TRY(maybe(state_in, "state_in"));
   OPS_TRY(maybe(state_out, "state_out"));
   if (state_out && state_out == state_in) return api_fail(KDA_ERR_UNSUPPORTED, "state_out must not be state_in");
+  if (T > 0 && o == x) return api_fail(KDA_ERR_UNSUPPORTED, "o must not be x");
   a.x = x; a.w = weight; a.bias = bias; a.state = state_in; a.lens = lens; a.o = o; a.state_out = state_out;
   a.B = B; a.H = H; a.T = T; a.d = d; a.K = K; a.silu = act == KDA_ACT_SILU;
   const hipError_t e = kda::launch_conv(a, dtype == KDA_BF16, kda::api_cu_count(), stream);
@@ -187,6 +190,7 @@ kda_status kda_conv_backward(const void* x, const kda_strides* xs, const void* w
   OPS_TRY(need(dx, "dx"));
   OPS_TRY(need_any(dweight, "dweight"));
   OPS_TRY(maybe(dstate_in, "dstate_in"));
+  if (dx == x || dx == dO) return api_fail(KDA_ERR_UNSUPPORTED, "dx must not be x or dO");
   const size_t bytes = kda_conv_backward_workspace_bytes(B, H, T, d, K, dtype);
   if (!workspace) return api_fail(KDA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", bytes);
   if (!aligned(workspace)) return api_fail(KDA_ERR_ALIGN, "workspace is not 16-byte aligned");
@@ -335,7 +339,8 @@ kda_status cache_dims(int n, int nslots, int H, int dk, int dv, kda_cache_format
   if (f != KDA_CACHE_INT8 && f != KDA_CACHE_E4M3) return api_fail(KDA_ERR_UNSUPPORTED, "unknown cache format %d", (int)f);
   if (dv % 32) return api_fail(KDA_ERR_UNSUPPORTED, "rows of %d values are not whole blocks of 32", dv);
   const long long e = (long long)dk * dv, nh = (long long)n * H;
-  if (e > (1 << 24) || nh > (1 << 24) || nh * e > kMaxElems || (long long)nslots * H > kMaxElems)
+  // (store looks each entry's slot up among the later ones)
+  if (n > (1 << 16) || e > (1 << 24) || nh > (1 << 24) || nh * e > kMaxElems || (long long)nslots * H > kMaxElems)
     return api_fail(KDA_ERR_SHAPE, "problem too large");
   return KDA_OK;
 }

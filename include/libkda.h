@@ -379,7 +379,8 @@ kda_status kda_conv_backward(const void* x, const kda_strides* xs, const void* w
  *   S0, S_T         : [B, H, dk, dv] fp32; S0 NULL for zero; S_T may be S0
  * dk and dv are 64 or 128, independently.  T == 0 copies S0 (or zeros) to S_T.
  * bf16 inputs use bf16 matrix products with fp32 accumulation; states are
- * carried in fp32.  Sequences too few to fill the device are cut into segments
+ * carried in fp32.  An infinity or NaN in q, k or v may also reach the other
+ * tokens of its 64-token chunk, or not reach the states behind a decay of zero.  Sequences too few to fill the device are cut into segments
  * (each one's zero-start end state, a merge, then every segment from its true
  * start); that needs kda_ssm_prefill_workspace_bytes() of workspace, and with
  * less, or NULL, the call walks each sequence in one piece.
@@ -434,7 +435,8 @@ kda_status kda_ssm_backward(const void* q, const void* k, const void* v, const v
  *   cache  : [nslots, H, dk, dv] bytes (int8 or OCP e4m3 values)
  *   scales : [nslots, H, dk, dv / 32] bytes: exponent + 127; 255 marks a block
  *            that held an infinity or NaN and reads back as NaN
- * dv is a multiple of 32.  slots, and scales, may have any alignment.
+ * dv is a multiple of 32, n at most 65536.  slots and scales may have any
+ * alignment of their elements.
  */
 typedef enum { KDA_CACHE_INT8 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_format;
 
