@@ -340,7 +340,7 @@ kda_status cache_dims(int n, int nslots, int H, int dk, int dv, kda_cache_format
   if (dv % 32) return api_fail(KDA_ERR_UNSUPPORTED, "rows of %d values are not whole blocks of 32", dv);
   const long long e = (long long)dk * dv, nh = (long long)n * H;
   // (store looks each entry's slot up among the later ones)
-  if (n > (1 << 16) || e > (1 << 24) || nh > (1 << 24) || nh * e > kMaxElems || (long long)nslots * H > kMaxElems)
+  if (n > (1 << 16) || e > (1 << 24) || nh >= (1 << 24) || nh * e > kMaxElems || (long long)nslots * H > kMaxElems)
     return api_fail(KDA_ERR_SHAPE, "problem too large");
   return KDA_OK;
 }

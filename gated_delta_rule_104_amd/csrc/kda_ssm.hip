@@ -691,8 +691,8 @@ struct Item {
   int b, g, seg, sub;
   bool valid;
 };
-__device__ __forceinline__ Item item_of(int B, int G, int nseg, int np) {
-  const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
+__device__ __forceinline__ Item item_of(int block, int B, int G, int nseg, int np) {
+  const int x = block & 7, y = block >> 3;
   const int grp = (y / np) * 8 + x;
   Item it;
   it.sub = y % np;
@@ -753,17 +753,17 @@ __device__ __forceinline__ void store_state(const State<NK, NC>& S, float* p, in
 // the segment's end, so the chunks are walked from that end on and the state needs no
 // scaling; once the decay to the end is exactly zero for both units, every token
 // before adds exactly zero (for finite inputs), and the walk stops.
+template <typename T, int DK> constexpr int kStateLds = Tile<T, DK>::BYTES + 2 * Tile<T, 64>::BYTES + 4 * kVecNoKappa * 4;
 template <typename T, int DK, bool REV>
-__global__ __launch_bounds__(512 / kNC<T>, 4 / kNC<T>) void kda_ssm_state_kernel(PassArgs a) {
+__device__ __forceinline__ void state_pass(const PassArgs& a, int block, char* smem) {
   typedef Tile<T, DK> KT;
   typedef Tile<T, 64> VT;
   constexpr int NC = kNC<T>, NWV = 8 / NC, NT = 64 * NWV, VS = kVecNoKappa;
-  __shared__ __attribute__((aligned(16))) char smem[KT::BYTES + 2 * VT::BYTES + 4 * VS * 4];
   char* const sk = smem;
   char* const sv = smem + KT::BYTES;
   float* const vecs = reinterpret_cast<float*>(sv + 2 * VT::BYTES);  // two buffers, two units
   const int cpu = a.dv / 64, nu = a.H / a.G * cpu;  // column units per head, units per group
-  const Item it = item_of(a.B, a.G, a.norders, (nu + 1) / 2);
+  const Item it = item_of(block, a.B, a.G, a.norders, (nu + 1) / 2);
   if (!it.valid) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int len = clamp_len(a.lens, it.b, a.T);
@@ -847,31 +847,61 @@ __global__ __launch_bounds__(512 / kNC<T>, 4 / kNC<T>) void kda_ssm_state_kernel
   if (part == 0 && un % cpu == 0 && l == 0) a.dec[(size_t)it.seg * a.B * a.H + bh] = dec;
 }
 
+template <typename T, int DK>
+__global__ __launch_bounds__(512 / kNC<T>, 4 / kNC<T>) void kda_ssm_state_kernel(PassArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[kStateLds<T, DK>];
+  state_pass<T, DK, false>(a, blockIdx.x, smem);
+}
+
+// Both directions of the gradients: blocks from nf on walk the reversed orders.  One
+// launch, so that the second direction starts where the first one's blocks end.
+template <typename T, int DK>
+__global__ __launch_bounds__(512 / kNC<T>, 4 / kNC<T>) void kda_ssm_states_kernel(PassArgs f, PassArgs r, int nf) {
+  __shared__ __attribute__((aligned(16))) char smem[kStateLds<T, DK>];
+  if ((int)blockIdx.x < nf) state_pass<T, DK, false>(f, blockIdx.x, smem);
+  else state_pass<T, DK, true>(r, blockIdx.x - nf, smem);
+}
+
 // slots[0] = start; slots[o + 1] = dec[o] slots[o] + slots[o + 1], o = 0 .. n - 1.  The
 // last one also goes to out (which may be start), with la times the decay of token 0.
+struct MergeArgs {
+  const float* start;
+  float* slots;
+  const float* dec;
+  int n;
+  float* out;
+  const void* la;
+  Str3 ls;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void kda_ssm_merge_kernel(const float* start, float* slots, const float* dec, long long BH,
-                                                            int elems, int n, float* out, const T* la, Str3 ls, int H) {
-  const long long f = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+__device__ __forceinline__ void merge_at(const MergeArgs& a, long long f, long long BH, int elems, int H) {
   if (f >= BH * elems) return;
   const long long bh = f / elems;
-  f32x4 s = start ? *reinterpret_cast<const f32x4*>(start + f) : zero4();
-  *reinterpret_cast<f32x4*>(slots + f) = s;
-  for (int o = 0; o < n; ++o) {
-    float* p = slots + (o + 1) * BH * elems + f;
+  f32x4 s = a.start ? *reinterpret_cast<const f32x4*>(a.start + f) : zero4();
+  *reinterpret_cast<f32x4*>(a.slots + f) = s;
+  for (int o = 0; o < a.n; ++o) {
+    float* p = a.slots + (o + 1) * BH * elems + f;
     const f32x4 z = *reinterpret_cast<const f32x4*>(p);
-    const float d = dec[o * BH + bh];
+    const float d = a.dec[o * BH + bh];
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] = d * s[e] + z[e];
     *reinterpret_cast<f32x4*>(p) = s;
   }
-  if (!out) return;
-  if (la) {
-    const float d = ex2(fmaxf(to_f32(la[(bh / H) * ls.b + (bh % H) * ls.h]) * kLog2e, -180.f));
+  if (!a.out) return;
+  if (a.la) {
+    const float d = ex2(fmaxf(to_f32(static_cast<const T*>(a.la)[(bh / H) * a.ls.b + (bh % H) * a.ls.h]) * kLog2e, -180.f));
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] *= d;
   }
-  *reinterpret_cast<f32x4*>(out + f) = s;
+  *reinterpret_cast<f32x4*>(a.out + f) = s;
+}
+// (blocks from nf on: the other direction)
+template <typename T>
+__global__ __launch_bounds__(256) void kda_ssm_merge_kernel(MergeArgs x, MergeArgs y, int nf, long long BH, int elems, int H) {
+  const bool first = (int)blockIdx.x < nf;
+  const long long f = ((long long)(first ? blockIdx.x : blockIdx.x - nf) * 256 + threadIdx.x) * 4;
+  if (first) merge_at<T>(x, f, BH, elems, H);
+  else merge_at<T>(y, f, BH, elems, H);
 }
 
 __global__ __launch_bounds__(256) void kda_ssm_copy_kernel(const float* src, float* dst, long long n4) {
@@ -912,7 +942,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
   float* const vecs = reinterpret_cast<float*>(smem + OVEC);
   float* const red = reinterpret_cast<float*>(smem + ORED);
   const int cpu = a.dv / 64, nu = a.H / a.G * cpu;
-  const Item it = item_of(a.B, a.G, a.nseg, (nu + 1) / 2);
+  const Item it = item_of(blockIdx.x, a.B, a.G, a.nseg, (nu + 1) / 2);
   if (!it.valid) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int len = clamp_len(a.lens, it.b, a.T);
@@ -1201,9 +1231,18 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
 // the heads stays in its accumulators; groups with more heads leave one partial
 // result per workgroup.  The forward pass also leaves, per head and token,
 // rs[i] = q_i . (the state's part of dq_i).
+struct GroupArgs : PassArgs {
+  const void* qin;  // forward: the q rows
+  Str3 qrs;
+  float* rs;
+  float* parts;
+};
+// LDS (rs: one sum per wave, head and token; four waves' where the score vectors were, four more)
 template <typename T, int DV, int DK, bool REV>
-__global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_group_kernel(PassArgs a, const void* qin, Str3 qrs,
-                                                                                          float* rs, float* parts) {
+constexpr int kGroupLds = Tile<T, DK>::BYTES + 128 / DV * (2 * Tile<T, DV>::BYTES + Scores<T>::BYTES + 2 * (REV ? kVecNoKappa : V_SIZE) * 4) +
+                          (!REV && DK / 16 / kNC<T> > 4 ? 128 / DV * 256 * 4 : 0);
+template <typename T, int DV, int DK, bool REV>
+__device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* smem) {
   constexpr int NC = kNC<T>, HG = 128 / DV, NW = DK / 16 / NC, NT = 64 * NW;
   constexpr int NI = NC == 2 ? 2 : 4;  // row tiles at a time: with two column tiles a half of the tokens
   constexpr bool KAPPA = !REV;
@@ -1213,8 +1252,9 @@ __global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_gr
   typedef Scores<T> SC;
   constexpr int OQ = VT::BYTES, OK = OQ + HG * QT::BYTES, OM = OK + HG * QT::BYTES;
   constexpr int OVEC = OM + HG * SC::BYTES, ORS = OVEC + 2 * HG * VS * 4;
-  // rs: one sum per wave, head and token; four waves' where the score vectors were, four more
-  __shared__ __attribute__((aligned(16))) char smem[ORS + (!REV && NW > 4 ? HG * 256 * 4 : 0)];
+  static_assert(ORS + (!REV && NW > 4 ? HG * 256 * 4 : 0) == kGroupLds<T, DV, DK, REV>, "layout");
+  const Str3 qrs = a.qrs;
+  float* const parts = a.parts;
   char* const sv = smem;
   char* const sq = smem + OQ;
   char* const sk = smem + OK;
@@ -1222,14 +1262,14 @@ __global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_gr
   float* const vecs = reinterpret_cast<float*>(smem + OVEC);
   float* const rsx = reinterpret_cast<float*>(smem + ORS);
   const int R = a.H / a.G, np = (R + HG - 1) / HG;
-  const Item it = item_of(a.B, a.G, a.nseg, np);
+  const Item it = item_of(block, a.B, a.G, a.nseg, np);
   if (!it.valid) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int nch = (a.T + CH - 1) / CH;
   const int seg = REV ? a.nseg - 1 - it.seg : it.seg;
   const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
   const T* V = static_cast<const T*>(a.V) + it.b * a.vs.b + it.g * a.vs.h;
-  const T* W = REV ? nullptr : static_cast<const T*>(qin) + it.b * qrs.b + it.g * qrs.h;
+  const T* W = REV ? nullptr : static_cast<const T*>(a.qin) + it.b * qrs.b + it.g * qrs.h;
   const int nh = min(HG, R - it.sub * HG);  // heads of this workgroup
   int head[HG];
   const T *Q[HG], *K[HG];
@@ -1429,17 +1469,26 @@ __global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_gr
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) s += w < 4 ? v[64 * w + l] : rsx[256 * wave + 64 * (w - 4) + l];
-        rs[((size_t)it.b * a.H + it.g * R + it.sub * HG + wave) * a.T + tok0 + l] = s;
+        a.rs[((size_t)it.b * a.H + it.g * R + it.sub * HG + wave) * a.T + tok0 + l] = s;
       }
     }
   }
 }
 
+// dq and dk in one launch: blocks from nf on are dk's.
+template <typename T, int DV, int DK>
+__global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_group_kernel(GroupArgs q, GroupArgs k, int nf) {
+  constexpr int F = kGroupLds<T, DV, DK, false>, R = kGroupLds<T, DV, DK, true>;
+  __shared__ __attribute__((aligned(16))) char smem[F > R ? F : R];
+  if ((int)blockIdx.x < nf) group_pass<T, DV, DK, false>(q, blockIdx.x, smem);
+  else group_pass<T, DV, DK, true>(k, blockIdx.x - nf, smem);
+}
+
 // out[row] = sum of np partials, rows of dk values
 template <typename T>
-__global__ __launch_bounds__(256) void kda_ssm_parts_kernel(const float* parts, int np, T* out, Str3 os, int B, int G, int T_, int dk) {
+__device__ __forceinline__ void sum_parts(const float* parts, int np, T* out, Str3 os, int B, int G, int T_, int dk, int block) {
   const long long rows = (long long)B * G * T_;
-  const long long f = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long f = (long long)block * 256 + threadIdx.x;
   const int vpr = dk / 8;
   const long long row = f / vpr;
   if (row >= rows) return;
@@ -1462,9 +1511,18 @@ __global__ __launch_bounds__(256) void kda_ssm_parts_kernel(const float* parts, 
 // dlog_alpha and dbeta of one (b, h, segment), and the segment's share of dD.
 //     dlog_alpha[t] = sum_{i >= t in the segment} (rows_i - beta_i dbeta_i) + <S, dS> at its end
 // slots_f, slots_r: start states of the segments in both directions.
+struct GateArgs {
+  const float *slots_f, *slots_r, *rs;
+  void *dla, *dbeta;
+  Str3 dls, dbs;
+  float* dDp;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void kda_ssm_finish_kernel(PassArgs a, const float* slots_f, const float* slots_r,
-                                                             const float* rs, T* dla, Str3 dls, T* dbeta, Str3 dbs, float* dDp) {
+__device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs& x_) {
+  const float *slots_f = x_.slots_f, *slots_r = x_.slots_r, *rs = x_.rs;
+  T *dla = static_cast<T*>(x_.dla), *dbeta = static_cast<T*>(x_.dbeta);
+  const Str3 dls = x_.dls, dbs = x_.dbs;
+  float* const dDp = x_.dDp;
   __shared__ float sh[8];
   const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63;
   const int seg = blockIdx.x % a.nseg;
@@ -1527,13 +1585,27 @@ __global__ __launch_bounds__(256) void kda_ssm_finish_kernel(PassArgs a, const f
   if (tid == 0 && dDp) dDp[((size_t)b * a.nseg + seg) * a.H + h] = dsum;
 }
 
+// What is left when the passes are done, in one launch: the gates' gradients (blocks
+// below ng), then the sums of dq's and dk's partials (npart blocks each).
 template <typename T>
-__global__ __launch_bounds__(64) void kda_ssm_skip_kernel(const float* dDp, T* dD, int H, int n) {
-  const int h = blockIdx.x * 64 + threadIdx.x;
-  if (h >= H) return;
+__global__ __launch_bounds__(256) void kda_ssm_finish_kernel(GroupArgs q, GroupArgs k, GateArgs gate, int ng, int npart, int np) {
+  const int b = (int)blockIdx.x - ng;
+  if (b < 0) gate_gradients<T>(q, gate);
+  else if (b < npart) sum_parts<T>(q.parts, np, static_cast<T*>(q.o), q.os, q.B, q.G, q.T, q.dk, b);
+  else sum_parts<T>(k.parts, np, static_cast<T*>(k.o), k.os, k.B, k.G, k.T, k.dk, b - npart);
+}
+
+// dD of 64 heads: four waves share the partials.
+template <typename T>
+__global__ __launch_bounds__(256) void kda_ssm_skip_kernel(const float* dDp, T* dD, int H, int n) {
+  __shared__ float sh[4][64];
+  const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, h = blockIdx.x * 64 + l;
   float s = 0.f;
-  for (int p = 0; p < n; ++p) s += dDp[(size_t)p * H + h];
-  dD[h] = from_f32<T>(s);
+  if (h < H)
+    for (int p = wave; p < n; p += 4) s += dDp[(size_t)p * H + h];
+  sh[wave][l] = s;
+  __syncthreads();
+  if (wave == 0 && h < H) dD[h] = from_f32<T>((sh[0][l] + sh[1][l]) + (sh[2][l] + sh[3][l]));
 }
 
 // ----------------------------------------------------------------- one token
@@ -1602,12 +1674,21 @@ __global__ __launch_bounds__(256) void kda_ssm_check_kernel(const T* la, Str3 ls
 }
 
 // ------------------------------------------------------------------ launch
-template <typename T, bool REV>
+template <typename T>
 hipError_t run_state(const PassArgs& a, hipStream_t s) {
   const int nu = a.H / a.G * (a.dv / 64);
   const dim3 grid(item_grid(a.B, a.G, a.norders, (nu + 1) / 2)), block(512 / kNC<T>);
-  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_state_kernel<T, 128, REV>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((kda_ssm_state_kernel<T, 64, REV>), grid, block, 0, s, a);
+  if (a.dk == 128) hipLaunchKernelGGL((kda_ssm_state_kernel<T, 128>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((kda_ssm_state_kernel<T, 64>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t run_states(const PassArgs& f, const PassArgs& r, hipStream_t s) {
+  const int nu = f.H / f.G * (f.dv / 64);
+  const unsigned nf = item_grid(f.B, f.G, f.norders, (nu + 1) / 2), nr = item_grid(r.B, r.G, r.norders, (nu + 1) / 2);
+  const dim3 block(512 / kNC<T>);
+  if (f.dk == 128) hipLaunchKernelGGL((kda_ssm_states_kernel<T, 128>), dim3(nf + nr), block, 0, s, f, r, (int)nf);
+  else hipLaunchKernelGGL((kda_ssm_states_kernel<T, 64>), dim3(nf + nr), block, 0, s, f, r, (int)nf);
   return hipGetLastError();
 }
 
@@ -1628,32 +1709,29 @@ hipError_t run_out(const PassArgs& a, hipStream_t s) {
   return run_out_terms<T, BWD, 3>(a, s);
 }
 
-template <typename T, bool REV>
-hipError_t run_group(const PassArgs& a, const void* qin, Str3 qrs, float* rs, float* parts, hipStream_t s) {
-  const int hg = 128 / a.dv, np = (a.H / a.G + hg - 1) / hg;
-  const dim3 grid(item_grid(a.B, a.G, a.nseg, np));
-#define KDA_GROUP(DV, DK)                                                                                            \
-  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK, REV>), grid, dim3(4 * DK / kNC<T>), 0, s, a, qin, qrs, rs, parts)
-  if (a.dv == 64 && a.dk == 64) KDA_GROUP(64, 64);
-  else if (a.dv == 64) KDA_GROUP(64, 128);
-  else if (a.dk == 64) KDA_GROUP(128, 64);
+int group_parts(int H, int G, int dv) {
+  const int hg = 128 / dv;
+  return (H / G + hg - 1) / hg;
+}
+template <typename T>
+hipError_t run_groups(const GroupArgs& q, const GroupArgs& k, hipStream_t s) {
+  const unsigned n = item_grid(q.B, q.G, q.nseg, group_parts(q.H, q.G, q.dv));
+#define KDA_GROUP(DV, DK) \
+  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK>), dim3(2 * n), dim3(4 * DK / kNC<T>), 0, s, q, k, (int)n)
+  if (q.dv == 64 && q.dk == 64) KDA_GROUP(64, 64);
+  else if (q.dv == 64) KDA_GROUP(64, 128);
+  else if (q.dk == 64) KDA_GROUP(128, 64);
   else KDA_GROUP(128, 128);
 #undef KDA_GROUP
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || np == 1) return e;
-  const long long n = (long long)a.B * a.G * a.T * (a.dk / 8);
-  hipLaunchKernelGGL((kda_ssm_parts_kernel<T>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, parts, np,
-                     static_cast<T*>(a.o), a.os, a.B, a.G, a.T, a.dk);
   return hipGetLastError();
 }
 
-// decayed: the last state owes the decay of token 0 too
 template <typename T>
-hipError_t run_merge(const float* start, float* slots, const PassArgs& a, int n, float* out, bool decayed, hipStream_t s) {
+hipError_t run_merge(const MergeArgs& x, const MergeArgs* y, const PassArgs& a, hipStream_t s) {
   const long long BH = (long long)a.B * a.H;
   const int elems = a.dk * a.dv;
-  hipLaunchKernelGGL((kda_ssm_merge_kernel<T>), dim3((unsigned)((BH * elems / 4 + 255) / 256)), dim3(256), 0, s, start, slots,
-                     a.dec, BH, elems, n, out, decayed ? static_cast<const T*>(a.la) : nullptr, a.ls, a.H);
+  const unsigned n = (unsigned)((BH * elems / 4 + 255) / 256);
+  hipLaunchKernelGGL((kda_ssm_merge_kernel<T>), dim3(y ? 2 * n : n), dim3(256), 0, s, x, y ? *y : x, (int)n, BH, elems, a.H);
   return hipGetLastError();
 }
 
@@ -1680,15 +1758,15 @@ hipError_t prefill(const SsmArgs& x, hipStream_t s) {
   a.dec = x.ws + (size_t)(x.nseg + 1) * x.B * x.H * x.dk * x.dv;
   a.end = x.ws;
   a.norders = x.nseg;
-  SSM_TRY((run_state<T, false>(a, s)));
-  SSM_TRY(run_merge<T>(x.S0, x.ws, a, x.nseg, x.S_T, false, s));
+  SSM_TRY(run_state<T>(a, s));
+  SSM_TRY(run_merge<T>(MergeArgs{x.S0, x.ws, a.dec, x.nseg, x.S_T, nullptr, Str3()}, nullptr, a, s));
   a.start = x.ws;
   a.end = nullptr;
   return run_out<T, false>(a, s);
 }
 
 struct BwdWs {
-  size_t slots_f, slots_r, dec, c, r, d, rs, dDp, parts, total;
+  size_t slots_f, slots_r, dec_f, dec_r, c, r, d, rs, dDp, parts_q, parts_k, total;
 };
 BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg) {
   BwdWs w;
@@ -1701,14 +1779,16 @@ BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg) {
   const size_t st = (size_t)B * H * dk * dv, bht = (size_t)B * H * T, cpu = dv / 64;
   w.slots_f = take((nseg + 1) * st);
   w.slots_r = take((nseg + 1) * st);
-  w.dec = take((size_t)nseg * B * H);
+  w.dec_f = take((size_t)nseg * B * H);
+  w.dec_r = take((size_t)nseg * B * H);
   w.c = take(bht * cpu);
   w.r = take(bht * cpu);
   w.d = take(bht * cpu);
   w.rs = take(bht);
   w.dDp = take((size_t)nseg * B * H);
-  const int hg = 128 / dv, np = (H / G + hg - 1) / hg;
-  w.parts = take(np > 1 ? (size_t)np * B * G * T * dk : 0);
+  const int np = group_parts(H, G, dv);
+  w.parts_q = take(np > 1 ? (size_t)np * B * G * T * dk : 0);
+  w.parts_k = take(np > 1 ? (size_t)np * B * G * T * dk : 0);
   w.total = at;
   return w;
 }
@@ -1723,42 +1803,50 @@ hipError_t backward(const SsmArgs& x, hipStream_t s) {
   a.B = x.B; a.H = x.H; a.G = x.G; a.T = x.T; a.dk = x.dk; a.dv = x.dv;
   a.nseg = x.nseg; a.seg_chunks = x.seg_chunks;
   a.c = ws + w.c; a.r = ws + w.r; a.d = ws + w.d;
-  a.dec = ws + w.dec;
-  // start states of the segments, forwards (with the end state) and reversed
-  a.K = x.k; a.ks = x.ks; a.V = x.v; a.vs = x.vs;
-  a.end = ws + w.slots_f;
-  a.norders = x.nseg;
-  SSM_TRY((run_state<T, false>(a, s)));
-  SSM_TRY(run_merge<T>(x.S0, ws + w.slots_f, a, x.nseg, nullptr, false, s));
-  a.K = x.q; a.ks = x.qs; a.V = x.dO; a.vs = x.dos;
-  a.end = ws + w.slots_r;
-  // (of one segment dS0 comes from the outputs' pass)
-  a.norders = x.nseg == 1 ? 0 : x.dS0 ? x.nseg : x.nseg - 1;
-  if (a.norders > 0) SSM_TRY((run_state<T, true>(a, s)));
-  SSM_TRY(run_merge<T>(x.dS_T, ws + w.slots_r, a, a.norders, x.nseg > 1 ? x.dS0 : nullptr, true, s));
+  // start states of the segments, forwards (with the end state) and reversed; of one
+  // segment dS0 comes from the outputs' pass
+  PassArgs f = a, r = a;
+  f.K = x.k; f.ks = x.ks; f.V = x.v; f.vs = x.vs;
+  f.end = ws + w.slots_f;
+  f.dec = ws + w.dec_f;
+  f.norders = x.nseg;
+  r.K = x.q; r.ks = x.qs; r.V = x.dO; r.vs = x.dos;
+  r.end = ws + w.slots_r;
+  r.dec = ws + w.dec_r;
+  r.norders = x.nseg == 1 ? 0 : x.dS0 ? x.nseg : x.nseg - 1;
+  SSM_TRY(run_states<T>(f, r, s));
+  const MergeArgs mr{x.dS_T, r.end, r.dec, r.norders, x.nseg > 1 ? x.dS0 : nullptr, x.la, x.ls};
+  SSM_TRY(run_merge<T>(MergeArgs{x.S0, f.end, f.dec, x.nseg, nullptr, nullptr, Str3()}, &mr, a, s));
   // dv, dbeta's and dlog_alpha's sums, dS0
-  a.Q = x.k; a.qs = x.ks;
-  a.V2 = x.v; a.v2s = x.vs;
-  a.o = x.dvv; a.os = x.dvs;
-  a.start = ws + w.slots_r;
-  a.end = x.nseg == 1 ? x.dS0 : nullptr;
-  SSM_TRY((run_out<T, true>(a, s)));
-  // dq
-  a.Q = x.dO; a.qs = x.dos; a.K = x.v; a.ks = x.vs; a.V = x.k; a.vs = x.ks;
-  a.o = x.dq; a.os = x.dqs;
-  a.start = ws + w.slots_f;
-  SSM_TRY((run_group<T, false>(a, x.q, x.qs, ws + w.rs, ws + w.parts, s)));
-  // dk
-  a.Q = x.v; a.qs = x.vs; a.K = x.dO; a.ks = x.dos; a.V = x.q; a.vs = x.qs;
-  a.o = x.dkk; a.os = x.dks;
-  a.start = ws + w.slots_r;
-  SSM_TRY((run_group<T, true>(a, nullptr, Str3(), nullptr, ws + w.parts, s)));
-  hipLaunchKernelGGL((kda_ssm_finish_kernel<T>), dim3((unsigned)((long long)x.B * x.H * x.nseg)), dim3(256), 0, s, a,
-                     ws + w.slots_f, ws + w.slots_r, ws + w.rs, static_cast<T*>(x.dla), x.dls, static_cast<T*>(x.dbeta), x.dbs,
-                     x.dD ? ws + w.dDp : nullptr);
+  PassArgs v = r;
+  v.Q = x.k; v.qs = x.ks;
+  v.V2 = x.v; v.v2s = x.vs;
+  v.o = x.dvv; v.os = x.dvs;
+  v.start = r.end;
+  v.end = x.nseg == 1 ? x.dS0 : nullptr;
+  SSM_TRY((run_out<T, true>(v, s)));
+  // dq and dk
+  GroupArgs q{}, k{};
+  static_cast<PassArgs&>(q) = a;
+  q.Q = x.dO; q.qs = x.dos; q.K = x.v; q.ks = x.vs; q.V = x.k; q.vs = x.ks;
+  q.o = x.dq; q.os = x.dqs;
+  q.start = f.end;
+  q.qin = x.q; q.qrs = x.qs;
+  q.rs = ws + w.rs;
+  q.parts = ws + w.parts_q;
+  static_cast<PassArgs&>(k) = a;
+  k.Q = x.v; k.qs = x.vs; k.K = x.dO; k.ks = x.dos; k.V = x.q; k.vs = x.qs;
+  k.o = x.dkk; k.os = x.dks;
+  k.start = r.end;
+  k.parts = ws + w.parts_k;
+  SSM_TRY(run_groups<T>(q, k, s));
+  const GateArgs gate{f.end, r.end, q.rs, x.dla, x.dbeta, x.dls, x.dbs, x.dD ? ws + w.dDp : nullptr};
+  const int np = group_parts(x.H, x.G, x.dv);
+  const long long ng = (long long)x.B * x.H * x.nseg, npart = np > 1 ? ((long long)x.B * x.G * x.T * (x.dk / 8) + 255) / 256 : 0;
+  hipLaunchKernelGGL((kda_ssm_finish_kernel<T>), dim3((unsigned)(ng + 2 * npart)), dim3(256), 0, s, q, k, gate, (int)ng, (int)npart, np);
   SSM_TRY(hipGetLastError());
   if (x.dD) {
-    hipLaunchKernelGGL((kda_ssm_skip_kernel<T>), dim3((x.H + 63) / 64), dim3(64), 0, s, ws + w.dDp, static_cast<T*>(x.dD), x.H,
+    hipLaunchKernelGGL((kda_ssm_skip_kernel<T>), dim3((x.H + 63) / 64), dim3(256), 0, s, ws + w.dDp, static_cast<T*>(x.dD), x.H,
                        x.B * x.nseg);
     SSM_TRY(hipGetLastError());
   }
