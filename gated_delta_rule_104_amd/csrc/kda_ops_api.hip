@@ -273,7 +273,7 @@ kda_status kda_ssm_step(const void* q, const void* k, const void* v, const void*
 size_t kda_ssm_backward_workspace_bytes(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype) {
   if (B <= 0 || H <= 0 || T <= 0 || ssm_dims(B, H, G, T, dk, dv, dtype) != KDA_OK) return 0;
   const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
-  return kda::ssm_backward_ws_floats(B, H, G, T, dk, dv, p.nseg) * sizeof(float);
+  return kda::ssm_backward_ws_floats(B, H, G, T, dk, dv, p.nseg, dtype == KDA_BF16) * sizeof(float);
 }
 
 kda_status kda_ssm_backward(const void* q, const void* k, const void* v, const void* log_alpha, const void* beta,
@@ -313,7 +313,7 @@ kda_status kda_ssm_backward(const void* q, const void* k, const void* v, const v
   if (D) OPS_TRY(need_any(dD, "dD"));
   OPS_TRY(maybe(dS0, "dS0"));
   const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
-  const size_t bytes = kda::ssm_backward_ws_floats(B, H, G, T, dk, dv, p.nseg) * sizeof(float);
+  const size_t bytes = kda::ssm_backward_ws_floats(B, H, G, T, dk, dv, p.nseg, dtype == KDA_BF16) * sizeof(float);
   if (!workspace) return api_fail(KDA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", bytes);
   if (!aligned(workspace)) return api_fail(KDA_ERR_ALIGN, "workspace is not 16-byte aligned");
   if (workspace_bytes < bytes)

@@ -1238,12 +1238,21 @@ struct GroupArgs : PassArgs {
   float* parts;
 };
 // LDS (rs: one sum per wave, head and token; four waves' where the score vectors were, four more)
-template <typename T, int DV, int DK, bool REV>
-constexpr int kGroupLds = Tile<T, DK>::BYTES + 128 / DV * (2 * Tile<T, DV>::BYTES + Scores<T>::BYTES + 2 * (REV ? kVecNoKappa : V_SIZE) * 4) +
-                          (!REV && DK / 16 / kNC<T> > 4 ? 128 / DV * 256 * 4 : 0);
-template <typename T, int DV, int DK, bool REV>
+// Heads of a workgroup, and column tiles of a wave.  The states of two heads of 64
+// columns fill the registers of waves with two column tiles.  WIDE doubles the heads
+// and gives each wave one column tile (twice the waves, the same registers): half the
+// partial results, against operands read from LDS for one product instead of two.
+// Measured (bf16, 32 heads in 4 groups): four 8192-token sequences, 128 x 64 states, 770
+// us for the whole call and 738 wide (the partials' sum 140 -> 79 us, this kernel 354 ->
+// 386); two of them with 128 x 128 states 720 and 671; 64 x 64 602 and 602.
+template <typename T, int DV, bool WIDE> constexpr int kGroupHeads = (WIDE ? 256 : 128) / DV;
+template <typename T, bool WIDE> constexpr int kGroupNC = WIDE ? 1 : kNC<T>;
+template <typename T, int DV, int DK, bool WIDE, bool REV>
+constexpr int kGroupLds = Tile<T, DK>::BYTES + kGroupHeads<T, DV, WIDE> * (2 * Tile<T, DV>::BYTES + Scores<T>::BYTES + 2 * (REV ? kVecNoKappa : V_SIZE) * 4) +
+                          (!REV && DK / 16 / kGroupNC<T, WIDE> > 4 ? kGroupHeads<T, DV, WIDE> * 256 * 4 : 0);
+template <typename T, int DV, int DK, bool WIDE, bool REV>
 __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* smem) {
-  constexpr int NC = kNC<T>, HG = 128 / DV, NW = DK / 16 / NC, NT = 64 * NW;
+  constexpr int NC = kGroupNC<T, WIDE>, HG = kGroupHeads<T, DV, WIDE>, NW = DK / 16 / NC, NT = 64 * NW;
   constexpr int NI = NC == 2 ? 2 : 4;  // row tiles at a time: with two column tiles a half of the tokens
   constexpr bool KAPPA = !REV;
   constexpr int VS = KAPPA ? V_SIZE : kVecNoKappa;
@@ -1252,7 +1261,7 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
   typedef Scores<T> SC;
   constexpr int OQ = VT::BYTES, OK = OQ + HG * QT::BYTES, OM = OK + HG * QT::BYTES;
   constexpr int OVEC = OM + HG * SC::BYTES, ORS = OVEC + 2 * HG * VS * 4;
-  static_assert(ORS + (!REV && NW > 4 ? HG * 256 * 4 : 0) == kGroupLds<T, DV, DK, REV>, "layout");
+  static_assert(ORS + (!REV && NW > 4 ? HG * 256 * 4 : 0) == kGroupLds<T, DV, DK, WIDE, REV>, "layout");
   const Str3 qrs = a.qrs;
   float* const parts = a.parts;
   char* const sv = smem;
@@ -1293,7 +1302,7 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
   }
   const int fh = wave - (NW - HG);  // the last HG waves fill the heads' decay vectors
   const bool filler = fh >= 0;
-  const int hv = fh == 1 ? head[HG - 1] : head[0];
+  const int hv = it.g * R + it.sub * HG + max(0, min(fh, nh - 1));
   const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
 
@@ -1349,15 +1358,15 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
       fk[h].put(sk + h * QT::BYTES, tid);
     }
     // the wave's columns of the q rows, for rs: straight from memory, in the layout of its results
-    u32x4 xq[4];
+    typedef typename std::conditional<4 * NC * sizeof(T) == 16, u32x4, u32x2>::type XQ;  // a lane's columns
+    XQ xq[4];
     const uint32_t oxq = ((uint32_t)(l & 15) * (uint32_t)qrs.t + 4u * NC * (l >> 4)) * (uint32_t)sizeof(T);
     if constexpr (!REV) {
-      static_assert(4 * NC * sizeof(T) == 16, "16 bytes a lane");
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
         const int p = 16 * I + (l & 15);
-        xq[I] = u32x4{0u, 0u, 0u, 0u};
-        if (p < n) xq[I] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(W + (tok0 + 16 * I) * qrs.t + 16 * NC * wave) + oxq);
+        xq[I] = XQ{};
+        if (p < n) xq[I] = *reinterpret_cast<const XQ*>(reinterpret_cast<const char*>(W + (tok0 + 16 * I) * qrs.t + 16 * NC * wave) + oxq);
       }
     }
     fetch_q(step + 1);
@@ -1368,10 +1377,12 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
 #pragma unroll
     for (int h = 0; h < HG; ++h) {
       f32x4 acc[kTiles<NW>];
-      score_tiles<T, DV, NW, sizeof(T) == 2 ? 2 : 0>(acc, sk + h * QT::BYTES, sq + h * QT::BYTES, qrow, wave);
+      // (eight waves share ten tiles: with several heads each wave has its turn at two)
+      const int turn = NW == 8 ? (wave + 2 * h) & 7 : wave;
+      score_tiles<T, DV, NW, sizeof(T) == 2 ? 2 : 0>(acc, sk + h * QT::BYTES, sq + h * QT::BYTES, qrow, turn);
       const float* v = vec + h * VS;
       if (h == 0) fetch_k(step + 1);
-      each_tile<NW>(wave, [&](int nt, int I, int J, auto diag) {
+      each_tile<NW>(turn, [&](int nt, int I, int J, auto diag) {
         f32x4 mm;
         if constexpr (decltype(diag)::value) {
           mm = weigh_diag<KAPPA>(acc[nt], v, I, g, i);
@@ -1476,12 +1487,12 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
 }
 
 // dq and dk in one launch: blocks from nf on are dk's.
-template <typename T, int DV, int DK>
-__global__ __launch_bounds__(4 * DK / kNC<T>, DK == 128 ? 2 : 1) void kda_ssm_group_kernel(GroupArgs q, GroupArgs k, int nf) {
-  constexpr int F = kGroupLds<T, DV, DK, false>, R = kGroupLds<T, DV, DK, true>;
+template <typename T, int DV, int DK, bool WIDE>
+__global__ __launch_bounds__((4 * DK / kGroupNC<T, WIDE>), DK == 128 ? 2 : 1) void kda_ssm_group_kernel(GroupArgs q, GroupArgs k, int nf) {
+  constexpr int F = kGroupLds<T, DV, DK, WIDE, false>, R = kGroupLds<T, DV, DK, WIDE, true>;
   __shared__ __attribute__((aligned(16))) char smem[F > R ? F : R];
-  if ((int)blockIdx.x < nf) group_pass<T, DV, DK, false>(q, blockIdx.x, smem);
-  else group_pass<T, DV, DK, true>(k, blockIdx.x - nf, smem);
+  if ((int)blockIdx.x < nf) group_pass<T, DV, DK, WIDE, false>(q, blockIdx.x, smem);
+  else group_pass<T, DV, DK, WIDE, true>(k, blockIdx.x - nf, smem);
 }
 
 // out[row] = sum of np partials, rows of dk values
@@ -1709,21 +1720,29 @@ hipError_t run_out(const PassArgs& a, hipStream_t s) {
   return run_out_terms<T, BWD, 3>(a, s);
 }
 
-int group_parts(int H, int G, int dv) {
-  const int hg = 128 / dv;
+bool group_wide(int H, int G, int dv, bool bf16_io) { return bf16_io && H / G > 128 / dv; }
+int group_parts(int H, int G, int dv, bool bf16_io) {
+  const int hg = (group_wide(H, G, dv, bf16_io) ? 256 : 128) / dv;
   return (H / G + hg - 1) / hg;
 }
-template <typename T>
-hipError_t run_groups(const GroupArgs& q, const GroupArgs& k, hipStream_t s) {
-  const unsigned n = item_grid(q.B, q.G, q.nseg, group_parts(q.H, q.G, q.dv));
+template <typename T, bool WIDE>
+hipError_t run_groups_of(const GroupArgs& q, const GroupArgs& k, hipStream_t s) {
+  const unsigned n = item_grid(q.B, q.G, q.nseg, group_parts(q.H, q.G, q.dv, sizeof(T) == 2));
 #define KDA_GROUP(DV, DK) \
-  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK>), dim3(2 * n), dim3(4 * DK / kNC<T>), 0, s, q, k, (int)n)
+  hipLaunchKernelGGL((kda_ssm_group_kernel<T, DV, DK, WIDE>), dim3(2 * n), dim3(4 * DK / kGroupNC<T, WIDE>), 0, s, q, k, (int)n)
   if (q.dv == 64 && q.dk == 64) KDA_GROUP(64, 64);
   else if (q.dv == 64) KDA_GROUP(64, 128);
   else if (q.dk == 64) KDA_GROUP(128, 64);
   else KDA_GROUP(128, 128);
 #undef KDA_GROUP
   return hipGetLastError();
+}
+template <typename T>
+hipError_t run_groups(const GroupArgs& q, const GroupArgs& k, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (group_wide(q.H, q.G, q.dv, true)) return run_groups_of<T, true>(q, k, s);
+  }
+  return run_groups_of<T, false>(q, k, s);
 }
 
 template <typename T>
@@ -1768,7 +1787,7 @@ hipError_t prefill(const SsmArgs& x, hipStream_t s) {
 struct BwdWs {
   size_t slots_f, slots_r, dec_f, dec_r, c, r, d, rs, dDp, parts_q, parts_k, total;
 };
-BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg) {
+BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg, bool bf16_io) {
   BwdWs w;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -1786,7 +1805,7 @@ BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg) {
   w.d = take(bht * cpu);
   w.rs = take(bht);
   w.dDp = take((size_t)nseg * B * H);
-  const int np = group_parts(H, G, dv);
+  const int np = group_parts(H, G, dv, bf16_io);
   w.parts_q = take(np > 1 ? (size_t)np * B * G * T * dk : 0);
   w.parts_k = take(np > 1 ? (size_t)np * B * G * T * dk : 0);
   w.total = at;
@@ -1795,7 +1814,7 @@ BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg) {
 
 template <typename T>
 hipError_t backward(const SsmArgs& x, hipStream_t s) {
-  const BwdWs w = backward_ws(x.B, x.H, x.G, x.T, x.dk, x.dv, x.nseg);
+  const BwdWs w = backward_ws(x.B, x.H, x.G, x.T, x.dk, x.dv, x.nseg, sizeof(T) == 2);
   float* const ws = x.ws;
   PassArgs a{};
   a.la = x.la; a.beta = x.beta; a.D = x.D;
@@ -1841,7 +1860,7 @@ hipError_t backward(const SsmArgs& x, hipStream_t s) {
   k.parts = ws + w.parts_k;
   SSM_TRY(run_groups<T>(q, k, s));
   const GateArgs gate{f.end, r.end, q.rs, x.dla, x.dbeta, x.dls, x.dbs, x.dD ? ws + w.dDp : nullptr};
-  const int np = group_parts(x.H, x.G, x.dv);
+  const int np = group_parts(x.H, x.G, x.dv, sizeof(T) == 2);
   const long long ng = (long long)x.B * x.H * x.nseg, npart = np > 1 ? ((long long)x.B * x.G * x.T * (x.dk / 8) + 255) / 256 : 0;
   hipLaunchKernelGGL((kda_ssm_finish_kernel<T>), dim3((unsigned)(ng + 2 * npart)), dim3(256), 0, s, q, k, gate, (int)ng, (int)npart, np);
   SSM_TRY(hipGetLastError());
@@ -1879,8 +1898,8 @@ size_t ssm_ws_floats(int B, int H, int dk, int dv, int nseg) {
   return (size_t)(nseg + 1) * B * H * dk * dv + ((size_t)nseg * B * H + 3) / 4 * 4;
 }
 
-size_t ssm_backward_ws_floats(int B, int H, int G, int T, int dk, int dv, int nseg) {
-  return backward_ws(B, H, G, T, dk, dv, nseg).total;
+size_t ssm_backward_ws_floats(int B, int H, int G, int T, int dk, int dv, int nseg, bool bf16_io) {
+  return backward_ws(B, H, G, T, dk, dv, nseg, bf16_io).total;
 }
 
 hipError_t launch_ssm_prefill(const SsmArgs& a, bool bf16_io, hipStream_t stream) {

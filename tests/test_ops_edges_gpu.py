@@ -358,6 +358,18 @@ def test_many_heads_in_one_piece():
     check_grads(got, orc.ssm_backward(*ssm_ref_args(c, True, True), c["dO"], c["dS_T"]), "bf16")
 
 
+@pytest.mark.parametrize("B,H,G,T,dk,dv", [(1, 7, 1, 130, 64, 128), (2, 10, 2, 150, 64, 64), (1, 9, 1, 100, 128, 128),
+                                         (1, 18, 2, 65, 128, 64), (3, 2, 1, 64, 64, 128), (1, 4, 1, 1, 128, 64)])
+def test_groups_of_many_heads(B, H, G, T, dk, dv):
+    """bf16 gradients summed over more heads than one workgroup's two, odd counts among them."""
+    print(f"[case] ssm_backward {B} {H}/{G} {T} {dk}x{dv}", flush=True)
+    c = ssm_case(B, H, G, T, dk, dv, "bf16", seed=H)
+    args, t = ssm_args(c, True, True, True)
+    got = kda.ssm_backward(*args, t["dO"], t["dS_T"])
+    torch.cuda.synchronize()
+    check_grads(got, orc.ssm_backward(*ssm_ref_args(c, True, True), c["dO"], c["dS_T"]), "bf16")
+
+
 def test_small_workspace_walks_in_one_piece():
     c = ssm_case(1, 2, 1, 700, 64, 64, "bf16", seed=18)
     args, _ = ssm_args(c, True, True, True)
