@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256) void kda_conv_kernel(ConvArgs a, int nvec, int
   const int len = seq_len(a.lens, b, a.T);
   const T* x = static_cast<const T*>(a.x) + b * a.xs.b + h * a.xs.h + j0;
   T* o = static_cast<T*>(a.o) + b * a.os.b + h * a.os.h + j0;
-  const long long sbase = ((long long)(b * a.H + h) * (K - 1)) * a.d + j0;
+  const long long sbase = (((long long)b * a.H + h) * (K - 1)) * a.d + j0;
   const T* state = a.state ? static_cast<const T*>(a.state) + sbase : nullptr;
   if (tile == 0 && a.state_out) {
     T* so = static_cast<T*>(a.state_out) + sbase;
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(ConvArgs a, int nvec,
     const T* x = static_cast<const T*>(a.x) + b * a.xs.b + h * a.xs.h + j0;
     const T* dO = static_cast<const T*>(a.dO) + b * a.dos.b + h * a.dos.h + j0;
     T* dx = static_cast<T*>(a.dx) + b * a.dxs.b + h * a.dxs.h + j0;
-    const long long sbase = ((long long)(b * a.H + h) * (K - 1)) * a.d + j0;
+    const long long sbase = (((long long)b * a.H + h) * (K - 1)) * a.d + j0;
     const T* state = a.state ? static_cast<const T*>(a.state) + sbase : nullptr;
     const T* dso = a.dstate_out ? static_cast<const T*>(a.dstate_out) + sbase : nullptr;
     T* ds = a.dstate ? static_cast<T*>(a.dstate) + sbase : nullptr;

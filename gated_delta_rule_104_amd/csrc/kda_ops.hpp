@@ -88,7 +88,7 @@ hipError_t launch_ssm_step(const void* q, const void* k, const void* v, const vo
                            const void* D, float* S, void* o, int N, int H, int G, int dk, int dv, bool bf16_io,
                            hipStream_t stream);
 // bit 0: a log_alpha above 0 or NaN, bit 1: a beta not finite.  Synchronises `stream`.
-hipError_t check_ssm_gates(const void* la, Str3 ls, const void* beta, Str3 bs, int B, int H, int T, bool bf16_io,
+hipError_t check_ssm_gates(const void* la, Str3 ls, const void* beta, Str3 bs, const int* lens, int B, int H, int T, bool bf16_io,
                            hipStream_t stream, unsigned int* bits_out);
 
 }  // namespace kda

@@ -4,6 +4,8 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <initializer_list>
+
 #include "kda_host.hpp"
 #include "kda_ops.hpp"
 
@@ -105,11 +107,11 @@ Plan ssm_plan(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype) {
   return p;
 }
 
-kda_status check_gates(const void* la, Str3 ls, const void* beta, Str3 bs, int B, int H, int T, kda_dtype dtype,
-                       hipStream_t stream) {
+kda_status check_gates(const void* la, Str3 ls, const void* beta, Str3 bs, const int* lens, int B, int H, int T,
+                       kda_dtype dtype, hipStream_t stream) {
   if (!kda::api_check_on()) return KDA_OK;
   unsigned int bits = 0u;
-  const hipError_t e = kda::check_ssm_gates(la, ls, beta, bs, B, H, T, dtype == KDA_BF16, stream, &bits);
+  const hipError_t e = kda::check_ssm_gates(la, ls, beta, bs, lens, B, H, T, dtype == KDA_BF16, stream, &bits);
   if (e != hipSuccess) return hip_fail(e, "input check");
   if (bits & 1u) return api_fail(KDA_ERR_PRECONDITION, "log_alpha has values above 0 or NaN (check mode)");
   if (bits & 2u) return api_fail(KDA_ERR_PRECONDITION, "beta has values that are not finite (check mode)");
@@ -233,7 +235,8 @@ kda_status kda_ssm_prefill(const void* q, const void* k, const void* v, const vo
     OPS_TRY(need_any(beta, "beta"));
     OPS_TRY(need(o, "o"));
     OPS_TRY(maybe(workspace, "workspace"));
-    OPS_TRY(check_gates(log_alpha, a.ls, beta, a.bs, B, H, T, dtype, stream));
+    if (o == q || o == k || o == v) return api_fail(KDA_ERR_UNSUPPORTED, "o must not be an input");
+    OPS_TRY(check_gates(log_alpha, a.ls, beta, a.bs, lens, B, H, T, dtype, stream));
   }
   a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.beta = beta; a.D = D; a.S0 = S0; a.lens = lens; a.o = o; a.S_T = S_T;
   a.B = B; a.H = H; a.G = G; a.T = T; a.dk = dk; a.dv = dv;
@@ -265,7 +268,7 @@ kda_status kda_ssm_step(const void* q, const void* k, const void* v, const void*
   OPS_TRY(need(S, "S"));
   OPS_TRY(need(o, "o"));
   const Str3 gs{H, 1, 0};
-  OPS_TRY(check_gates(log_alpha, gs, beta, gs, N, H, 1, dtype, stream));
+  OPS_TRY(check_gates(log_alpha, gs, beta, gs, nullptr, N, H, 1, dtype, stream));
   const hipError_t e = kda::launch_ssm_step(q, k, v, log_alpha, beta, D, S, o, N, H, G, dk, dv, dtype == KDA_BF16, stream);
   return e == hipSuccess ? api_ok() : hip_fail(e, "kda_ssm_step launch");
 }
@@ -312,13 +315,18 @@ kda_status kda_ssm_backward(const void* q, const void* k, const void* v, const v
   OPS_TRY(need_any(dbeta, "dbeta"));
   if (D) OPS_TRY(need_any(dD, "dD"));
   OPS_TRY(maybe(dS0, "dS0"));
+  // (later launches read the inputs again)
+  for (const void* out : {dq, dk_, dv_, dlog_alpha, dbeta})
+    for (const void* in : {q, k, v, log_alpha, beta, dO})
+      if (out == in) return api_fail(KDA_ERR_UNSUPPORTED, "a gradient must not be an input");
+  if (dS0 && (dS0 == S0 || dS0 == dS_T)) return api_fail(KDA_ERR_UNSUPPORTED, "dS0 must not be S0 or dS_T");
   const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
   const size_t bytes = kda::ssm_backward_ws_floats(B, H, G, T, dk, dv, p.nseg, dtype == KDA_BF16) * sizeof(float);
   if (!workspace) return api_fail(KDA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", bytes);
   if (!aligned(workspace)) return api_fail(KDA_ERR_ALIGN, "workspace is not 16-byte aligned");
   if (workspace_bytes < bytes)
     return api_fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, bytes);
-  OPS_TRY(check_gates(log_alpha, a.ls, beta, a.bs, B, H, T, dtype, stream));
+  OPS_TRY(check_gates(log_alpha, a.ls, beta, a.bs, nullptr, B, H, T, dtype, stream));
   a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.beta = beta; a.D = D; a.S0 = S0; a.dO = dO; a.dS_T = dS_T;
   a.dq = dq; a.dkk = dk_; a.dvv = dv_; a.dla = dlog_alpha; a.dbeta = dbeta; a.dD = D ? dD : nullptr; a.dS0 = dS0;
   a.B = B; a.H = H; a.G = G; a.T = T; a.dk = dk; a.dv = dv;

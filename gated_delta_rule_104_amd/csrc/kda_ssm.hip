@@ -1683,12 +1683,13 @@ __device__ unsigned int g_ssm_check_bits;
 __global__ void kda_ssm_check_clear_kernel(unsigned int* bits) { *bits = 0u; }
 
 template <typename T>
-__global__ __launch_bounds__(256) void kda_ssm_check_kernel(const T* la, Str3 ls, const T* beta, Str3 bs, int H, int T_,
-                                                            long long n, unsigned int* bits) {
+__global__ __launch_bounds__(256) void kda_ssm_check_kernel(const T* la, Str3 ls, const T* beta, Str3 bs, const int* lens, int H,
+                                                            int T_, long long n, unsigned int* bits) {
   unsigned int b = 0u;
   for (long long f = (long long)blockIdx.x * 256 + threadIdx.x; f < n; f += (long long)gridDim.x * 256) {
     const int t = (int)(f % T_);
     const long long bh = f / T_, bb = bh / H, h = bh % H;
+    if (t >= clamp_len(lens, (int)bb, T_)) continue;
     if (!(to_f32(la[bb * ls.b + h * ls.h + t * ls.t]) <= 0.f)) b |= 1u;
     if (!(fabsf(to_f32(beta[bb * bs.b + h * bs.h + t * bs.t])) < __builtin_inff())) b |= 2u;
   }
@@ -1946,8 +1947,8 @@ hipError_t launch_ssm_step(const void* q, const void* k, const void* v, const vo
   return hipGetLastError();
 }
 
-hipError_t check_ssm_gates(const void* la, Str3 ls, const void* beta, Str3 bs, int B, int H, int T, bool bf16_io,
-                           hipStream_t stream, unsigned int* bits_out) {
+hipError_t check_ssm_gates(const void* la, Str3 ls, const void* beta, Str3 bs, const int* lens, int B, int H, int T,
+                           bool bf16_io, hipStream_t stream, unsigned int* bits_out) {
   static std::mutex mu;
   std::lock_guard<std::mutex> lk(mu);  // one check at a time: the flag is the device's only one
   void* p = nullptr;
@@ -1961,10 +1962,10 @@ hipError_t check_ssm_gates(const void* la, Str3 ls, const void* beta, Str3 bs, i
   const dim3 grid((unsigned)(nb < 2048 ? nb : 2048));
   if (bf16_io)
     hipLaunchKernelGGL(kda_ssm_check_kernel<bf16>, grid, dim3(256), 0, stream, static_cast<const bf16*>(la), ls,
-                       static_cast<const bf16*>(beta), bs, H, T, n, f);
+                       static_cast<const bf16*>(beta), bs, lens, H, T, n, f);
   else
     hipLaunchKernelGGL(kda_ssm_check_kernel<float>, grid, dim3(256), 0, stream, static_cast<const float*>(la), ls,
-                       static_cast<const float*>(beta), bs, H, T, n, f);
+                       static_cast<const float*>(beta), bs, lens, H, T, n, f);
   SSM_TRY(hipGetLastError());
   unsigned int h = 0u;
   if ((e = hipMemcpyAsync(&h, f, sizeof(h), hipMemcpyDeviceToHost, stream)) != hipSuccess) return e;

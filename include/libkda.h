@@ -374,7 +374,8 @@ kda_status kda_conv_backward(const void* x, const kda_strides* xs, const void* w
  *   v, o            : [B, H, T, dv] dtype
  *   log_alpha, beta : [B, H, T] dtype (strides b, h, t in elements, any element
  *                     alignment), log_alpha <= 0 (-inf clears the state), beta
- *                     finite.  Option "check" validates that before launching.
+ *                     finite.  Option "check" validates that (padding excepted)
+ *                     before launching.
  *   D               : [H] dtype (any element alignment) or NULL (no skip)
  *   S0, S_T         : [B, H, dk, dv] fp32; S0 NULL for zero; S_T may be S0
  * dk and dv are 64 or 128, independently.  T == 0 copies S0 (or zeros) to S_T.

@@ -94,6 +94,8 @@ def test_ssm_prefill_refusals(lib):
     for n in ("q", "k", "v", "o", "S_T", "S0"):
         assert ssm(lib, **{n: A + 8}) == ERR_ALIGN, n
     assert ssm(lib, ws=A + 8, nws=64) == ERR_ALIGN
+    for n in ("q", "k", "v"):
+        assert ssm(lib, **{n: A + 64}) == ERR_UNSUPPORTED, n
     bad = kda._SsmStrides(*(st(4096, 64, 64) for _ in range(6)))
     bad.o = st(4096, 64, 60)
     assert ssm(lib, strides=bad) == ERR_ALIGN
@@ -132,8 +134,8 @@ def test_ssm_backward_refusals(lib):
     assert need > 0 and lib.kda_ssm_backward_workspace_bytes(1, 4, 2, 0, 64, 64, BF16) == 0
 
     def f(B=1, H=4, G=2, T=70, dk=64, dv=64, dt=BF16, ws=A, nws=need, gst=None, **p):
-        a = dict(q=A, k=A, v=A, la=A + 2, beta=A + 2, D=None, S0=None, dO=A, dS_T=None, dq=A, dk_=A, dv_=A, dla=A + 2,
-                 dbeta=A + 2, dD=None, dS0=None)
+        a = dict(q=A, k=A, v=A, la=A + 2, beta=A + 2, D=None, S0=None, dO=A, dS_T=None, dq=A + 64, dk_=A + 128, dv_=A + 192,
+                 dla=A + 256, dbeta=A + 320, dD=None, dS0=None)
         a.update(p)
         return lib.kda_ssm_backward(*a.values(), None, gst, B, H, G, T, dk, dv, dt, ws, nws, None)
     assert f(T=0) == ERR_SHAPE and f(B=0) == ERR_SHAPE and f(dk=80) == ERR_UNSUPPORTED and f(H=0, G=1) == OK
@@ -143,6 +145,9 @@ def test_ssm_backward_refusals(lib):
     for n in ("dO", "dS_T", "dq", "dS0"):
         assert f(**{n: A + 4}) == ERR_ALIGN, n
     assert f(ws=None) == ERR_WORKSPACE and f(nws=need - 1) == ERR_WORKSPACE and f(ws=A + 8) == ERR_ALIGN
+    for n in ("dq", "dk_", "dv_", "dla", "dbeta"):  # a later launch would read what an earlier one wrote
+        assert f(**{n: A}) == ERR_UNSUPPORTED, n
+    assert f(S0=A + 512, dS0=A + 512) == ERR_UNSUPPORTED and f(dS_T=A + 512, dS0=A + 512) == ERR_UNSUPPORTED
     g = kda._SsmGradStrides(*(st(4096 * 4, 4096, 64) for _ in range(6)))
     g.dbeta = st(280, 70, 0)
     assert f(gst=g) == ERR_SHAPE

@@ -438,6 +438,39 @@ def test_input_check():
     assert torch.equal(o, o1) and torch.equal(S, S1)
 
 
+def test_input_check_leaves_padding_alone():
+    c = ssm_case(2, 2, 1, 70, 64, 64, "bf16", seed=21)
+    c["log_alpha"][0, :, 30:], c["beta"][0, :, 30:] = float("nan"), float("inf")
+    args, _ = ssm_args(c, True, True, True)
+    lens = torch.tensor([30, 70], dtype=torch.int32)
+    with kda.options(check=1):
+        o, S = kda.ssm_prefill(*args, lens=up(lens))
+    torch.cuda.synchronize()
+    ro, rS = orc.ssm(*ssm_ref_args(c, True, True), lens=lens)
+    assert orc.rel(S, rS) <= 1e-5 and orc.rel(o, ro) <= TOL["bf16"]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradients_of_far_apart_tokens(dt):
+    """Inputs and incoming gradients with tokens 2^22 elements apart, heads between them."""
+    wide, H = 2 ** 22, 2
+    c = ssm_case(1, H, 1, 70, 64, 64, dt, seed=22)
+    base = torch.empty(69 * wide + 4 * H * 64 + 128, dtype=DT[dt], device=dev())
+    at, v = 0, {}
+    for n in ("q", "k", "v", "dO"):
+        rows = c[n].shape[1]
+        v[n] = base.as_strided((1, rows, 70, 64), (0, 64, wide, 1), at)
+        v[n].copy_(up(c[n]))
+        at += rows * 64
+    rest = [up(c[n]) for n in ("log_alpha", "beta", "D", "S0")]
+    near = [up(c[n]) for n in ("q", "k", "v")]
+    g = kda.ssm_backward(v["q"], v["k"], v["v"], *rest, v["dO"], up(c["dS_T"]))
+    g1 = kda.ssm_backward(*near, *rest, up(c["dO"]), up(c["dS_T"]))
+    torch.cuda.synchronize()
+    for n in g:
+        assert torch.equal(g[n], g1[n]), n
+
+
 def test_refusals_of_the_bindings():
     c = {n: up(t) for n, t in ssm_case(1, 2, 1, 10, 64, 64, "bf16", seed=20).items()}
     a = [c["q"], c["k"], c["v"], c["log_alpha"], c["beta"]]
