@@ -758,8 +758,9 @@ __device__ __forceinline__ void store_state(const State<NK, NC>& S, float* p, in
 // End state of every segment from zero.  Workgroup = two 64-column units of one
 // group, wave = 16 NC columns of one.  The weight of a token is the decay from it to
 // the segment's end, so the chunks are walked from that end on and the state needs no
-// scaling; once the decay to the end is exactly zero for both units, every token
-// before adds exactly zero (for finite inputs), and the walk stops.  Matrix cores are
+// scaling; once the decay to the end is exactly zero for a unit, every token before
+// adds exactly zero (for finite inputs): its waves only keep step with the other
+// unit's, and the walk stops when both have come to zero.  Matrix cores are
 // busy half of the waves' life (three terms); the slowest decays set the kernel's end.
 // Two buffers for the tiles took longer (268 us against 253, 64K tokens, 64 heads).
 template <typename T, int DK> constexpr int kStateLds = Tile<T, DK>::BYTES + 2 * Tile<T, 64>::BYTES + 4 * kVecNoKappa * 4;
@@ -796,7 +797,7 @@ __device__ __forceinline__ void state_pass(const PassArgs& a, int block, char* s
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
   State<DK / 16, NC> S;
   S.zero();
-  float dec = 1.f;  // decay of the chunks walked
+  float dec[2] = {1.f, 1.f};  // decays of the chunks walked
   Fetch<T, DK, NT> fk;
   Fetch<T, 64, NT> fv[2];
   const uint32_t ofk = fk.template lane_off<REV>(a.ks.t, tid), ofv = fv[0].template lane_off<REV>(a.vs.t, tid);
@@ -807,7 +808,8 @@ __device__ __forceinline__ void state_pass(const PassArgs& a, int block, char* s
     const int tok0 = chunk(step) * CH, n = min(CH, len - tok0);
     fk.template get<REV>(K, a.ks.t, tok0, n, ofk, tid);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) fv[u].template get<REV>(V[u], a.vs.t, tok0, n, ofv, tid);
+    for (int u = 0; u < 2; ++u)
+      if (dec[u] != 0.f) fv[u].template get<REV>(V[u], a.vs.t, tok0, n, ofv, tid);
   };
   auto fetch_gates = [&](int step) {
     if (!filler || step >= c1 - c0) return;
@@ -836,15 +838,18 @@ __device__ __forceinline__ void state_pass(const PassArgs& a, int block, char* s
     fetch_gates(step + 2);
     const int ln = fresh_lane(l), g = ln >> 4, i = ln & 15;
     const uint32_t vcol = VT::template vtile_off<NC>(g, i, part);
-    typename Op<T>::F vf[NC][2];
+    if ((uw ? dec[1] : dec[0]) != 0.f) {
+      typename Op<T>::F vf[NC][2];
 #pragma unroll
-    for (int p = 0; p < NC; ++p)
+      for (int p = 0; p < NC; ++p)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) vf[p][m] = VT::template vtile<NC>(sv + uw * VT::BYTES, vcol, m, p);
-    update<T, DK / 16, NC, 3, false, KT>(S, sk, vf, vec + uw * VS + V_WS, 1.f, KT::col_off(g, i), g);
-    const float r0 = vec[V_GM], r1 = vec[VS + V_GM];
-    dec = uw ? r1 : r0;
-    if (__builtin_amdgcn_readfirstlane(r0 == 0.f && r1 == 0.f)) break;
+        for (int m = 0; m < 2; ++m) vf[p][m] = VT::template vtile<NC>(sv + uw * VT::BYTES, vcol, m, p);
+      update<T, DK / 16, NC, 3, false, KT>(S, sk, vf, vec + uw * VS + V_WS, 1.f, KT::col_off(g, i), g);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      dec[u] = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(vec[u * VS + V_GM])));
+    if (dec[0] == 0.f && dec[1] == 0.f) break;
     sync_lds();
   }
   const int un = 2 * it.sub + uw;
@@ -853,7 +858,7 @@ __device__ __forceinline__ void state_pass(const PassArgs& a, int block, char* s
   // order o's end state lies in slot o + 1
   float* out = a.end + ((size_t)(it.seg + 1) * a.B * a.H + bh) * a.dk * a.dv;
   store_state(S, out, a.dv, (un % cpu) * 64 + part * 16 * NC, l >> 4, l & 15, 1.f);
-  if (part == 0 && un % cpu == 0 && l == 0) a.dec[(size_t)it.seg * a.B * a.H + bh] = dec;
+  if (part == 0 && un % cpu == 0 && l == 0) a.dec[(size_t)it.seg * a.B * a.H + bh] = uw ? dec[1] : dec[0];
 }
 
 template <typename T, int DK>
