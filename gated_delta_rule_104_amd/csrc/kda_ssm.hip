@@ -256,6 +256,11 @@ struct Fetch {
       }
     }
   }
+  // nothing: a fetch that is left out would keep the last tile's registers alive
+  __device__ __forceinline__ void none() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = u32x4{0u, 0u, 0u, 0u};
+  }
   __device__ __forceinline__ void put(char* s, int tid) const {
     tid = fresh_lane(tid);  // (formed again for every chunk rather than kept in a register)
     const int row = tid / L::GPR, c = tid % L::GPR;
@@ -360,6 +365,14 @@ struct Scores {
 };
 
 // sum over a row of 16 lanes, in every lane of it
+// Sum over the four rows of 16 lanes, in every lane: both exchanges are vector moves,
+// where a shuffle goes through the LDS and waits for it.
+__device__ __forceinline__ float rows_sum(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
 __device__ __forceinline__ float row16_sum(float x) {
   x += dpp<DPP_QUAD_SWAP1>(x);
   x += dpp<DPP_QUAD_SWAP2>(x);
@@ -946,7 +959,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
   // (one where two would leave a compute unit with one workgroup)
   constexpr int NB = sizeof(T) == 2 && BWD && DK == 128 ? 1 : 2;
   constexpr int OVEC = OM + 2 * SC::BYTES, ORED = OVEC + NB * 2 * VS * 4;
-  constexpr int RED = 160 + 160 + (NPU > 3 ? 64 : 0);  // column and row sums of the ten tiles, a fourth wave's sums
+  constexpr int RED = 160 + 160;  // column and row sums of the ten tiles
   __shared__ __attribute__((aligned(16))) char smem[ORED + (BWD ? 2 * RED * 4 : 0)];
   char* const sq = smem;
   char* const sk = smem + KT::BYTES;
@@ -1004,17 +1017,30 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
   // held the issuing wave up for a sixth of the chunk's cycles (64K tokens: 501 us, in
   // parts 480)
   auto fetch_q = [&](int step) {
-    if (step >= c1 - c0) return;
+    if (step >= c1 - c0) {
+      fq.none();
+      return;
+    }
     const int c = BWD ? c1 - 1 - step : c0 + step;
     fq.template get<BWD>(Q, a.qs.t, c * CH, min(CH, len - c * CH), ofq, tid);
   };
   auto fetch_k = [&](int step) {
-    if (step >= c1 - c0) return;
+    if (step >= c1 - c0) {
+      fk.none();
+      return;
+    }
     const int c = BWD ? c1 - 1 - step : c0 + step;
     fk.template get<BWD>(K, a.ks.t, c * CH, min(CH, len - c * CH), ofk, tid);
   };
   auto fetch_v = [&](int step) {
-    if (step >= c1 - c0) return;
+    if (step >= c1 - c0) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        fv[u].none();
+        if constexpr (BWD) fw[u].none();
+      }
+      return;
+    }
     const int c = BWD ? c1 - 1 - step : c0 + step;
     const int tok0 = c * CH, n = min(CH, len - tok0);
 #pragma unroll
@@ -1085,37 +1111,69 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
         });
       }
     } else {
-      fetch_k(step + 1);
-      // (tile by tile: two products' worth of operands and sums fill the registers)
+      // tile by tile, the operands of its three products read together
 #pragma unroll 1
       for (int n = 0; n < kTiles<NWV>; ++n) {
         const int t = wave_tile<NWV>(wave, n);
         if (t >= 10) break;
         const int I = tile_i(t), J = tile_j(t);
-        const f32x4 acc = score_tile<T, DK>(sk, sq, krow, I, J);
+        f32x4 acc, dd[2], mm[2];
+        if constexpr (sizeof(T) == 2) {
+          const uint32_t vrow = VT::row_off(g, i);
+          typename Op<T>::F x[DK / 32], z[DK / 32], dx[2][2], dz[2][2];
+#pragma unroll
+          for (int m = 0; m < DK / 32; ++m) {
+            x[m] = KT::row(sk, krow, J, m);
+            z[m] = KT::row(sq, krow, I, m);
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              dx[u][m] = VT::row(sv + u * VT::BYTES, vrow, J, m);
+              dz[u][m] = VT::row(sv2 + u * VT::BYTES, vrow, I, m);
+            }
+          __builtin_amdgcn_sched_barrier(0);
+          acc = zero4();
+#pragma unroll
+          for (int m = 0; m < DK / 32; ++m) acc = Op<T>::mma(acc, x[m], z[m]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            dd[u] = zero4();
+#pragma unroll
+            for (int m = 0; m < 2; ++m) dd[u] = Op<T>::mma(dd[u], dx[u][m], dz[u][m]);
+          }
+        } else {
+          acc = score_tile<T, DK>(sk, sq, krow, I, J);
+        }
+        if (I == J) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) mm[u] = weigh_diag<KAPPA>(acc, vec + u * VS, I, g, i);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) mm[u] = weigh_below(acc, vec + u * VS, I, J, g, i);
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float* v = vec + u * VS;
-          const f32x4 mm = I == J ? weigh_diag<KAPPA>(acc, v, I, g, i) : weigh_below(acc, v, I, J, g, i);
-          const f32x4 dd = score_tile<T, 64>(sv + u * VT::BYTES, sv2 + u * VT::BYTES, VT::row_off(g, i), I, J);
+          if constexpr (sizeof(T) == 4) dd[u] = score_tile<T, 64>(sv + u * VT::BYTES, sv2 + u * VT::BYTES, VT::row_off(g, i), I, J);
           float* rd = red + u * RED + 16 * SC::tile(I, J);
-          const float bi = v[V_RH + 16 * I + i];
+          const float bi = vec[u * VS + V_RH + 16 * I + i];
           float cs = 0.f, rs[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float pp = mm[e] * dd[e];
+            const float pp = mm[u][e] * dd[u][e];
             cs += pp;
             rs[e] = bi * pp;
           }
-          cs += __shfl_xor(cs, 16);
-          cs += __shfl_xor(cs, 32);
+          cs = rows_sum(cs);
           if (g == 0) rd[i] = cs;
 #pragma unroll
           for (int e = 0; e < 4; ++e) rs[e] = row16_sum(rs[e]);
           if (i == 0) *reinterpret_cast<f32x4*>(rd + 160 + 4 * g) = f32x4{rs[0], rs[1], rs[2], rs[3]};
-          SC::put(sm + u * SC::BYTES, I, J, l, mm);
+          SC::put(sm + u * SC::BYTES, I, J, l, mm[u]);
         }
       }
+      fetch_k(step + 1);
     }
     if (NB == 2) {
       fill(step + 1);
@@ -1136,7 +1194,8 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
     sync_lds();
     if constexpr (BWD) {
       // the state's part of c, z.v before the chunk's own part joins z, one sum per
-      // wave, left where the score vectors were
+      // wave, left in the dead Q tile: its u-th KiB is wave u's to put, which adds unit
+      // u's sums before it does
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
         float x[4 * NC], z[4 * NC], s = 0.f;
@@ -1144,9 +1203,8 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
         gather(y, I, z);
 #pragma unroll
         for (int e = 0; e < 4 * NC; ++e) s += z[e] * x[e];
-        s += __shfl_xor(s, 16);
-        s += __shfl_xor(s, 32);
-        if (g == 0) (part < 3 ? v + 64 * part : red + uw * RED + 320)[16 * I + i] = s;
+        s = rows_sum(s);
+        if (g == 0) reinterpret_cast<float*>(sq + 1024 * uw)[64 * part + 16 * I + i] = s;
       }
     }
     typename Op<T>::F vf[NC][2];
@@ -1206,8 +1264,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
 #pragma unroll
             for (int e = 0; e < 4 * NC; ++e) d += x[e] * gy[e];
           }
-          d += __shfl_xor(d, 16);
-          d += __shfl_xor(d, 32);
+          d = rows_sum(d);
           if (g == 0 && p < n && mine)
             a.d[((size_t)it.b * a.H * cpu + (size_t)hw * cpu + (cw >> 6)) * a.T + tok0 + n - 1 - p] = d;
         }
@@ -1215,17 +1272,17 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
     }
     sync_lds();
     if constexpr (BWD) {
-      // one wave writes a unit's sums, the one that fills that unit's vectors
-      if (filler && 2 * it.sub + fu < nu && l < n) {
-        const float* rd = red + fu * RED;
-        const float* w = vec + fu * VS;
+      // one wave writes a unit's sums (not one of those that fill the vectors meanwhile)
+      if (wave < 2 && 2 * it.sub + wave < nu && l < n) {
+        const float* rd = red + wave * RED;
+        const float* w = reinterpret_cast<const float*>(sq + 1024 * wave);
         float cs = 0.f, rs = 0.f;
 #pragma unroll
-        for (int q = 0; q < NPU; ++q) cs += q < 3 ? w[64 * q + l] : rd[320 + l];
+        for (int q = 0; q < NPU; ++q) cs += w[64 * q + l];
         const int blk = l >> 4;
         for (int J = 0; J <= blk; ++J) cs += rd[16 * SC::tile(blk, J) + (l & 15)];
         for (int I = blk; I < 4; ++I) rs += rd[160 + 16 * SC::tile(I, blk) + (l & 15)];
-        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)hv * cpu + (2 * it.sub + fu) % cpu) * a.T + tok0 + n - 1 - l;
+        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)(wave == 1 ? head[1] : head[0]) * cpu + (2 * it.sub + wave) % cpu) * a.T + tok0 + n - 1 - l;
         a.c[at] = cs;
         a.r[at] = rs;
       }
@@ -1328,19 +1385,30 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
   T fx = T(0.f), fb = T(0.f);
   // (in three parts, as above)
   auto fetch_q = [&](int step) {
-    if (step >= c1 - c0) return;
+    if (step >= c1 - c0) {
+#pragma unroll
+      for (int h = 0; h < HG; ++h) fq[h].none();
+      return;
+    }
     const int c = REV ? c1 - 1 - step : c0 + step;
 #pragma unroll
     for (int h = 0; h < HG; ++h) fq[h].template get<REV>(Q[h], a.qs.t, c * CH, min(CH, a.T - c * CH), ofq, tid);
   };
   auto fetch_k = [&](int step) {
-    if (step >= c1 - c0) return;
+    if (step >= c1 - c0) {
+#pragma unroll
+      for (int h = 0; h < HG; ++h) fk[h].none();
+      return;
+    }
     const int c = REV ? c1 - 1 - step : c0 + step;
 #pragma unroll
     for (int h = 0; h < HG; ++h) fk[h].template get<REV>(K[h], a.ks.t, c * CH, min(CH, a.T - c * CH), ofk, tid);
   };
   auto fetch_v = [&](int step) {
-    if (step >= c1 - c0) return;
+    if (step >= c1 - c0) {
+      fv.none();
+      return;
+    }
     const int c = REV ? c1 - 1 - step : c0 + step;
     fv.template get<REV>(V, a.vs.t, c * CH, min(CH, a.T - c * CH), ofv, tid);
   };
@@ -1444,8 +1512,7 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
               dot += zz[e] * __uint_as_float(sizeof(T) == 4 ? w : (e & 1 ? w & 0xffff0000u : w << 16));
             }
             dot *= s;
-            dot += __shfl_xor(dot, 16);
-            dot += __shfl_xor(dot, 32);
+            dot = rows_sum(dot);
             // (the score vectors are no longer needed)
             if (g == 0) (wave < 4 ? v + 64 * wave : rsx + 256 * h + 64 * (wave - 4))[16 * (I0 + I) + i] = dot;
           }
