@@ -364,15 +364,32 @@ struct Scores {
   }
 };
 
-// sum over a row of 16 lanes, in every lane of it
-// Sum over the four rows of 16 lanes, in every lane: both exchanges are vector moves,
-// where a shuffle goes through the LDS and waits for it.
-__device__ __forceinline__ float rows_sum(float x) {
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+// Sums over the four rows of 16 lanes, of one, two or four values.  The exchanges are
+// vector moves (a shuffle goes through the LDS and waits for it), and halves of two
+// values share them: of N values a lane ends up with the sum of value rows_value<N>(g),
+// the same for N = 1 in every row, for N = 2 in two.
+__device__ __forceinline__ float swap_sum16(float x, float y) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
+__device__ __forceinline__ float swap_sum32(float x, float y) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+template <int N>
+__device__ __forceinline__ float rows_sum(const float (&x)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "values");
+  // lanes 0 .. 31: x[0] over rows g and g + 2; lanes 32 .. 63: x[1]
+  const float a = swap_sum32(x[0], x[N > 1 ? 1 : 0]);
+  // even rows: a over rows g and g + 1; odd rows: the other pair's
+  return swap_sum16(a, N == 4 ? swap_sum32(x[N == 4 ? 2 : 0], x[N == 4 ? 3 : 0]) : a);
+}
+template <int N>
+__device__ __forceinline__ int rows_value(int g) { return N == 4 ? (g >> 1) | ((g & 1) << 1) : N == 2 ? g >> 1 : 0; }
+// whether lane row g is the first with its value
+template <int N>
+__device__ __forceinline__ bool rows_first(int g) { return N == 4 || (N == 2 ? (g & 1) == 0 : g == 0); }
+// sum over a row of 16 lanes, in every lane of it
 __device__ __forceinline__ float row16_sum(float x) {
   x += dpp<DPP_QUAD_SWAP1>(x);
   x += dpp<DPP_QUAD_SWAP2>(x);
@@ -1165,7 +1182,8 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
             cs += pp;
             rs[e] = bi * pp;
           }
-          cs = rows_sum(cs);
+          const float c1[1] = {cs};
+          cs = rows_sum(c1);
           if (g == 0) rd[i] = cs;
 #pragma unroll
           for (int e = 0; e < 4; ++e) rs[e] = row16_sum(rs[e]);
@@ -1196,16 +1214,17 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
       // the state's part of c, z.v before the chunk's own part joins z, one sum per
       // wave, left in the dead Q tile: its u-th KiB is wave u's to put, which adds unit
       // u's sums before it does
+      float zv[4];
 #pragma unroll
       for (int I = 0; I < 4; ++I) {
-        float x[4 * NC], z[4 * NC], s = 0.f;
+        float x[4 * NC], z[4 * NC];
         VT::template place<NC>(sv2 + uw * VT::BYTES, I, i, part, g, x);
         gather(y, I, z);
+        zv[I] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4 * NC; ++e) s += z[e] * x[e];
-        s = rows_sum(s);
-        if (g == 0) reinterpret_cast<float*>(sq + 1024 * uw)[64 * part + 16 * I + i] = s;
+        for (int e = 0; e < 4 * NC; ++e) zv[I] += z[e] * x[e];
       }
+      reinterpret_cast<float*>(sq + 1024 * uw)[64 * part + 16 * rows_value<4>(g) + i] = rows_sum(zv);
     }
     typename Op<T>::F vf[NC][2];
     const uint32_t vcol = VT::template vtile_off<NC>(g, i, part);
@@ -1252,22 +1271,24 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
     if constexpr (BWD) {
       // dO.v of the unit's rows, 64 / NPU rows a wave
       if (a.D) {
+        constexpr int RI = 4 / NPU;
+        float d[RI];
 #pragma unroll
-        for (int r = 0; r < 4 / NPU; ++r) {
-          const int I = part * (4 / NPU) + r, p = 16 * I + i;
-          float d = 0.f;
+        for (int r = 0; r < RI; ++r) {
+          d[r] = 0.f;
 #pragma unroll
           for (int w = 0; w < 4 / NC; ++w) {
             float x[4 * NC], gy[4 * NC];
-            VT::template place<NC>(sv2 + uw * VT::BYTES, I, i, w, g, x);
-            VT::template place<NC>(sv + uw * VT::BYTES, I, i, w, g, gy);
+            VT::template place<NC>(sv2 + uw * VT::BYTES, part * RI + r, i, w, g, x);
+            VT::template place<NC>(sv + uw * VT::BYTES, part * RI + r, i, w, g, gy);
 #pragma unroll
-            for (int e = 0; e < 4 * NC; ++e) d += x[e] * gy[e];
+            for (int e = 0; e < 4 * NC; ++e) d[r] += x[e] * gy[e];
           }
-          d = rows_sum(d);
-          if (g == 0 && p < n && mine)
-            a.d[((size_t)it.b * a.H * cpu + (size_t)hw * cpu + (cw >> 6)) * a.T + tok0 + n - 1 - p] = d;
         }
+        const int p = 16 * (part * RI + rows_value<RI>(g)) + i;
+        const float s = rows_sum(d);
+        if (rows_first<RI>(g) && p < n && mine)
+          a.d[((size_t)it.b * a.H * cpu + (size_t)hw * cpu + (cw >> 6)) * a.T + tok0 + n - 1 - p] = s;
       }
     }
     sync_lds();
@@ -1372,8 +1393,10 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
                                                          pair_chan(t, 4 * (l >> 4)));
     }
   }
-  const int fh = wave - (NW - HG);  // the last HG waves fill the heads' decay vectors
-  const bool filler = fh >= 0;
+  // HG waves fill the heads' decay vectors: the last ones, or of eight the first, which
+  // are ahead of the others that share their SIMDs
+  const int fh = NW == 8 ? wave : wave - (NW - HG);
+  const bool filler = fh >= 0 && fh < HG;
   const int hv = it.g * R + it.sub * HG + max(0, min(fh, nh - 1));
   const T* la = static_cast<const T*>(a.la) + it.b * a.ls.b + hv * a.ls.h;
   const T* beta = static_cast<const T*>(a.beta) + it.b * a.bs.b + hv * a.bs.h;
@@ -1499,6 +1522,7 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
       for (int h = 0; h < HG; ++h) {
         float* v = vec + h * VS;
         f32x4 z[NC][NI];
+        float dots[NI];
         inter<T, DV / 16, NC, REV ? 1 : 2, NI, QT>(z, S[h], sq + h * QT::BYTES, qrow, I0);
 #pragma unroll
         for (int I = 0; I < NI; ++I) {
@@ -1511,15 +1535,17 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
               const uint32_t w = xq[I0 + I][e * (int)sizeof(T) / 4];
               dot += zz[e] * __uint_as_float(sizeof(T) == 4 ? w : (e & 1 ? w & 0xffff0000u : w << 16));
             }
-            dot *= s;
-            dot = rows_sum(dot);
-            // (the score vectors are no longer needed)
-            if (g == 0) (wave < 4 ? v + 64 * wave : rsx + 256 * h + 64 * (wave - 4))[16 * (I0 + I) + i] = dot;
+            dots[I] = s * dot;
           }
 #pragma unroll
           for (int p = 0; p < NC; ++p)
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[p][I][e] += s * z[p][I][e];
+        }
+        if constexpr (!REV) {
+          // (the score vectors are no longer needed)
+          const float dot = rows_sum(dots);
+          if (rows_first<NI>(g)) (wave < 4 ? v + 64 * wave : rsx + 256 * h + 64 * (wave - 4))[16 * (I0 + rows_value<NI>(g)) + i] = dot;
         }
         __builtin_amdgcn_sched_barrier(0);
         if (h == 0 && I0 == 0) {
