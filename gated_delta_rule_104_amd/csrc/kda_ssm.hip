@@ -31,7 +31,7 @@
 // a SIMD; the columns taken in the same paired order, so that results are stored 16
 // bytes a lane), one with fp32, whose tiles fill the LDS and whose products are long.
 // bf16 with one column tile and twice the waves took 580 us where this took 561, for
-// the outputs of 64K tokens, 64 heads of 128 x 64 (now 480).
+// the outputs of 64K tokens, 64 heads of 128 x 64 (now 464).
 //
 // Precision.  bf16 inputs are exact operands.  The scores and the state are
 // rounded once to bf16 where they multiply V and Q (both times one rounding in
@@ -42,9 +42,10 @@
 // sums it needs are taken from fp32 scores and the state terms from a two-term
 // (16-bit) state.  fp32 inputs run the same kernels on the fp32 matrix instructions.
 //
-// Measured (bf16): 64K tokens, 64 heads of 128 x 64 in 8 groups 0.61-0.65 ms, of that
-// outputs 0.48 (1.4 GB, 2.9 TB/s) and the state pass 0.25 when traced alone; gradients
-// of four 8K sequences, 32 heads in 4 groups 0.72-0.74 ms.  Bound by the latency of a
+// Measured (bf16): 64K tokens, 64 heads of 128 x 64 in 8 groups 0.60 ms, of that
+// outputs 0.46 (1.4 GB, 3.0 TB/s) and the state pass 0.24 when traced alone; gradients
+// of four 8K sequences, 32 heads in 4 groups 0.68 ms (dq and dk 0.36, reversed outputs
+// 0.20, states 0.13, the sums of partial results 0.08).  Bound by the latency of a
 // chunk's chain (scores, products, state, with a barrier between) at the two waves a
 // SIMD that the states' registers leave: vector issue 52% and matrix cores 34% of a
 // SIMD's cycles in the outputs, a third of a wave's cycles waiting for LDS.
@@ -790,8 +791,8 @@ __device__ __forceinline__ void store_state(const State<NK, NC>& S, float* p, in
 // the segment's end, so the chunks are walked from that end on and the state needs no
 // scaling; once the decay to the end is exactly zero for a unit, every token before
 // adds exactly zero (for finite inputs): its waves only keep step with the other
-// unit's, and the walk stops when both have come to zero.  Matrix cores are
-// busy half of the waves' life (three terms); the slowest decays set the kernel's end.
+// unit's, and the walk stops when both have come to zero.  The slowest decays set the
+// kernel's end: 239 us for 64K tokens, 64 heads.
 // Two buffers for the tiles took longer (268 us against 253, 64K tokens, 64 heads).
 template <typename T, int DK> constexpr int kStateLds = Tile<T, DK>::BYTES + 2 * Tile<T, 64>::BYTES + 4 * kVecNoKappa * 4;
 template <typename T, int DK, bool REV>
@@ -1337,7 +1338,7 @@ struct GroupArgs : PassArgs {
 // partial results, against operands read from LDS for one product instead of two.
 // Measured (bf16, 32 heads in 4 groups): four 8192-token sequences, 128 x 64 states, 770
 // us for the whole call and 738 wide (the partials' sum 140 -> 79 us, this kernel 354 ->
-// 386); two of them with 128 x 128 states 720 and 671; 64 x 64 602 and 602.
+// 386, since then 360); two of them with 128 x 128 states 720 and 671; 64 x 64 602 and 602.
 template <typename T, int DV, bool WIDE> constexpr int kGroupHeads = (WIDE ? 256 : 128) / DV;
 template <typename T, bool WIDE> constexpr int kGroupNC = WIDE ? 1 : kNC<T>;
 template <typename T, int DV, int DK, bool WIDE, bool REV>
