@@ -1636,6 +1636,7 @@ struct GateArgs {
   void *dla, *dbeta;
   Str3 dls, dbs;
   float* dDp;
+  bool from_zero;  // no start state
 };
 template <typename T>
 __device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs& x_) {
@@ -1699,7 +1700,8 @@ __device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs
     float base = tail;
     for (int w = 0; w < wave; ++w) base += sh[4 + w];
     tail += (sh[4] + sh[5]) + (sh[6] + sh[7]);
-    if (t >= t0) dla[b * dls.b + h * dls.h + (long long)t * dls.t] = from_f32<T>(base + s);
+    // (the first token's decay acts on the start state: nothing, and not the sums' rounding)
+    if (t >= t0) dla[b * dls.b + h * dls.h + (long long)t * dls.t] = from_f32<T>(t == 0 && x_.from_zero ? 0.f : base + s);
   }
   dsum = block_sum(dsum);
   if (tid == 0 && dDp) dDp[((size_t)b * a.nseg + seg) * a.H + h] = dsum;
@@ -1970,7 +1972,7 @@ hipError_t backward(const SsmArgs& x, hipStream_t s) {
   k.start = r.end;
   k.parts = ws + w.parts_k;
   SSM_TRY(run_groups<T>(q, k, s));
-  const GateArgs gate{f.end, r.end, q.rs, x.dla, x.dbeta, x.dls, x.dbs, x.dD ? ws + w.dDp : nullptr};
+  const GateArgs gate{f.end, r.end, q.rs, x.dla, x.dbeta, x.dls, x.dbs, x.dD ? ws + w.dDp : nullptr, x.S0 == nullptr};
   const int np = group_parts(x.H, x.G, x.dv, sizeof(T) == 2);
   const long long ng = (long long)x.B * x.H * x.nseg, npart = np > 1 ? ((long long)x.B * x.G * x.T * (x.dk / 8) + 255) / 256 : 0;
   hipLaunchKernelGGL((kda_ssm_finish_kernel<T>), dim3((unsigned)(ng + 2 * npart)), dim3(256), 0, s, q, k, gate, (int)ng, (int)npart, np);

@@ -316,6 +316,8 @@ kda_status kda_prefill_backward(const void* q, const void* k, const void* v, con
  *  - `lens` (NULL: every sequence has T tokens) is a device array of B ints:
  *    sequence b has its first lens[b] tokens (clamped to [0, T]).  The padding
  *    behind them is neither read into the results nor written.
+ *  - a workspace belongs to its call until that call's work is done: calls that
+ *    can overlap (on several streams, or in graphs replayed at once) take one each.
  * Outputs must not overlap inputs except where stated.
  */
 typedef struct { long long b, h, t; } kda_strides;

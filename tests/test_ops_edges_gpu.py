@@ -370,6 +370,18 @@ def test_groups_of_many_heads(B, H, G, T, dk, dv):
     check_grads(got, orc.ssm_backward(*ssm_ref_args(c, True, True), c["dO"], c["dS_T"]), "bf16")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 130])
+def test_first_decay_without_a_start_state(T, dt):
+    """The first token's decay multiplies nothing: its gradient is zero, not what rounding leaves."""
+    c = ssm_case(2, 4, 2, T, 64, 128, dt, seed=T)
+    args, t = ssm_args(c, True, False, False)
+    got = kda.ssm_backward(*args, t["dO"], t["dS_T"])
+    torch.cuda.synchronize()
+    assert (got["dlog_alpha"][:, :, 0] == 0).all()
+    check_grads(got, orc.ssm_backward(*ssm_ref_args(c, True, False), c["dO"], c["dS_T"]), dt)
+
+
 def test_small_workspace_walks_in_one_piece():
     c = ssm_case(1, 2, 1, 700, 64, 64, "bf16", seed=18)
     args, _ = ssm_args(c, True, True, True)
