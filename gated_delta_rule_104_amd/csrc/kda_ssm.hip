@@ -281,12 +281,18 @@ constexpr int kVecNoKappa = V_KP;  // floats of a head's vectors without KP
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The binary logarithm of a decay from log_alpha, held at -180.  A NaN passes, which a
+// maximum of the two would not let it.
+__device__ __forceinline__ float log2_decay(float x) {
+  x *= kLog2e;
+  return x < -180.f ? -180.f : x;
+}
+
 // One wave fills a head's vectors; lane r is position r with decay x.  WS is also
 // multiplied by run.  Returns e^{l_end}.
 template <bool KAPPA>
 __device__ __forceinline__ float fill_vec(float* v, int r, float x, float kappa, float rho, float rh, float run = 1.f) {
-  x *= kLog2e;
-  x = x < -180.f ? -180.f : x;  // (a NaN passes)
+  x = log2_decay(x);
   float pre = x;
   pre += dpp<DPP_ROW_SHR + 1>(pre);
   pre += dpp<DPP_ROW_SHR + 2>(pre);
@@ -934,7 +940,7 @@ __device__ __forceinline__ void merge_at(const MergeArgs& a, long long f, long l
   }
   if (!a.out) return;
   if (a.la) {
-    const float d = ex2(fmaxf(to_f32(static_cast<const T*>(a.la)[(bh / H) * a.ls.b + (bh % H) * a.ls.h]) * kLog2e, -180.f));
+    const float d = ex2(log2_decay(to_f32(static_cast<const T*>(a.la)[(bh / H) * a.ls.b + (bh % H) * a.ls.h])));
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] *= d;
   }
@@ -1313,7 +1319,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
   if (it.seg == a.nseg - 1 && a.end && mine) {
     // reversed: the state before the first token owes its own decay too
     float s = 1.f;
-    if (BWD) s = ex2(fmaxf(to_f32((static_cast<const T*>(a.la) + it.b * a.ls.b + hw * a.ls.h)[0]) * kLog2e, -180.f));
+    if (BWD) s = ex2(log2_decay(to_f32((static_cast<const T*>(a.la) + it.b * a.ls.b + hw * a.ls.h)[0])));
     store_state(S, a.end + bh * a.dk * a.dv, a.dv, cw, l >> 4, l & 15, s);
   }
 }
@@ -1671,7 +1677,7 @@ __device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs
     }
   }
   float tail = block_sum(dot);
-  if (t1 < a.T) tail *= ex2(fmaxf(to_f32(la[(long long)t1 * a.ls.t]) * kLog2e, -180.f));
+  if (t1 < a.T) tail *= ex2(log2_decay(to_f32(la[(long long)t1 * a.ls.t])));
   float dsum = 0.f;
   // 256 tokens at a time, last ones first; lane order is token order reversed
   for (int e = t1; e > t0; e -= 256) {
