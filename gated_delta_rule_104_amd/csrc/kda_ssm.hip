@@ -20,6 +20,11 @@
 // e^{l_i - l_j} = w_j E.. u_i across blocks is a product of factors <= 1, and
 // inside a block the exponential of a difference of 16-token sums.  Nothing
 // overflows for any log_alpha <= 0; -inf is held at 2^-180, which is zero in fp32.
+// That difference still loses digits behind a strong decay or a reset in the block: up
+// to 16 times 180 in fp32, whose step there is 2.4e-4.  With fp32 inputs the sums are
+// formed in 64 bits and kept in two floats (48 bits), whose differences are exact to the
+// difference's own digits.  With bf16 inputs, whose scores are rounded to 2^-9 of themselves,
+// one float is enough: 1.7e-4 of a decay at the most.
 //
 // Tiles.  v_mfma 16x16: the accumulator's rows 4g + e (g = lane / 16) are also the
 // contraction order of the next product's operand, so the scores (formed
@@ -275,31 +280,49 @@ struct Fetch {
 // Per head of the chunk, floats.  PB: sums from the block's start; U: u rho; W: w
 // kappa; RH: rho (or, in the reversed outputs, beta); IN: rho e^{l_i}; WS: kappa
 // e^{l_end - l_j}; ET: E of the four blocks; GM: e^{l_end}; KP: kappa, where it is not
-// one.  PB, U, W and KP are read only while the scores are formed.
-enum { V_PB = 0, V_U = 64, V_W = 128, V_RH = 192, V_IN = 256, V_WS = 320, V_ET = 384, V_GM = 388, V_KP = 392, V_SIZE = 456 };
-constexpr int kVecNoKappa = V_KP;  // floats of a head's vectors without KP
+// one; behind them, with fp32, what PB's rounding left.  All but RH, IN, WS and GM are
+// read only while the scores are formed.
+enum { V_PB = 0, V_U = 64, V_W = 128, V_RH = 192, V_IN = 256, V_WS = 320, V_ET = 384, V_GM = 388, V_KP = 392 };
+template <bool KAPPA> constexpr int kVecLow = KAPPA ? V_KP + 64 : V_KP;
+template <typename T, bool KAPPA> constexpr int kVecSize = kVecLow<KAPPA> + (sizeof(T) == 4 ? 64 : 0);  // floats of a head's vectors
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// The binary logarithm of a decay from log_alpha, held at -180.  A NaN passes, which a
-// maximum of the two would not let it.
-__device__ __forceinline__ float log2_decay(float x) {
-  x *= kLog2e;
-  return x < -180.f ? -180.f : x;
+// 2^x to fp32's digits: the exponent's own rounding would cost |x| 2^-24 of the result.
+__device__ __forceinline__ float ex2(double x) {
+  const float hi = (float)x, e = ex2(hi);
+  return fmaf(e, (float)(x - hi) * 0.69314718055994530942f, e);
+}
+using kda::dpp;
+template <int CTRL>
+__device__ __forceinline__ double dpp(double x) {
+  const u32x2 w = __builtin_bit_cast(u32x2, x);
+  return __builtin_bit_cast(double, u32x2{dppu<CTRL>(w[0]), dppu<CTRL>(w[1])});
 }
 
-// One wave fills a head's vectors; lane r is position r with decay x.  WS is also
+// The binary logarithm of a decay from log_alpha, held at -180, in the type that decays
+// are summed in.  A NaN passes, which a maximum of the two would not let it.
+__device__ __forceinline__ float log2_decay(bf16 la) {
+  const float x = to_f32(la) * kLog2e;
+  return x < -180.f ? -180.f : x;
+}
+__device__ __forceinline__ double log2_decay(float la) {
+  const double x = la * 1.44269504088896340736;
+  return x < -180. ? -180. : x;
+}
+
+// One wave fills a head's vectors; lane r is position r with gate la.  WS is also
 // multiplied by run.  Returns e^{l_end}.
-template <bool KAPPA>
-__device__ __forceinline__ float fill_vec(float* v, int r, float x, float kappa, float rho, float rh, float run = 1.f) {
-  x = log2_decay(x);
-  float pre = x;
+template <typename T, bool KAPPA>
+__device__ __forceinline__ float fill_vec(float* v, int r, T la, float kappa, float rho, float rh, float run = 1.f) {
+  const auto x = log2_decay(la);
+  auto pre = x;
   pre += dpp<DPP_ROW_SHR + 1>(pre);
   pre += dpp<DPP_ROW_SHR + 2>(pre);
   pre += dpp<DPP_ROW_SHR + 4>(pre);
   pre += dpp<DPP_ROW_SHR + 8>(pre);
   constexpr int DPP_ROW_SHL = 0x100;
-  float suf = dpp<DPP_ROW_SHL + 1>(x);
+  auto suf = dpp<DPP_ROW_SHL + 1>(x);
   suf += dpp<DPP_ROW_SHL + 1>(suf);
   suf += dpp<DPP_ROW_SHL + 2>(suf);
   suf += dpp<DPP_ROW_SHL + 4>(suf);
@@ -310,7 +333,8 @@ __device__ __forceinline__ float fill_vec(float* v, int r, float x, float kappa,
   const float before = (blk > 0 ? e0 : 1.f) * (blk > 1 ? e1 : 1.f) * (blk > 2 ? e2 : 1.f);
   const float after = (blk < 1 ? e1 : 1.f) * (blk < 2 ? e2 : 1.f) * (blk < 3 ? e3 : 1.f);
   const float u = ex2(pre), w = ex2(suf);
-  v[V_PB + r] = pre;
+  v[V_PB + r] = (float)pre;
+  if (sizeof(T) == 4) v[kVecLow<KAPPA> + r] = (float)(pre - (float)pre);
   v[V_U + r] = u * rho;
   v[V_W + r] = w * kappa;
   if (KAPPA) v[V_KP + r] = kappa;
@@ -411,15 +435,24 @@ __device__ __forceinline__ int tile_j(int t) { return (int)((0x0910e4u >> (2 * t
 
 // Decayed, weighted scores of a transposed tile: rows j = 16J + 4g + e, column
 // i = 16I + r16; on the diagonal and below it.
-template <bool KAPPA>
+template <typename T, bool KAPPA>
 __device__ __forceinline__ f32x4 weigh_diag(f32x4 acc, const float* v, int I, int g, int r16) {
   f32x4 m;
   const float pi = v[V_PB + 16 * I + r16];
   const f32x4 pj = *reinterpret_cast<const f32x4*>(v + V_PB + 16 * I + 4 * g);
+  f32x4 x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = pi - pj[e];
+  if constexpr (sizeof(T) == 4) {
+    const float li = v[kVecLow<KAPPA> + 16 * I + r16];
+    const f32x4 lj = *reinterpret_cast<const f32x4*>(v + kVecLow<KAPPA> + 16 * I + 4 * g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] += li - lj[e];
+  }
   f32x4 kp = {1.f, 1.f, 1.f, 1.f};
   if (KAPPA) kp = *reinterpret_cast<const f32x4*>(v + V_KP + 16 * I + 4 * g);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) m[e] = 4 * g + e <= r16 ? acc[e] * (KAPPA ? ex2(pi - pj[e]) * kp[e] : ex2(pi - pj[e])) : 0.f;
+  for (int e = 0; e < 4; ++e) m[e] = 4 * g + e <= r16 ? acc[e] * (KAPPA ? ex2(x[e]) * kp[e] : ex2(x[e])) : 0.f;
   return m;
 }
 __device__ __forceinline__ f32x4 weigh_below(f32x4 acc, const float* v, int I, int J, int g, int r16) {
@@ -800,12 +833,12 @@ __device__ __forceinline__ void store_state(const State<NK, NC>& S, float* p, in
 // unit's, and the walk stops when both have come to zero.  The slowest decays set the
 // kernel's end: 239 us for 64K tokens, 64 heads.
 // Two buffers for the tiles took longer (268 us against 253, 64K tokens, 64 heads).
-template <typename T, int DK> constexpr int kStateLds = Tile<T, DK>::BYTES + 2 * Tile<T, 64>::BYTES + 4 * kVecNoKappa * 4;
+template <typename T, int DK> constexpr int kStateLds = Tile<T, DK>::BYTES + 2 * Tile<T, 64>::BYTES + 4 * kVecSize<T, false> * 4;
 template <typename T, int DK, bool REV>
 __device__ __forceinline__ void state_pass(const PassArgs& a, int block, char* smem) {
   typedef Tile<T, DK> KT;
   typedef Tile<T, 64> VT;
-  constexpr int NC = kNC<T>, NWV = 8 / NC, NT = 64 * NWV, VS = kVecNoKappa;
+  constexpr int NC = kNC<T>, NWV = 8 / NC, NT = 64 * NWV, VS = kVecSize<T, false>;
   char* const sk = smem;
   char* const sv = smem + KT::BYTES;
   float* const vecs = reinterpret_cast<float*>(sv + 2 * VT::BYTES);  // two buffers, two units
@@ -857,7 +890,7 @@ __device__ __forceinline__ void state_pass(const PassArgs& a, int block, char* s
   auto fill = [&](int step) {
     if (!filler || step >= c1 - c0) return;
     float* v = vecs + ((step & 1) * 2 + fu) * VS;
-    run *= fill_vec<false>(v, l, to_f32(fx), REV ? 1.f : to_f32(fb), 1.f, 1.f, run);
+    run *= fill_vec<T, false>(v, l, fx, REV ? 1.f : to_f32(fb), 1.f, 1.f, run);
     if (l == 0) v[V_GM] = run;
   };
   fetch_gates(0);
@@ -940,7 +973,7 @@ __device__ __forceinline__ void merge_at(const MergeArgs& a, long long f, long l
   }
   if (!a.out) return;
   if (a.la) {
-    const float d = ex2(log2_decay(to_f32(static_cast<const T*>(a.la)[(bh / H) * a.ls.b + (bh % H) * a.ls.h])));
+    const float d = ex2(log2_decay(static_cast<const T*>(a.la)[(bh / H) * a.ls.b + (bh % H) * a.ls.h]));
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] *= d;
   }
@@ -977,7 +1010,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
   typedef Scores<T> SC;
   constexpr int NC = kNC<T>, NWV = 8 / NC, NT = 64 * NWV, NPU = NWV / 2;  // waves, threads, waves per unit
   constexpr bool KAPPA = !BWD;
-  constexpr int VS = KAPPA ? V_SIZE : kVecNoKappa;
+  constexpr int VS = kVecSize<T, KAPPA>;
   constexpr int OV = 2 * KT::BYTES, OV2 = OV + 2 * VT::BYTES, OM = OV2 + (BWD ? 2 * VT::BYTES : 0);
   // two buffers of decay vectors, the next chunk's filled beside this one's products
   // (one where two would leave a compute unit with one workgroup)
@@ -1083,7 +1116,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
   };
   auto fill = [&](int step) {
     if (filler && step < c1 - c0)
-      fill_vec<KAPPA>(vecs + ((step % NB) * 2 + fu) * VS, l, to_f32(fx), BWD ? 1.f : to_f32(fb), 1.f, to_f32(fb));
+      fill_vec<T, KAPPA>(vecs + ((step % NB) * 2 + fu) * VS, l, fx, BWD ? 1.f : to_f32(fb), 1.f, to_f32(fb));
   };
   fetch_gates(0);
   fetch_q(0);
@@ -1123,7 +1156,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
         each_tile<NWV>(wave, [&](int nt, int I, int J, auto diag) {
           f32x4 mm;
           if constexpr (decltype(diag)::value) {
-            mm = weigh_diag<KAPPA>(acc[nt], v, I, g, i);
+            mm = weigh_diag<T, KAPPA>(acc[nt], v, I, g, i);
             if constexpr (sizeof(T) == 4) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) mm[e] += 4 * g + e == i ? skip[u] : 0.f;
@@ -1172,7 +1205,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
         }
         if (I == J) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) mm[u] = weigh_diag<KAPPA>(acc, vec + u * VS, I, g, i);
+          for (int u = 0; u < 2; ++u) mm[u] = weigh_diag<T, KAPPA>(acc, vec + u * VS, I, g, i);
         } else {
 #pragma unroll
           for (int u = 0; u < 2; ++u) mm[u] = weigh_below(acc, vec + u * VS, I, J, g, i);
@@ -1319,7 +1352,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
   if (it.seg == a.nseg - 1 && a.end && mine) {
     // reversed: the state before the first token owes its own decay too
     float s = 1.f;
-    if (BWD) s = ex2(log2_decay(to_f32((static_cast<const T*>(a.la) + it.b * a.ls.b + hw * a.ls.h)[0])));
+    if (BWD) s = ex2(log2_decay((static_cast<const T*>(a.la) + it.b * a.ls.b + hw * a.ls.h)[0]));
     store_state(S, a.end + bh * a.dk * a.dv, a.dv, cw, l >> 4, l & 15, s);
   }
 }
@@ -1348,14 +1381,14 @@ struct GroupArgs : PassArgs {
 template <typename T, int DV, bool WIDE> constexpr int kGroupHeads = (WIDE ? 256 : 128) / DV;
 template <typename T, bool WIDE> constexpr int kGroupNC = WIDE ? 1 : kNC<T>;
 template <typename T, int DV, int DK, bool WIDE, bool REV>
-constexpr int kGroupLds = Tile<T, DK>::BYTES + kGroupHeads<T, DV, WIDE> * (2 * Tile<T, DV>::BYTES + Scores<T>::BYTES + 2 * (REV ? kVecNoKappa : V_SIZE) * 4) +
+constexpr int kGroupLds = Tile<T, DK>::BYTES + kGroupHeads<T, DV, WIDE> * (2 * Tile<T, DV>::BYTES + Scores<T>::BYTES + 2 * kVecSize<T, !REV> * 4) +
                           (!REV && DK / 16 / kGroupNC<T, WIDE> > 4 ? kGroupHeads<T, DV, WIDE> * 256 * 4 : 0);
 template <typename T, int DV, int DK, bool WIDE, bool REV>
 __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* smem) {
   constexpr int NC = kGroupNC<T, WIDE>, HG = kGroupHeads<T, DV, WIDE>, NW = DK / 16 / NC, NT = 64 * NW;
   constexpr int NI = NC == 2 ? 2 : 4;  // row tiles at a time: with two column tiles a half of the tokens
   constexpr bool KAPPA = !REV;
-  constexpr int VS = KAPPA ? V_SIZE : kVecNoKappa;
+  constexpr int VS = kVecSize<T, KAPPA>;
   typedef Tile<T, DV> QT;
   typedef Tile<T, DK> VT;
   typedef Scores<T> SC;
@@ -1452,7 +1485,7 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
   };
   auto fill = [&](int step) {
     if (filler && step < c1 - c0)
-      fill_vec<KAPPA>(vecs + ((step & 1) * HG + fh) * VS, l, to_f32(fx), REV ? 1.f : to_f32(fb), REV ? to_f32(fb) : 1.f, to_f32(fb));
+      fill_vec<T, KAPPA>(vecs + ((step & 1) * HG + fh) * VS, l, fx, REV ? 1.f : to_f32(fb), REV ? to_f32(fb) : 1.f, to_f32(fb));
   };
   fetch_gates(0);
   fetch_q(0);
@@ -1498,7 +1531,7 @@ __device__ __forceinline__ void group_pass(const GroupArgs& a, int block, char* 
       each_tile<NW>(turn, [&](int nt, int I, int J, auto diag) {
         f32x4 mm;
         if constexpr (decltype(diag)::value) {
-          mm = weigh_diag<KAPPA>(acc[nt], v, I, g, i);
+          mm = weigh_diag<T, KAPPA>(acc[nt], v, I, g, i);
           if constexpr (REV) {
             const float rho = v[V_RH + 16 * I + i];
 #pragma unroll
@@ -1677,7 +1710,7 @@ __device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs
     }
   }
   float tail = block_sum(dot);
-  if (t1 < a.T) tail *= ex2(log2_decay(to_f32(la[(long long)t1 * a.ls.t])));
+  if (t1 < a.T) tail *= ex2(log2_decay(la[(long long)t1 * a.ls.t]));
   float dsum = 0.f;
   // 256 tokens at a time, last ones first; lane order is token order reversed
   for (int e = t1; e > t0; e -= 256) {
