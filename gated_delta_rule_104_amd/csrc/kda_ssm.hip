@@ -43,9 +43,9 @@
 // front of an fp32 sum, like the output's own); the weighted V that updates the
 // fp32 state is carried in three bf16 terms (24 bits) where the state is a result,
 // in two (16 bits) where it only multiplies Q afterwards, rounded to fewer.  The
-// gradient of log_alpha is a difference of two sums that nearly cancel, so the score
-// sums it needs are taken from fp32 scores and the state terms from a two-term
-// (16-bit) state.  fp32 inputs run the same kernels on the fp32 matrix instructions.
+// gradient of log_alpha sums what pairs of tokens owe each other, so the score sums it
+// needs are taken from fp32 scores and the state terms from a two-term (16-bit)
+// state.  fp32 inputs run the same kernels on the fp32 matrix instructions.
 //
 // Measured (bf16): 64K tokens, 64 heads of 128 x 64 in 8 groups 0.60 ms, of that
 // outputs 0.46 (1.4 GB, 3.0 TB/s) and the state pass 0.24 when traced alone; gradients
@@ -294,6 +294,7 @@ __device__ __forceinline__ float ex2(double x) {
   return fmaf(e, (float)(x - hi) * 0.69314718055994530942f, e);
 }
 using kda::dpp;
+constexpr int DPP_ROW_SHL = 0x100;
 template <int CTRL>
 __device__ __forceinline__ double dpp(double x) {
   const u32x2 w = __builtin_bit_cast(u32x2, x);
@@ -321,7 +322,6 @@ __device__ __forceinline__ float fill_vec(float* v, int r, T la, float kappa, fl
   pre += dpp<DPP_ROW_SHR + 2>(pre);
   pre += dpp<DPP_ROW_SHR + 4>(pre);
   pre += dpp<DPP_ROW_SHR + 8>(pre);
-  constexpr int DPP_ROW_SHL = 0x100;
   auto suf = dpp<DPP_ROW_SHL + 1>(x);
   suf += dpp<DPP_ROW_SHL + 1>(suf);
   suf += dpp<DPP_ROW_SHL + 2>(suf);
@@ -420,6 +420,17 @@ __device__ __forceinline__ int rows_value(int g) { return N == 4 ? (g >> 1) | ((
 // whether lane row g is the first with its value
 template <int N>
 __device__ __forceinline__ bool rows_first(int g) { return N == 4 || (N == 2 ? (g & 1) == 0 : g == 0); }
+// The total x of a lane row (the same in its 16 lanes): sums of the rows before and behind, and of all.
+struct RowTotals {
+  float before, behind, all;
+};
+__device__ __forceinline__ RowTotals row_totals(float x, int g) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  const float even = __uint_as_float(a[0]), odd = __uint_as_float(a[1]), pair = even + odd;
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(pair), __float_as_uint(pair), false, false);
+  const float lo = __uint_as_float(b[0]), hi = __uint_as_float(b[1]);
+  return RowTotals{(g & 1 ? even : 0.f) + (g > 1 ? lo : 0.f), (g & 1 ? 0.f : odd) + (g > 1 ? 0.f : hi), lo + hi};
+}
 // sum over a row of 16 lanes, in every lane of it
 __device__ __forceinline__ float row16_sum(float x) {
   x += dpp<DPP_QUAD_SWAP1>(x);
@@ -427,6 +438,32 @@ __device__ __forceinline__ float row16_sum(float x) {
   x += dpp<0x124>(x);  // rotations by 4 and 8 within the row
   x += dpp<DPP_ROW_ROR8>(x);
   return x;
+}
+
+// sums over the lanes of a row of 16 up to this one, and behind it
+__device__ __forceinline__ float row16_prefix(float x) {
+  x += dpp<DPP_ROW_SHR + 1>(x);
+  x += dpp<DPP_ROW_SHR + 2>(x);
+  x += dpp<DPP_ROW_SHR + 4>(x);
+  x += dpp<DPP_ROW_SHR + 8>(x);
+  return x;
+}
+__device__ __forceinline__ float row16_behind(float x) {
+  x = dpp<DPP_ROW_SHL + 1>(x);
+  x += dpp<DPP_ROW_SHL + 1>(x);
+  x += dpp<DPP_ROW_SHL + 2>(x);
+  x += dpp<DPP_ROW_SHL + 4>(x);
+  x += dpp<DPP_ROW_SHL + 8>(x);
+  return x;
+}
+// Of a 16 x 16 tile, rows j = 4g + e and column i in a lane: row p becomes its sum over
+// rows j <= p, in the columns i > p, and zero in the others.
+__device__ __forceinline__ void crossing(float (&x)[4], int g, int i) {
+#pragma unroll
+  for (int e = 1; e < 4; ++e) x[e] += x[e - 1];
+  const float before = row_totals(x[3], g).before;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = i > 4 * g + e ? x[e] + before : 0.f;
 }
 
 // tile t of the ten (I, J <= I), diagonal first
@@ -798,8 +835,9 @@ struct PassArgs {
   float* end;          // end state of the last order [B, H, dk, dv], or null
   float* dec;          // state pass: e^{sum of decays} of order o at dec + o * B * H
   float* c;            // reversed outputs: [B, H * dv / 64, T] each
-  float* r;
+  float* x;
   float* d;
+  float* xe;           // [B, H * dv / 64, chunks]
   int B, H, G, T, dk, dv, nseg, seg_chunks;
   int norders;  // state pass: orders walked (the last ones' end states may not be needed)
 };
@@ -1000,9 +1038,11 @@ __global__ __launch_bounds__(256) void kda_ssm_copy_kernel(const float* src, flo
 // state on.  The next chunk's tiles are loaded to registers meanwhile.
 // TERMS: of the state's updates; three where the state is written at the end.
 // BWD: the reversed pass, which also leaves, per unit and token, what the
-// gradients of beta and log_alpha need:
-//   c[j] = sum_i P_ij (and the state's part), r[i] = sum_j beta_j P_ij (inside the
-//   chunk), d[i] = dO_i.v_i, with P_ij = (dO_i.v_j) (q_i.k_j) e^{l_i - l_j}.
+// gradients of beta, log_alpha and D need, with P_ij = (dO_i.v_j) (q_i.k_j) e^{l_i - l_j}
+// inside the chunk and s_j the same with the state, for the tokens behind the chunk:
+//   c[j] = sum_i P_ij + s_j,   d[i] = dO_i.v_i,
+//   x[t] = sum_{i >= t > j} beta_j P_ij + sum_{j < t} beta_j s_j,   xe = sum_j beta_j s_j.
+// x are the pairs that t's decay lies between.
 template <typename T, int DK, bool BWD, int TERMS>
 __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a) {
   typedef Tile<T, DK> KT;
@@ -1225,6 +1265,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
           const float c1[1] = {cs};
           cs = rows_sum(c1);
           if (g == 0) rd[i] = cs;
+          if (I == J) crossing(rs, g, i);
 #pragma unroll
           for (int e = 0; e < 4; ++e) rs[e] = row16_sum(rs[e]);
           if (i == 0) *reinterpret_cast<f32x4*>(rd + 160 + 4 * g) = f32x4{rs[0], rs[1], rs[2], rs[3]};
@@ -1331,21 +1372,41 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
           a.d[((size_t)it.b * a.H * cpu + (size_t)hw * cpu + (cw >> 6)) * a.T + tok0 + n - 1 - p] = s;
       }
     }
+    float bl = 0.f;  // (the vectors may be filled anew behind the barrier)
+    if (BWD && wave < 2) bl = vec[wave * VS + V_RH + l];
     sync_lds();
     if constexpr (BWD) {
       // one wave writes a unit's sums (not one of those that fill the vectors meanwhile)
-      if (wave < 2 && 2 * it.sub + wave < nu && l < n) {
-        const float* rd = red + wave * RED;
+      if (wave < 2 && 2 * it.sub + wave < nu) {
+        const float* rd = red + wave * RED + i;
         const float* w = reinterpret_cast<const float*>(sq + 1024 * wave);
-        float cs = 0.f, rs = 0.f;
+        float st = 0.f;
 #pragma unroll
-        for (int q = 0; q < NPU; ++q) cs += w[64 * q + l];
-        const int blk = l >> 4;
-        for (int J = 0; J <= blk; ++J) cs += rd[16 * SC::tile(blk, J) + (l & 15)];
-        for (int I = blk; I < 4; ++I) rs += rd[160 + 16 * SC::tile(I, blk) + (l & 15)];
-        const size_t at = ((size_t)it.b * a.H * cpu + (size_t)(wave == 1 ? head[1] : head[0]) * cpu + (2 * it.sub + wave) % cpu) * a.T + tok0 + n - 1 - l;
-        a.c[at] = cs;
-        a.r[at] = rs;
+        for (int q = 0; q < NPU; ++q) st += w[64 * q + l];
+        // lane = position p: of the tiles, p as a key in front of other blocks' queries,
+        // p as a query behind other blocks' keys, whole tiles across p's block, and p's own
+        float cs = st, key = 0.f, query = 0.f, across = 0.f;
+#pragma unroll
+        for (int J = 0; J < 3; ++J)
+          if (J < g) {
+            const float x = rd[16 * SC::tile(g, J)];
+            cs += x;
+            key += x;
+            for (int I = g + 1; I < 4; ++I) across += rd[160 + 16 * SC::tile(I, J)];
+          }
+        cs += rd[16 * SC::tile(g, g)];
+        for (int I = g + 1; I < 4; ++I) query += rd[160 + 16 * SC::tile(I, g)];
+        st = l < n ? bl * st : 0.f;  // (a row behind the last token has no key, but may have met an infinite state)
+        key = l < n ? bl * key : 0.f;
+        const RowTotals ends = row_totals(row16_sum(st), g);
+        const float x = rd[160 + 16 * SC::tile(g, g)] + row16_prefix(query) + row16_behind(key + st) + row16_sum(across) + ends.behind;
+        const size_t un = (size_t)it.b * a.H * cpu + (size_t)(wave == 1 ? head[1] : head[0]) * cpu + (2 * it.sub + wave) % cpu;
+        if (l < n) {
+          const size_t at = un * a.T + tok0 + n - 1 - l;
+          a.c[at] = cs;
+          a.x[at] = x;
+        }
+        if (l == 0) a.xe[un * ((a.T + CH - 1) / CH) + c] = ends.all;
       }
     }
   }
@@ -1363,7 +1424,7 @@ __global__ __launch_bounds__(512 / kNC<T>, 2) void kda_ssm_out_kernel(PassArgs a
 // one group, wave = 16 NC of the DK columns for all of them, so that the sum over
 // the heads stays in its accumulators; groups with more heads leave one partial
 // result per workgroup.  The forward pass also leaves, per head and token,
-// rs[i] = q_i . (the state's part of dq_i).
+// rs[i] = q_i . (the state's part of dq_i), what the tokens before the chunk owe i.
 struct GroupArgs : PassArgs {
   const void* qin;  // forward: the q rows
   Str3 qrs;
@@ -1668,7 +1729,19 @@ __device__ __forceinline__ void sum_parts(const float* parts, int np, T* out, St
 }
 
 // dlog_alpha and dbeta of one (b, h, segment), and the segment's share of dD.
-//     dlog_alpha[t] = sum_{i >= t in the segment} (rows_i - beta_i dbeta_i) + <S, dS> at its end
+// dlog_alpha[t] is what lies on both sides of t's decay: the pairs (i >= t > j) in t's
+// chunk, the tokens from t on with the chunk's start state, the tokens before t with the
+// gradient that enters at its end, and those two with each other, X = e^{l_end} <S, dS>:
+//     dlog_alpha[t] = x[t] + sum_{i >= t} rs_i + X.
+// The sum N = sum_i rs_i + X at a chunk's first token is also the chunk before's xe + X, so
+// that X = N - xe, from <S, dS> at the segment's end on and chunk by chunk to its
+// start.  X is zero where the chunk's decay is zero in fp32 or there is no start state.
+// Where the decay is below 2^-48 and N - xe no more than the rounding of the two (bf16:
+// states of 16 bits; fp32) it is taken as zero too: it is, unless the states before the
+// chunk are 2^30 times larger, and even then this is off by that rounding at most.
+// (One sum of q.dq - beta dbeta over the segment's tokens is shorter, but leaves all its
+// rounding in every gradient before it: 8e-5 after 2048 tokens with decays of e^-3, and
+// anything but zero at resets.)
 // slots_f, slots_r: start states of the segments in both directions.
 struct GateArgs {
   const float *slots_f, *slots_r, *rs;
@@ -1683,15 +1756,14 @@ __device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs
   T *dla = static_cast<T*>(x_.dla), *dbeta = static_cast<T*>(x_.dbeta);
   const Str3 dls = x_.dls, dbs = x_.dbs;
   float* const dDp = x_.dDp;
-  __shared__ float sh[8];
+  __shared__ float sh[12];
   const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63;
   const int seg = blockIdx.x % a.nseg;
   const long long bh = blockIdx.x / a.nseg;
   const int b = (int)(bh / a.H), h = (int)(bh % a.H), cpu = a.dv / 64;
-  const int t0 = seg * a.seg_chunks * CH, t1 = min(t0 + a.seg_chunks * CH, a.T);
+  const int nch = (a.T + CH - 1) / CH, c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
   const size_t elems = (size_t)a.dk * a.dv, all = (size_t)a.B * a.H * elems;
   const T* la = static_cast<const T*>(a.la) + b * a.ls.b + h * a.ls.h;
-  const T* beta = static_cast<const T*>(a.beta) + b * a.bs.b + h * a.bs.h;
   auto block_sum = [&](float s) {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
@@ -1709,38 +1781,50 @@ __device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs
       dot += (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
     }
   }
-  float tail = block_sum(dot);
-  if (t1 < a.T) tail *= ex2(log2_decay(la[(long long)t1 * a.ls.t]));
+  float N = block_sum(dot);
+  if (c1 < nch) N *= ex2(log2_decay(la[(long long)c1 * CH * a.ls.t]));
+  constexpr float kSmall = sizeof(T) == 2 ? 0x1p-12f : 0x1p-18f;
   float dsum = 0.f;
-  // 256 tokens at a time, last ones first; lane order is token order reversed
-  for (int e = t1; e > t0; e -= 256) {
-    const int t = e - 1 - tid;
-    float x = 0.f;
-    if (t >= t0) {
-      float c = 0.f, r = rs[bh * a.T + t];
+  // four chunks at a time, one a wave, last ones first; lane order is token order reversed
+  for (int ce = c1; ce > c0; ce -= 4) {
+    const int c = ce - 1 - wave, n = min(CH, a.T - c * CH), t = c * CH + n - 1 - l;
+    float s = 0.f, x = 0.f, xe = 0.f;
+    decltype(log2_decay(T())) dec = 0;
+    if (c >= c0 && l < n) {
+      float db = 0.f;
+      s = rs[bh * a.T + t];
+      dec = log2_decay(la[(long long)t * a.ls.t]);
       for (int u = 0; u < cpu; ++u) {
-        const size_t at = ((size_t)bh * cpu + u) * a.T + t;
-        c += a.c[at];
-        r += a.r[at];
+        const size_t un = (size_t)bh * cpu + u, at = un * a.T + t;
+        db += a.c[at];
+        x += a.x[at];
+        xe += a.xe[un * nch + c];
         if (dDp) dsum += a.d[at];
       }
-      x = r - to_f32(beta[(long long)t * a.bs.t]) * c;
-      dbeta[b * dbs.b + h * dbs.h + (long long)t * dbs.t] = from_f32<T>(c);
+      dbeta[b * dbs.b + h * dbs.h + (long long)t * dbs.t] = from_f32<T>(db);
     }
-    float s = x;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const float y = __shfl_up(s, off);
       s += l >= off ? y : 0.f;
+      dec += __shfl_xor(dec, off);
     }
     __syncthreads();
-    if (l == 63) sh[4 + wave] = s;
+    if (l == 63) sh[wave] = s;
+    if (l == 0) {
+      sh[4 + wave] = xe;
+      sh[8 + wave] = c == 0 && x_.from_zero ? -180.f : (float)dec;
+    }
     __syncthreads();
-    float base = tail;
-    for (int w = 0; w < wave; ++w) base += sh[4 + w];
-    tail += (sh[4] + sh[5]) + (sh[6] + sh[7]);
-    // (the first token's decay acts on the start state: nothing, and not the sums' rounding)
-    if (t >= t0) dla[b * dls.b + h * dls.h + (long long)t * dls.t] = from_f32<T>(t == 0 && x_.from_zero ? 0.f : base + s);
+    float X = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float y = N - sh[4 + w];
+      if (sh[8 + w] < -150.f || (sh[8 + w] < -48.f && fabsf(y) <= kSmall * fabsf(N))) y = 0.f;
+      if (w == wave) X = y;
+      N = sh[w] + y;
+    }
+    if (c >= c0 && l < n) dla[b * dls.b + h * dls.h + (long long)t * dls.t] = from_f32<T>(x + s + X);
   }
   dsum = block_sum(dsum);
   if (tid == 0 && dDp) dDp[((size_t)b * a.nseg + seg) * a.H + h] = dsum;
@@ -1937,7 +2021,7 @@ hipError_t prefill(const SsmArgs& x, hipStream_t s) {
 }
 
 struct BwdWs {
-  size_t slots_f, slots_r, dec_f, dec_r, c, r, d, rs, dDp, parts_q, parts_k, total;
+  size_t slots_f, slots_r, dec_f, dec_r, c, x, d, xe, rs, dDp, parts_q, parts_k, total;
 };
 BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg, bool bf16_io) {
   BwdWs w;
@@ -1953,8 +2037,9 @@ BwdWs backward_ws(int B, int H, int G, int T, int dk, int dv, int nseg, bool bf1
   w.dec_f = take((size_t)nseg * B * H);
   w.dec_r = take((size_t)nseg * B * H);
   w.c = take(bht * cpu);
-  w.r = take(bht * cpu);
+  w.x = take(bht * cpu);
   w.d = take(bht * cpu);
+  w.xe = take((size_t)B * H * cpu * ((T + CH - 1) / CH));
   w.rs = take(bht);
   w.dDp = take((size_t)nseg * B * H);
   const int np = group_parts(H, G, dv, bf16_io);
@@ -1973,7 +2058,7 @@ hipError_t backward(const SsmArgs& x, hipStream_t s) {
   a.ls = x.ls; a.bs = x.bs;
   a.B = x.B; a.H = x.H; a.G = x.G; a.T = x.T; a.dk = x.dk; a.dv = x.dv;
   a.nseg = x.nseg; a.seg_chunks = x.seg_chunks;
-  a.c = ws + w.c; a.r = ws + w.r; a.d = ws + w.d;
+  a.c = ws + w.c; a.x = ws + w.x; a.d = ws + w.d; a.xe = ws + w.xe;
   // start states of the segments, forwards (with the end state) and reversed; of one
   // segment dS0 comes from the outputs' pass
   PassArgs f = a, r = a;

@@ -4,7 +4,9 @@ lost, against the fp64 references in ops_oracle.py.
 Tolerances.  fp32: 2^-19 of a head's norm.  A result passes through at most about a
 thousand roundings of 2^-24 (a score's 64 or 128, a chunk's 64 tokens, the state's 64
 of every chunk that its decay still reaches), which are independent: 2^-24 sqrt(1000) =
-2^-19.  bf16: 8e-3 as in test_ops_gpu.py.
+2^-19.  dlog_alpha adds to each chunk's state terms the rounding of those behind it, one
+chunk's 2^-19 each, up to 32 of them here: 2^-19 sqrt(32) = 1.1e-5, so 1e-5 as in
+test_ops_gpu.py.  bf16: 8e-3 as there.
 """
 import math
 
@@ -13,7 +15,7 @@ import torch
 
 import gated_delta_rule_104_amd as kda
 import ops_oracle as orc
-from test_ops_gpu import TOL, gen, ssm_args, ssm_case, ssm_ref_args
+from test_ops_gpu import DT, TOL, gen, ssm_args, ssm_case, ssm_ref_args, up
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +100,72 @@ def test_slow_decays_behind_strong_ones(per_block, strong):
         assert e <= F32, n
     for n in ("dq", "dk", "dS0"):
         assert orc.rel(got[n], ref[n]) <= F32, n
+
+
+# ---------------------------------------------------------- dlog_alpha
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H,G,T,dk,dv", [(1, 2, 1, 330, 64, 64), (1, 3, 3, 200, 128, 64), (2, 5, 1, 130, 64, 128),
+                                         (1, 9, 1, 150, 128, 128)])
+def test_a_resets_gradient_is_zero(B, H, G, T, dk, dv, dt):
+    """A decay of exactly zero stays so under any small change of log_alpha.  Resets at the edges of
+    16-token blocks, chunks and segments, two in a row, at the first and last token."""
+    c = ssm_case(B, H, G, T, dk, dv, dt, seed=50 + T)
+    at = [0, 5, 15, 16, 63, 64, 65, 100, 127, 128, T - 1]
+    c["log_alpha"][:, 0, at] = -math.inf
+    c["log_alpha"][:, H - 1, at[::2]] = -math.inf
+    args, t = ssm_args(c, True, True, True)
+    got = kda.ssm_backward(*args, t["dO"], t["dS_T"])
+    torch.cuda.synchronize()
+    ref = orc.ssm_backward(*ssm_ref_args(c, True, True), c["dO"], c["dS_T"])
+    la = got["dlog_alpha"].float().cpu()
+    assert (la[c["log_alpha"] == -math.inf] == 0).all()
+    for n in ("dq", "dk", "dv", "dlog_alpha", "dbeta", "dS0", "dD"):
+        assert orc.rel(got[n], ref[n]) <= (1e-5 if n == "dS0" else TOL[dt]), n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rate", [10.0, 25.0, 40.0])
+def test_gradient_of_decays_that_leave_little(rate, dt):
+    """dlog_alpha is as small as the decay itself, and right to its own digits."""
+    H, T = 3, 330
+    c = ssm_case(1, H, 1, T, 64, 64, dt, seed=60)
+    g = torch.rand(1, H, T, generator=gen(61)) * 0.2 + 0.9
+    c["log_alpha"] = (-rate * g).to(DT[dt])
+    args, t = ssm_args(c, True, True, True)
+    got = kda.ssm_backward(*args, t["dO"], t["dS_T"])
+    torch.cuda.synchronize()
+    ref = orc.ssm_backward(*ssm_ref_args(c, True, True), c["dO"], c["dS_T"])
+    for h in range(H):
+        e = orc.rel(got["dlog_alpha"][:, h], ref["dlog_alpha"][:, h])
+        end = orc.rel(got["dlog_alpha"][:, h, 320:], ref["dlog_alpha"][:, h, 320:])  # in front of a large dS_T
+        print(f"    head {h} {e:.2e} {end:.2e}", flush=True)
+        assert max(e, end) <= TOL[dt]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradient_of_decays_over_a_long_piece(dt):
+    """Enough heads to fill the device: a sequence is not cut, and the gradient of its decays stays
+    exact over all of it, for heads that keep much and little."""
+    H, T = 512, 2048
+    assert kda.ssm_prefill_workspace_bytes(1, H, H, T, 64, 64, DT[dt]) == 0
+    heads = (0, 200, 511)
+    rates = (3.2, 1.0, 0.05)
+    g = gen(70)
+    few = ssm_case(1, 3, 3, T, 64, 64, dt, seed=71)
+    for i, r in enumerate(rates):
+        few["log_alpha"][0, i] = (-r * (0.8 + 0.4 * torch.rand(T, generator=g))).to(DT[dt])
+    t = {}
+    for n, x in few.items():
+        d = 0 if n == "D" else 1
+        t[n] = up(x).index_select(d, torch.arange(H, device="cuda") % 3)
+        at = torch.tensor(heads, device="cuda")
+        t[n].index_copy_(d, at, up(x))
+    got = kda.ssm_backward(t["q"], t["k"], t["v"], t["log_alpha"], t["beta"], t["D"], t["S0"], t["dO"], t["dS_T"])
+    torch.cuda.synchronize()
+    ref = orc.ssm_backward(*ssm_ref_args(few, True, True), few["dO"], few["dS_T"])
+    for i, h in enumerate(heads):
+        for n in ("dlog_alpha", "dbeta", "dv", "dq", "dk"):
+            e = orc.rel(got[n][:, h], ref[n][:, i])
+            first = orc.rel(got[n][:, h, :T // 8], ref[n][:, i, :T // 8])
+            print(f"    rate {rates[i]} {n} {e:.2e} {first:.2e}", flush=True)
+            assert max(e, first) <= TOL[dt], (n, rates[i])
