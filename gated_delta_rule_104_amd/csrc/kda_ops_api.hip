@@ -160,6 +160,10 @@ kda_status kda_conv_step(const void* x, const kda_strides* xs, void* state, cons
   OPS_TRY(need(state, "state"));
   OPS_TRY(need_any(weight, "weight"));
   OPS_TRY(need(o, "o"));
+  for (const void* in : {x, static_cast<const void*>(state), weight, bias})
+    if (o == in) return api_fail(KDA_ERR_UNSUPPORTED, "o must not be an input");
+  for (const void* in : {x, weight, bias})
+    if (state == in) return api_fail(KDA_ERR_UNSUPPORTED, "state must not be another input");
   a.x = x; a.w = weight; a.bias = bias; a.state_out = state; a.o = o;
   a.B = N; a.H = H; a.T = 1; a.d = d; a.K = K; a.silu = act == KDA_ACT_SILU;
   const hipError_t e = kda::launch_conv_step(a, dtype == KDA_BF16, stream);
@@ -267,6 +271,11 @@ kda_status kda_ssm_step(const void* q, const void* k, const void* v, const void*
   OPS_TRY(need_any(beta, "beta"));
   OPS_TRY(need(S, "S"));
   OPS_TRY(need(o, "o"));
+  // (a group's q and k are read by the workgroups of all its heads)
+  for (const void* in : {q, k, v, log_alpha, beta, static_cast<const void*>(S)})
+    if (o == in) return api_fail(KDA_ERR_UNSUPPORTED, "o must not be an input");
+  for (const void* in : {q, k, v})
+    if (S == in) return api_fail(KDA_ERR_UNSUPPORTED, "S must not be another input");
   const Str3 gs{H, 1, 0};
   OPS_TRY(check_gates(log_alpha, gs, beta, gs, nullptr, N, H, 1, dtype, stream));
   const hipError_t e = kda::launch_ssm_step(q, k, v, log_alpha, beta, D, S, o, N, H, G, dk, dv, dtype == KDA_BF16, stream);

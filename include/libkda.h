@@ -318,7 +318,8 @@ kda_status kda_prefill_backward(const void* q, const void* k, const void* v, con
  *    behind them is neither read into the results nor written.
  *  - a workspace belongs to its call until that call's work is done: calls that
  *    can overlap (on several streams, or in graphs replayed at once) take one each.
- * Outputs must not overlap inputs except where stated.
+ * Outputs must not overlap inputs except where stated; one that starts at the same
+ * address as an input of q, k, v or x is refused with KDA_ERR_UNSUPPORTED.
  */
 typedef struct { long long b, h, t; } kda_strides;
 

@@ -153,6 +153,26 @@ def test_ssm_backward_refusals(lib):
     assert f(gst=g) == ERR_SHAPE
 
 
+# ------------------------------------------- outputs that are inputs, one token
+def test_steps_refuse_outputs_that_are_inputs(lib):
+    """A head's q and k are read by the workgroups of its whole group, so an output in their place would
+    be read by some of them; the calls refuse every such output, as the prompt calls do."""
+    def conv_step(x=A, state=A + 64, w=A + 256, bias=A + 320, o=A + 128):
+        return lib.kda_conv_step(x, None, state, w, bias, o, None, 2, 1, 8, 4, 0, BF16, None)
+
+    def ssm_step(**p):
+        a = dict(q=A, k=A + 4096, v=A + 8192, la=A + 12288, beta=A + 12352, D=A + 12416, S=A + 16384, o=A + 65536 * 8)
+        a.update(p)
+        return lib.kda_ssm_step(*a.values(), 2, 4, 2, 64, 64, BF16, None)
+    assert conv_step(o=A) == ERR_UNSUPPORTED and conv_step(o=A + 64) == ERR_UNSUPPORTED
+    assert conv_step(o=A + 256) == ERR_UNSUPPORTED and conv_step(o=A + 320) == ERR_UNSUPPORTED
+    assert conv_step(state=A) == ERR_UNSUPPORTED
+    for n, at in (("q", A), ("k", A + 4096), ("v", A + 8192), ("la", A + 12288), ("beta", A + 12352), ("S", A + 16384)):
+        assert ssm_step(o=at) == ERR_UNSUPPORTED, n
+    for n, at in (("q", A), ("k", A + 4096), ("v", A + 8192)):
+        assert ssm_step(S=at) == ERR_UNSUPPORTED, n
+
+
 # -------------------------------------------------------------- state cache
 def test_state_cache_refusals(lib):
     def store(S=A, slots=A + 4, c=A, sc=A + 1, n=2, ns=4, H=1, dk=64, dv=64, f=0):
