@@ -73,10 +73,21 @@ struct Taps {
 };
 
 // The hardware's exponential and reciprocal, each within a unit in the last place of
-// fp32 (the exponent's product adds |x| 2^-24): with the correctly rounded division
-// and expf the four 8K prompts took 145 us, bound by vector instructions.
+// fp32: with the correctly rounded division and expf the four 8K prompts (bf16) took 145
+// us, bound by vector instructions.  The exponent's own rounding is |x| 2^-24 of the
+// result, nothing beside bf16's; fp32 takes it back: t = x c is rounded, r what that and c's
+// rounding left, e^-x = 2^t (1 + r ln 2).  (Past 128 the result is 0 or 1 whatever x
+// is, and r of an infinity would be NaN; a NaN is held too, but x multiplies the result.)
+template <typename T>
 __device__ __forceinline__ float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * x));
+  constexpr float c = -1.44269504088896340736f, c_low = -1.92596299e-8f;  // -log2(e) in two floats
+  if constexpr (sizeof(T) == 2) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(c * x));
+  } else {
+    x = fminf(fmaxf(x, -128.f), 128.f);
+    const float t = c * x, r = fmaf(c_low, x, fmaf(c, x, -t));
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t) * fmaf(r, 0.69314718055994530942f, 1.f));
+  }
 }
 
 // Row r of e, r = token + K - 1: the state's rows come first.
@@ -136,7 +147,7 @@ __global__ __launch_bounds__(256) void kda_conv_kernel(ConvArgs a, int nvec, int
         float s = taps.b[c];
 #pragma unroll
         for (int k = 0; k < K; ++k) s += taps.w[k][c] * e[i + k].v[c];
-        y.v[c] = SILU ? s * sigmoid(s) : s;
+        y.v[c] = SILU ? s * sigmoid<T>(s) : s;
       }
       if (t + i < t1) st16(o + (long long)(t + i) * a.os.t, pack<T>(y));
     }
@@ -173,7 +184,7 @@ __global__ __launch_bounds__(256) void kda_conv_step_kernel(ConvArgs a, int nvec
   }
   if constexpr (SILU) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) y.v[c] *= sigmoid(y.v[c]);
+    for (int c = 0; c < V; ++c) y.v[c] *= sigmoid<T>(y.v[c]);
   }
   st16(static_cast<T*>(a.o) + b * a.os.b + h * a.os.h + j0, pack<T>(y));
 #pragma unroll
@@ -242,7 +253,7 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(ConvArgs a, int nvec,
             float s = taps.b[c];
 #pragma unroll
             for (int k = 0; k < K; ++k) s += taps.w[k][c] * e[i + k].v[c];
-            const float sg = sigmoid(s);
+            const float sg = sigmoid<T>(s);
             gy.v[c] *= sg * (1.f + s * (1.f - sg));
           }
           if (!have) gy.v[c] = 0.f;

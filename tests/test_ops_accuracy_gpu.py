@@ -169,3 +169,50 @@ def test_gradient_of_decays_over_a_long_piece(dt):
             first = orc.rel(got[n][:, h, :T // 8], ref[n][:, i, :T // 8])
             print(f"    rate {rates[i]} {n} {e:.2e} {first:.2e}", flush=True)
             assert max(e, first) <= TOL[dt], (n, rates[i])
+
+
+# ------------------------------------------------------------------- SiLU
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_silu_far_from_zero(dt):
+    """SiLU and its derivative, element by element, where the exponential is large or small.  fp32: one
+    rounding each of the exponential (2^-23, the hardware's), its correction, the sum, the
+    reciprocal (2^-23) and the product, under 2^-21 together, and in the derivative of each
+    term.  bf16: the output's 2^-8, and the exponent's own rounding, 87 * 2^-24 of the value."""
+    T = 4096
+    x = torch.linspace(-87, 87, T * 8, dtype=torch.float64).reshape(1, 1, T, 8).to(DT[dt])
+    w = torch.tensor([0.0, 1.0]).expand(1, 8, 2).contiguous().to(DT[dt])
+    dO = torch.ones(1, 1, T, 8, dtype=DT[dt])
+    o, _ = kda.conv_prefill(up(x), up(w))
+    s = kda.conv_step(up(x[:, 0].transpose(0, 1).contiguous()), torch.zeros(T, 1, 1, 8, dtype=DT[dt], device="cuda"), up(w))
+    g = kda.conv_backward(up(x), up(w), None, None, up(dO))["dx"]
+    torch.cuda.synchronize()
+    xd = x.double()
+    sig = 1 / (1 + torch.exp(-xd))
+    tol = 2.0 ** -21 if dt == "f32" else 2.0 ** -8 + 2.0 ** -16
+    assert ((o.cpu().double() - xd * sig).abs() <= tol * (xd * sig).abs()).all()
+    assert torch.equal(s[:, 0], o[0, 0])
+    assert ((g.cpu().double() - (sig + xd * sig * (1 - sig))).abs() <= tol * sig * (1 + xd.abs())).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_not_finite_rows_stay_in_their_window(act, dt):
+    """An infinity or NaN in a valid row is in the outputs of its K tokens and channel, as from the
+    formula, and in no other."""
+    K, T = 4, 150
+    x = torch.randn(1, 2, T, 8, generator=gen(80)).to(DT[dt])
+    w = torch.rand(2, 8, K, generator=gen(81)).add(0.5).to(DT[dt])
+    clean, _ = kda.conv_prefill(up(x), up(w), activation=act)
+    bad = x.clone()
+    for c, v in enumerate((math.inf, -math.inf, math.nan)):
+        bad[0, 1, 70, c] = v
+    o, st = kda.conv_prefill(up(bad), up(w), activation=act)
+    torch.cuda.synchronize()
+    o, clean = o.cpu().float(), clean.cpu().float()
+    hit = torch.zeros(1, 2, T, 8, dtype=torch.bool)
+    hit[0, 1, 70:70 + K, :3] = True
+    assert torch.equal(o[~hit], clean[~hit])
+    low = -math.inf if act is None else math.nan  # -inf * 0
+    for c, v in enumerate((math.inf, low, math.nan)):
+        y = o[0, 1, 70:70 + K, c]
+        assert torch.isnan(y).all() if math.isnan(v) else (y == v).all()
