@@ -355,7 +355,8 @@ kda_status kda_conv_step(const void* x, const kda_strides* xs, void* state, cons
  * Gradients of kda_conv_prefill (without lens) for dL/do = dO and dL/dstate_out =
  * dstate_out (NULL: zero): dx as x, dweight as weight, dbias as bias (NULL: not
  * written), dstate_in as state_in (NULL: not written), each in dtype; sums over
- * tokens and sequences are held in fp32 and added in a fixed order.  T >= 1.
+ * tokens and sequences are held in fp32 and added in a fixed order.  B and T are at
+ * least 1 (unless H * d is 0, when there is nothing to do).
  * The workspace (kda_conv_backward_workspace_bytes) holds partial sums.
  */
 size_t kda_conv_backward_workspace_bytes(int B, int H, int T, int d, int K, kda_dtype dtype);
@@ -414,7 +415,8 @@ kda_status kda_ssm_step(const void* q, const void* k, const void* v, const void*
  * zero).  dq, dk_ (summed over a group's heads), dv_, dlog_alpha, dbeta and dD
  * (NULL without D) take their input's shape, in dtype, dS0 fp32 (NULL: not
  * written).  Sums are fp32 in a fixed order.  The strides of dlog_alpha and
- * dbeta are free; T >= 1.
+ * dbeta are free; B and T are at least 1 (unless H is 0).  A gate of -inf has a
+ * dlog_alpha of zero.
  */
 typedef struct { kda_strides dO, dq, dk, dv, dlog_alpha, dbeta; } kda_ssm_grad_strides;
 
@@ -430,9 +432,12 @@ kda_status kda_ssm_backward(const void* q, const void* k, const void* v, const v
 /*
  * The quantised state cache: KDA or scan states (prefix snapshots, parked
  * requests) in 8 bits.  A row of dv values is cut into blocks of 32 that share a
- * power-of-two scale, so that only the rounding of each value loses anything:
- * at most half a step of the block's largest value / 127 .. 2/127 (int8), or
- * 2^-4 of the value itself (e4m3).
+ * power-of-two scale 2^p, the smallest (at least 2^-126) that brings the block's
+ * largest value to at most 127 (int8) or 448 (e4m3), so that only the rounding of
+ * each value loses anything: at most 2^(p-1), that is, 1/254 to 1/127 of the
+ * block's largest value (int8), or the larger of 2^-4 of the value itself and
+ * 2^(p-10) (e4m3).  A value far below its block's largest becomes zero: up to
+ * 2^(p-1) (int8) or 2^(p-10) (e4m3, about 2^-18 of the largest).
  *   S      : [n, H, dk, dv] fp32 (S_snap of kda_chunk_prefill_snap as it stands)
  *   slots  : [n] ints on the device, the cache entry of each state.  Store skips
  *            entries outside [0, nslots); of entries that name the same slot

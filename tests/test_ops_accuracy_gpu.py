@@ -216,3 +216,25 @@ def test_not_finite_rows_stay_in_their_window(act, dt):
     for c, v in enumerate((math.inf, low, math.nan)):
         y = o[0, 1, 70:70 + K, c]
         assert torch.isnan(y).all() if math.isnan(v) else (y == v).all()
+
+
+# ------------------------------------------------------------- state cache
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_state_cache_loses_no_more_than_stated(fmt):
+    """Values from a block's largest down to 2^-30 of it: off by 2^(p-1) (int8) or the larger of 2^-4 of
+    themselves and 2^(p-10) (e4m3, whose subnormals share one step of 2^-9); the smallest are zero."""
+    g = gen(90)
+    S = torch.randn(2, 3, 64, 64, generator=g) * torch.exp2(-30 * torch.rand(2, 3, 64, 64, generator=g))
+    S = S * torch.exp2(torch.randint(-60, 60, (2, 3, 64, 1), generator=g).float())
+    cache, scales = kda.state_cache(2, 3, 64, 64, fmt, "cuda")
+    slots = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    kda.state_store(up(S), slots, cache, scales)
+    back = kda.state_load(cache, scales, slots)
+    torch.cuda.synchronize()
+    p, _ = orc.quantise(S, 127.0 if fmt == "int8" else 448.0)
+    unit = torch.exp2(p).repeat_interleave(32, -1)
+    x, off = S.double(), (back.cpu().double() - S.double()).abs()
+    bound = unit / 2 if fmt == "int8" else torch.maximum(x.abs() / 16, unit / 1024)
+    assert (off <= bound).all()
+    least = unit / 2 if fmt == "int8" else unit / 1024
+    assert (back.cpu()[x.abs() < least] == 0).all() and (off > x.abs() / 16).any()
