@@ -238,3 +238,35 @@ def test_state_cache_loses_no_more_than_stated(fmt):
     assert (off <= bound).all()
     least = unit / 2 if fmt == "int8" else unit / 1024
     assert (back.cpu()[x.abs() < least] == 0).all() and (off > x.abs() / 16).any()
+
+
+# ------------------------------------------------------- one head, many segments
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_one_head_in_many_segments(dt):
+    """A single head of 16384 tokens is cut into as many segments as the device has room for (64 or
+    128 tokens each): decays that reach over many of them, results and gradients."""
+    T = 16384
+    assert kda.ssm_prefill_workspace_bytes(1, 1, 1, T, 64, 64, DT[dt]) >= 100 * 64 * 64 * 4
+    c = ssm_case(1, 1, 1, T, 64, 64, dt, seed=95, slow=0.02)
+    args, t = ssm_args(c, True, True, True)
+    o, S = kda.ssm_prefill(*args)
+    got = kda.ssm_backward(*args, t["dO"], t["dS_T"])
+    torch.cuda.synchronize()
+    ro, rS = orc.ssm(*ssm_ref_args(c, True, True))
+    assert orc.rel(o, ro) <= TOL[dt] and orc.rel(S, rS) <= 1e-5
+    ref = orc.ssm_backward(*ssm_ref_args(c, True, True), c["dO"], c["dS_T"])
+    for n, x in got.items():
+        if n == "dD":
+            continue
+        e = orc.rel(x, ref[n])
+        print(f"    {n} {e:.2e}", flush=True)
+        assert e <= (1e-5 if n == "dS0" else TOL[dt]), n
+    # dD is one sum of 2^20 products of both signs, which may leave any part of them.  Each is in its
+    # own rounding and in those of at most 127 sums on its way (8 in a lane, 3 of lanes, 2 tokens of a
+    # thread, 8 of a block, 64 segments of a wave, 2 at the end); the sums of one level are of
+    # disjoint products, so their roundings are at most 2^-24 of the products' root sum of
+    # squares a level where the signs are independent: 2^-17 of it together.
+    norm = float((c["dO"].double() * c["v"].double()).norm())
+    off = abs(float(got["dD"]) - float(ref["dD"]))
+    print(f"    dD off {off:.2e} of {float(ref['dD']):.2e}, products {norm:.2e}", flush=True)
+    assert off <= 2.0 ** -17 * norm + (2.0 ** -8 * abs(float(ref["dD"])) if dt == "bf16" else 0)
