@@ -8,8 +8,9 @@
 // multiply-adds.  A lane owns one 16-byte group of channels of a run of tokens
 // and keeps the K - 1 rows before the current one in registers, so only the
 // first rows of a run are read twice.  Sums are fp32, rounded once on the store.
-// Measured: four 8192-token sequences of 4096 channels, bf16 with SiLU, 113 us (4.85
-// TB/s), gradients 181 us (4.8 TB/s); one token of 256 sequences 6.8 us.
+// Measured: four 8192-token sequences of 4096 channels, bf16 with SiLU, 113 us (4.9
+// TB/s), gradients 181 us (4.8 TB/s); fp32 217 and 346 us (twice the bytes); one token of 256
+// sequences 6.6 us, a chain of latencies (index divisions, taps, one row) and not HBM.
 #include "kda_ops.hpp"
 
 namespace kda {

@@ -23,8 +23,8 @@
 // That difference still loses digits behind a strong decay or a reset in the block: up
 // to 16 times 180 in fp32, whose step there is 2.4e-4.  With fp32 inputs the sums are
 // formed in 64 bits and kept in two floats (48 bits), whose differences are exact to the
-// difference's own digits.  With bf16 inputs, whose scores are rounded to 2^-9 of themselves,
-// one float is enough: 1.7e-4 of a decay at the most.
+// difference's own digits.  With bf16 inputs, whose scores are rounded by up to 2^-8 of
+// themselves, one float is enough: it costs a decay 2e-4 or so, with a reset every second token.
 //
 // Tiles.  v_mfma 16x16: the accumulator's rows 4g + e (g = lane / 16) are also the
 // contraction order of the next product's operand, so the scores (formed
@@ -36,7 +36,8 @@
 // a SIMD; the columns taken in the same paired order, so that results are stored 16
 // bytes a lane), one with fp32, whose tiles fill the LDS and whose products are long.
 // bf16 with one column tile and twice the waves took 580 us where this took 561, for
-// the outputs of 64K tokens, 64 heads of 128 x 64 (now 464).
+// the outputs of 64K tokens, 64 heads of 128 x 64 (now 464 in the same trace, of a
+// process's first calls; 375 after some tens of calls).
 //
 // Precision.  bf16 inputs are exact operands.  The scores and the state are
 // rounded once to bf16 where they multiply V and Q (both times one rounding in
@@ -47,13 +48,16 @@
 // needs are taken from fp32 scores and the state terms from a two-term (16-bit)
 // state.  fp32 inputs run the same kernels on the fp32 matrix instructions.
 //
-// Measured (bf16): 64K tokens, 64 heads of 128 x 64 in 8 groups 0.60 ms, of that
-// outputs 0.46 (1.4 GB, 3.0 TB/s) and the state pass 0.24 when traced alone; gradients
-// of four 8K sequences, 32 heads in 4 groups 0.68 ms (dq and dk 0.36, reversed outputs
-// 0.20, states 0.13, the sums of partial results 0.08).  Bound by the latency of a
-// chunk's chain (scores, products, state, with a barrier between) at the two waves a
-// SIMD that the states' registers leave: vector issue 52% and matrix cores 34% of a
-// SIMD's cycles in the outputs, a third of a wave's cycles waiting for LDS.
+// Measured (bf16): 64K tokens, 64 heads of 128 x 64 in 8 groups 0.59 ms, of that
+// outputs 0.375 (1.4 GB, 3.75 TB/s), the state pass 0.198 and the merge 0.016; gradients
+// of four 8K sequences, 32 heads in 4 groups 0.67 ms (dq and dk 0.285, reversed outputs
+// 0.167, states 0.109, the sums of partial results 0.080, merges and dD 0.029).  Bound by
+// the latency of a chunk's chain (scores, products, state, with a barrier between) at the
+// two waves a SIMD that the states' registers leave: vector issue 52% and matrix cores 34%
+// of a SIMD's cycles in the outputs, a third of a wave's cycles waiting for LDS.  fp32: one
+// sequence of 8192 tokens, 8 heads of 128 x 64 in 2 groups 0.078 ms, gradients 0.198.
+// Figures of variants against each other below are of the first calls of a process, in
+// which these kernels take a fifth longer (what HBM bounds does not).
 #include <mutex>
 #include <type_traits>
 
@@ -869,7 +873,7 @@ __device__ __forceinline__ void store_state(const State<NK, NC>& S, float* p, in
 // scaling; once the decay to the end is exactly zero for a unit, every token before
 // adds exactly zero (for finite inputs): its waves only keep step with the other
 // unit's, and the walk stops when both have come to zero.  The slowest decays set the
-// kernel's end: 239 us for 64K tokens, 64 heads.
+// kernel's end: 198 us for 64K tokens, 64 heads (239 in a process's first calls).
 // Two buffers for the tiles took longer (268 us against 253, 64K tokens, 64 heads).
 template <typename T, int DK> constexpr int kStateLds = Tile<T, DK>::BYTES + 2 * Tile<T, 64>::BYTES + 4 * kVecSize<T, false> * 4;
 template <typename T, int DK, bool REV>
@@ -1438,7 +1442,8 @@ struct GroupArgs : PassArgs {
 // partial results, against operands read from LDS for one product instead of two.
 // Measured (bf16, 32 heads in 4 groups): four 8192-token sequences, 128 x 64 states, 770
 // us for the whole call and 738 wide (the partials' sum 140 -> 79 us, this kernel 354 ->
-// 386, since then 360); two of them with 128 x 128 states 720 and 671; 64 x 64 602 and 602.
+// 386, since then 360, or 285 after some tens of calls); two of them with 128 x 128 states
+// 720 and 671; 64 x 64 602 and 602.
 template <typename T, int DV, bool WIDE> constexpr int kGroupHeads = (WIDE ? 256 : 128) / DV;
 template <typename T, bool WIDE> constexpr int kGroupNC = WIDE ? 1 : kNC<T>;
 template <typename T, int DV, int DK, bool WIDE, bool REV>
