@@ -79,7 +79,7 @@ struct SsmArgs {
 };
 constexpr int kSsmChunk = 64;
 // segments for a call (1: none), chunks per segment
-int ssm_plan(int B, int H, int G, int T, int dk, int dv, bool bf16_io, int cus, int* seg_chunks);
+int ssm_plan(int B, int H, int G, int T, int dk, int dv, bool bf16_io, bool gradients, int cus, int* seg_chunks);
 size_t ssm_ws_floats(int B, int H, int dk, int dv, int nseg);
 size_t ssm_backward_ws_floats(int B, int H, int G, int T, int dk, int dv, int nseg, bool bf16_io);
 hipError_t launch_ssm_prefill(const SsmArgs& a, bool bf16_io, hipStream_t stream);

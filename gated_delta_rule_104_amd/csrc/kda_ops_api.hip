@@ -101,9 +101,9 @@ kda_status ssm_dims(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype)
 struct Plan {
   int nseg, chunks;
 };
-Plan ssm_plan(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype) {
+Plan ssm_plan(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype, bool gradients) {
   Plan p;
-  p.nseg = kda::ssm_plan(B, H, G, T, dk, dv, dtype == KDA_BF16, kda::api_cu_count(), &p.chunks);
+  p.nseg = kda::ssm_plan(B, H, G, T, dk, dv, dtype == KDA_BF16, gradients, kda::api_cu_count(), &p.chunks);
   return p;
 }
 
@@ -211,7 +211,7 @@ kda_status kda_conv_backward(const void* x, const kda_strides* xs, const void* w
 
 size_t kda_ssm_prefill_workspace_bytes(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype) {
   if (B <= 0 || H <= 0 || T <= 0 || ssm_dims(B, H, G, T, dk, dv, dtype) != KDA_OK) return 0;
-  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
+  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype, false);
   return kda::ssm_ws_floats(B, H, dk, dv, p.nseg) * sizeof(float);
 }
 
@@ -245,7 +245,7 @@ kda_status kda_ssm_prefill(const void* q, const void* k, const void* v, const vo
   a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.beta = beta; a.D = D; a.S0 = S0; a.lens = lens; a.o = o; a.S_T = S_T;
   a.B = B; a.H = H; a.G = G; a.T = T; a.dk = dk; a.dv = dv;
   if (T > 0) {
-    Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
+    Plan p = ssm_plan(B, H, G, T, dk, dv, dtype, false);
     if (p.nseg > 1 && (!workspace || workspace_bytes < kda::ssm_ws_floats(B, H, dk, dv, p.nseg) * sizeof(float)))
       p = Plan{1, (T + kda::kSsmChunk - 1) / kda::kSsmChunk};
     a.nseg = p.nseg;
@@ -284,7 +284,7 @@ kda_status kda_ssm_step(const void* q, const void* k, const void* v, const void*
 
 size_t kda_ssm_backward_workspace_bytes(int B, int H, int G, int T, int dk, int dv, kda_dtype dtype) {
   if (B <= 0 || H <= 0 || T <= 0 || ssm_dims(B, H, G, T, dk, dv, dtype) != KDA_OK) return 0;
-  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
+  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype, true);
   return kda::ssm_backward_ws_floats(B, H, G, T, dk, dv, p.nseg, dtype == KDA_BF16) * sizeof(float);
 }
 
@@ -329,7 +329,7 @@ kda_status kda_ssm_backward(const void* q, const void* k, const void* v, const v
     for (const void* in : {q, k, v, log_alpha, beta, dO})
       if (out == in) return api_fail(KDA_ERR_UNSUPPORTED, "a gradient must not be an input");
   if (dS0 && (dS0 == S0 || dS0 == dS_T)) return api_fail(KDA_ERR_UNSUPPORTED, "dS0 must not be S0 or dS_T");
-  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype);
+  const Plan p = ssm_plan(B, H, G, T, dk, dv, dtype, true);
   const size_t bytes = kda::ssm_backward_ws_floats(B, H, G, T, dk, dv, p.nseg, dtype == KDA_BF16) * sizeof(float);
   if (!workspace) return api_fail(KDA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", bytes);
   if (!aligned(workspace)) return api_fail(KDA_ERR_ALIGN, "workspace is not 16-byte aligned");

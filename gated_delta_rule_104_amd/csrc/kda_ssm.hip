@@ -1738,12 +1738,13 @@ __device__ __forceinline__ void sum_parts(const float* parts, int np, T* out, St
 // chunk, the tokens from t on with the chunk's start state, the tokens before t with the
 // gradient that enters at its end, and those two with each other, X = e^{l_end} <S, dS>:
 //     dlog_alpha[t] = x[t] + sum_{i >= t} rs_i + X.
-// The sum N = sum_i rs_i + X at a chunk's first token is also the chunk before's xe + X, so
-// that X = N - xe, from <S, dS> at the segment's end on and chunk by chunk to its
-// start.  X is zero where the chunk's decay is zero in fp32 or there is no start state.
-// Where the decay is below 2^-48 and N - xe no more than the rounding of the two (bf16:
-// states of 16 bits; fp32) it is taken as zero too: it is, unless the states before the
-// chunk are 2^30 times larger, and even then this is off by that rounding at most.
+// Of a segment of one chunk, X is formed from its states.  Else the sum N = sum_i rs_i + X
+// at a chunk's first token is also the chunk before's xe + X, so that X = N - xe, from
+// <S, dS> at the segment's end on and chunk by chunk to its start.  X is zero where the
+// chunk's decay is zero in fp32 or there is no start state.  Where the decay is below 2^-20
+// and N - xe no more than the rounding of the two (bf16: states of 16 bits; fp32) it is
+// taken as zero too, which is off by that rounding at most and leaves none of it to the
+// chunks before.  Otherwise each chunk adds its own: fp32 segments end after 16 (ssm_plan).
 // (One sum of q.dq - beta dbeta over the segment's tokens is shorter, but leaves all its
 // rounding in every gradient before it: 8e-5 after 2048 tokens with decays of e^-3, and
 // anything but zero at resets.)
@@ -1767,6 +1768,7 @@ __device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs
   const long long bh = blockIdx.x / a.nseg;
   const int b = (int)(bh / a.H), h = (int)(bh % a.H), cpu = a.dv / 64;
   const int nch = (a.T + CH - 1) / CH, c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, nch);
+  const bool one = c1 - c0 == 1;
   const size_t elems = (size_t)a.dk * a.dv, all = (size_t)a.B * a.H * elems;
   const T* la = static_cast<const T*>(a.la) + b * a.ls.b + h * a.ls.h;
   auto block_sum = [&](float s) {
@@ -1779,7 +1781,7 @@ __device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs
   };
   float dot = 0.f;
   {
-    const float* p = slots_f + (seg + 1) * all + bh * elems;
+    const float* p = slots_f + (seg + (one ? 0 : 1)) * all + bh * elems;
     const float* q = slots_r + (a.nseg - 1 - seg) * all + bh * elems;
     for (size_t e = tid * 4; e < elems; e += 1024) {
       const f32x4 x = *reinterpret_cast<const f32x4*>(p + e), y = *reinterpret_cast<const f32x4*>(q + e);
@@ -1821,11 +1823,11 @@ __device__ __forceinline__ void gate_gradients(const PassArgs& a, const GateArgs
       sh[8 + wave] = c == 0 && x_.from_zero ? -180.f : (float)dec;
     }
     __syncthreads();
-    float X = 0.f;
+    float X = one ? N * ex2(dec) : 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < 4 && !one; ++w) {
       float y = N - sh[4 + w];
-      if (sh[8 + w] < -150.f || (sh[8 + w] < -48.f && fabsf(y) <= kSmall * fabsf(N))) y = 0.f;
+      if (sh[8 + w] < -150.f || (sh[8 + w] < -20.f && fabsf(y) <= kSmall * fabsf(N))) y = 0.f;
       if (w == wave) X = y;
       N = sh[w] + y;
     }
@@ -2123,14 +2125,20 @@ hipError_t backward(const SsmArgs& x, hipStream_t s) {
 // chunks: 16 heads, 512 tokens, bf16 37 -> 23 us; 8 heads, 333 tokens, fp32 55 -> 26;
 // gradients of 8 heads, 256 tokens, bf16 128 -> 68.  Past 16 bf16 chunks runs of two
 // are as good or better (8 heads, 2048 tokens: 30 us, 32 with runs of one).
-int ssm_plan(int B, int H, int G, int T, int dk, int dv, bool bf16_io, int cus, int* seg_chunks) {
+// The gradients of fp32 inputs cut every sequence after 16 chunks, however many there are:
+// the gradient of log_alpha takes <S, dS> at the cuts, and between them its rounding adds up
+// chunk by chunk (512 heads, 8192 tokens, decays of 0.999: 4e-6 of a head's norm and 1.1e-5
+// over its first tokens, with the cuts 1.2e-6; the call takes 10.9 ms, uncut 9.4, for the
+// reversed states at the cuts).  bf16's own rounding hides that.
+int ssm_plan(int B, int H, int G, int T, int dk, int dv, bool bf16_io, bool gradients, int cus, int* seg_chunks) {
   const int nch = (T + CH - 1) / CH;
   const long long np = ((long long)H / G * (dv / 64) + 1) / 2, base = (long long)B * G * np;
   const int least = bf16_io && nch > 16 ? 2 : 1;
   long long nseg = base > 0 ? (bf16_io ? 2 : 1) * (long long)cus / base : 1;
   if (nseg > nch / least) nseg = nch / least;
   if (nseg < 1 || nch < (bf16_io ? 4 : 3)) nseg = 1;
-  const int sc = (int)((nch + nseg - 1) / nseg);
+  int sc = (int)((nch + nseg - 1) / nseg);
+  if (gradients && !bf16_io && sc > 16) sc = 16;
   *seg_chunks = sc > 0 ? sc : 1;
   return nch > 0 ? (nch + *seg_chunks - 1) / *seg_chunks : 1;
 }

@@ -5,8 +5,8 @@ Tolerances.  fp32: 2^-19 of a head's norm.  A result passes through at most abou
 thousand roundings of 2^-24 (a score's 64 or 128, a chunk's 64 tokens, the state's 64
 of every chunk that its decay still reaches), which are independent: 2^-24 sqrt(1000) =
 2^-19.  dlog_alpha adds to each chunk's state terms the rounding of those behind it, one
-chunk's 2^-19 each, up to 32 of them here: 2^-19 sqrt(32) = 1.1e-5, so 1e-5 as in
-test_ops_gpu.py.  bf16: 8e-3 as there.
+chunk's 2^-19 each, up to 16 of them between two cuts of a sequence: 2^-19 sqrt(16) = 8e-6,
+so 1e-5 as in test_ops_gpu.py.  bf16: 8e-3 as there.
 """
 import math
 
@@ -143,32 +143,50 @@ def test_gradient_of_decays_that_leave_little(rate, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_gradient_of_decays_over_a_long_piece(dt):
-    """Enough heads to fill the device: a sequence is not cut, and the gradient of its decays stays
-    exact over all of it, for heads that keep much and little."""
-    H, T = 512, 2048
+@pytest.mark.parametrize("T", [1, 2, 40, 64])
+@pytest.mark.parametrize("rate", [0.1, 5.0, 9.0, 14.0])
+def test_gradient_of_decays_in_one_chunk(rate, T, dt):
+    """Between a start state and a gradient of the end state that are both larger than what the
+    decays leave of them."""
+    H = 8
+    c = ssm_case(1, H, H, T, 64, 64, dt, seed=65)
+    c["log_alpha"] = (-rate * (0.9 + 0.2 * torch.rand(1, H, T, generator=gen(66)))).to(DT[dt])
+    args, t = ssm_args(c, True, True, True)
+    got = kda.ssm_backward(*args, t["dO"], t["dS_T"])
+    torch.cuda.synchronize()
+    ref = orc.ssm_backward(*ssm_ref_args(c, True, True), c["dO"], c["dS_T"])
+    e = orc.rel(got["dlog_alpha"], ref["dlog_alpha"])
+    print(f"    {e:.2e}", flush=True)
+    assert e <= TOL[dt]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradient_of_decays_over_a_long_sequence(dt):
+    """Enough heads to fill the device, so that few cuts or none help: the gradient of the decays stays
+    exact over all of the sequence, for heads that keep much and little."""
+    H, T = 512, 8192
     assert kda.ssm_prefill_workspace_bytes(1, H, H, T, 64, 64, DT[dt]) == 0
-    heads = (0, 200, 511)
-    rates = (3.2, 1.0, 0.05)
+    rates = (3.2, 1.0, 0.3, 0.05, 0.001)
+    n = len(rates)
+    heads = [0, 101, 202, 303, 511]
+    few = ssm_case(1, n, n, T, 64, 64, dt, seed=71)
     g = gen(70)
-    few = ssm_case(1, 3, 3, T, 64, 64, dt, seed=71)
     for i, r in enumerate(rates):
         few["log_alpha"][0, i] = (-r * (0.8 + 0.4 * torch.rand(T, generator=g))).to(DT[dt])
     t = {}
-    for n, x in few.items():
-        d = 0 if n == "D" else 1
-        t[n] = up(x).index_select(d, torch.arange(H, device="cuda") % 3)
-        at = torch.tensor(heads, device="cuda")
-        t[n].index_copy_(d, at, up(x))
+    for name, x in few.items():
+        d = 0 if name == "D" else 1
+        t[name] = up(x).index_select(d, torch.arange(H, device="cuda") % n)
+        t[name].index_copy_(d, torch.tensor(heads, device="cuda"), up(x))
     got = kda.ssm_backward(t["q"], t["k"], t["v"], t["log_alpha"], t["beta"], t["D"], t["S0"], t["dO"], t["dS_T"])
     torch.cuda.synchronize()
     ref = orc.ssm_backward(*ssm_ref_args(few, True, True), few["dO"], few["dS_T"])
     for i, h in enumerate(heads):
-        for n in ("dlog_alpha", "dbeta", "dv", "dq", "dk"):
-            e = orc.rel(got[n][:, h], ref[n][:, i])
-            first = orc.rel(got[n][:, h, :T // 8], ref[n][:, i, :T // 8])
-            print(f"    rate {rates[i]} {n} {e:.2e} {first:.2e}", flush=True)
-            assert max(e, first) <= TOL[dt], (n, rates[i])
+        for name in ("dlog_alpha", "dbeta", "dv", "dq", "dk"):
+            e = orc.rel(got[name][:, h], ref[name][:, i])
+            first = orc.rel(got[name][:, h, :T // 8], ref[name][:, i, :T // 8])
+            print(f"    rate {rates[i]} {name} {e:.2e} {first:.2e}", flush=True)
+            assert max(e, first) <= TOL[dt], (name, rates[i])
 
 
 # ------------------------------------------------------------------- SiLU
