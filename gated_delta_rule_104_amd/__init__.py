@@ -25,6 +25,14 @@ Entry points (same names as the C-ABI):
     ssm_backward(q, k, v, log_alpha, beta, D, S0, dO, dS_T) -> dict of gradients
     state_cache(nslots, H, dk, dv, fmt, device)        -> (cache, scales)
     state_store(S, slots, cache, scales), state_load(cache, scales, slots) -> S
+    glr_prefill(x, log_alpha, beta=None, h0=None, ...)  -> (o, h_T)
+    glr_step(x, log_alpha, h, beta=None, ...)          -> o          (h updated in place)
+    glr_backward(x, log_alpha, beta, h0, o, dO, dh_T=None, ...) -> dict of gradients
+    rms_norm(x, weight, residual=None, gate=None, ...) -> y or (y, residual_out)
+    rms_norm_quant(x, weight, residual=None, gate=None, ...) -> (values, scales[, residual_out])
+    rms_norm_backward(x, weight, dy, dresidual_out=None, gate=None, ...) -> dict of gradients
+    draft_verify(target, draft, tokens, uniforms, ...) -> (accepted, out)
+    state_commit(S_pos, index, S)                      (S updated in place)
     set_option(name, value), get_option(name), options(**values) (context manager)
 """
 from __future__ import annotations
@@ -48,6 +56,9 @@ _DT = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 # kda_activation, kda_cache_format
 _ACT = {None: 0, "silu": 1}
 _CACHE = {torch.int8: 0, torch.float8_e4m3fn: 1}
+# kda_gate, and kda_norm_output by format and scales
+_GATE = {"sigmoid": 0, "silu": 1}
+_NORM_OUT = {("int8", "row"): 1, ("e4m3", "row"): 2, ("int8", "block"): 3, ("e4m3", "block"): 4}
 
 _lib = None
 
@@ -65,6 +76,26 @@ class _SsmStrides(ctypes.Structure):
 class _SsmGradStrides(ctypes.Structure):
     """kda_ssm_grad_strides."""
     _fields_ = [(n, _Strides) for n in ("dO", "dq", "dk", "dv", "dlog_alpha", "dbeta")]
+
+
+class _GlrStrides(ctypes.Structure):
+    """kda_glr_strides."""
+    _fields_ = [(n, _Strides) for n in ("x", "log_alpha", "beta", "o")]
+
+
+class _GlrGradStrides(ctypes.Structure):
+    """kda_glr_grad_strides."""
+    _fields_ = [(n, _Strides) for n in ("dO", "dx", "dlog_alpha", "dbeta")]
+
+
+class _NormStrides(ctypes.Structure):
+    """kda_norm_strides."""
+    _fields_ = [(n, _Strides) for n in ("x", "residual", "gate", "y", "residual_out", "scales")]
+
+
+class _NormGradStrides(ctypes.Structure):
+    """kda_norm_grad_strides."""
+    _fields_ = [(n, _Strides) for n in ("x", "gate", "dy", "dresidual_out", "dx", "dgate")]
 
 
 class KdaError(RuntimeError):
@@ -120,6 +151,26 @@ def load() -> ctypes.CDLL:
                                      [i] * 7 + [vp, sz, vp])
     lib.kda_state_store.argtypes = [vp] * 4 + [i] * 6 + [vp]
     lib.kda_state_load.argtypes = [vp] * 4 + [i] * 6 + [vp]
+    gs, fl = ctypes.POINTER(_GlrStrides), ctypes.c_float
+    lib.kda_glr_prefill_workspace_bytes.argtypes = [i] * 5
+    lib.kda_glr_prefill_workspace_bytes.restype = sz
+    lib.kda_glr_prefill.argtypes = [vp] * 7 + [gs] + [i] * 6 + [vp, sz, vp]
+    lib.kda_glr_step.argtypes = [vp] * 5 + [gs] + [i] * 5 + [vp]
+    lib.kda_glr_backward_workspace_bytes.argtypes = [i] * 5
+    lib.kda_glr_backward_workspace_bytes.restype = sz
+    lib.kda_glr_backward.argtypes = [vp] * 12 + [gs, ctypes.POINTER(_GlrGradStrides)] + [i] * 6 + [vp, sz, vp]
+    lib.kda_rms_norm.argtypes = [vp] * 7 + [ctypes.POINTER(_NormStrides)] + [i] * 5 + [fl] + [i] * 3 + [vp]
+    lib.kda_rms_norm_backward_workspace_bytes.argtypes = [i] * 6
+    lib.kda_rms_norm_backward_workspace_bytes.restype = sz
+    lib.kda_rms_norm_backward.argtypes = ([vp] * 8 + [ctypes.POINTER(_NormGradStrides)] + [i] * 5 + [fl] + [i] * 2 +
+                                          [vp, sz, vp])
+    lib.kda_draft_verify_workspace_bytes.argtypes = [i] * 4
+    lib.kda_draft_verify_workspace_bytes.restype = sz
+    lib.kda_draft_verify.argtypes = [vp, st, vp, st] + [vp] * 5 + [i] * 4 + [vp, sz, vp]
+    lib.kda_state_commit.argtypes = [vp] * 3 + [i] * 5 + [vp]
+    for f in (lib.kda_glr_prefill, lib.kda_glr_step, lib.kda_glr_backward, lib.kda_rms_norm, lib.kda_rms_norm_backward,
+              lib.kda_draft_verify, lib.kda_state_commit):
+        f.restype = i
     for f in (lib.kda_conv_prefill, lib.kda_conv_step, lib.kda_conv_backward, lib.kda_ssm_prefill, lib.kda_ssm_step,
               lib.kda_ssm_backward, lib.kda_state_store, lib.kda_state_load):
         f.restype = i
@@ -811,3 +862,243 @@ def state_load(cache, scales, slots, S=None) -> torch.Tensor:
                                _CACHE[cache.dtype], _stream())
     _check(rc, "kda_state_load")
     return S
+
+
+# ------------------------------------------------ gated linear recurrence
+def _glr_args(x, log_alpha, beta, h0, name="h0"):
+    B, H, T, d = x.shape if x.dim() == 4 else (*x.shape[:2], 1, x.shape[2])
+    dt, dev = x.dtype, _device(x, "x")
+    st = _GlrStrides(x=_view(x, "x", dt, x.shape, dev), log_alpha=_view(log_alpha, "log_alpha", dt, x.shape, dev))
+    if beta is not None:
+        st.beta = _view(beta, "beta", dt, x.shape, dev)
+    if h0 is not None:
+        _dense(h0, name, torch.float32, (B, H, d), dev)
+    return (B, H, T, d), st, dev
+
+
+def glr_prefill(x, log_alpha, beta=None, h0=None, normalise=False, lens=None, o=None, h_T=None, workspace=None):
+    """Gated linear recurrence over a prompt (kda_glr_prefill): per channel
+    h_t = exp(log_alpha_t) h_{t-1} + n_t beta_t x_t with n = 1, or sqrt(1 - exp(2 log_alpha)) with
+    normalise.  x, log_alpha, beta [B,H,T,d] (strides free, rows contiguous; beta None for 1), h0
+    [B,H,d] fp32 or None, lens [B] int32 or None.  Returns o, the state at every token (in x's memory
+    order unless given, rows behind lens not written), and h_T fp32."""
+    _rank(x, "x", 4)
+    dt = _dtype(x)
+    (B, H, T, d), st, dev = _glr_args(x, log_alpha, beta, h0)
+    if lens is not None:
+        _dense(lens, "lens", torch.int32, (B,), dev)
+    if o is None:
+        o = _new_like(x)
+    st.o = _view(o, "o", x.dtype, (B, H, T, d), dev)
+    if h_T is None:
+        h_T = torch.empty(B, H, d, dtype=torch.float32, device=x.device)
+    _dense(h_T, "h_T", torch.float32, (B, H, d), dev)
+    lib = load()
+    workspace = _scratch(workspace, int(lib.kda_glr_prefill_workspace_bytes(B, H, T, d, dt)), x.device)
+    rc = lib.kda_glr_prefill(_ptr(x), _ptr(log_alpha), _ptr(beta), _ptr(h0), _ptr(lens), _ptr(o), _ptr(h_T), st, B, H, T,
+                             d, int(bool(normalise)), dt, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                             _stream())
+    _check(rc, "kda_glr_prefill")
+    return o, h_T
+
+
+def glr_step(x, log_alpha, h, beta=None, normalise=False, o=None) -> torch.Tensor:
+    """One token of the recurrence: x, log_alpha, beta [N,H,d] (strides free), h [N,H,d] fp32 updated
+    in place.  Returns o [N,H,d]."""
+    _rank(x, "x", 3)
+    dt = _dtype(x)
+    if h is None:
+        raise KdaError("h is required")
+    (N, H, _, d), st, dev = _glr_args(x, log_alpha, beta, h, "h")
+    if o is None:
+        o = torch.empty(N, H, d, dtype=x.dtype, device=dev)
+    st.o = _view(o, "o", x.dtype, (N, H, d), dev)
+    rc = load().kda_glr_step(_ptr(x), _ptr(log_alpha), _ptr(beta), _ptr(h), _ptr(o), st, N, H, d, int(bool(normalise)),
+                             dt, _stream())
+    _check(rc, "kda_glr_step")
+    return o
+
+
+def glr_backward(x, log_alpha, beta, h0, o, dO, dh_T=None, normalise=False, lens=None, workspace=None):
+    """Gradients of L = sum(dO * o) + sum(dh_T * h_T) of glr_prefill, whose outputs o are read back.
+    Returns a dict: dx, dlog_alpha, and dbeta and dh0 (fp32) where beta and h0 were given; the
+    gradients of padding are zero."""
+    _rank(x, "x", 4)
+    dt = _dtype(x)
+    (B, H, T, d), st, dev = _glr_args(x, log_alpha, beta, h0)
+    st.o = _view(o, "o", x.dtype, (B, H, T, d), dev)
+    if lens is not None:
+        _dense(lens, "lens", torch.int32, (B,), dev)
+    if dh_T is not None:
+        _dense(dh_T, "dh_T", torch.float32, (B, H, d), dev)
+    out = dict(dx=_new_like(x), dlog_alpha=_new_like(log_alpha))
+    if beta is not None:
+        out["dbeta"] = _new_like(beta)
+    gst = _GlrGradStrides(dO=_view(dO, "dO", x.dtype, (B, H, T, d), dev),
+                          **{n: _Strides(*t.stride()[:3]) for n, t in out.items()})
+    if h0 is not None:
+        out["dh0"] = _new_like(h0)
+    lib = load()
+    workspace = _scratch(workspace, int(lib.kda_glr_backward_workspace_bytes(B, H, T, d, dt)), x.device)
+    rc = lib.kda_glr_backward(_ptr(x), _ptr(log_alpha), _ptr(beta), _ptr(h0), _ptr(o), _ptr(dO), _ptr(dh_T), _ptr(lens),
+                              _ptr(out["dx"]), _ptr(out["dlog_alpha"]), _ptr(out.get("dbeta")), _ptr(out.get("dh0")), st,
+                              gst, B, H, T, d, int(bool(normalise)), dt, _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), _stream())
+    _check(rc, "kda_glr_backward")
+    return out
+
+
+# ------------------------------------------------------------------- norm
+def _gate_act(activation) -> int:
+    if activation not in _GATE:
+        raise KdaError(f"unknown gate activation {activation!r} ('sigmoid' or 'silu')")
+    return _GATE[activation]
+
+
+def _norm_args(x, weight, gate):
+    """x as [B,H,T,d] (leading dimensions of 1 for fewer), the weight's rows per head or not."""
+    _rank(x, "x", 4)
+    dev = _device(x, "x")
+    H, d = x.shape[1], x.shape[3]
+    per_head = weight is not None and weight.dim() == 2
+    if weight is not None:
+        _dense(weight, "weight", x.dtype, (H, d) if per_head else (d,), dev)
+    return x.shape, per_head, dev
+
+
+def _norm(x, weight, residual, gate, gate_activation, eps, output, y, scales, residual_out):
+    dt = _dtype(x)
+    (B, H, T, d), per_head, dev = _norm_args(x, weight, gate)
+    st = _NormStrides(x=_view(x, "x", x.dtype, x.shape, dev), y=_view(y, "y", y.dtype, x.shape, dev))
+    if residual is not None:
+        st.residual = _view(residual, "residual", x.dtype, x.shape, dev)
+        if residual_out is None:
+            residual_out = _new_like(residual)
+        st.residual_out = _view(residual_out, "residual_out", x.dtype, x.shape, dev)
+    elif residual_out is not None:
+        raise KdaError("residual_out without a residual")
+    if gate is not None:
+        st.gate = _view(gate, "gate", x.dtype, x.shape, dev)
+    if scales is not None:
+        st.scales = _Strides(*scales.stride()[:3])
+    rc = load().kda_rms_norm(_ptr(x), _ptr(residual), _ptr(gate), _ptr(weight), _ptr(y), _ptr(scales),
+                             _ptr(residual_out), st, B, H, T, d, int(per_head), eps, _gate_act(gate_activation), output,
+                             dt, _stream())
+    _check(rc, "kda_rms_norm")
+    return residual_out
+
+
+def rms_norm(x, weight, residual=None, gate=None, gate_activation="sigmoid", eps=1e-6, y=None, residual_out=None):
+    """Root-mean-square norm of rows (kda_rms_norm): s = x + residual (rounded to its type),
+    y = s (mean(s^2) + eps)^(-1/2) weight act(gate).  x, residual, gate [B,H,T,d] (strides free, rows
+    contiguous), weight [d] or [H,d] or None.  Returns y (in x's memory order unless given), and with a
+    residual (y, residual_out); residual_out may be residual itself."""
+    if y is None:
+        y = _new_like(x)
+    s = _norm(x, weight, residual, gate, gate_activation, eps, 0, y, None, residual_out)
+    return y if s is None else (y, s)
+
+
+def rms_norm_quant(x, weight, residual=None, gate=None, gate_activation="sigmoid", eps=1e-6, fmt="e4m3",
+                   scales="block", residual_out=None):
+    """rms_norm with y in 8 bits: values [B,H,T,d] (fmt "e4m3" as torch.float8_e4m3fn, or "int8"), in x's
+    memory order, and their scales: "row" one fp32 per row [B,H,T], "block" a power of two for each 32
+    values [B,H,T,d/32] as torch.float8_e8m0fnu, contiguous.  A value stands for itself times its scale.
+    Returns (values, scales), with a residual (values, scales, residual_out)."""
+    if (fmt, scales) not in _NORM_OUT:
+        raise KdaError(f"unknown 8-bit output {fmt!r}, {scales!r} ('e4m3' or 'int8', 'row' or 'block')")
+    _rank(x, "x", 4)
+    B, H, T, d = x.shape
+    if scales == "block" and d % 32:
+        raise KdaError(f"rows of {d} values are not whole blocks of 32")
+    y = _new_like(x, torch.float8_e4m3fn if fmt == "e4m3" else torch.int8)
+    if scales == "row":
+        sc = torch.empty(B, H, T, dtype=torch.float32, device=x.device)
+    else:
+        sc = torch.empty(B, H, T, d // 32, dtype=torch.float8_e8m0fnu, device=x.device)
+    s = _norm(x, weight, residual, gate, gate_activation, eps, _NORM_OUT[fmt, scales], y, sc, residual_out)
+    return (y, sc) if s is None else (y, sc, s)
+
+
+def rms_norm_backward(x, weight, dy, dresidual_out=None, gate=None, gate_activation="sigmoid", eps=1e-6, workspace=None):
+    """Gradients of rms_norm; x is what was normalised (residual_out where a residual was added).
+    Returns a dict: dx (the gradient of x and of the residual alike), dweight where a weight and dgate
+    where a gate was given."""
+    dt = _dtype(x)
+    (B, H, T, d), per_head, dev = _norm_args(x, weight, gate)
+    out = dict(dx=_new_like(x))
+    st = _NormGradStrides(x=_view(x, "x", x.dtype, x.shape, dev), dy=_view(dy, "dy", x.dtype, x.shape, dev),
+                          dx=_Strides(*out["dx"].stride()[:3]))
+    if dresidual_out is not None:
+        st.dresidual_out = _view(dresidual_out, "dresidual_out", x.dtype, x.shape, dev)
+    if gate is not None:
+        st.gate = _view(gate, "gate", x.dtype, x.shape, dev)
+        out["dgate"] = _new_like(gate)
+        st.dgate = _Strides(*out["dgate"].stride()[:3])
+    lib = load()
+    need = 0
+    if weight is not None:
+        out["dweight"] = _new_like(weight)
+        need = int(lib.kda_rms_norm_backward_workspace_bytes(B, H, T, d, int(per_head), dt))
+    workspace = _scratch(workspace, need, x.device)
+    rc = lib.kda_rms_norm_backward(_ptr(x), _ptr(gate), _ptr(weight), _ptr(dy), _ptr(dresidual_out), _ptr(out["dx"]),
+                                   _ptr(out.get("dgate")), _ptr(out.get("dweight")), st, B, H, T, d, int(per_head), eps,
+                                   _gate_act(gate_activation), dt, _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream())
+    _check(rc, "kda_rms_norm_backward")
+    return out
+
+
+# ----------------------------------------------------------------- drafts
+def draft_verify(target, draft, tokens, uniforms, counts=None, accepted=None, out=None, workspace=None):
+    """Verification of drafted tokens (kda_draft_verify): target [N,K+1,V] the target's probabilities,
+    draft [N,K,V] the draft's (None: greedy drafts), tokens [N,K] int32, uniforms [N,K+1] fp32 in [0, 1),
+    counts [N] int32 drafts of each sequence or None for K.  Rows of V are contiguous, other strides
+    free.  Returns accepted [N] and out [N,K+1] int32: the accepted drafts, the next token, then -1."""
+    _rank(target, "target", 3)
+    N, K1, V = target.shape
+    K = K1 - 1
+    if K < 0:
+        raise KdaError("target has no rows (K + 1 = 0)")
+    dt, dev = _dtype(target), _device(target, "target")
+
+    def rows(t, name, n):
+        if t.device != dev or t.dtype != target.dtype or t.shape != (N, n, V):
+            _wrong(t, name, target.dtype, (N, n, V), dev)
+            raise KdaError(f"{name} does not fit")
+        if t.stride(2) != 1 and V > 1:
+            raise KdaError(f"{name} must have contiguous rows")
+        return _Strides(t.stride(0), 0, t.stride(1))
+    ts = rows(target, "target", K1)
+    ds = rows(draft, "draft", K) if draft is not None else None
+    _dense(tokens, "tokens", torch.int32, (N, K), dev)
+    _dense(uniforms, "uniforms", torch.float32, (N, K1), dev)
+    if counts is not None:
+        _dense(counts, "counts", torch.int32, (N,), dev)
+    if accepted is None:
+        accepted = torch.empty(N, dtype=torch.int32, device=dev)
+    _dense(accepted, "accepted", torch.int32, (N,), dev)
+    if out is None:
+        out = torch.empty(N, K1, dtype=torch.int32, device=dev)
+    _dense(out, "out", torch.int32, (N, K1), dev)
+    lib = load()
+    workspace = _scratch(workspace, int(lib.kda_draft_verify_workspace_bytes(N, K, V, dt)), dev)
+    rc = lib.kda_draft_verify(_ptr(target), ts, _ptr(draft), ds, _ptr(tokens), _ptr(uniforms), _ptr(counts),
+                              _ptr(accepted), _ptr(out), N, K, V, dt, _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), _stream())
+    _check(rc, "kda_draft_verify")
+    return accepted, out
+
+
+def state_commit(S_pos, index, S) -> None:
+    """S[n] = S_pos[n, index[n]] (kda_state_commit): the states of decode_tokens' positions [N,ntok,H,dk,dv]
+    behind the accepted drafts become the states [N,H,dk,dv], in place.  Entries of index [N] int32 outside
+    [0, ntok) leave their state as it is."""
+    _rank(S_pos, "S_pos", 5)
+    N, ntok, H, dk, dv = S_pos.shape
+    dev = _device(S_pos, "S_pos")
+    _dense(S_pos, "S_pos", torch.float32, S_pos.shape, dev)
+    _dense(index, "index", torch.int32, (N,), dev)
+    _dense(S, "S", torch.float32, (N, H, dk, dv), dev)
+    rc = load().kda_state_commit(_ptr(S_pos), _ptr(index), _ptr(S), N, ntok, H, dk, dv, _stream())
+    _check(rc, "kda_state_commit")

@@ -1,0 +1,495 @@
+// Root-mean-square norm of rows of d values, with the residual's addition in front and a
+// gate behind, in the input's type or in 8 bits, and its gradients:
+//     s = x + residual (rounded to its type),  r = (mean s^2 + eps)^-1/2,  y = s r w g(gate)
+//     dn = dy w g,  ds = r (dn - s r mean(dn s r)) + ds_out,  dw = sum dy s r g,  dgate = dy s r w g'
+//
+// Every value is read and written once, so HBM bounds all of it.  A row stays in the
+// registers of the lanes that share it: 8 to 64 lanes of a wave for short rows, whose sums
+// then take lane exchanges only, and 4 or 16 waves for long ones, whose sums meet in LDS.
+// Sums are fp32 in a fixed order (lanes by a butterfly, waves in order), results rounded once.
+#include "kda_ops.hpp"
+#include "kda_vec.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int DPP_HALF_MIRROR = 0x141, DPP_MIRROR = 0x140;
+
+// Over a group of 4, 8, 16, 32 or 64 neighbouring lanes; all of them get the same bits.  (In a
+// row of 16 lanes a mirror reaches the other half, whose lanes are equal by then.)
+template <int LANES, bool MAX>
+__device__ __forceinline__ float across(float v) {
+  const auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+  v = join(v, dpp<DPP_QUAD_SWAP1>(v));
+  v = join(v, dpp<DPP_QUAD_SWAP2>(v));
+  if constexpr (LANES >= 8) v = join(v, dpp<DPP_HALF_MIRROR>(v));
+  if constexpr (LANES >= 16) v = join(v, dpp<DPP_MIRROR>(v));
+  if constexpr (LANES >= 32) v = join(v, __shfl_xor(v, 16));
+  if constexpr (LANES >= 64) v = join(v, __shfl_xor(v, 32));
+  return v;
+}
+
+// NR values of as many rows, over the lanes and waves that share a row.
+template <int LANES, int WAVES, int NR, bool MAX = false>
+__device__ __forceinline__ void row_reduce(float (&v)[NR], float* red) {
+#pragma unroll
+  for (int j = 0; j < NR; ++j) v[j] = across<LANES, MAX>(v[j]);
+  if constexpr (WAVES > 1) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();  // (red may still be read from the sum before)
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int j = 0; j < NR; ++j) red[j * WAVES + w] = v[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      v[j] = red[j * WAVES];
+#pragma unroll
+      for (int u = 1; u < WAVES; ++u) v[j] = MAX ? fmaxf(v[j], red[j * WAVES + u]) : v[j] + red[j * WAVES + u];
+    }
+  }
+}
+
+// The gate's factor and, times z's own change, its derivative.
+template <typename T>
+__device__ __forceinline__ float gate_of(float z, bool silu) {
+  float s = sigmoid<T>(z);
+  if constexpr (sizeof(T) == 4) s = z == z ? s : z;  // (sigmoid holds its argument, and so a NaN, in range)
+  return silu ? z * s : s;
+}
+template <typename T>
+__device__ __forceinline__ void gate_grad(float z, bool silu, float& g, float& dg) {
+  float s = sigmoid<T>(z);
+  if constexpr (sizeof(T) == 4) s = z == z ? s : z;
+  const float c = sigmoid<T>(-z);  // 1 - s without its cancellation
+  g = silu ? z * s : s;
+  dg = silu ? s * (1.f + z * c) : s * c;
+}
+
+// Offsets of a row in each tensor: its place (i0, i1, i2) in the dimensions that are left
+// after neighbouring ones have been joined.
+struct Place {
+  int i[3];
+  __device__ __forceinline__ Place(int row, int n1, int n2) {
+    i[2] = n2 > 1 ? row % n2 : 0;
+    const int q = n2 > 1 ? row / n2 : row;
+    i[1] = n1 > 1 ? q % n1 : 0;
+    i[0] = n1 > 1 ? q / n1 : q;
+  }
+  __device__ __forceinline__ long long at(const Str3& s) const { return i[0] * s.b + i[1] * s.h + i[2] * s.t; }
+};
+
+template <bool E4M3>
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
+  if constexpr (E4M3) {
+    const int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+  } else {
+    return ((uint32_t)(int)rintf(a) & 255u) | (((uint32_t)(int)rintf(b) & 255u) << 8) |
+           (((uint32_t)(int)rintf(c) & 255u) << 16) | ((uint32_t)(int)rintf(d) << 24);
+  }
+}
+
+// 8 or 4 values of a lane in 8 bits.
+template <typename T>
+__device__ __forceinline__ void store8(unsigned char* p, const Row<T>& y, float scale, bool e4m3) {
+  uint32_t w[kVec<T> / 4];
+#pragma unroll
+  for (int i = 0; i < kVec<T> / 4; ++i) {
+    const float a = y.v[4 * i] * scale, b = y.v[4 * i + 1] * scale, c = y.v[4 * i + 2] * scale, d = y.v[4 * i + 3] * scale;
+    w[i] = e4m3 ? quant4<true>(a, b, c, d) : quant4<false>(a, b, c, d);
+  }
+  if constexpr (kVec<T> == 8) *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
+  else *reinterpret_cast<uint32_t*>(p) = w[0];
+}
+
+template <typename T>
+__device__ __forceinline__ float most(const Row<T>& y, bool* bad) {
+  float m = 0.f;
+#pragma unroll
+  for (int c = 0; c < kVec<T>; ++c) {
+    m = fmaxf(m, fabsf(y.v[c]));
+    *bad |= !(fabsf(y.v[c]) < __builtin_inff());
+  }
+  return m;
+}
+
+// NR groups of rows per block; a row is shared by LANES lanes of WAVES waves, NV vectors of 16
+// bytes each (vector i * LANES * WAVES + lane: neighbouring lanes read neighbouring 16 bytes).
+template <typename T, int LANES, int WAVES, int NV, int NR, bool BITS8>
+__global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(NormArgs a) {
+  constexpr int V = kVec<T>, THREADS = WAVES > 4 ? 64 * WAVES : 256;
+  constexpr int PER = LANES * WAVES, GROUPS = THREADS / PER;  // lanes of a row, rows at once
+  __shared__ float red[WAVES > 1 ? NR * WAVES : 1];
+  const int lane = threadIdx.x % PER;
+  const int row0 = (int)blockIdx.x * (GROUPS * NR) + threadIdx.x / PER;
+  const int nvec = a.d / V;
+  u32x4 xr[NR][NV], rr[NR][NV], gr[NR][NV];
+  bool have[NR];
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const int row = row0 + j * GROUPS;
+    have[j] = row < a.rows;
+    const Place p(have[j] ? row : 0, a.n1, a.n2);
+    const T* x = static_cast<const T*>(a.x) + p.at(a.xs);
+    const T* r = a.residual ? static_cast<const T*>(a.residual) + p.at(a.rs) : nullptr;
+    const T* g = a.gate ? static_cast<const T*>(a.gate) + p.at(a.gs) : nullptr;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vec = i * PER + lane;
+      const bool on = have[j] && vec < nvec;
+      xr[j][i] = rr[j][i] = gr[j][i] = u32x4{0u, 0u, 0u, 0u};
+      if (on) xr[j][i] = ld16(x + vec * V);
+      if (on && r) rr[j][i] = ld16(r + vec * V);
+      if (on && g) gr[j][i] = ld16(g + vec * V);
+    }
+  }
+  float sum[NR];
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    sum[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Row<T> s = unpack<T>(xr[j][i]);
+      if (a.residual) {
+        const Row<T> r = unpack<T>(rr[j][i]);
+#pragma unroll
+        for (int c = 0; c < V; ++c) s.v[c] += r.v[c];
+        // (what is normalised is what later layers and the gradients read)
+        xr[j][i] = pack<T>(s);
+        s = unpack<T>(xr[j][i]);
+      }
+#pragma unroll
+      for (int c = 0; c < V; ++c) sum[j] = fmaf(s.v[c], s.v[c], sum[j]);
+    }
+  }
+  row_reduce<LANES, WAVES, NR>(sum, red);
+  float scale[NR], top[NR];
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    scale[j] = 1.f / sqrtf(sum[j] * a.inv_d + a.eps);
+    top[j] = 0.f;
+  }
+  const auto value = [&](int j, int i, const T* w) {
+    Row<T> y = unpack<T>(xr[j][i]);
+    const int vec = i * PER + lane;
+#pragma unroll
+    for (int c = 0; c < V; ++c) y.v[c] *= scale[j];
+    if (w) {
+      const Row<T> k = unpack<T>(vec < nvec ? ld16(w + vec * V) : u32x4{0u, 0u, 0u, 0u});
+#pragma unroll
+      for (int c = 0; c < V; ++c) y.v[c] *= k.v[c];
+    }
+    if (a.gate) {
+      const Row<T> g = unpack<T>(gr[j][i]);
+#pragma unroll
+      for (int c = 0; c < V; ++c) y.v[c] *= gate_of<T>(g.v[c], a.silu);
+    }
+    return y;
+  };
+  Row<T> keep[BITS8 ? NR : 1][BITS8 ? NV : 1];
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const Place p(have[j] ? row0 + j * GROUPS : 0, a.n1, a.n2);
+    const T* w = a.w ? static_cast<const T*>(a.w) + p.at(a.ws) : nullptr;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vec = i * PER + lane;
+      const bool on = have[j] && vec < nvec;
+      if (a.s && on) st16(static_cast<T*>(a.s) + p.at(a.ss) + vec * V, xr[j][i]);
+      Row<T> y = value(j, i, w);
+      if constexpr (!BITS8) {
+        if (on) st16(static_cast<T*>(a.y) + p.at(a.ys) + vec * V, pack<T>(y));
+      } else {
+        // (lanes behind the row's end have y = 0 r, NaN where the row's factor is not finite, as it is for the others)
+        unsigned char* out = static_cast<unsigned char*>(a.y) + p.at(a.ys) + vec * V;
+        if (a.blocks) {
+          bool off = false;
+          float m = most<T>(y, &off);
+          m = across<kVec<T> == 8 ? 4 : 8, true>(off ? __builtin_inff() : m);
+          const bool none = m == __builtin_inff();
+          // m = f 2^ex with f in [1, 2): 127 = 1.984375 2^6, 448 = 1.75 2^8
+          const uint32_t mb = __float_as_uint(m), frac = mb & 0x7fffffu;
+          const int ex = (int)(mb >> 23) - 127;
+          int e = a.e4m3 ? ex - 8 + (frac > 0x600000u) : ex - 6 + (frac > 0x7e0000u);
+          e = e < -126 ? -126 : e;
+          if (on) {
+            if (none) y = unpack<T>(u32x4{0u, 0u, 0u, 0u});
+            store8<T>(out, y, __uint_as_float((uint32_t)(127 - e) << 23), a.e4m3);
+            if ((vec * V & 31) == 0)
+              static_cast<unsigned char*>(a.scales)[p.at(a.cs) + (vec * V >> 5)] = none ? 255 : (unsigned char)(e + 127);
+          }
+        } else {
+          keep[j][i] = y;
+          top[j] = fmaxf(top[j], most<T>(y, &bad));
+        }
+      }
+    }
+    if (bad) top[j] = __builtin_inff();
+  }
+  if constexpr (BITS8) {
+    if (a.blocks) return;
+    row_reduce<LANES, WAVES, NR, true>(top, red);
+    const float limit = a.e4m3 ? 448.f : 127.f;
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      const Place p(have[j] ? row0 + j * GROUPS : 0, a.n1, a.n2);
+      // (a row of zeros, or one so small that its scale would not be a normal number, takes the smallest
+      // scale; its values are then rounded to multiples of that, like a block's)
+      const bool none = top[j] == __builtin_inff();
+      const float sc = none ? __builtin_nanf("") : fmaxf(top[j] / limit, 1.17549435e-38f), inv = 1.f / sc;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int vec = i * PER + lane;
+        if (!have[j] || vec >= nvec) continue;
+        if (none) keep[j][i] = unpack<T>(u32x4{0u, 0u, 0u, 0u});
+        store8<T>(static_cast<unsigned char*>(a.y) + p.at(a.ys) + vec * V, keep[j][i], none ? 0.f : inv, a.e4m3);
+      }
+      if (have[j] && lane == 0) static_cast<float*>(a.scales)[p.at(a.cs)] = sc;
+    }
+  }
+}
+
+// Gradients.  A block walks rows part, part + nparts, ... (in units of NR groups) of one weight row's
+// rows, so that a lane's columns stay the same and dw is summed in registers; one partial row of
+// sums per block goes to the workspace, and a second kernel adds the partials in a fixed order.
+template <typename T, int LANES, int WAVES, int NV, int NR>
+__global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_bwd_kernel(NormArgs a) {
+  constexpr int V = kVec<T>, THREADS = WAVES > 4 ? 64 * WAVES : 256;
+  constexpr int PER = LANES * WAVES, GROUPS = THREADS / PER;
+  __shared__ float red[WAVES > 1 ? 2 * NR * WAVES : 1];
+  __shared__ float cols[GROUPS > 1 ? THREADS * NV * V : 1];
+  const int lane = threadIdx.x % PER, group = threadIdx.x / PER;
+  const int part = blockIdx.x % a.nparts, hw = blockIdx.x / a.nparts;
+  const int nvec = a.d / V;
+  // rows of this weight row: (b, h, t), or (b, t) of head hw
+  const int rows = a.w_heads > 1 ? a.rows / a.w_heads : a.rows;
+  const T* w = a.w ? static_cast<const T*>(a.w) + (long long)hw * a.d : nullptr;
+  Row<T> wk[NV];
+  float dw[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int vec = i * PER + lane;
+    wk[i] = unpack<T>(w && vec < nvec ? ld16(w + vec * V) : u32x4{0u, 0u, 0u, 0u});
+    if (!w) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) wk[i].v[c] = 1.f;
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c) dw[i][c] = 0.f;
+  }
+  for (long long base = (long long)part * (GROUPS * NR); base < rows; base += (long long)a.nparts * (GROUPS * NR)) {
+    u32x4 sr[NR][NV], yr[NR][NV], gr[NR][NV], dr[NR][NV];
+    long long xo[NR], go[NR];
+    bool have[NR];
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      const long long row = base + j * GROUPS + group;
+      have[j] = row < rows;
+      Place p(have[j] ? (int)row : 0, a.w_heads > 1 ? 1 : a.n1, a.n2);
+      if (a.w_heads > 1) p.i[1] = hw;
+      const T* s = static_cast<const T*>(a.x) + p.at(a.xs);
+      const T* dy = static_cast<const T*>(a.dy) + p.at(a.dys);
+      const T* g = a.gate ? static_cast<const T*>(a.gate) + p.at(a.gs) : nullptr;
+      const T* ds = a.ds ? static_cast<const T*>(a.ds) + p.at(a.dss) : nullptr;
+      xo[j] = p.at(a.dxs);
+      go[j] = p.at(a.dgs);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int vec = i * PER + lane;
+        const bool on = have[j] && vec < nvec;
+        sr[j][i] = yr[j][i] = gr[j][i] = dr[j][i] = u32x4{0u, 0u, 0u, 0u};
+        if (on) sr[j][i] = ld16(s + vec * V);
+        if (on) yr[j][i] = ld16(dy + vec * V);
+        if (on && g) gr[j][i] = ld16(g + vec * V);
+        if (on && ds) dr[j][i] = ld16(ds + vec * V);
+      }
+    }
+    float sum[2 * NR];
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      sum[2 * j] = sum[2 * j + 1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Row<T> s = unpack<T>(sr[j][i]), dy = unpack<T>(yr[j][i]), z = unpack<T>(gr[j][i]);
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          const float dn = dy.v[c] * wk[i].v[c] * (a.gate ? gate_of<T>(z.v[c], a.silu) : 1.f);
+          sum[2 * j] = fmaf(s.v[c], s.v[c], sum[2 * j]);
+          sum[2 * j + 1] = fmaf(dn, s.v[c], sum[2 * j + 1]);
+        }
+      }
+    }
+    row_reduce<LANES, WAVES, 2 * NR>(sum, red);
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      const float r = have[j] ? 1.f / sqrtf(sum[2 * j] * a.inv_d + a.eps) : 0.f;
+      const float back = r * (r * (r * (sum[2 * j + 1] * a.inv_d)));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int vec = i * PER + lane;
+        const Row<T> s = unpack<T>(sr[j][i]), dy = unpack<T>(yr[j][i]), z = unpack<T>(gr[j][i]);
+        Row<T> dx = unpack<T>(dr[j][i]), dz;
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          float g = 1.f, dg = 0.f;
+          if (a.gate) gate_grad<T>(z.v[c], a.silu, g, dg);
+          const float n = s.v[c] * r, yn = dy.v[c] * n;
+          dx.v[c] += r * (dy.v[c] * wk[i].v[c] * g) - s.v[c] * back;
+          dz.v[c] = yn * wk[i].v[c] * dg;
+          dw[i][c] = fmaf(yn, g, dw[i][c]);
+        }
+        if (!have[j] || vec >= nvec) continue;
+        st16(static_cast<T*>(a.dx) + xo[j] + vec * V, pack<T>(dx));
+        if (a.dgate) st16(static_cast<T*>(a.dgate) + go[j] + vec * V, pack<T>(dz));
+      }
+    }
+  }
+  if (!a.dw) return;
+  float* out = a.scratch + ((size_t)part * a.w_heads + hw) * a.d;
+  if constexpr (GROUPS > 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int c = 0; c < V; ++c) cols[(group * NV * PER + i * PER + lane) * V + c] = dw[i][c];
+    __syncthreads();
+    for (int k = threadIdx.x; k < a.d; k += THREADS) {
+      float s = 0.f;
+#pragma unroll 8
+      for (int g = 0; g < GROUPS; ++g) s += cols[g * NV * PER * V + k];
+      out[k] = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vec = i * PER + lane;
+      if (vec >= nvec) continue;
+#pragma unroll
+      for (int c = 0; c < V; c += 4) *reinterpret_cast<f32x4*>(out + vec * V + c) = f32x4{dw[i][c], dw[i][c + 1], dw[i][c + 2], dw[i][c + 3]};
+    }
+  }
+}
+
+// dw[k]: the sum of the partials, 32 interleaved runs of them per column, joined in a fixed order.
+template <typename T>
+__global__ __launch_bounds__(1024) void kda_norm_dw_kernel(const float* ws, T* dw, int n, int nparts) {
+  __shared__ float red[32][32];
+  const int l = threadIdx.x & 31, u = threadIdx.x >> 5, k = blockIdx.x * 32 + l;
+  float s = 0.f;
+  if (k < n) {
+#pragma unroll 8
+    for (int p = u; p < nparts; p += 32) s += ws[(size_t)p * n + k];
+  }
+  red[u][l] = s;
+  __syncthreads();
+  if (u == 0 && k < n) {
+#pragma unroll
+    for (int i = 1; i < 32; ++i) s += red[i][l];
+    dw[k] = from_f32<T>(s);
+  }
+}
+
+// Joins neighbouring dimensions whose rows lie evenly in every tensor (and drops those of size 1), so that
+// a row's place takes few divisions and single tokens of many sequences fill whole blocks.
+void join_dims(NormArgs& a, int B, int H, int T) {
+  constexpr int N = 7;
+  Str3* const all[N] = {&a.xs, &a.rs, &a.gs, &a.ys, &a.ss, &a.ws, &a.cs};
+  struct Dim {
+    long long n = 1, st[N] = {};
+  } dims[3];
+  int k = 0;
+  for (int i = 0; i < 3; ++i) {
+    Dim d;
+    d.n = i == 0 ? B : (i == 1 ? H : T);
+    if (d.n == 1) continue;
+    bool even = k > 0;
+    for (int j = 0; j < N; ++j) {
+      d.st[j] = i == 0 ? all[j]->b : (i == 1 ? all[j]->h : all[j]->t);
+      even = even && dims[k - 1].st[j] == d.n * d.st[j];
+    }
+    if (even) d.n *= dims[--k].n;
+    dims[k++] = d;
+  }
+  const Dim none;
+  const Dim &d0 = k > 2 ? dims[0] : none, &d1 = k > 1 ? dims[k - 2] : none, &d2 = k > 0 ? dims[k - 1] : none;
+  for (int j = 0; j < N; ++j) *all[j] = Str3{d0.st[j], d1.st[j], d2.st[j]};
+  a.n1 = (int)d1.n;
+  a.n2 = (int)d2.n;
+}
+
+// Calls f(lanes, waves, vectors a lane, rows at once) with the shape for rows of nvec vectors, as
+// integral constants.  Rows of up to 64 vectors stay inside a wave, and a lane reads from four of
+// them at once so that its loads cover the latency; longer ones give a lane up to 8 vectors.
+template <int N> struct Int { static constexpr int value = N; };
+template <typename F>
+auto with_shape(int nvec, F f) {
+  if (nvec <= 8) return f(Int<8>(), Int<1>(), Int<1>(), Int<4>());
+  if (nvec <= 16) return f(Int<16>(), Int<1>(), Int<1>(), Int<4>());
+  if (nvec <= 32) return f(Int<32>(), Int<1>(), Int<1>(), Int<4>());
+  if (nvec <= 64) return f(Int<64>(), Int<1>(), Int<1>(), Int<4>());
+  if (nvec <= 128) return f(Int<64>(), Int<1>(), Int<2>(), Int<2>());
+  if (nvec <= 256) return f(Int<64>(), Int<4>(), Int<1>(), Int<2>());
+  if (nvec <= 512) return f(Int<64>(), Int<4>(), Int<2>(), Int<1>());
+  if (nvec <= 1024) return f(Int<64>(), Int<4>(), Int<4>(), Int<1>());
+  if (nvec <= 2048) return f(Int<64>(), Int<16>(), Int<2>(), Int<1>());
+  if (nvec <= 4096) return f(Int<64>(), Int<16>(), Int<4>(), Int<1>());
+  return f(Int<64>(), Int<16>(), Int<8>(), Int<1>());
+}
+
+template <typename T, bool BITS8>
+hipError_t norm_fwd(const NormArgs& a, hipStream_t stream) {
+  return with_shape(a.d / kVec<T>, [&](auto l, auto w, auto nv, auto nr) {
+    constexpr int LANES = decltype(l)::value, WAVES = decltype(w)::value, NV = decltype(nv)::value, NR = decltype(nr)::value;
+    constexpr int THREADS = WAVES > 4 ? 64 * WAVES : 256, per = THREADS / (LANES * WAVES) * NR;
+    hipLaunchKernelGGL((kda_norm_kernel<T, LANES, WAVES, NV, NR, BITS8>), dim3((unsigned)((a.rows + per - 1) / per)),
+                       dim3(THREADS), 0, stream, a);
+    return hipGetLastError();
+  });
+}
+
+template <typename T>
+hipError_t norm_bwd(const NormArgs& a, hipStream_t stream) {
+  const hipError_t e = with_shape(a.d / kVec<T>, [&](auto l, auto w, auto nv, auto nr) {
+    constexpr int LANES = decltype(l)::value, WAVES = decltype(w)::value, NV = decltype(nv)::value, NR = decltype(nr)::value;
+    constexpr int THREADS = WAVES > 4 ? 64 * WAVES : 256, R = NR > 2 ? 2 : NR;
+    hipLaunchKernelGGL((kda_norm_bwd_kernel<T, LANES, WAVES, NV, R>), dim3((unsigned)(a.nparts * a.w_heads)),
+                       dim3(THREADS), 0, stream, a);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || !a.dw) return e;
+  const int n = a.w_heads * a.d;
+  hipLaunchKernelGGL((kda_norm_dw_kernel<T>), dim3((unsigned)((n + 31) / 32)), dim3(1024), 0, stream, a.scratch,
+                     static_cast<T*>(a.dw), n, a.nparts);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Blocks per weight row: four a compute unit (one of 1024 threads), no more than there are units of rows.
+int norm_parts(int rows, int d, int w_heads, bool bf16_io, int cus) {
+  const int nvec = d / (bf16_io ? 8 : 4);
+  return with_shape(nvec, [&](auto l, auto w, auto, auto nr) {
+    constexpr int LANES = decltype(l)::value, WAVES = decltype(w)::value, R = decltype(nr)::value > 2 ? 2 : decltype(nr)::value;
+    constexpr int THREADS = WAVES > 4 ? 64 * WAVES : 256, per = THREADS / (LANES * WAVES) * R;
+    const int own = rows / w_heads;
+    int most = (WAVES > 4 ? 1 : 4) * cus / w_heads;
+    most = most < 1 ? 1 : most;
+    const int units = (own + per - 1) / per;
+    return units < most ? (units < 1 ? 1 : units) : most;
+  });
+}
+
+hipError_t launch_norm(NormArgs a, int B, int H, int T, bool bits8, bool bf16_io, hipStream_t stream) {
+  join_dims(a, B, H, T);
+  if (bits8) return bf16_io ? norm_fwd<bf16, true>(a, stream) : norm_fwd<float, true>(a, stream);
+  return bf16_io ? norm_fwd<bf16, false>(a, stream) : norm_fwd<float, false>(a, stream);
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, bool bf16_io, hipStream_t stream) {
+  return bf16_io ? norm_bwd<bf16>(a, stream) : norm_bwd<float>(a, stream);
+}
+
+}  // namespace kda

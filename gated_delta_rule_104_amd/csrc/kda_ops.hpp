@@ -1,5 +1,6 @@
 // Internal launch interface of the companion operators (short convolution,
-// selective scan, quantised state cache).  Host-side only; no validation here.
+// selective scan, quantised state cache, gated linear recurrence, norm, drafts).
+// Host-side only; no validation here.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -90,5 +91,81 @@ hipError_t launch_ssm_step(const void* q, const void* k, const void* v, const vo
 // bit 0: a log_alpha above 0 or NaN, bit 1: a beta not finite.  Synchronises `stream`.
 hipError_t check_ssm_gates(const void* la, Str3 ls, const void* beta, Str3 bs, const int* lens, int B, int H, int T, bool bf16_io,
                            hipStream_t stream, unsigned int* bits_out);
+
+
+// ------------------------------------------------ gated linear recurrence
+struct GlrArgs {
+  const void* x;     // [B, H, T, d]
+  const void* la;
+  const void* beta;  // or null (1)
+  const float* h0;   // [B, H, d] or null (zero)
+  const int* lens;   // [B] or null (T)
+  void* o;           // (backward: the outputs, read)
+  float* h_T;
+  Str3 xs, ls, bs, os;
+  int B, H, T, d;
+  bool norm;
+  // backward
+  const void* dO = nullptr;
+  const float* dh_T = nullptr;
+  void* dx = nullptr;
+  void* dla = nullptr;
+  void* dbeta = nullptr;
+  float* dh0 = nullptr;
+  Str3 dos, dxs, dls, dbs;
+  void* ws = nullptr;
+};
+size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients, int cus);
+hipError_t launch_glr(const GlrArgs& a, bool bf16_io, int cus, hipStream_t stream);
+hipError_t launch_glr_step(const GlrArgs& a, bool bf16_io, hipStream_t stream);
+hipError_t launch_glr_backward(const GlrArgs& a, bool bf16_io, int cus, hipStream_t stream);
+// bit 0: a log_alpha above 0 or NaN, bit 1: a beta not finite.  Synchronises `stream`.
+hipError_t check_glr_gates(const GlrArgs& a, bool bf16_io, hipStream_t stream, unsigned int* bits_out);
+
+// ------------------------------------------------------------------- norm
+struct NormArgs {
+  const void* x;         // [B, H, T, d] (backward: the rows that were normalised)
+  const void* residual;  // or null
+  const void* gate;      // or null
+  const void* w;         // [d], [H, d] or null (1)
+  void* y;
+  void* scales;          // 8 bits: a float per row, or a byte per 32 values
+  void* s;               // x + residual, or null
+  Str3 xs, rs, gs, ys, ss, ws, cs;  // ws: the weight's, 0 but for one row per head
+  int rows, d, n1, n2;   // rows = n0 n1 n2
+  int w_heads;           // rows of the weight
+  float eps, inv_d;
+  bool silu, e4m3, blocks;
+  // backward
+  const void* dy = nullptr;
+  const void* ds = nullptr;  // or null
+  void* dx = nullptr;
+  void* dgate = nullptr;
+  void* dw = nullptr;        // or null
+  Str3 dys, dss, dxs, dgs;
+  float* scratch = nullptr;
+  int nparts = 0;
+};
+int norm_parts(int rows, int d, int w_heads, bool bf16_io, int cus);
+hipError_t launch_norm(NormArgs a, int B, int H, int T, bool bits8, bool bf16_io, hipStream_t stream);
+hipError_t launch_norm_backward(const NormArgs& a, bool bf16_io, hipStream_t stream);
+
+// ----------------------------------------------------------------- drafts
+struct VerifyArgs {
+  const void* p;       // [N, K + 1, V]
+  const void* q;       // [N, K, V] or null (one at the token)
+  const int* tokens;   // [N, K]
+  const float* u;      // [N, K + 1]
+  const int* counts;   // [N] or null (K)
+  int* accepted;       // [N]
+  int* out;            // [N, K + 1]
+  long long pn, pt, qn, qt;  // elements between sequences and tokens
+  int N, K, V;
+  double* ws;
+};
+size_t verify_ws_bytes(int N, int V);
+hipError_t launch_verify(const VerifyArgs& a, bool bf16_io, hipStream_t stream);
+hipError_t launch_state_commit(const float* S_pos, const int* index, float* S, int N, int ntok, long long elems,
+                               hipStream_t stream);
 
 }  // namespace kda

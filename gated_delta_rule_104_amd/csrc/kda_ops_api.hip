@@ -391,4 +391,341 @@ kda_status kda_state_load(const void* cache, const void* scales, const int* slot
   return e == hipSuccess ? api_ok() : hip_fail(e, "kda_state_load launch");
 }
 
+// ------------------------------------------------ gated linear recurrence
+namespace {
+kda_status glr_dims(int B, int H, int T, int d, kda_dtype dtype) {
+  if (B < 0 || H < 0 || T < 0 || d < 0)
+    return api_fail(KDA_ERR_SHAPE, "negative size B=%d H=%d T=%d d=%d", B, H, T, d);
+  OPS_TRY(check_dtype(dtype));
+  const int es = dtype == KDA_BF16 ? 2 : 4;
+  if ((long long)d * es % 16) return api_fail(KDA_ERR_UNSUPPORTED, "rows of %d elements are not a multiple of 16 bytes", d);
+  const long long C = (long long)H * d;
+  if (C > (1 << 28) || T > (1 << 30) || (long long)B * C > kMaxElems || (long long)B * C * T > kMaxElems ||
+      (long long)B * C * (T / 16 + 1) / 8 / 32 > INT32_MAX)
+    return api_fail(KDA_ERR_SHAPE, "problem too large");
+  return KDA_OK;
+}
+
+kda_status glr_inputs(kda::GlrArgs& a, const kda_glr_strides* st, int B, int H, int T, int d, bool has_beta, bool o_out,
+                      kda_dtype dtype) {
+  OPS_TRY(glr_dims(B, H, T, d, dtype));
+  const int es = dtype == KDA_BF16 ? 2 : 4;
+  OPS_TRY(take_strides(st ? &st->x : nullptr, B, H, T, d, es, true, false, "x", &a.xs));
+  OPS_TRY(take_strides(st ? &st->log_alpha : nullptr, B, H, T, d, es, true, false, "log_alpha", &a.ls));
+  if (has_beta) OPS_TRY(take_strides(st ? &st->beta : nullptr, B, H, T, d, es, true, false, "beta", &a.bs));
+  OPS_TRY(take_strides(st ? &st->o : nullptr, B, H, T, d, es, true, o_out, "o", &a.os));
+  a.B = B; a.H = H; a.T = T; a.d = d;
+  return KDA_OK;
+}
+
+kda_status glr_check(const kda::GlrArgs& a, kda_dtype dtype, hipStream_t stream) {
+  if (!kda::api_check_on()) return KDA_OK;
+  unsigned int bits = 0u;
+  const hipError_t e = kda::check_glr_gates(a, dtype == KDA_BF16, stream, &bits);
+  if (e != hipSuccess) return hip_fail(e, "input check");
+  if (bits & 1u) return api_fail(KDA_ERR_PRECONDITION, "log_alpha has values above 0 or NaN (check mode)");
+  if (bits & 2u) return api_fail(KDA_ERR_PRECONDITION, "beta has values that are not finite (check mode)");
+  return KDA_OK;
+}
+
+kda_status need_workspace(const void* workspace, size_t have, size_t bytes) {
+  if (!bytes) return KDA_OK;
+  if (!workspace) return api_fail(KDA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", bytes);
+  if (!aligned(workspace)) return api_fail(KDA_ERR_ALIGN, "workspace is not 16-byte aligned");
+  if (have < bytes) return api_fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", have, bytes);
+  return KDA_OK;
+}
+}  // namespace
+
+size_t kda_glr_prefill_workspace_bytes(int B, int H, int T, int d, kda_dtype dtype) {
+  if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || glr_dims(B, H, T, d, dtype) != KDA_OK) return 0;
+  return kda::glr_ws_bytes(B, H, T, d, dtype == KDA_BF16, false, kda::api_cu_count());
+}
+
+kda_status kda_glr_prefill(const void* x, const void* log_alpha, const void* beta, const float* h0, const int* lens,
+                           void* o, float* h_T, const kda_glr_strides* st, int B, int H, int T, int d, int normalise,
+                           kda_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  kda::GlrArgs a{};
+  OPS_TRY(glr_inputs(a, st, B, H, T, d, beta != nullptr, true, dtype));
+  if ((long long)B * H * d == 0) return api_ok();
+  OPS_TRY(maybe(h0, "h0"));
+  OPS_TRY(need(h_T, "h_T"));
+  if (T > 0) {
+    OPS_TRY(need(x, "x"));
+    OPS_TRY(need(log_alpha, "log_alpha"));
+    OPS_TRY(maybe(beta, "beta"));
+    OPS_TRY(need(o, "o"));
+    if (o == x || o == log_alpha || o == beta) return api_fail(KDA_ERR_UNSUPPORTED, "o must not be an input");
+    OPS_TRY(need_workspace(workspace, workspace_bytes, kda_glr_prefill_workspace_bytes(B, H, T, d, dtype)));
+  }
+  a.x = x; a.la = log_alpha; a.beta = beta; a.h0 = h0; a.lens = lens; a.o = o; a.h_T = h_T;
+  a.norm = normalise != 0;
+  a.ws = workspace;
+  if (T > 0) OPS_TRY(glr_check(a, dtype, stream));
+  const hipError_t e = kda::launch_glr(a, dtype == KDA_BF16, kda::api_cu_count(), stream);
+  return e == hipSuccess ? api_ok() : hip_fail(e, "kda_glr_prefill launch");
+}
+
+kda_status kda_glr_step(const void* x, const void* log_alpha, const void* beta, float* h, void* o,
+                        const kda_glr_strides* st, int N, int H, int d, int normalise, kda_dtype dtype,
+                        hipStream_t stream) {
+  kda::GlrArgs a{};
+  OPS_TRY(glr_inputs(a, st, N, H, 1, d, beta != nullptr, true, dtype));
+  if ((long long)N * H * d == 0) return api_ok();
+  OPS_TRY(need(x, "x"));
+  OPS_TRY(need(log_alpha, "log_alpha"));
+  OPS_TRY(maybe(beta, "beta"));
+  OPS_TRY(need(h, "h"));
+  OPS_TRY(need(o, "o"));
+  for (const void* in : {x, log_alpha, beta, static_cast<const void*>(h)})
+    if (o == in) return api_fail(KDA_ERR_UNSUPPORTED, "o must not be an input");
+  for (const void* in : {x, log_alpha, beta})
+    if (h == in) return api_fail(KDA_ERR_UNSUPPORTED, "h must not be another input");
+  a.x = x; a.la = log_alpha; a.beta = beta; a.h_T = h; a.o = o;
+  a.norm = normalise != 0;
+  OPS_TRY(glr_check(a, dtype, stream));
+  const hipError_t e = kda::launch_glr_step(a, dtype == KDA_BF16, stream);
+  return e == hipSuccess ? api_ok() : hip_fail(e, "kda_glr_step launch");
+}
+
+size_t kda_glr_backward_workspace_bytes(int B, int H, int T, int d, kda_dtype dtype) {
+  if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || glr_dims(B, H, T, d, dtype) != KDA_OK) return 0;
+  return kda::glr_ws_bytes(B, H, T, d, dtype == KDA_BF16, true, kda::api_cu_count());
+}
+
+kda_status kda_glr_backward(const void* x, const void* log_alpha, const void* beta, const float* h0, const void* o,
+                            const void* dO, const float* dh_T, const int* lens, void* dx, void* dlog_alpha, void* dbeta,
+                            float* dh0, const kda_glr_strides* st, const kda_glr_grad_strides* gst, int B, int H, int T,
+                            int d, int normalise, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream) {
+  kda::GlrArgs a{};
+  OPS_TRY(glr_inputs(a, st, B, H, T, d, beta != nullptr, false, dtype));
+  const int es = dtype == KDA_BF16 ? 2 : 4;
+  OPS_TRY(take_strides(gst ? &gst->dO : nullptr, B, H, T, d, es, true, false, "dO", &a.dos));
+  OPS_TRY(take_strides(gst ? &gst->dx : nullptr, B, H, T, d, es, true, true, "dx", &a.dxs));
+  OPS_TRY(take_strides(gst ? &gst->dlog_alpha : nullptr, B, H, T, d, es, true, true, "dlog_alpha", &a.dls));
+  if (beta) OPS_TRY(take_strides(gst ? &gst->dbeta : nullptr, B, H, T, d, es, true, true, "dbeta", &a.dbs));
+  if ((long long)H * d == 0) return api_ok();
+  if (B == 0 || T == 0) return api_fail(KDA_ERR_SHAPE, "the gradients need B >= 1 and T >= 1 (B=%d T=%d)", B, T);
+  OPS_TRY(need(x, "x"));
+  OPS_TRY(need(log_alpha, "log_alpha"));
+  OPS_TRY(maybe(beta, "beta"));
+  OPS_TRY(maybe(h0, "h0"));
+  OPS_TRY(need(o, "o"));
+  OPS_TRY(need(dO, "dO"));
+  OPS_TRY(maybe(dh_T, "dh_T"));
+  OPS_TRY(need(dx, "dx"));
+  OPS_TRY(need(dlog_alpha, "dlog_alpha"));
+  if (beta) OPS_TRY(need(dbeta, "dbeta"));
+  OPS_TRY(maybe(dh0, "dh0"));
+  for (const void* out : {dx, dlog_alpha, beta ? dbeta : dx})
+    for (const void* in : {x, log_alpha, beta, o, dO})
+      if (out == in) return api_fail(KDA_ERR_UNSUPPORTED, "a gradient must not be an input");
+  if (dx == dlog_alpha || (beta && (dbeta == dx || dbeta == dlog_alpha)))
+    return api_fail(KDA_ERR_UNSUPPORTED, "gradients must not share memory");
+  if (dh0 && (dh0 == h0 || dh0 == dh_T)) return api_fail(KDA_ERR_UNSUPPORTED, "dh0 must not be h0 or dh_T");
+  OPS_TRY(need_workspace(workspace, workspace_bytes, kda_glr_backward_workspace_bytes(B, H, T, d, dtype)));
+  a.x = x; a.la = log_alpha; a.beta = beta; a.h0 = h0; a.lens = lens; a.o = const_cast<void*>(o); a.dO = dO; a.dh_T = dh_T;
+  a.dx = dx; a.dla = dlog_alpha; a.dbeta = beta ? dbeta : nullptr; a.dh0 = dh0;
+  a.norm = normalise != 0;
+  a.ws = workspace;
+  OPS_TRY(glr_check(a, dtype, stream));
+  const hipError_t e = kda::launch_glr_backward(a, dtype == KDA_BF16, kda::api_cu_count(), stream);
+  return e == hipSuccess ? api_ok() : hip_fail(e, "kda_glr_backward launch");
+}
+
+// ------------------------------------------------------------------- norm
+namespace {
+kda_status norm_dims(int B, int H, int T, int d, float eps, kda_gate gate_activation, kda_dtype dtype) {
+  if (B < 0 || H < 0 || T < 0 || d < 0)
+    return api_fail(KDA_ERR_SHAPE, "negative size B=%d H=%d T=%d d=%d", B, H, T, d);
+  OPS_TRY(check_dtype(dtype));
+  const int es = dtype == KDA_BF16 ? 2 : 4;
+  if ((long long)d * es % 16) return api_fail(KDA_ERR_UNSUPPORTED, "rows of %d elements are not a multiple of 16 bytes", d);
+  if (d > 32768) return api_fail(KDA_ERR_UNSUPPORTED, "rows of %d elements, at most 32768 are supported", d);
+  if (gate_activation != KDA_GATE_SIGMOID && gate_activation != KDA_GATE_SILU)
+    return api_fail(KDA_ERR_UNSUPPORTED, "unknown gate activation %d", (int)gate_activation);
+  if (!(eps >= 0.f && eps < 1e30f)) return api_fail(KDA_ERR_UNSUPPORTED, "eps = %g is not a finite number of at least 0", eps);
+  if ((long long)B * H > INT32_MAX || (long long)B * H * T > INT32_MAX - 65536 || (long long)H * d > (1 << 28))
+    return api_fail(KDA_ERR_SHAPE, "problem too large");
+  return KDA_OK;
+}
+}  // namespace
+
+kda_status kda_rms_norm(const void* x, const void* residual, const void* gate, const void* weight, void* y,
+                        void* scales, void* residual_out, const kda_norm_strides* st, int B, int H, int T, int d,
+                        int weight_per_head, float eps, kda_gate gate_activation, kda_norm_output output,
+                        kda_dtype dtype, hipStream_t stream) {
+  OPS_TRY(norm_dims(B, H, T, d, eps, gate_activation, dtype));
+  if (output < KDA_OUT_SAME || output > KDA_OUT_E4M3_BLOCKS) return api_fail(KDA_ERR_UNSUPPORTED, "unknown output %d", (int)output);
+  const bool bits8 = output != KDA_OUT_SAME, blocks = output == KDA_OUT_INT8_BLOCKS || output == KDA_OUT_E4M3_BLOCKS;
+  if (blocks && d % 32) return api_fail(KDA_ERR_UNSUPPORTED, "rows of %d values are not whole blocks of 32", d);
+  const int es = dtype == KDA_BF16 ? 2 : 4;
+  kda::NormArgs a{};
+  OPS_TRY(take_strides(st ? &st->x : nullptr, B, H, T, d, es, true, false, "x", &a.xs));
+  if (residual) OPS_TRY(take_strides(st ? &st->residual : nullptr, B, H, T, d, es, true, false, "residual", &a.rs));
+  if (gate) OPS_TRY(take_strides(st ? &st->gate : nullptr, B, H, T, d, es, true, false, "gate", &a.gs));
+  // (8-bit rows are written 8 or 4 bytes at a time)
+  OPS_TRY(take_strides(st ? &st->y : nullptr, B, H, T, d, es, true, true, "y", &a.ys));
+  if (residual_out) OPS_TRY(take_strides(st ? &st->residual_out : nullptr, B, H, T, d, es, true, true, "residual_out", &a.ss));
+  if (bits8) OPS_TRY(take_strides(st ? &st->scales : nullptr, B, H, T, blocks ? d / 32 : 1, 4, false, true, "scales", &a.cs));
+  if ((long long)B * H * T * d == 0) return api_ok();
+  OPS_TRY(need(x, "x"));
+  OPS_TRY(maybe(residual, "residual"));
+  OPS_TRY(maybe(gate, "gate"));
+  OPS_TRY(maybe(weight, "weight"));
+  OPS_TRY(need(y, "y"));
+  OPS_TRY(maybe(residual_out, "residual_out"));
+  if (bits8) OPS_TRY(need_any(scales, "scales"));
+  if (bits8 && !blocks && (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return api_fail(KDA_ERR_ALIGN, "scales is not aligned to its floats");
+  if (residual_out && !residual) return api_fail(KDA_ERR_UNSUPPORTED, "residual_out without a residual");
+  for (const void* in : {x, residual, gate, weight})
+    if (y == in || (bits8 && scales == in)) return api_fail(KDA_ERR_UNSUPPORTED, "y must not be an input");
+  for (const void* in : {x, gate, weight})
+    if (residual_out && residual_out == in) return api_fail(KDA_ERR_UNSUPPORTED, "residual_out must not be an input but residual");
+  if (residual_out && residual_out == residual && (a.ss.b != a.rs.b || a.ss.h != a.rs.h || a.ss.t != a.rs.t))
+    return api_fail(KDA_ERR_UNSUPPORTED, "residual_out in the place of residual has other strides");
+  if (residual_out && residual_out == y) return api_fail(KDA_ERR_UNSUPPORTED, "residual_out must not be y");
+  a.x = x; a.residual = residual; a.gate = gate; a.w = weight; a.y = y; a.scales = scales; a.s = residual_out;
+  if (weight && weight_per_head && H > 1) a.ws.h = d;
+  a.rows = B * H * T; a.d = d; a.eps = eps; a.inv_d = 1.f / (float)d;
+  a.silu = gate_activation == KDA_GATE_SILU;
+  a.e4m3 = output == KDA_OUT_E4M3_ROWS || output == KDA_OUT_E4M3_BLOCKS;
+  a.blocks = blocks;
+  const hipError_t e = kda::launch_norm(a, B, H, T, bits8, dtype == KDA_BF16, stream);
+  return e == hipSuccess ? api_ok() : hip_fail(e, "kda_rms_norm launch");
+}
+
+size_t kda_rms_norm_backward_workspace_bytes(int B, int H, int T, int d, int weight_per_head, kda_dtype dtype) {
+  if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || norm_dims(B, H, T, d, 0.f, KDA_GATE_SIGMOID, dtype) != KDA_OK) return 0;
+  const int heads = weight_per_head ? H : 1;
+  return (size_t)kda::norm_parts(B * H * T, d, heads, dtype == KDA_BF16, kda::api_cu_count()) * heads * d * sizeof(float);
+}
+
+kda_status kda_rms_norm_backward(const void* x, const void* gate, const void* weight, const void* dy,
+                                 const void* dresidual_out, void* dx, void* dgate, void* dweight,
+                                 const kda_norm_grad_strides* st, int B, int H, int T, int d, int weight_per_head,
+                                 float eps, kda_gate gate_activation, kda_dtype dtype, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+  OPS_TRY(norm_dims(B, H, T, d, eps, gate_activation, dtype));
+  const int es = dtype == KDA_BF16 ? 2 : 4;
+  kda::NormArgs a{};
+  OPS_TRY(take_strides(st ? &st->x : nullptr, B, H, T, d, es, true, false, "x", &a.xs));
+  if (gate) OPS_TRY(take_strides(st ? &st->gate : nullptr, B, H, T, d, es, true, false, "gate", &a.gs));
+  OPS_TRY(take_strides(st ? &st->dy : nullptr, B, H, T, d, es, true, false, "dy", &a.dys));
+  if (dresidual_out)
+    OPS_TRY(take_strides(st ? &st->dresidual_out : nullptr, B, H, T, d, es, true, false, "dresidual_out", &a.dss));
+  OPS_TRY(take_strides(st ? &st->dx : nullptr, B, H, T, d, es, true, true, "dx", &a.dxs));
+  if (gate) OPS_TRY(take_strides(st ? &st->dgate : nullptr, B, H, T, d, es, true, true, "dgate", &a.dgs));
+  if ((long long)H * d == 0) return api_ok();
+  if (B == 0 || T == 0) return api_fail(KDA_ERR_SHAPE, "the gradients need B >= 1 and T >= 1 (B=%d T=%d)", B, T);
+  OPS_TRY(need(x, "x"));
+  OPS_TRY(maybe(gate, "gate"));
+  OPS_TRY(maybe(weight, "weight"));
+  OPS_TRY(need(dy, "dy"));
+  OPS_TRY(maybe(dresidual_out, "dresidual_out"));
+  OPS_TRY(need(dx, "dx"));
+  if (gate) OPS_TRY(need(dgate, "dgate"));
+  if (weight) OPS_TRY(need_any(dweight, "dweight"));
+  for (const void* out : {dx, gate ? dgate : dx, weight ? dweight : dx})
+    for (const void* in : {x, gate, weight, dy, dresidual_out})
+      if (out == in) return api_fail(KDA_ERR_UNSUPPORTED, "a gradient must not be an input");
+  if ((gate && dgate == dx) || (weight && (dweight == dx || (gate && dweight == dgate))))
+    return api_fail(KDA_ERR_UNSUPPORTED, "gradients must not share memory");
+  const int heads = weight_per_head ? H : 1;
+  if (weight)
+    OPS_TRY(need_workspace(workspace, workspace_bytes,
+                           kda_rms_norm_backward_workspace_bytes(B, H, T, d, weight_per_head, dtype)));
+  a.x = x; a.gate = gate; a.w = weight; a.dy = dy; a.ds = dresidual_out; a.dx = dx;
+  a.dgate = gate ? dgate : nullptr;
+  a.dw = weight ? dweight : nullptr;
+  a.rows = B * H * T; a.d = d; a.n1 = H; a.n2 = T; a.w_heads = heads; a.eps = eps; a.inv_d = 1.f / (float)d;
+  a.silu = gate_activation == KDA_GATE_SILU;
+  a.scratch = static_cast<float*>(workspace);
+  a.nparts = kda::norm_parts(a.rows, d, heads, dtype == KDA_BF16, kda::api_cu_count());
+  const hipError_t e = kda::launch_norm_backward(a, dtype == KDA_BF16, stream);
+  return e == hipSuccess ? api_ok() : hip_fail(e, "kda_rms_norm_backward launch");
+}
+
+// ----------------------------------------------------------------- drafts
+namespace {
+kda_status verify_dims(int N, int K, int V, kda_dtype dtype) {
+  if (N < 0 || K < 0 || V < 0) return api_fail(KDA_ERR_SHAPE, "negative size N=%d K=%d V=%d", N, K, V);
+  OPS_TRY(check_dtype(dtype));
+  if (N > (1 << 24) || K > (1 << 16) || V > (1 << 30) || (long long)N * (V / 4096 + 1) > (1 << 30))
+    return api_fail(KDA_ERR_SHAPE, "problem too large");
+  return KDA_OK;
+}
+
+// The strides of rows of V probabilities, with the largest distances that sums in 64 bits hold.
+kda_status row_strides(const kda_strides* s, int N, int K, int V, const char* name, long long* n, long long* t) {
+  *n = s ? s->b : (long long)K * V;
+  *t = s ? s->t : V;
+  if (N <= 1) *n = 0;
+  if (K <= 1) *t = 0;
+  if (*n < 0 || *t < 0 || *n > kMaxElems || *t > kMaxElems)
+    return api_fail(KDA_ERR_SHAPE, "%s: strides %lld and %lld are not usable", name, *n, *t);
+  return KDA_OK;
+}
+}  // namespace
+
+size_t kda_draft_verify_workspace_bytes(int N, int K, int V, kda_dtype dtype) {
+  if (N <= 0 || V <= 0 || verify_dims(N, K, V, dtype) != KDA_OK) return 0;
+  return kda::verify_ws_bytes(N, V);
+}
+
+kda_status kda_draft_verify(const void* target, const kda_strides* target_strides, const void* draft,
+                            const kda_strides* draft_strides, const int* tokens, const float* uniforms,
+                            const int* counts, int* accepted, int* out, int N, int K, int V, kda_dtype dtype,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  OPS_TRY(verify_dims(N, K, V, dtype));
+  kda::VerifyArgs a{};
+  OPS_TRY(row_strides(target_strides, N, K + 1, V, "target", &a.pn, &a.pt));
+  OPS_TRY(row_strides(draft_strides, N, K, V, "draft", &a.qn, &a.qt));
+  if (N == 0) return api_ok();
+  if (V == 0) return api_fail(KDA_ERR_SHAPE, "no vocabulary (V = 0)");
+  OPS_TRY(need_any(target, "target"));
+  if (K > 0) OPS_TRY(need_any(tokens, "tokens"));
+  OPS_TRY(need_any(uniforms, "uniforms"));
+  OPS_TRY(need_any(accepted, "accepted"));
+  OPS_TRY(need_any(out, "out"));
+  const uintptr_t es = dtype == KDA_BF16 ? 2 : 4;
+  for (const void* p : {target, draft})
+    if (reinterpret_cast<uintptr_t>(p) % es) return api_fail(KDA_ERR_ALIGN, "probabilities are not aligned to their elements");
+  for (const void* p : {static_cast<const void*>(tokens), static_cast<const void*>(uniforms), static_cast<const void*>(counts),
+                        static_cast<const void*>(accepted), static_cast<const void*>(out)})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return api_fail(KDA_ERR_ALIGN, "an array of 32-bit values is not aligned to them");
+  // (a second launch reads the inputs again)
+  for (const void* o : {static_cast<const void*>(accepted), static_cast<const void*>(out)})
+    for (const void* in : {target, draft, static_cast<const void*>(tokens), static_cast<const void*>(uniforms),
+                           static_cast<const void*>(counts)})
+      if (o == in) return api_fail(KDA_ERR_UNSUPPORTED, "an output must not be an input");
+  if (accepted == out) return api_fail(KDA_ERR_UNSUPPORTED, "accepted must not be out");
+  OPS_TRY(need_workspace(workspace, workspace_bytes, kda_draft_verify_workspace_bytes(N, K, V, dtype)));
+  a.p = target; a.q = draft; a.tokens = tokens; a.u = uniforms; a.counts = counts; a.accepted = accepted; a.out = out;
+  a.N = N; a.K = K; a.V = V;
+  a.ws = static_cast<double*>(workspace);
+  const hipError_t e = kda::launch_verify(a, dtype == KDA_BF16, stream);
+  return e == hipSuccess ? api_ok() : hip_fail(e, "kda_draft_verify launch");
+}
+
+kda_status kda_state_commit(const float* S_pos, const int* index, float* S, int N, int ntok, int H, int dk, int dv,
+                            hipStream_t stream) {
+  if (N < 0 || ntok < 0 || H < 0 || dk < 0 || dv < 0)
+    return api_fail(KDA_ERR_SHAPE, "negative size N=%d ntok=%d H=%d dk=%d dv=%d", N, ntok, H, dk, dv);
+  const long long e = (long long)dk * dv;
+  if (N > (1 << 24) || ntok > (1 << 16) || e > (1 << 24) || (long long)H * e > (1LL << 36) ||
+      (long long)N * ntok > kMaxElems / ((long long)H * e + 1))
+    return api_fail(KDA_ERR_SHAPE, "problem too large");
+  if ((long long)H * e % 4) return api_fail(KDA_ERR_UNSUPPORTED, "states of %lld floats are not a multiple of 16 bytes", (long long)H * e);
+  if (N == 0 || ntok == 0 || H * e == 0) return api_ok();
+  OPS_TRY(need(S_pos, "S_pos"));
+  OPS_TRY(need_any(index, "index"));
+  OPS_TRY(need(S, "S"));
+  if (S == S_pos) return api_fail(KDA_ERR_UNSUPPORTED, "S must not be S_pos");
+  const hipError_t err = kda::launch_state_commit(S_pos, index, S, N, ntok, H * e, stream);
+  return err == hipSuccess ? api_ok() : hip_fail(err, "kda_state_commit launch");
+}
+
 }  // extern "C"

@@ -456,6 +456,149 @@ kda_status kda_state_load(const void* cache, const void* scales, const int* slot
                           int nslots, int H, int dk, int dv, kda_cache_format format, hipStream_t stream);
 
 /*
+ * Gated linear recurrence: one decay per channel and token, a vector as state.  Per
+ * channel, with a = exp(log_alpha):
+ *     h_t = a_t h_{t-1} + n_t beta_t x_t,   o_t = h_t,
+ * n = 1, or with `normalise` sqrt(1 - a^2), which keeps the size of h at that of
+ * beta x whatever the decay.
+ *   x, log_alpha, beta, o : [B, H, T, d] dtype (strides), d * sizeof(dtype) a
+ *                 multiple of 16; beta NULL for 1
+ *   log_alpha   : <= 0; -inf (any value below -104) clears the state, whatever it
+ *                 held: packed documents start that way.  Option "check" validates
+ *                 that, and that beta is finite (padding excepted), before launching.
+ *   h0, h_T     : [B, H, d] fp32, contiguous; h0 NULL for zero; h_T may be h0
+ * States are carried in fp32 (fp32 inputs: in 64 bits inside a run of tokens) and
+ * decays near 1 as their distance from it, so that slow ones keep their digits.
+ * T == 0 copies h0 (or zeros) to h_T.  An infinity or NaN in x stays in its channel's
+ * state until that is cleared.
+ * The sequences are cut into runs of tokens that fill the device; the workspace
+ * (kda_glr_prefill_workspace_bytes; may be 0) holds what passes between them.
+ */
+typedef struct { kda_strides x, log_alpha, beta, o; } kda_glr_strides;
+
+size_t kda_glr_prefill_workspace_bytes(int B, int H, int T, int d, kda_dtype dtype);
+kda_status kda_glr_prefill(const void* x, const void* log_alpha, const void* beta, const float* h0,
+                           const int* lens, void* o, float* h_T, const kda_glr_strides* strides, int B,
+                           int H, int T, int d, int normalise, kda_dtype dtype, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token of the recurrence for N sequences: x, log_alpha, beta, o [N, H, d]
+ * (strides b and h; t is ignored), h [N, H, d] fp32 in place.
+ */
+kda_status kda_glr_step(const void* x, const void* log_alpha, const void* beta, float* h, void* o,
+                        const kda_glr_strides* strides, int N, int H, int d, int normalise, kda_dtype dtype,
+                        hipStream_t stream);
+
+/*
+ * Gradients of kda_glr_prefill for dL/do = dO and dL/dh_T = dh_T (NULL: zero).  `o`
+ * holds the outputs that the forward pass wrote, and stands for the states between
+ * tokens.  dx, dlog_alpha and dbeta (NULL without beta) take their input's shape, in
+ * dtype; dh0 [B, H, d] fp32 (NULL: not written).  The gradients of padding are zero,
+ * whatever it holds.  A decay of zero has a dlog_alpha of zero, and where
+ * log_alpha = 0 the part of dlog_alpha that goes through the normaliser, which has no
+ * limit there, is left out.  B and T are at least 1 (unless H * d is 0).
+ */
+typedef struct { kda_strides dO, dx, dlog_alpha, dbeta; } kda_glr_grad_strides;
+
+size_t kda_glr_backward_workspace_bytes(int B, int H, int T, int d, kda_dtype dtype);
+kda_status kda_glr_backward(const void* x, const void* log_alpha, const void* beta, const float* h0,
+                            const void* o, const void* dO, const float* dh_T, const int* lens, void* dx,
+                            void* dlog_alpha, void* dbeta, float* dh0, const kda_glr_strides* strides,
+                            const kda_glr_grad_strides* grad_strides, int B, int H, int T, int d,
+                            int normalise, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/*
+ * Root-mean-square norm of rows of d values, with the residual's addition in front (a
+ * layer's entry) and a gate behind (a recurrence's heads), in dtype or in 8 bits for
+ * the projections that follow:
+ *     s = x + residual, rounded to dtype;   y = s (mean(s^2) + eps)^(-1/2) w act(gate)
+ *   x, residual, gate : [B, H, T, d] dtype (strides), d * sizeof(dtype) a multiple of 16,
+ *                  d at most 32768; residual and gate may be NULL
+ *   weight       : [d], or with weight_per_head [H, d]; NULL for 1
+ *   residual_out : s, [B, H, T, d] dtype (strides), or NULL; may be residual itself
+ *   y            : [B, H, T, d] (strides): dtype, or for the 8-bit outputs bytes, whose
+ *                  strides are multiples of 8 (bf16) or 4 (fp32)
+ *   scales       : of the 8-bit outputs, any element alignment of their own type:
+ *                  ROWS    [B, H, T] fp32, the row's largest |y| / 127 (int8) or 448 (e4m3), at
+ *                          least 2^-126; NaN marks a row that held an infinity or NaN
+ *                  BLOCKS  [B, H, T, d / 32] bytes (strides, contiguous rows of d / 32),
+ *                          d a multiple of 32: exponent + 127 of a power of two for each 32
+ *                          values, chosen and marked as in the quantised state cache above
+ *                  values are rounded to nearest even, and 0 where marked
+ * Sums are fp32.
+ */
+typedef enum { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 } kda_gate;
+typedef enum {
+  KDA_OUT_SAME = 0,
+  KDA_OUT_INT8_ROWS = 1,
+  KDA_OUT_E4M3_ROWS = 2,
+  KDA_OUT_INT8_BLOCKS = 3,
+  KDA_OUT_E4M3_BLOCKS = 4
+} kda_norm_output;
+typedef struct { kda_strides x, residual, gate, y, residual_out, scales; } kda_norm_strides;
+
+kda_status kda_rms_norm(const void* x, const void* residual, const void* gate, const void* weight, void* y,
+                        void* scales, void* residual_out, const kda_norm_strides* strides, int B, int H,
+                        int T, int d, int weight_per_head, float eps, kda_gate gate_activation,
+                        kda_norm_output output, kda_dtype dtype, hipStream_t stream);
+
+/*
+ * Its gradients for dL/dy = dy (of y before any rounding to 8 bits) and, with a
+ * residual, dL/dresidual_out = dresidual_out (NULL: none).  x is what was normalised:
+ * residual_out where a residual was added.  dx is the gradient of x and of the residual
+ * alike; dgate (required with a gate) as gate; dweight (required with a weight) as
+ * weight, in dtype, summed in fp32 in a fixed order.  B and T are at least 1 (unless
+ * H * d is 0).  The workspace holds partial sums of dweight, and may be NULL without one.
+ */
+typedef struct { kda_strides x, gate, dy, dresidual_out, dx, dgate; } kda_norm_grad_strides;
+
+size_t kda_rms_norm_backward_workspace_bytes(int B, int H, int T, int d, int weight_per_head,
+                                             kda_dtype dtype);
+kda_status kda_rms_norm_backward(const void* x, const void* gate, const void* weight, const void* dy,
+                                 const void* dresidual_out, void* dx, void* dgate, void* dweight,
+                                 const kda_norm_grad_strides* strides, int B, int H, int T, int d,
+                                 int weight_per_head, float eps, kda_gate gate_activation, kda_dtype dtype,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Verification of drafted tokens (speculative sampling): kda_decode_tokens runs the last
+ * token and K drafted ones, and this call says how many of the K stand, and which token
+ * comes next.  Draft j of sequence n is accepted while
+ *     uniforms[n, j] * q_j(token_j) < p_j(token_j).
+ * At the first refusal, j = a, the next token is drawn from max(p_a - q_a, 0), and behind the
+ * last accepted draft from p: it is the smallest i whose sum of probabilities 0..i is above
+ * uniforms[n, K] times the sum of all of them.  A token of no mass is never drawn; where
+ * max(p - q, 0) has none at all, p is drawn from, and where p has none the token is -1.
+ *   target   : [N, K + 1, V] dtype, p: the target's probabilities (they need not add up to
+ *              1; NaN and negative ones count as 0)
+ *   draft    : [N, K, V] dtype, q: the draft's; NULL for one at each drafted token (greedy
+ *              drafts).  Strides b and t of both in elements (h is ignored), any element
+ *              alignment, rows of V contiguous; NULL for contiguous.
+ *   tokens   : [N, K] the drafted tokens; one outside [0, V) is refused
+ *   uniforms : [N, K + 1] fp32 random numbers in [0, 1)
+ *   counts   : [N] drafts of each sequence (clamped to [0, K]), or NULL for K
+ *   accepted : [N] written: accepted drafts a
+ *   out      : [N, K + 1] written: the a accepted drafts, the next token, then -1
+ * Sums are fp64.  K == 0 draws one token from each row.  The workspace holds partial sums.
+ */
+size_t kda_draft_verify_workspace_bytes(int N, int K, int V, kda_dtype dtype);
+kda_status kda_draft_verify(const void* target, const kda_strides* target_strides, const void* draft,
+                            const kda_strides* draft_strides, const int* tokens, const float* uniforms,
+                            const int* counts, int* accepted, int* out, int N, int K, int V,
+                            kda_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The states that go with them: S[n] = S_pos[n, index[n]] for S_pos [N, ntok, H, dk, dv] of
+ * kda_decode_tokens and S [N, H, dk, dv], all fp32.  With the last verified token in front of the
+ * drafts, `accepted` is the index.  Where index[n] is outside [0, ntok), S[n] stays as it is.
+ * H * dk * dv is a multiple of 4.
+ */
+kda_status kda_state_commit(const float* S_pos, const int* index, float* S, int N, int ntok, int H, int dk,
+                            int dv, hipStream_t stream);
+
+/*
  * Process-wide options.  Each starts from the environment variable of the same
  * name in capitals with a KDA_ prefix (KDA_SPLIT, ...), read once, at the first
  * call that needs the options; kda_set_option changes one for every later call
@@ -489,7 +632,8 @@ kda_status kda_state_load(const void* cache, const void* scales, const int* slot
  *                      chunk's gradients.  Same results bit for bit
  *   "check"            1: validate log_alpha and beta on the device before every
  *                      call that reads them (see the conventions above; for the
- *                      scan log_alpha <= 0 and beta finite); default 0
+ *                      scan and the gated linear recurrence log_alpha <= 0 and beta
+ *                      finite); default 0
  *   "log"              1: print every launch's shape to stderr; default 0
  * kda_set_option returns KDA_ERR_SHAPE for an unknown name or a value the option
  * does not take; kda_get_option writes the value in effect (-1: default).
