@@ -45,7 +45,7 @@ bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0
 // environment variable, read once; -1 means the library's default.
 enum Opt {
   OPT_SPLIT, OPT_COST16, OPT_MAP_SKIP, OPT_NC, OPT_BW_SPLIT, OPT_CHECK, OPT_LOG, OPT_FIXUP, OPT_HEAD,
-  OPT_BW_OVERLAP, OPT_COUNT
+  OPT_BW_OVERLAP, OPT_GLR_POLLS, OPT_COUNT
 };
 struct OptDesc {
   const char* name;
@@ -55,7 +55,8 @@ const OptDesc kOpts[OPT_COUNT] = {{"split", "KDA_SPLIT"},       {"transfer_cost1
                                   {"map_skip", "KDA_MAP_SKIP"}, {"nc", "KDA_NC"},
                                   {"bw_split", "KDA_BW_SPLIT"}, {"check", "KDA_CHECK"},
                                   {"log", "KDA_LOG"},           {"fixup", "KDA_FIXUP"},
-                                  {"head_chunks", "KDA_HEAD_CHUNKS"}, {"bw_overlap", "KDA_BW_OVERLAP"}};
+                                  {"head_chunks", "KDA_HEAD_CHUNKS"}, {"bw_overlap", "KDA_BW_OVERLAP"},
+                                  {"glr_polls", "KDA_GLR_POLLS"}};
 std::atomic<long long> g_opt[OPT_COUNT];
 std::once_flag g_opt_once;
 
@@ -67,6 +68,7 @@ bool opt_valid(int o, long long v) {
     case OPT_NC: return v == 1 || v == 2 || v == 4 || v == 8;
     case OPT_BW_SPLIT: return v == 1 || v == 2;
     case OPT_HEAD: return v >= 1 && v <= 1024;
+    case OPT_GLR_POLLS: return v >= 0 && v <= (1 << 20);
     default: return v == 0 || v == 1;  // map_skip, check, log, fixup, bw_overlap
   }
 }
@@ -489,6 +491,11 @@ kda_status api_ok() { return ok(); }
 int api_cu_count() { return cu_count(); }
 bool api_check_on() { return opt(OPT_CHECK) == 1; }
 bool api_log_on() { return log_on(); }
+// By default far beyond what any predecessor takes (a poll is about a microsecond).
+int api_glr_polls() {
+  const long long v = opt(OPT_GLR_POLLS);
+  return v < 0 ? 1 << 16 : (int)v;
+}
 
 }  // namespace kda
 

@@ -16,5 +16,7 @@ int api_cu_count();
 // Options "check" and "log".
 bool api_check_on();
 bool api_log_on();
+// Option "glr_polls".
+int api_glr_polls();
 
 }  // namespace kda

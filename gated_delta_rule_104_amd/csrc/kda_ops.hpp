@@ -116,9 +116,10 @@ struct GlrArgs {
   void* ws = nullptr;
 };
 size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients, int cus);
-hipError_t launch_glr(const GlrArgs& a, bool bf16_io, int cus, hipStream_t stream);
+// polls: how often a run of tokens looks for the state in front of it before it walks the sequence itself
+hipError_t launch_glr(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream);
 hipError_t launch_glr_step(const GlrArgs& a, bool bf16_io, hipStream_t stream);
-hipError_t launch_glr_backward(const GlrArgs& a, bool bf16_io, int cus, hipStream_t stream);
+hipError_t launch_glr_backward(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream);
 // bit 0: a log_alpha above 0 or NaN, bit 1: a beta not finite.  Synchronises `stream`.
 hipError_t check_glr_gates(const GlrArgs& a, bool bf16_io, hipStream_t stream, unsigned int* bits_out);
 

@@ -401,7 +401,7 @@ kda_status glr_dims(int B, int H, int T, int d, kda_dtype dtype) {
   if ((long long)d * es % 16) return api_fail(KDA_ERR_UNSUPPORTED, "rows of %d elements are not a multiple of 16 bytes", d);
   const long long C = (long long)H * d;
   if (C > (1 << 28) || T > (1 << 30) || (long long)B * C > kMaxElems || (long long)B * C * T > kMaxElems ||
-      (long long)B * C * (T / 16 + 1) / 8 / 32 > INT32_MAX)
+      (long long)B * ((C + 63) / 64) * (T / 32 + 1) > INT32_MAX)
     return api_fail(KDA_ERR_SHAPE, "problem too large");
   return KDA_OK;
 }
@@ -462,7 +462,7 @@ kda_status kda_glr_prefill(const void* x, const void* log_alpha, const void* bet
   a.norm = normalise != 0;
   a.ws = workspace;
   if (T > 0) OPS_TRY(glr_check(a, dtype, stream));
-  const hipError_t e = kda::launch_glr(a, dtype == KDA_BF16, kda::api_cu_count(), stream);
+  const hipError_t e = kda::launch_glr(a, dtype == KDA_BF16, kda::api_glr_polls(), stream);
   return e == hipSuccess ? api_ok() : hip_fail(e, "kda_glr_prefill launch");
 }
 
@@ -530,7 +530,7 @@ kda_status kda_glr_backward(const void* x, const void* log_alpha, const void* be
   a.norm = normalise != 0;
   a.ws = workspace;
   OPS_TRY(glr_check(a, dtype, stream));
-  const hipError_t e = kda::launch_glr_backward(a, dtype == KDA_BF16, kda::api_cu_count(), stream);
+  const hipError_t e = kda::launch_glr_backward(a, dtype == KDA_BF16, kda::api_glr_polls(), stream);
   return e == hipSuccess ? api_ok() : hip_fail(e, "kda_glr_backward launch");
 }
 

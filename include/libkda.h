@@ -630,6 +630,11 @@ kda_status kda_state_commit(const float* S_pos, const int* index, float* S, int 
  *                      gradients beside the earlier half's chain, on the side
  *                      stream; 0 (default) runs the chain whole, then every
  *                      chunk's gradients.  Same results bit for bit
+ *   "glr_polls"        how often a run of tokens of the gated linear recurrence looks
+ *                      for the state in front of it, published by the run before,
+ *                      until it walks the sequence from its start by itself
+ *                      (0..1048576; default 65536, which a call that shares its
+ *                      workspace with no other never reaches)
  *   "check"            1: validate log_alpha and beta on the device before every
  *                      call that reads them (see the conventions above; for the
  *                      scan and the gated linear recurrence log_alpha <= 0 and beta
