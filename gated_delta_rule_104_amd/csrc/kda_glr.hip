@@ -82,6 +82,16 @@ __device__ __forceinline__ Row<T> ones() {
 // between them is needed.  Waiting is bounded: a tile whose predecessors do not answer walks the
 // sequence from its start by itself, so the call ends whatever order workgroups run in.
 
+// Inputs are read and outputs written once: past the caches' normal order (four 8K prompts 241 -> 229 us).
+template <typename T>
+__device__ __forceinline__ u32x4 ld_once(const T* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+template <typename T>
+__device__ __forceinline__ void st_once(T* p, u32x4 v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+}
+
 constexpr int kSlab = 64;                // channels of a tile
 constexpr int kWords = 3 * kSlab;        // of a tile: l, z and the end state of each channel
 constexpr uint32_t kEmpty = 0xffffffffu;  // (a NaN that no published value has)
@@ -99,46 +109,73 @@ template <typename T> constexpr int kSub = 64 / kLpr<T>;
 
 template <typename T, int WAVES>
 struct RelayMem {
-  float e[WAVES * kSub<T>][kSlab], l[WAVES * kSub<T>][kSlab];
-  State<T> z[WAVES * kSub<T>][kSlab];
+  static constexpr int SUBS = WAVES * kSub<T>, WINDOW = SUBS / 2;
+  float e[SUBS][kSlab];  // decays of the lanes' tokens
+  // the sums of their logs; later decays and end states from zero of the tiles looked back at
+  union {
+    float l[SUBS][kSlab];
+    float past[2][WINDOW][kSlab];
+  };
+  State<T> z[SUBS][kSlab];  // end states from zero; later the states in front
   float we[WAVES][kSlab], wl[WAVES][kSlab], h[kSlab];
   State<T> wz[WAVES][kSlab];
+  float ends[WINDOW][kSlab];
+  uint32_t sums_there[WAVES], end_there[WAVES];
 };
 
-// The state in front of tile s >= 1 of a chain, lane = channel; false if the tiles before it did not
-// answer.  words: the chain's tile 0, hop words to the next one; first: the state in front of tile 0.
-template <typename T>
-__device__ __forceinline__ bool look_back(const uint32_t* words, long long hop, int s, float first, int polls, float* state) {
-  constexpr int W = 8;  // tiles looked at together
-  const int lane = threadIdx.x & 63;
+// The state in front of tile s >= 1 of a chain, lane = channel, for wave 0; false if the tiles before it did
+// not answer.  words: the chain's tile 0, hop words to the next one; first: the state in front of tile 0;
+// window: how many tiles to look at, shared out over the waves, which have nothing else to do.
+template <typename T, int WAVES>
+__device__ __forceinline__ bool look_back(RelayMem<T, WAVES>& m, const uint32_t* words, long long hop, int s, float first,
+                                          int window, int polls, float* state) {
+  constexpr int W = RelayMem<T, WAVES>::WINDOW, OWN = W / WAVES;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int poll = 0; poll < polls; ++poll) {
-    uint32_t p[W], l[W], z[W];
+    uint32_t p[OWN], l[OWN], z[OWN], sums = 0u, ends = 0u;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const uint32_t* q = words + (long long)max(s - 1 - i, 0) * hop + lane;
-      p[i] = published(q + 2 * kSlab);
-      l[i] = published(q);
-      z[i] = published(q + kSlab);
-    }
-    int found = -1;
-    bool open = true;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if (!open || found >= 0) continue;
-      if (i >= s || __ballot(p[i] == kEmpty) == 0ull) found = i;
-      else if (__ballot(l[i] == kEmpty || z[i] == kEmpty) != 0ull) open = false;
-    }
-    if (found >= 0) {
-      float h = first;
-#pragma unroll
-      for (int i = W - 1; i >= 0; --i) {
-        if (i == found && i < s) h = __uint_as_float(p[i]);
-        if (i < found) h = advance(decay_of<T>(__uint_as_float(l[i])), h, __uint_as_float(z[i]));
+    for (int k = 0; k < OWN; ++k) {
+      const int i = k * WAVES + w;
+      p[k] = l[k] = z[k] = kEmpty;
+      if (i < window && i < s) {
+        const uint32_t* q = words + (long long)(s - 1 - i) * hop + lane;
+        p[k] = published(q + 2 * kSlab);
+        l[k] = published(q);
+        z[k] = published(q + kSlab);
       }
-      *state = h;
+    }
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) {
+      const int i = k * WAVES + w;
+      m.past[0][i][lane] = decay_of<T>(__uint_as_float(l[k]));
+      m.past[1][i][lane] = __uint_as_float(z[k]);
+      m.ends[i][lane] = __uint_as_float(p[k]);
+      if (__ballot(l[k] == kEmpty || z[k] == kEmpty) == 0ull) sums |= 1u << i;
+      if (i == s || __ballot(p[k] == kEmpty) == 0ull) ends |= 1u << i;  // (what is in front of tile 0 is known)
+    }
+    if (lane == 0) {
+      m.sums_there[w] = sums;
+      m.end_there[w] = ends;
+    }
+    __syncthreads();
+    sums = ends = 0u;
+#pragma unroll
+    for (int u = 0; u < WAVES; ++u) {
+      sums |= m.sums_there[u];
+      ends |= m.end_there[u];
+    }
+    // the nearest tile whose end state is known, if everything in between is
+    const int found = __ffs(ends) - 1;
+    if (found >= 0 && (~sums & ((1u << found) - 1u)) == 0u) {
+      if (w == 0) {
+        float h = found == s ? first : m.ends[found][lane];
+        for (int i = found - 1; i >= 0; --i) h = advance(m.past[0][i][lane], h, m.past[1][i][lane]);
+        *state = h;
+      }
       return true;
     }
-    __builtin_amdgcn_s_sleep(4);
+    __builtin_amdgcn_s_sleep(1);
+    __syncthreads();
   }
   return false;
 }
@@ -149,7 +186,7 @@ __device__ __forceinline__ bool look_back(const uint32_t* words, long long hop, 
 template <typename T, int WAVES, typename Self>
 __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kVec<T>], const State<T> (&z)[kVec<T>],
                                       State<T> (&h)[kVec<T>], uint32_t* words, long long hop, int s, bool last, float first,
-                                      int polls, float* end, Self self) {
+                                      int window, int polls, float* end, Self self) {
   constexpr int V = kVec<T>, LPR = kLpr<T>, SUB = kSub<T>;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = w * SUB + lane / LPR, c0 = lane % LPR * V;
 #pragma unroll
@@ -170,23 +207,23 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
   m.wl[w][lane] = lw;
   m.wz[w][lane] = zw;
   __syncthreads();
+  float lt = 0.f, front = first;
+  State<T> zt = 0;
+  uint32_t* own = words + s * hop + lane;
   if (w == 0) {
-    float lt = 0.f;
-    State<T> zt = 0;
 #pragma unroll
     for (int u = 0; u < WAVES; ++u) {
       zt = advance(m.we[u][lane], zt, m.wz[u][lane]);
       lt += m.wl[u][lane];
     }
-    uint32_t* own = words + s * hop + lane;
-    float front = first;
-    if (s > 0) {
-      if (!last) {
-        publish(own, lt);
-        publish(own + kSlab, (float)zt);
-      }
-      if (!look_back<T>(words, hop, s, first, polls, &front)) front = self();
+    if (s > 0 && !last) {
+      publish(own, lt);
+      publish(own + kSlab, (float)zt);
     }
+  }
+  const bool known = s == 0 || look_back<T, WAVES>(m, words, hop, s, first, window, polls, &front);
+  if (w == 0) {
+    if (!known) front = self();
     const float out = advance(decay_of<T>(lt), front, (float)zt);
     if (!last) publish(own + 2 * kSlab, out);
     else if (end) *end = out;
@@ -206,27 +243,58 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
   for (int c = 0; c < V; ++c) h[c] = m.z[sub][c0 + c];
 }
 
-// Which tile a workgroup has, and a lane's place in it.
+// Which tile a workgroup has.  Tiles are handed out run by run, so that the ones in front of a tile are
+// under way before it.  Consecutive workgroups go to the 8 XCDs in turn; with enough chains (or a
+// multiple of 8) every XCD gets neighbouring ones, whose rows of 128 bytes lie side by side
+// in memory (four 8K prompts 228 -> 206 us); with few chains all XCDs share each.
+struct GlrGrid {
+  int nslab, ntile, nchain, blocks;  // blocks: workgroups per run of all chains
+  bool spread;
+};
 struct GlrTile {
   int b, slab, s, len, ntile;  // sequence, slab, number in the chain, tokens and tiles of the sequence
   int chain;
-  __device__ __forceinline__ GlrTile(const GlrArgs& a, int nslab, int run) {
-    const int nchain = nslab * a.B;
-    s = blockIdx.x / nchain;
-    chain = blockIdx.x % nchain;
-    b = chain / nslab;
-    slab = chain % nslab;
-    len = seq_len(a.lens, b, a.T);
+  bool none;
+  __device__ __forceinline__ GlrTile(const GlrArgs& a, const GlrGrid& n, int run) {
+    s = blockIdx.x / n.blocks;
+    chain = blockIdx.x % n.blocks;
+    none = false;
+    if (n.spread) {
+      const int x = chain & 7, first = x * n.nchain / 8;
+      chain = first + (chain >> 3);
+      none = chain >= (x + 1) * n.nchain / 8;
+    }
+    b = chain / n.nslab;
+    slab = chain % n.nslab;
+    len = none ? 0 : seq_len(a.lens, b, a.T);
     ntile = max(1, (len + run - 1) / run);
   }
 };
 
+// NT rows of a lane's 16 bytes, at tokens t0, t0 + STEP, ...  Where not all of a tile's rows and channels are
+// there (full false), rows outside [0, len) are read from inside and set to zero.
+template <typename T, int NT, int STEP>
+__device__ __forceinline__ void load_rows(u32x4 (&r)[NT], const T* p, long long st, int t0, int len, bool on, bool full) {
+  if (full) {
+    p += t0 * st;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) r[i] = ld_once(p + i * (STEP * st));
+  } else {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = t0 + i * STEP;
+      r[i] = ld_once(p + min(max(t, 0), len - 1) * st);
+      if (!on || t < 0 || t >= len) r[i] = u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+}
+
 template <typename T, int NT, int WAVES, bool NORM, bool BETA>
-__global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, int nslab, int polls) {
+__global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, GlrGrid n, int window, int polls) {
   constexpr int V = kVec<T>, LPR = kLpr<T>, SUB = kSub<T>, RUN = WAVES * SUB * NT;
   __shared__ RelayMem<T, WAVES> mem;
-  const GlrTile g(a, nslab, RUN);
-  if (g.s >= g.ntile) return;
+  const GlrTile g(a, n, RUN);
+  if (g.none || g.s >= g.ntile) return;
   const int lane = threadIdx.x & 63, C = a.H * a.d, first_t = g.s * RUN;
   const int t0 = first_t + ((int)(threadIdx.x >> 6) * SUB + lane / LPR) * NT;
   const int c0 = g.slab * kSlab + lane % LPR * V;
@@ -235,18 +303,18 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, int nsla
   const T* x = static_cast<const T*>(a.x) + g.b * a.xs.b + hd * a.xs.h + j0;
   const T* la = static_cast<const T*>(a.la) + g.b * a.ls.b + hd * a.ls.h + j0;
   const T* beta = BETA ? static_cast<const T*>(a.beta) + g.b * a.bs.b + hd * a.bs.h + j0 : nullptr;
-  u32x4 rx[NT], rl[NT], rb[NT];
-  const u32x4 zero{0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    rx[i] = rl[i] = rb[i] = zero;
-    if (on && t0 + i < g.len) {
-      const long long t = t0 + i;
-      rl[i] = ld16(la + t * a.ls.t);
-      rx[i] = ld16(x + t * a.xs.t);
-      if constexpr (BETA) rb[i] = ld16(beta + t * a.bs.t);
-    }
+  const int cl = g.slab * kSlab + lane;  // lane = channel
+  const long long at = (long long)g.b * C + cl;
+  const float first = a.h0 && cl < C ? a.h0[at] : 0.f;
+  if (g.len == 0) {
+    if (threadIdx.x < 64 && cl < C) a.h_T[at] = first;
+    return;
   }
+  const bool full = first_t + RUN <= g.len && (g.slab + 1) * kSlab <= C;
+  u32x4 rx[NT], rl[NT], rb[NT];
+  load_rows<T, NT, 1>(rl, la, a.ls.t, t0, g.len, on, full);
+  load_rows<T, NT, 1>(rx, x, a.xs.t, t0, g.len, on, full);
+  if constexpr (BETA) load_rows<T, NT, 1>(rb, beta, a.bs.t, t0, g.len, on, full);
   float e[NT][V], in[NT][V], l[V];
   State<T> h[V], z[V];
 #pragma unroll
@@ -256,7 +324,7 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, int nsla
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const Row<T> xv = unpack<T>(rx[i]), lv = unpack<T>(rl[i]), bv = unpack<T>(rb[i]);
+    const Row<T> xv = unpack<T>(rx[i]), lv = unpack<T>(rl[i]), bv = BETA ? unpack<T>(rb[i]) : ones<T>();
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       e[i][c] = decay_of<T>(lv.v[c]);
@@ -267,9 +335,6 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, int nsla
       l[c] += lv.v[c];
     }
   }
-  const int cl = g.slab * kSlab + lane;  // lane = channel
-  const long long at = (long long)g.b * C + cl;
-  const float first = a.h0 && cl < C ? a.h0[at] : 0.f;
   const auto self = [&]() {
     if (cl >= C) return 0.f;
     const int hh = cl / a.d, jj = cl % a.d;
@@ -287,9 +352,13 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, int nsla
     return (float)run;
   };
   uint32_t* words = static_cast<uint32_t*>(a.ws) + (long long)g.chain * kWords;
-  relay<T, WAVES>(mem, l, z, h, words, (long long)nslab * a.B * kWords, g.s, g.s == g.ntile - 1, first, polls,
+  relay<T, WAVES>(mem, l, z, h, words, (long long)n.nchain * kWords, g.s, g.s == g.ntile - 1, first, window, polls,
                   cl < C ? a.h_T + at : nullptr, self);
   if (!on) return;
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int c = 0; c < V; ++c) asm volatile("" : "+v"(e[i][c]), "+v"(in[i][c]));
   T* o = static_cast<T*>(a.o) + g.b * a.os.b + hd * a.os.h + j0;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
@@ -299,7 +368,7 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, int nsla
       h[c] = advance<State<T>>(e[i][c], h[c], in[i][c]);
       y.v[c] = (float)h[c];
     }
-    if (t0 + i < g.len) st16(o + (long long)(t0 + i) * a.os.t, pack<T>(y));
+    if (full || t0 + i < g.len) st_once(o + (t0 + i) * a.os.t, pack<T>(y));
   }
 }
 
@@ -342,10 +411,11 @@ __global__ __launch_bounds__(256) void kda_glr_step_kernel(GlrArgs a, int nvec) 
 // The gradients' chain runs from the last token to the first: mu_t = a_t (dO_t + mu_{t+1}), the same relay
 // with the tiles, and the tokens in them, in reverse.
 template <typename T, int NT, int WAVES, bool NORM, bool BETA>
-__global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, int nslab, int polls) {
+__global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, GlrGrid n, int window, int polls) {
   constexpr int V = kVec<T>, LPR = kLpr<T>, SUB = kSub<T>, RUN = WAVES * SUB * NT;
   __shared__ RelayMem<T, WAVES> mem;
-  const GlrTile g(a, nslab, RUN);
+  const GlrTile g(a, n, RUN);
+  if (g.none) return;
   const int lane = threadIdx.x & 63, C = a.H * a.d;
   const int tile = g.s < g.ntile ? g.ntile - 1 - g.s : g.s;  // behind the sequence: only zeros
   const int t0 = (tile + 1) * RUN - 1 - ((int)(threadIdx.x >> 6) * SUB + lane / LPR) * NT;  // a lane's tokens: t0, t0 - 1, ...
@@ -372,25 +442,20 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, int 
   const T* beta = BETA ? static_cast<const T*>(a.beta) + g.b * a.bs.b + hd * a.bs.h + j0 : nullptr;
   const T* o = static_cast<const T*>(a.o) + g.b * a.os.b + hd * a.os.h + j0;
   const T* dO = static_cast<const T*>(a.dO) + g.b * a.dos.b + hd * a.dos.h + j0;
+  const int cl = g.slab * kSlab + lane;  // lane = channel
+  const long long at = (long long)g.b * C;
+  const float first = a.dh_T && cl < C ? a.dh_T[at + cl] : 0.f;
+  if (g.len == 0) {
+    if (threadIdx.x < 64 && cl < C && a.dh0) a.dh0[at + cl] = first;
+    return;
+  }
+  const bool full = (tile + 1) * RUN <= g.len && (g.slab + 1) * kSlab <= C;
   u32x4 rx[NT], rl[NT], rb[NT], rg[NT], ro[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    rx[i] = rl[i] = rb[i] = rg[i] = ro[i] = zero;
-    if (on && t0 - i < g.len) {
-      const long long t = t0 - i;
-      rl[i] = ld16(la + t * a.ls.t);
-      rg[i] = ld16(dO + t * a.dos.t);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    if (on && t0 - i < g.len) {
-      const long long t = t0 - i;
-      rx[i] = ld16(x + t * a.xs.t);
-      if constexpr (BETA) rb[i] = ld16(beta + t * a.bs.t);
-      if (t > 0) ro[i] = ld16(o + (t - 1) * a.os.t);
-    }
-  }
+  load_rows<T, NT, -1>(rl, la, a.ls.t, t0, g.len, on, full);
+  load_rows<T, NT, -1>(rg, dO, a.dos.t, t0, g.len, on, full);
+  load_rows<T, NT, -1>(rx, x, a.xs.t, t0, g.len, on, full);
+  if constexpr (BETA) load_rows<T, NT, -1>(rb, beta, a.bs.t, t0, g.len, on, full);
+  load_rows<T, NT, -1>(ro, o, a.os.t, t0 - 1, g.len, on, full && tile > 0);
   float e[NT][V], l[V];
   State<T> mu[V], z[V];
 #pragma unroll
@@ -408,9 +473,6 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, int 
       l[c] += lv.v[c];
     }
   }
-  const int cl = g.slab * kSlab + lane;  // lane = channel
-  const long long at = (long long)g.b * C;
-  const float first = a.dh_T && cl < C ? a.dh_T[at + cl] : 0.f;
   const auto self = [&]() {
     if (cl >= C) return 0.f;
     const int hh = cl / a.d, jj = cl % a.d;
@@ -422,7 +484,7 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, int 
     return (float)run;
   };
   uint32_t* words = static_cast<uint32_t*>(a.ws) + (long long)g.chain * kWords;
-  relay<T, WAVES>(mem, l, z, mu, words, (long long)nslab * a.B * kWords, g.s, g.s == g.ntile - 1, first, polls,
+  relay<T, WAVES>(mem, l, z, mu, words, (long long)n.nchain * kWords, g.s, g.s == g.ntile - 1, first, window, polls,
                   a.dh0 && cl < C ? a.dh0 + at + cl : nullptr, self);
   if (!on) return;
 #pragma unroll
@@ -441,17 +503,17 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, int 
       float n = 1.f, part = 0.f;
       if constexpr (NORM) {
         n = unit_of(ee);
-        part = n > 0.f ? al * al / n * (bv.v[c] * xv.v[c]) : 0.f;
+        part = n > 0.f ? al * al * __builtin_amdgcn_rcpf(n) * (bv.v[c] * xv.v[c]) : 0.f;
       }
       gx.v[c] = n * bv.v[c] * lam;
       gb.v[c] = n * xv.v[c] * lam;
       gl.v[c] = al == 0.f ? 0.f : (al * before.v[c] - part) * lam;
       mu[c] = advance<State<T>>(ee, mu[c], 0);
     }
-    if (t >= g.len) continue;
-    st16(dx + t * a.dxs.t, pack<T>(gx));
-    st16(dla + t * a.dls.t, pack<T>(gl));
-    if constexpr (BETA) st16(dbeta + t * a.dbs.t, pack<T>(gb));
+    if (!full && t >= g.len) continue;
+    st_once(dx + t * a.dxs.t, pack<T>(gx));
+    st_once(dla + t * a.dls.t, pack<T>(gl));
+    if constexpr (BETA) st_once(dbeta + t * a.dbs.t, pack<T>(gb));
   }
 }
 
@@ -481,43 +543,50 @@ __global__ __launch_bounds__(256) void kda_glr_check_kernel(GlrArgs a, int nvec,
   if (bad) atomicOr(bits, bad);
 }
 
+// Tokens per lane.  More of them make a tile longer, and a chain's way through its tiles shorter, but
+// take registers, and with them the waves that hide each other's latency.  Measured, in us: four 8K prompts in
+// bf16 271, 228, 270 with 2, 4, 8 and their gradients 456, 497 with 2, 4; two in fp32 234, 201, 199 with 2, 4,
+// 8, one 16K prompt of 2048 channels 139, 96, 83, gradients 422, 431 with 2, 4.
 #ifndef GLR_NT
-#define GLR_NT 8
+#define GLR_NT (sizeof(T) == 2 ? 4 : 8)
 #endif
 #ifndef GLR_NTB
-#define GLR_NTB 4
+#define GLR_NTB 2
 #endif
-#ifndef GLR_WAVES
-#define GLR_WAVES 4
-#endif
-struct GlrPlan {
-  int nslab, ntile;
-  long long chains;
-};
-template <typename T>
-GlrPlan glr_plan(int B, int H, int T_, int d, int nt, int waves) {
-  GlrPlan p;
-  p.nslab = (H * d + kSlab - 1) / kSlab;
-  p.chains = (long long)p.nslab * B;
-  const int run = waves * kSub<T> * nt;
-  p.ntile = T_ > 0 ? (int)(((long long)T_ + run - 1) / run) : 1;
-  return p;
+template <typename T, bool GRADIENTS> constexpr int kTokens = GRADIENTS ? GLR_NTB : GLR_NT;
+constexpr int kWaves = 4;
+
+template <typename T, bool GRADIENTS>
+GlrGrid glr_grid(int B, int H, int len, int d) {
+  constexpr int run = kWaves * kSub<T> * kTokens<T, GRADIENTS>;
+  GlrGrid n;
+  n.nslab = (H * d + kSlab - 1) / kSlab;
+  n.nchain = n.nslab * B;
+  n.ntile = len > 0 ? (len + run - 1) / run : 1;
+  n.spread = n.nchain >= 64 || (n.nchain % 8 == 0 && n.nchain > 0);
+  n.blocks = n.spread ? (n.nchain + 7) / 8 * 8 : n.nchain;
+  return n;
 }
 
-template <typename T, int NT, int WAVES, bool BWD>
+template <typename T, bool GRADIENTS>
 hipError_t glr_launch(const GlrArgs& a, int polls, hipStream_t stream) {
-  const GlrPlan p = glr_plan<T>(a.B, a.H, a.T, a.d, NT, WAVES);
-  if (p.ntile > 1) {
-    const long long n = p.chains * p.ntile * kWords / 4;
-    hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, static_cast<u32x4*>(a.ws), n);
+  constexpr int NT = kTokens<T, GRADIENTS>;
+  const GlrGrid n = glr_grid<T, GRADIENTS>(a.B, a.H, a.T, a.d);
+  if (n.ntile > 1) {
+    const long long words = (long long)n.nchain * n.ntile * kWords / 4;
+    hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream, static_cast<u32x4*>(a.ws), words);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 grid((unsigned)(p.chains * p.ntile));
-#define KDA_GLR(NO, BE)                                                                                                        \
-  do {                                                                                                                         \
-    if constexpr (BWD) hipLaunchKernelGGL((kda_glr_bwd_kernel<T, NT, WAVES, NO, BE>), grid, dim3(64 * WAVES), 0, stream, a, p.nslab, polls); \
-    else hipLaunchKernelGGL((kda_glr_kernel<T, NT, WAVES, NO, BE>), grid, dim3(64 * WAVES), 0, stream, a, p.nslab, polls);     \
+  const dim3 grid((unsigned)((long long)n.blocks * n.ntile));
+  // tiles of a chain that are under way together, and one more: 1024 workgroups fit the device
+  const int window = 1 + 1024 / n.nchain;
+#define KDA_GLR(NO, BE)                                                                                                   \
+  do {                                                                                                                    \
+    if constexpr (GRADIENTS)                                                                                              \
+      hipLaunchKernelGGL((kda_glr_bwd_kernel<T, NT, kWaves, NO, BE>), grid, dim3(64 * kWaves), 0, stream, a, n, window, polls); \
+    else                                                                                                                  \
+      hipLaunchKernelGGL((kda_glr_kernel<T, NT, kWaves, NO, BE>), grid, dim3(64 * kWaves), 0, stream, a, n, window, polls);     \
   } while (0)
   if (a.norm && a.beta) KDA_GLR(true, true);
   else if (a.norm) KDA_GLR(true, false);
@@ -525,6 +594,12 @@ hipError_t glr_launch(const GlrArgs& a, int polls, hipStream_t stream) {
   else KDA_GLR(false, false);
 #undef KDA_GLR
   return hipGetLastError();
+}
+
+template <typename T, bool GRADIENTS>
+size_t glr_words(int B, int H, int len, int d) {
+  const GlrGrid n = glr_grid<T, GRADIENTS>(B, H, len, d);
+  return n.ntile > 1 ? (size_t)n.nchain * n.ntile * kWords : 0;
 }
 
 template <typename T>
@@ -537,18 +612,18 @@ hipError_t glr_step(const GlrArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients, int) {
-  const int nt = gradients ? GLR_NTB : GLR_NT;
-  const GlrPlan p = bf16_io ? glr_plan<bf16>(B, H, T, d, nt, GLR_WAVES) : glr_plan<float>(B, H, T, d, nt, GLR_WAVES);
-  return p.ntile > 1 ? (size_t)p.chains * p.ntile * kWords * sizeof(uint32_t) : 0;
+size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients) {
+  const size_t n = bf16_io ? (gradients ? glr_words<bf16, true>(B, H, T, d) : glr_words<bf16, false>(B, H, T, d))
+                           : (gradients ? glr_words<float, true>(B, H, T, d) : glr_words<float, false>(B, H, T, d));
+  return n * sizeof(uint32_t);
 }
 
 hipError_t launch_glr(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream) {
-  return bf16_io ? glr_launch<bf16, GLR_NT, GLR_WAVES, false>(a, polls, stream) : glr_launch<float, GLR_NT, GLR_WAVES, false>(a, polls, stream);
+  return bf16_io ? glr_launch<bf16, false>(a, polls, stream) : glr_launch<float, false>(a, polls, stream);
 }
 
 hipError_t launch_glr_backward(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream) {
-  return bf16_io ? glr_launch<bf16, GLR_NTB, GLR_WAVES, true>(a, polls, stream) : glr_launch<float, GLR_NTB, GLR_WAVES, true>(a, polls, stream);
+  return bf16_io ? glr_launch<bf16, true>(a, polls, stream) : glr_launch<float, true>(a, polls, stream);
 }
 
 hipError_t launch_glr_step(const GlrArgs& a, bool bf16_io, hipStream_t stream) {

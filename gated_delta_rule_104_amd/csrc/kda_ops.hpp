@@ -115,7 +115,7 @@ struct GlrArgs {
   Str3 dos, dxs, dls, dbs;
   void* ws = nullptr;
 };
-size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients, int cus);
+size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients);
 // polls: how often a run of tokens looks for the state in front of it before it walks the sequence itself
 hipError_t launch_glr(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream);
 hipError_t launch_glr_step(const GlrArgs& a, bool bf16_io, hipStream_t stream);

@@ -401,7 +401,7 @@ kda_status glr_dims(int B, int H, int T, int d, kda_dtype dtype) {
   if ((long long)d * es % 16) return api_fail(KDA_ERR_UNSUPPORTED, "rows of %d elements are not a multiple of 16 bytes", d);
   const long long C = (long long)H * d;
   if (C > (1 << 28) || T > (1 << 30) || (long long)B * C > kMaxElems || (long long)B * C * T > kMaxElems ||
-      (long long)B * ((C + 63) / 64) * (T / 32 + 1) > INT32_MAX)
+      ((long long)B * ((C + 63) / 64) + 8) * (T / 32 + 1) > INT32_MAX)
     return api_fail(KDA_ERR_SHAPE, "problem too large");
   return KDA_OK;
 }
@@ -439,7 +439,7 @@ kda_status need_workspace(const void* workspace, size_t have, size_t bytes) {
 
 size_t kda_glr_prefill_workspace_bytes(int B, int H, int T, int d, kda_dtype dtype) {
   if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || glr_dims(B, H, T, d, dtype) != KDA_OK) return 0;
-  return kda::glr_ws_bytes(B, H, T, d, dtype == KDA_BF16, false, kda::api_cu_count());
+  return kda::glr_ws_bytes(B, H, T, d, dtype == KDA_BF16, false);
 }
 
 kda_status kda_glr_prefill(const void* x, const void* log_alpha, const void* beta, const float* h0, const int* lens,
@@ -490,7 +490,7 @@ kda_status kda_glr_step(const void* x, const void* log_alpha, const void* beta, 
 
 size_t kda_glr_backward_workspace_bytes(int B, int H, int T, int d, kda_dtype dtype) {
   if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || glr_dims(B, H, T, d, dtype) != KDA_OK) return 0;
-  return kda::glr_ws_bytes(B, H, T, d, dtype == KDA_BF16, true, kda::api_cu_count());
+  return kda::glr_ws_bytes(B, H, T, d, dtype == KDA_BF16, true);
 }
 
 kda_status kda_glr_backward(const void* x, const void* log_alpha, const void* beta, const float* h0, const void* o,
