@@ -543,63 +543,56 @@ __global__ __launch_bounds__(256) void kda_glr_check_kernel(GlrArgs a, int nvec,
   if (bad) atomicOr(bits, bad);
 }
 
-// Tokens per lane.  More of them make a tile longer, and a chain's way through its tiles shorter, but
-// take registers, and with them the waves that hide each other's latency.  Measured, in us: four 8K prompts in
-// bf16 271, 228, 270 with 2, 4, 8 and their gradients 456, 497 with 2, 4; two in fp32 234, 201, 199 with 2, 4,
-// 8, one 16K prompt of 2048 channels 139, 96, 83, gradients 422, 431 with 2, 4.
-#ifndef GLR_NT
-#define GLR_NT (sizeof(T) == 2 ? 4 : 8)
-#endif
-#ifndef GLR_NTB
-#define GLR_NTB 2
-#endif
-template <typename T, bool GRADIENTS> constexpr int kTokens = GRADIENTS ? GLR_NTB : GLR_NT;
 constexpr int kWaves = 4;
 
-template <typename T, bool GRADIENTS>
-GlrGrid glr_grid(int B, int H, int len, int d) {
-  constexpr int run = kWaves * kSub<T> * kTokens<T, GRADIENTS>;
+// Tokens per lane.  More of them make a tile longer, and a chain's way through its tiles shorter, but take
+// registers, and with them the waves that hide each other's latency.  So few chains, whose way
+// bounds the call, take more than many, and calls without beta, which hold a tensor less, more than
+// calls with it.  bf16, 268M values in up to 64K tokens (fewer with under 16 chains), us with 4 / 6 / 8 tokens:
+//   prompt           256 chains 211 / 268 / 244   64 223 / 272 / 245   16 134 / 152 / 140   4  74 / 53 / 48
+//   without beta     256        171 / 168 / 203   64 179 / 173 / 206   16 111 / 105 / 116   4  72 / 53 / 43
+// with 2 / 3 / 4 tokens:
+//   gradients        256        439 / 444 / 468   64 443 / 456 / 468   40 453 / 429 / 456   4 141 / 105 / 86
+//   without beta     256        310 / 272 / 273   64 323 / 293 / 285   40 340 / 292 / 282   4 133 / 95 / 73
+// fp32 holds half as many values per lane and token: prompts of 128 chains 234 / 201 / 199 with 2 / 4 / 8, gradients 403 /
+// 377 with 2 / 4, and the longer ones win with fewer chains too.
+int glr_tokens(bool bf16_io, bool gradients, bool beta, int nchain) {
+  if (!bf16_io) return gradients ? 4 : 8;
+  if (gradients) return !beta || nchain <= 8 ? 4 : (nchain < 64 ? 3 : 2);
+  return nchain <= 8 ? 8 : (beta ? 4 : 6);
+}
+
+GlrGrid glr_grid(int B, int H, int len, int d, bool bf16_io, bool gradients, bool beta, int* tokens) {
   GlrGrid n;
   n.nslab = (H * d + kSlab - 1) / kSlab;
   n.nchain = n.nslab * B;
+  *tokens = glr_tokens(bf16_io, gradients, beta, n.nchain);
+  const int run = kWaves * (bf16_io ? kSub<bf16> : kSub<float>) * *tokens;
   n.ntile = len > 0 ? (len + run - 1) / run : 1;
   n.spread = n.nchain >= 64 || (n.nchain % 8 == 0 && n.nchain > 0);
   n.blocks = n.spread ? (n.nchain + 7) / 8 * 8 : n.nchain;
   return n;
 }
 
-template <typename T, bool GRADIENTS>
-hipError_t glr_launch(const GlrArgs& a, int polls, hipStream_t stream) {
-  constexpr int NT = kTokens<T, GRADIENTS>;
-  const GlrGrid n = glr_grid<T, GRADIENTS>(a.B, a.H, a.T, a.d);
+template <typename T, bool GRADIENTS, int NT, bool BETA>
+hipError_t glr_launch(const GlrArgs& a, const GlrGrid& n, int polls, hipStream_t stream) {
   if (n.ntile > 1) {
     const long long words = (long long)n.nchain * n.ntile * kWords / 4;
     hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream, static_cast<u32x4*>(a.ws), words);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 grid((unsigned)((long long)n.blocks * n.ntile));
-  // tiles of a chain that are under way together, and one more: 1024 workgroups fit the device
+  const dim3 grid((unsigned)((long long)n.blocks * n.ntile)), threads(64 * kWaves);
+  // tiles of a chain that are under way together, and one more: about 1024 workgroups fit the device
   const int window = 1 + 1024 / n.nchain;
-#define KDA_GLR(NO, BE)                                                                                                   \
-  do {                                                                                                                    \
-    if constexpr (GRADIENTS)                                                                                              \
-      hipLaunchKernelGGL((kda_glr_bwd_kernel<T, NT, kWaves, NO, BE>), grid, dim3(64 * kWaves), 0, stream, a, n, window, polls); \
-    else                                                                                                                  \
-      hipLaunchKernelGGL((kda_glr_kernel<T, NT, kWaves, NO, BE>), grid, dim3(64 * kWaves), 0, stream, a, n, window, polls);     \
-  } while (0)
-  if (a.norm && a.beta) KDA_GLR(true, true);
-  else if (a.norm) KDA_GLR(true, false);
-  else if (a.beta) KDA_GLR(false, true);
-  else KDA_GLR(false, false);
-#undef KDA_GLR
+  if constexpr (GRADIENTS) {
+    if (a.norm) hipLaunchKernelGGL((kda_glr_bwd_kernel<T, NT, kWaves, true, BETA>), grid, threads, 0, stream, a, n, window, polls);
+    else hipLaunchKernelGGL((kda_glr_bwd_kernel<T, NT, kWaves, false, BETA>), grid, threads, 0, stream, a, n, window, polls);
+  } else {
+    if (a.norm) hipLaunchKernelGGL((kda_glr_kernel<T, NT, kWaves, true, BETA>), grid, threads, 0, stream, a, n, window, polls);
+    else hipLaunchKernelGGL((kda_glr_kernel<T, NT, kWaves, false, BETA>), grid, threads, 0, stream, a, n, window, polls);
+  }
   return hipGetLastError();
-}
-
-template <typename T, bool GRADIENTS>
-size_t glr_words(int B, int H, int len, int d) {
-  const GlrGrid n = glr_grid<T, GRADIENTS>(B, H, len, d);
-  return n.ntile > 1 ? (size_t)n.nchain * n.ntile * kWords : 0;
 }
 
 template <typename T>
@@ -613,17 +606,31 @@ hipError_t glr_step(const GlrArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients) {
-  const size_t n = bf16_io ? (gradients ? glr_words<bf16, true>(B, H, T, d) : glr_words<bf16, false>(B, H, T, d))
-                           : (gradients ? glr_words<float, true>(B, H, T, d) : glr_words<float, false>(B, H, T, d));
-  return n * sizeof(uint32_t);
+  size_t most = 0;
+  for (int beta = 0; beta < 2; ++beta) {
+    int nt;
+    const GlrGrid n = glr_grid(B, H, T, d, bf16_io, gradients, beta != 0, &nt);
+    const size_t bytes = n.ntile > 1 ? (size_t)n.nchain * n.ntile * kWords * sizeof(uint32_t) : 0;
+    most = bytes > most ? bytes : most;
+  }
+  return most;
 }
 
 hipError_t launch_glr(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream) {
-  return bf16_io ? glr_launch<bf16, false>(a, polls, stream) : glr_launch<float, false>(a, polls, stream);
+  int nt;
+  const GlrGrid n = glr_grid(a.B, a.H, a.T, a.d, bf16_io, false, a.beta != nullptr, &nt);
+  if (!bf16_io) return a.beta ? glr_launch<float, false, 8, true>(a, n, polls, stream) : glr_launch<float, false, 8, false>(a, n, polls, stream);
+  if (a.beta) return nt == 8 ? glr_launch<bf16, false, 8, true>(a, n, polls, stream) : glr_launch<bf16, false, 4, true>(a, n, polls, stream);
+  return nt == 8 ? glr_launch<bf16, false, 8, false>(a, n, polls, stream) : glr_launch<bf16, false, 6, false>(a, n, polls, stream);
 }
 
 hipError_t launch_glr_backward(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream) {
-  return bf16_io ? glr_launch<bf16, true>(a, polls, stream) : glr_launch<float, true>(a, polls, stream);
+  int nt;
+  const GlrGrid n = glr_grid(a.B, a.H, a.T, a.d, bf16_io, true, a.beta != nullptr, &nt);
+  if (!bf16_io) return a.beta ? glr_launch<float, true, 4, true>(a, n, polls, stream) : glr_launch<float, true, 4, false>(a, n, polls, stream);
+  if (!a.beta) return glr_launch<bf16, true, 4, false>(a, n, polls, stream);
+  if (nt == 2) return glr_launch<bf16, true, 2, true>(a, n, polls, stream);
+  return nt == 3 ? glr_launch<bf16, true, 3, true>(a, n, polls, stream) : glr_launch<bf16, true, 4, true>(a, n, polls, stream);
 }
 
 hipError_t launch_glr_step(const GlrArgs& a, bool bf16_io, hipStream_t stream) {

@@ -175,13 +175,13 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(
   const auto value = [&](int j, int i, const T* w) {
     Row<T> y = unpack<T>(xr[j][i]);
     const int vec = i * PER + lane;
-#pragma unroll
-    for (int c = 0; c < V; ++c) y.v[c] *= scale[j];
-    if (w) {
+    if (w) {  // (of bf16 values this product is exact)
       const Row<T> k = unpack<T>(vec < nvec ? ld16(w + vec * V) : u32x4{0u, 0u, 0u, 0u});
 #pragma unroll
       for (int c = 0; c < V; ++c) y.v[c] *= k.v[c];
     }
+#pragma unroll
+    for (int c = 0; c < V; ++c) y.v[c] *= scale[j];
     if (a.gate) {
       const Row<T> g = unpack<T>(gr[j][i]);
 #pragma unroll
