@@ -16,7 +16,7 @@ namespace kda {
 
 namespace {
 
-constexpr int kChunk = 8192;  // probabilities of a row per workgroup
+constexpr int kChunk = 4096;  // probabilities of a row per workgroup
 
 struct Choice {
   int accepted, count, token;  // token: the refused one
@@ -62,11 +62,10 @@ struct Rows {
   const T* p;
   const T* q;  // after a refusal
   int token;   // after a refusal without q: the token whose q is one, else -1
-  __device__ __forceinline__ Rows(const VerifyArgs& a, int n, const Choice& c) {
-    const bool refused = c.accepted < c.count;
-    p = static_cast<const T*>(a.p) + n * a.pn + c.accepted * a.pt;
-    q = refused && a.q ? static_cast<const T*>(a.q) + n * a.qn + c.accepted * a.qt : nullptr;
-    token = refused && !a.q ? c.token : -1;
+  __device__ __forceinline__ Rows(const VerifyArgs& a, int n, int accepted, int refused_token, bool refused) {
+    p = static_cast<const T*>(a.p) + n * a.pn + accepted * a.pt;
+    q = refused && a.q ? static_cast<const T*>(a.q) + n * a.qn + accepted * a.qt : nullptr;
+    token = refused && !a.q ? refused_token : -1;
   }
 };
 
@@ -111,15 +110,26 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// The sums of every chunk: what is left, and the whole.  The first chunk's block writes how far the
-// sequence is accepted.
+// A sequence's record in the workspace: (accepted, refused token or -1, refused, 0), then the chunks' sums.
+struct Record {
+  int4* choice;
+  double2* sums;  // of every chunk: what is left, and the whole
+  __device__ __forceinline__ Record(const VerifyArgs& a, int n, int nchunk)
+      : choice(reinterpret_cast<int4*>(a.ws) + (size_t)n * (nchunk + 1)), sums(reinterpret_cast<double2*>(choice + 1)) {}
+};
+
+// The first chunk's block writes how far the sequence is accepted.
 template <typename T>
 __global__ __launch_bounds__(256) void kda_verify_sum_kernel(VerifyArgs a, int nchunk) {
   __shared__ double red[2][4];
   const int n = blockIdx.x / nchunk, chunk = blockIdx.x % nchunk;
   const Choice choice = accept<T>(a, n);
-  if (chunk == 0 && threadIdx.x == 0) a.accepted[n] = choice.accepted;
-  const Rows<T> r(a, n, choice);
+  const Record rec(a, n, nchunk);
+  if (chunk == 0 && threadIdx.x == 0) {
+    a.accepted[n] = choice.accepted;
+    *rec.choice = int4{choice.accepted, choice.token, choice.accepted < choice.count, 0};
+  }
+  const Rows<T> r(a, n, choice.accepted, choice.token, choice.accepted < choice.count);
   const int c0 = chunk * kChunk, end = min(c0 + kChunk, a.V);
   double s = 0.0, whole = 0.0;
   constexpr int V = kVec<T>;
@@ -142,89 +152,70 @@ __global__ __launch_bounds__(256) void kda_verify_sum_kernel(VerifyArgs a, int n
   __syncthreads();
   if (threadIdx.x < 2) {
     const double* v = red[threadIdx.x];
-    a.ws[((size_t)n * nchunk + chunk) * 2 + threadIdx.x] = ((v[0] + v[1]) + v[2]) + v[3];
+    reinterpret_cast<double*>(rec.sums + chunk)[threadIdx.x] = ((v[0] + v[1]) + v[2]) + v[3];
   }
 }
 
-// The sum in front of each of the block's 256 threads, and the whole one.
-__device__ __forceinline__ double block_scan(double v, double* red, double* total) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  double s = v;
+// The sum up to and including each lane's v.
+__device__ __forceinline__ double wave_scan(double v) {
+  const int lane = lane_id();
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
-    const double u = __shfl_up(s, m);
-    if (lane >= m) s += u;
+    const double u = __shfl_up(v, m);
+    if (lane >= m) v += u;
   }
-  double front = __shfl_up(s, 1);
-  if (lane == 0) front = 0.0;
-  __syncthreads();  // (red may still be read from the scan before)
-  if (lane == 63) red[w] = s;
-  __syncthreads();
-  for (int u = 0; u < w; ++u) front += red[u];
-  *total = ((red[0] + red[1]) + red[2]) + red[3];
-  return front;
+  return v;
 }
 
-// One workgroup per sequence: which chunk the threshold lies in, and which token.  Where rounding
-// leaves no sum above the threshold, the last token that has mass is taken.
+// One workgroup per sequence: every wave finds the chunk that the threshold lies in (lane = chunk), then the block
+// walks it, 8 probabilities a thread.  Where rounding leaves no sum above the threshold, the last token that has
+// mass is taken.  A chain of latencies: the record, the chunk, the sums over lanes and waves.
 template <typename T>
-__global__ __launch_bounds__(256) void kda_verify_pick_kernel(VerifyArgs a, int nchunk) {
-  constexpr int V = kVec<T>, OWN = kChunk / 256;  // a thread's neighbouring probabilities of the chunk
+__global__ __launch_bounds__(512) void kda_verify_pick_kernel(VerifyArgs a, int nchunk) {
+  constexpr int V = kVec<T>, OWN = kChunk / 512;  // a thread's neighbouring probabilities of the chunk
   constexpr int NONE = 0x7fffffff;
-  __shared__ double red[4], front_s;
+  __shared__ double front_of[8];
   __shared__ int first, last;
-  const int n = blockIdx.x, tid = threadIdx.x;
+  const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Record rec(a, n, nchunk);
+  const int4 choice = *rec.choice;
+  const float u = a.u[(long long)n * (a.K + 1) + a.K];
+  double2 v{0.0, 0.0};
+  if (lane < nchunk) v = rec.sums[lane];
   if (tid == 0) {
     first = NONE;
     last = -1;
   }
-  Choice c{a.accepted[n], a.K, -1};
-  if (a.counts) c.count = min(max(a.counts[n], 0), a.K);
-  if (c.accepted < c.count) c.token = a.tokens[(long long)n * a.K + c.accepted];
-  const double* sums = a.ws + (size_t)n * nchunk * 2;
-  double left = 0.0, whole = 0.0, total_left, total;
-  for (int i = tid; i < nchunk; i += 256) {
-    left += sums[2 * i];
-    whole += sums[2 * i + 1];
+  double left = v.x, whole = v.y;
+  for (int i = lane + 64; i < nchunk; i += 64) {
+    const double2 x = rec.sums[i];
+    left += x.x;
+    whole += x.y;
   }
-  block_scan(left, red, &total_left);
-  block_scan(whole, red, &total);
-  Rows<T> r(a, n, c);
-  const bool rest = total_left > 0.0;
-  if (rest) {
-    total = total_left;
-  } else {  // q covers all of p: the token is drawn from p
-    r.q = nullptr;
-    r.token = -1;
-  }
-  const double goal = (double)a.u[(long long)n * (a.K + 1) + a.K] * total;
-  double base = 0.0;
-  for (int i0 = 0; i0 < nchunk; i0 += 256) {
-    const int i = i0 + tid;
-    const double v = i < nchunk ? sums[2 * i + (rest ? 0 : 1)] : 0.0;
-    double all;
-    const double before = base + block_scan(v, red, &all);
-    if (v > 0.0) {
-      atomicMax(&last, i);
-      if (before + v > goal) atomicMin(&first, i);
+  left = wave_sum(left);
+  whole = wave_sum(whole);
+  const bool rest = left > 0.0;  // else q covers all of p: the token is drawn from p
+  const Rows<T> r(a, n, choice.x, rest ? choice.y : -1, rest && choice.z);
+  const double goal = (double)u * (rest ? left : whole);
+  int chunk = -1;  // the first one whose running sum is above the goal, or the last that has mass
+  bool sure = false;
+  double front = 0.0, base = 0.0;
+  for (int i0 = 0; i0 < nchunk; i0 += 64) {
+    if (i0 > 0) v = i0 + lane < nchunk ? rec.sums[i0 + lane] : double2{0.0, 0.0};
+    const double mine = rest ? v.x : v.y, sum = base + wave_scan(mine);
+    const unsigned long long above = __ballot(mine > 0.0 && sum > goal), any = __ballot(mine > 0.0);
+    if (above) {
+      const int at = __ffsll(above) - 1;
+      chunk = i0 + at;
+      sure = true;
+      front = at ? __shfl(sum, at - 1) : base;
+      break;
     }
-    __syncthreads();
-    if (i == first) front_s = before;
-    base += all;
-    const bool done = first != NONE;
-    __syncthreads();
-    if (done) break;
+    if (any) chunk = i0 + 63 - __clzll(any);
+    base = __shfl(sum, 63);
   }
-  const int chunk = first != NONE ? first : last;
-  const bool sure = first != NONE;
-  const double front = front_s;
   int token = -1;
   if (chunk >= 0) {
-    __syncthreads();
-    if (tid == 0) {
-      first = NONE;
-      last = -1;
-    }
     const int c0 = chunk * kChunk, end = min(c0 + kChunk, a.V), mine = c0 + tid * OWN;
     double w[OWN], s = 0.0;
 #pragma unroll
@@ -236,7 +227,12 @@ __global__ __launch_bounds__(256) void kda_verify_pick_kernel(VerifyArgs a, int 
     }
 #pragma unroll
     for (int i = 0; i < OWN; ++i) s += w[i];
-    double all, run = front + block_scan(s, red, &all);  // (its barriers order the reset above)
+    const double upto = wave_scan(s);
+    if (lane == 63) front_of[wave] = upto;
+    __syncthreads();
+    double run = __shfl_up(upto, 1);
+    run = (lane ? run : 0.0) + front;
+    for (int k = 0; k < wave; ++k) run += front_of[k];
     int hit = NONE, behind = -1;
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
@@ -246,14 +242,15 @@ __global__ __launch_bounds__(256) void kda_verify_pick_kernel(VerifyArgs a, int 
         if (hit == NONE && run > goal) hit = mine + i;
       }
     }
-    if (sure && hit != NONE) atomicMin(&first, hit);
-    if (behind >= 0) atomicMax(&last, behind);
+    const unsigned long long hits = __ballot(hit != NONE), some = __ballot(behind >= 0);
+    if (sure && hits && lane == __ffsll(hits) - 1) atomicMin(&first, hit);
+    if (some && lane == 63 - __clzll(some)) atomicMax(&last, behind);
     __syncthreads();
     token = first != NONE ? first : last;
   }
-  for (int j = tid; j <= a.K; j += 256)
+  for (int j = tid; j <= a.K; j += 512)
     a.out[(long long)n * (a.K + 1) + j] =
-        j < c.accepted ? a.tokens[(long long)n * a.K + j] : (j == c.accepted ? token : -1);
+        j < choice.x ? a.tokens[(long long)n * a.K + j] : (j == choice.x ? token : -1);
 }
 
 // S[n] = S_pos[n][index[n]], by shares of a state's values; an index outside leaves S[n] as it is.
@@ -284,13 +281,13 @@ hipError_t verify(const VerifyArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((kda_verify_sum_kernel<T>), dim3((unsigned)((long long)a.N * nchunk)), dim3(256), 0, stream, a, nchunk);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((kda_verify_pick_kernel<T>), dim3((unsigned)a.N), dim3(256), 0, stream, a, nchunk);
+  hipLaunchKernelGGL((kda_verify_pick_kernel<T>), dim3((unsigned)a.N), dim3(512), 0, stream, a, nchunk);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t verify_ws_bytes(int N, int V) { return (size_t)N * verify_chunks(V) * 2 * sizeof(double); }
+size_t verify_ws_bytes(int N, int V) { return (size_t)N * (verify_chunks(V) + 1) * 16; }
 
 hipError_t launch_verify(const VerifyArgs& a, bool bf16_io, hipStream_t stream) {
   return bf16_io ? verify<bf16>(a, stream) : verify<float>(a, stream);

@@ -82,16 +82,6 @@ __device__ __forceinline__ Row<T> ones() {
 // between them is needed.  Waiting is bounded: a tile whose predecessors do not answer walks the
 // sequence from its start by itself, so the call ends whatever order workgroups run in.
 
-// Inputs are read and outputs written once: past the caches' normal order (four 8K prompts 241 -> 229 us).
-template <typename T>
-__device__ __forceinline__ u32x4 ld_once(const T* p) {
-  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-}
-template <typename T>
-__device__ __forceinline__ void st_once(T* p, u32x4 v) {
-  __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
-}
-
 constexpr int kSlab = 64;                // channels of a tile
 constexpr int kWords = 3 * kSlab;        // of a tile: l, z and the end state of each channel
 constexpr uint32_t kEmpty = 0xffffffffu;  // (a NaN that no published value has)
@@ -368,14 +358,18 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, GlrGrid 
       h[c] = advance<State<T>>(e[i][c], h[c], in[i][c]);
       y.v[c] = (float)h[c];
     }
-    if (full || t0 + i < g.len) st_once(o + (t0 + i) * a.os.t, pack<T>(y));
+    if (full || t0 + i < g.len) store_by(o + (t0 + i) * a.os.t, pack<T>(y), a.lines);
   }
 }
 
-// Empties the words of a call's tiles.
+// Empties the words of a call's tiles, 64 bytes a thread.
 __global__ __launch_bounds__(256) void kda_glr_clear_kernel(u32x4* words, long long n) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) words[i] = u32x4{kEmpty, kEmpty, kEmpty, kEmpty};
+  const u32x4 v{kEmpty, kEmpty, kEmpty, kEmpty};
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const long long i = (long long)blockIdx.x * 1024 + u * 256 + threadIdx.x;
+    if (i < n) words[i] = v;
+  }
 }
 
 // One token per sequence, the state in place.
@@ -511,9 +505,9 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, GlrG
       mu[c] = advance<State<T>>(ee, mu[c], 0);
     }
     if (!full && t >= g.len) continue;
-    st_once(dx + t * a.dxs.t, pack<T>(gx));
-    st_once(dla + t * a.dls.t, pack<T>(gl));
-    if constexpr (BETA) st_once(dbeta + t * a.dbs.t, pack<T>(gb));
+    store_by(dx + t * a.dxs.t, pack<T>(gx), a.lines);
+    store_by(dla + t * a.dls.t, pack<T>(gl), a.lines);
+    if constexpr (BETA) store_by(dbeta + t * a.dbs.t, pack<T>(gb), a.lines);
   }
 }
 
@@ -578,7 +572,7 @@ template <typename T, bool GRADIENTS, int NT, bool BETA>
 hipError_t glr_launch(const GlrArgs& a, const GlrGrid& n, int polls, hipStream_t stream) {
   if (n.ntile > 1) {
     const long long words = (long long)n.nchain * n.ntile * kWords / 4;
-    hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, stream, static_cast<u32x4*>(a.ws), words);
+    hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((words + 1023) / 1024)), dim3(256), 0, stream, static_cast<u32x4*>(a.ws), words);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -616,7 +610,15 @@ size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients) {
   return most;
 }
 
-hipError_t launch_glr(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream) {
+// (a tile's rows are 64 channels of heads that may lie apart)
+bool glr_lines(const GlrArgs& a, const void* p, Str3 s, bool bf16_io) {
+  const int es = bf16_io ? 2 : 4;
+  return whole_lines(p, s, (long long)a.B * a.H * a.T, (long long)a.d * es, es);
+}
+
+hipError_t launch_glr(const GlrArgs& args, bool bf16_io, int polls, hipStream_t stream) {
+  GlrArgs a = args;
+  a.lines = glr_lines(a, a.o, a.os, bf16_io);
   int nt;
   const GlrGrid n = glr_grid(a.B, a.H, a.T, a.d, bf16_io, false, a.beta != nullptr, &nt);
   if (!bf16_io) return a.beta ? glr_launch<float, false, 8, true>(a, n, polls, stream) : glr_launch<float, false, 8, false>(a, n, polls, stream);
@@ -624,7 +626,10 @@ hipError_t launch_glr(const GlrArgs& a, bool bf16_io, int polls, hipStream_t str
   return nt == 8 ? glr_launch<bf16, false, 8, false>(a, n, polls, stream) : glr_launch<bf16, false, 6, false>(a, n, polls, stream);
 }
 
-hipError_t launch_glr_backward(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream) {
+hipError_t launch_glr_backward(const GlrArgs& args, bool bf16_io, int polls, hipStream_t stream) {
+  GlrArgs a = args;
+  a.lines = glr_lines(a, a.dx, a.dxs, bf16_io) && glr_lines(a, a.dla, a.dls, bf16_io) &&
+            (!a.dbeta || glr_lines(a, a.dbeta, a.dbs, bf16_io));
   int nt;
   const GlrGrid n = glr_grid(a.B, a.H, a.T, a.d, bf16_io, true, a.beta != nullptr, &nt);
   if (!bf16_io) return a.beta ? glr_launch<float, true, 4, true>(a, n, polls, stream) : glr_launch<float, true, 4, false>(a, n, polls, stream);

@@ -52,21 +52,26 @@ __device__ __forceinline__ void row_reduce(float (&v)[NR], float* red) {
   }
 }
 
-// The gate's factor and, times z's own change, its derivative.
+// The gate's factor g(z) and its derivative, from sigma(z) and 1 - sigma(z) = e^-z sigma(z), which has all its
+// digits that way.  (e^-z is held below 2^126, where sigma is as good as zero.)
 template <typename T>
-__device__ __forceinline__ float gate_of(float z, bool silu) {
-  float s = sigmoid<T>(z);
-  if constexpr (sizeof(T) == 4) s = z == z ? s : z;  // (sigmoid holds its argument, and so a NaN, in range)
-  return silu ? z * s : s;
-}
-template <typename T>
-__device__ __forceinline__ void gate_grad(float z, bool silu, float& g, float& dg) {
-  float s = sigmoid<T>(z);
-  if constexpr (sizeof(T) == 4) s = z == z ? s : z;
-  const float c = sigmoid<T>(-z);  // 1 - s without its cancellation
-  g = silu ? z * s : s;
-  dg = silu ? s * (1.f + z * c) : s * c;
-}
+struct Gate {
+  float g, dg;
+  __device__ __forceinline__ Gate(float z, bool silu) {
+    constexpr float c = -1.44269504088896340736f, c_low = -1.92596299e-8f;  // -log2(e) in two floats
+    float e;
+    if constexpr (sizeof(T) == 2) {
+      e = __builtin_amdgcn_exp2f(fminf(c * z, 126.f));
+    } else {  // the exponent's own rounding is taken back
+      const float y = fminf(fmaxf(z, -87.f), 87.f), t = c * y, r = fmaf(c_low, y, fmaf(c, y, -t));
+      e = __builtin_amdgcn_exp2f(t) * fmaf(r, 0.69314718055994530942f, 1.f);
+    }
+    const float s = __builtin_amdgcn_rcpf(1.f + e), one_less = e * s;
+    g = silu ? z * s : s;
+    dg = silu ? s * fmaf(z, one_less, 1.f) : s * one_less;
+    if (z != z) g = dg = z;  // (the bounds above turn a NaN into a number)
+  }
+};
 
 // Offsets of a row in each tensor: its place (i0, i1, i2) in the dimensions that are left
 // after neighbouring ones have been joined.
@@ -101,8 +106,11 @@ __device__ __forceinline__ void store8(unsigned char* p, const Row<T>& y, float 
     const float a = y.v[4 * i] * scale, b = y.v[4 * i + 1] * scale, c = y.v[4 * i + 2] * scale, d = y.v[4 * i + 3] * scale;
     w[i] = e4m3 ? quant4<true>(a, b, c, d) : quant4<false>(a, b, c, d);
   }
-  if constexpr (kVec<T> == 8) *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
-  else *reinterpret_cast<uint32_t*>(p) = w[0];
+  if constexpr (kVec<T> == 8) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
+  } else {
+    *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
 }
 
 template <typename T>
@@ -141,9 +149,9 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(
       const int vec = i * PER + lane;
       const bool on = have[j] && vec < nvec;
       xr[j][i] = rr[j][i] = gr[j][i] = u32x4{0u, 0u, 0u, 0u};
-      if (on) xr[j][i] = ld16(x + vec * V);
-      if (on && r) rr[j][i] = ld16(r + vec * V);
-      if (on && g) gr[j][i] = ld16(g + vec * V);
+      if (on) xr[j][i] = ld_once(x + vec * V);
+      if (on && r) rr[j][i] = ld_once(r + vec * V);
+      if (on && g) gr[j][i] = ld_once(g + vec * V);
     }
   }
   float sum[NR];
@@ -185,7 +193,7 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(
     if (a.gate) {
       const Row<T> g = unpack<T>(gr[j][i]);
 #pragma unroll
-      for (int c = 0; c < V; ++c) y.v[c] *= gate_of<T>(g.v[c], a.silu);
+      for (int c = 0; c < V; ++c) y.v[c] *= Gate<T>(g.v[c], a.silu).g;
     }
     return y;
   };
@@ -199,10 +207,10 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(
     for (int i = 0; i < NV; ++i) {
       const int vec = i * PER + lane;
       const bool on = have[j] && vec < nvec;
-      if (a.s && on) st16(static_cast<T*>(a.s) + p.at(a.ss) + vec * V, xr[j][i]);
+      if (a.s && on) store_by(static_cast<T*>(a.s) + p.at(a.ss) + vec * V, xr[j][i], a.lines);
       Row<T> y = value(j, i, w);
       if constexpr (!BITS8) {
-        if (on) st16(static_cast<T*>(a.y) + p.at(a.ys) + vec * V, pack<T>(y));
+        if (on) store_by(static_cast<T*>(a.y) + p.at(a.ys) + vec * V, pack<T>(y), a.lines);
       } else {
         // (lanes behind the row's end have y = 0 r, NaN where the row's factor is not finite, as it is for the others)
         unsigned char* out = static_cast<unsigned char*>(a.y) + p.at(a.ys) + vec * V;
@@ -253,99 +261,115 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(
   }
 }
 
-// Gradients.  A block walks rows part, part + nparts, ... (in units of NR groups) of one weight row's
-// rows, so that a lane's columns stay the same and dw is summed in registers; one partial row of
-// sums per block goes to the workspace, and a second kernel adds the partials in a fixed order.
-template <typename T, int LANES, int WAVES, int NV, int NR>
+// Raw values that the compiler must take as freshly loaded: it would otherwise keep their fp32 forms, twice
+// the registers, from the sums over the row to the gradients.
+template <int NV>
+__device__ __forceinline__ void forget(u32x4 (&r)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(r[i]));
+}
+
+// NV vectors of a row, zeros outside.
+template <typename T, int PER, int NV, bool ONCE>
+__device__ __forceinline__ void load_row(u32x4 (&r)[NV], const T* p, int lane, int nvec, bool on) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int vec = i * PER + lane;
+    r[i] = u32x4{0u, 0u, 0u, 0u};
+    if (on && vec < nvec) r[i] = ONCE ? ld_once(p + vec * kVec<T>) : ld16(p + vec * kVec<T>);
+  }
+}
+
+// Gradients.  A block walks rows part, part + nparts, ... of one weight row's rows, so that a lane's columns
+// stay the same and dw is summed in registers; one partial row of sums per block goes to the workspace,
+// and a second kernel adds the partials in a fixed order.  AGAIN: rows too long for the registers are read
+// a second time, from the caches.
+template <typename T, int LANES, int WAVES, int NV, bool GATE, bool AGAIN>
 __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_bwd_kernel(NormArgs a) {
   constexpr int V = kVec<T>, THREADS = WAVES > 4 ? 64 * WAVES : 256;
   constexpr int PER = LANES * WAVES, GROUPS = THREADS / PER;
-  __shared__ float red[WAVES > 1 ? 2 * NR * WAVES : 1];
+  __shared__ float red[WAVES > 1 ? 2 * WAVES : 1];
   __shared__ float cols[GROUPS > 1 ? THREADS * NV * V : 1];
   const int lane = threadIdx.x % PER, group = threadIdx.x / PER;
   const int part = blockIdx.x % a.nparts, hw = blockIdx.x / a.nparts;
   const int nvec = a.d / V;
-  // rows of this weight row: (b, h, t), or (b, t) of head hw
-  const int rows = a.w_heads > 1 ? a.rows / a.w_heads : a.rows;
-  const T* w = a.w ? static_cast<const T*>(a.w) + (long long)hw * a.d : nullptr;
-  Row<T> wk[NV];
+  const int rows = a.rows / a.w_heads;  // of this row of the weight
+  u32x4 wr[NV];
   float dw[NV][V];
+  if (a.w) {
+    load_row<T, PER, NV, false>(wr, static_cast<const T*>(a.w) + (long long)hw * a.d, lane, nvec, true);
+  } else {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int vec = i * PER + lane;
-    wk[i] = unpack<T>(w && vec < nvec ? ld16(w + vec * V) : u32x4{0u, 0u, 0u, 0u});
-    if (!w) {
+    for (int i = 0; i < NV; ++i) wr[i] = sizeof(T) == 2 ? u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}
+                                                       : u32x4{0x3f800000u, 0x3f800000u, 0x3f800000u, 0x3f800000u};  // ones
+  }
 #pragma unroll
-      for (int c = 0; c < V; ++c) wk[i].v[c] = 1.f;
-    }
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int c = 0; c < V; ++c) dw[i][c] = 0.f;
-  }
-  for (long long base = (long long)part * (GROUPS * NR); base < rows; base += (long long)a.nparts * (GROUPS * NR)) {
-    u32x4 sr[NR][NV], yr[NR][NV], gr[NR][NV], dr[NR][NV];
-    long long xo[NR], go[NR];
-    bool have[NR];
+  for (long long base = (long long)part * GROUPS; base < rows; base += (long long)a.nparts * GROUPS) {
+    const long long row = base + group;
+    const bool have = row < rows;
+    const Place p(have ? (int)row : 0, a.n1, a.n2);
+    const T* s_p = static_cast<const T*>(a.x) + hw * a.hx + p.at(a.xs);
+    const T* y_p = static_cast<const T*>(a.dy) + hw * a.hdy + p.at(a.dys);
+    const T* g_p = GATE ? static_cast<const T*>(a.gate) + hw * a.hg + p.at(a.gs) : nullptr;
+    const T* d_p = a.ds ? static_cast<const T*>(a.ds) + hw * a.hds + p.at(a.dss) : nullptr;
+    u32x4 sr[NV], yr[NV], gr[NV], dr[NV];
+    load_row<T, PER, NV, !AGAIN>(sr, s_p, lane, nvec, have);
+    load_row<T, PER, NV, !AGAIN>(yr, y_p, lane, nvec, have);
+    if constexpr (GATE) load_row<T, PER, NV, !AGAIN>(gr, g_p, lane, nvec, have);
+    if constexpr (!AGAIN) load_row<T, PER, NV, !AGAIN>(dr, d_p, lane, nvec, have && a.ds);
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NR; ++j) {
-      const long long row = base + j * GROUPS + group;
-      have[j] = row < rows;
-      Place p(have[j] ? (int)row : 0, a.w_heads > 1 ? 1 : a.n1, a.n2);
-      if (a.w_heads > 1) p.i[1] = hw;
-      const T* s = static_cast<const T*>(a.x) + p.at(a.xs);
-      const T* dy = static_cast<const T*>(a.dy) + p.at(a.dys);
-      const T* g = a.gate ? static_cast<const T*>(a.gate) + p.at(a.gs) : nullptr;
-      const T* ds = a.ds ? static_cast<const T*>(a.ds) + p.at(a.dss) : nullptr;
-      xo[j] = p.at(a.dxs);
-      go[j] = p.at(a.dgs);
+    for (int i = 0; i < NV; ++i) {
+      const Row<T> s = unpack<T>(sr[i]), dy = unpack<T>(yr[i]), w = unpack<T>(wr[i]);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int vec = i * PER + lane;
-        const bool on = have[j] && vec < nvec;
-        sr[j][i] = yr[j][i] = gr[j][i] = dr[j][i] = u32x4{0u, 0u, 0u, 0u};
-        if (on) sr[j][i] = ld16(s + vec * V);
-        if (on) yr[j][i] = ld16(dy + vec * V);
-        if (on && g) gr[j][i] = ld16(g + vec * V);
-        if (on && ds) dr[j][i] = ld16(ds + vec * V);
+      for (int c = 0; c < V; ++c) {
+        float dn = dy.v[c] * w.v[c];
+        if constexpr (GATE) dn *= Gate<T>(unpack<T>(gr[i]).v[c], a.silu).g;
+        sum[0] = fmaf(s.v[c], s.v[c], sum[0]);
+        sum[1] = fmaf(dn, s.v[c], sum[1]);
       }
     }
-    float sum[2 * NR];
-#pragma unroll
-    for (int j = 0; j < NR; ++j) {
-      sum[2 * j] = sum[2 * j + 1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const Row<T> s = unpack<T>(sr[j][i]), dy = unpack<T>(yr[j][i]), z = unpack<T>(gr[j][i]);
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-          const float dn = dy.v[c] * wk[i].v[c] * (a.gate ? gate_of<T>(z.v[c], a.silu) : 1.f);
-          sum[2 * j] = fmaf(s.v[c], s.v[c], sum[2 * j]);
-          sum[2 * j + 1] = fmaf(dn, s.v[c], sum[2 * j + 1]);
-        }
-      }
+    row_reduce<LANES, WAVES, 2>(sum, red);
+    const float r = have ? 1.f / sqrtf(sum[0] * a.inv_d + a.eps) : 0.f;
+    const float back = r * (r * (r * (sum[1] * a.inv_d)));
+    if constexpr (AGAIN) {
+      asm volatile("" ::: "memory");
+      load_row<T, PER, NV, true>(sr, s_p, lane, nvec, have);
+      load_row<T, PER, NV, true>(yr, y_p, lane, nvec, have);
+      if constexpr (GATE) load_row<T, PER, NV, true>(gr, g_p, lane, nvec, have);
+      load_row<T, PER, NV, true>(dr, d_p, lane, nvec, have && a.ds);
+    } else {
+      forget(sr);
+      forget(yr);
+      if constexpr (GATE && NV > 1) forget(gr);  // (a single vector's gates are kept)
     }
-    row_reduce<LANES, WAVES, 2 * NR>(sum, red);
+    forget(wr);
+    T* dx_p = static_cast<T*>(a.dx) + hw * a.hdx + p.at(a.dxs);
+    T* dz_p = GATE ? static_cast<T*>(a.dgate) + hw * a.hdg + p.at(a.dgs) : nullptr;
 #pragma unroll
-    for (int j = 0; j < NR; ++j) {
-      const float r = have[j] ? 1.f / sqrtf(sum[2 * j] * a.inv_d + a.eps) : 0.f;
-      const float back = r * (r * (r * (sum[2 * j + 1] * a.inv_d)));
+    for (int i = 0; i < NV; ++i) {
+      const int vec = i * PER + lane;
+      const Row<T> s = unpack<T>(sr[i]), dy = unpack<T>(yr[i]), w = unpack<T>(wr[i]);
+      Row<T> dx = unpack<T>(dr[i]), dz;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int vec = i * PER + lane;
-        const Row<T> s = unpack<T>(sr[j][i]), dy = unpack<T>(yr[j][i]), z = unpack<T>(gr[j][i]);
-        Row<T> dx = unpack<T>(dr[j][i]), dz;
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-          float g = 1.f, dg = 0.f;
-          if (a.gate) gate_grad<T>(z.v[c], a.silu, g, dg);
-          const float n = s.v[c] * r, yn = dy.v[c] * n;
-          dx.v[c] += r * (dy.v[c] * wk[i].v[c] * g) - s.v[c] * back;
-          dz.v[c] = yn * wk[i].v[c] * dg;
-          dw[i][c] = fmaf(yn, g, dw[i][c]);
+      for (int c = 0; c < V; ++c) {
+        const float n = s.v[c] * r, yn = dy.v[c] * n;
+        if constexpr (GATE) {
+          const Gate<T> f(unpack<T>(gr[i]).v[c], a.silu);
+          dx.v[c] += r * (dy.v[c] * w.v[c] * f.g) - s.v[c] * back;
+          dz.v[c] = yn * w.v[c] * f.dg;
+          dw[i][c] = fmaf(yn, f.g, dw[i][c]);
+        } else {
+          dx.v[c] += r * (dy.v[c] * w.v[c]) - s.v[c] * back;
+          dw[i][c] += yn;
         }
-        if (!have[j] || vec >= nvec) continue;
-        st16(static_cast<T*>(a.dx) + xo[j] + vec * V, pack<T>(dx));
-        if (a.dgate) st16(static_cast<T*>(a.dgate) + go[j] + vec * V, pack<T>(dz));
       }
+      if (!have || vec >= nvec) continue;
+      store_by(dx_p + vec * V, pack<T>(dx), a.lines);
+      if constexpr (GATE) store_by(dz_p + vec * V, pack<T>(dz), a.lines);
     }
   }
   if (!a.dw) return;
@@ -392,29 +416,34 @@ __global__ __launch_bounds__(1024) void kda_norm_dw_kernel(const float* ws, T* d
   }
 }
 
-// Joins neighbouring dimensions whose rows lie evenly in every tensor (and drops those of size 1), so that
-// a row's place takes few divisions and single tokens of many sequences fill whole blocks.
-void join_dims(NormArgs& a, int B, int H, int T) {
-  constexpr int N = 7;
-  Str3* const all[N] = {&a.xs, &a.rs, &a.gs, &a.ys, &a.ss, &a.ws, &a.cs};
+// Puts the dimensions in the order of the output (the first of `all`) in memory, joins neighbouring ones whose rows
+// lie evenly in every tensor, and drops those of size 1: blocks then walk memory in order (heads of a token-major
+// tensor 193 -> 161 us), a row's place takes few divisions, and single tokens of many sequences fill whole blocks.
+template <int N>
+void join_dims(NormArgs& a, Str3* const (&all)[N], int B, int H, int T) {
   struct Dim {
     long long n = 1, st[N] = {};
-  } dims[3];
+  } in[3], out[3];
   int k = 0;
   for (int i = 0; i < 3; ++i) {
     Dim d;
     d.n = i == 0 ? B : (i == 1 ? H : T);
     if (d.n == 1) continue;
-    bool even = k > 0;
-    for (int j = 0; j < N; ++j) {
-      d.st[j] = i == 0 ? all[j]->b : (i == 1 ? all[j]->h : all[j]->t);
-      even = even && dims[k - 1].st[j] == d.n * d.st[j];
-    }
-    if (even) d.n *= dims[--k].n;
-    dims[k++] = d;
+    for (int j = 0; j < N; ++j) d.st[j] = i == 0 ? all[j]->b : (i == 1 ? all[j]->h : all[j]->t);
+    int at = k++;
+    for (; at > 0 && in[at - 1].st[0] < d.st[0]; --at) in[at] = in[at - 1];
+    in[at] = d;
+  }
+  int m = 0;
+  for (int i = 0; i < k; ++i) {
+    Dim d = in[i];
+    bool even = m > 0;
+    for (int j = 0; j < N; ++j) even = even && out[m - 1].st[j] == d.n * d.st[j];
+    if (even) d.n *= out[--m].n;
+    out[m++] = d;
   }
   const Dim none;
-  const Dim &d0 = k > 2 ? dims[0] : none, &d1 = k > 1 ? dims[k - 2] : none, &d2 = k > 0 ? dims[k - 1] : none;
+  const Dim &d0 = m > 2 ? out[0] : none, &d1 = m > 1 ? out[m - 2] : none, &d2 = m > 0 ? out[m - 1] : none;
   for (int j = 0; j < N; ++j) *all[j] = Str3{d0.st[j], d1.st[j], d2.st[j]};
   a.n1 = (int)d1.n;
   a.n2 = (int)d2.n;
@@ -424,8 +453,9 @@ void join_dims(NormArgs& a, int B, int H, int T) {
 // integral constants.  Rows of up to 64 vectors stay inside a wave, and a lane reads from four of
 // them at once so that its loads cover the latency; longer ones give a lane up to 8 vectors.
 template <int N> struct Int { static constexpr int value = N; };
-template <typename F>
-auto with_shape(int nvec, F f) {
+template <typename T, typename F>
+auto with_shape(int d, F f) {
+  const int nvec = d / kVec<T>;
   if (nvec <= 8) return f(Int<8>(), Int<1>(), Int<1>(), Int<4>());
   if (nvec <= 16) return f(Int<16>(), Int<1>(), Int<1>(), Int<4>());
   if (nvec <= 32) return f(Int<32>(), Int<1>(), Int<1>(), Int<4>());
@@ -435,13 +465,13 @@ auto with_shape(int nvec, F f) {
   if (nvec <= 512) return f(Int<64>(), Int<4>(), Int<2>(), Int<1>());
   if (nvec <= 1024) return f(Int<64>(), Int<4>(), Int<4>(), Int<1>());
   if (nvec <= 2048) return f(Int<64>(), Int<16>(), Int<2>(), Int<1>());
-  if (nvec <= 4096) return f(Int<64>(), Int<16>(), Int<4>(), Int<1>());
-  return f(Int<64>(), Int<16>(), Int<8>(), Int<1>());
+  if (sizeof(T) == 2 || nvec <= 4096) return f(Int<64>(), Int<16>(), Int<4>(), Int<1>());
+  return f(Int<64>(), Int<16>(), Int<sizeof(T) == 2 ? 4 : 8>(), Int<1>());
 }
 
 template <typename T, bool BITS8>
 hipError_t norm_fwd(const NormArgs& a, hipStream_t stream) {
-  return with_shape(a.d / kVec<T>, [&](auto l, auto w, auto nv, auto nr) {
+  return with_shape<T>(a.d, [&](auto l, auto w, auto nv, auto nr) {
     constexpr int LANES = decltype(l)::value, WAVES = decltype(w)::value, NV = decltype(nv)::value, NR = decltype(nr)::value;
     constexpr int THREADS = WAVES > 4 ? 64 * WAVES : 256, per = THREADS / (LANES * WAVES) * NR;
     hipLaunchKernelGGL((kda_norm_kernel<T, LANES, WAVES, NV, NR, BITS8>), dim3((unsigned)((a.rows + per - 1) / per)),
@@ -450,13 +480,31 @@ hipError_t norm_fwd(const NormArgs& a, hipStream_t stream) {
   });
 }
 
+// The gradients' shapes: one row per group of lanes, fewer vectors per lane.
+template <typename T, typename F>
+auto with_bwd_shape(int d, F f) {
+  const int nvec = d / kVec<T>;
+  if (nvec <= 8) return f(Int<8>(), Int<1>(), Int<1>());
+  if (nvec <= 16) return f(Int<16>(), Int<1>(), Int<1>());
+  if (nvec <= 32) return f(Int<32>(), Int<1>(), Int<1>());
+  if (nvec <= 64) return f(Int<64>(), Int<1>(), Int<1>());
+  if (nvec <= 128) return f(Int<64>(), Int<1>(), Int<2>());
+  if (nvec <= 256) return f(Int<64>(), Int<4>(), Int<1>());
+  if (nvec <= 512) return f(Int<64>(), Int<4>(), Int<2>());
+  if (nvec <= 1024) return f(Int<64>(), Int<8>(), Int<2>());
+  if (nvec <= 2048) return f(Int<64>(), Int<16>(), Int<2>());
+  if (sizeof(T) == 2 || nvec <= 4096) return f(Int<64>(), Int<16>(), Int<4>());
+  return f(Int<64>(), Int<16>(), Int<sizeof(T) == 2 ? 4 : 8>());
+}
+
 template <typename T>
 hipError_t norm_bwd(const NormArgs& a, hipStream_t stream) {
-  const hipError_t e = with_shape(a.d / kVec<T>, [&](auto l, auto w, auto nv, auto nr) {
-    constexpr int LANES = decltype(l)::value, WAVES = decltype(w)::value, NV = decltype(nv)::value, NR = decltype(nr)::value;
-    constexpr int THREADS = WAVES > 4 ? 64 * WAVES : 256, R = NR > 2 ? 2 : NR;
-    hipLaunchKernelGGL((kda_norm_bwd_kernel<T, LANES, WAVES, NV, R>), dim3((unsigned)(a.nparts * a.w_heads)),
-                       dim3(THREADS), 0, stream, a);
+  const hipError_t e = with_bwd_shape<T>(a.d, [&](auto l, auto w, auto nv) {
+    constexpr int LANES = decltype(l)::value, WAVES = decltype(w)::value, NV = decltype(nv)::value;
+    constexpr int THREADS = WAVES > 4 ? 64 * WAVES : 256;
+    const dim3 grid((unsigned)(a.nparts * a.w_heads));
+    if (a.gate) hipLaunchKernelGGL((kda_norm_bwd_kernel<T, LANES, WAVES, NV, true, (NV > 2)>), grid, dim3(THREADS), 0, stream, a);
+    else hipLaunchKernelGGL((kda_norm_bwd_kernel<T, LANES, WAVES, NV, false, (NV > 2)>), grid, dim3(THREADS), 0, stream, a);
     return hipGetLastError();
   });
   if (e != hipSuccess || !a.dw) return e;
@@ -468,27 +516,44 @@ hipError_t norm_bwd(const NormArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Blocks per weight row: four a compute unit (one of 1024 threads), no more than there are units of rows.
+// Blocks per weight row: three of 256 threads a compute unit, two of 512 or one of 1024 (32K rows of 4096 bf16 values,
+// blocks of 256: 261, 179, 182, 196 us with one to four; heads of 128 with a gate 449, 289, 274, 267), no more than there
+// are units of rows.
 int norm_parts(int rows, int d, int w_heads, bool bf16_io, int cus) {
-  const int nvec = d / (bf16_io ? 8 : 4);
-  return with_shape(nvec, [&](auto l, auto w, auto, auto nr) {
-    constexpr int LANES = decltype(l)::value, WAVES = decltype(w)::value, R = decltype(nr)::value > 2 ? 2 : decltype(nr)::value;
-    constexpr int THREADS = WAVES > 4 ? 64 * WAVES : 256, per = THREADS / (LANES * WAVES) * R;
+  const auto parts = [&](auto l, auto w, auto) {
+    constexpr int LANES = decltype(l)::value, WAVES = decltype(w)::value;
+    constexpr int THREADS = WAVES > 4 ? 64 * WAVES : 256, per = THREADS / (LANES * WAVES);
     const int own = rows / w_heads;
-    int most = (WAVES > 4 ? 1 : 4) * cus / w_heads;
+    int most = (THREADS > 512 ? 1 : (THREADS > 256 ? 2 : 3)) * cus / w_heads;
     most = most < 1 ? 1 : most;
     const int units = (own + per - 1) / per;
     return units < most ? (units < 1 ? 1 : units) : most;
-  });
+  };
+  return bf16_io ? with_bwd_shape<bf16>(d, parts) : with_bwd_shape<float>(d, parts);
 }
 
 hipError_t launch_norm(NormArgs a, int B, int H, int T, bool bits8, bool bf16_io, hipStream_t stream) {
-  join_dims(a, B, H, T);
+  const long long es = bf16_io ? 2 : 4;
+  // (8-bit rows go through the caches in any case: 143 us against 154 for 32K rows of 4096)
+  a.lines = (bits8 || whole_lines(a.y, a.ys, a.rows, a.d * es, es)) && (!a.s || whole_lines(a.s, a.ss, a.rows, a.d * es, es));
+  Str3* const all[] = {&a.ys, &a.xs, &a.rs, &a.gs, &a.ss, &a.ws, &a.cs};
+  join_dims(a, all, B, H, T);
   if (bits8) return bf16_io ? norm_fwd<bf16, true>(a, stream) : norm_fwd<float, true>(a, stream);
   return bf16_io ? norm_fwd<bf16, false>(a, stream) : norm_fwd<float, false>(a, stream);
 }
 
-hipError_t launch_norm_backward(const NormArgs& a, bool bf16_io, hipStream_t stream) {
+hipError_t launch_norm_backward(NormArgs a, int B, int H, int T, bool bf16_io, hipStream_t stream) {
+  const long long es = bf16_io ? 2 : 4;
+  // (rows of a wave or less; longer ones are slower that way: 173 us against 182 for 32K rows of 4096)
+  a.lines = a.d * es <= 1024 && whole_lines(a.dx, a.dxs, a.rows, a.d * es, es) &&
+            (!a.dgate || whole_lines(a.dgate, a.dgs, a.rows, a.d * es, es));
+  Str3* const all[] = {&a.dxs, &a.xs, &a.gs, &a.dys, &a.dss, &a.dgs};
+  if (a.w_heads > 1) {  // a block stays with one head
+    a.hx = a.xs.h; a.hg = a.gs.h; a.hdy = a.dys.h; a.hds = a.dss.h; a.hdx = a.dxs.h; a.hdg = a.dgs.h;
+    H = 1;
+    for (Str3* s : all) s->h = 0;
+  }
+  join_dims(a, all, B, H, T);
   return bf16_io ? norm_bwd<bf16>(a, stream) : norm_bwd<float>(a, stream);
 }
 

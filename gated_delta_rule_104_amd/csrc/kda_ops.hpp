@@ -93,6 +93,14 @@ hipError_t check_ssm_gates(const void* la, Str3 ls, const void* beta, Str3 bs, c
                            hipStream_t stream, unsigned int* bits_out);
 
 
+// Whether an output of n rows of `bytes` bytes is written past the caches: rows that are whole 128-byte lines (parts
+// of lines are joined in the caches only: a norm's rows of 2000 bytes 84 us against 112) of an output that they would
+// not keep until it is read (32 MiB of L2).
+inline bool whole_lines(const void* p, Str3 s, long long rows, long long bytes, long long elem) {
+  return rows * bytes >= (32LL << 20) && bytes % 128 == 0 && reinterpret_cast<uintptr_t>(p) % 128 == 0 &&
+         s.b * elem % 128 == 0 && s.h * elem % 128 == 0 && s.t * elem % 128 == 0;
+}
+
 // ------------------------------------------------ gated linear recurrence
 struct GlrArgs {
   const void* x;     // [B, H, T, d]
@@ -114,6 +122,7 @@ struct GlrArgs {
   float* dh0 = nullptr;
   Str3 dos, dxs, dls, dbs;
   void* ws = nullptr;
+  bool lines = false;  // outputs are written past the caches (set by the launch)
 };
 size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients);
 // polls: how often a run of tokens looks for the state in front of it before it walks the sequence itself
@@ -146,10 +155,13 @@ struct NormArgs {
   Str3 dys, dss, dxs, dgs;
   float* scratch = nullptr;
   int nparts = 0;
+  // set by the launches
+  bool lines = false;                                 // outputs are written past the caches
+  long long hx = 0, hg = 0, hdy = 0, hds = 0, hdx = 0, hdg = 0;  // backward: from one row of the weight to the next
 };
 int norm_parts(int rows, int d, int w_heads, bool bf16_io, int cus);
 hipError_t launch_norm(NormArgs a, int B, int H, int T, bool bits8, bool bf16_io, hipStream_t stream);
-hipError_t launch_norm_backward(const NormArgs& a, bool bf16_io, hipStream_t stream);
+hipError_t launch_norm_backward(NormArgs a, int B, int H, int T, bool bf16_io, hipStream_t stream);
 
 // ----------------------------------------------------------------- drafts
 struct VerifyArgs {
@@ -162,7 +174,7 @@ struct VerifyArgs {
   int* out;            // [N, K + 1]
   long long pn, pt, qn, qt;  // elements between sequences and tokens
   int N, K, V;
-  double* ws;
+  void* ws;
 };
 size_t verify_ws_bytes(int N, int V);
 hipError_t launch_verify(const VerifyArgs& a, bool bf16_io, hipStream_t stream);

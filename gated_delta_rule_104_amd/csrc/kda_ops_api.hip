@@ -640,11 +640,11 @@ kda_status kda_rms_norm_backward(const void* x, const void* gate, const void* we
   a.x = x; a.gate = gate; a.w = weight; a.dy = dy; a.ds = dresidual_out; a.dx = dx;
   a.dgate = gate ? dgate : nullptr;
   a.dw = weight ? dweight : nullptr;
-  a.rows = B * H * T; a.d = d; a.n1 = H; a.n2 = T; a.w_heads = heads; a.eps = eps; a.inv_d = 1.f / (float)d;
+  a.rows = B * H * T; a.d = d; a.w_heads = heads; a.eps = eps; a.inv_d = 1.f / (float)d;
   a.silu = gate_activation == KDA_GATE_SILU;
   a.scratch = static_cast<float*>(workspace);
   a.nparts = kda::norm_parts(a.rows, d, heads, dtype == KDA_BF16, kda::api_cu_count());
-  const hipError_t e = kda::launch_norm_backward(a, dtype == KDA_BF16, stream);
+  const hipError_t e = kda::launch_norm_backward(a, B, H, T, dtype == KDA_BF16, stream);
   return e == hipSuccess ? api_ok() : hip_fail(e, "kda_rms_norm_backward launch");
 }
 
@@ -705,7 +705,7 @@ kda_status kda_draft_verify(const void* target, const kda_strides* target_stride
   OPS_TRY(need_workspace(workspace, workspace_bytes, kda_draft_verify_workspace_bytes(N, K, V, dtype)));
   a.p = target; a.q = draft; a.tokens = tokens; a.u = uniforms; a.counts = counts; a.accepted = accepted; a.out = out;
   a.N = N; a.K = K; a.V = V;
-  a.ws = static_cast<double*>(workspace);
+  a.ws = workspace;
   const hipError_t e = kda::launch_verify(a, dtype == KDA_BF16, stream);
   return e == hipSuccess ? api_ok() : hip_fail(e, "kda_draft_verify launch");
 }

@@ -46,6 +46,29 @@ __device__ __forceinline__ void st16(T* p, u32x4 w) {
   *reinterpret_cast<u32x4*>(p) = w;
 }
 
+// The same for values that nothing reads again soon: they pass the caches without pushing out others.
+template <typename T>
+__device__ __forceinline__ u32x4 ld_once(const T* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+template <typename V>
+__device__ __forceinline__ void st_once(void* p, V w) {
+  __builtin_nontemporal_store(w, static_cast<V*>(p));
+}
+
+// Either, by a choice that is the same for all lanes.  (Two stores to one place in two branches would be joined to
+// one plain store; the empty statements keep them apart.)
+template <typename V>
+__device__ __forceinline__ void store_by(void* p, V w, bool once) {
+  if (once) {
+    asm volatile("");
+    st_once(p, w);
+    asm volatile("");
+  } else {
+    *static_cast<V*>(p) = w;
+  }
+}
+
 __device__ __forceinline__ int seq_len(const int* lens, int b, int T) {
   if (!lens) return T;
   const int n = lens[b];
