@@ -865,15 +865,50 @@ def state_load(cache, scales, slots, S=None) -> torch.Tensor:
 
 
 # ------------------------------------------------ gated linear recurrence
-def _glr_args(x, log_alpha, beta, h0, name="h0"):
-    B, H, T, d = x.shape if x.dim() == 4 else (*x.shape[:2], 1, x.shape[2])
-    dt, dev = x.dtype, _device(x, "x")
-    st = _GlrStrides(x=_view(x, "x", dt, x.shape, dev), log_alpha=_view(log_alpha, "log_alpha", dt, x.shape, dev))
+def _fits(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: torch.device) -> None:
+    """_view's checks without its strides."""
+    if t.device != dev or t.dtype != dtype or t.shape != shape:
+        _wrong(t, name, dtype, shape, dev)
+        raise KdaError(f"{name} does not fit")
+
+
+def _plain(*tensors) -> bool:
+    """Whether all are contiguous, as the library takes them without strides."""
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            return False
+    return True
+
+
+def _rows(t: Optional[torch.Tensor], name: str) -> _Strides:
+    """The strides of a tensor that has been checked but for its rows."""
+    if t is None:
+        return _Strides()
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise KdaError(f"{name} must have contiguous rows")
+    return _Strides(*st[:3])
+
+
+def _glr_args(x, log_alpha, beta, h0, o, lens, name="h0"):
+    """Checks what the recurrence's calls share; o may be missing."""
+    shape, dt, dev = x.shape, x.dtype, _device(x, "x")
+    _fits(log_alpha, "log_alpha", dt, shape, dev)
     if beta is not None:
-        st.beta = _view(beta, "beta", dt, x.shape, dev)
+        _fits(beta, "beta", dt, shape, dev)
+    if o is not None:
+        _fits(o, "o", dt, shape, dev)
     if h0 is not None:
-        _dense(h0, name, torch.float32, (B, H, d), dev)
-    return (B, H, T, d), st, dev
+        _dense(h0, name, torch.float32, (shape[0], shape[1], shape[-1]), dev)
+    if lens is not None:
+        _dense(lens, "lens", torch.int32, (shape[0],), dev)
+    return dev
+
+
+def _glr_strides(x, log_alpha, beta, o) -> Optional[_GlrStrides]:
+    if _plain(x, log_alpha, beta, o):
+        return None
+    return _GlrStrides(_rows(x, "x"), _rows(log_alpha, "log_alpha"), _rows(beta, "beta"), _rows(o, "o"))
 
 
 def glr_prefill(x, log_alpha, beta=None, h0=None, normalise=False, lens=None, o=None, h_T=None, workspace=None):
@@ -884,12 +919,11 @@ def glr_prefill(x, log_alpha, beta=None, h0=None, normalise=False, lens=None, o=
     order unless given, rows behind lens not written), and h_T fp32."""
     _rank(x, "x", 4)
     dt = _dtype(x)
-    (B, H, T, d), st, dev = _glr_args(x, log_alpha, beta, h0)
-    if lens is not None:
-        _dense(lens, "lens", torch.int32, (B,), dev)
+    dev = _glr_args(x, log_alpha, beta, h0, o, lens)
+    B, H, T, d = x.shape
     if o is None:
         o = _new_like(x)
-    st.o = _view(o, "o", x.dtype, (B, H, T, d), dev)
+    st = _glr_strides(x, log_alpha, beta, o)
     if h_T is None:
         h_T = torch.empty(B, H, d, dtype=torch.float32, device=x.device)
     _dense(h_T, "h_T", torch.float32, (B, H, d), dev)
@@ -909,10 +943,11 @@ def glr_step(x, log_alpha, h, beta=None, normalise=False, o=None) -> torch.Tenso
     dt = _dtype(x)
     if h is None:
         raise KdaError("h is required")
-    (N, H, _, d), st, dev = _glr_args(x, log_alpha, beta, h, "h")
+    dev = _glr_args(x, log_alpha, beta, h, o, None, "h")
+    N, H, d = x.shape
     if o is None:
         o = torch.empty(N, H, d, dtype=x.dtype, device=dev)
-    st.o = _view(o, "o", x.dtype, (N, H, d), dev)
+    st = _glr_strides(x, log_alpha, beta, o)
     rc = load().kda_glr_step(_ptr(x), _ptr(log_alpha), _ptr(beta), _ptr(h), _ptr(o), st, N, H, d, int(bool(normalise)),
                              dt, _stream())
     _check(rc, "kda_glr_step")
@@ -925,17 +960,18 @@ def glr_backward(x, log_alpha, beta, h0, o, dO, dh_T=None, normalise=False, lens
     gradients of padding are zero."""
     _rank(x, "x", 4)
     dt = _dtype(x)
-    (B, H, T, d), st, dev = _glr_args(x, log_alpha, beta, h0)
-    st.o = _view(o, "o", x.dtype, (B, H, T, d), dev)
-    if lens is not None:
-        _dense(lens, "lens", torch.int32, (B,), dev)
+    dev = _glr_args(x, log_alpha, beta, h0, o, lens)
+    B, H, T, d = x.shape
+    _fits(dO, "dO", x.dtype, x.shape, dev)
     if dh_T is not None:
         _dense(dh_T, "dh_T", torch.float32, (B, H, d), dev)
     out = dict(dx=_new_like(x), dlog_alpha=_new_like(log_alpha))
     if beta is not None:
         out["dbeta"] = _new_like(beta)
-    gst = _GlrGradStrides(dO=_view(dO, "dO", x.dtype, (B, H, T, d), dev),
-                          **{n: _Strides(*t.stride()[:3]) for n, t in out.items()})
+    st = _glr_strides(x, log_alpha, beta, o)
+    gst = None
+    if not _plain(dO, *out.values()):
+        gst = _GlrGradStrides(dO=_rows(dO, "dO"), **{n: _rows(t, n) for n, t in out.items()})
     if h0 is not None:
         out["dh0"] = _new_like(h0)
     lib = load()
@@ -955,32 +991,34 @@ def _gate_act(activation) -> int:
     return _GATE[activation]
 
 
-def _norm_args(x, weight, gate):
-    """x as [B,H,T,d] (leading dimensions of 1 for fewer), the weight's rows per head or not."""
+def _norm_args(x, weight, **others):
+    """Checks x [B,H,T,d], the weight and tensors of x's kind; whether the weight has a row per head."""
     _rank(x, "x", 4)
-    dev = _device(x, "x")
-    H, d = x.shape[1], x.shape[3]
+    shape, dev = x.shape, _device(x, "x")
     per_head = weight is not None and weight.dim() == 2
     if weight is not None:
-        _dense(weight, "weight", x.dtype, (H, d) if per_head else (d,), dev)
-    return x.shape, per_head, dev
+        _dense(weight, "weight", x.dtype, (shape[1], shape[3]) if per_head else (shape[3],), dev)
+    for name, t in others.items():
+        if t is not None:
+            _fits(t, name, x.dtype, shape, dev)
+    return per_head, dev
 
 
 def _norm(x, weight, residual, gate, gate_activation, eps, output, y, scales, residual_out):
     dt = _dtype(x)
-    (B, H, T, d), per_head, dev = _norm_args(x, weight, gate)
-    st = _NormStrides(x=_view(x, "x", x.dtype, x.shape, dev), y=_view(y, "y", y.dtype, x.shape, dev))
-    if residual is not None:
-        st.residual = _view(residual, "residual", x.dtype, x.shape, dev)
-        if residual_out is None:
-            residual_out = _new_like(residual)
-        st.residual_out = _view(residual_out, "residual_out", x.dtype, x.shape, dev)
-    elif residual_out is not None:
-        raise KdaError("residual_out without a residual")
-    if gate is not None:
-        st.gate = _view(gate, "gate", x.dtype, x.shape, dev)
-    if scales is not None:
-        st.scales = _Strides(*scales.stride()[:3])
+    per_head, dev = _norm_args(x, weight, residual=residual, gate=gate, residual_out=residual_out)
+    if residual is None:
+        if residual_out is not None:
+            raise KdaError("residual_out without a residual")
+    elif residual_out is None:
+        residual_out = _new_like(residual)
+    st = None
+    if not _plain(x, residual, gate, y, residual_out, scales):
+        st = _NormStrides(_rows(x, "x"), _rows(residual, "residual"), _rows(gate, "gate"), _rows(y, "y"),
+                          _rows(residual_out, "residual_out"))
+        if scales is not None:
+            st.scales = _Strides(*scales.stride()[:3])
+    B, H, T, d = x.shape
     rc = load().kda_rms_norm(_ptr(x), _ptr(residual), _ptr(gate), _ptr(weight), _ptr(y), _ptr(scales),
                              _ptr(residual_out), st, B, H, T, d, int(per_head), eps, _gate_act(gate_activation), output,
                              dt, _stream())
@@ -995,6 +1033,8 @@ def rms_norm(x, weight, residual=None, gate=None, gate_activation="sigmoid", eps
     residual (y, residual_out); residual_out may be residual itself."""
     if y is None:
         y = _new_like(x)
+    else:
+        _fits(y, "y", x.dtype, x.shape, x.device)
     s = _norm(x, weight, residual, gate, gate_activation, eps, 0, y, None, residual_out)
     return y if s is None else (y, s)
 
@@ -1025,16 +1065,15 @@ def rms_norm_backward(x, weight, dy, dresidual_out=None, gate=None, gate_activat
     Returns a dict: dx (the gradient of x and of the residual alike), dweight where a weight and dgate
     where a gate was given."""
     dt = _dtype(x)
-    (B, H, T, d), per_head, dev = _norm_args(x, weight, gate)
+    per_head, dev = _norm_args(x, weight, dy=dy, dresidual_out=dresidual_out, gate=gate)
+    B, H, T, d = x.shape
     out = dict(dx=_new_like(x))
-    st = _NormGradStrides(x=_view(x, "x", x.dtype, x.shape, dev), dy=_view(dy, "dy", x.dtype, x.shape, dev),
-                          dx=_Strides(*out["dx"].stride()[:3]))
-    if dresidual_out is not None:
-        st.dresidual_out = _view(dresidual_out, "dresidual_out", x.dtype, x.shape, dev)
     if gate is not None:
-        st.gate = _view(gate, "gate", x.dtype, x.shape, dev)
         out["dgate"] = _new_like(gate)
-        st.dgate = _Strides(*out["dgate"].stride()[:3])
+    st = None
+    if not _plain(x, gate, dy, dresidual_out, *out.values()):
+        st = _NormGradStrides(_rows(x, "x"), _rows(gate, "gate"), _rows(dy, "dy"), _rows(dresidual_out, "dresidual_out"),
+                              _rows(out["dx"], "dx"), _rows(out.get("dgate"), "dgate"))
     lib = load()
     need = 0
     if weight is not None:
