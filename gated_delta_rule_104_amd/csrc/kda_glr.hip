@@ -49,15 +49,80 @@ __device__ __forceinline__ A advance(float e, A h, A b) {
   else return fma(old, (double)e, b) + keep;
 }
 
-// n = sqrt(1 - a^2) = sqrt((1 - a)(1 + a)).
-__device__ __forceinline__ float unit_of(float e) {
-  const float d = slow(e) ? -e : 1.f - e, s = slow(e) ? 2.f + e : 1.f + e;
-  return __builtin_amdgcn_sqrtf(d * s);
-}
-
 // The state between tokens: fp32 inputs carry it in 64 bits, since its own rounding, 2^-25 a token,
 // would be the largest error of outputs that are stored with 24 bits.
 template <typename T> using State = typename std::conditional<sizeof(T) == 2, float, double>::type;
+
+// A single token's decay.  bf16 takes it as a float: inside a lane's few tokens its rounding does not add up, and what
+// passes from one lane's tokens to the next one's takes the decay of the sum of their logs (above).
+template <typename T>
+__device__ __forceinline__ float token_decay(float x) {
+  if constexpr (sizeof(T) == 2) return __builtin_amdgcn_exp2f(1.44269504088896340736f * x);
+  else return decay_of<T>(x);
+}
+template <typename T>
+__device__ __forceinline__ float factor_of(float e) {  // a itself
+  if constexpr (sizeof(T) == 2) return e;
+  else return slow(e) ? 1.f + e : e;
+}
+
+// What a lane keeps of its tokens' log decays until the second walk: bf16 as they are, and takes the exponential
+// again (half the registers), fp32 the decays in their place.
+template <typename T, int NT>
+__device__ __forceinline__ void hold_decays(u32x4 (&r)[NT]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) r[i][c] = __float_as_uint(decay_of<T>(__uint_as_float(r[i][c])));
+  } else {
+    forget(r);
+  }
+}
+template <typename T, int NT>
+__device__ __forceinline__ void add_logs(const u32x4 (&r)[NT], float (&l)[kVec<T>]) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int c = 0; c < kVec<T>; ++c) l[c] += unpack<T>(r[i]).v[c];
+}
+template <typename T>
+__device__ __forceinline__ float held_decay(u32x4 r, int c) {
+  const float x = unpack<T>(r).v[c];
+  return sizeof(T) == 2 ? token_decay<T>(x) : x;
+}
+
+// a h + b for one token.  CAREFUL: a decay of zero clears an infinity or NaN too; bf16 calls look at the last
+// state of a run and walk it again if it has become one (the look costs less than the choice at every token).
+template <typename T, bool CAREFUL>
+__device__ __forceinline__ State<T> walk(float e, State<T> h, State<T> b) {
+  if constexpr (sizeof(T) == 2) return fmaf(CAREFUL && e == 0.f ? 0.f : h, e, b);
+  else return advance<State<T>>(e, h, b);
+}
+template <typename T>
+__device__ __forceinline__ bool all_finite(const State<T> (&h)[kVec<T>]) {
+  if constexpr (sizeof(T) == 4) return true;  // fp32 is always careful
+  float zero = 0.f;
+#pragma unroll
+  for (int c = 0; c < kVec<T>; ++c) zero = fmaf((float)h[c], 0.f, zero);
+  return zero == 0.f;
+}
+
+// n = sqrt(1 - a^2) from x = log a and the token's decay: bf16 from the series of 1 - e^2x above -1/16 (what follows is below
+// y^5 / 720 of it, y = 2x, 2^-24), fp32 as sqrt((1 - a)(1 + a)) with 1 - a in all its digits.
+template <typename T>
+__device__ __forceinline__ float unit_of(float x, float e) {
+  if constexpr (sizeof(T) == 2) {
+    float p = fmaf(x, 2.f / 15, 1.f / 3);
+    p = fmaf(x, p, 2.f / 3);
+    p = fmaf(x, p, 1.f);
+    p = fmaf(x, p, 1.f);
+    return __builtin_amdgcn_sqrtf(fabsf(x) < 0.0625f ? -2.f * x * p : fmaf(-e, e, 1.f));
+  } else {
+    const float d = slow(e) ? -e : 1.f - e;
+    return __builtin_amdgcn_sqrtf(d * (2.f - d));
+  }
+}
 
 template <typename T>
 __device__ __forceinline__ Row<T> ones() {
@@ -170,6 +235,14 @@ __device__ __forceinline__ bool look_back(RelayMem<T, WAVES>& m, const uint32_t*
   return false;
 }
 
+// The state in front of a lane's tokens, once relay has found it.
+template <typename T, int WAVES>
+__device__ __forceinline__ void front_state(const RelayMem<T, WAVES>& m, State<T> (&h)[kVec<T>]) {
+  const int lane = threadIdx.x & 63, sub = (threadIdx.x >> 6) * kSub<T> + lane / kLpr<T>;
+#pragma unroll
+  for (int c = 0; c < kVec<T>; ++c) h[c] = m.z[sub][lane % kLpr<T> * kVec<T> + c];
+}
+
 // From each lane's (l, z) to the state in front of its tokens, h.  s: the tile's number in its chain;
 // self: the state in front of the tile without the others' help; end: where the chain's end state goes
 // (lane = channel), or null.
@@ -229,8 +302,7 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
     run = advance(m.e[w * SUB + r][lane], run, zr);
   }
   wave_lds_fence();
-#pragma unroll
-  for (int c = 0; c < V; ++c) h[c] = m.z[sub][c0 + c];
+  front_state(m, h);
 }
 
 // Which tile a workgroup has.  Tiles are handed out run by run, so that the ones in front of a tile are
@@ -279,8 +351,13 @@ __device__ __forceinline__ void load_rows(u32x4 (&r)[NT], const T* p, long long 
   }
 }
 
+// Waves per SIMD that the registers have to leave room for.
+template <typename T, int NT, bool GRADIENTS, bool BETA>
+constexpr int kResident = GRADIENTS ? (sizeof(T) == 4 || NT == 2 ? 4 : (NT == 3 || !BETA ? 3 : 2))
+                                    : (sizeof(T) == 4 || NT == 6 ? 3 : (NT == 4 ? 4 : 2));
+
 template <typename T, int NT, int WAVES, bool NORM, bool BETA>
-__global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, GlrGrid n, int window, int polls) {
+__global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void kda_glr_kernel(GlrArgs a, GlrGrid n, int window, int polls) {
   constexpr int V = kVec<T>, LPR = kLpr<T>, SUB = kSub<T>, RUN = WAVES * SUB * NT;
   __shared__ RelayMem<T, WAVES> mem;
   const GlrTile g(a, n, RUN);
@@ -305,26 +382,40 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, GlrGrid 
   load_rows<T, NT, 1>(rl, la, a.ls.t, t0, g.len, on, full);
   load_rows<T, NT, 1>(rx, x, a.xs.t, t0, g.len, on, full);
   if constexpr (BETA) load_rows<T, NT, 1>(rb, beta, a.bs.t, t0, g.len, on, full);
-  float e[NT][V], in[NT][V], l[V];
+  float in[NT][V], l[V];
   State<T> h[V], z[V];
 #pragma unroll
-  for (int c = 0; c < V; ++c) {
-    l[c] = 0.f;
-    z[c] = 0;
+  for (int c = 0; c < V; ++c) l[c] = 0.f;
+  if constexpr (sizeof(T) == 4) {
+    add_logs<T>(rl, l);
+    hold_decays<T>(rl);
   }
+#pragma unroll
+  for (int c = 0; c < V; ++c) z[c] = 0;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const Row<T> xv = unpack<T>(rx[i]), lv = unpack<T>(rl[i]), bv = BETA ? unpack<T>(rb[i]) : ones<T>();
+    const Row<T> xv = unpack<T>(rx[i]), bv = BETA ? unpack<T>(rb[i]) : ones<T>();
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      e[i][c] = decay_of<T>(lv.v[c]);
+      const float e = held_decay<T>(rl[i], c);
       float v = BETA ? bv.v[c] * xv.v[c] : xv.v[c];
-      if constexpr (NORM) v *= unit_of(e[i][c]);
+      if constexpr (NORM) v *= unit_of<T>(unpack<T>(rl[i]).v[c], e);
       in[i][c] = v;
-      z[c] = advance<State<T>>(e[i][c], z[c], v);
-      l[c] += lv.v[c];
+      z[c] = walk<T, false>(e, z[c], v);
+      if constexpr (sizeof(T) == 2) l[c] += unpack<T>(rl[i]).v[c];
+    }
+    __builtin_amdgcn_sched_barrier(0);  // (token by token: interleaved, they would hold all decays at once)
+  }
+  if (__builtin_expect(!all_finite<T>(z), 0)) {
+    forget(rl);
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      z[c] = 0;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) z[c] = walk<T, true>(held_decay<T>(rl[i], c), z[c], in[i][c]);
     }
   }
+  if constexpr (sizeof(T) == 2) hold_decays<T>(rl);
   const auto self = [&]() {
     if (cl >= C) return 0.f;
     const int hh = cl / a.d, jj = cl % a.d;
@@ -333,11 +424,11 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, GlrGrid 
     const T* pb = BETA ? static_cast<const T*>(a.beta) + g.b * a.bs.b + hh * a.bs.h + jj : nullptr;
     State<T> run = first;
     for (long long t = 0; t < first_t; ++t) {
-      const float ee = decay_of<T>(to_f32(pl[t * a.ls.t]));
+      const float x1 = to_f32(pl[t * a.ls.t]);
       float v = to_f32(px[t * a.xs.t]);
       if constexpr (BETA) v *= to_f32(pb[t * a.bs.t]);
-      if constexpr (NORM) v *= unit_of(ee);
-      run = advance<State<T>>(ee, run, v);
+      if constexpr (NORM) v *= unit_of<T>(x1, token_decay<T>(x1));
+      run = advance<State<T>>(decay_of<T>(x1), run, v);
     }
     return (float)run;
   };
@@ -345,20 +436,29 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_kernel(GlrArgs a, GlrGrid 
   relay<T, WAVES>(mem, l, z, h, words, (long long)n.nchain * kWords, g.s, g.s == g.ntile - 1, first, window, polls,
                   cl < C ? a.h_T + at : nullptr, self);
   if (!on) return;
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int c = 0; c < V; ++c) asm volatile("" : "+v"(e[i][c]), "+v"(in[i][c]));
+  if constexpr (sizeof(T) == 4) {  // (what was kept in 64 bits)
+    forget(rl);
+    forget(in);
+  }
   T* o = static_cast<T*>(a.o) + g.b * a.os.b + hd * a.os.h + j0;
+  const auto outputs = [&](auto careful) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    Row<T> y;
+    for (int i = 0; i < NT; ++i) {
+      Row<T> y;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      h[c] = advance<State<T>>(e[i][c], h[c], in[i][c]);
-      y.v[c] = (float)h[c];
+      for (int c = 0; c < V; ++c) {
+        h[c] = walk<T, decltype(careful)::value>(held_decay<T>(rl[i], c), h[c], in[i][c]);
+        y.v[c] = (float)h[c];
+      }
+      if (full || t0 + i < g.len) store_by(o + (t0 + i) * a.os.t, pack<T>(y), a.lines);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (full || t0 + i < g.len) store_by(o + (t0 + i) * a.os.t, pack<T>(y), a.lines);
+  };
+  outputs(std::false_type());
+  if (__builtin_expect(!all_finite<T>(h), 0)) {
+    forget(rl);
+    front_state(mem, h);
+    outputs(std::true_type());
   }
 }
 
@@ -393,7 +493,7 @@ __global__ __launch_bounds__(256) void kda_glr_step_kernel(GlrArgs a, int nvec) 
   for (int c = 0; c < V; ++c) {
     const float e = decay_of<T>(lv.v[c]);
     float in = bv.v[c] * xv.v[c];
-    if (a.norm) in *= unit_of(e);
+    if (a.norm) in *= unit_of<T>(lv.v[c], token_decay<T>(lv.v[c]));
     y.v[c] = (float)advance<State<T>>(e, hv[c / 4][c % 4], in);
     hv[c / 4][c % 4] = y.v[c];
   }
@@ -405,7 +505,7 @@ __global__ __launch_bounds__(256) void kda_glr_step_kernel(GlrArgs a, int nvec) 
 // The gradients' chain runs from the last token to the first: mu_t = a_t (dO_t + mu_{t+1}), the same relay
 // with the tiles, and the tokens in them, in reverse.
 template <typename T, int NT, int WAVES, bool NORM, bool BETA>
-__global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, GlrGrid n, int window, int polls) {
+__global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, true, BETA>)) void kda_glr_bwd_kernel(GlrArgs a, GlrGrid n, int window, int polls) {
   constexpr int V = kVec<T>, LPR = kLpr<T>, SUB = kSub<T>, RUN = WAVES * SUB * NT;
   __shared__ RelayMem<T, WAVES> mem;
   const GlrTile g(a, n, RUN);
@@ -447,26 +547,41 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, GlrG
   u32x4 rx[NT], rl[NT], rb[NT], rg[NT], ro[NT];
   load_rows<T, NT, -1>(rl, la, a.ls.t, t0, g.len, on, full);
   load_rows<T, NT, -1>(rg, dO, a.dos.t, t0, g.len, on, full);
-  load_rows<T, NT, -1>(rx, x, a.xs.t, t0, g.len, on, full);
+  if constexpr (NORM || BETA) load_rows<T, NT, -1>(rx, x, a.xs.t, t0, g.len, on, full);
   if constexpr (BETA) load_rows<T, NT, -1>(rb, beta, a.bs.t, t0, g.len, on, full);
   load_rows<T, NT, -1>(ro, o, a.os.t, t0 - 1, g.len, on, full && tile > 0);
-  float e[NT][V], l[V];
+  float l[V];
   State<T> mu[V], z[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) {
     l[c] = 0.f;
     z[c] = 0;
   }
+  if constexpr (sizeof(T) == 4) {
+    add_logs<T>(rl, l);
+    hold_decays<T>(rl);
+  }
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const Row<T> lv = unpack<T>(rl[i]), gv = unpack<T>(rg[i]);
+    const Row<T> gv = unpack<T>(rg[i]);
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      e[i][c] = decay_of<T>(lv.v[c]);
-      z[c] = advance<State<T>>(e[i][c], z[c] + gv.v[c], 0);
-      l[c] += lv.v[c];
+      z[c] = walk<T, false>(held_decay<T>(rl[i], c), z[c] + gv.v[c], 0);
+      if constexpr (sizeof(T) == 2) l[c] += unpack<T>(rl[i]).v[c];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (__builtin_expect(!all_finite<T>(z), 0)) {
+    forget(rl);
+    forget(rg);
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      z[c] = 0;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) z[c] = walk<T, true>(held_decay<T>(rl[i], c), z[c] + unpack<T>(rg[i]).v[c], 0);
     }
   }
+  if constexpr (sizeof(T) == 2) hold_decays<T>(rl);
   const auto self = [&]() {
     if (cl >= C) return 0.f;
     const int hh = cl / a.d, jj = cl % a.d;
@@ -481,33 +596,51 @@ __global__ __launch_bounds__(64 * WAVES) void kda_glr_bwd_kernel(GlrArgs a, GlrG
   relay<T, WAVES>(mem, l, z, mu, words, (long long)n.nchain * kWords, g.s, g.s == g.ntile - 1, first, window, polls,
                   a.dh0 && cl < C ? a.dh0 + at + cl : nullptr, self);
   if (!on) return;
+  forget(rl);
+  forget(rg);
+  const auto gradients = [&](auto careful) {
+    constexpr bool CAREFUL = decltype(careful)::value;
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const long long t = t0 - i;
-    const Row<T> xv = unpack<T>(rx[i]), bv = BETA ? unpack<T>(rb[i]) : ones<T>(), gv = unpack<T>(rg[i]);
-    Row<T> before = unpack<T>(ro[i]), gx, gl, gb;
-    if (t == 0 && a.h0) {
+    for (int i = 0; i < NT; ++i) {
+      const long long t = t0 - i;
+      const Row<T> xv = NORM || BETA ? unpack<T>(rx[i]) : ones<T>(), bv = BETA ? unpack<T>(rb[i]) : ones<T>();
+      const Row<T> gv = unpack<T>(rg[i]);
+      Row<T> before = unpack<T>(ro[i]), gx, gl, gb;
+      if (t == 0 && a.h0) {
 #pragma unroll
-      for (int c = 0; c < V; ++c) before.v[c] = a.h0[at + c0 + c];
-    }
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-      mu[c] += (State<T>)gv.v[c];
-      const float lam = (float)mu[c], ee = e[i][c], al = slow(ee) ? 1.f + ee : ee;
-      float n = 1.f, part = 0.f;
-      if constexpr (NORM) {
-        n = unit_of(ee);
-        part = n > 0.f ? al * al * __builtin_amdgcn_rcpf(n) * (bv.v[c] * xv.v[c]) : 0.f;
+        for (int c = 0; c < V; ++c) before.v[c] = a.h0[at + c0 + c];
       }
-      gx.v[c] = n * bv.v[c] * lam;
-      gb.v[c] = n * xv.v[c] * lam;
-      gl.v[c] = al == 0.f ? 0.f : (al * before.v[c] - part) * lam;
-      mu[c] = advance<State<T>>(ee, mu[c], 0);
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        mu[c] += (State<T>)gv.v[c];
+        const float lam = (float)mu[c], ee = held_decay<T>(rl[i], c), al = factor_of<T>(ee);
+        float nl = lam, part = 0.f;
+        if constexpr (NORM) {
+          const float n = unit_of<T>(unpack<T>(rl[i]).v[c], ee);
+          nl *= n;
+          part = n > 0.f ? al * al * __builtin_amdgcn_rcpf(n) * (BETA ? bv.v[c] * xv.v[c] : xv.v[c]) : 0.f;
+        }
+        gx.v[c] = BETA ? nl * bv.v[c] : nl;
+        gb.v[c] = nl * xv.v[c];
+        gl.v[c] = (al * before.v[c] - part) * lam;
+        if constexpr (CAREFUL || sizeof(T) == 4) gl.v[c] = al == 0.f ? 0.f : gl.v[c];
+        mu[c] = walk<T, CAREFUL>(ee, mu[c], 0);
+      }
+      if (!full && t >= g.len) continue;
+      store_by(dx + t * a.dxs.t, pack<T>(gx), a.lines);
+      store_by(dla + t * a.dls.t, pack<T>(gl), a.lines);
+      if constexpr (BETA) store_by(dbeta + t * a.dbs.t, pack<T>(gb), a.lines);
     }
-    if (!full && t >= g.len) continue;
-    store_by(dx + t * a.dxs.t, pack<T>(gx), a.lines);
-    store_by(dla + t * a.dls.t, pack<T>(gl), a.lines);
-    if constexpr (BETA) store_by(dbeta + t * a.dbs.t, pack<T>(gb), a.lines);
+  };
+  gradients(std::false_type());
+  if (__builtin_expect(!all_finite<T>(mu), 0)) {
+    forget(rl);
+    if constexpr (NORM || BETA) forget(rx);
+    if constexpr (BETA) forget(rb);
+    forget(rg);
+    forget(ro);
+    front_state(mem, mu);
+    gradients(std::true_type());
   }
 }
 

@@ -253,20 +253,17 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(
       for (int i = 0; i < NV; ++i) {
         const int vec = i * PER + lane;
         if (!have[j] || vec >= nvec) continue;
-        if (none) keep[j][i] = unpack<T>(u32x4{0u, 0u, 0u, 0u});
-        store8<T>(static_cast<unsigned char*>(a.y) + p.at(a.ys) + vec * V, keep[j][i], none ? 0.f : inv, a.e4m3);
+        Row<T>& y = keep[j][i];
+#pragma unroll
+        for (int c = 0; c < V; ++c) {  // y / sc, its rounding taken back once
+          const float q = y.v[c] * inv;
+          y.v[c] = none ? 0.f : fmaf(fmaf(-q, sc, y.v[c]), inv, q);
+        }
+        store8<T>(static_cast<unsigned char*>(a.y) + p.at(a.ys) + vec * V, y, 1.f, a.e4m3);
       }
       if (have[j] && lane == 0) static_cast<float*>(a.scales)[p.at(a.cs)] = sc;
     }
   }
-}
-
-// Raw values that the compiler must take as freshly loaded: it would otherwise keep their fp32 forms, twice
-// the registers, from the sums over the row to the gradients.
-template <int NV>
-__device__ __forceinline__ void forget(u32x4 (&r)[NV]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(r[i]));
 }
 
 // NV vectors of a row, zeros outside.
@@ -342,6 +339,7 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_bwd_ker
       if constexpr (GATE) load_row<T, PER, NV, true>(gr, g_p, lane, nvec, have);
       load_row<T, PER, NV, true>(dr, d_p, lane, nvec, have && a.ds);
     } else {
+      // (else the fp32 forms, twice the registers, would be kept from the sums to the gradients)
       forget(sr);
       forget(yr);
       if constexpr (GATE && NV > 1) forget(gr);  // (a single vector's gates are kept)

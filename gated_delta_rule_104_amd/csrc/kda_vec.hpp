@@ -46,6 +46,21 @@ __device__ __forceinline__ void st16(T* p, u32x4 w) {
   *reinterpret_cast<u32x4*>(p) = w;
 }
 
+// Registers whose contents the compiler must take as new: what it has computed from them before is then
+// computed again where it is used again, instead of being kept.
+template <int N>
+__device__ __forceinline__ void forget(u32x4 (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(r[i]));
+}
+template <int N, int M>
+__device__ __forceinline__ void forget(float (&r)[N][M]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < M; ++j) asm volatile("" : "+v"(r[i][j]));
+}
+
 // The same for values that nothing reads again soon: they pass the caches without pushing out others.
 template <typename T>
 __device__ __forceinline__ u32x4 ld_once(const T* p) {
