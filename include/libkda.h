@@ -497,7 +497,7 @@ kda_status kda_glr_step(const void* x, const void* log_alpha, const void* beta, 
  * dtype; dh0 [B, H, d] fp32 (NULL: not written).  The gradients of padding are zero,
  * whatever it holds.  A decay of zero has a dlog_alpha of zero, and where
  * log_alpha = 0 the part of dlog_alpha that goes through the normaliser, which has no
- * limit there, is left out.  B and T are at least 1 (unless H * d is 0).
+ * limit there, is left out.  B and T are at least 1 (unless H is 0).
  */
 typedef struct { kda_strides dO, dx, dlog_alpha, dbeta; } kda_glr_grad_strides;
 
@@ -550,7 +550,7 @@ kda_status kda_rms_norm(const void* x, const void* residual, const void* gate, c
  * residual_out where a residual was added.  dx is the gradient of x and of the residual
  * alike; dgate (required with a gate) as gate; dweight (required with a weight) as
  * weight, in dtype, summed in fp32 in a fixed order.  B and T are at least 1 (unless
- * H * d is 0).  The workspace holds partial sums of dweight, and may be NULL without one.
+ * H is 0).  The workspace holds partial sums of dweight, and may be NULL without one.
  */
 typedef struct { kda_strides x, gate, dy, dresidual_out, dx, dgate; } kda_norm_grad_strides;
 

@@ -82,8 +82,8 @@ def rms_norm_backward(s, w, dy, ds=None, gate=None, act="sigmoid", eps=1e-6):
     per = dy * n * g
     out["dweight"] = per.sum((0, 2)) if w is not None and w.dim() == 2 else per.sum((0, 1, 2))
     if z is not None:
-        sig = 1 / (1 + torch.exp(-z))
-        dg = sig * (1 - sig) if act == "sigmoid" else sig * (1 + z * (1 - sig))
+        sig, rest = 1 / (1 + torch.exp(-z)), 1 / (1 + torch.exp(z))  # (1 - sig would be 0 far from zero)
+        dg = sig * rest if act == "sigmoid" else sig * (1 + z * rest)
         out["dgate"] = dy * n * k * dg
     return out
 

@@ -9,9 +9,11 @@ Tolerances, element by element.  A result in bf16 is off by half a step, 2^-8 of
   what is left are the decay's distance from 1 (a polynomial, 2^-22 of it, and it acts for as many tokens as it
   is small) and the input's products, 2^-22 H each, 2^-21 H together; they leave their 64 bits a few times
   where a sequence is cut.
-  normalise adds n's own error, once: 1 - a is off by 1.5 2^-24 (the exponential) of at least 0.22, 2^-21.3 of
-  itself (below 1/4 the polynomial's 2^-22), half of that in the root, 2^-22.3, whose own rounding is 2^-23,
-  and three products: less than 2^-21 together.
+  normalise adds n's own error, once.  fp32: 1 - a is off by 1.5 2^-24 (the exponential) of at least 0.22, 2^-21.3
+  of itself (below 1/4 the polynomial's 2^-22), half of that in the root, 2^-22.3, whose own rounding is 2^-23,
+  and three products: less than 2^-21 together.  bf16: from 1/16 on a is off by 1.2 2^-24, so 1 - a^2 by 2.4 2^-24
+  of at least 0.117, 2^-19.6 of itself, half of that in the root, 2^-20.6, the root's rounding 2^-23 and two
+  products: less than 2^-20.
   Norm: a sum of squares of positive terms takes at most 86 roundings in a row (64 in a lane, 6 over lanes, 16 over
   waves), half of that in its root, and six more products: 49 2^-24 < 2^-18 of the result.  The gradients'
   second sum adds 86 roundings of its terms' absolute sum: 2^-16 of the absolute terms.  dweight adds rows,
@@ -73,7 +75,7 @@ def glr_scale(c, norm, lens=None):
 
 
 def slack(dt, T):
-    return (T * 2.0 ** -22 if dt == "bf16" else 2.0 ** -21) + 2.0 ** -21
+    return T * 2.0 ** -22 + 2.0 ** -20 if dt == "bf16" else 2.0 ** -21 + 2.0 ** -21
 
 
 def check_glr(c, norm, dt, o, h, lens=None):
