@@ -79,12 +79,21 @@ __device__ __forceinline__ void hold_decays(u32x4 (&r)[NT]) {
     forget(r);
   }
 }
+// Sums of log decays: a decay of zero makes a run's decay zero, also next to a gate of NaN (NaN - inf is NaN).
+__device__ __forceinline__ float add_log(float sum, float x, bool clears) {
+  return clears || sum == -__builtin_inff() ? -__builtin_inff() : sum + x;
+}
 template <typename T, int NT>
 __device__ __forceinline__ void add_logs(const u32x4 (&r)[NT], float (&l)[kVec<T>]) {
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int c = 0; c < kVec<T>; ++c) {
+    l[c] = 0.f;
 #pragma unroll
-    for (int c = 0; c < kVec<T>; ++c) l[c] += unpack<T>(r[i]).v[c];
+    for (int i = 0; i < NT; ++i) {
+      const float x = unpack<T>(r[i]).v[c];
+      l[c] = add_log(l[c], x, __float_as_uint(token_decay<T>(x)) == 0u);
+    }
+  }
 }
 template <typename T>
 __device__ __forceinline__ float held_decay(u32x4 r, int c) {
@@ -263,8 +272,9 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
   State<T> zw = 0;
 #pragma unroll
   for (int r = 0; r < SUB; ++r) {
-    zw = advance(m.e[w * SUB + r][lane], zw, m.z[w * SUB + r][lane]);
-    lw += m.l[w * SUB + r][lane];
+    const float e = m.e[w * SUB + r][lane];
+    zw = advance(e, zw, m.z[w * SUB + r][lane]);
+    lw = add_log(lw, m.l[w * SUB + r][lane], __float_as_uint(e) == 0u);
   }
   m.we[w][lane] = decay_of<T>(lw);
   m.wl[w][lane] = lw;
@@ -276,8 +286,9 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
   if (w == 0) {
 #pragma unroll
     for (int u = 0; u < WAVES; ++u) {
-      zt = advance(m.we[u][lane], zt, m.wz[u][lane]);
-      lt += m.wl[u][lane];
+      const float e = m.we[u][lane];
+      zt = advance(e, zt, m.wz[u][lane]);
+      lt = add_log(lt, m.wl[u][lane], __float_as_uint(e) == 0u);
     }
     if (s > 0 && !last) {
       publish(own, lt);
@@ -408,6 +419,7 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
   }
   if (__builtin_expect(!all_finite<T>(z), 0)) {
     forget(rl);
+    add_logs<T>(rl, l);
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       z[c] = 0;
@@ -573,6 +585,7 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, true, BETA>)) void kd
   }
   if (__builtin_expect(!all_finite<T>(z), 0)) {
     forget(rl);
+    add_logs<T>(rl, l);
     forget(rg);
 #pragma unroll
     for (int c = 0; c < V; ++c) {
@@ -623,7 +636,7 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, true, BETA>)) void kd
         gx.v[c] = BETA ? nl * bv.v[c] : nl;
         gb.v[c] = nl * xv.v[c];
         gl.v[c] = (al * before.v[c] - part) * lam;
-        if constexpr (CAREFUL || sizeof(T) == 4) gl.v[c] = al == 0.f ? 0.f : gl.v[c];
+        gl.v[c] = al == 0.f ? 0.f : gl.v[c];  // (also where the state in front is not finite)
         mu[c] = walk<T, CAREFUL>(ee, mu[c], 0);
       }
       if (!full && t >= g.len) continue;

@@ -469,8 +469,9 @@ kda_status kda_state_load(const void* cache, const void* scales, const int* slot
  *   h0, h_T     : [B, H, d] fp32, contiguous; h0 NULL for zero; h_T may be h0
  * States are carried in fp32 (fp32 inputs: in 64 bits inside a run of tokens) and
  * decays near 1 as their distance from it, so that slow ones keep their digits.
- * T == 0 copies h0 (or zeros) to h_T.  An infinity or NaN in x stays in its channel's
- * state until that is cleared.
+ * T == 0 copies h0 (or zeros) to h_T.  An infinity or NaN in x, log_alpha or beta stays
+ * in its channel's state until that is cleared, or until decays that together come to
+ * less than e^-104 have passed over it.
  * The sequences are cut into runs of tokens that fill the device; the workspace
  * (kda_glr_prefill_workspace_bytes; may be 0) holds what passes between them.
  */
