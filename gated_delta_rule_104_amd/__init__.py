@@ -608,6 +608,14 @@ def _scratch(workspace, need: int, device) -> torch.Tensor:
     return workspace
 
 
+def _room(workspace, need: int, device):
+    """(tensor, pointer, bytes) of the workspace of a call that may need none."""
+    if workspace is None and not need:
+        return None, None, 0
+    workspace = _scratch(workspace, need, device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _dtype(t: torch.Tensor) -> int:
     if t.dtype not in _DT:
         raise KdaError(f"unsupported dtype {t.dtype}")
@@ -928,10 +936,9 @@ def glr_prefill(x, log_alpha, beta=None, h0=None, normalise=False, lens=None, o=
         h_T = torch.empty(B, H, d, dtype=torch.float32, device=x.device)
     _dense(h_T, "h_T", torch.float32, (B, H, d), dev)
     lib = load()
-    workspace = _scratch(workspace, int(lib.kda_glr_prefill_workspace_bytes(B, H, T, d, dt)), x.device)
+    workspace, ws, nws = _room(workspace, lib.kda_glr_prefill_workspace_bytes(B, H, T, d, dt), x.device)
     rc = lib.kda_glr_prefill(_ptr(x), _ptr(log_alpha), _ptr(beta), _ptr(h0), _ptr(lens), _ptr(o), _ptr(h_T), st, B, H, T,
-                             d, int(bool(normalise)), dt, _ptr(workspace), workspace.numel() * workspace.element_size(),
-                             _stream())
+                             d, int(bool(normalise)), dt, ws, nws, _stream())
     _check(rc, "kda_glr_prefill")
     return o, h_T
 
@@ -975,11 +982,10 @@ def glr_backward(x, log_alpha, beta, h0, o, dO, dh_T=None, normalise=False, lens
     if h0 is not None:
         out["dh0"] = _new_like(h0)
     lib = load()
-    workspace = _scratch(workspace, int(lib.kda_glr_backward_workspace_bytes(B, H, T, d, dt)), x.device)
+    workspace, ws, nws = _room(workspace, lib.kda_glr_backward_workspace_bytes(B, H, T, d, dt), x.device)
     rc = lib.kda_glr_backward(_ptr(x), _ptr(log_alpha), _ptr(beta), _ptr(h0), _ptr(o), _ptr(dO), _ptr(dh_T), _ptr(lens),
                               _ptr(out["dx"]), _ptr(out["dlog_alpha"]), _ptr(out.get("dbeta")), _ptr(out.get("dh0")), st,
-                              gst, B, H, T, d, int(bool(normalise)), dt, _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _stream())
+                              gst, B, H, T, d, int(bool(normalise)), dt, ws, nws, _stream())
     _check(rc, "kda_glr_backward")
     return out
 
@@ -1079,11 +1085,10 @@ def rms_norm_backward(x, weight, dy, dresidual_out=None, gate=None, gate_activat
     if weight is not None:
         out["dweight"] = _new_like(weight)
         need = int(lib.kda_rms_norm_backward_workspace_bytes(B, H, T, d, int(per_head), dt))
-    workspace = _scratch(workspace, need, x.device)
+    workspace, ws, nws = _room(workspace, need, x.device)
     rc = lib.kda_rms_norm_backward(_ptr(x), _ptr(gate), _ptr(weight), _ptr(dy), _ptr(dresidual_out), _ptr(out["dx"]),
                                    _ptr(out.get("dgate")), _ptr(out.get("dweight")), st, B, H, T, d, int(per_head), eps,
-                                   _gate_act(gate_activation), dt, _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream())
+                                   _gate_act(gate_activation), dt, ws, nws, _stream())
     _check(rc, "kda_rms_norm_backward")
     return out
 
@@ -1121,10 +1126,9 @@ def draft_verify(target, draft, tokens, uniforms, counts=None, accepted=None, ou
         out = torch.empty(N, K1, dtype=torch.int32, device=dev)
     _dense(out, "out", torch.int32, (N, K1), dev)
     lib = load()
-    workspace = _scratch(workspace, int(lib.kda_draft_verify_workspace_bytes(N, K, V, dt)), dev)
+    workspace, ws, nws = _room(workspace, lib.kda_draft_verify_workspace_bytes(N, K, V, dt), dev)
     rc = lib.kda_draft_verify(_ptr(target), ts, _ptr(draft), ds, _ptr(tokens), _ptr(uniforms), _ptr(counts),
-                              _ptr(accepted), _ptr(out), N, K, V, dt, _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _stream())
+                              _ptr(accepted), _ptr(out), N, K, V, dt, ws, nws, _stream())
     _check(rc, "kda_draft_verify")
     return accepted, out
 
