@@ -6,9 +6,13 @@
 // u times the whole one.  Products of fp32 numbers are exact in fp64, and sums are fp64, so that the
 // choice is the one of the exact sums but for a threshold within about 1e-14 of a border.
 //
-// One row of V probabilities (two after a refusal) is all that has to be read, and HBM bounds that.
-// A row is cut into chunks that fill the chip with few sequences too: one launch adds every chunk up,
-// a second one finds the chunk that holds the threshold and walks it alone.
+// One row of V probabilities (two after a refusal) is all that has to be read, and HBM bounds that where
+// there are many long ones.  A row is cut into chunks that fill the chip with few sequences too: one launch adds every
+// chunk up, a second one finds the chunk that holds the threshold and walks it alone.  Short rows
+// take one launch, a workgroup each, since what two launches cost the host is more than they save.
+// fp32, 4 drafts: 256 rows of 128K, greedy drafts accepted in part, 42 us (sums 40 us at HBM's rate, the
+// choice 6.6); 1 row of 50K 14.3 us, 4.2 + 4.6 of it kernels; 64 rows of 20K 11 us, bounded by the host's launch.
+// Choosing 64 states of 32 x 128 x 128 out of 5 takes 51 us for 268 MB, 5.2 TB/s.
 #include "kda_ops.hpp"
 #include "kda_vec.hpp"
 
@@ -17,6 +21,7 @@ namespace kda {
 namespace {
 
 constexpr int kChunk = 4096;  // probabilities of a row per workgroup
+constexpr int kRowChunks = 16;  // of a row that one workgroup takes
 
 struct Choice {
   int accepted, count, token;  // token: the refused one
@@ -78,7 +83,8 @@ __device__ __forceinline__ Row<T> load_any(const T* p) {
 }
 
 // A lane's vector of both rows: what is left of p behind q, and p, in fp64; NaN and what is negative
-// count as no mass.
+// count as no mass, an infinity as the largest number.  The clamps are in fp32, whose instructions are
+// cheaper; p - min(q, p) of fp32 numbers is exact in fp64 unless one is 2^28 times the other.
 template <typename T>
 __device__ __forceinline__ void masses(const Rows<T>& r, int i0, int end, double* w, double* whole) {
   constexpr int V = kVec<T>;
@@ -95,12 +101,11 @@ __device__ __forceinline__ void masses(const Rows<T>& r, int i0, int end, double
   }
 #pragma unroll
   for (int c = 0; c < V; ++c) {
-    const double x = (double)p.v[c];
-    double y = r.q ? (double)q.v[c] : 0.0;
-    if (i0 + c == r.token) y = 1.0;
-    whole[c] = x > 0.0 ? x : 0.0;
-    w[c] = x > y ? x - y : 0.0;
-    if (!(y > 0.0)) w[c] = whole[c];
+    const float x = fminf(fmaxf(p.v[c], 0.f), 3.402823466e38f);
+    float y = r.q ? q.v[c] : 0.f;
+    if (i0 + c == r.token) y = 1.f;
+    whole[c] = (double)x;
+    w[c] = whole[c] - (double)fminf(fmaxf(y, 0.f), x);
   }
 }
 
@@ -108,6 +113,25 @@ __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
   return v;
+}
+
+// A thread's share of the sums over [c0, end), THREADS of them together.
+template <typename T, int THREADS, int DEEP>
+__device__ __forceinline__ void add_up(const Rows<T>& r, int c0, int end, int thread, double* left, double* whole) {
+  constexpr int V = kVec<T>;
+  double s = 0.0, t = 0.0;
+#pragma unroll DEEP
+  for (int i = c0 + thread * V; i < end; i += THREADS * V) {
+    double w[V], z[V];
+    masses<T>(r, i, end, w, z);
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      s += w[c];
+      t += z[c];
+    }
+  }
+  *left = s;
+  *whole = t;
 }
 
 // A sequence's record in the workspace: (accepted, refused token or -1, refused, 0), then the chunks' sums.
@@ -130,19 +154,9 @@ __global__ __launch_bounds__(256) void kda_verify_sum_kernel(VerifyArgs a, int n
     *rec.choice = int4{choice.accepted, choice.token, choice.accepted < choice.count, 0};
   }
   const Rows<T> r(a, n, choice.accepted, choice.token, choice.accepted < choice.count);
-  const int c0 = chunk * kChunk, end = min(c0 + kChunk, a.V);
-  double s = 0.0, whole = 0.0;
-  constexpr int V = kVec<T>;
-#pragma unroll 4
-  for (int i = c0 + (int)threadIdx.x * V; i < end; i += 256 * V) {
-    double w[V], z[V];
-    masses<T>(r, i, end, w, z);
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-      s += w[c];
-      whole += z[c];
-    }
-  }
+  const int c0 = chunk * kChunk;
+  double s, whole;
+  add_up<T, 256, 4>(r, c0, min(c0 + kChunk, a.V), threadIdx.x, &s, &whole);
   s = wave_sum(s);
   whole = wave_sum(whole);
   if ((threadIdx.x & 63) == 0) {
@@ -167,28 +181,25 @@ __device__ __forceinline__ double wave_scan(double v) {
   return v;
 }
 
-// One workgroup per sequence: every wave finds the chunk that the threshold lies in (lane = chunk), then the block
-// walks it, 8 probabilities a thread.  Where rounding leaves no sum above the threshold, the last token that has
-// mass is taken.  A chain of latencies: the record, the chunk, the sums over lanes and waves.
-template <typename T>
-__global__ __launch_bounds__(512) void kda_verify_pick_kernel(VerifyArgs a, int nchunk) {
+// The token, by a workgroup of WAVES waves: every wave finds the chunk that the threshold lies in (lane = chunk), then
+// 512 threads walk it, 8 probabilities each.  Where rounding leaves no sum above the threshold, the last token that
+// has mass is taken.  choice and sums: a sequence's record.
+template <typename T, int WAVES>
+__device__ __forceinline__ void pick(const VerifyArgs& a, int n, int4 choice, float u, const double2* sums, int nchunk, int size) {
   constexpr int V = kVec<T>, OWN = kChunk / 512;  // a thread's neighbouring probabilities of the chunk
   constexpr int NONE = 0x7fffffff;
-  __shared__ double front_of[8];
+  __shared__ double front_of[WAVES];
   __shared__ int first, last;
-  const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Record rec(a, n, nchunk);
-  const int4 choice = *rec.choice;
-  const float u = a.u[(long long)n * (a.K + 1) + a.K];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   double2 v{0.0, 0.0};
-  if (lane < nchunk) v = rec.sums[lane];
+  if (lane < nchunk) v = sums[lane];
   if (tid == 0) {
     first = NONE;
     last = -1;
   }
   double left = v.x, whole = v.y;
   for (int i = lane + 64; i < nchunk; i += 64) {
-    const double2 x = rec.sums[i];
+    const double2 x = sums[i];
     left += x.x;
     whole += x.y;
   }
@@ -201,7 +212,7 @@ __global__ __launch_bounds__(512) void kda_verify_pick_kernel(VerifyArgs a, int 
   bool sure = false;
   double front = 0.0, base = 0.0;
   for (int i0 = 0; i0 < nchunk; i0 += 64) {
-    if (i0 > 0) v = i0 + lane < nchunk ? rec.sums[i0 + lane] : double2{0.0, 0.0};
+    if (i0 > 0) v = i0 + lane < nchunk ? sums[i0 + lane] : double2{0.0, 0.0};
     const double mine = rest ? v.x : v.y, sum = base + wave_scan(mine);
     const unsigned long long above = __ballot(mine > 0.0 && sum > goal), any = __ballot(mine > 0.0);
     if (above) {
@@ -216,7 +227,7 @@ __global__ __launch_bounds__(512) void kda_verify_pick_kernel(VerifyArgs a, int 
   }
   int token = -1;
   if (chunk >= 0) {
-    const int c0 = chunk * kChunk, end = min(c0 + kChunk, a.V), mine = c0 + tid * OWN;
+    const int c0 = chunk * size, end = min(c0 + size, a.V), mine = c0 + tid * OWN;
     double w[OWN], s = 0.0;
 #pragma unroll
     for (int i = 0; i < OWN; i += V) {
@@ -248,9 +259,46 @@ __global__ __launch_bounds__(512) void kda_verify_pick_kernel(VerifyArgs a, int 
     __syncthreads();
     token = first != NONE ? first : last;
   }
-  for (int j = tid; j <= a.K; j += 512)
+  for (int j = tid; j <= a.K; j += 64 * WAVES)
     a.out[(long long)n * (a.K + 1) + j] =
         j < choice.x ? a.tokens[(long long)n * a.K + j] : (j == choice.x ? token : -1);
+}
+
+// One workgroup per sequence, a chain of latencies: the record, the chunk, the sums over lanes and waves.
+template <typename T>
+__global__ __launch_bounds__(512) void kda_verify_pick_kernel(VerifyArgs a, int nchunk) {
+  const int n = blockIdx.x;
+  const Record rec(a, n, nchunk);
+  const float u = a.u[(long long)n * (a.K + 1) + a.K];
+  pick<T, 8>(a, n, *rec.choice, u, rec.sums, nchunk, kChunk);
+}
+
+// Short rows in one launch: a workgroup per sequence, a chunk per wave.  Only what is left is added up; where that is
+// nothing, p itself.
+template <typename T>
+__global__ __launch_bounds__(1024) void kda_verify_row_kernel(VerifyArgs a, int nchunk, int size) {
+  __shared__ double2 sums[kRowChunks];
+  const int n = blockIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const float u = a.u[(long long)n * (a.K + 1) + a.K];
+  const Choice choice = accept<T>(a, n);
+  if (threadIdx.x == 0) a.accepted[n] = choice.accepted;
+  for (bool refused = choice.accepted < choice.count;; refused = false) {
+    if (wave < nchunk) {
+      const Rows<T> r(a, n, choice.accepted, choice.token, refused);
+      double left, whole;
+      add_up<T, 64, 4>(r, wave * size, min((wave + 1) * size, a.V), lane, &left, &whole);
+      left = wave_sum(left);
+      if (lane == 0) sums[wave] = double2{left, left};
+    }
+    __syncthreads();
+    bool any = !refused;
+    for (int i = 0; i < nchunk; ++i) any = any || sums[i].x > 0.0;
+    if (any) {
+      pick<T, 16>(a, n, int4{choice.accepted, refused ? choice.token : -1, refused, 0}, u, sums, nchunk, size);
+      return;
+    }
+    __syncthreads();
+  }
 }
 
 // S[n] = S_pos[n][index[n]], by shares of a state's values; an index outside leaves S[n] as it is.
@@ -274,10 +322,19 @@ __global__ __launch_bounds__(256) void kda_state_commit_kernel(const float* __re
 }
 
 int verify_chunks(int V) { return (V + kChunk - 1) / kChunk; }
+// Whether a workgroup takes a whole row: one launch less and no workspace, but a row's sums then are one CU's work.
+// With a draft, fp32, us in one launch / two: 1 row of 4K 10.6 / 14.3, 32K 11.2 / 15.0, 64K 14.7 / 14.3; 64 rows 10.7 / 14.7,
+// 13.2 / 14.1, 18.9 / 14.7; 256 rows 10.7 / 14.7, 16.7 / 20.1; with more rows than CUs, 1024 of 1K, 34 / 15.
+bool verify_row(int N, int V) { return N <= 256 && V <= 32768; }
 
 template <typename T>
 hipError_t verify(const VerifyArgs& a, hipStream_t stream) {
   const int nchunk = verify_chunks(a.V);
+  if (verify_row(a.N, a.V)) {
+    const int size = ((a.V + kRowChunks - 1) / kRowChunks + 511) / 512 * 512;
+    hipLaunchKernelGGL((kda_verify_row_kernel<T>), dim3((unsigned)a.N), dim3(1024), 0, stream, a, (a.V + size - 1) / size, size);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL((kda_verify_sum_kernel<T>), dim3((unsigned)((long long)a.N * nchunk)), dim3(256), 0, stream, a, nchunk);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -287,7 +344,10 @@ hipError_t verify(const VerifyArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t verify_ws_bytes(int N, int V) { return (size_t)N * (verify_chunks(V) + 1) * 16; }
+size_t verify_ws_bytes(int N, int V) {
+  const int nchunk = verify_chunks(V);
+  return verify_row(N, V) ? 0 : (size_t)N * (nchunk + 1) * 16;
+}
 
 hipError_t launch_verify(const VerifyArgs& a, bool bf16_io, hipStream_t stream) {
   return bf16_io ? verify<bf16>(a, stream) : verify<float>(a, stream);

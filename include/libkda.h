@@ -573,7 +573,7 @@ kda_status kda_rms_norm_backward(const void* x, const void* gate, const void* we
  * uniforms[n, K] times the sum of all of them.  A token of no mass is never drawn; where
  * max(p - q, 0) has none at all, p is drawn from, and where p has none the token is -1.
  *   target   : [N, K + 1, V] dtype, p: the target's probabilities (they need not add up to
- *              1; NaN and negative ones count as 0)
+ *              1; NaN and negative ones count as 0, infinite ones as the largest number)
  *   draft    : [N, K, V] dtype, q: the draft's; NULL for one at each drafted token (greedy
  *              drafts).  Strides b and t of both in elements (h is ignored), any element
  *              alignment, rows of V contiguous; NULL for contiguous.
@@ -582,7 +582,8 @@ kda_status kda_rms_norm_backward(const void* x, const void* gate, const void* we
  *   counts   : [N] drafts of each sequence (clamped to [0, K]), or NULL for K
  *   accepted : [N] written: accepted drafts a
  *   out      : [N, K + 1] written: the a accepted drafts, the next token, then -1
- * Sums are fp64.  K == 0 draws one token from each row.  The workspace holds partial sums.
+ * Sums are fp64.  K == 0 draws one token from each row.  The workspace holds partial sums
+ * (0 bytes where each row is taken by one workgroup).
  */
 size_t kda_draft_verify_workspace_bytes(int N, int K, int V, kda_dtype dtype);
 kda_status kda_draft_verify(const void* target, const kda_strides* target_strides, const void* draft,

@@ -104,6 +104,7 @@ def calls(dt):
     c["o"], _ = kda.glr_prefill(c["x"], c["la"], c["beta"], c["h0"], normalise=True)
     n = {k: up(t) for k, t in norm_case(2, 3, 50, 64, dt, 2, True, True, True).items()}
     p, q, tok, u = (up(t) for t in verify_case(7, 3, 9001, dt, 3))
+    long = dict(zip(("p", "q", "tok", "u"), (up(t) for t in verify_case(3, 3, 40001, dt, 6))))
     S_pos, S = torch.randn(7, 4, 2, 16, 16, generator=gen(4)).to(dev()), torch.randn(7, 2, 16, 16, generator=gen(5)).to(dev())
     fwd = lambda t: (t["x"], t["la"], t["beta"], t["h0"])  # noqa: E731
 
@@ -126,10 +127,11 @@ def calls(dt):
                                      for x in kda.rms_norm_quant(t["x"], t["w"], t["residual"], t["gate"])]),
         "norm_backward": (n, lambda t: kda.rms_norm_backward(t["x"], t["w"], t["dy"], t["ds"], t["gate"])),
         "drafts": (dict(p=p, q=q, u=u, S_pos=S_pos, S=S), drafts),
+        "drafts_of_long_rows": (long, lambda t: kda.draft_verify(t["p"], t["q"], t["tok"], t["u"])),
     }
 
 
-NAMES = ["glr", "glr_backward", "glr_step", "norm", "norm_quant", "norm_backward", "drafts"]
+NAMES = ["glr", "glr_backward", "glr_step", "norm", "norm_quant", "norm_backward", "drafts", "drafts_of_long_rows"]
 
 
 def redraw(inputs, g):

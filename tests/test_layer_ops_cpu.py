@@ -167,10 +167,11 @@ def test_norm_backward_refusals(lib):
 
 # ----------------------------------------------------------------- drafts
 def test_verify_refusals(lib):
-    need = lib.kda_draft_verify_workspace_bytes(2, 3, 1000, F32)
-    assert need > 0 and lib.kda_draft_verify_workspace_bytes(0, 3, 1000, F32) == 0
+    need = lib.kda_draft_verify_workspace_bytes(2, 3, 40000, F32)
+    assert need > 0 and lib.kda_draft_verify_workspace_bytes(0, 3, 40000, F32) == 0
+    assert lib.kda_draft_verify_workspace_bytes(2, 3, 1000, F32) == 0  # (short rows need none)
 
-    def f(N=2, K=3, V=1000, dt=F32, ws=A, nws=need, ts=None, qs=None, **p):
+    def f(N=2, K=3, V=40000, dt=F32, ws=A, nws=need, ts=None, qs=None, **p):
         a = dict(p=A + 4, q=A + 8, tok=A + 12, u=A + 16, counts=None, acc=A + 20, out=A + 24)
         a.update(p)
         return lib.kda_draft_verify(a["p"], ts, a["q"], qs, a["tok"], a["u"], a["counts"], a["acc"], a["out"], N, K, V, dt, ws,

@@ -418,7 +418,7 @@ def verify_case(N, K, V, dt, seed, sharp=3.0):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("N,K,V", [(1, 1, 1), (3, 4, 7), (40, 3, 257), (9, 0, 1000), (5, 70, 33), (17, 5, 8192), (6, 2, 50257),
-                                   (2, 1, 150001)])
+                                   (2, 1, 150001), (256, 2, 40), (257, 2, 40), (2, 3, 32768), (2, 3, 32769)])
 def test_draft_verify(N, K, V, dt):
     print(f"[case] draft_verify {N} {K} {V} {dt}", flush=True)
     p, q, tok, u = verify_case(N, K, V, dt, N + V)
@@ -449,10 +449,11 @@ def test_draft_verify_counts_and_strides():
     assert torch.equal(a.cpu(), ra) and torch.equal(out.cpu(), ro)
 
 
-def test_draft_verify_borders():
+@pytest.mark.parametrize("V", [20000, 40000])
+def test_draft_verify_borders(V):
     """Uniforms of 0 and just below 1, masses only at the ends, equal distributions, none at all, tokens outside
     the vocabulary, NaN."""
-    V, K = 20000, 2
+    K = 2
     z = torch.zeros(10, K + 1, V)
     q = torch.zeros(10, K, V)
     tok = torch.zeros(10, K, dtype=torch.int32)
