@@ -474,13 +474,14 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
   }
 }
 
-// Empties the words of a call's tiles, 64 bytes a thread.
-__global__ __launch_bounds__(256) void kda_glr_clear_kernel(u32x4* words, long long n) {
+// Empties the words of a call's tiles, 64 bytes a thread, and copies nh vectors of first states behind them.
+__global__ __launch_bounds__(256) void kda_glr_clear_kernel(u32x4* words, long long n, const float* h, long long nh) {
   const u32x4 v{kEmpty, kEmpty, kEmpty, kEmpty};
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const long long i = (long long)blockIdx.x * 1024 + u * 256 + threadIdx.x;
     if (i < n) words[i] = v;
+    else if (i < n + nh) words[i] = ld16(h + 4 * (i - n));
   }
 }
 
@@ -715,10 +716,15 @@ GlrGrid glr_grid(int B, int H, int len, int d, bool bf16_io, bool gradients, boo
 }
 
 template <typename T, bool GRADIENTS, int NT, bool BETA>
-hipError_t glr_launch(const GlrArgs& a, const GlrGrid& n, int polls, hipStream_t stream) {
+hipError_t glr_launch(GlrArgs a, const GlrGrid& n, int polls, hipStream_t stream) {
   if (n.ntile > 1) {
     const long long words = (long long)n.nchain * n.ntile * kWords / 4;
-    hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((words + 1023) / 1024)), dim3(256), 0, stream, static_cast<u32x4*>(a.ws), words);
+    // a chain's last tile may write h_T before another one has read h0: in place, the tiles read a copy
+    const bool place = !GRADIENTS && a.h0 && a.h0 == a.h_T;
+    const long long copy = place ? (long long)a.B * a.H * a.d / 4 : 0;
+    hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((words + copy + 1023) / 1024)), dim3(256), 0, stream,
+                       static_cast<u32x4*>(a.ws), words, a.h0, copy);
+    if (place) a.h0 = reinterpret_cast<const float*>(static_cast<u32x4*>(a.ws) + words);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -750,7 +756,9 @@ size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients) {
   for (int beta = 0; beta < 2; ++beta) {
     int nt;
     const GlrGrid n = glr_grid(B, H, T, d, bf16_io, gradients, beta != 0, &nt);
-    const size_t bytes = n.ntile > 1 ? (size_t)n.nchain * n.ntile * kWords * sizeof(uint32_t) : 0;
+    // (the words of the tiles, and for prompts a copy of h0)
+    const size_t words = (size_t)n.nchain * n.ntile * kWords + (gradients ? 0 : (size_t)B * H * d);
+    const size_t bytes = n.ntile > 1 ? words * sizeof(uint32_t) : 0;
     most = bytes > most ? bytes : most;
   }
   return most;

@@ -97,6 +97,25 @@ def test_glr_same_bits_every_time():
         assert all(torch.equal(grads[n], g[n]) for n in grads)
 
 
+@pytest.mark.parametrize("polls", [None, 0])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_glr_states_in_place(dt, polls, kda_opts):
+    """h_T in h0's place, with more runs of tokens than the device holds at a time and unequal lengths: whichever run
+    ends first, all of them start from the state that was given."""
+    if polls is not None:
+        kda_opts("glr_polls", polls)
+    c = glr_case(6, 16, 2500, 64, dt, 21)
+    lens = torch.tensor([2500, 0, 1, 2499, 128, 1300], dtype=torch.int32, device=dev())
+    args = [up(c[n]) for n in ("x", "la", "beta")]
+    h = up(c["h0"])
+    o0, h0 = kda.glr_prefill(*args, h.clone(), lens=lens, o=torch.zeros_like(args[0]))
+    for _ in range(3):
+        at = h.clone()
+        o, got = kda.glr_prefill(*args, at, lens=lens, o=torch.zeros_like(args[0]), h_T=at)
+        torch.cuda.synchronize()
+        assert got is at and torch.equal(at, h0) and torch.equal(o, o0)
+
+
 # ------------------------------------------------- captured, concurrent
 def calls(dt):
     """name -> (static inputs, function of them that returns what it wrote)."""
