@@ -4,9 +4,11 @@
 //     lam_t = dO_t + a_{t+1} lam_{t+1} (+ dh_T at the end),   dx = n beta lam,   dbeta = n x lam,
 //     dlog_alpha = a h_{t-1} lam - (a^2 / n) beta x lam,   dh0 = a_1 lam_1,
 // where h_{t-1} is read back from the forward pass's outputs.
+#include <cstdio>
 #include <mutex>
 #include <type_traits>
 
+#include "kda_host.hpp"
 #include "kda_ops.hpp"
 #include "kda_vec.hpp"
 
@@ -174,13 +176,13 @@ template <typename T> constexpr int kSub = 64 / kLpr<T>;
 template <typename T, int WAVES>
 struct RelayMem {
   static constexpr int SUBS = WAVES * kSub<T>, WINDOW = SUBS / 2;
-  float e[SUBS][kSlab];  // decays of the lanes' tokens
+  alignas(16) float e[SUBS][kSlab];  // decays of the lanes' tokens
   // the sums of their logs; later decays and end states from zero of the tiles looked back at
   union {
     float l[SUBS][kSlab];
     float past[2][WINDOW][kSlab];
   };
-  State<T> z[SUBS][kSlab];  // end states from zero; later the states in front
+  alignas(16) State<T> z[SUBS][kSlab];  // end states from zero; later the states in front
   float we[WAVES][kSlab], wl[WAVES][kSlab], h[kSlab];
   State<T> wz[WAVES][kSlab];
   float ends[WINDOW][kSlab];
@@ -252,6 +254,21 @@ __device__ __forceinline__ void front_state(const RelayMem<T, WAVES>& m, State<T
   for (int c = 0; c < kVec<T>; ++c) h[c] = m.z[sub][lane % kLpr<T> * kVec<T> + c];
 }
 
+// N neighbouring values to LDS, 16 bytes at a time: single ones, which the compiler would make of them, have the lanes
+// of eight groups of tokens on the same banks.
+template <int N, typename A>
+__device__ __forceinline__ void put(A* p, const A (&v)[N]) {
+  using Vec = A __attribute__((ext_vector_type(16 / sizeof(A))));
+  constexpr int W = 16 / sizeof(A);
+#pragma unroll
+  for (int i = 0; i < N / W; ++i) {
+    Vec w;
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = v[i * W + k];
+    reinterpret_cast<Vec*>(p)[i] = w;
+  }
+}
+
 // From each lane's (l, z) to the state in front of its tokens, h.  s: the tile's number in its chain;
 // self: the state in front of the tile without the others' help; end: where the chain's end state goes
 // (lane = channel), or null.
@@ -261,12 +278,12 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
                                       int window, int polls, float* end, Self self) {
   constexpr int V = kVec<T>, LPR = kLpr<T>, SUB = kSub<T>;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = w * SUB + lane / LPR, c0 = lane % LPR * V;
+  float e[V];
 #pragma unroll
-  for (int c = 0; c < V; ++c) {
-    m.e[sub][c0 + c] = decay_of<T>(l[c]);
-    m.l[sub][c0 + c] = l[c];
-    m.z[sub][c0 + c] = z[c];
-  }
+  for (int c = 0; c < V; ++c) e[c] = decay_of<T>(l[c]);
+  put<V>(&m.e[sub][c0], e);
+  put<V>(&m.l[sub][c0], l);
+  put<V>(&m.z[sub][c0], z);
   wave_lds_fence();
   float lw = 0.f;
   State<T> zw = 0;
@@ -728,6 +745,9 @@ hipError_t glr_launch(GlrArgs a, const GlrGrid& n, int polls, hipStream_t stream
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  if (api_log_on())
+    fprintf(stderr, "[kda] %s B=%d H=%d T=%d d=%d: %d chains of %d runs of %d tokens\n", GRADIENTS ? "glr_backward" : "glr_prefill",
+            a.B, a.H, a.T, a.d, n.nchain, n.ntile, kWaves * kSub<T> * NT);
   const dim3 grid((unsigned)((long long)n.blocks * n.ntile)), threads(64 * kWaves);
   // tiles of a chain that are under way together, and one more: about 1024 workgroups fit the device
   const int window = 1 + 1024 / n.nchain;

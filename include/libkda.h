@@ -528,7 +528,8 @@ kda_status kda_glr_backward(const void* x, const void* log_alpha, const void* be
  *                          d a multiple of 32: exponent + 127 of a power of two for each 32
  *                          values, chosen and marked as in the quantised state cache above
  *                  values are rounded to nearest even, and 0 where marked
- * Sums are fp32.
+ * Sums are fp32, as is the factor they give: a row whose squares add up to more than
+ * 3.4e38 becomes zeros, and a row of zeros with eps = 0 NaN.
  */
 typedef enum { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 } kda_gate;
 typedef enum {
