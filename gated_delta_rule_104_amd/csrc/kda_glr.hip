@@ -190,11 +190,11 @@ struct RelayMem {
 };
 
 // The state in front of tile s >= 1 of a chain, lane = channel, for wave 0; false if the tiles before it did
-// not answer.  words: the chain's tile 0, hop words to the next one; first: the state in front of tile 0;
+// not answer.  words: the chain's tile 0, hop words to the next one (tile 0 publishes its end state alone);
 // window: how many tiles to look at, shared out over the waves, which have nothing else to do.
 template <typename T, int WAVES>
-__device__ __forceinline__ bool look_back(RelayMem<T, WAVES>& m, const uint32_t* words, long long hop, int s, float first,
-                                          int window, int polls, float* state) {
+__device__ __forceinline__ bool look_back(RelayMem<T, WAVES>& m, const uint32_t* words, long long hop, int s, int window,
+                                          int polls, float* state) {
   constexpr int W = RelayMem<T, WAVES>::WINDOW, OWN = W / WAVES;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int poll = 0; poll < polls; ++poll) {
@@ -217,7 +217,7 @@ __device__ __forceinline__ bool look_back(RelayMem<T, WAVES>& m, const uint32_t*
       m.past[1][i][lane] = __uint_as_float(z[k]);
       m.ends[i][lane] = __uint_as_float(p[k]);
       if (__ballot(l[k] == kEmpty || z[k] == kEmpty) == 0ull) sums |= 1u << i;
-      if (i == s || __ballot(p[k] == kEmpty) == 0ull) ends |= 1u << i;  // (what is in front of tile 0 is known)
+      if (__ballot(p[k] == kEmpty) == 0ull) ends |= 1u << i;
     }
     if (lane == 0) {
       m.sums_there[w] = sums;
@@ -234,7 +234,7 @@ __device__ __forceinline__ bool look_back(RelayMem<T, WAVES>& m, const uint32_t*
     const int found = __ffs(ends) - 1;
     if (found >= 0 && (~sums & ((1u << found) - 1u)) == 0u) {
       if (w == 0) {
-        float h = found == s ? first : m.ends[found][lane];
+        float h = m.ends[found][lane];
         for (int i = found - 1; i >= 0; --i) h = advance(m.past[0][i][lane], h, m.past[1][i][lane]);
         *state = h;
       }
@@ -312,7 +312,7 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
       publish(own + kSlab, (float)zt);
     }
   }
-  const bool known = s == 0 || look_back<T, WAVES>(m, words, hop, s, first, window, polls, &front);
+  const bool known = s == 0 || look_back<T, WAVES>(m, words, hop, s, window, polls, &front);
   if (w == 0) {
     if (!known) front = self();
     const float out = advance(decay_of<T>(lt), front, (float)zt);
@@ -340,6 +340,7 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
 struct GlrGrid {
   int nslab, ntile, nchain, blocks;  // blocks: workgroups per run of all chains
   bool spread;
+  bool place;  // the first states are in the words
 };
 struct GlrTile {
   int b, slab, s, len, ntile;  // sequence, slab, number in the chain, tokens and tiles of the sequence
@@ -382,7 +383,7 @@ __device__ __forceinline__ void load_rows(u32x4 (&r)[NT], const T* p, long long 
 // Waves per SIMD that the registers have to leave room for.
 template <typename T, int NT, bool GRADIENTS, bool BETA>
 constexpr int kResident = GRADIENTS ? (sizeof(T) == 4 || NT == 2 ? 4 : (NT == 3 || !BETA ? 3 : 2))
-                                    : (sizeof(T) == 4 || NT == 6 ? 3 : (NT == 4 ? 4 : 2));
+                                    : (sizeof(T) == 2 && NT == 4 ? 4 : 3);
 
 template <typename T, int NT, int WAVES, bool NORM, bool BETA>
 __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void kda_glr_kernel(GlrArgs a, GlrGrid n, int window, int polls) {
@@ -400,7 +401,8 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
   const T* beta = BETA ? static_cast<const T*>(a.beta) + g.b * a.bs.b + hd * a.bs.h + j0 : nullptr;
   const int cl = g.slab * kSlab + lane;  // lane = channel
   const long long at = (long long)g.b * C + cl;
-  const float first = a.h0 && cl < C ? a.h0[at] : 0.f;
+  uint32_t* words = static_cast<uint32_t*>(a.ws) + (long long)g.chain * kWords;
+  const float first = a.h0 && cl < C ? (n.place ? __uint_as_float(words[lane]) : a.h0[at]) : 0.f;
   if (g.len == 0) {
     if (threadIdx.x < 64 && cl < C) a.h_T[at] = first;
     return;
@@ -410,8 +412,19 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
   load_rows<T, NT, 1>(rl, la, a.ls.t, t0, g.len, on, full);
   load_rows<T, NT, 1>(rx, x, a.xs.t, t0, g.len, on, full);
   if constexpr (BETA) load_rows<T, NT, 1>(rb, beta, a.bs.t, t0, g.len, on, full);
-  float in[NT][V], l[V];
+  // longer runs of bf16 are kept as they were read, and their inputs are formed again: fewer registers
+  constexpr bool AGAIN = sizeof(T) == 2 && NT > 4;
+  float in[AGAIN ? 1 : NT][V], l[V];
   State<T> h[V], z[V];
+  const auto input = [&](int i, int c, float e) {
+    if constexpr (!AGAIN) {
+      return in[i][c];
+    } else {
+      float v = unpack<T>(rx[i]).v[c];
+      if constexpr (BETA) v *= unpack<T>(rb[i]).v[c];
+      return NORM ? v * unit_of<T>(unpack<T>(rl[i]).v[c], e) : v;
+    }
+  };
 #pragma unroll
   for (int c = 0; c < V; ++c) l[c] = 0.f;
   if constexpr (sizeof(T) == 4) {
@@ -428,7 +441,7 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
       const float e = held_decay<T>(rl[i], c);
       float v = BETA ? bv.v[c] * xv.v[c] : xv.v[c];
       if constexpr (NORM) v *= unit_of<T>(unpack<T>(rl[i]).v[c], e);
-      in[i][c] = v;
+      if constexpr (!AGAIN) in[i][c] = v;
       z[c] = walk<T, false>(e, z[c], v);
       if constexpr (sizeof(T) == 2) l[c] += unpack<T>(rl[i]).v[c];
     }
@@ -436,15 +449,22 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
   }
   if (__builtin_expect(!all_finite<T>(z), 0)) {
     forget(rl);
+    if constexpr (AGAIN) forget(rx);
+    if constexpr (AGAIN && BETA) forget(rb);
     add_logs<T>(rl, l);
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       z[c] = 0;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) z[c] = walk<T, true>(held_decay<T>(rl[i], c), z[c], in[i][c]);
+      for (int i = 0; i < NT; ++i) {
+        const float e = held_decay<T>(rl[i], c);
+        z[c] = walk<T, true>(e, z[c], input(i, c, e));
+      }
     }
   }
   if constexpr (sizeof(T) == 2) hold_decays<T>(rl);
+  if constexpr (AGAIN) forget(rx);
+  if constexpr (AGAIN && BETA) forget(rb);
   const auto self = [&]() {
     if (cl >= C) return 0.f;
     const int hh = cl / a.d, jj = cl % a.d;
@@ -461,7 +481,6 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
     }
     return (float)run;
   };
-  uint32_t* words = static_cast<uint32_t*>(a.ws) + (long long)g.chain * kWords;
   relay<T, WAVES>(mem, l, z, h, words, (long long)n.nchain * kWords, g.s, g.s == g.ntile - 1, first, window, polls,
                   cl < C ? a.h_T + at : nullptr, self);
   if (!on) return;
@@ -476,7 +495,8 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
       Row<T> y;
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        h[c] = walk<T, decltype(careful)::value>(held_decay<T>(rl[i], c), h[c], in[i][c]);
+        const float e = held_decay<T>(rl[i], c);
+        h[c] = walk<T, decltype(careful)::value>(e, h[c], input(i, c, e));
         y.v[c] = (float)h[c];
       }
       if (full || t0 + i < g.len) store_by(o + (t0 + i) * a.os.t, pack<T>(y), a.lines);
@@ -486,19 +506,26 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
   outputs(std::false_type());
   if (__builtin_expect(!all_finite<T>(h), 0)) {
     forget(rl);
+    if constexpr (AGAIN) forget(rx);
+    if constexpr (AGAIN && BETA) forget(rb);
     front_state(mem, h);
     outputs(std::true_type());
   }
 }
 
-// Empties the words of a call's tiles, 64 bytes a thread, and copies nh vectors of first states behind them.
-__global__ __launch_bounds__(256) void kda_glr_clear_kernel(u32x4* words, long long n, const float* h, long long nh) {
-  const u32x4 v{kEmpty, kEmpty, kEmpty, kEmpty};
+// Empties the words of a call's tiles, 64 bytes a thread.  With h0 the first states, of C channels a sequence, are put
+// where a chain's first tile would have the sums of its logs, which nobody asks it for.
+__global__ __launch_bounds__(256) void kda_glr_clear_kernel(u32x4* words, long long n, const float* h0, int nchain, int nslab, int C) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const long long i = (long long)blockIdx.x * 1024 + u * 256 + threadIdx.x;
-    if (i < n) words[i] = v;
-    else if (i < n + nh) words[i] = ld16(h + 4 * (i - n));
+    if (i >= n) continue;
+    u32x4 v{kEmpty, kEmpty, kEmpty, kEmpty};
+    if (h0 && i < (long long)nchain * (kWords / 4)) {
+      const int chain = (int)(i / (kWords / 4)), word = (int)(i % (kWords / 4)) * 4, c = chain % nslab * kSlab + word;
+      if (word < kSlab && c < C) v = ld16(h0 + (long long)(chain / nslab) * C + c);
+    }
+    words[i] = v;
   }
 }
 
@@ -704,44 +731,55 @@ __global__ __launch_bounds__(256) void kda_glr_check_kernel(GlrArgs a, int nvec,
 constexpr int kWaves = 4;
 
 // Tokens per lane.  More of them make a tile longer, and a chain's way through its tiles shorter, but take
-// registers, and with them the waves that hide each other's latency.  So few chains, whose way
-// bounds the call, take more than many, and calls without beta, which hold a tensor less, more than
-// calls with it.  bf16, 268M values in up to 64K tokens (fewer with under 16 chains), us with 4 / 6 / 8 tokens:
-//   prompt           256 chains 211 / 268 / 244   64 223 / 272 / 245   16 134 / 152 / 140   4  74 / 53 / 48
-//   without beta     256        171 / 168 / 203   64 179 / 173 / 206   16 111 / 105 / 116   4  72 / 53 / 43
-// with 2 / 3 / 4 tokens:
-//   gradients        256        439 / 444 / 468   64 443 / 456 / 468   40 453 / 429 / 456   4 141 / 105 / 86
-//   without beta     256        310 / 272 / 273   64 323 / 293 / 285   40 340 / 292 / 282   4 133 / 95 / 73
+// registers, and with them the waves that hide each other's latency, and leave short sequences with few tiles.  So long
+// sequences, and few chains, whose way bounds the call, take more than others, and calls without beta, which hold a tensor
+// less, more than calls with it.  Prompts form their inputs again with more than 4 tokens (fewer registers), which a
+// normaliser makes dearer.  bf16, us; prompts by chains of 64 channels and tokens:
+//   with beta, normalised    4 / 8 tokens       4 x 32000 45 / 33   40 x 32000 143 / 135   64 x 32000 209 / 204   128 x 32000 386 / 392
+//                                               4 x 8000 18 / 19    40 x 8000 42 / 44      64 x 8000 60 / 63      256 x 8000 192 / 203
+//   without, normalised      4 / 8 / 12         4 x 32000 43 / 30 / 29   64 x 32000 177 / 172 / 169   256 x 32000 625 / 651 / 626
+//                                               4 x 8000 17 / 17 / 19    64 x 8000 50 / 52 / 55       256 x 8000 161 / 172 / 164
+//   without either           4 / 8 / 12         4 x 32000 43 / 28 / 26   64 x 32000 170 / 152 / 149   256 x 32000 564 / 555 / 543
+//                                               4 x 8000 17 / 15 / 15    64 x 8000 48 / 46 / 48       256 x 2000 44 / 44 / 47
+// gradients of 134M values with beta (268M without) in up to 64K tokens by chains, with 2 / 3 / 4 tokens:
+//   with beta                256 439 / 444 / 468   64 443 / 456 / 468   40 453 / 429 / 456   4 141 / 105 / 86
+//   without                  256 310 / 272 / 273   64 323 / 293 / 285   40 340 / 292 / 282   4 133 / 95 / 73
+// Where the longer run is the whole sequence, the call needs no second launch: prompts with beta of 200 tokens, 4 / 8:
+// 64 chains 14.5 / 12.1, 128 13.5 / 12.8, 512 19.3 / 20.5; without either of 300, 8 / 12: 64 chains 12.9 / 10.6, 512
+// 22.2 / 17.0 (normalised, 4 / 12: 13.3 / 13.1, 22.4 / 24.2); gradients with beta of 100, 3 or 2 / 4: 15 chains 18.1 / 13.9,
+// 512 20.8 / 17.1.
 // fp32 holds half as many values per lane and token: prompts of 128 chains 234 / 201 / 199 with 2 / 4 / 8, gradients 403 /
 // 377 with 2 / 4, and the longer ones win with fewer chains too.
-int glr_tokens(bool bf16_io, bool gradients, bool beta, int nchain) {
+int glr_tokens(bool bf16_io, bool gradients, bool beta, bool norm, int nchain, int len) {
   if (!bf16_io) return gradients ? 4 : 8;
-  if (gradients) return !beta || nchain <= 8 ? 4 : (nchain < 64 ? 3 : 2);
-  return nchain <= 8 ? 8 : (beta ? 4 : 6);
+  const bool longer = len >= 16384;
+  if (gradients) return !beta || nchain <= 8 || (len > 64 && len <= 128) ? 4 : (nchain < 64 ? 3 : 2);
+  if (beta) return nchain < 128 && (longer || (len > 128 && len <= 256)) ? 8 : 4;
+  if (norm) return longer ? 12 : 4;
+  return longer || (len > 256 && len <= 384) ? 12 : 8;
 }
 
-GlrGrid glr_grid(int B, int H, int len, int d, bool bf16_io, bool gradients, bool beta, int* tokens) {
+GlrGrid glr_grid(int B, int H, int len, int d, bool bf16_io, bool gradients, bool beta, bool norm, int* tokens) {
   GlrGrid n;
   n.nslab = (H * d + kSlab - 1) / kSlab;
   n.nchain = n.nslab * B;
-  *tokens = glr_tokens(bf16_io, gradients, beta, n.nchain);
+  *tokens = glr_tokens(bf16_io, gradients, beta, norm, n.nchain, len);
   const int run = kWaves * (bf16_io ? kSub<bf16> : kSub<float>) * *tokens;
   n.ntile = len > 0 ? (len + run - 1) / run : 1;
   n.spread = n.nchain >= 64 || (n.nchain % 8 == 0 && n.nchain > 0);
   n.blocks = n.spread ? (n.nchain + 7) / 8 * 8 : n.nchain;
+  n.place = false;
   return n;
 }
 
-template <typename T, bool GRADIENTS, int NT, bool BETA>
-hipError_t glr_launch(GlrArgs a, const GlrGrid& n, int polls, hipStream_t stream) {
+template <typename T, bool GRADIENTS, int NT, bool BETA, bool NORM>
+hipError_t glr_launch(const GlrArgs& a, GlrGrid n, int polls, hipStream_t stream) {
   if (n.ntile > 1) {
     const long long words = (long long)n.nchain * n.ntile * kWords / 4;
     // a chain's last tile may write h_T before another one has read h0: in place, the tiles read a copy
-    const bool place = !GRADIENTS && a.h0 && a.h0 == a.h_T;
-    const long long copy = place ? (long long)a.B * a.H * a.d / 4 : 0;
-    hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((words + copy + 1023) / 1024)), dim3(256), 0, stream,
-                       static_cast<u32x4*>(a.ws), words, a.h0, copy);
-    if (place) a.h0 = reinterpret_cast<const float*>(static_cast<u32x4*>(a.ws) + words);
+    n.place = !GRADIENTS && a.h0 && a.h0 == a.h_T;
+    hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((words + 1023) / 1024)), dim3(256), 0, stream,
+                       static_cast<u32x4*>(a.ws), words, n.place ? a.h0 : nullptr, n.nchain, n.nslab, a.H * a.d);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -751,14 +789,13 @@ hipError_t glr_launch(GlrArgs a, const GlrGrid& n, int polls, hipStream_t stream
   const dim3 grid((unsigned)((long long)n.blocks * n.ntile)), threads(64 * kWaves);
   // tiles of a chain that are under way together, and one more: about 1024 workgroups fit the device
   const int window = 1 + 1024 / n.nchain;
-  if constexpr (GRADIENTS) {
-    if (a.norm) hipLaunchKernelGGL((kda_glr_bwd_kernel<T, NT, kWaves, true, BETA>), grid, threads, 0, stream, a, n, window, polls);
-    else hipLaunchKernelGGL((kda_glr_bwd_kernel<T, NT, kWaves, false, BETA>), grid, threads, 0, stream, a, n, window, polls);
-  } else {
-    if (a.norm) hipLaunchKernelGGL((kda_glr_kernel<T, NT, kWaves, true, BETA>), grid, threads, 0, stream, a, n, window, polls);
-    else hipLaunchKernelGGL((kda_glr_kernel<T, NT, kWaves, false, BETA>), grid, threads, 0, stream, a, n, window, polls);
-  }
+  if constexpr (GRADIENTS) hipLaunchKernelGGL((kda_glr_bwd_kernel<T, NT, kWaves, NORM, BETA>), grid, threads, 0, stream, a, n, window, polls);
+  else hipLaunchKernelGGL((kda_glr_kernel<T, NT, kWaves, NORM, BETA>), grid, threads, 0, stream, a, n, window, polls);
   return hipGetLastError();
+}
+template <typename T, bool GRADIENTS, int NT, bool BETA>
+hipError_t glr_launch(const GlrArgs& a, const GlrGrid& n, int polls, hipStream_t stream) {
+  return a.norm ? glr_launch<T, GRADIENTS, NT, BETA, true>(a, n, polls, stream) : glr_launch<T, GRADIENTS, NT, BETA, false>(a, n, polls, stream);
 }
 
 template <typename T>
@@ -773,12 +810,10 @@ hipError_t glr_step(const GlrArgs& a, hipStream_t stream) {
 
 size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients) {
   size_t most = 0;
-  for (int beta = 0; beta < 2; ++beta) {
+  for (int k = 0; k < 4; ++k) {
     int nt;
-    const GlrGrid n = glr_grid(B, H, T, d, bf16_io, gradients, beta != 0, &nt);
-    // (the words of the tiles, and for prompts a copy of h0)
-    const size_t words = (size_t)n.nchain * n.ntile * kWords + (gradients ? 0 : (size_t)B * H * d);
-    const size_t bytes = n.ntile > 1 ? words * sizeof(uint32_t) : 0;
+    const GlrGrid n = glr_grid(B, H, T, d, bf16_io, gradients, k & 1, k & 2, &nt);
+    const size_t bytes = n.ntile > 1 ? (size_t)n.nchain * n.ntile * kWords * sizeof(uint32_t) : 0;
     most = bytes > most ? bytes : most;
   }
   return most;
@@ -794,10 +829,11 @@ hipError_t launch_glr(const GlrArgs& args, bool bf16_io, int polls, hipStream_t 
   GlrArgs a = args;
   a.lines = glr_lines(a, a.o, a.os, bf16_io);
   int nt;
-  const GlrGrid n = glr_grid(a.B, a.H, a.T, a.d, bf16_io, false, a.beta != nullptr, &nt);
+  const GlrGrid n = glr_grid(a.B, a.H, a.T, a.d, bf16_io, false, a.beta != nullptr, a.norm, &nt);
   if (!bf16_io) return a.beta ? glr_launch<float, false, 8, true>(a, n, polls, stream) : glr_launch<float, false, 8, false>(a, n, polls, stream);
   if (a.beta) return nt == 8 ? glr_launch<bf16, false, 8, true>(a, n, polls, stream) : glr_launch<bf16, false, 4, true>(a, n, polls, stream);
-  return nt == 8 ? glr_launch<bf16, false, 8, false>(a, n, polls, stream) : glr_launch<bf16, false, 6, false>(a, n, polls, stream);
+  if (nt == 12) return glr_launch<bf16, false, 12, false>(a, n, polls, stream);
+  return a.norm ? glr_launch<bf16, false, 4, false, true>(a, n, polls, stream) : glr_launch<bf16, false, 8, false, false>(a, n, polls, stream);
 }
 
 hipError_t launch_glr_backward(const GlrArgs& args, bool bf16_io, int polls, hipStream_t stream) {
@@ -805,7 +841,7 @@ hipError_t launch_glr_backward(const GlrArgs& args, bool bf16_io, int polls, hip
   a.lines = glr_lines(a, a.dx, a.dxs, bf16_io) && glr_lines(a, a.dla, a.dls, bf16_io) &&
             (!a.dbeta || glr_lines(a, a.dbeta, a.dbs, bf16_io));
   int nt;
-  const GlrGrid n = glr_grid(a.B, a.H, a.T, a.d, bf16_io, true, a.beta != nullptr, &nt);
+  const GlrGrid n = glr_grid(a.B, a.H, a.T, a.d, bf16_io, true, a.beta != nullptr, a.norm, &nt);
   if (!bf16_io) return a.beta ? glr_launch<float, true, 4, true>(a, n, polls, stream) : glr_launch<float, true, 4, false>(a, n, polls, stream);
   if (!a.beta) return glr_launch<bf16, true, 4, false>(a, n, polls, stream);
   if (nt == 2) return glr_launch<bf16, true, 2, true>(a, n, polls, stream);

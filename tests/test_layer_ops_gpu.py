@@ -97,6 +97,11 @@ GLR = [  # B, H, T, d, dtype, beta, h0, normalise, token-major, rate
     (1, 5, 517, 72, "bf16", False, True, False, True, 1.0),
     (5, 1, 16, 256, "bf16", True, True, True, False, 0.3),
     (1, 1, 300, 24, "f32", False, False, False, True, 30.0),
+    (2, 3, 256, 40, "bf16", True, True, True, True, 0.1),
+    (2, 3, 129, 40, "bf16", True, True, False, True, 0.1),
+    (2, 3, 384, 40, "bf16", False, True, False, True, 0.1),
+    (2, 3, 385, 40, "bf16", False, True, False, True, 0.1),
+    (9, 3, 128, 40, "bf16", True, True, True, False, 0.1),
 ]
 
 
@@ -125,6 +130,25 @@ def test_glr_lens(lens, dt):
     torch.cuda.synchronize()
     ref = check_glr(c, True, dt, o, h, lens)
     assert (o.cpu().double()[torch.isnan(ref)] == 7.0).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("beta", [True, False])
+@pytest.mark.parametrize("norm", [True, False])
+def test_glr_long(norm, beta, dt):
+    """More than 16384 tokens, where the runs of tokens are longer; channels that end inside a slab, a ragged batch."""
+    T = 16384 + 777
+    lens = [T, 9001, 16384]
+    c = glr_case(3, 3, T, 24, dt, 77, beta=beta)
+    c["la"][:, :, 5000:5003] = -float("inf")
+    ln = torch.tensor(lens, dtype=torch.int32, device=dev())
+    args = [up(c[n]) for n in ("x", "la", "beta", "h0")]
+    o = torch.zeros(3, 3, T, 24, dtype=DT[dt], device=dev())
+    _, h = kda.glr_prefill(*args, normalise=norm, o=o, lens=ln)
+    got = kda.glr_backward(*args, o, up(c["dO"]), up(c["dh_T"]), normalise=norm, lens=ln)
+    torch.cuda.synchronize()
+    check_glr(c, norm, dt, o, h, lens)
+    check_glr_grads(got, c, o.cpu(), norm, dt, lens)
 
 
 def test_glr_no_tokens():
