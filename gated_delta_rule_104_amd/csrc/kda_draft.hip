@@ -10,9 +10,9 @@
 // there are many long ones.  A row is cut into chunks that fill the chip with few sequences too: one launch adds every
 // chunk up, a second one finds the chunk that holds the threshold and walks it alone.  Short rows
 // take one launch, a workgroup each, since what two launches cost the host is more than they save.
-// fp32, 4 drafts: 256 rows of 128K, greedy drafts accepted in part, 42 us (sums 40 us at HBM's rate, the
-// choice 6.6); 1 row of 50K 14.3 us, 4.2 + 4.6 of it kernels; 64 rows of 20K 11 us, bounded by the host's launch.
-// Choosing 64 states of 32 x 128 x 128 out of 5 takes 51 us for 268 MB, 5.2 TB/s.
+// fp32, 4 drafts: 256 rows of 128K 39-41 us for 188 MB (the sums at HBM's rate, then the choice, 6); 1 row of 50K 15 us, 4.4 + 4.5
+// of it kernels; 64 rows of 20K 11 us, bounded by the host's launch.
+// Choosing 64 states of 32 x 128 x 128 out of 5 takes 51-54 us for 268 MB, 5.0-5.2 TB/s.
 #include "kda_ops.hpp"
 #include "kda_vec.hpp"
 
@@ -74,24 +74,25 @@ struct Rows {
   }
 };
 
-// 16 bytes at any element's address.
-template <typename T>
+// 16 bytes at any element's address; ONCE: past the caches (256 rows of 128K 43.7 -> 41.4 us).
+template <typename T, bool ONCE>
 __device__ __forceinline__ Row<T> load_any(const T* p) {
-  u32x4 w;
-  __builtin_memcpy(&w, p, 16);
+  using Any = uint32_t __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+  const Any* at = reinterpret_cast<const Any*>(p);
+  const u32x4 w = ONCE ? __builtin_nontemporal_load(at) : *at;
   return unpack<T>(w);
 }
 
 // A lane's vector of both rows: what is left of p behind q, and p, in fp64; NaN and what is negative
 // count as no mass, an infinity as the largest number.  The clamps are in fp32, whose instructions are
 // cheaper; p - min(q, p) of fp32 numbers is exact in fp64 unless one is 2^28 times the other.
-template <typename T>
+template <typename T, bool ONCE>
 __device__ __forceinline__ void masses(const Rows<T>& r, int i0, int end, double* w, double* whole) {
   constexpr int V = kVec<T>;
   Row<T> p, q;
   if (i0 + V <= end) {
-    p = load_any(r.p + i0);
-    if (r.q) q = load_any(r.q + i0);
+    p = load_any<T, ONCE>(r.p + i0);
+    if (r.q) q = load_any<T, ONCE>(r.q + i0);
   } else {
 #pragma unroll
     for (int c = 0; c < V; ++c) {
@@ -115,15 +116,15 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// A thread's share of the sums over [c0, end), THREADS of them together.
-template <typename T, int THREADS, int DEEP>
+// A thread's share of the sums over [c0, end), THREADS of them together, DEEP vectors at a time.
+template <typename T, int THREADS, int DEEP, bool ONCE>
 __device__ __forceinline__ void add_up(const Rows<T>& r, int c0, int end, int thread, double* left, double* whole) {
   constexpr int V = kVec<T>;
   double s = 0.0, t = 0.0;
 #pragma unroll DEEP
   for (int i = c0 + thread * V; i < end; i += THREADS * V) {
     double w[V], z[V];
-    masses<T>(r, i, end, w, z);
+    masses<T, ONCE>(r, i, end, w, z);
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       s += w[c];
@@ -156,7 +157,9 @@ __global__ __launch_bounds__(256) void kda_verify_sum_kernel(VerifyArgs a, int n
   const Rows<T> r(a, n, choice.accepted, choice.token, choice.accepted < choice.count);
   const int c0 = chunk * kChunk;
   double s, whole;
-  add_up<T, 256, 4>(r, c0, min(c0 + kChunk, a.V), threadIdx.x, &s, &whole);
+  // (more vectors at a time take registers, and with them waves: 1024 rows of 50257 in bf16 70, 62, 56 us with 4, 2, 1,
+  // 256 of 128K in fp32 41.4, 41.2, 41.8)
+  add_up<T, 256, sizeof(T) == 2 ? 1 : 2, true>(r, c0, min(c0 + kChunk, a.V), threadIdx.x, &s, &whole);
   s = wave_sum(s);
   whole = wave_sum(whole);
   if ((threadIdx.x & 63) == 0) {
@@ -234,7 +237,7 @@ __device__ __forceinline__ void pick(const VerifyArgs& a, int n, int4 choice, fl
       double z[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) w[i + k] = 0.0;
-      if (mine + i < end) masses<T>(r, mine + i, end, w + i, z);
+      if (mine + i < end) masses<T, false>(r, mine + i, end, w + i, z);
     }
 #pragma unroll
     for (int i = 0; i < OWN; ++i) s += w[i];
@@ -286,7 +289,7 @@ __global__ __launch_bounds__(1024) void kda_verify_row_kernel(VerifyArgs a, int 
     if (wave < nchunk) {
       const Rows<T> r(a, n, choice.accepted, choice.token, refused);
       double left, whole;
-      add_up<T, 64, 4>(r, wave * size, min((wave + 1) * size, a.V), lane, &left, &whole);
+      add_up<T, 64, 1, false>(r, wave * size, min((wave + 1) * size, a.V), lane, &left, &whole);
       left = wave_sum(left);
       if (lane == 0) sums[wave] = double2{left, left};
     }

@@ -4,6 +4,13 @@
 //     lam_t = dO_t + a_{t+1} lam_{t+1} (+ dh_T at the end),   dx = n beta lam,   dbeta = n x lam,
 //     dlog_alpha = a h_{t-1} lam - (a^2 / n) beta x lam,   dh0 = a_1 lam_1,
 // where h_{t-1} is read back from the forward pass's outputs.
+//
+// Nothing but the inputs and outputs has to move, so HBM bounds long calls: four prompts of 8192 tokens, 4096 channels, bf16,
+// with beta and normalised, 198-203 us for 1.07 GB (5.3-5.4 TB/s); one of 65536 tokens, 2560 channels, without either 185-190
+// for 1.01 GB; the gradients of the former 387-430, by card, for 2.15 GB.  A chain of products with a decay is short: 40% of a
+// SIMD's cycles go to vector instructions.  What costs is that every token waits for the one before it; the
+// relay below keeps that to a few microseconds a tile and hides it behind other tiles.  One token of 256 sequences
+// x 4096 channels: 7.4 us, 5.4 of them the kernel.  Short prompts are bounded by their launches: 9 us with one, 13 with two.
 #include <cstdio>
 #include <mutex>
 #include <type_traits>
