@@ -7,9 +7,9 @@
 //
 // Nothing but the inputs and outputs has to move, so HBM bounds long calls: four prompts of 8192 tokens, 4096 channels, bf16,
 // with beta and normalised, 198-203 us for 1.07 GB (5.3-5.4 TB/s); one of 65536 tokens, 2560 channels, without either 185-190
-// for 1.01 GB; the gradients of the former 387-430, by card, for 2.15 GB.  A chain of products with a decay is short: 40% of a
-// SIMD's cycles go to vector instructions.  What costs is that every token waits for the one before it; the
-// relay below keeps that to a few microseconds a tile and hides it behind other tiles.  One token of 256 sequences
+// for 1.01 GB; the gradients of the former 387-430, by card, for 2.15 GB.  Vector instructions, about 42 a value with
+// its share of the relay in the first and the last of these, take 70% of the SIMDs' cycles beside that.  Every token
+// waits for the one before it; the relay below keeps that to a few microseconds a tile, behind other tiles' loads.  One token of 256 sequences
 // x 4096 channels: 7.4 us, 5.4 of them the kernel.  Short prompts are bounded by their launches: 9 us with one, 13 with two.
 #include <cstdio>
 #include <mutex>
