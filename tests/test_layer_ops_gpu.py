@@ -506,6 +506,22 @@ def test_draft_verify_borders(V):
     assert out[7].tolist() == [-1, -1, -1] and out[2].tolist() == [0, 0, V - 1] and int(a[9]) == 2
 
 
+@pytest.mark.parametrize("V", [300, 40000])
+def test_draft_verify_infinities(V):
+    """An infinite probability counts as the largest number: the next token is that one, unless the draft's is too."""
+    p, q = torch.full((3, 2, V), 1.0 / V), torch.zeros(3, 1, V)
+    p[:, 0, 7] = float("inf")
+    p[:, 0, 0] = 0.0
+    q[1, 0, 7], q[2, 0, 7] = 0.5, float("inf")
+    tok = torch.zeros(3, 1, dtype=torch.int32)  # refused: its probability is 0
+    u = torch.full((3, 2), 0.5)
+    a, out = kda.draft_verify(*map(up, (p, q, tok, u)))
+    torch.cuda.synchronize()
+    assert not a.any() and out[:2, 0].tolist() == [7, 7] and (out[:, 1] == -1).all()
+    # (behind token 7 the others' V - 2 equal masses: half of them)
+    assert abs(out[2, 0].item() - V // 2) <= 1 and out[2, 0] != 7
+
+
 @pytest.mark.parametrize("N,ntok,H,dk,dv", [(1, 1, 1, 2, 2), (5, 3, 2, 64, 64), (7, 4, 3, 128, 64), (3, 2, 1, 6, 10)])
 def test_state_commit(N, ntok, H, dk, dv):
     g = gen(N)
