@@ -6,8 +6,8 @@
 // where h_{t-1} is read back from the forward pass's outputs.
 //
 // Nothing but the inputs and outputs has to move, so HBM bounds long calls: four prompts of 8192 tokens, 4096 channels, bf16,
-// with beta and normalised, 198-203 us for 1.07 GB (5.3-5.4 TB/s); one of 65536 tokens, 2560 channels, without either 185-190
-// for 1.01 GB; the gradients of the former 387-430, by card, for 2.15 GB.  Vector instructions, about 42 a value with
+// with beta and normalised, 198-203 us for 1.07 GB (5.3-5.4 TB/s); one of 65536 tokens, 2560 channels, without either 187-193
+// for 1.01 GB; the gradients of the former 387-436, by card and place in memory, for 2.15 GB.  Vector instructions, about 42 a value with
 // its share of the relay in the first and the last of these, take 70% of the SIMDs' cycles beside that.  Every token
 // waits for the one before it; the relay below keeps that to a few microseconds a tile, behind other tiles' loads.  One token of 256 sequences
 // x 4096 channels: 7.4 us, 5.4 of them the kernel.  Short prompts are bounded by their launches: 9 us with one, 13 with two.
@@ -158,21 +158,23 @@ __device__ __forceinline__ Row<T> ones() {
 //     them is e^l h + z.  They are joined over the lanes and waves in LDS, lane = channel;
 //   - the tile publishes its (l, z), looks back at the tiles before it in the sequence for the nearest one
 //     whose end state is known, goes forwards from there through the (l, z) in between, and publishes its
-//     own end state.  A state is always carried through tile after tile in order, so that it has the
-//     same bits however far a tile had to look;
+//     own end state as (-inf, end): a tile that clears what comes in and ends in that state.  A state is always
+//     carried through tile after tile in order, so that it has the same bits however far a tile had to look;
 //   - every lane's first state follows, and its tokens are walked again from registers.
-// What is published are single 32-bit words that are valid once they are not the empty one, so no order
+// What is published are single 64-bit words that are valid once they are not the empty one, so no order
 // between them is needed.  Waiting is bounded: a tile whose predecessors do not answer walks the
 // sequence from its start by itself, so the call ends whatever order workgroups run in.
 
 constexpr int kSlab = 64;                // channels of a tile
-constexpr int kWords = 3 * kSlab;        // of a tile: l, z and the end state of each channel
-constexpr uint32_t kEmpty = 0xffffffffu;  // (a NaN that no published value has)
+constexpr uint32_t kEmpty = 0xffffffffu;    // in the place of l (a NaN that no published value has)
+constexpr uint32_t kCleared = 0xff800000u;  // -inf
 
-__device__ __forceinline__ void publish(uint32_t* p, float v) {
-  __hip_atomic_store(p, v == v ? __float_as_uint(v) : 0x7fc00000u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// A channel's word of a tile: l below, z above.
+__device__ __forceinline__ void publish(uint64_t* p, float l, float z) {
+  const uint32_t low = l == l ? __float_as_uint(l) : 0x7fc00000u;
+  __hip_atomic_store(p, (uint64_t)__float_as_uint(z) << 32 | low, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ uint32_t published(const uint32_t* p) {
+__device__ __forceinline__ uint64_t published(const uint64_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
@@ -192,7 +194,6 @@ struct RelayMem {
   alignas(16) State<T> z[SUBS][kSlab];  // end states from zero; later the states in front
   float we[WAVES][kSlab], wl[WAVES][kSlab], h[kSlab];
   State<T> wz[WAVES][kSlab];
-  float ends[WINDOW][kSlab];
   uint32_t sums_there[WAVES], end_there[WAVES];
 };
 
@@ -200,31 +201,27 @@ struct RelayMem {
 // not answer.  words: the chain's tile 0, hop words to the next one (tile 0 publishes its end state alone);
 // window: how many tiles to look at, shared out over the waves, which have nothing else to do.
 template <typename T, int WAVES>
-__device__ __forceinline__ bool look_back(RelayMem<T, WAVES>& m, const uint32_t* words, long long hop, int s, int window,
+__device__ __forceinline__ bool look_back(RelayMem<T, WAVES>& m, const uint64_t* words, long long hop, int s, int window,
                                           int polls, float* state) {
   constexpr int W = RelayMem<T, WAVES>::WINDOW, OWN = W / WAVES;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int poll = 0; poll < polls; ++poll) {
-    uint32_t p[OWN], l[OWN], z[OWN], sums = 0u, ends = 0u;
+    uint32_t sums = 0u, ends = 0u;
+    uint64_t word[OWN];
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
       const int i = k * WAVES + w;
-      p[k] = l[k] = z[k] = kEmpty;
-      if (i < window && i < s) {
-        const uint32_t* q = words + (long long)(s - 1 - i) * hop + lane;
-        p[k] = published(q + 2 * kSlab);
-        l[k] = published(q);
-        z[k] = published(q + kSlab);
-      }
+      word[k] = kEmpty;
+      if (i < window && i < s) word[k] = published(words + (long long)(s - 1 - i) * hop + lane);
     }
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
       const int i = k * WAVES + w;
-      m.past[0][i][lane] = decay_of<T>(__uint_as_float(l[k]));
-      m.past[1][i][lane] = __uint_as_float(z[k]);
-      m.ends[i][lane] = __uint_as_float(p[k]);
-      if (__ballot(l[k] == kEmpty || z[k] == kEmpty) == 0ull) sums |= 1u << i;
-      if (__ballot(p[k] == kEmpty) == 0ull) ends |= 1u << i;
+      const uint32_t l = (uint32_t)word[k];
+      if (__ballot(l == kEmpty) == 0ull) sums |= 1u << i;
+      if (__ballot(l != kCleared) == 0ull) ends |= 1u << i;
+      m.past[0][i][lane] = decay_of<T>(__uint_as_float(l));
+      m.past[1][i][lane] = __uint_as_float((uint32_t)(word[k] >> 32));
     }
     if (lane == 0) {
       m.sums_there[w] = sums;
@@ -241,7 +238,7 @@ __device__ __forceinline__ bool look_back(RelayMem<T, WAVES>& m, const uint32_t*
     const int found = __ffs(ends) - 1;
     if (found >= 0 && (~sums & ((1u << found) - 1u)) == 0u) {
       if (w == 0) {
-        float h = m.ends[found][lane];
+        float h = m.past[1][found][lane];
         for (int i = found - 1; i >= 0; --i) h = advance(m.past[0][i][lane], h, m.past[1][i][lane]);
         *state = h;
       }
@@ -281,7 +278,7 @@ __device__ __forceinline__ void put(A* p, const A (&v)[N]) {
 // (lane = channel), or null.
 template <typename T, int WAVES, typename Self>
 __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kVec<T>], const State<T> (&z)[kVec<T>],
-                                      State<T> (&h)[kVec<T>], uint32_t* words, long long hop, int s, bool last, float first,
+                                      State<T> (&h)[kVec<T>], uint64_t* words, long long hop, int s, bool last, float first,
                                       int window, int polls, float* end, Self self) {
   constexpr int V = kVec<T>, LPR = kLpr<T>, SUB = kSub<T>;
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = w * SUB + lane / LPR, c0 = lane % LPR * V;
@@ -306,7 +303,7 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
   __syncthreads();
   float lt = 0.f, front = first;
   State<T> zt = 0;
-  uint32_t* own = words + s * hop + lane;
+  uint64_t* own = words + s * hop + lane;
   if (w == 0) {
 #pragma unroll
     for (int u = 0; u < WAVES; ++u) {
@@ -314,16 +311,13 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
       zt = advance(e, zt, m.wz[u][lane]);
       lt = add_log(lt, m.wl[u][lane], __float_as_uint(e) == 0u);
     }
-    if (s > 0 && !last) {
-      publish(own, lt);
-      publish(own + kSlab, (float)zt);
-    }
+    if (s > 0 && !last) publish(own, lt, (float)zt);
   }
   const bool known = s == 0 || look_back<T, WAVES>(m, words, hop, s, window, polls, &front);
   if (w == 0) {
     if (!known) front = self();
     const float out = advance(decay_of<T>(lt), front, (float)zt);
-    if (!last) publish(own + 2 * kSlab, out);
+    if (!last) publish(own, -__builtin_inff(), out);
     else if (end) *end = out;
     m.h[lane] = front;
   }
@@ -347,7 +341,7 @@ __device__ __forceinline__ void relay(RelayMem<T, WAVES>& m, const float (&l)[kV
 struct GlrGrid {
   int nslab, ntile, nchain, blocks;  // blocks: workgroups per run of all chains
   bool spread;
-  bool place;  // the first states are in the words
+  bool place;  // the first states are in the words of the last tiles
 };
 struct GlrTile {
   int b, slab, s, len, ntile;  // sequence, slab, number in the chain, tokens and tiles of the sequence
@@ -408,8 +402,8 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
   const T* beta = BETA ? static_cast<const T*>(a.beta) + g.b * a.bs.b + hd * a.bs.h + j0 : nullptr;
   const int cl = g.slab * kSlab + lane;  // lane = channel
   const long long at = (long long)g.b * C + cl;
-  uint32_t* words = static_cast<uint32_t*>(a.ws) + (long long)g.chain * kWords;
-  const float first = a.h0 && cl < C ? (n.place ? __uint_as_float(words[lane]) : a.h0[at]) : 0.f;
+  uint64_t* words = static_cast<uint64_t*>(a.ws) + (long long)g.chain * kSlab;
+  const float first = a.h0 && cl < C ? (n.place ? __uint_as_float((uint32_t)words[(long long)(n.ntile - 1) * n.nchain * kSlab + lane]) : a.h0[at]) : 0.f;
   if (g.len == 0) {
     if (threadIdx.x < 64 && cl < C) a.h_T[at] = first;
     return;
@@ -488,7 +482,7 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
     }
     return (float)run;
   };
-  relay<T, WAVES>(mem, l, z, h, words, (long long)n.nchain * kWords, g.s, g.s == g.ntile - 1, first, window, polls,
+  relay<T, WAVES>(mem, l, z, h, words, (long long)n.nchain * kSlab, g.s, g.s == g.ntile - 1, first, window, polls,
                   cl < C ? a.h_T + at : nullptr, self);
   if (!on) return;
   if constexpr (sizeof(T) == 4) {  // (what was kept in 64 bits)
@@ -520,17 +514,22 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, false, BETA>)) void k
   }
 }
 
-// Empties the words of a call's tiles, 64 bytes a thread.  With h0 the first states, of C channels a sequence, are put
-// where a chain's first tile would have the sums of its logs, which nobody asks it for.
+// Empties the n / 2 words of a call's tiles, 64 bytes a thread.  With h0 the first states, of C channels a sequence, are
+// put into the words of the chains' last tiles, which publish nothing.
 __global__ __launch_bounds__(256) void kda_glr_clear_kernel(u32x4* words, long long n, const float* h0, int nchain, int nslab, int C) {
+  const long long last = n - (long long)nchain * (kSlab / 2);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const long long i = (long long)blockIdx.x * 1024 + u * 256 + threadIdx.x;
     if (i >= n) continue;
     u32x4 v{kEmpty, kEmpty, kEmpty, kEmpty};
-    if (h0 && i < (long long)nchain * (kWords / 4)) {
-      const int chain = (int)(i / (kWords / 4)), word = (int)(i % (kWords / 4)) * 4, c = chain % nslab * kSlab + word;
-      if (word < kSlab && c < C) v = ld16(h0 + (long long)(chain / nslab) * C + c);
+    if (h0 && i >= last) {
+      const int chain = (int)((i - last) / (kSlab / 2)), c = chain % nslab * kSlab + (int)((i - last) % (kSlab / 2)) * 2;
+      if (c < C) {  // (C is even)
+        const float* h = h0 + (long long)(chain / nslab) * C + c;
+        v[0] = __float_as_uint(h[0]);
+        v[2] = __float_as_uint(h[1]);
+      }
     }
     words[i] = v;
   }
@@ -657,8 +656,8 @@ __global__ __launch_bounds__(64 * WAVES, (kResident<T, NT, true, BETA>)) void kd
       run = advance<State<T>>(decay_of<T>(to_f32(pl[t * a.ls.t])), run + to_f32(pg[t * a.dos.t]), 0);
     return (float)run;
   };
-  uint32_t* words = static_cast<uint32_t*>(a.ws) + (long long)g.chain * kWords;
-  relay<T, WAVES>(mem, l, z, mu, words, (long long)n.nchain * kWords, g.s, g.s == g.ntile - 1, first, window, polls,
+  uint64_t* words = static_cast<uint64_t*>(a.ws) + (long long)g.chain * kSlab;
+  relay<T, WAVES>(mem, l, z, mu, words, (long long)n.nchain * kSlab, g.s, g.s == g.ntile - 1, first, window, polls,
                   a.dh0 && cl < C ? a.dh0 + at + cl : nullptr, self);
   if (!on) return;
   forget(rl);
@@ -782,7 +781,7 @@ GlrGrid glr_grid(int B, int H, int len, int d, bool bf16_io, bool gradients, boo
 template <typename T, bool GRADIENTS, int NT, bool BETA, bool NORM>
 hipError_t glr_launch(const GlrArgs& a, GlrGrid n, int polls, hipStream_t stream) {
   if (n.ntile > 1) {
-    const long long words = (long long)n.nchain * n.ntile * kWords / 4;
+    const long long words = (long long)n.nchain * n.ntile * (kSlab / 2);  // 16 bytes each
     // a chain's last tile may write h_T before another one has read h0: in place, the tiles read a copy
     n.place = !GRADIENTS && a.h0 && a.h0 == a.h_T;
     hipLaunchKernelGGL(kda_glr_clear_kernel, dim3((unsigned)((words + 1023) / 1024)), dim3(256), 0, stream,
@@ -820,7 +819,7 @@ size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients) {
   for (int k = 0; k < 4; ++k) {
     int nt;
     const GlrGrid n = glr_grid(B, H, T, d, bf16_io, gradients, k & 1, k & 2, &nt);
-    const size_t bytes = n.ntile > 1 ? (size_t)n.nchain * n.ntile * kWords * sizeof(uint32_t) : 0;
+    const size_t bytes = n.ntile > 1 ? (size_t)n.nchain * n.ntile * kSlab * sizeof(uint64_t) : 0;
     most = bytes > most ? bytes : most;
   }
   return most;

@@ -56,9 +56,9 @@ def test_glr_prefill_refusals(lib):
 
 def test_glr_workspaces(lib):
     ws, bw = lib.kda_glr_prefill_workspace_bytes, lib.kda_glr_backward_workspace_bytes
-    # one tile of tokens needs none; each tile of 64 channels else takes three words a channel
-    assert ws(4, 32, 100, 128, BF16) == 0 and ws(4, 32, 8192, 128, BF16) == 4 * 64 * (8192 // 128) * 3 * 64 * 4
-    assert bw(4, 32, 8192, 128, BF16) == 4 * 64 * (8192 // 64) * 3 * 64 * 4
+    # one tile of tokens needs none; each tile of 64 channels else takes a word of 64 bits a channel
+    assert ws(4, 32, 100, 128, BF16) == 0 and ws(4, 32, 8192, 128, BF16) == 4 * 64 * (8192 // 128) * 64 * 8
+    assert bw(4, 32, 8192, 128, BF16) == 4 * 64 * (8192 // 64) * 64 * 8
     for f in (ws, bw):
         assert f(0, 1, 100, 64, BF16) == 0 and f(1, 1, 0, 64, BF16) == 0 and f(1, 1, 1000, 12, BF16) == 0 and f(1, 1, 100, 64, 7) == 0
         assert f(1, 1, 1000, 8, F32) > 0
