@@ -523,7 +523,9 @@ kda_status kda_glr_backward(const void* x, const void* log_alpha, const void* be
  *                  strides are multiples of 8 (bf16) or 4 (fp32)
  *   scales       : of the 8-bit outputs, any element alignment of their own type:
  *                  ROWS    [B, H, T] fp32, the row's largest |y| / 127 (int8) or 448 (e4m3), at
- *                          least 2^-126; NaN marks a row that held an infinity or NaN
+ *                          least 2^-126; NaN marks a row that held an infinity or NaN.  Values
+ *                          are y 127 (448) / largest |y|, before the scale's own rounding; of
+ *                          bf16 rows without a gate every one is the nearest
  *                  BLOCKS  [B, H, T, d / 32] bytes (strides, contiguous rows of d / 32),
  *                          d a multiple of 32: exponent + 127 of a power of two for each 32
  *                          values, chosen and marked as in the quantised state cache above

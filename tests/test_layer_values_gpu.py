@@ -1,0 +1,91 @@
+"""GPU tests of values that lie on borders or far outside the ordinary."""
+import pytest
+import torch
+
+import gated_delta_rule_104_amd as kda
+import layer_oracle as orc
+from test_layer_ops_gpu import gen, norm_case, summed, up
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------- 8-bit rows
+def nearest(q, fmt):
+    """fp64 values to the nearest of the format's, ties to even (all inside its range)."""
+    if fmt == "int8":
+        return q.round()
+    step = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 3)
+    return (q / step).round() * step
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("B,H,T,d,weight", [(1, 1, 64, 4096, True), (3, 2, 50, 64, False), (2, 1, 9, 1000, True), (1, 1, 5, 32768, True)])
+def test_quantised_rows_round_to_nearest_even(B, H, T, d, weight, fmt):
+    """bf16 rows without a gate: value = p L / m with p = s w of 16 bits, m the row's largest and L = 448 or 127, whatever
+    the row's factor is.  A border k between two 8-bit values has at most 8 bits (e4m3: 5), and p L = k m or the two, as
+    whole numbers, differ by 1 at least: 1 / (k m) > 2^-24 of k, with k below 2^8 and m below 2^16.  A quotient of fp32 is
+    then on the same side of it as the exact one, or equal to it: every value can be rounded exactly, ties to even."""
+    top = 448 if fmt == "e4m3" else 127
+    c = norm_case(B, H, T, d, "bf16", d, True, False)
+    s = summed(c)
+    # half of the rows: a largest value of L and others on borders, times a power of two
+    g = gen(d + 1)
+    ties = nearest(torch.rand(B, H, T, d, generator=g, dtype=torch.float64) * (top - 20), fmt)
+    half = 0.5 if fmt == "int8" else torch.exp2(torch.floor(torch.log2(ties.clamp(min=2.0 ** -6))) - 4)
+    ties = (ties + half) * torch.where(torch.rand(B, H, T, d, generator=g) < 0.5, -1.0, 1.0)
+    ties[..., 3] = top
+    odd = torch.arange(T) % 2 == 1
+    s[:, :, odd] = (ties * 0.125).to(torch.bfloat16)[:, :, odd]
+    w = c["w"] if weight else None
+    if weight:  # (powers of two keep the borders, and none above 1 the largest value)
+        w = w.clamp(max=1)
+        w[: d // 2] = torch.tensor([1.0, 0.5, 0.25, 1.0]).to(torch.bfloat16).repeat(d // 8)
+    p = s.double() * (w.double() if weight else 1.0)
+    ref = nearest(p * top / p.abs().amax(-1, keepdim=True), fmt)
+    v, sc = kda.rms_norm_quant(up(s), up(w), fmt=fmt, scales="row")
+    torch.cuda.synchronize()
+    wrong = (v.cpu().double() != ref)
+    assert not wrong.any(), (int(wrong.sum()), wrong.numel())
+    want = orc.rms_norm(s, w).abs().amax(-1) / top
+    assert ((sc.cpu().double() - want).abs() <= 2.0 ** -18 * want).all()
+
+
+def test_quantised_rows_at_the_ends_of_fp32():
+    """Rows whose products, or whose factor, are near the ends of fp32's range; the smallest scale; zeros."""
+    d = 64
+    x = torch.rand(1, 1, 9, d, generator=gen(1)) + 0.5
+    scale = torch.tensor([1e18, 1e-18, 1e-30, 3e-39, 1.0, 1.0, 1.0, 0.0, 1e18])
+    x = x * scale[:, None]
+    for f, eps in ((1.0, 1e-6), (1.0, 0.0), (1e19, 1e-6), (1e-30, 1e-6), (1e-44, 1e-6)):
+        w = torch.full((d,), f)
+        for fmt, top in (("e4m3", 448), ("int8", 127)):
+            v, sc = kda.rms_norm_quant(up(x), up(w), fmt=fmt, scales="row", eps=eps)
+            torch.cuda.synchronize()
+            sums = x.square().sum(-1)
+            ok = (sums > 1e-30) if eps == 0.0 else torch.ones_like(sums, dtype=torch.bool)  # (squares below fp32's range are lost)
+            p = x.double() * w.double()
+            ok &= p.abs().amax(-1) < 3e38
+            ref = orc.rms_norm(x, w, eps=eps)
+            s = sc.cpu().double()[..., None]
+            assert torch.isfinite(s[ok]).all() and (s[ok] >= 2.0 ** -126).all()
+            got = v.cpu().double() * s
+            tol = s * (0.5 if fmt == "int8" else 2.0 ** -10)
+            tol = tol.expand_as(ref) if fmt == "int8" else torch.maximum(tol, 2.0 ** -4 * ref.abs())
+            # (products of fp32 below 2^-126 may be flushed; the factor takes them up by at most its own size)
+            r = 1 / torch.sqrt(x.double().square().mean(-1, keepdim=True) + eps)
+            off = (got - ref).abs() - (1.001 * tol + 2.0 ** -17 * ref.abs() + 2.0 ** -126 * (1 + r))
+            assert (off[ok] <= 0).all(), (f, eps, fmt)
+
+
+def test_quantised_rows_of_large_products():
+    """Rows whose values times weight and gate pass fp32's range, but not their norm's."""
+    d = 64
+    x = (torch.rand(1, 1, 3, d, generator=gen(2)) + 0.5) * torch.tensor([1e18, 1e10, 1.0])[:, None]
+    gate = torch.full((1, 1, 3, d), 1e25)
+    for fmt, top in (("e4m3", 448), ("int8", 127)):
+        v, sc = kda.rms_norm_quant(up(x), None, gate=up(gate), gate_activation="silu", fmt=fmt, scales="row")
+        torch.cuda.synchronize()
+        ref, s = orc.rms_norm(x) * 1e25, sc.cpu().double()[..., None]
+        assert (s / (ref.abs().amax(-1, keepdim=True) / top) - 1).abs().max() <= 2.0 ** -18
+        step = s * 0.5 if fmt == "int8" else 2.0 ** -4 * ref.abs()
+        assert ((v.cpu().double() * s - ref).abs() <= 1.001 * step + 2.0 ** -17 * ref.abs()).all()
