@@ -57,23 +57,24 @@ __device__ __forceinline__ void row_reduce(float (&v)[NR], float* red) {
 }
 
 // The gate's factor g(z) and its derivative, from sigma(z) and 1 - sigma(z) = e^-z sigma(z), which has all its
-// digits that way.  (e^-z is held below 2^126, where sigma is as good as zero.)
+// digits that way.  Below -88 or so e^-z is infinite and sigma zero; z is held to finite numbers where it meets
+// them, and e^-z to 2^126.  (sigma of a NaN is one.)  bf16's exponent is rounded, |z| 2^-24 of sigma; fp32's has that taken back.
 template <typename T>
 struct Gate {
   float g, dg;
   __device__ __forceinline__ Gate(float z, bool silu) {
     constexpr float c = -1.44269504088896340736f, c_low = -1.92596299e-8f;  // -log2(e) in two floats
+    constexpr float most = 3.402823466e38f;
     float e;
     if constexpr (sizeof(T) == 2) {
-      e = __builtin_amdgcn_exp2f(fminf(c * z, 126.f));
+      e = __builtin_amdgcn_exp2f(c * z);
     } else {  // the exponent's own rounding is taken back
-      const float y = fminf(fmaxf(z, -87.f), 87.f), t = c * y, r = fmaf(c_low, y, fmaf(c, y, -t));
-      e = __builtin_amdgcn_exp2f(t) * fmaf(r, 0.69314718055994530942f, 1.f);
+      const float y = __builtin_amdgcn_fmed3f(z, -128.f, 128.f), t = c * y, r = fmaf(c_low, y, fmaf(c, y, -t));
+      e = z == z ? __builtin_amdgcn_exp2f(t) * fmaf(r, 0.69314718055994530942f, 1.f) : z;
     }
-    const float s = __builtin_amdgcn_rcpf(1.f + e), one_less = e * s;
-    g = silu ? z * s : s;
-    dg = silu ? s * fmaf(z, one_less, 1.f) : s * one_less;
-    if (z != z) g = dg = z;  // (the bounds above turn a NaN into a number)
+    const float s = __builtin_amdgcn_rcpf(1.f + e), one_less = fminf(e, 0x1p126f) * s;
+    g = silu ? fmaxf(z, -most) * s : s;
+    dg = silu ? s * fmaf(__builtin_amdgcn_fmed3f(z, -most, most), one_less, 1.f) : s * one_less;
   }
 };
 

@@ -531,7 +531,9 @@ kda_status kda_glr_backward(const void* x, const void* log_alpha, const void* be
  *                          values, chosen and marked as in the quantised state cache above
  *                  values are rounded to nearest even, and 0 where marked
  * Sums are fp32, as is the factor they give: a row whose squares add up to more than
- * 3.4e38 becomes zeros, and a row of zeros with eps = 0 NaN.
+ * 3.4e38 becomes zeros, and a row of zeros with eps = 0 NaN (one whose squares are below
+ * fp32's range infinities).  act of a gate z is off by 2^-21 of itself, with bf16 gates
+ * (where y has 8 bits, or an 8-bit value's 4 to 7) by |z| 2^-24 more; below -87 it is 0.
  */
 typedef enum { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 } kda_gate;
 typedef enum {

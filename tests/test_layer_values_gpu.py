@@ -4,7 +4,7 @@ import torch
 
 import gated_delta_rule_104_amd as kda
 import layer_oracle as orc
-from test_layer_ops_gpu import gen, norm_case, summed, up
+from test_layer_ops_gpu import DT, HALF, gen, norm_case, summed, up, within
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,52 @@ def test_quantised_rows_of_large_products():
         assert (s / (ref.abs().amax(-1, keepdim=True) / top) - 1).abs().max() <= 2.0 ** -18
         step = s * 0.5 if fmt == "int8" else 2.0 ** -4 * ref.abs()
         assert ((v.cpu().double() * s - ref).abs() <= 1.001 * step + 2.0 ** -17 * ref.abs()).all()
+
+
+# ------------------------------------------------------------------ gates
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_silu_far_from_zero(dt):
+    """SiLU and its slope where the sigmoid has reached 0 or 1: z s(z) is 0 or z, the slope 0 or 1."""
+    inf = float("inf")
+    low, high = [-100.0, -200.0, -1e30, -1e37, -3e38, -inf], [100.0, 200.0, 1e30, 1e37, 3e38, inf]
+    z = torch.tensor((low + high) * 2 + [0.0, 1.0, -1.0, 5.0, -5.0, 2.0, -2.0, 0.5]).to(DT[dt])
+    d = z.numel()
+    c = norm_case(1, 1, 7, d, dt, 4, False, True)
+    c["gate"] = z.expand(1, 1, 7, d).contiguous()
+    y = kda.rms_norm(up(c["x"]), up(c["w"]), gate=up(c["gate"]), gate_activation="silu")
+    g = kda.rms_norm_backward(up(c["x"]), up(c["w"]), up(c["dy"]), gate=up(c["gate"]), gate_activation="silu")
+    torch.cuda.synchronize()
+    n = orc.rms_norm(c["x"], c["w"])
+    zz, small = z.double(), z.double().abs() < 50
+    sig = torch.sigmoid(zz)
+    value = torch.where(small, zz * sig, torch.where(zz < 0, 0.0, zz))
+    slope = torch.where(small, sig * (1 + zz * (1 - sig)), (zz > 0).double())
+    most = torch.finfo(DT[dt]).max
+    ref = n * value
+    ref[(ref.abs() > 0.999 * most) | ~torch.isfinite(ref)] = float("nan")  # (an infinity, or next to one)
+    # e^-87 times the bounds that the kernels take: 128 e^-87 < 2^-118 of n
+    within(y, ref, (HALF[dt] + 2.0 ** -17) * ref.abs() + 2.0 ** -118 * n.abs(), "y")
+    assert (y.cpu().double()[..., (zz == inf)].abs() == inf).all()
+    ref = c["dy"].double() * n * slope
+    within(g["dgate"], ref, HALF[dt] * ref.abs() + 2.0 ** -15 * (c["dy"].double() * n).abs() * (small | (zz > 0)) + 2.0 ** -110, "dgate")
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gates_of_nan(dt, act):
+    """A gate of NaN makes its own result and gradient NaN, and its row's dx, and nothing else."""
+    c = norm_case(1, 1, 5, 64, dt, 6, False, True)
+    z = c["gate"].clone()
+    z[0, 0, 2, 9] = float("nan")
+    f = lambda gate: (kda.rms_norm(up(c["x"]), up(c["w"]), gate=up(gate), gate_activation=act),  # noqa: E731
+                      kda.rms_norm_backward(up(c["x"]), up(c["w"]), up(c["dy"]), gate=up(gate), gate_activation=act))
+    (y, g), (y1, g1) = f(z), f(c["gate"])
+    torch.cuda.synchronize()
+    hit = torch.zeros(1, 1, 5, 64, dtype=torch.bool)
+    hit[0, 0, 2, 9] = True
+    for a, b in ((y, y1), (g["dgate"], g1["dgate"])):
+        assert torch.equal(torch.isnan(a.cpu()), hit) and torch.equal(a.cpu()[~hit], b.cpu()[~hit])
+    hit[0, 0, 2] = True
+    assert torch.equal(torch.isnan(g["dx"].cpu()), hit) and torch.equal(g["dx"].cpu()[~hit], g1["dx"].cpu()[~hit])
+    col = torch.arange(64) == 9
+    assert torch.equal(torch.isnan(g["dweight"].cpu()), col)
