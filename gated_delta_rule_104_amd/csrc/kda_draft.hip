@@ -1,7 +1,7 @@
 // Drafted tokens: how many the target's probabilities accept, the token behind them, and the
 // states that go with them.
 //
-// Token j is accepted while u_j q_j(tok_j) < p_j(tok_j).  At the first refusal the next token is drawn
+// Token j is accepted while u_j q_j(tok_j) < p_j(tok_j), both as they count below.  At the first refusal the next token is drawn
 // from max(p_j - q_j, 0), behind the last accepted one from p: the smallest i whose running sum is above
 // u times the whole one.  Products of fp32 numbers are exact in fp64, and sums are fp64, so that the
 // choice is the one of the exact sums but for a threshold within about 1e-14 of a border.
@@ -22,6 +22,9 @@ namespace {
 
 constexpr int kChunk = 4096;  // probabilities of a row per workgroup
 constexpr int kRowChunks = 16;  // of a row that one workgroup takes
+
+// A probability as it counts: NaN and what is negative as none, an infinity as the largest number.
+__device__ __forceinline__ float mass(float p) { return fminf(fmaxf(p, 0.f), 3.402823466e38f); }
 
 struct Choice {
   int accepted, count, token;  // token: the refused one
@@ -45,9 +48,10 @@ __device__ __forceinline__ Choice accept(const VerifyArgs& a, int n) {
       tok = a.tokens[(long long)n * a.K + j];
       ok = false;
       if (tok >= 0 && tok < a.V) {
-        const double p = (double)to_f32(static_cast<const T*>(a.p)[n * a.pn + j * a.pt + tok]);
-        const double q = a.q ? (double)to_f32(static_cast<const T*>(a.q)[n * a.qn + j * a.qt + tok]) : 1.0;
-        ok = (double)a.u[(long long)n * (a.K + 1) + j] * q < p;
+        const float p = to_f32(static_cast<const T*>(a.p)[n * a.pn + j * a.pt + tok]);
+        const float q = a.q ? to_f32(static_cast<const T*>(a.q)[n * a.qn + j * a.qt + tok]) : 1.f;
+        // (a NaN is not below or above anything: refused)
+        ok = q == q && (double)a.u[(long long)n * (a.K + 1) + j] * (double)mass(q) < (double)mass(p);
       }
     }
     const unsigned long long no = __ballot(!ok);
@@ -83,9 +87,8 @@ __device__ __forceinline__ Row<T> load_any(const T* p) {
   return unpack<T>(w);
 }
 
-// A lane's vector of both rows: what is left of p behind q, and p, in fp64; NaN and what is negative
-// count as no mass, an infinity as the largest number.  The clamps are in fp32, whose instructions are
-// cheaper; p - min(q, p) of fp32 numbers is exact in fp64 unless one is 2^28 times the other.
+// A lane's vector of both rows: what is left of p behind q, and p, in fp64.  The clamps are in fp32, whose instructions
+// are cheaper; p - min(q, p) of fp32 numbers is exact in fp64 unless one is 2^28 times the other.
 template <typename T, bool ONCE>
 __device__ __forceinline__ void masses(const Rows<T>& r, int i0, int end, double* w, double* whole) {
   constexpr int V = kVec<T>;
@@ -102,7 +105,7 @@ __device__ __forceinline__ void masses(const Rows<T>& r, int i0, int end, double
   }
 #pragma unroll
   for (int c = 0; c < V; ++c) {
-    const float x = fminf(fmaxf(p.v[c], 0.f), 3.402823466e38f);
+    const float x = mass(p.v[c]);
     float y = r.q ? q.v[c] : 0.f;
     if (i0 + c == r.token) y = 1.f;
     whole[c] = (double)x;

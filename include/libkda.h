@@ -579,7 +579,8 @@ kda_status kda_rms_norm_backward(const void* x, const void* gate, const void* we
  * max(p - q, 0) has none at all, p is drawn from, and where p has none the token is -1.
  *   target   : [N, K + 1, V] dtype, p: the target's probabilities (they need not add up to
  *              1; NaN and negative ones count as 0, infinite ones as the largest number)
- *   draft    : [N, K, V] dtype, q: the draft's; NULL for one at each drafted token (greedy
+ *   draft    : [N, K, V] dtype, q: the draft's, which count in the same way, but that a NaN at
+ *              the drafted token refuses it; NULL for one at each drafted token (greedy
  *              drafts).  Strides b and t of both in elements (h is ignored), any element
  *              alignment, rows of V contiguous; NULL for contiguous.
  *   tokens   : [N, K] the drafted tokens; one outside [0, V) is refused

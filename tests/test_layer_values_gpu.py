@@ -138,3 +138,29 @@ def test_gates_of_nan(dt, act):
     assert torch.equal(torch.isnan(g["dx"].cpu()), hit) and torch.equal(g["dx"].cpu()[~hit], g1["dx"].cpu()[~hit])
     col = torch.arange(64) == 9
     assert torch.equal(torch.isnan(g["dweight"].cpu()), col)
+
+
+# ----------------------------------------------------------------- drafts
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [100, 40000])
+def test_draft_probabilities_that_are_none(V, dt):
+    """What is accepted goes by the same numbers as what is drawn: negative probabilities count as 0 and infinite ones as
+    the largest number, the draft's like the target's; a NaN of either at a drafted token refuses it."""
+    inf, nan = float("inf"), float("nan")
+    rows = [  # target's, draft's, random number, whether it stands
+        (0.0, -0.5, 0.5, False), (-0.1, -1.0, 0.5, False), (-0.5, -0.25, 0.9, False), (0.25, -0.25, 0.9, True),
+        (inf, inf, 0.5, True), (inf, inf, 0.0, True), (inf, 0.5, 0.5, True), (0.25, inf, 0.5, False), (0.25, inf, 0.0, True),
+        (0.25, nan, 0.0, False), (nan, 0.25, 0.5, False), (nan, -0.25, 0.5, False), (0.25, 0.25, 0.5, True), (-inf, -inf, 0.5, False),
+    ]
+    N = len(rows)
+    p, q = torch.full((N, 2, V), 0.5 / V), torch.full((N, 1, V), 0.5 / V)
+    tok, u = torch.full((N, 1), 7, dtype=torch.int32), torch.full((N, 2), 0.5)
+    for i, (a, b, r, _) in enumerate(rows):
+        p[i, 0, 7], q[i, 0, 7], u[i, 0] = a, b, r
+    acc, out = kda.draft_verify(up(p.to(DT[dt])), up(q.to(DT[dt])), up(tok), up(u))
+    torch.cuda.synchronize()
+    assert acc.tolist() == [int(r[3]) for r in rows]
+    for (a, b, _, stands), row in zip(rows, out.tolist()):
+        assert (row[0] == 7 and 0 <= row[1] < V) if stands else (0 <= row[0] < V and row[1] == -1)
+        if not stands and not a > 0:
+            assert row[0] != 7  # a token of no mass
