@@ -355,6 +355,10 @@ size_t verify_ws_bytes(int N, int V) {
   return verify_row(N, V) ? 0 : (size_t)N * (nchunk + 1) * 16;
 }
 
+bool verify_fits(int N, int V) {
+  return verify_row(N, V) || (launchable((long long)N * verify_chunks(V), 256) && launchable(N, 512));
+}
+
 hipError_t launch_verify(const VerifyArgs& a, bool bf16_io, hipStream_t stream) {
   return bf16_io ? verify<bf16>(a, stream) : verify<float>(a, stream);
 }

@@ -825,6 +825,15 @@ size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients) {
   return most;
 }
 
+bool glr_fits(int B, int H, int T, int d, bool beta, bool norm, bool bf16_io, bool gradients) {
+  int nt;
+  const GlrGrid n = glr_grid(B, H, T, d, bf16_io, gradients, beta, norm, &nt);
+  return launchable((long long)n.blocks * n.ntile, 64 * kWaves);
+}
+bool glr_step_fits(int N, int H, int d, bool bf16_io) {
+  return launchable(((long long)N * (H * d / (bf16_io ? 8 : 4)) + 255) / 256, 256);
+}
+
 // (a tile's rows are 64 channels of heads that may lie apart)
 bool glr_lines(const GlrArgs& a, const void* p, Str3 s, bool bf16_io) {
   const int es = bf16_io ? 2 : 4;

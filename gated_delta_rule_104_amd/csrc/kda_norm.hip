@@ -531,6 +531,22 @@ hipError_t norm_bwd(const NormArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+bool norm_fits(int rows, int d, bool bf16_io) {
+  const auto fits = [&](auto l, auto w, auto, auto nr) {
+    constexpr int LANES = decltype(l)::value, WAVES = decltype(w)::value, THREADS = WAVES > 4 ? 64 * WAVES : 256;
+    constexpr int per = THREADS / (LANES * WAVES) * decltype(nr)::value;
+    return launchable(((long long)rows + per - 1) / per, THREADS);
+  };
+  return bf16_io ? with_shape<bf16>(d, fits) : with_shape<float>(d, fits);
+}
+bool norm_backward_fits(int nparts, int d, int w_heads, bool weight, bool bf16_io) {
+  const auto fits = [&](auto, auto w, auto) {
+    constexpr int WAVES = decltype(w)::value, THREADS = WAVES > 4 ? 64 * WAVES : 256;
+    return launchable((long long)nparts * w_heads, THREADS) && (!weight || launchable(((long long)w_heads * d + 31) / 32, 1024));
+  };
+  return bf16_io ? with_bwd_shape<bf16>(d, fits) : with_bwd_shape<float>(d, fits);
+}
+
 // Blocks per weight row: three of 256 threads a compute unit, two of 512 or one of 1024 (32K rows of 4096 bf16 values,
 // blocks of 256: 261, 179, 182, 196 us with one to four; heads of 128 with a gate 449, 289, 274, 267), no more than there
 // are units of rows.

@@ -101,6 +101,9 @@ inline bool whole_lines(const void* p, Str3 s, long long rows, long long bytes, 
          s.b * elem % 128 == 0 && s.h * elem % 128 == 0 && s.t * elem % 128 == 0;
 }
 
+// A launch holds fewer than 2^32 threads.  The *_fits say whether a call's launches do.
+inline bool launchable(long long blocks, int threads) { return blocks * threads < (1LL << 32); }
+
 // ------------------------------------------------ gated linear recurrence
 struct GlrArgs {
   const void* x;     // [B, H, T, d]
@@ -125,6 +128,8 @@ struct GlrArgs {
   bool lines = false;  // outputs are written past the caches (set by the launch)
 };
 size_t glr_ws_bytes(int B, int H, int T, int d, bool bf16_io, bool gradients);
+bool glr_fits(int B, int H, int T, int d, bool beta, bool norm, bool bf16_io, bool gradients);
+bool glr_step_fits(int N, int H, int d, bool bf16_io);
 // polls: how often a run of tokens looks for the state in front of it before it walks the sequence itself
 hipError_t launch_glr(const GlrArgs& a, bool bf16_io, int polls, hipStream_t stream);
 hipError_t launch_glr_step(const GlrArgs& a, bool bf16_io, hipStream_t stream);
@@ -159,6 +164,8 @@ struct NormArgs {
   bool lines = false;                                 // outputs are written past the caches
   long long hx = 0, hg = 0, hdy = 0, hds = 0, hdx = 0, hdg = 0;  // backward: from one row of the weight to the next
 };
+bool norm_fits(int rows, int d, bool bf16_io);
+bool norm_backward_fits(int nparts, int d, int w_heads, bool weight, bool bf16_io);
 int norm_parts(int rows, int d, int w_heads, bool bf16_io, int cus);
 hipError_t launch_norm(NormArgs a, int B, int H, int T, bool bits8, bool bf16_io, hipStream_t stream);
 hipError_t launch_norm_backward(NormArgs a, int B, int H, int T, bool bf16_io, hipStream_t stream);
@@ -177,6 +184,7 @@ struct VerifyArgs {
   void* ws;
 };
 size_t verify_ws_bytes(int N, int V);
+bool verify_fits(int N, int V);
 hipError_t launch_verify(const VerifyArgs& a, bool bf16_io, hipStream_t stream);
 hipError_t launch_state_commit(const float* S_pos, const int* index, float* S, int N, int ntok, long long elems,
                                hipStream_t stream);

@@ -30,6 +30,7 @@ kda_status need(const void* p, const char* name) {
   if (!aligned(p)) return api_fail(KDA_ERR_ALIGN, "%s is not 16-byte aligned", name);
   return KDA_OK;
 }
+kda_status too_large() { return api_fail(KDA_ERR_SHAPE, "problem too large"); }
 kda_status need_any(const void* p, const char* name) {
   return p ? KDA_OK : api_fail(KDA_ERR_NULL, "%s is NULL", name);
 }
@@ -402,7 +403,7 @@ kda_status glr_dims(int B, int H, int T, int d, kda_dtype dtype) {
   const long long C = (long long)H * d;
   if (C > (1 << 28) || T > (1 << 30) || (long long)B * C > kMaxElems || (long long)B * C * T > kMaxElems ||
       ((long long)B * ((C + 63) / 64) + 8) * (T / 32 + 1) > INT32_MAX)
-    return api_fail(KDA_ERR_SHAPE, "problem too large");
+    return too_large();
   return KDA_OK;
 }
 
@@ -448,6 +449,7 @@ kda_status kda_glr_prefill(const void* x, const void* log_alpha, const void* bet
   kda::GlrArgs a{};
   OPS_TRY(glr_inputs(a, st, B, H, T, d, beta != nullptr, true, dtype));
   if ((long long)B * H * d == 0) return api_ok();
+  if (!kda::glr_fits(B, H, T, d, beta != nullptr, normalise != 0, dtype == KDA_BF16, false)) return too_large();
   OPS_TRY(maybe(h0, "h0"));
   OPS_TRY(need(h_T, "h_T"));
   if (T > 0) {
@@ -472,6 +474,7 @@ kda_status kda_glr_step(const void* x, const void* log_alpha, const void* beta, 
   kda::GlrArgs a{};
   OPS_TRY(glr_inputs(a, st, N, H, 1, d, beta != nullptr, true, dtype));
   if ((long long)N * H * d == 0) return api_ok();
+  if (!kda::glr_step_fits(N, H, d, dtype == KDA_BF16)) return too_large();
   OPS_TRY(need(x, "x"));
   OPS_TRY(need(log_alpha, "log_alpha"));
   OPS_TRY(maybe(beta, "beta"));
@@ -507,6 +510,7 @@ kda_status kda_glr_backward(const void* x, const void* log_alpha, const void* be
   if (beta) OPS_TRY(take_strides(gst ? &gst->dbeta : nullptr, B, H, T, d, es, true, true, "dbeta", &a.dbs));
   if ((long long)H * d == 0) return api_ok();
   if (B == 0 || T == 0) return api_fail(KDA_ERR_SHAPE, "the gradients need B >= 1 and T >= 1 (B=%d T=%d)", B, T);
+  if (!kda::glr_fits(B, H, T, d, beta != nullptr, normalise != 0, dtype == KDA_BF16, true)) return too_large();
   OPS_TRY(need(x, "x"));
   OPS_TRY(need(log_alpha, "log_alpha"));
   OPS_TRY(maybe(beta, "beta"));
@@ -547,7 +551,7 @@ kda_status norm_dims(int B, int H, int T, int d, float eps, kda_gate gate_activa
     return api_fail(KDA_ERR_UNSUPPORTED, "unknown gate activation %d", (int)gate_activation);
   if (!(eps >= 0.f && eps < 1e30f)) return api_fail(KDA_ERR_UNSUPPORTED, "eps = %g is not a finite number of at least 0", eps);
   if ((long long)B * H > INT32_MAX || (long long)B * H * T > INT32_MAX - 65536 || (long long)H * d > (1 << 28))
-    return api_fail(KDA_ERR_SHAPE, "problem too large");
+    return too_large();
   return KDA_OK;
 }
 }  // namespace
@@ -570,6 +574,7 @@ kda_status kda_rms_norm(const void* x, const void* residual, const void* gate, c
   if (residual_out) OPS_TRY(take_strides(st ? &st->residual_out : nullptr, B, H, T, d, es, true, true, "residual_out", &a.ss));
   if (bits8) OPS_TRY(take_strides(st ? &st->scales : nullptr, B, H, T, blocks ? d / 32 : 1, 4, false, true, "scales", &a.cs));
   if ((long long)B * H * T * d == 0) return api_ok();
+  if (!kda::norm_fits(B * H * T, d, dtype == KDA_BF16)) return too_large();
   OPS_TRY(need(x, "x"));
   OPS_TRY(maybe(residual, "residual"));
   OPS_TRY(maybe(gate, "gate"));
@@ -620,6 +625,8 @@ kda_status kda_rms_norm_backward(const void* x, const void* gate, const void* we
   if (gate) OPS_TRY(take_strides(st ? &st->dgate : nullptr, B, H, T, d, es, true, true, "dgate", &a.dgs));
   if ((long long)H * d == 0) return api_ok();
   if (B == 0 || T == 0) return api_fail(KDA_ERR_SHAPE, "the gradients need B >= 1 and T >= 1 (B=%d T=%d)", B, T);
+  const int heads = weight_per_head ? H : 1, nparts = kda::norm_parts(B * H * T, d, heads, dtype == KDA_BF16, kda::api_cu_count());
+  if (!kda::norm_backward_fits(nparts, d, heads, weight != nullptr, dtype == KDA_BF16)) return too_large();
   OPS_TRY(need(x, "x"));
   OPS_TRY(maybe(gate, "gate"));
   OPS_TRY(maybe(weight, "weight"));
@@ -633,7 +640,6 @@ kda_status kda_rms_norm_backward(const void* x, const void* gate, const void* we
       if (out == in) return api_fail(KDA_ERR_UNSUPPORTED, "a gradient must not be an input");
   if ((gate && dgate == dx) || (weight && (dweight == dx || (gate && dweight == dgate))))
     return api_fail(KDA_ERR_UNSUPPORTED, "gradients must not share memory");
-  const int heads = weight_per_head ? H : 1;
   if (weight)
     OPS_TRY(need_workspace(workspace, workspace_bytes,
                            kda_rms_norm_backward_workspace_bytes(B, H, T, d, weight_per_head, dtype)));
@@ -643,7 +649,7 @@ kda_status kda_rms_norm_backward(const void* x, const void* gate, const void* we
   a.rows = B * H * T; a.d = d; a.w_heads = heads; a.eps = eps; a.inv_d = 1.f / (float)d;
   a.silu = gate_activation == KDA_GATE_SILU;
   a.scratch = static_cast<float*>(workspace);
-  a.nparts = kda::norm_parts(a.rows, d, heads, dtype == KDA_BF16, kda::api_cu_count());
+  a.nparts = nparts;
   const hipError_t e = kda::launch_norm_backward(a, B, H, T, dtype == KDA_BF16, stream);
   return e == hipSuccess ? api_ok() : hip_fail(e, "kda_rms_norm_backward launch");
 }
@@ -653,8 +659,7 @@ namespace {
 kda_status verify_dims(int N, int K, int V, kda_dtype dtype) {
   if (N < 0 || K < 0 || V < 0) return api_fail(KDA_ERR_SHAPE, "negative size N=%d K=%d V=%d", N, K, V);
   OPS_TRY(check_dtype(dtype));
-  if (N > (1 << 24) || K > (1 << 16) || V > (1 << 30) || (long long)N * (V / 4096 + 1) > (1 << 30))
-    return api_fail(KDA_ERR_SHAPE, "problem too large");
+  if (N > (1 << 24) || K > (1 << 16) || V > (1 << 30) || !kda::verify_fits(N, V)) return too_large();
   return KDA_OK;
 }
 
@@ -715,9 +720,9 @@ kda_status kda_state_commit(const float* S_pos, const int* index, float* S, int 
   if (N < 0 || ntok < 0 || H < 0 || dk < 0 || dv < 0)
     return api_fail(KDA_ERR_SHAPE, "negative size N=%d ntok=%d H=%d dk=%d dv=%d", N, ntok, H, dk, dv);
   const long long e = (long long)dk * dv;
-  if (N > (1 << 24) || ntok > (1 << 16) || e > (1 << 24) || (long long)H * e > (1LL << 36) ||
+  if (N >= (1 << 24) || ntok > (1 << 16) || e > (1 << 24) || (long long)H * e > (1LL << 36) ||
       (long long)N * ntok > kMaxElems / ((long long)H * e + 1))
-    return api_fail(KDA_ERR_SHAPE, "problem too large");
+    return too_large();
   if ((long long)H * e % 4) return api_fail(KDA_ERR_UNSUPPORTED, "states of %lld floats are not a multiple of 16 bytes", (long long)H * e);
   if (N == 0 || ntok == 0 || H * e == 0) return api_ok();
   OPS_TRY(need(S_pos, "S_pos"));
