@@ -463,15 +463,17 @@ kda_status kda_state_load(const void* cache, const void* scales, const int* slot
  * beta x whatever the decay.
  *   x, log_alpha, beta, o : [B, H, T, d] dtype (strides), d * sizeof(dtype) a
  *                 multiple of 16; beta NULL for 1
- *   log_alpha   : <= 0; -inf (any value below -104) clears the state, whatever it
- *                 held: packed documents start that way.  Option "check" validates
+ *   log_alpha   : <= 0; -inf (any value below -88, whose decay is no normal number)
+ *                 clears the state, whatever it held: packed documents start that
+ *                 way.  Option "check" validates
  *                 that, and that beta is finite (padding excepted), before launching.
  *   h0, h_T     : [B, H, d] fp32, contiguous; h0 NULL for zero; h_T may be h0
  * States are carried in fp32 (fp32 inputs: in 64 bits inside a run of tokens) and
  * decays near 1 as their distance from it, so that slow ones keep their digits.
- * T == 0 copies h0 (or zeros) to h_T.  An infinity or NaN in x, log_alpha or beta stays
- * in its channel's state until that is cleared, or until decays that together come to
- * less than e^-104 have passed over it.
+ * T == 0 copies h0 (or zeros) to h_T.  An infinity or NaN in x, log_alpha or beta makes
+ * its channel's state one of the two until that is cleared.  A stretch of strong decays
+ * that together come to less than e^-88 may clear it too: that goes by how the sequence is
+ * cut into runs, and no program should count on it, nor on the opposite.
  * The sequences are cut into runs of tokens that fill the device; the workspace
  * (kda_glr_prefill_workspace_bytes; may be 0) holds what passes between them.
  */

@@ -4,7 +4,7 @@ import torch
 
 import gated_delta_rule_104_amd as kda
 import layer_oracle as orc
-from test_layer_ops_gpu import DT, HALF, gen, norm_case, summed, up, within
+from test_layer_ops_gpu import DT, HALF, gen, glr_case, norm_case, summed, up, within
 
 pytestmark = pytest.mark.gpu
 
@@ -138,6 +138,42 @@ def test_gates_of_nan(dt, act):
     assert torch.equal(torch.isnan(g["dx"].cpu()), hit) and torch.equal(g["dx"].cpu()[~hit], g1["dx"].cpu()[~hit])
     col = torch.arange(64) == 9
     assert torch.equal(torch.isnan(g["dweight"].cpu()), col)
+
+
+# ------------------------------------------------------ decays that clear
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,beta", [(1, True), (40, True), (300, False), (1500, True)])
+def test_single_gates_that_clear(T, beta, dt):
+    """Any log_alpha below -88 does what -inf does, bit by bit, to states that are not finite too: in a prompt, in one
+    token, and in the gradients."""
+    values = [-88.5, -90.0, -95.0, -103.0, -104.0, -105.0, -1e4, -3e38]
+    d = 2 * len(values)
+    c = glr_case(1, 2, T, d, dt, T, beta=beta)
+    at = T // 2
+    la, end = c["la"].clone(), c["la"].clone()
+    la[:, :, at], end[:, :, at] = torch.tensor(values * 2).to(DT[dt]), -float("inf")
+    x, h0 = c["x"].clone(), c["h0"].clone()
+    h0[0, 0], h0[0, 1, : d // 2] = float("nan"), float("inf")
+    if at:
+        x[0, 1, at - 1, d // 2:] = float("nan")
+    be = up(c["beta"])
+    for norm in (False, True):
+        got = kda.glr_prefill(up(x), up(la), be, up(h0), normalise=norm)
+        ref = kda.glr_prefill(up(x), up(end), be, up(h0), normalise=norm)
+        one = [t[:, :, at] if t is not None else None for t in (up(x), up(la), be)]
+        h = up(h0)
+        o = kda.glr_step(one[0], one[1], h, one[2], normalise=norm)
+        g = kda.glr_backward(up(x), up(la), be, up(h0), ref[0], up(c["dO"]), up(c["dh_T"]), normalise=norm)
+        r = kda.glr_backward(up(x), up(end), be, up(h0), ref[0], up(c["dO"]), up(c["dh_T"]), normalise=norm)
+        torch.cuda.synchronize()
+        assert torch.isfinite(ref[0][:, :, at:]).all() and torch.isfinite(ref[1]).all()
+        assert torch.equal(got[0][:, :, at:], ref[0][:, :, at:]) and torch.equal(got[1], ref[1])
+        assert torch.isfinite(h).all() and torch.isfinite(o).all()
+        start = torch.zeros_like(h)
+        assert torch.equal(o, kda.glr_step(one[0], one[1], start, one[2], normalise=norm)) and torch.equal(h, start)
+        for n in g:
+            assert torch.equal(torch.nan_to_num(g[n]), torch.nan_to_num(r[n])) and torch.equal(torch.isnan(g[n]), torch.isnan(r[n])), n
+        assert not g["dlog_alpha"][:, :, at].any() and torch.isfinite(g["dh0"]).all()
 
 
 # ----------------------------------------------------------------- drafts
