@@ -73,7 +73,9 @@ struct Gate {
       e = z == z ? __builtin_amdgcn_exp2f(t) * fmaf(r, 0.69314718055994530942f, 1.f) : z;
     }
     const float s = __builtin_amdgcn_rcpf(1.f + e), one_less = fminf(e, 0x1p126f) * s;
-    g = silu ? fmaxf(z, -most) * s : s;
+    // (-inf, the largest bits but for negative NaN, to the lowest number: one instruction less than a maximum)
+    const float low = __uint_as_float(min(__float_as_uint(z), 0xff7fffffu));
+    g = silu ? low * s : s;
     dg = silu ? s * fmaf(__builtin_amdgcn_fmed3f(z, -most, most), one_less, 1.f) : s * one_less;
   }
 };
@@ -179,18 +181,14 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(
     }
   }
   row_reduce<LANES, WAVES, NR>(sum, red);
-  // Rows in 8 bits first take their factor's power of two alone, which rounds nothing: with the whole of it, quotients
-  // y / largest that lie on a border between two 8-bit values (3 or 4 in 10,000 of rows of 4096 in bf16) come to
-  // either side of it.
-  float scale[NR], rest[NR], top[NR];
+  // Rows in 8 bits without a gate leave their factor to their scale: its rounding would put quotients value / largest
+  // that lie on a border between two 8-bit values (3 or 4 in 10,000 of rows of 4096 in bf16) to either side of it.
+  const bool later = BITS8 && !a.blocks && !a.gate;
+  float scale[NR], top[NR];
 #pragma unroll
   for (int j = 0; j < NR; ++j) {
     scale[j] = 1.f / sqrtf(sum[j] * a.inv_d + a.eps);
     top[j] = 0.f;
-    if (BITS8 && !a.blocks) {
-      rest[j] = __builtin_amdgcn_frexp_mantf(scale[j]);
-      if (scale[j] != 0.f) scale[j] = ldexpf(1.f, __builtin_amdgcn_frexp_expf(scale[j]));
-    }
   }
   const auto value = [&](int j, int i, const T* w) {
     Row<T> y = unpack<T>(xr[j][i]);
@@ -200,8 +198,10 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(
 #pragma unroll
       for (int c = 0; c < V; ++c) y.v[c] *= k.v[c];
     }
+    if (!later) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) y.v[c] *= scale[j];
+      for (int c = 0; c < V; ++c) y.v[c] *= scale[j];
+    }
     if (a.gate) {
       const Row<T> g = unpack<T>(gr[j][i]);
 #pragma unroll
@@ -259,12 +259,18 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void kda_norm_kernel(
       const Place p(have[j] ? row0 + j * GROUPS : 0, a.n1, a.n2);
       // (a row of zeros, or one so small that its scale would not be a normal number, takes the smallest
       // scale; its values are then rounded to multiples of that, like a block's)
-      const float most_y = top[j] * rest[j], sc_y = most_y / limit;
-      const bool none = !(most_y < __builtin_inff()), least = sc_y < 1.17549435e-38f;
+      const float most_y = later ? top[j] * scale[j] : top[j], sc_y = most_y / limit;
+      const bool none = !(most_y < __builtin_inff());
       const float sc = none ? __builtin_nanf("") : fmaxf(sc_y, 1.17549435e-38f);
-      // v limit / top with top = m 2^ex, as v (limit 2^-ex) / m: of bf16 without a gate all but the quotient is exact
-      const int ex = max(__builtin_amdgcn_frexp_expf(top[j]), -100);
-      const float m = least ? 0x1p-126f : ldexpf(top[j], -ex), by = least ? rest[j] : ldexpf(limit, -ex);
+      // y / sc; without the factor v limit / top, as v (limit 2^-ex) / m with top = m 2^ex, of which bf16 rounds the
+      // quotient alone
+      float m = sc, by = 1.f;
+      if (later) {
+        const bool least = sc_y < 1.17549435e-38f;
+        const int ex = max(__builtin_amdgcn_frexp_expf(top[j]), -100);
+        m = least ? 0x1p-126f : ldexpf(top[j], -ex);
+        by = least ? scale[j] : ldexpf(limit, -ex);
+      }
       const float inv = __builtin_amdgcn_rcpf(m);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
