@@ -7,8 +7,9 @@
 //
 // Nothing but the inputs and outputs has to move, so HBM bounds long calls: four prompts of 8192 tokens, 4096 channels, bf16,
 // with beta and normalised, 198-203 us for 1.07 GB (5.3-5.4 TB/s); one of 65536 tokens, 2560 channels, without either 187-193
-// for 1.01 GB; the gradients of the former 387-436, by card and place in memory, for 2.15 GB.  Vector instructions, about 42 a value with
-// its share of the relay in the first and the last of these, take 70% of the SIMDs' cycles beside that.  Every token
+// for 1.01 GB; the gradients of the former 387-436, by card and place in memory, for 2.15 GB.  Vector instructions take 70% of
+// the SIMDs' cycles beside that in the first and the last of these: 41 a value in the prompt and 82 in the gradients, whose
+// lanes hold half as many tokens for the same joining and relay.  Every token
 // waits for the one before it; the relay below keeps that to a few microseconds a tile, behind other tiles' loads.  One token of 256 sequences
 // x 4096 channels: 7.4 us, 5.4 of them the kernel.  Short prompts are bounded by their launches: 9 us with one, 13 with two.
 #include <cstdio>
@@ -747,6 +748,8 @@ constexpr int kWaves = 4;
 //                                               4 x 8000 17 / 17 / 19    64 x 8000 50 / 52 / 55       256 x 8000 161 / 172 / 164
 //   without either           4 / 8 / 12         4 x 32000 43 / 28 / 26   64 x 32000 170 / 152 / 149   256 x 32000 564 / 555 / 543
 //                                               4 x 8000 17 / 15 / 15    64 x 8000 48 / 46 / 48       256 x 2000 44 / 44 / 47
+// (The joining of lanes and the relay cost a lane the same whatever its tokens: with 2 a lane the gradients' share of it is
+// twice the prompts' with 4.)
 // gradients of 134M values with beta (268M without) in up to 64K tokens by chains, with 2 / 3 / 4 tokens:
 //   with beta                256 439 / 444 / 468   64 443 / 456 / 468   40 453 / 429 / 456   4 141 / 105 / 86
 //   without                  256 310 / 272 / 273   64 323 / 293 / 285   40 340 / 292 / 282   4 133 / 95 / 73

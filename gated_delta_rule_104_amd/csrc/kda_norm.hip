@@ -3,14 +3,17 @@
 //     s = x + residual (rounded to its type),  r = (mean s^2 + eps)^-1/2,  y = s r w g(gate)
 //     dn = dy w g,  ds = r (dn - s r mean(dn s r)) + ds_out,  dw = sum dy s r g,  dgate = dy s r w g'
 //
-// Every value is read and written once, so HBM bounds all of it.  A row stays in the
+// Every value is read and written once, so HBM bounds long rows; short ones with a gate are bound by vector instructions (an
+// exponential and a reciprocal a value, and a row's addresses in every lane for few values).  A row stays in the
 // registers of the lanes that share it: 8 to 64 lanes of a wave for short rows, whose sums
 // then take lane exchanges only, and 4 or 16 waves for long ones, whose sums meet in LDS.
 // Sums are fp32 in a fixed order (lanes by a butterfly, waves in order), results rounded once.
 //
-// 32K rows of 4096 bf16 values: with a residual in front and e4m3 blocks behind 143-145 us for 943 MB, gradients 184-195 us
-// for 1.07 GB; 1M rows of 128 with a gate 142 us for 805 MB: 5.5-6.5 TB/s (a large copy reaches 5.4).  256 rows of 4096 with
-// e4m3 rows: 10.6 us, of which the kernel, one chain of load, two sums and store, 5.8 and the call the rest.
+// 32K rows of 4096 bf16 values: with a residual in front and e4m3 blocks behind 143-146 us for 943 MB (in rows 149-151, fp32
+// 274 and 280 for 1.75 GB), gradients 184-195 us for 1.07 GB (fp32 390): 5.5-6.5 TB/s (a large copy reaches 5.4).  1M rows of
+// 128 with a gate 142 us for 805 MB, 1268 vector instructions a wave or 135 us of the SIMDs' cycles; in e4m3 blocks 166 and in
+// rows 196 us for 675 MB; gradients 252-258 for 1.34 GB.  256 rows of 4096 with
+// e4m3 rows: 10.6 us, of which the kernel, one chain of load, two sums and store, 5.9 and the call the rest.
 #include "kda_ops.hpp"
 #include "kda_vec.hpp"
 
@@ -554,7 +557,7 @@ bool norm_backward_fits(int nparts, int d, int w_heads, bool weight, bool bf16_i
 }
 
 // Blocks per weight row: three of 256 threads a compute unit, two of 512 or one of 1024 (32K rows of 4096 bf16 values,
-// blocks of 256: 261, 179, 182, 196 us with one to four; heads of 128 with a gate 449, 289, 274, 267), no more than there
+// blocks of 256: 262, 178, 182-186, 195 us with one to four; heads of 128 with a gate 437, 280, 257, 269), no more than there
 // are units of rows.
 int norm_parts(int rows, int d, int w_heads, bool bf16_io, int cus) {
   const auto parts = [&](auto l, auto w, auto) {

@@ -46,21 +46,6 @@ __device__ __forceinline__ void st16(T* p, u32x4 w) {
   *reinterpret_cast<u32x4*>(p) = w;
 }
 
-// Registers whose contents the compiler must take as new: what it has computed from them before is then
-// computed again where it is used again, instead of being kept.
-template <int N>
-__device__ __forceinline__ void forget(u32x4 (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(r[i]));
-}
-template <int N, int M>
-__device__ __forceinline__ void forget(float (&r)[N][M]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int j = 0; j < M; ++j) asm volatile("" : "+v"(r[i][j]));
-}
-
 // The same for values that nothing reads again soon: they pass the caches without pushing out others.
 template <typename T>
 __device__ __forceinline__ u32x4 ld_once(const T* p) {
@@ -84,14 +69,29 @@ __device__ __forceinline__ void store_by(void* p, V w, bool once) {
   }
 }
 
+// Registers whose contents the compiler must take as new: what it has computed from them before is then
+// computed again where it is used again, instead of being kept.
+template <int N>
+__device__ __forceinline__ void forget(u32x4 (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(r[i]));
+}
+template <int N, int M>
+__device__ __forceinline__ void forget(float (&r)[N][M]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < M; ++j) asm volatile("" : "+v"(r[i][j]));
+}
+
 __device__ __forceinline__ int seq_len(const int* lens, int b, int T) {
   if (!lens) return T;
   const int n = lens[b];
   return n < 0 ? 0 : (n > T ? T : n);
 }
 
-// The hardware's exponential and reciprocal, each within a unit in the last place of
-// fp32: with the correctly rounded division and expf the four 8K prompts (bf16) took 145
+// The short convolution's SiLU: x times this.  The hardware's exponential and reciprocal, each within a unit in the last
+// place of fp32: with the correctly rounded division and expf its four prompts of 8192 tokens (4096 channels, bf16) took 145
 // us, bound by vector instructions.  The exponent's own rounding is |x| 2^-24 of the
 // result, nothing beside bf16's; fp32 takes it back: t = x c is rounded, r what that and c's
 // rounding left, e^-x = 2^t (1 + r ln 2).  (Past 128 the result is 0 or 1 whatever x
