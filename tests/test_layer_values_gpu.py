@@ -91,6 +91,21 @@ def test_quantised_rows_of_large_products():
         assert ((v.cpu().double() * s - ref).abs() <= 1.001 * step + 2.0 ** -17 * ref.abs()).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_quantised_rows_of_subnormal_values(dt):
+    """Rows below fp32's normal numbers that their factor brings back among them."""
+    d = 64
+    x = ((torch.rand(1, 1, 5, d, generator=gen(3)) - 0.5) * 1e-38).to(DT[dt])
+    x[..., 0] = 9e-39
+    for fmt, top in (("e4m3", 448), ("int8", 127)):
+        v, sc = kda.rms_norm_quant(up(x), None, fmt=fmt, scales="row", eps=1e-20)
+        torch.cuda.synchronize()
+        ref, s = orc.rms_norm(x, eps=1e-20), sc.cpu().double()[..., None]
+        assert (s / (ref.abs().amax(-1, keepdim=True) / top) - 1).abs().max() <= 2.0 ** -18
+        step = s * 0.5 if fmt == "int8" else torch.maximum(s * 2.0 ** -10, 2.0 ** -4 * ref.abs())
+        assert ((v.cpu().double() * s - ref).abs() <= 1.001 * step + 2.0 ** -17 * ref.abs()).all()
+
+
 # ------------------------------------------------------------------ gates
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_silu_far_from_zero(dt):
