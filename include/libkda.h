@@ -496,11 +496,12 @@ kda_status kda_glr_step(const void* x, const void* log_alpha, const void* beta, 
 /*
  * Gradients of kda_glr_prefill for dL/do = dO and dL/dh_T = dh_T (NULL: zero).  `o`
  * holds the outputs that the forward pass wrote, and stands for the states between
- * tokens (in bf16 with 8 bits, half a step of which dlog_alpha takes over).  dx, dlog_alpha and dbeta (NULL without beta) take their input's shape, in
- * dtype; dh0 [B, H, d] fp32 (NULL: not written).  The gradients of padding are zero,
- * whatever it holds.  A decay of zero has a dlog_alpha of zero, and where
- * log_alpha = 0 the part of dlog_alpha that goes through the normaliser, which has no
- * limit there, is left out.  B and T are at least 1 (unless H is 0).
+ * tokens (in bf16 with 8 bits, half a step of which dlog_alpha takes over).  dx,
+ * dlog_alpha and dbeta (NULL without beta) take their input's shape, in dtype; dh0
+ * [B, H, d] fp32 (NULL: not written).  The gradients of padding are zero, whatever it
+ * holds.  A decay of zero has a dlog_alpha of zero, and where log_alpha = 0 the part of
+ * dlog_alpha that goes through the normaliser, which has no limit there, is left out.
+ * B and T are at least 1 (unless H is 0).
  */
 typedef struct { kda_strides dO, dx, dlog_alpha, dbeta; } kda_glr_grad_strides;
 
